@@ -12,6 +12,10 @@
  *                          output rows, accumulated in fp32.
  * ep_dispatch_layout_offsets runs steps 1 and 2 in one launch, and ep_dispatch
  * steps 1 to 3 in one call (a single kernel for a decode-sized batch).
+ * Around them: ep_route makes the picks and weights from router logits, and
+ * ep_expert_matmul is the experts' product between steps 3 and 4; ep_route_backward,
+ * ep_expert_matmul_dgrad, ep_expert_matmul_wgrad and ep_unpermute_backward are their
+ * gradients and the combine's.
  * Nothing in between goes back to the host: every count, offset and total stays
  * in device memory, and the permuted buffer is sized at the T*k upper bound.
  *
@@ -75,12 +79,14 @@ typedef enum {
     EPD_ERR_INVALID_EXPERT = 4, /* (status word) topk_idx held an id outside [-1, E) */
     EPD_ERR_TIMEOUT = 5,        /* (status word) a bounded look-back wait gave up */
     EPD_ERR_CAPACITY = 6,       /* (status word) a slot fell outside [0, capacity_rows) */
+    EPD_ERR_NONFINITE = 7,      /* (status word) a router logit was NaN or +inf */
 } epd_status_t;
 
 typedef enum {
     EPD_BF16 = 0,      /* rows of H bfloat16 values (2H bytes), H % 8 == 0 */
     EPD_FP8_E4M3 = 1,  /* rows of H float8_e4m3fn values (H bytes) plus H/128 fp32
                           scales per row, H % 128 == 0 */
+    EPD_F32 = 2,       /* float32 (router logits) */
 } epd_dtype_t;
 
 #define EPD_MAX_EXPERTS 4096
@@ -373,6 +379,172 @@ EPD_API epd_status_t ep_dispatch_lowlatency(const void *x_bf16, const int64_t *t
 EPD_API epd_status_t ep_unpermute(const void *expert_out, int64_t capacity_rows,
                           const int32_t *output_index, const float *topk_weights, int num_tokens,
                           int num_topk, int hidden, void *y, int32_t *status, epd_stream_t stream);
+
+/* ------------------------------------------------------------------ routing
+ * The step before the layout: topk_idx and topk_weights from router logits. */
+typedef enum {
+    EPD_SCORE_SOFTMAX = 0, /* s[t, e] = exp(l[t, e] - max) / sum over the row */
+    EPD_SCORE_SIGMOID = 1, /* s[t, e] = 1 / (1 + exp(-l[t, e])) */
+} epd_scoring_t;
+
+typedef enum {
+    EPD_GROUP_MAX = 0,  /* a group scores as its best expert */
+    EPD_GROUP_TOP2 = 1, /* a group scores as the sum of its two best experts */
+} epd_group_score_t;
+
+#define EPD_MAX_GROUPS 64
+
+/*
+ * Routing to experts. For every token, from its logits l[t, 0..E):
+ *   s = softmax(l) or sigmoid(l) (fp32);
+ *   c = s + bias (the balance bias; it takes part in the choice only, not in the
+ *       weights; NULL for none);
+ *   the experts form num_groups equal runs of consecutive experts; the topk_groups
+ *       groups with the highest group score stay (all of them where topk_groups ==
+ *       num_groups); EPD_GROUP_TOP2 sums what a group has where that is one expert;
+ *   topk_idx[t, 0..k) = the k experts of those groups with the highest c, highest
+ *       first; equal values go to the lowest index, for groups and for experts;
+ *   topk_weights[t, j] = s[topk_idx[t, j]], divided by their sum over j if
+ *       `renormalize` (0 where that sum is 0), times routed_scale.
+ * Softmax scores without a bias are compared by their logits, which order them
+ * exactly as the scores do but never round two different ones to the same value.
+ * An expert whose logit is -inf cannot be chosen; where fewer than k are left the
+ * rest of the row is -1 with weight 0 (the type's lowest finite value is an ordinary
+ * logit). A NaN or +inf logit sets EPD_ERR_NONFINITE in *status and counts as -inf.
+ *   logits: [T, E] float32 (EPD_F32) or bfloat16 (EPD_BF16);  bias: [E] float32;
+ *   topk_idx: [T, k] int64;  topk_weights: [T, k] float32.
+ * E in [1, EPD_MAX_EXPERTS], k in [1, min(E, EPD_MAX_TOPK)], num_groups in
+ * [1, EPD_MAX_GROUPS] dividing E, topk_groups in [1, num_groups].
+ */
+EPD_API epd_status_t ep_route(const void *logits, epd_dtype_t dtype, const float *bias,
+                              int num_tokens, int num_topk, int num_experts, int num_groups,
+                              int topk_groups, epd_group_score_t group_score,
+                              epd_scoring_t scoring, int renormalize, float routed_scale,
+                              int64_t *topk_idx, float *topk_weights, int32_t *status,
+                              epd_stream_t stream);
+
+/*
+ * Gradient of the weights of ep_route with respect to the logits (the choice itself
+ * has none, and the bias does not enter the weights). With g = routed_scale *
+ * grad_weights[t, :] and S the sum of the picks' scores:
+ *   ds[topk_idx[t, j]] += g_j                                     (no renormalize)
+ *                      += sum over i of (g_j - g_i) s_i / S / S   (renormalize),
+ *   grad_logits = ds * s * (1 - s)                                (sigmoid)
+ *               = s * (ds - sum over e of ds_e s_e)               (softmax).
+ * Picks of -1 have no gradient; an id outside [-1, E) sets EPD_ERR_INVALID_EXPERT and
+ * counts as -1. Every element of grad_logits [T, E] (the logits' type) is written, 0
+ * for an expert that cannot be chosen. An expert that a row picks twice gets both
+ * picks' terms.
+ */
+EPD_API epd_status_t ep_route_backward(const float *grad_weights, const void *logits,
+                                       epd_dtype_t dtype, const int64_t *topk_idx, int num_tokens,
+                                       int num_topk, int num_experts, epd_scoring_t scoring,
+                                       int renormalize, float routed_scale, void *grad_logits,
+                                       int32_t *status, epd_stream_t stream);
+
+/* ------------------------------------------------------- the experts' products
+ * Matrix products over the expert-contiguous buffer that ep_permute fills (or the
+ * rectangles of ep_permute_lowlatency), between permute and combine. */
+
+/*
+ * Where each expert's rows lie. Expert e owns rows [start, start + tokens_per_expert[e])
+ * with start = expert_start_loc[e], or e * rows_per_expert where expert_start_loc is NULL
+ * (rectangles). The counts and starts are device memory, read by the kernel: nothing goes
+ * back to the host. Regions must not overlap. A negative count or start sets
+ * EPD_ERR_INVALID_ARG in *status and counts as no rows; a region that does not end within
+ * capacity_rows (or within its rectangle) sets EPD_ERR_CAPACITY and is cut there.
+ */
+typedef struct {
+    int num_experts;
+    int64_t capacity_rows;            /* rows of every row buffer of the call, <= INT32_MAX */
+    int64_t rows_per_expert;          /* rectangles only: E * rows_per_expert <= capacity_rows */
+    const int32_t *expert_start_loc;  /* device [E], or NULL */
+    const int32_t *tokens_per_expert; /* device [E] */
+} epd_expert_rows_t;
+
+typedef enum {
+    EPD_ACT_NONE = 0,
+    EPD_ACT_RELU = 1,
+    EPD_ACT_SILU = 2,   /* z * sigmoid(z) */
+    EPD_ACT_GELU = 3,   /* z * Phi(z), the exact form with erf */
+    EPD_ACT_SWIGLU = 4, /* silu(gate) * up: the weight has 2N rows, gate first, then up */
+} epd_activation_t;
+
+/*
+ * The experts' product with its epilogue. For every row s of expert e:
+ *   z[s, :] = x[s, :] . w[e]^T + bias[e]           (fp32 accumulation)
+ *   y[s, :] = bf16( act(z[s, :]) + residual[s, :] )
+ * and, where `preact` is given, preact[s, :] = bf16(z[s, :]) for the backward pass.
+ * Rows that belong to no expert are not written. Each value is rounded once, from fp32;
+ * the result does not depend on how blocks are scheduled.
+ *   x: [capacity_rows, K] bfloat16 (K % 8 == 0), or e4m3 (K % 128 == 0) with
+ *      x_scale, one fp32 scale per row and 128 columns: the scale of row s of expert e and
+ *      column block c is x_scale[s * scale_row_stride + c * scale_col_stride + e *
+ *      scale_expert_stride] -- (K/128, 1, 0) for the rows of ep_permute, (1, scale_ld, 0)
+ *      for its column-major scales and (1, rows, (K/128 - 1) * rows) for the rectangles of
+ *      ep_permute_lowlatency;
+ *   w: [E, NW, K] of x's type, NW = N (2N for EPD_ACT_SWIGLU); with e4m3 w_scale is
+ *      [E, ceil(NW/128), K/128] float32, one scale per 128 x 128 block;
+ *   bias: [E, NW] float32 or NULL; residual: [capacity_rows, N] bfloat16 or NULL;
+ *   y: [capacity_rows, N], preact: [capacity_rows, NW] bfloat16 (preact may be NULL).
+ * N % 8 == 0; for EPD_ACT_SWIGLU N % 16 == 0, with e4m3 N % 128 == 0. All row buffers and w
+ * 16-byte aligned. One expert over the whole buffer is an ordinary linear layer.
+ */
+EPD_API epd_status_t ep_expert_matmul(const epd_expert_rows_t *rows, const void *x,
+                                      epd_dtype_t dtype, const float *x_scale,
+                                      int64_t scale_row_stride, int64_t scale_col_stride,
+                                      int64_t scale_expert_stride, const void *w,
+                                      const float *w_scale, int in_features, int out_features,
+                                      epd_activation_t activation, const float *bias,
+                                      const void *residual, void *y, void *preact,
+                                      int32_t *status, epd_stream_t stream);
+
+/*
+ * Gradient of the product's input, with the gradient of the activation that made the input in
+ * its epilogue. For every row s of expert e, with d[s, :] = dy[s, :] . w[e] (fp32):
+ *   dx[s, :] = d[s, :]                                     (EPD_ACT_NONE, preact NULL)
+ *            = d[s, :] * act'(preact[s, :])                (the gradient of preact)
+ *            = [d * up * silu'(gate), d * silu(gate)]      (EPD_ACT_SWIGLU, 2K columns)
+ * rounded once to bfloat16.
+ *   dy: [capacity_rows, N], w: [E, N, K], dx and preact: [capacity_rows, K or 2K], all
+ *   bfloat16 and 16-byte aligned; N % 8 == 0, K % 8 == 0.
+ */
+EPD_API epd_status_t ep_expert_matmul_dgrad(const epd_expert_rows_t *rows, const void *dy,
+                                            const void *w, int in_features, int out_features,
+                                            epd_activation_t activation, const void *preact,
+                                            void *dx, int32_t *status, epd_stream_t stream);
+
+/*
+ * Gradients of the weights and the bias: for every expert e
+ *   dw[e] = sum over its rows s of dy[s, :]^T x[s, :]   (fp32, rounded once to bfloat16)
+ *   dbias[e] = sum over its rows s of dy[s, :]          (float32; NULL to leave it out)
+ * in an order that depends on the row numbers alone; 0 for an expert without rows. Rows outside the experts' regions
+ * are not used, whatever they hold.
+ *   dy: [capacity_rows, N], x: [capacity_rows, K], dw: [E, N, K] bfloat16, 16-byte aligned;
+ *   dbias: [E, N] float32; N % 8 == 0, K % 8 == 0.
+ */
+EPD_API epd_status_t ep_expert_matmul_wgrad(const epd_expert_rows_t *rows, const void *dy,
+                                            const void *x, int in_features, int out_features,
+                                            void *dw, float *dbias, int32_t *status,
+                                            epd_stream_t stream);
+
+/*
+ * Gradient of the combine (ep_unpermute). For every pair with slot = output_index[t, j]:
+ *   grad_expert_out[slot, :] = bf16( topk_weights[t, j] * grad_y[t, :] )
+ *   grad_weights[t, j]       = sum over h of grad_y[t, h] * expert_out[slot, h]   (fp32)
+ * and grad_weights[t, j] = 0 where output_index is -1. Rows of grad_expert_out that no pair
+ * fills are not written (the products above do not read them). The gradient of ep_permute's
+ * input is ep_unpermute of the rows' gradients with weights of 1.
+ *   grad_y: [T, H], expert_out and grad_expert_out: [capacity_rows, H] bfloat16, 16-byte
+ *   aligned, H % 8 == 0; topk_weights and grad_weights: [T, k] float32.
+ * A slot outside [-1, capacity_rows) sets EPD_ERR_CAPACITY and is skipped.
+ */
+EPD_API epd_status_t ep_unpermute_backward(const void *grad_y, const void *expert_out,
+                                           int64_t capacity_rows, const int32_t *output_index,
+                                           const float *topk_weights, int num_tokens,
+                                           int num_topk, int hidden, void *grad_expert_out,
+                                           float *grad_weights, int32_t *status,
+                                           epd_stream_t stream);
 
 /*
  * Allocation-free variant of ep_dispatch_layout. The pages have no counterpart:

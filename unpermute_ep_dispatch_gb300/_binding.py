@@ -26,10 +26,16 @@ EPD_ERR_CUDA = 3
 EPD_ERR_INVALID_EXPERT = 4
 EPD_ERR_TIMEOUT = 5
 EPD_ERR_CAPACITY = 6
+EPD_ERR_NONFINITE = 7
 EPD_BF16 = 0
 EPD_FP8_E4M3 = 1
+EPD_F32 = 2
 EPD_MAX_EXPERTS = 4096
 EPD_MAX_TOPK = 64
+EPD_MAX_GROUPS = 64
+SCORING = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORE = {"max": 0, "top2": 1}
+ACTIVATION = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 4}
 
 class PermuteView(ctypes.Structure):
     """epd_permute_view_t."""
@@ -38,9 +44,18 @@ class PermuteView(ctypes.Structure):
                 ("scale_ld", ctypes.c_int64)]
 
 
+class ExpertRows(ctypes.Structure):
+    """epd_expert_rows_t."""
+    _fields_ = [("num_experts", ctypes.c_int), ("capacity_rows", ctypes.c_int64),
+                ("rows_per_expert", ctypes.c_int64), ("expert_start_loc", ctypes.c_void_p),
+                ("tokens_per_expert", ctypes.c_void_p)]
+
+
 # name -> (restype, argtypes); mirrors include/epd.h
 _P, _I, _I64, _U32, _SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint32,
                            ctypes.c_size_t)
+_F = ctypes.c_float
+_ROWS = ctypes.POINTER(ExpertRows)
 SIGNATURES = {
     "epd_status_string": (ctypes.c_char_p, [_I]),
     "epd_version": (_I, []),
@@ -62,6 +77,13 @@ SIGNATURES = {
                                    _P, _P]),
     "ep_dispatch_lowlatency": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I64, _P, _P, _P, _P,
                                     _P, _P, _P, _P]),
+    "ep_route": (_I, [_P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P]),
+    "ep_route_backward": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _I, _F, _P, _P, _P]),
+    "ep_expert_matmul": (_I, [_ROWS, _P, _I, _P, _I64, _I64, _I64, _P, _P, _I, _I, _I, _P, _P, _P,
+                              _P, _P, _P]),
+    "ep_expert_matmul_dgrad": (_I, [_ROWS, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
+    "ep_expert_matmul_wgrad": (_I, [_ROWS, _P, _P, _I, _I, _P, _P, _P, _P]),
+    "ep_unpermute_backward": (_I, [_P, _P, _I64, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
     "ep_dispatch_layout_noalloc": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
     "epd_test_layout_stalled_tile": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _I,
                                           _U32, _P]),
@@ -540,6 +562,242 @@ def ep_unpermute(expert_out: torch.Tensor, output_index: torch.Tensor,
                                      T, k, H, _ptr(y), _ptr(status), _stream(stream, dev))
     _check(rc, "ep_unpermute")
     return y
+
+
+# ----------------------------------------------------------------------------- routing
+def _choose(table, key, name):
+    try:
+        return table[key]
+    except KeyError:
+        raise ValueError(f"{name} must be one of {sorted(table)}, got {key!r}") from None
+
+
+def _logits(t):
+    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits must be a float32 or bfloat16 tensor")
+    _want(t, "logits", t.dtype)
+    if t.dim() != 2:
+        raise ValueError("logits must be [num_tokens, num_experts]")
+    return EPD_F32 if t.dtype == torch.float32 else EPD_BF16
+
+
+def ep_route(logits: torch.Tensor, num_topk: int, status: torch.Tensor, scoring: str = "softmax",
+             bias: Optional[torch.Tensor] = None, num_groups: int = 1, topk_groups: int = 1,
+             group_score: str = "max", renormalize: bool = True, routed_scale: float = 1.0,
+             topk_idx=None, topk_weights=None, stream=None):
+    """Routing: the picks of ep_dispatch_layout and the weights of ep_unpermute from router
+    logits [T, E] (float32 or bfloat16). scoring: "softmax" or "sigmoid"; bias [E] float32
+    takes part in the choice only; group_score: "max" or "top2". Returns (topk_idx [T, k]
+    int64, topk_weights [T, k] float32); see epd.h."""
+    dt = _logits(logits)
+    sc = _choose(SCORING, scoring, "scoring")
+    gs = _choose(GROUP_SCORE, group_score, "group_score")
+    dev = logits.device
+    T, E = logits.shape
+    k = int(num_topk)
+    _want(status, "status", torch.int32, (1,), dev)
+    if bias is not None:
+        _want(bias, "bias", torch.float32, (E,), dev)
+    topk_idx = _out(topk_idx, "topk_idx", torch.int64, (T, k), dev)
+    topk_weights = _out(topk_weights, "topk_weights", torch.float32, (T, k), dev)
+    rc = load_library().ep_route(_ptr(logits), dt, _ptr(bias), T, k, E, int(num_groups),
+                                 int(topk_groups), gs, sc, int(bool(renormalize)),
+                                 float(routed_scale), _ptr(topk_idx), _ptr(topk_weights),
+                                 _ptr(status), _stream(stream, dev))
+    _check(rc, "ep_route")
+    return topk_idx, topk_weights
+
+
+def ep_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor,
+                      status: torch.Tensor, scoring: str = "softmax", renormalize: bool = True,
+                      routed_scale: float = 1.0, grad_logits=None, stream=None):
+    """Gradient of ep_route's weights with respect to its logits, for the same options.
+    Returns grad_logits [T, E] of the logits' type."""
+    dt = _logits(logits)
+    sc = _choose(SCORING, scoring, "scoring")
+    dev = logits.device
+    T, E = logits.shape
+    _want(topk_idx, "topk_idx", torch.int64, device=dev)
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError("topk_idx must be [T, k] with the T of logits")
+    k = topk_idx.shape[1]
+    _want(grad_weights, "grad_weights", torch.float32, (T, k), dev)
+    _want(status, "status", torch.int32, (1,), dev)
+    grad_logits = _out(grad_logits, "grad_logits", logits.dtype, (T, E), dev)
+    rc = load_library().ep_route_backward(_ptr(grad_weights), _ptr(logits), dt, _ptr(topk_idx), T,
+                                          k, E, sc, int(bool(renormalize)), float(routed_scale),
+                                          _ptr(grad_logits), _ptr(status), _stream(stream, dev))
+    _check(rc, "ep_route_backward")
+    return grad_logits
+
+
+# ----------------------------------------------------------------------------- experts' products
+def _expert_rows(x, E, tokens_per_expert, expert_start_loc, dev):
+    """epd_expert_rows_t of row buffers shaped like x: [M, *] with expert_start_loc, or the
+    rectangles [E, rows, *] without."""
+    _want(tokens_per_expert, "tokens_per_expert", torch.int32, (E,), dev)
+    if x.dim() == 3:
+        if expert_start_loc is not None:
+            raise ValueError("rectangles [E, rows, *] take no expert_start_loc")
+        if x.shape[0] != E:
+            raise ValueError(f"rectangles must be [{E}, rows, *], got {tuple(x.shape)}")
+        return ExpertRows(E, E * x.shape[1], x.shape[1], None, tokens_per_expert.data_ptr())
+    if x.dim() != 2:
+        raise ValueError("rows must be [M, *], or [E, rows, *] rectangles")
+    if expert_start_loc is None:
+        raise ValueError("rows [M, *] need expert_start_loc")
+    _want(expert_start_loc, "expert_start_loc", torch.int32, (E,), dev)
+    return ExpertRows(E, x.shape[0], 0, expert_start_loc.data_ptr(), tokens_per_expert.data_ptr())
+
+
+def ep_expert_matmul(x: torch.Tensor, w: torch.Tensor, tokens_per_expert: torch.Tensor,
+                     status: torch.Tensor, expert_start_loc: Optional[torch.Tensor] = None,
+                     x_scale: Optional[torch.Tensor] = None,
+                     w_scale: Optional[torch.Tensor] = None, scale_col_major: bool = False,
+                     bias: Optional[torch.Tensor] = None, activation: str = "none",
+                     residual: Optional[torch.Tensor] = None, y=None, preact=None,
+                     with_preact: bool = False, stream=None):
+    """The experts' product y = act(x w^T + bias) + residual over the rows that ep_permute
+    laid out (x [M, K] with expert_start_loc) or the low-latency rectangles (x [E, rows, K]).
+    w: [E, N, K], or [E, 2N, K] (gate, then up) for "swiglu". bfloat16, or float8_e4m3fn
+    with w_scale [E, ceil(NW/128), K/128] and x_scale [M, K/128] (scale_col_major: [K/128,
+    ld]; rectangles: [E, K/128, rows]) float32. bias [E, NW] float32, residual like y.
+    activation: "none", "relu", "silu", "gelu" or "swiglu". Returns (y [M, N] or
+    [E, rows, N] bfloat16, preact [.., NW] bfloat16 or None); see epd.h."""
+    act = _choose(ACTIVATION, activation, "activation")
+    if x.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError(f"x must be bfloat16 or float8_e4m3fn, got {x.dtype}")
+    _want(x, "x", x.dtype)
+    dev = x.device
+    _want(w, "w", x.dtype, device=dev)
+    if w.dim() != 3 or w.shape[2] != x.shape[-1]:
+        raise ValueError(f"w must be [E, N, {x.shape[-1]}], got {tuple(w.shape)}")
+    E, NW, K = w.shape
+    if act == 4 and NW % 2:
+        raise ValueError("swiglu weights have an even number of rows")
+    N = NW // 2 if act == 4 else NW
+    rows = _expert_rows(x, E, tokens_per_expert, expert_start_loc, dev)
+    _want(status, "status", torch.int32, (1,), dev)
+    lead = tuple(x.shape[:-1])
+    srow = scol = sexp = 0
+    if x.dtype == torch.float8_e4m3fn:
+        C = K // 128
+        if x_scale is None or w_scale is None:
+            raise ValueError("fp8 rows need x_scale and w_scale")
+        _want(w_scale, "w_scale", torch.float32, (E, (NW + 127) // 128, C), dev)
+        if x.dim() == 3:
+            R = x.shape[1]
+            _want(x_scale, "x_scale", torch.float32, (E, C, R), dev)
+            srow, scol, sexp = 1, R, (C - 1) * R
+        elif scale_col_major:
+            _want(x_scale, "x_scale", torch.float32, device=dev)
+            if x_scale.dim() != 2 or x_scale.shape[0] != C or x_scale.shape[1] < x.shape[0]:
+                raise ValueError(f"x_scale must be [{C}, ld >= {x.shape[0]}]")
+            srow, scol = 1, x_scale.shape[1]
+        else:
+            _want(x_scale, "x_scale", torch.float32, (x.shape[0], C), dev)
+            srow, scol = C, 1
+        dt = EPD_FP8_E4M3
+    else:
+        if x_scale is not None or w_scale is not None:
+            raise ValueError("bf16 rows take no scales")
+        dt = EPD_BF16
+    if bias is not None:
+        _want(bias, "bias", torch.float32, (E, NW), dev)
+    if residual is not None:
+        _want(residual, "residual", torch.bfloat16, (*lead, N), dev)
+    y = _out(y, "y", torch.bfloat16, (*lead, N), dev)
+    if preact is not None or with_preact:
+        preact = _out(preact, "preact", torch.bfloat16, (*lead, NW), dev)
+    rc = load_library().ep_expert_matmul(
+        ctypes.byref(rows), _ptr(x), dt, _ptr(x_scale), srow, scol, sexp, _ptr(w), _ptr(w_scale),
+        K, N, act, _ptr(bias), _ptr(residual), _ptr(y), _ptr(preact), _ptr(status),
+        _stream(stream, dev))
+    _check(rc, "ep_expert_matmul")
+    return y, preact
+
+
+def ep_expert_matmul_dgrad(dy: torch.Tensor, w: torch.Tensor, tokens_per_expert: torch.Tensor,
+                           status: torch.Tensor, expert_start_loc: Optional[torch.Tensor] = None,
+                           activation: str = "none", preact: Optional[torch.Tensor] = None,
+                           dx=None, stream=None):
+    """Gradient of ep_expert_matmul's x, dy w, times the gradient of the activation that made
+    x from `preact` ([.., K], or [.., 2K] for "swiglu"; "none" takes no preact). dy: [M, N] or
+    [E, rows, N], w: [E, N, K], bfloat16. Returns dx, shaped like preact (or [.., K])."""
+    act = _choose(ACTIVATION, activation, "activation")
+    _want(dy, "dy", torch.bfloat16)
+    dev = dy.device
+    _want(w, "w", torch.bfloat16, device=dev)
+    if w.dim() != 3 or w.shape[1] != dy.shape[-1]:
+        raise ValueError(f"w must be [E, {dy.shape[-1]}, K], got {tuple(w.shape)}")
+    E, N, K = w.shape
+    rows = _expert_rows(dy, E, tokens_per_expert, expert_start_loc, dev)
+    _want(status, "status", torch.int32, (1,), dev)
+    shape = (*dy.shape[:-1], 2 * K if act == 4 else K)
+    if act:
+        _want(preact, "preact", torch.bfloat16, shape, dev)
+    elif preact is not None:
+        raise ValueError('activation "none" takes no preact')
+    dx = _out(dx, "dx", torch.bfloat16, shape, dev)
+    rc = load_library().ep_expert_matmul_dgrad(ctypes.byref(rows), _ptr(dy), _ptr(w), K, N, act,
+                                               _ptr(preact), _ptr(dx), _ptr(status),
+                                               _stream(stream, dev))
+    _check(rc, "ep_expert_matmul_dgrad")
+    return dx
+
+
+def ep_expert_matmul_wgrad(dy: torch.Tensor, x: torch.Tensor, tokens_per_expert: torch.Tensor,
+                           status: torch.Tensor, expert_start_loc: Optional[torch.Tensor] = None,
+                           dw=None, dbias=None, with_dbias: bool = False, stream=None):
+    """Gradients of ep_expert_matmul's weights and bias: dw[e] = dy_e^T x_e [E, N, K] bfloat16
+    and dbias[e] = the sum of dy's rows [E, N] float32 (or None). dy: [M, N], x: [M, K] (or
+    rectangles) bfloat16."""
+    _want(dy, "dy", torch.bfloat16)
+    dev = dy.device
+    _want(x, "x", torch.bfloat16, device=dev)
+    if x.shape[:-1] != dy.shape[:-1]:
+        raise ValueError("dy and x must have the same rows")
+    if not isinstance(tokens_per_expert, torch.Tensor) or tokens_per_expert.dim() != 1:
+        raise ValueError("tokens_per_expert must be [E]")
+    E = tokens_per_expert.shape[0]
+    N, K = dy.shape[-1], x.shape[-1]
+    rows = _expert_rows(dy, E, tokens_per_expert, expert_start_loc, dev)
+    _want(status, "status", torch.int32, (1,), dev)
+    dw = _out(dw, "dw", torch.bfloat16, (E, N, K), dev)
+    if dbias is not None or with_dbias:
+        dbias = _out(dbias, "dbias", torch.float32, (E, N), dev)
+    rc = load_library().ep_expert_matmul_wgrad(ctypes.byref(rows), _ptr(dy), _ptr(x), K, N,
+                                               _ptr(dw), _ptr(dbias), _ptr(status),
+                                               _stream(stream, dev))
+    _check(rc, "ep_expert_matmul_wgrad")
+    return dw, dbias
+
+
+def ep_unpermute_backward(grad_y: torch.Tensor, expert_out: torch.Tensor,
+                          output_index: torch.Tensor, topk_weights: torch.Tensor,
+                          status: torch.Tensor, grad_expert_out=None, grad_weights=None,
+                          stream=None):
+    """Gradient of ep_unpermute. Returns (grad_expert_out [M, H] bf16, rows that no pair fills
+    not written; grad_weights [T, k] float32)."""
+    _want(expert_out, "expert_out", torch.bfloat16)
+    if expert_out.dim() != 2:
+        raise ValueError("expert_out must be [M, H]")
+    dev = expert_out.device
+    M, H = expert_out.shape
+    _want(output_index, "output_index", torch.int32, device=dev)
+    if output_index.dim() != 2:
+        raise ValueError("output_index must be [T, k]")
+    T, k = output_index.shape
+    _want(grad_y, "grad_y", torch.bfloat16, (T, H), dev)
+    _want(topk_weights, "topk_weights", torch.float32, (T, k), dev)
+    _want(status, "status", torch.int32, (1,), dev)
+    grad_expert_out = _out(grad_expert_out, "grad_expert_out", torch.bfloat16, (M, H), dev)
+    grad_weights = _out(grad_weights, "grad_weights", torch.float32, (T, k), dev)
+    rc = load_library().ep_unpermute_backward(
+        _ptr(grad_y), _ptr(expert_out), M, _ptr(output_index), _ptr(topk_weights), T, k, H,
+        _ptr(grad_expert_out), _ptr(grad_weights), _ptr(status), _stream(stream, dev))
+    _check(rc, "ep_unpermute_backward")
+    return grad_expert_out, grad_weights
 
 
 def ep_dispatch_layout_noalloc(topk_idx: torch.Tensor, num_experts: int, num_ranks: int,

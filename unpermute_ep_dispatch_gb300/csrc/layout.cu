@@ -1064,13 +1064,14 @@ const char *epd_status_string(int code) {
         case EPD_ERR_UNSUPPORTED: return "unsupported size";
         case EPD_ERR_CUDA: return "CUDA launch error";
         case EPD_ERR_INVALID_EXPERT: return "expert id outside [-1, E)";
-        case EPD_ERR_TIMEOUT: return "look-back wait gave up";
+        case EPD_ERR_TIMEOUT: return "look-back or pipeline wait gave up";
         case EPD_ERR_CAPACITY: return "slot outside the permuted buffer";
+        case EPD_ERR_NONFINITE: return "NaN or +inf router logit";
         default: return "unknown status";
     }
 }
 
-int epd_version(void) { return 10000; }
+int epd_version(void) { return 10100; }
 
 int epd_last_cuda_error(void) { return epd::last_cuda_error(); }
 
