@@ -316,7 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t acc_full = tail + 8 * kStages, acc_empty = acc_full + 16;
     const uint32_t sc_full = acc_empty + 16, sc_empty = sc_full + 16, slot = sc_empty + 16;
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int rank = (int)cluster_ctarank();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -353,47 +353,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp >= kEpilogueWarps) {
     if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kProducerWarp) {
-        const uint32_t lead_full = map_to_rank(full, 0);
+        const uint32_t lead_full = map_to_rank(full, 0), own_tail = map_to_rank(tail, rank);
         int stage = 0, issued = 0;
         uint32_t parity = 1;
         for (int tile = pair; ok && walk.next(tile, t); tile += pairs) {
             const int half = t.n / 2;
             const int boxes = MODE == kWgrad ? (half + 63) / 64 : (half + kRowBox - 1) / kRowBox;
             const uint32_t bytes = kOperandBytes + boxes * (MODE == kWgrad ? 64 : kRowBox) * 128;
-            for (int k = 0; k < t.steps; ++k) {
-                if (!(ok = mbar_wait_cluster(empty + 8 * stage, parity))) break;
-                if (lane == 0) {
-                    const uint32_t a = base + stage * kStageBytes, b = a + kOperandBytes;
+            // one thread runs the tile's steps, the warp rejoins for the next tile
+            if (elect_one()) {
+                const int feat = t.feat0 + rank * (kHalf ? 64 : 128);
+                const int row = t.row0 + rank * half;
+                int st = stage;
+                uint32_t ph = parity;
+                for (int k = 0; k < t.steps; ++k) {
+                    if (!(ok = mbar_wait_cluster(empty + 8 * st, ph))) break;
+                    const uint32_t a = base + st * kStageBytes, b = a + kOperandBytes;
                     // a ragged last step of wgrad completes on this block's own barrier: its
                     // rows past the region are cleared before the pair sees the stage
                     const bool ragged = MODE == kWgrad && k == t.steps - 1 && (t.count & 63) != 0;
-                    uint32_t bar = lead_full + 8 * stage;
-                    if (ragged) bar = map_to_rank(tail, rank) + 8 * stage;
+                    const uint32_t bar = (ragged ? own_tail : lead_full) + 8 * st;
                     mbar_arrive_tx_cluster(bar, bytes);
                     if (MODE == kForward) {
                         if (kHalf)
-                            tma_5d(a, &map_m, k * kStep, 0, 0, (t.feat0 + rank * 64) / 16, t.e, bar);
+                            tma_5d(a, &map_m, k * kStep, 0, 0, feat / 16, t.e, bar);
                         else
-                            tma_3d(a, &map_m, k * kStep, t.feat0 + rank * 128, t.e, bar);
+                            tma_3d(a, &map_m, k * kStep, feat, t.e, bar);
                     } else if (MODE == kDgrad) {
-                        tma_3d(a, &map_m, t.feat0 + rank * 128, k * kStep, t.e, bar);
-                        tma_3d(a + 8192, &map_m, t.feat0 + rank * 128 + 64, k * kStep, t.e, bar);
+                        tma_3d(a, &map_m, feat, k * kStep, t.e, bar);
+                        tma_3d(a + 8192, &map_m, feat + 64, k * kStep, t.e, bar);
                     } else {
-                        tma_2d(a, &map_m, t.feat0 + rank * 128, t.start + k * kStep, bar);
-                        tma_2d(a + 8192, &map_m, t.feat0 + rank * 128 + 64, t.start + k * kStep, bar);
+                        tma_2d(a, &map_m, feat, t.start + k * kStep, bar);
+                        tma_2d(a + 8192, &map_m, feat + 64, t.start + k * kStep, bar);
                     }
                     for (int i = 0; i < boxes; ++i) {
                         if (MODE == kWgrad)
-                            tma_2d(b + i * 8192, &map_n, t.row0 + rank * half + i * 64, t.start + k * kStep, bar);
+                            tma_2d(b + i * 8192, &map_n, row + i * 64, t.start + k * kStep, bar);
                         else
-                            tma_2d(b + i * kRowBox * 128, &map_n, k * kStep,
-                                   t.start + t.row0 + rank * half + i * kRowBox, bar);
+                            tma_2d(b + i * kRowBox * 128, &map_n, k * kStep, t.start + row + i * kRowBox, bar);
                     }
+                    if (++st == kStages) st = 0, ph ^= 1;
                 }
-                __syncwarp();
-                ++issued;
-                if (++stage == kStages) stage = 0, parity ^= 1;
             }
+            ok = __all_sync(0xffffffffu, ok);
+            issued += t.steps;
+            stage += t.steps;
+            parity ^= (stage / kStages) & 1;
+            stage %= kStages;
         }
         // the last stages' releases arrive before this block may go
         for (int i = 0; ok && i < min(issued, kStages); ++i) {
@@ -404,34 +410,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (rank == 0) {
             int stage = 0, buf = 0;
             uint32_t parity = 0, acc_parity = 1;
+            const uint64_t desc_a = smem_desc(base, 8192), desc_b = smem_desc(base + kOperandBytes, 8192);
             for (int tile = pair; ok && walk.next(tile, t); tile += pairs) {
                 if (t.steps == 0) continue;
                 const uint32_t desc = mma_desc<FP8, MODE != kForward, MODE == kWgrad>(t.n);
-                for (int k = 0; k < t.steps; ++k) {
-                    const bool fresh = FP8 || k == 0;
-                    if (fresh && !(ok = mbar_wait_cluster(acc_empty + 8 * buf, acc_parity))) break;
-                    if (!(ok = mbar_wait_cluster(full + 8 * stage, parity))) break;
-                    tcgen05_fence_after();
-                    if (lane == 0) {
-                        const uint32_t a = base + stage * kStageBytes, b = a + kOperandBytes;
-                        const uint64_t da = smem_desc(a, 8192), db = smem_desc(b, 8192);
-                        const uint32_t d = tmem + buf * kTileRows;
+                if (elect_one()) {
+                    int st = stage, bf = buf;
+                    uint32_t ph = parity, aph = acc_parity;
+                    for (int k = 0; k < t.steps; ++k) {
+                        const bool fresh = FP8 || k == 0, last = FP8 || k == t.steps - 1;
+                        if (fresh && !(ok = mbar_wait_cluster(acc_empty + 8 * bf, aph))) break;
+                        if (!(ok = mbar_wait_cluster(full + 8 * st, ph))) break;
+                        if (MODE == kWgrad && k == t.steps - 1 && (t.count & 63)) fence_acquire_cluster();
+                        tcgen05_fence_after();
                         // a quarter of the stage's reduction: 32 bytes along a K-major row, or
                         // 16 rows of 128 bytes
                         constexpr uint64_t kA = MODE != kForward ? 128 : 2, kB = MODE == kWgrad ? 128 : 2;
+                        const uint64_t da = desc_a + (uint32_t)(st * (kStageBytes >> 4));
+                        const uint64_t db = desc_b + (uint32_t)(st * (kStageBytes >> 4));
+                        const uint32_t d = tmem + bf * kTileRows;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            mma_pair<FP8>(d, da + q * kA, db + q * kB, desc, !(fresh && q == 0));
-                        mma_commit_pair(empty + 8 * stage);
-                        if (FP8 || k == t.steps - 1) mma_commit_pair(acc_full + 8 * buf);
-                    }
-                    __syncwarp();
-                    if (++stage == kStages) stage = 0, parity ^= 1;
-                    if (FP8 || k == t.steps - 1) {
-                        buf ^= 1;
-                        if (buf == 0) acc_parity ^= 1;
+                        for (int q = 0; q < 4; ++q) mma_pair<FP8>(d, da + q * kA, db + q * kB, desc, !(fresh && q == 0));
+                        mma_commit_pair(empty + 8 * st);
+                        if (last) {
+                            mma_commit_pair(acc_full + 8 * bf);
+                            bf ^= 1;
+                            if (bf == 0) aph ^= 1;
+                        }
+                        if (++st == kStages) st = 0, ph ^= 1;
                     }
                 }
+                ok = __all_sync(0xffffffffu, ok);
+                stage += t.steps;
+                parity ^= (stage / kStages) & 1;
+                stage %= kStages;
+                buf += FP8 ? t.steps : 1;
+                acc_parity ^= (buf >> 1) & 1;
+                buf &= 1;
             }
         }
     } else if (warp >= kAuxWarp) {
@@ -507,7 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(lead_full + 8 * stage);
+                if (lane == 0) mbar_arrive_release_cluster(lead_full + 8 * stage);
             }
         }
     }
