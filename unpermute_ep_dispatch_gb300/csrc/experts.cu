@@ -36,16 +36,18 @@ namespace {
 
 enum { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
-constexpr int kThreads = 384;
-constexpr int kEpilogueWarps = 8;
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kAuxWarp = 10, kAuxWarps = 2;
+// The epilogue warps, then four of which one feeds TMA, one issues the mma and two are
+// helpers. e4m3 has its sums in registers: 16 warps of 64 columns each.
+template <bool FP8>
+constexpr int kEpiWarpsOf = FP8 ? 16 : 8;
+template <bool FP8>
+constexpr int kThreadsOf = (kEpiWarpsOf<FP8> + 4) * 32;
+constexpr int kAuxWarps = 2;
 constexpr int kTileRows = 256;                  // most token rows (wgrad: output rows) of a tile
 constexpr int kOperandBytes = 128 * 128;        // 128 rows of 128 bytes: one operand of a stage
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kRowBox = 32;                     // token rows per TMA box
-constexpr int kStageStride = 36;                // floats per staged row: conflict-free both ways
-constexpr int kStageCols = 16;
-constexpr int kStagingBytes = kEpilogueWarps * kStageCols * kStageStride * 4;
+constexpr int kStagingBytes = 32 * 80;          // per epilogue warp: 32 rows of 64 bytes, 80 apart
 constexpr int kScaleGroup = 4;                  // reduction steps per group of staged scales
 constexpr int kScaleBytes = 2 * kScaleGroup * 2 * kTileRows * 4;
 constexpr int kGroupTiles = 8;                  // token tiles that share a pass over the features
@@ -54,7 +56,7 @@ template <bool FP8>
 constexpr int kStagesOf = FP8 ? 5 : 6;
 
 template <bool FP8>
-constexpr int kSmemOf = kStagesOf<FP8> *kStageBytes + kStagingBytes + (FP8 ? kScaleBytes : 0) + 512;
+constexpr int kSmemOf = kStagesOf<FP8> *kStageBytes + kEpiWarpsOf<FP8> * kStagingBytes + (FP8 ? kScaleBytes : 0) + 512;
 
 struct ExpertArgs {
     epd_expert_rows_t rows;
@@ -162,154 +164,265 @@ struct Walker {
     }
 };
 
-// What the epilogue needs of a tile's features, for the octet of features of this lane.
-struct Octet {
-    float bias[8], bias_up[8];
-    int feat;
-    bool live;
+// ---------------------------------------------------------------------------- epilogue
+// A warp's 32 features x 32 columns of D are held as fragments f[h][4u + 2i + b]: feature
+// 16h + 8b + lane / 4, column 8u + 4i + lane % 4. Packed to bf16 in pairs over i they are 8 x 8
+// blocks for stmatrix, whose row j is column 8u + 4 (j % 2) + j / 2 of D; it turns them over, so
+// that rows of 32 (a gated product: 16) features lie together and leave for memory 16 bytes a
+// lane. In a gated product's tiles features 0-15
+// of a warp are 16 gate features (h = 0) and 16-31 the same features' up (h = 1).
+using Frag = float[2][16];
+
+constexpr int kPitch = 80;  // bytes per staged row of 64: eight rows fall in different banks
+
+// Row and 16-byte part of this lane in pass `it` over 32 rows of 64 bytes: the two rows of a
+// quarter warp are four apart, which keeps them in different banks.
+__device__ __forceinline__ int lane_row(int it) {
+    const int lane = threadIdx.x & 31;
+    return it * 8 + (lane >> 3) + (lane & 4);
+}
+
+// Column of D within its eight that row j of a block is.
+__device__ __forceinline__ int block_column(int j) { return 4 * (j & 1) + (j >> 1); }
+
+template <int ACT>
+__device__ __forceinline__ void apply(Frag &f) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) f[h][r] = activate<ACT>(f[h][r]);
+}
+
+// Writes the first `rows` of 32 staged rows, `parts` of their four 16-byte parts each, to
+// at + row * pitch. SPLIT: `parts` of the first two there, and of the last two `apart` further.
+template <bool SPLIT = false>
+__device__ __forceinline__ void put_frag(uint32_t stage, const Frag &f, uint8_t *at, int64_t pitch, int rows, int parts,
+                                         int64_t apart = 0) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        stmatrix_t(stage + (u * 8 + block_column(lane & 7)) * kPitch + (lane >> 3) * 16,
+                   pack2_bf16(f[0][4 * u], f[0][4 * u + 2]), pack2_bf16(f[0][4 * u + 1], f[0][4 * u + 3]),
+                   pack2_bf16(f[1][4 * u], f[1][4 * u + 2]), pack2_bf16(f[1][4 * u + 1], f[1][4 * u + 3]));
+    __syncwarp();
+    const int part = lane & 3;
+    const int own = SPLIT ? part & 1 : part;
+    at += own * 16 + (SPLIT && part >= 2 ? apart : 0);
+    const bool live = own < parts;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int row = lane_row(it);
+        const uint4 v = lds16(stage + row * kPitch + part * 16);
+        if (live && row < rows) st16(at + row * pitch, v);
+    }
+}
+
+// The same for the 16 features f[0] of a gated product.
+__device__ __forceinline__ void put_half(uint32_t stage, const Frag &f, uint8_t *at, int64_t pitch, int rows, int parts) {
+    constexpr int kHalfPitch = 48;
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int u = 0; u < 4; u += 2)
+        stmatrix_t(stage + ((u + (lane >> 4)) * 8 + block_column(lane & 7)) * kHalfPitch + ((lane >> 3) & 1) * 16,
+                   pack2_bf16(f[0][4 * u], f[0][4 * u + 2]), pack2_bf16(f[0][4 * u + 1], f[0][4 * u + 3]),
+                   pack2_bf16(f[0][4 * u + 4], f[0][4 * u + 6]), pack2_bf16(f[0][4 * u + 5], f[0][4 * u + 7]));
+    __syncwarp();
+    const int part = lane & 1;
+#pragma unroll
+    for (int it = 0; it < 2; ++it) {
+        const int row = it * 16 + (lane >> 1);
+        const uint4 v = lds16(stage + row * kHalfPitch + part * 16);
+        if (part < parts && row < rows) st16(at + row * pitch + part * 16, v);
+    }
+}
+
+// 32 rows of 64 (32) bytes of a bf16 operand, fetched ahead of their use and then turned into
+// fragments by way of the staging rows. What lies outside is zero.
+struct Ahead {
+    uint4 v[4];
+
+    __device__ __forceinline__ void fetch(const uint8_t *at, int64_t pitch, int rows, int parts) {
+        const int part = threadIdx.x & 3;
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const int row = lane_row(it);
+            v[it] = part < parts && row < rows ? ld_stream16(at + row * pitch + part * 16) : make_uint4(0, 0, 0, 0);
+        }
+    }
+
+    __device__ __forceinline__ void turn(uint32_t stage, uint32_t (&w)[2][8]) const {
+        const int lane = threadIdx.x & 31;
+        __syncwarp();
+#pragma unroll
+        for (int it = 0; it < 4; ++it) sts16(stage + lane_row(it) * kPitch + (lane & 3) * 16, v[it]);
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            ldmatrix_t(stage + (u * 8 + block_column(lane & 7)) * kPitch + (lane >> 3) * 16, w[0][2 * u], w[0][2 * u + 1],
+                       w[1][2 * u], w[1][2 * u + 1]);
+    }
 };
 
+// Element r of fragments f[h] in the words that Ahead::turn gives.
+__device__ __forceinline__ float element(const uint32_t (&w)[8], int r) {
+    const uint32_t v = w[(r >> 2) * 2 + (r & 1)];
+    return r & 2 ? hi_bf16(v) : lo_bf16(v);
+}
+
+__device__ __forceinline__ void load_scales(float4 (&w)[2], const float *at) {
+    w[0] = reinterpret_cast<const float4 *>(at)[0];
+    w[1] = reinterpret_cast<const float4 *>(at)[1];
+}
+
+// A warp's share of a tile's output.
 template <int MODE, bool GATED>
-__device__ __forceinline__ void finish_octet(const ExpertArgs &p, const Tile &t, const Octet &o, int row,
-                                             float (&v)[8], float (&u)[8]) {
-    if (MODE == kWgrad) {
-        st16(p.y + (((int64_t)t.e * p.N + t.row0 + row) * p.K + o.feat) * 2, pack8_bf16(v));
-        return;
-    }
-    const int64_t s = (int64_t)t.start + t.row0 + row;
-    if (MODE == kDgrad) {
-        if (GATED) {
-            const uint8_t *zr = p.preact_in + (s * 2 * p.K + o.feat) * 2;
-            float g[8], up[8];
-            unpack8_bf16(ld_stream16(zr), g);
-            unpack8_bf16(ld_stream16(zr + (int64_t)p.K * 2), up);
+struct Output {
+    static constexpr bool kHalf = GATED && MODE == kForward;
+    const ExpertArgs &p;
+    uint32_t stage;
+    int feat, parts;       // first feature, and how many octets of them exist
+    int rows;              // of the tile
+    int64_t pitch;         // bytes between output rows
+    int64_t row;           // first row of the tile in the row buffers (wgrad: in dw)
+    float bias[2][2];      // of features 16h + 8b + lane / 4
+    Ahead a, b;            // the residual, or dgrad's pre-activations (b: their up part)
+
+    __device__ Output(const ExpertArgs &args, uint32_t stage_) : p(args), stage(stage_) {}
+
+    __device__ __forceinline__ void begin(const Tile &t, int rank, int quadrant) {
+        const int lane = threadIdx.x & 31;
+        const int features = MODE == kForward ? p.N : p.K;
+        feat = t.feat0 + (kHalf ? rank * 64 + quadrant * 16 : rank * 128 + quadrant * 32);
+        parts = max(0, min(kHalf ? 2 : 4, (features - feat) / 8));
+        rows = t.rows;
+        pitch = (int64_t)features * 2 * (MODE == kDgrad && GATED ? 2 : 1);
+        row = (MODE == kWgrad ? (int64_t)t.e * p.N : t.start) + t.row0;
+        if (MODE == kForward && p.bias) {
+            const float *at = p.bias + (int64_t)t.e * p.N * (GATED ? 2 : 1);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                u[i] = v[i] * g[i] * sigmoid_f32(g[i]);
-                v[i] = v[i] * up[i] * activate_grad<EPD_ACT_SWIGLU>(g[i]);
-            }
-            uint8_t *yr = p.y + (s * 2 * p.K + o.feat) * 2;
-            st16(yr, pack8_bf16(v));
-            st16(yr + (int64_t)p.K * 2, pack8_bf16(u));
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    const int f = feat + (kHalf ? 0 : 16 * h) + 8 * o + lane / 4;
+                    bias[h][o] = f < features ? at[f + (kHalf && h ? p.N : 0)] : 0.0f;
+                }
+        }
+    }
+
+    __device__ __forceinline__ void fetch(int col0) {
+        if (MODE == kForward && p.residual)
+            a.fetch(p.residual + (row + col0) * pitch + feat * 2, pitch, rows - col0, parts);
+        if (MODE == kDgrad && p.act != EPD_ACT_NONE) {
+            const uint8_t *z = p.preact_in + (row + col0) * pitch + feat * 2;
+            a.fetch(z, pitch, rows - col0, parts);
+            if (GATED) b.fetch(z + (int64_t)p.K * 2, pitch, rows - col0, parts);
+        }
+    }
+
+    template <int ACT>
+    __device__ __forceinline__ void times_slope(Frag &f, const uint32_t (&z)[2][8]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) f[h][r] *= activate_grad<ACT>(element(z[h], r));
+    }
+
+    // Columns col0 .. col0 + 31; `next` are fetched ahead if there are any.
+    __device__ __forceinline__ void finish(Frag &f, int col0, int next) {
+        uint8_t *at = p.y + (row + col0) * pitch + feat * 2;
+        const int left = rows - col0;
+        if (MODE == kWgrad) {
+            put_frag(stage, f, at, pitch, left, parts);
             return;
         }
-        const int64_t at = (s * p.K + o.feat) * 2;
-        if (p.act != EPD_ACT_NONE) {
-            float z[8];
-            unpack8_bf16(ld_stream16(p.preact_in + at), z);
-            if (p.act == EPD_ACT_RELU) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= activate_grad<EPD_ACT_RELU>(z[i]);
-            } else if (p.act == EPD_ACT_SILU) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= activate_grad<EPD_ACT_SILU>(z[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= activate_grad<EPD_ACT_GELU>(z[i]);
+        if (MODE == kDgrad) {
+            if (p.act == EPD_ACT_NONE) {
+                put_frag(stage, f, at, pitch, left, parts);
+                return;
             }
-        }
-        st16(p.y + at, pack8_bf16(v));
-        return;
-    }
-    const int64_t NW = GATED ? 2 * (int64_t)p.N : p.N;
-    if (p.bias) {
+            uint32_t z[2][8];
+            a.turn(stage, z);
+            if (GATED) {
+                uint32_t u[2][8];
+                b.turn(stage, u);
+                if (next < rows) fetch(next);
+                Frag up;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += o.bias[i];
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const float g = element(z[h], r), w = element(u[h], r);
+                        const float s = fast_sigmoid(g);
+                        up[h][r] = f[h][r] * g * s;
+                        f[h][r] = f[h][r] * w * (s * (1.0f + g * (1.0f - s)));
+                    }
+                put_frag(stage, f, at, pitch, left, parts);
+                put_frag(stage, up, at + (int64_t)p.K * 2, pitch, left, parts);
+                return;
+            }
+            if (next < rows) fetch(next);
+            if (p.act == EPD_ACT_RELU)
+                times_slope<EPD_ACT_RELU>(f, z);
+            else if (p.act == EPD_ACT_SILU)
+                times_slope<EPD_ACT_SILU>(f, z);
+            else
+                times_slope<EPD_ACT_GELU>(f, z);
+            put_frag(stage, f, at, pitch, left, parts);
+            return;
+        }
+        if (p.bias) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) f[h][r] += bias[h][r & 1];
+        }
+        if (p.preact) {
+            const int64_t zp = (int64_t)p.N * 2 * (GATED ? 2 : 1);
+            put_frag<kHalf>(stage, f, p.preact + (row + col0) * zp + feat * 2, zp, left, parts, (int64_t)p.N * 2);
+        }
         if (GATED) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) u[i] += o.bias_up[i];
+            for (int r = 0; r < 16; ++r) f[0][r] = f[0][r] * fast_sigmoid(f[0][r]) * f[1][r];
+        } else if (p.act == EPD_ACT_RELU) {
+            apply<EPD_ACT_RELU>(f);
+        } else if (p.act == EPD_ACT_SILU) {
+            apply<EPD_ACT_SILU>(f);
+        } else if (p.act == EPD_ACT_GELU) {
+            apply<EPD_ACT_GELU>(f);
         }
-    }
-    if (p.preact) {
-        uint8_t *zr = p.preact + (s * NW + o.feat) * 2;
-        st16(zr, pack8_bf16(v));
-        if (GATED) st16(zr + (int64_t)p.N * 2, pack8_bf16(u));
-    }
-    if (GATED) {
+        if (p.residual) {
+            uint32_t z[2][8];
+            a.turn(stage, z);
+            if (next < rows) fetch(next);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] * sigmoid_f32(v[i]) * u[i];
-    } else if (p.act == EPD_ACT_RELU) {
+            for (int h = 0; h < (GATED ? 1 : 2); ++h)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = activate<EPD_ACT_RELU>(v[i]);
-    } else if (p.act == EPD_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = activate<EPD_ACT_SILU>(v[i]);
-    } else if (p.act == EPD_ACT_GELU) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = activate<EPD_ACT_GELU>(v[i]);
-    }
-    const int64_t at = (s * p.N + o.feat) * 2;
-    if (p.residual) {
-        float r[8];
-        unpack8_bf16(ld_stream16(p.residual + at), r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += r[i];
-    }
-    st16(p.y + at, pack8_bf16(v));
-}
-
-// 32 columns of D (thread = feature, v[c] = column c) turned over in shared memory, so that a
-// lane has eight consecutive features of one row and reads and writes 16 bytes at a time. A
-// gated warp's lanes 0-15 are 16 gate features and 16-31 the same features' up.
-template <int MODE, bool GATED>
-__device__ __forceinline__ void finish_columns(const ExpertArgs &p, const Tile &t, const Octet &o, float *stage,
-                                               const float (&v)[32], int col0) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int h = 0; h < 32 / kStageCols; ++h) {
-        const int c0 = col0 + h * kStageCols;
-        if (c0 >= t.rows) break;
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < kStageCols; ++c) stage[c * kStageStride + lane] = v[h * kStageCols + c];
-        __syncwarp();
-        constexpr int kOcts = GATED && MODE == kForward ? 2 : 4;
-#pragma unroll
-        for (int i = 0; i < kStageCols * kOcts / 32; ++i) {
-            const int c = (i * 32 + lane) / kOcts;
-            const float4 *src = reinterpret_cast<const float4 *>(stage + c * kStageStride + (lane % kOcts) * 8);
-            const float4 a = src[0], b = src[1];
-            float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            float u[8];
-            if (GATED && MODE == kForward) {
-                const float4 ua = src[4], ub = src[5];
-                u[0] = ua.x, u[1] = ua.y, u[2] = ua.z, u[3] = ua.w;
-                u[4] = ub.x, u[5] = ub.y, u[6] = ub.z, u[7] = ub.w;
-            }
-            if (o.live && c0 + c < t.rows) finish_octet<MODE, GATED>(p, t, o, c0 + c, f, u);
+                for (int r = 0; r < 16; ++r) f[h][r] += element(z[h], r);
         }
+        if (GATED)
+            put_half(stage, f, at, pitch, left, parts);
+        else
+            put_frag(stage, f, at, pitch, left, parts);
     }
-}
-
-template <int MODE, bool GATED>
-__device__ __forceinline__ void load_octet(const ExpertArgs &p, const Tile &t, int rank, int quadrant, Octet &o) {
-    const int lane = threadIdx.x & 31;
-    constexpr bool kHalf = GATED && MODE == kForward;
-    o.feat = t.feat0 + (kHalf ? rank * 64 + quadrant * 16 + (lane % 2) * 8 : rank * 128 + quadrant * 32 + (lane % 4) * 8);
-    o.live = o.feat < (MODE == kForward ? p.N : p.K);
-    if (MODE == kForward && p.bias && o.live) {
-        const float *b = p.bias + (int64_t)t.e * (GATED ? 2 * (int64_t)p.N : p.N) + o.feat;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o.bias[i] = b[i];
-        if (GATED) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o.bias_up[i] = b[p.N + i];
-        }
-    }
-}
+};
 
 template <int MODE, bool FP8, bool GATED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
     expert_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUtensorMap map_n,
                   const ExpertArgs p) {
     constexpr bool kHalf = GATED && MODE == kForward;  // half of a block's 128 lanes are up features
     constexpr int kStages = kStagesOf<FP8>;
+    constexpr int kEpiWarps = kEpiWarpsOf<FP8>;
+    constexpr int kProducerWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kAuxWarp = kEpiWarps + 2;
     constexpr int kStep = FP8 ? 128 : 64;              // reduction elements per stage
     constexpr int kFeatStep = kHalf ? 128 : 256;       // output features per pair
     extern __shared__ __align__(1024) uint8_t smem[];
     float *staging = reinterpret_cast<float *>(smem + kStages * kStageBytes);
-    float *scales = reinterpret_cast<float *>(smem + kStages * kStageBytes + kStagingBytes);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes + kStagingBytes + (FP8 ? kScaleBytes : 0));
+    float *scales = reinterpret_cast<float *>(smem + kStages * kStageBytes + kEpiWarps * kStagingBytes);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes + kEpiWarps * kStagingBytes +
+                                                  (FP8 ? kScaleBytes : 0));
     const uint32_t base = smem_addr(smem);
     const uint32_t bar0 = smem_addr(bars);
     const uint32_t full = bar0, empty = full + 8 * kStages, tail = empty + 8 * kStages;
@@ -326,9 +439,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bars + 3 * kStages + i, 1);
-            mbar_init(bars + 3 * kStages + 2 + i, 2 * kEpilogueWarps);
+            mbar_init(bars + 3 * kStages + 2 + i, 2 * kEpiWarps);
             mbar_init(bars + 3 * kStages + 4 + i, kAuxWarps);
-            mbar_init(bars + 3 * kStages + 6 + i, kEpilogueWarps);
+            mbar_init(bars + 3 * kStages + 6 + i, kEpiWarps);
         }
         mbar_init_fence();
         tma_prefetch_map(&map_m);
@@ -349,9 +462,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Tile t;
     bool ok = true;
 
-    // 384 threads launch with 168 registers each; the e4m3 sums of 128 columns need more
-    if (warp >= kEpilogueWarps) {
-    if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // e4m3: 640 threads launch with 96 registers each, 61440 in all: 512 x 104 + 128 x 64
+    if (warp >= kEpiWarps) {
+    if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == kProducerWarp) {
         const uint32_t lead_full = map_to_rank(full, 0), own_tail = map_to_rank(tail, rank);
         int stage = 0, issued = 0;
@@ -490,10 +603,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < kTileRows / 64; ++i) {
                         const int c = i * 64 + tid;
                         if (c < t.n) {
+                            // the eight columns of 32 that a lane's fragments hold, side by side
+                            const int to = (c & ~31) + 8 * (c & 3) + ((c >> 2) & 7);
 #pragma unroll
                             for (int k = 0; k < kScaleGroup; ++k) {
-                                dst[(k * 2) * kTileRows + c] = sx[i][k] * sw[0][k];
-                                if (kHalf) dst[(k * 2 + 1) * kTileRows + c] = sx[i][k] * sw[1][k];
+                                dst[(k * 2) * kTileRows + to] = sx[i][k] * sw[0][k];
+                                if (kHalf) dst[(k * 2 + 1) * kTileRows + to] = sx[i][k] * sw[1][k];
                             }
                         }
                     }
@@ -527,86 +642,105 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
     } else {
-        if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        const int quadrant = warp & 3, half = warp >> 2;
-        float *stage = staging + warp * kStageCols * kStageStride;
-        const uint32_t lead_empty = map_to_rank(acc_empty, 0);
+        if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        constexpr int kShare = kEpiWarps / 4, kCols = kTileRows / 32 / kShare;  // warps, chunks of columns each
+        const int quadrant = warp & 3, share = warp >> 2;
+        const uint32_t lead_empty = map_to_rank(acc_empty, 0), own_sc_empty = map_to_rank(sc_empty, rank);
         const uint32_t my_tmem = tmem + ((uint32_t)(quadrant * 32) << 16);
+        const float *my_scales = scales + 8 * (lane & 3);
         int buf = 0;
         uint32_t parity = 0;
         int sbuf = 0;
         uint32_t sparity = 0;
-        Octet o;
+        Output<MODE, GATED> out(p, smem_addr(staging) + warp * kStagingBytes);
         for (int tile = pair; ok && walk.next(tile, t); tile += pairs) {
-            load_octet<MODE, GATED>(p, t, rank, quadrant, o);
+            if (!FP8) out.begin(t, rank, quadrant);
             const int chunks = t.n / 32;
+            // (e4m3: after the sums, whose registers it would need)
+            if (!FP8 && share < chunks) out.fetch(share * 32);
             if (FP8) {
-                float acc[4][32];
+                Frag acc[kCols];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < kCols; ++i)
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) acc[i][c] = 0.0f;
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) acc[i][h][r] = 0.0f;
                 for (int k = 0; k < t.steps; ++k) {
                     const int kg = k % kScaleGroup;
                     if (kg == 0 && !(ok = mbar_wait_cluster(sc_full + 8 * sbuf, sparity))) break;
-                    const float *sc = scales + ((sbuf * kScaleGroup + kg) * 2 + (kHalf && lane >= 16 ? 1 : 0)) * kTileRows;
+                    const float *sc = my_scales + (sbuf * kScaleGroup + kg) * 2 * kTileRows;
                     if (!(ok = mbar_wait_cluster(acc_full + 8 * buf, parity))) break;
                     tcgen05_fence_after();
+                    const uint32_t from = my_tmem + buf * kTileRows;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int ch = 2 * i + half;
+                    for (int i = 0; i < kCols; ++i) {
+                        const int ch = i * kShare + share;
                         if (ch < chunks) {
-                            uint32_t v[32];
-                            tmem_ld32(v, my_tmem + buf * kTileRows + ch * 32);
-                            tmem_wait_ld();
+                            float4 w[2];
 #pragma unroll
-                            for (int c = 0; c < 32; c += 4) {
-                                const float4 s = *reinterpret_cast<const float4 *>(sc + ch * 32 + c);
-                                acc[i][c] = fmaf(__uint_as_float(v[c]), s.x, acc[i][c]);
-                                acc[i][c + 1] = fmaf(__uint_as_float(v[c + 1]), s.y, acc[i][c + 1]);
-                                acc[i][c + 2] = fmaf(__uint_as_float(v[c + 2]), s.z, acc[i][c + 2]);
-                                acc[i][c + 3] = fmaf(__uint_as_float(v[c + 3]), s.w, acc[i][c + 3]);
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t v[16];
+                                tmem_ld_frag(v, from + ch * 32 + (h ? 16u << 16 : 0u));
+                                // scales of columns 4c + lane % 4
+                                if (h == 0) load_scales(w, sc + ch * 32);
+                                if (kHalf && h) load_scales(w, sc + ch * 32 + kTileRows);
+                                tmem_wait_ld();
+                                const float f[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+                                for (int r = 0; r < 16; ++r)
+                                    acc[i][h][r] = fmaf(__uint_as_float(v[r]), f[r >> 1], acc[i][h][r]);
                             }
                         }
                     }
                     tcgen05_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(lead_empty + 8 * buf);
+                    if (elect_one()) mbar_arrive_cluster(lead_empty + 8 * buf);
                     buf ^= 1;
                     if (buf == 0) parity ^= 1;
                     if (kg == kScaleGroup - 1 || k == t.steps - 1) {
-                        if (lane == 0) mbar_arrive_cluster(map_to_rank(sc_empty, rank) + 8 * sbuf);
+                        __syncwarp();
+                        if (elect_one()) mbar_arrive_cluster(own_sc_empty + 8 * sbuf);
                         sbuf ^= 1;
                         if (sbuf == 0) sparity ^= 1;
                     }
                 }
                 if (!ok) break;
+                out.begin(t, rank, quadrant);
+                if (share < chunks) out.fetch(share * 32);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (2 * i + half < chunks) finish_columns<MODE, GATED>(p, t, o, stage, acc[i], (2 * i + half) * 32);
+                for (int i = 0; i < kCols; ++i) {
+                    const int col0 = (i * kShare + share) * 32;
+                    if (i * kShare + share < chunks) out.finish(acc[i], col0, col0 + kShare * 32);
+                }
             } else {
                 if (t.steps > 0) {
                     if (!(ok = mbar_wait_cluster(acc_full + 8 * buf, parity))) break;
                     tcgen05_fence_after();
                 }
-                for (int ch = half; ch < chunks; ch += 2) {
-                    uint32_t v[32];
-                    float f[32];
+                for (int ch = share; ch < chunks; ch += kShare) {
+                    Frag f;
                     if (t.steps > 0) {
-                        tmem_ld32(v, my_tmem + buf * kTileRows + ch * 32);
+                        uint32_t v[2][16];
+                        tmem_ld_frag(v[0], my_tmem + buf * kTileRows + ch * 32);
+                        tmem_ld_frag(v[1], my_tmem + buf * kTileRows + ch * 32 + (16u << 16));
                         tmem_wait_ld();
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) f[c] = __uint_as_float(v[c]);
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) f[h][r] = __uint_as_float(v[h][r]);
                     } else {  // wgrad of an expert without rows
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) f[c] = 0.0f;
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) f[h][r] = 0.0f;
                     }
-                    finish_columns<MODE, GATED>(p, t, o, stage, f, ch * 32);
+                    out.finish(f, ch * 32, (ch + kShare) * 32);
                 }
                 if (t.steps > 0) {
                     tcgen05_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(lead_empty + 8 * buf);
+                    if (elect_one()) mbar_arrive_cluster(lead_empty + 8 * buf);
                     buf ^= 1;
                     if (buf == 0) parity ^= 1;
                 }
@@ -702,7 +836,7 @@ epd_status_t launch(const CUtensorMap &m, const CUtensorMap &n, const ExpertArgs
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(sm_count() / 2 * 2));
-        cfg.blockDim = dim3(kThreads);
+        cfg.blockDim = dim3(kThreadsOf<FP8>);
         cfg.dynamicSmemBytes = kSmem;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -724,7 +858,7 @@ epd_status_t launch(const CUtensorMap &m, const CUtensorMap &n, const ExpertArgs
                                                                             : p.rows.capacity_rows);
     const int64_t most = feat_tiles * row_tiles;
     if (most > INT32_MAX / 2) return EPD_ERR_UNSUPPORTED;
-    return launch_pdl(kernel, 2 * (int)(most < pairs ? most : pairs), kThreads, kSmem, stream, m, n, p);
+    return launch_pdl(kernel, 2 * (int)(most < pairs ? most : pairs), kThreadsOf<FP8>, kSmem, stream, m, n, p);
 }
 
 bool rows_ok(const epd_expert_rows_t *r) {
