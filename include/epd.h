@@ -487,7 +487,7 @@ typedef enum {
  *      [E, ceil(NW/128), K/128] float32, one scale per 128 x 128 block;
  *   bias: [E, NW] float32 or NULL; residual: [capacity_rows, N] bfloat16 or NULL;
  *   y: [capacity_rows, N], preact: [capacity_rows, NW] bfloat16 (preact may be NULL).
- * N % 8 == 0; for EPD_ACT_SWIGLU N % 16 == 0, with e4m3 N % 128 == 0. All row buffers and w
+ * N % 8 == 0; for EPD_ACT_SWIGLU with e4m3 N % 128 == 0. All row buffers and w
  * 16-byte aligned. One expert over the whole buffer is an ordinary linear layer.
  */
 EPD_API epd_status_t ep_expert_matmul(const epd_expert_rows_t *rows, const void *x,

@@ -55,7 +55,7 @@ def test_expert_matmul_rejects_bad_args(lib):
                                              N=32, act=0, bias=None, res=None, y=FAKE, pre=None, st=FAKE, s=None))
     for kw in ([dict(r=rows(**b)) for b in BAD_ROWS] + [
             dict(r=None), dict(dt=2), dict(dt=5), dict(K=60), dict(K=0), dict(N=20), dict(N=0), dict(act=5),
-            dict(act=-1), dict(act=4, N=24), dict(x=None), dict(x=ODD), dict(w=None), dict(w=ODD), dict(y=None),
+            dict(act=-1), dict(act=4, N=20), dict(x=None), dict(x=ODD), dict(w=None), dict(w=ODD), dict(y=None),
             dict(y=ODD), dict(res=ODD), dict(pre=ODD), dict(bias=ctypes.c_void_p(0x10002)), dict(st=None),
             dict(xs=FAKE), dict(ws=FAKE), dict(dt=1), dict(dt=1, xs=FAKE, K=128),
             dict(dt=1, xs=FAKE, ws=FAKE, K=64), dict(dt=1, xs=FAKE, ws=FAKE, K=128, act=4, N=64)]):

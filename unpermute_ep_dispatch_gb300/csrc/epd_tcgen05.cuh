@@ -20,7 +20,7 @@ __device__ __forceinline__ uint64_t global_ns() {
     return t;
 }
 
-__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_try_pipe(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -34,12 +34,15 @@ __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) 
 
 // Waits for phase `parity` of `bar`, for two seconds or 2^24 polls at most: a wait inside
 // these kernels is for one tile's work (microseconds), so running out means that something
-// is wrong, and the kernel returns with an error instead of hanging.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity) {
-    if (mbar_try_cluster(bar, parity)) return true;
+// is wrong, and the kernel returns with an error instead of hanging. The waits are at block
+// scope: what they order is the work of the TMA and tensor-core units, and a wait that
+// acquires at cluster scope costs hundreds of cycles (dense 8192^3: 1558 us with, 661 us
+// without).
+__device__ __forceinline__ bool mbar_wait_pipe(uint32_t bar, uint32_t parity) {
+    if (mbar_try_pipe(bar, parity)) return true;
     uint64_t t0 = 0;
     for (uint32_t i = 1; i < (1u << 24); ++i) {
-        if (mbar_try_cluster(bar, parity)) return true;
+        if (mbar_try_pipe(bar, parity)) return true;
         if ((i & 255u) == 0) {
             const uint64_t t = global_ns();
             if (t0 == 0) t0 = t;
@@ -71,13 +74,10 @@ __device__ __forceinline__ void mbar_arrive_tx_cluster(uint32_t bar, uint32_t by
                  : "memory");
 }
 
-// The same after this thread's block has written operands itself (its writes are ordered
-// before the arrival for whoever waits, in either block).
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// An arrival on a barrier of this block.
+__device__ __forceinline__ void mbar_arrive_own(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-
-__device__ __forceinline__ void fence_acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 // TMA tile loads into this block's shared memory. `bar` may lie in the pair's other block.
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
@@ -96,12 +96,12 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int
         : "memory");
 }
 
-__device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4,
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
                                        uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
         : "memory");
 }
 
@@ -125,15 +125,22 @@ __device__ __forceinline__ void tcgen05_fence_before() { asm volatile("tcgen05.f
 __device__ __forceinline__ void tcgen05_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// 32 columns of 16 lanes (the lane offset of `addr` a multiple of 16), as fragments: of thread
-// t, v[2c + b] is lane 8b + t / 4, column 4c + t % 4. (The 16x256b shape, whose fragments are
-// the mma's own, reads tensor memory at half the rate: 256 against over 440 bytes a clock.)
+// 32 (16) columns of 16 lanes (the lane offset of `addr` a multiple of 16), as fragments: of
+// thread t, v[2c + b] is lane 8b + t / 4, column 4c + t % 4. (The 16x256b shape, whose fragments
+// are the mma's own, reads tensor memory at half the rate: 256 against over 440 bytes a clock.)
 __device__ __forceinline__ void tmem_ld_frag(uint32_t (&v)[16], uint32_t addr) {
     asm volatile(
         "tcgen05.ld.sync.aligned.16x128b.x8.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
           "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_ld_frag(uint32_t (&v)[8], uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
         : "r"(addr));
 }
 
@@ -158,8 +165,23 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ float4 lds16f(uint32_t addr) {
+    const uint4 v = lds16(addr);
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+
 __device__ __forceinline__ void sts16(uint32_t addr, const uint4 &v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// (a0, a1) += (d0, d1) * s, one instruction for both.
+__device__ __forceinline__ void fma2(float &a0, float &a1, uint32_t d0, uint32_t d1, float s) {
+    uint64_t a, d, ss;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(d0), "r"(d1));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(d), "l"(ss));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
 }
 
 // ---------------------------------------------------------------------------- matrix instructions

@@ -17,11 +17,12 @@
 // token rows per step of the reduction (128 bytes wide), so a token row that both blocks
 // multiply is staged once.
 //
-// Warps: 0-7 epilogue, 8 TMA producer, 9 issues the mma (in the pair's first block), 10 and
-// 11 load row scales (e4m3) or clear the ragged end of a region (wgrad). Accumulators are
-// double-buffered in tensor memory, so a tile's epilogue runs under the next tile's mma.
-// Blocks walk the tiles of all experts in a fixed order (persistent, one pair per two SMs);
-// the experts' counts are read from device memory, 32 at a time, by the warps themselves.
+// Warps: the epilogue's 8 (e4m3: 16), the producer, which walks the tiles, publishes them to
+// the others and feeds TMA, one that issues the mma (in the pair's first block), and for e4m3
+// two that load row scales. Accumulators are double-buffered in tensor memory, so a tile's
+// epilogue runs under the next tile's mma. Blocks walk the tiles of all experts in a fixed
+// order (persistent, one pair per two SMs); the experts' counts are read from device memory,
+// 32 at a time, by the producer itself.
 //
 // e4m3: rows are scaled per 128 columns and weights per 128 x 128, so the product of one
 // 128-wide step cannot stay in the tensor core's accumulator: every step's D goes to
@@ -36,27 +37,29 @@ namespace {
 
 enum { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
-// The epilogue warps, then four of which one feeds TMA, one issues the mma and two are
-// helpers. e4m3 has its sums in registers: 16 warps of 64 columns each.
+// e4m3 has its sums in registers: 16 epilogue warps of 64 columns each.
 template <bool FP8>
 constexpr int kEpiWarpsOf = FP8 ? 16 : 8;
+constexpr int kScaleWarps = 2;
 template <bool FP8>
-constexpr int kThreadsOf = (kEpiWarpsOf<FP8> + 4) * 32;
-constexpr int kAuxWarps = 2;
+constexpr int kThreadsOf = (kEpiWarpsOf<FP8> + 2 + (FP8 ? kScaleWarps : 0)) * 32;
 constexpr int kTileRows = 256;                  // most token rows (wgrad: output rows) of a tile
 constexpr int kOperandBytes = 128 * 128;        // 128 rows of 128 bytes: one operand of a stage
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kRowBox = 32;                     // token rows per TMA box
 constexpr int kStagingBytes = 32 * 80;          // per epilogue warp: 32 rows of 64 bytes, 80 apart
+constexpr int kTailBytes = 512;                 // published tiles and barriers
 constexpr int kScaleGroup = 4;                  // reduction steps per group of staged scales
 constexpr int kScaleBytes = 2 * kScaleGroup * 2 * kTileRows * 4;
+constexpr int kRing = 4;                        // tiles published ahead
+constexpr int kCuts = 7;                        // boxes of 64, 32, ... 1 rows (wgrad)
 constexpr int kGroupTiles = 8;                  // token tiles that share a pass over the features
 
 template <bool FP8>
 constexpr int kStagesOf = FP8 ? 5 : 6;
 
 template <bool FP8>
-constexpr int kSmemOf = kStagesOf<FP8> *kStageBytes + kEpiWarpsOf<FP8> * kStagingBytes + (FP8 ? kScaleBytes : 0) + 512;
+constexpr int kSmemOf = kStagesOf<FP8> *kStageBytes + kEpiWarpsOf<FP8> * kStagingBytes + (FP8 ? kScaleBytes : 0) + kTailBytes;
 
 struct ExpertArgs {
     epd_expert_rows_t rows;
@@ -89,16 +92,46 @@ __device__ __forceinline__ void expert_region(const epd_expert_rows_t &r, int e,
     start = count > 0 ? (int)at : 0;
 }
 
+// The operands' TMA maps. wgrad's reduction runs over a region's rows, whose last step may hold
+// fewer than 64: it is loaded in boxes of 32, 16, ... 1 rows, and what is missing to a multiple
+// of 16 (one mma's reduction) in boxes past the end of the buffer, which read as zero. The
+// other rows of the buffer are never multiplied.
+template <int MODE>
+struct Maps {
+    static constexpr int kCount = MODE == kWgrad ? kCuts : 1;
+    CUtensorMap m[kCount], n[kCount];
+};
+
 // One tile of the work: `rows` valid columns of D from row `row0` (a token row; for wgrad an
 // output row of the expert's gradient), n of them computed; features from feat0.
-struct Tile {
-    int e, start, count;
+struct alignas(16) Tile {
+    int e, start, count;  // e = -1 past the last tile
     int feat0, row0, rows, n;
     int steps;  // of the reduction
 };
 
-// Walks the tiles of one pair. Every warp that needs them runs its own walker: lane l holds
-// expert batch + l, and a tile's expert is found by a ballot over the running tile counts.
+// The producer's tiles, as the other warps of the block get them: a ring in shared memory.
+struct Ring {
+    const Tile *slots;
+    uint32_t full, empty;
+    int at = 0;
+    uint32_t parity = 0;
+
+    // Waits for the next tile. The slot stays this warp's until drop().
+    __device__ __forceinline__ bool next(bool &ok) {
+        ok = mbar_wait_pipe(full + 8 * at, parity);
+        return ok && slots[at].e >= 0;
+    }
+    __device__ __forceinline__ const Tile &tile() const { return slots[at]; }
+    __device__ __forceinline__ void drop() {
+        __syncwarp();
+        if (elect_one()) mbar_arrive_own(empty + 8 * at);
+        if (++at == kRing) at = 0, parity ^= 1;
+    }
+};
+
+// Walks the tiles of one pair, a warp together: lane l holds expert batch + l, and a tile's
+// expert is found by a ballot over the running tile counts.
 template <int MODE, int STEP>
 struct Walker {
     const ExpertArgs &p;
@@ -169,8 +202,8 @@ struct Walker {
 // 16h + 8b + lane / 4, column 8u + 4i + lane % 4. Packed to bf16 in pairs over i they are 8 x 8
 // blocks for stmatrix, whose row j is column 8u + 4 (j % 2) + j / 2 of D; it turns them over, so
 // that rows of 32 (a gated product: 16) features lie together and leave for memory 16 bytes a
-// lane. In a gated product's tiles features 0-15
-// of a warp are 16 gate features (h = 0) and 16-31 the same features' up (h = 1).
+// lane. In a gated product a block's 128 features are 64 gate features (quadrants 0 and 1) and
+// the same features' up (quadrants 2 and 3).
 using Frag = float[2][16];
 
 constexpr int kPitch = 80;  // bytes per staged row of 64: eight rows fall in different banks
@@ -194,10 +227,9 @@ __device__ __forceinline__ void apply(Frag &f) {
 }
 
 // Writes the first `rows` of 32 staged rows, `parts` of their four 16-byte parts each, to
-// at + row * pitch. SPLIT: `parts` of the first two there, and of the last two `apart` further.
-template <bool SPLIT = false>
-__device__ __forceinline__ void put_frag(uint32_t stage, const Frag &f, uint8_t *at, int64_t pitch, int rows, int parts,
-                                         int64_t apart = 0) {
+// at + row * pitch.
+__device__ __forceinline__ void put_frag(uint32_t stage, const Frag &f, uint8_t *at, int64_t pitch, int rows,
+                                         int parts) {
     const int lane = threadIdx.x & 31;
     __syncwarp();
 #pragma unroll
@@ -207,9 +239,8 @@ __device__ __forceinline__ void put_frag(uint32_t stage, const Frag &f, uint8_t 
                    pack2_bf16(f[1][4 * u], f[1][4 * u + 2]), pack2_bf16(f[1][4 * u + 1], f[1][4 * u + 3]));
     __syncwarp();
     const int part = lane & 3;
-    const int own = SPLIT ? part & 1 : part;
-    at += own * 16 + (SPLIT && part >= 2 ? apart : 0);
-    const bool live = own < parts;
+    at += part * 16;
+    const bool live = part < parts;
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
         const int row = lane_row(it);
@@ -218,16 +249,16 @@ __device__ __forceinline__ void put_frag(uint32_t stage, const Frag &f, uint8_t 
     }
 }
 
-// The same for the 16 features f[0] of a gated product.
-__device__ __forceinline__ void put_half(uint32_t stage, const Frag &f, uint8_t *at, int64_t pitch, int rows, int parts) {
+// The same for 16 features, a half of the warp's.
+__device__ __forceinline__ void put_half(uint32_t stage, const float (&f)[16], uint8_t *at, int64_t pitch, int rows, int parts) {
     constexpr int kHalfPitch = 48;
     const int lane = threadIdx.x & 31;
     __syncwarp();
 #pragma unroll
     for (int u = 0; u < 4; u += 2)
         stmatrix_t(stage + ((u + (lane >> 4)) * 8 + block_column(lane & 7)) * kHalfPitch + ((lane >> 3) & 1) * 16,
-                   pack2_bf16(f[0][4 * u], f[0][4 * u + 2]), pack2_bf16(f[0][4 * u + 1], f[0][4 * u + 3]),
-                   pack2_bf16(f[0][4 * u + 4], f[0][4 * u + 6]), pack2_bf16(f[0][4 * u + 5], f[0][4 * u + 7]));
+                   pack2_bf16(f[4 * u], f[4 * u + 2]), pack2_bf16(f[4 * u + 1], f[4 * u + 3]),
+                   pack2_bf16(f[4 * u + 4], f[4 * u + 6]), pack2_bf16(f[4 * u + 5], f[4 * u + 7]));
     __syncwarp();
     const int part = lane & 1;
 #pragma unroll
@@ -265,15 +296,30 @@ struct Ahead {
     }
 };
 
+// Sixteen values a lane to the same lane of the pair's other warp, by way of the staging rows.
+__device__ __forceinline__ bool swap_half(uint32_t mine, uint32_t other, uint32_t bar, const float (&out)[16], float (&in)[16]) {
+    const uint32_t at = (threadIdx.x & 31) * 16;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        sts16(mine + i * 512 + at, make_uint4(__float_as_uint(out[4 * i]), __float_as_uint(out[4 * i + 1]),
+                                              __float_as_uint(out[4 * i + 2]), __float_as_uint(out[4 * i + 3])));
+    mbar_arrive_own(bar);  // of 64: the barrier's two phases, written and read, end as they began
+    bool ok = mbar_wait_pipe(bar, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 v = lds16f(other + i * 512 + at);
+        in[4 * i] = v.x, in[4 * i + 1] = v.y, in[4 * i + 2] = v.z, in[4 * i + 3] = v.w;
+    }
+    mbar_arrive_own(bar);
+    ok = ok && mbar_wait_pipe(bar, 1);
+    return __all_sync(0xffffffffu, ok);
+}
+
 // Element r of fragments f[h] in the words that Ahead::turn gives.
 __device__ __forceinline__ float element(const uint32_t (&w)[8], int r) {
     const uint32_t v = w[(r >> 2) * 2 + (r & 1)];
     return r & 2 ? hi_bf16(v) : lo_bf16(v);
-}
-
-__device__ __forceinline__ void load_scales(float4 (&w)[2], const float *at) {
-    w[0] = reinterpret_cast<const float4 *>(at)[0];
-    w[1] = reinterpret_cast<const float4 *>(at)[1];
 }
 
 // A warp's share of a tile's output.
@@ -281,21 +327,29 @@ template <int MODE, bool GATED>
 struct Output {
     static constexpr bool kHalf = GATED && MODE == kForward;
     const ExpertArgs &p;
-    uint32_t stage;
-    int feat, parts;       // first feature, and how many octets of them exist
+    uint32_t stage, other; // staging rows; a gated product's: of the warp with the other half
+    uint32_t bar;          // for the two of them
+    bool ok = true;
+    int up;                // this warp has up features
+    int feat, parts;       // first feature of the warp, and how many octets of them exist
     int rows;              // of the tile
     int64_t pitch;         // bytes between output rows
     int64_t row;           // first row of the tile in the row buffers (wgrad: in dw)
     float bias[2][2];      // of features 16h + 8b + lane / 4
     Ahead a, b;            // the residual, or dgrad's pre-activations (b: their up part)
 
-    __device__ Output(const ExpertArgs &args, uint32_t stage_) : p(args), stage(stage_) {}
+    __device__ Output(const ExpertArgs &args, uint32_t staging, uint32_t bars, int warp) : p(args) {
+        stage = staging + warp * kStagingBytes;
+        other = staging + (warp ^ 2) * kStagingBytes;
+        up = kHalf ? (warp >> 1) & 1 : 0;
+        bar = bars + 8 * ((warp >> 2) * 2 + (warp & 1));
+    }
 
     __device__ __forceinline__ void begin(const Tile &t, int rank, int quadrant) {
         const int lane = threadIdx.x & 31;
         const int features = MODE == kForward ? p.N : p.K;
-        feat = t.feat0 + (kHalf ? rank * 64 + quadrant * 16 : rank * 128 + quadrant * 32);
-        parts = max(0, min(kHalf ? 2 : 4, (features - feat) / 8));
+        feat = t.feat0 + (kHalf ? rank * 64 + (quadrant & 1) * 32 : rank * 128 + quadrant * 32);
+        parts = max(0, min(4, (features - feat) / 8));
         rows = t.rows;
         pitch = (int64_t)features * 2 * (MODE == kDgrad && GATED ? 2 : 1);
         row = (MODE == kWgrad ? (int64_t)t.e * p.N : t.start) + t.row0;
@@ -305,8 +359,8 @@ struct Output {
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int o = 0; o < 2; ++o) {
-                    const int f = feat + (kHalf ? 0 : 16 * h) + 8 * o + lane / 4;
-                    bias[h][o] = f < features ? at[f + (kHalf && h ? p.N : 0)] : 0.0f;
+                    const int f = feat + 16 * h + 8 * o + lane / 4;
+                    bias[h][o] = f < features ? at[f + (up ? p.N : 0)] : 0.0f;
                 }
         }
     }
@@ -380,12 +434,32 @@ struct Output {
         }
         if (p.preact) {
             const int64_t zp = (int64_t)p.N * 2 * (GATED ? 2 : 1);
-            put_frag<kHalf>(stage, f, p.preact + (row + col0) * zp + feat * 2, zp, left, parts, (int64_t)p.N * 2);
+            put_frag(stage, f, p.preact + (row + col0) * zp + ((int64_t)feat + (up ? p.N : 0)) * 2, zp, left, parts);
         }
         if (GATED) {
+            // the gate warp finishes the first 16 features and the up warp the last: each sends
+            // the other what it needs for them
+            float in[16];
+            if (up) {
+                ok = ok && swap_half(stage, other, bar, f[0], in);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) f[0][r] = f[0][r] * fast_sigmoid(f[0][r]) * f[1][r];
-        } else if (p.act == EPD_ACT_RELU) {
+                for (int r = 0; r < 16; ++r) f[1][r] = in[r] * fast_sigmoid(in[r]) * f[1][r];
+            } else {
+                ok = ok && swap_half(stage, other, bar, f[1], in);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) f[1][r] = f[0][r] * fast_sigmoid(f[0][r]) * in[r];
+            }
+            if (p.residual) {
+                uint32_t z[2][8];
+                a.turn(stage, z);
+                if (next < rows) fetch(next);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) f[1][r] += up ? element(z[1], r) : element(z[0], r);
+            }
+            put_half(stage, f[1], at + up * 32, pitch, left, max(0, min(2, parts - 2 * up)));
+            return;
+        }
+        if (p.act == EPD_ACT_RELU) {
             apply<EPD_ACT_RELU>(f);
         } else if (p.act == EPD_ACT_SILU) {
             apply<EPD_ACT_SILU>(f);
@@ -397,144 +471,173 @@ struct Output {
             a.turn(stage, z);
             if (next < rows) fetch(next);
 #pragma unroll
-            for (int h = 0; h < (GATED ? 1 : 2); ++h)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) f[h][r] += element(z[h], r);
         }
-        if (GATED)
-            put_half(stage, f, at, pitch, left, parts);
-        else
-            put_frag(stage, f, at, pitch, left, parts);
+        put_frag(stage, f, at, pitch, left, parts);
     }
 };
 
 template <int MODE, bool FP8, bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
-    expert_kernel(const __grid_constant__ CUtensorMap map_m, const __grid_constant__ CUtensorMap map_n,
-                  const ExpertArgs p) {
+    expert_kernel(const __grid_constant__ Maps<MODE> maps, const ExpertArgs p) {
     constexpr bool kHalf = GATED && MODE == kForward;  // half of a block's 128 lanes are up features
     constexpr int kStages = kStagesOf<FP8>;
     constexpr int kEpiWarps = kEpiWarpsOf<FP8>;
-    constexpr int kProducerWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kAuxWarp = kEpiWarps + 2;
+    constexpr int kProducerWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kScaleWarp = kEpiWarps + 2;
     constexpr int kStep = FP8 ? 128 : 64;              // reduction elements per stage
     constexpr int kFeatStep = kHalf ? 128 : 256;       // output features per pair
     extern __shared__ __align__(1024) uint8_t smem[];
-    float *staging = reinterpret_cast<float *>(smem + kStages * kStageBytes);
-    float *scales = reinterpret_cast<float *>(smem + kStages * kStageBytes + kEpiWarps * kStagingBytes);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kStages * kStageBytes + kEpiWarps * kStagingBytes +
-                                                  (FP8 ? kScaleBytes : 0));
-    const uint32_t base = smem_addr(smem);
-    const uint32_t bar0 = smem_addr(bars);
-    const uint32_t full = bar0, empty = full + 8 * kStages, tail = empty + 8 * kStages;
-    const uint32_t acc_full = tail + 8 * kStages, acc_empty = acc_full + 16;
-    const uint32_t sc_full = acc_empty + 16, sc_empty = sc_full + 16, slot = sc_empty + 16;
+    uint8_t *after = smem + kStages * kStageBytes;
+    const uint32_t staging = smem_addr(after);
+    after += kEpiWarps * kStagingBytes;
+    float *scales = reinterpret_cast<float *>(after);
+    if (FP8) after += kScaleBytes;
+    Tile *slots = reinterpret_cast<Tile *>(after);
+    after += kRing * sizeof(Tile);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(after);
+    constexpr int kEmpty = kStages, kAccFull = 2 * kStages, kAccEmpty = kAccFull + 2, kScFull = kAccEmpty + 2,
+                  kScEmpty = kScFull + 2, kTileFull = kScEmpty + 2, kTileEmpty = kTileFull + kRing,
+                  kSwap = kTileEmpty + kRing, kSlot = kSwap + kEpiWarps / 2;
+    static_assert((kSlot + 1) * 8 + kRing * sizeof(Tile) <= kTailBytes, "the barriers fit");
+    const uint32_t base = smem_addr(smem), bar0 = smem_addr(bars);
+    const uint32_t full = bar0, empty = bar0 + 8 * kEmpty, acc_full = bar0 + 8 * kAccFull,
+                   acc_empty = bar0 + 8 * kAccEmpty, sc_full = bar0 + 8 * kScFull, sc_empty = bar0 + 8 * kScEmpty;
 
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int rank = (int)cluster_ctarank();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(bars + i, 2);                 // both blocks' producers (or tail clearers)
-            mbar_init(bars + kStages + i, 1);       // a commit
-            mbar_init(bars + 2 * kStages + i, 1);   // this block's own tail loads
+            mbar_init(bars + i, 2);           // both blocks' producers
+            mbar_init(bars + kEmpty + i, 1);  // a commit
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bars + 3 * kStages + i, 1);
-            mbar_init(bars + 3 * kStages + 2 + i, 2 * kEpiWarps);
-            mbar_init(bars + 3 * kStages + 4 + i, kAuxWarps);
-            mbar_init(bars + 3 * kStages + 6 + i, kEpiWarps);
+            mbar_init(bars + kAccFull + i, 1);
+            mbar_init(bars + kAccEmpty + i, 2 * kEpiWarps);
+            mbar_init(bars + kScFull + i, kScaleWarps);
+            mbar_init(bars + kScEmpty + i, kEpiWarps);
         }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(bars + kTileFull + i, 1);
+            mbar_init(bars + kTileEmpty + i, kEpiWarps + (rank == 0) + (FP8 ? kScaleWarps : 0));
+        }
+        for (int i = 0; i < kEpiWarps / 2; ++i) mbar_init(bars + kSwap + i, 64);
         mbar_init_fence();
-        tma_prefetch_map(&map_m);
-        tma_prefetch_map(&map_n);
+        for (int i = 0; i < Maps<MODE>::kCount; ++i) {
+            tma_prefetch_map(&maps.m[i]);
+            tma_prefetch_map(&maps.n[i]);
+        }
     }
-    if (warp == kMmaWarp) tmem_alloc_pair(slot, 512);
+    if (warp == kMmaWarp) tmem_alloc_pair(bar0 + 8 * kSlot, 512);
     tcgen05_fence_before();
     __syncthreads();
     cluster_arrive_release();
     cluster_wait_acquire();
     tcgen05_fence_after();
-    const uint32_t tmem = *reinterpret_cast<const volatile uint32_t *>(bars + 3 * kStages + 8);
+    const uint32_t tmem = *reinterpret_cast<const volatile uint32_t *>(bars + kSlot);
     pdl_wait();
     pdl_trigger();
 
-    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
-    Walker<MODE, kStep> walk(p, kFeatStep);
-    Tile t;
+    Ring ring{slots, bar0 + 8 * kTileFull, bar0 + 8 * kTileEmpty};
     bool ok = true;
-
-    // e4m3: 640 threads launch with 96 registers each, 61440 in all: 512 x 104 + 128 x 64
     if (warp >= kEpiWarps) {
-    if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == kProducerWarp) {
-        const uint32_t lead_full = map_to_rank(full, 0), own_tail = map_to_rank(tail, rank);
-        int stage = 0, issued = 0;
-        uint32_t parity = 1;
-        for (int tile = pair; ok && walk.next(tile, t); tile += pairs) {
-            const int half = t.n / 2;
-            const int boxes = MODE == kWgrad ? (half + 63) / 64 : (half + kRowBox - 1) / kRowBox;
-            const uint32_t bytes = kOperandBytes + boxes * (MODE == kWgrad ? 64 : kRowBox) * 128;
-            // one thread runs the tile's steps, the warp rejoins for the next tile
-            if (elect_one()) {
-                const int feat = t.feat0 + rank * (kHalf ? 64 : 128);
-                const int row = t.row0 + rank * half;
-                int st = stage;
-                uint32_t ph = parity;
-                for (int k = 0; k < t.steps; ++k) {
-                    if (!(ok = mbar_wait_cluster(empty + 8 * st, ph))) break;
-                    const uint32_t a = base + st * kStageBytes, b = a + kOperandBytes;
-                    // a ragged last step of wgrad completes on this block's own barrier: its
-                    // rows past the region are cleared before the pair sees the stage
-                    const bool ragged = MODE == kWgrad && k == t.steps - 1 && (t.count & 63) != 0;
-                    const uint32_t bar = (ragged ? own_tail : lead_full) + 8 * st;
-                    mbar_arrive_tx_cluster(bar, bytes);
-                    if (MODE == kForward) {
-                        if (kHalf)
-                            tma_5d(a, &map_m, k * kStep, 0, 0, feat / 16, t.e, bar);
-                        else
-                            tma_3d(a, &map_m, k * kStep, feat, t.e, bar);
-                    } else if (MODE == kDgrad) {
-                        tma_3d(a, &map_m, feat, k * kStep, t.e, bar);
-                        tma_3d(a + 8192, &map_m, feat + 64, k * kStep, t.e, bar);
-                    } else {
-                        tma_2d(a, &map_m, feat, t.start + k * kStep, bar);
-                        tma_2d(a + 8192, &map_m, feat + 64, t.start + k * kStep, bar);
-                    }
-                    for (int i = 0; i < boxes; ++i) {
-                        if (MODE == kWgrad)
-                            tma_2d(b + i * 8192, &map_n, row + i * 64, t.start + k * kStep, bar);
-                        else
-                            tma_2d(b + i * kRowBox * 128, &map_n, k * kStep, t.start + row + i * kRowBox, bar);
-                    }
-                    if (++st == kStages) st = 0, ph ^= 1;
+        // e4m3: 640 threads launch with 96 registers each, 61440 in all: 512 x 104 + 128 x 64
+        if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == kProducerWarp) {
+            const uint32_t lead_full = map_to_rank(full, 0);
+            const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+            Walker<MODE, kStep> walk(p, kFeatStep);
+            int stage = 0, issued = 0;
+            uint32_t parity = 1;
+            for (int tile = pair; ok; tile += pairs) {
+                Tile t;
+                const bool more = walk.next(tile, t);
+                if (!(ok = mbar_wait_pipe(ring.empty + 8 * ring.at, ring.parity ^ 1))) break;
+                if (elect_one()) {
+                    if (!more) t.e = -1;
+                    slots[ring.at] = t;
+                    mbar_arrive_own(ring.full + 8 * ring.at);
                 }
+                if (++ring.at == kRing) ring.at = 0, ring.parity ^= 1;
+                if (!more) break;
+                const int half = t.n / 2;
+                const int boxes = MODE == kWgrad ? (half + 63) / 64 : (half + kRowBox - 1) / kRowBox;
+                const uint32_t bytes = kOperandBytes + boxes * (MODE == kWgrad ? 64 : kRowBox) * 128;
+                // one thread runs the tile's steps, the warp rejoins for the next tile
+                if (elect_one()) {
+                    const int feat = t.feat0 + rank * (kHalf ? 64 : 128);
+                    const int row = t.row0 + rank * half;
+                    for (int k = 0; k < t.steps; ++k) {
+                        if (!(ok = mbar_wait_pipe(empty + 8 * stage, parity))) break;
+                        const uint32_t a = base + stage * kStageBytes, b = a + kOperandBytes;
+                        const uint32_t bar = lead_full + 8 * stage;
+                        if (MODE == kWgrad) {
+                            const int at = t.start + k * kStep, left = t.count - k * kStep;
+                            if (left >= kStep) {
+                                mbar_arrive_tx_cluster(bar, bytes);
+                                tma_2d(a, &maps.m[0], feat, at, bar);
+                                tma_2d(a + 8192, &maps.m[0], feat + 64, at, bar);
+                                for (int i = 0; i < boxes; ++i) tma_2d(b + i * 8192, &maps.n[0], row + i * 64, at, bar);
+                            } else {
+                                const int used = (left + 15) & ~15;
+                                mbar_arrive_tx_cluster(bar, (2 + boxes) * used * 128);
+                                int r = 0;
+#pragma unroll 1
+                                for (int c = 1; c < kCuts + 4; ++c) {
+                                    // the region's rows in falling powers of two, then the zeros
+                                    const int cut = c < kCuts ? c : c - kCuts + 3;
+                                    if (!(((c < kCuts ? left : used - left) << cut) & 64)) continue;
+                                    const int from = c < kCuts ? at + r : (int)p.rows.capacity_rows;
+                                    tma_2d(a + r * 128, &maps.m[cut % Maps<MODE>::kCount], feat, from, bar);
+                                    tma_2d(a + 8192 + r * 128, &maps.m[cut % Maps<MODE>::kCount], feat + 64, from, bar);
+                                    for (int i = 0; i < boxes; ++i)
+                                        tma_2d(b + i * 8192 + r * 128, &maps.n[cut % Maps<MODE>::kCount], row + i * 64, from, bar);
+                                    r += 64 >> cut;
+                                }
+                            }
+                        } else {
+                            mbar_arrive_tx_cluster(bar, bytes);
+                            if (MODE == kDgrad) {
+                                tma_3d(a, &maps.m[0], feat, k * kStep, t.e, bar);
+                                tma_3d(a + 8192, &maps.m[0], feat + 64, k * kStep, t.e, bar);
+                            } else if (kHalf) {
+                                tma_4d(a, &maps.m[0], k * kStep, feat, 0, t.e, bar);
+                            } else {
+                                tma_3d(a, &maps.m[0], k * kStep, feat, t.e, bar);
+                            }
+                            for (int i = 0; i < boxes; ++i)
+                                tma_2d(b + i * kRowBox * 128, &maps.n[0], k * kStep, t.start + row + i * kRowBox, bar);
+                        }
+                        if (++stage == kStages) stage = 0, parity ^= 1;
+                    }
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                issued += t.steps;
+                stage = __shfl_sync(0xffffffffu, issued % kStages, 0);
+                parity = 1 ^ ((issued / kStages) & 1);
             }
-            ok = __all_sync(0xffffffffu, ok);
-            issued += t.steps;
-            stage += t.steps;
-            parity ^= (stage / kStages) & 1;
-            stage %= kStages;
-        }
-        // the last stages' releases arrive before this block may go
-        for (int i = 0; ok && i < min(issued, kStages); ++i) {
-            ok = mbar_wait_cluster(empty + 8 * stage, parity);
-            if (++stage == kStages) stage = 0, parity ^= 1;
-        }
-    } else if (warp == kMmaWarp) {
-        if (rank == 0) {
+            // the last stages' releases arrive before this block may go
+            for (int i = 0; ok && i < min(issued, kStages); ++i) {
+                ok = mbar_wait_pipe(empty + 8 * stage, parity);
+                if (++stage == kStages) stage = 0, parity ^= 1;
+            }
+        } else if (warp == kMmaWarp) {
+            const uint64_t desc_a = smem_desc(base, 8192), desc_b = smem_desc(base + kOperandBytes, 8192);
             int stage = 0, buf = 0;
             uint32_t parity = 0, acc_parity = 1;
-            const uint64_t desc_a = smem_desc(base, 8192), desc_b = smem_desc(base + kOperandBytes, 8192);
-            for (int tile = pair; ok && walk.next(tile, t); tile += pairs) {
-                if (t.steps == 0) continue;
-                const uint32_t desc = mma_desc<FP8, MODE != kForward, MODE == kWgrad>(t.n);
+            while (rank == 0 && ring.next(ok)) {
+                const int steps = ring.tile().steps, n = ring.tile().n, left = ring.tile().count & 63;
+                ring.drop();
+                if (steps == 0) continue;
+                const uint32_t desc = mma_desc<FP8, MODE != kForward, MODE == kWgrad>(n);
+                int st = stage, bf = buf;
+                uint32_t ph = parity, aph = acc_parity;
                 if (elect_one()) {
-                    int st = stage, bf = buf;
-                    uint32_t ph = parity, aph = acc_parity;
-                    for (int k = 0; k < t.steps; ++k) {
-                        const bool fresh = FP8 || k == 0, last = FP8 || k == t.steps - 1;
-                        if (fresh && !(ok = mbar_wait_cluster(acc_empty + 8 * bf, aph))) break;
-                        if (!(ok = mbar_wait_cluster(full + 8 * st, ph))) break;
-                        if (MODE == kWgrad && k == t.steps - 1 && (t.count & 63)) fence_acquire_cluster();
+                    for (int k = 0; k < steps; ++k) {
+                        const bool fresh = FP8 || k == 0, last = FP8 || k == steps - 1;
+                        if (fresh && !(ok = mbar_wait_pipe(acc_empty + 8 * bf, aph))) break;
+                        if (!(ok = mbar_wait_pipe(full + 8 * st, ph))) break;
                         tcgen05_fence_after();
                         // a quarter of the stage's reduction: 32 bytes along a K-major row, or
                         // 16 rows of 128 bytes
@@ -542,8 +645,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                         const uint64_t da = desc_a + (uint32_t)(st * (kStageBytes >> 4));
                         const uint64_t db = desc_b + (uint32_t)(st * (kStageBytes >> 4));
                         const uint32_t d = tmem + bf * kTileRows;
+                        const int quarters = MODE == kWgrad && left && k == steps - 1 ? (left + 15) / 16 : 4;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) mma_pair<FP8>(d, da + q * kA, db + q * kB, desc, !(fresh && q == 0));
+                        for (int q = 0; q < 4; ++q)
+                            if (q < quarters) mma_pair<FP8>(d, da + q * kA, db + q * kB, desc, !(fresh && q == 0));
                         mma_commit_pair(empty + 8 * st);
                         if (last) {
                             mma_commit_pair(acc_full + 8 * bf);
@@ -553,24 +658,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                         if (++st == kStages) st = 0, ph ^= 1;
                     }
                 }
-                ok = __all_sync(0xffffffffu, ok);
-                stage += t.steps;
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                stage += steps;
                 parity ^= (stage / kStages) & 1;
                 stage %= kStages;
-                buf += FP8 ? t.steps : 1;
+                buf += FP8 ? steps : 1;
                 acc_parity ^= (buf >> 1) & 1;
                 buf &= 1;
             }
-        }
-    } else if (warp >= kAuxWarp) {
-        if (FP8) {
-            const int tid = threadIdx.x - kAuxWarp * 32;
+        } else if (FP8) {
+            const int tid = threadIdx.x - kScaleWarp * 32;
             const int C = p.K / 128;
-            const int NW = GATED ? 2 * p.N : p.N;
-            const int64_t blocks = (NW + 127) / 128;
+            const int64_t blocks = ((GATED ? 2 * p.N : p.N) + 127) / 128;
             int buf = 0;
             uint32_t parity = 1;
-            for (int tile = pair; ok && walk.next(tile, t); tile += pairs) {
+            while (ok && ring.next(ok)) {
+                const Tile t = ring.tile();
+                ring.drop();
                 int b0 = (t.feat0 + rank * (kHalf ? 64 : 128)) / 128;
                 int b1 = kHalf ? b0 + p.N / 128 : b0;
                 if (b0 >= blocks) b0 = 0;  // a block past the features: nothing of it is kept
@@ -583,7 +687,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
 #pragma unroll
                     for (int k = 0; k < kScaleGroup; ++k) {
                         sw[0][k] = g + k < C ? w0[g + k] : 0.0f;
-                        sw[1][k] = g + k < C ? w1[g + k] : 0.0f;
+                        sw[1][k] = kHalf && g + k < C ? w1[g + k] : 0.0f;
                     }
 #pragma unroll
                     for (int i = 0; i < kTileRows / 64; ++i) {
@@ -597,7 +701,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                                 sx[i][k] = c < t.rows && g + k < C ? xs[c * p.srow + (g + k) * p.scol] : 0.0f;
                         }
                     }
-                    if (!(ok = mbar_wait_cluster(sc_empty + 8 * buf, parity))) break;
+                    if (!(ok = mbar_wait_pipe(sc_empty + 8 * buf, parity))) break;
                     float *dst = scales + buf * kScaleGroup * 2 * kTileRows;
 #pragma unroll
                     for (int i = 0; i < kTileRows / 64; ++i) {
@@ -613,52 +717,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                         }
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(map_to_rank(sc_full, rank) + 8 * buf);
+                    if (elect_one()) mbar_arrive_own(sc_full + 8 * buf);
                     buf ^= 1;
                     if (buf == 0) parity ^= 1;
                 }
-            }
-        } else if (MODE == kWgrad && warp == kAuxWarp) {
-            const uint32_t lead_full = map_to_rank(full, 0);
-            int at = 0;                // stages used so far, modulo their number
-            uint32_t parities = 0;     // of each stage's tail barrier
-            for (int tile = pair; ok && walk.next(tile, t); tile += pairs) {
-                at = (at + t.steps) % kStages;
-                if ((t.count & 63) == 0) continue;
-                const int stage = (at + kStages - 1) % kStages;
-                if (!(ok = mbar_wait_cluster(tail + 8 * stage, (parities >> stage) & 1))) break;
-                parities ^= 1u << stage;
-                const int from = t.count & 63;
-                const int boxes = 2 + (t.n / 2 + 63) / 64;  // the features' two, then the rows'
-                uint8_t *s = smem + stage * kStageBytes;
-                for (int i = lane; i < boxes * (64 - from) * 8; i += 32) {
-                    const int box = i / ((64 - from) * 8), r = i - box * (64 - from) * 8;
-                    *reinterpret_cast<uint4 *>(s + box * 8192 + from * 128 + r * 16) = make_uint4(0, 0, 0, 0);
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive_release_cluster(lead_full + 8 * stage);
+                ok = __all_sync(0xffffffffu, ok);
             }
         }
-    }
     } else {
         if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         constexpr int kShare = kEpiWarps / 4, kCols = kTileRows / 32 / kShare;  // warps, chunks of columns each
         const int quadrant = warp & 3, share = warp >> 2;
-        const uint32_t lead_empty = map_to_rank(acc_empty, 0), own_sc_empty = map_to_rank(sc_empty, rank);
+        const uint32_t lead_empty = map_to_rank(acc_empty, 0);
         const uint32_t my_tmem = tmem + ((uint32_t)(quadrant * 32) << 16);
-        const float *my_scales = scales + 8 * (lane & 3);
         int buf = 0;
         uint32_t parity = 0;
-        int sbuf = 0;
-        uint32_t sparity = 0;
-        Output<MODE, GATED> out(p, smem_addr(staging) + warp * kStagingBytes);
-        for (int tile = pair; ok && walk.next(tile, t); tile += pairs) {
-            if (!FP8) out.begin(t, rank, quadrant);
-            const int chunks = t.n / 32;
-            // (e4m3: after the sums, whose registers it would need)
-            if (!FP8 && share < chunks) out.fetch(share * 32);
-            if (FP8) {
+        if (FP8) {
+            const float *my_scales = scales + 8 * (lane & 3) + (kHalf && quadrant >= 2 ? kTileRows : 0) + share * 32;
+            int sbuf = 0;
+            uint32_t sparity = 0;
+            while (ok && ring.next(ok)) {
+                const int steps = ring.tile().steps;
+                const int own = (ring.tile().n / 32 - share + kShare - 1) / kShare;  // chunks of this warp, of kCols
                 Frag acc[kCols];
 #pragma unroll
                 for (int i = 0; i < kCols; ++i)
@@ -666,30 +746,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int r = 0; r < 16; ++r) acc[i][h][r] = 0.0f;
-                for (int k = 0; k < t.steps; ++k) {
+                for (int k = 0; k < steps; ++k) {
                     const int kg = k % kScaleGroup;
-                    if (kg == 0 && !(ok = mbar_wait_cluster(sc_full + 8 * sbuf, sparity))) break;
+                    if (kg == 0 && !(ok = mbar_wait_pipe(sc_full + 8 * sbuf, sparity))) break;
                     const float *sc = my_scales + (sbuf * kScaleGroup + kg) * 2 * kTileRows;
-                    if (!(ok = mbar_wait_cluster(acc_full + 8 * buf, parity))) break;
+                    if (!(ok = mbar_wait_pipe(acc_full + 8 * buf, parity))) break;
                     tcgen05_fence_after();
-                    const uint32_t from = my_tmem + buf * kTileRows;
+                    const uint32_t from = my_tmem + buf * kTileRows + share * 32;
 #pragma unroll
                     for (int i = 0; i < kCols; ++i) {
-                        const int ch = i * kShare + share;
-                        if (ch < chunks) {
-                            float4 w[2];
+                        if (i < own) {
+                            float4 w[2];  // scales of columns 4c + lane % 4
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 uint32_t v[16];
-                                tmem_ld_frag(v, from + ch * 32 + (h ? 16u << 16 : 0u));
-                                // scales of columns 4c + lane % 4
-                                if (h == 0) load_scales(w, sc + ch * 32);
-                                if (kHalf && h) load_scales(w, sc + ch * 32 + kTileRows);
+                                tmem_ld_frag(v, from + i * kShare * 32 + (h ? 16u << 16 : 0u));
+                                if (h == 0) {
+                                    w[0] = reinterpret_cast<const float4 *>(sc + i * kShare * 32)[0];
+                                    w[1] = reinterpret_cast<const float4 *>(sc + i * kShare * 32)[1];
+                                }
                                 tmem_wait_ld();
                                 const float f[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
-                                for (int r = 0; r < 16; ++r)
-                                    acc[i][h][r] = fmaf(__uint_as_float(v[r]), f[r >> 1], acc[i][h][r]);
+                                for (int r = 0; r < 16; r += 2)
+                                    fma2(acc[i][h][r], acc[i][h][r + 1], v[r], v[r + 1], f[r >> 1]);
                             }
                         }
                     }
@@ -698,29 +778,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     if (elect_one()) mbar_arrive_cluster(lead_empty + 8 * buf);
                     buf ^= 1;
                     if (buf == 0) parity ^= 1;
-                    if (kg == kScaleGroup - 1 || k == t.steps - 1) {
+                    if (kg == kScaleGroup - 1 || k == steps - 1) {
                         __syncwarp();
-                        if (elect_one()) mbar_arrive_cluster(own_sc_empty + 8 * sbuf);
+                        if (elect_one()) mbar_arrive_own(sc_empty + 8 * sbuf);
                         sbuf ^= 1;
                         if (sbuf == 0) sparity ^= 1;
                     }
                 }
-                if (!ok) break;
-                out.begin(t, rank, quadrant);
-                if (share < chunks) out.fetch(share * 32);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                Output<MODE, GATED> out(p, staging, bar0 + 8 * kSwap, warp);
+                out.begin(ring.tile(), rank, quadrant);
+                if (own > 0) out.fetch(share * 32);
 #pragma unroll
-                for (int i = 0; i < kCols; ++i) {
-                    const int col0 = (i * kShare + share) * 32;
-                    if (i * kShare + share < chunks) out.finish(acc[i], col0, col0 + kShare * 32);
-                }
-            } else {
-                if (t.steps > 0) {
-                    if (!(ok = mbar_wait_cluster(acc_full + 8 * buf, parity))) break;
+                for (int i = 0; i < kCols; ++i)
+                    if (i < own) out.finish(acc[i], (i * kShare + share) * 32, ((i + 1) * kShare + share) * 32);
+                ok = out.ok;
+                ring.drop();
+            }
+        } else {
+            Output<MODE, GATED> out(p, staging, bar0 + 8 * kSwap, warp);
+            while (ok && ring.next(ok)) {
+                const Tile &t = ring.tile();
+                out.begin(t, rank, quadrant);
+                const int chunks = t.n / 32;
+                const bool any = t.steps > 0;  // else wgrad of an expert without rows
+                ring.drop();
+                if (share < chunks) out.fetch(share * 32);
+                if (any) {
+                    if (!(ok = mbar_wait_pipe(acc_full + 8 * buf, parity))) break;
                     tcgen05_fence_after();
                 }
                 for (int ch = share; ch < chunks; ch += kShare) {
                     Frag f;
-                    if (t.steps > 0) {
+                    if (any) {
                         uint32_t v[2][16];
                         tmem_ld_frag(v[0], my_tmem + buf * kTileRows + ch * 32);
                         tmem_ld_frag(v[1], my_tmem + buf * kTileRows + ch * 32 + (16u << 16));
@@ -729,7 +819,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                         for (int h = 0; h < 2; ++h)
 #pragma unroll
                             for (int r = 0; r < 16; ++r) f[h][r] = __uint_as_float(v[h][r]);
-                    } else {  // wgrad of an expert without rows
+                    } else {
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -737,13 +827,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     }
                     out.finish(f, ch * 32, (ch + kShare) * 32);
                 }
-                if (t.steps > 0) {
+                if (any) {
                     tcgen05_fence_before();
                     __syncwarp();
                     if (elect_one()) mbar_arrive_cluster(lead_empty + 8 * buf);
                     buf ^= 1;
                     if (buf == 0) parity ^= 1;
                 }
+                ok = __all_sync(0xffffffffu, out.ok);
             }
         }
     }
@@ -829,7 +920,7 @@ bool encode_rows(CUtensorMap *map, bool fp8, const void *at, int64_t count, int6
 }
 
 template <int MODE, bool FP8, bool GATED>
-epd_status_t launch(const CUtensorMap &m, const CUtensorMap &n, const ExpertArgs &p, cudaStream_t stream) {
+epd_status_t launch(const Maps<MODE> &maps, const ExpertArgs &p, cudaStream_t stream) {
     constexpr int kSmem = kSmemOf<FP8>;
     auto kernel = expert_kernel<MODE, FP8, GATED>;
     static const int pairs = [&] {
@@ -858,7 +949,7 @@ epd_status_t launch(const CUtensorMap &m, const CUtensorMap &n, const ExpertArgs
                                                                             : p.rows.capacity_rows);
     const int64_t most = feat_tiles * row_tiles;
     if (most > INT32_MAX / 2) return EPD_ERR_UNSUPPORTED;
-    return launch_pdl(kernel, 2 * (int)(most < pairs ? most : pairs), kThreadsOf<FP8>, kSmem, stream, m, n, p);
+    return launch_pdl(kernel, 2 * (int)(most < pairs ? most : pairs), kThreadsOf<FP8>, kSmem, stream, maps, p);
 }
 
 bool rows_ok(const epd_expert_rows_t *r) {
@@ -888,7 +979,7 @@ extern "C" epd_status_t ep_expert_matmul(const epd_expert_rows_t *rows, const vo
     const bool fp8 = dtype == EPD_FP8_E4M3, gated = activation == EPD_ACT_SWIGLU;
     if (!rows_ok(rows) || !act_ok(activation)) return EPD_ERR_INVALID_ARG;
     if (dtype != EPD_BF16 && !fp8) return EPD_ERR_INVALID_ARG;
-    if (K < 1 || N < 1 || K % (fp8 ? 128 : 8) != 0 || N % (gated ? (fp8 ? 128 : 16) : 8) != 0)
+    if (K < 1 || N < 1 || K % (fp8 ? 128 : 8) != 0 || N % (gated && fp8 ? 128 : 8) != 0)
         return EPD_ERR_INVALID_ARG;
     if (N > INT32_MAX / 2) return EPD_ERR_UNSUPPORTED;
     if (fp8 != (x_scale != nullptr) || fp8 != (w_scale != nullptr)) return EPD_ERR_INVALID_ARG;
@@ -917,26 +1008,26 @@ extern "C" epd_status_t ep_expert_matmul(const epd_expert_rows_t *rows, const vo
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     p.scale_vec = fp8 && scale_col_stride == 1 && K % 512 == 0 && scale_row_stride % 4 == 0 &&
                   scale_expert_stride % 4 == 0 && aligned16(x_scale);
-    CUtensorMap mw, mx;
-    bool done = encode_rows(&mx, fp8, x, rows->capacity_rows, K, kRowBox);
+    Maps<kForward> maps;
+    bool done = encode_rows(&maps.n[0], fp8, x, rows->capacity_rows, K, kRowBox);
     const cuuint32_t wide = fp8 ? 128 : 64;
     const cuuint64_t E = (cuuint64_t)rows->num_experts;
     if (gated) {
-        // 16 gate rows, then the same features' 16 up rows: one warp's lanes of the accumulator
-        const cuuint64_t size[5] = {(cuuint64_t)K, 16, 2, (cuuint64_t)N / 16, E};
-        const int64_t stride[4] = {K, (int64_t)N * K, 16 * (int64_t)K, 2 * (int64_t)N * K};
-        const cuuint32_t box[5] = {wide, 16, 2, 4, 1};
-        done = done && encode(&mw, fp8, 5, w, size, stride, box);
+        // 64 gate rows, then the same features' 64 up rows
+        const cuuint64_t size[4] = {(cuuint64_t)K, (cuuint64_t)N, 2, E};
+        const int64_t stride[3] = {K, (int64_t)N * K, 2 * (int64_t)N * K};
+        const cuuint32_t box[4] = {wide, 64, 2, 1};
+        done = done && encode(&maps.m[0], fp8, 4, w, size, stride, box);
     } else {
         const cuuint64_t size[3] = {(cuuint64_t)K, (cuuint64_t)N, E};
         const int64_t stride[2] = {K, (int64_t)N * K};
         const cuuint32_t box[3] = {wide, 128, 1};
-        done = done && encode(&mw, fp8, 3, w, size, stride, box);
+        done = done && encode(&maps.m[0], fp8, 3, w, size, stride, box);
     }
     if (!done) return EPD_ERR_CUDA;
     if (fp8)
-        return gated ? launch<kForward, true, true>(mw, mx, p, st) : launch<kForward, true, false>(mw, mx, p, st);
-    return gated ? launch<kForward, false, true>(mw, mx, p, st) : launch<kForward, false, false>(mw, mx, p, st);
+        return gated ? launch<kForward, true, true>(maps, p, st) : launch<kForward, true, false>(maps, p, st);
+    return gated ? launch<kForward, false, true>(maps, p, st) : launch<kForward, false, false>(maps, p, st);
 }
 
 extern "C" epd_status_t ep_expert_matmul_dgrad(const epd_expert_rows_t *rows, const void *dy,
@@ -961,15 +1052,16 @@ extern "C" epd_status_t ep_expert_matmul_dgrad(const epd_expert_rows_t *rows, co
     p.preact_in = static_cast<const uint8_t *>(preact);
     p.y = static_cast<uint8_t *>(dx);
     p.status = status;
-    CUtensorMap mw, my;
+    Maps<kDgrad> maps;
     const cuuint64_t size[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)rows->num_experts};
     const int64_t stride[2] = {K, (int64_t)N * K};
     const cuuint32_t box[3] = {64, 64, 1};
-    if (!encode_rows(&my, false, dy, rows->capacity_rows, N, kRowBox) || !encode(&mw, false, 3, w, size, stride, box))
+    if (!encode_rows(&maps.n[0], false, dy, rows->capacity_rows, N, kRowBox) ||
+        !encode(&maps.m[0], false, 3, w, size, stride, box))
         return EPD_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return activation == EPD_ACT_SWIGLU ? launch<kDgrad, false, true>(mw, my, p, st)
-                                        : launch<kDgrad, false, false>(mw, my, p, st);
+    return activation == EPD_ACT_SWIGLU ? launch<kDgrad, false, true>(maps, p, st)
+                                        : launch<kDgrad, false, false>(maps, p, st);
 }
 
 extern "C" epd_status_t ep_expert_matmul_wgrad(const epd_expert_rows_t *rows, const void *dy,
@@ -993,11 +1085,12 @@ extern "C" epd_status_t ep_expert_matmul_wgrad(const epd_expert_rows_t *rows, co
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     // without rows nothing is loaded, but a map has to lie somewhere
     const bool any = rows->capacity_rows > 0;
-    CUtensorMap mx, my;
-    if (!encode_rows(&mx, false, any ? x : dw, rows->capacity_rows, K, 64) ||
-        !encode_rows(&my, false, any ? dy : dw, rows->capacity_rows, N, 64))
-        return EPD_ERR_CUDA;
-    const epd_status_t rc = launch<kWgrad, false, false>(mx, my, p, st);
+    Maps<kWgrad> maps;
+    for (int i = 0; i < kCuts; ++i)
+        if (!encode_rows(&maps.m[i], false, any ? x : dw, rows->capacity_rows, K, 64 >> i) ||
+            !encode_rows(&maps.n[i], false, any ? dy : dw, rows->capacity_rows, N, 64 >> i))
+            return EPD_ERR_CUDA;
+    const epd_status_t rc = launch<kWgrad, false, false>(maps, p, st);
     if (rc != EPD_OK || !dbias) return rc;
     bias_grad_kernel<<<dim3((N + 63) / 64, rows->num_experts), 256, 0, st>>>(
         *rows, static_cast<const uint8_t *>(dy), N, dbias, status);
