@@ -406,8 +406,10 @@ typedef enum {
  *       first; equal values go to the lowest index, for groups and for experts;
  *   topk_weights[t, j] = s[topk_idx[t, j]], divided by their sum over j if
  *       `renormalize` (0 where that sum is 0), times routed_scale.
- * Softmax scores without a bias are compared by their logits, which order them
- * exactly as the scores do but never round two different ones to the same value.
+ * Scores without a bias are compared by their logits, which order them exactly as
+ * the scores do but never round two different ones to the same value; with a bias
+ * (and in a group's sum of two) they are fp32 values within a few units in the last
+ * place. The weights' scores are computed to the last place or two.
  * An expert whose logit is -inf cannot be chosen; where fewer than k are left the
  * rest of the row is -1 with weight 0 (the type's lowest finite value is an ordinary
  * logit). A NaN or +inf logit sets EPD_ERR_NONFINITE in *status and counts as -inf.

@@ -105,6 +105,8 @@ class EpdError(RuntimeError):
 def load_library(path: str = LIB_PATH):
     """Load libepd.so (built in-tree by ``build()``); raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -133,17 +135,23 @@ def _check(rc: int, where: str):
         raise EpdError(rc, where)
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream, device) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream)
+def _stream(stream, device) -> int:
+    if stream is None:  # the current stream's handle, without making a Stream object
+        index = device.index
+        return torch._C._cuda_getCurrentRawStream(
+            torch.cuda.current_device() if index is None else index)
+    return stream.cuda_stream
 
 
 def _want(t, name, dtype, shape=None, device=None):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and (shape is None or t.shape == shape)
+            and (t.is_cuda if device is None else t.device == device and t.is_cuda)
+            and t.is_contiguous()):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:

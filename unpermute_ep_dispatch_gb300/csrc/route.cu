@@ -1,214 +1,245 @@
 // route.cu -- routing to experts and its gradient (ep_route, ep_route_backward).
 //
-// One warp owns one token: lane l holds experts l, l + 32, ... of the row as keys in
-// registers, so a row is read once and every reduction is a warp reduction. A key is the
-// choice score c mapped to an unsigned integer of the same order (0 for an expert that
-// cannot be chosen), which makes the argmax two integer warp reductions: the largest key,
-// then the lowest index that has it -- the tie rule at no extra cost.
-#include <math_constants.h>
-
-#include "epd_math.cuh"
+// One warp owns one token: a row is read once, 16 bytes a lane where its alignment allows, and
+// kept in registers as the values that decide the choice. The argmax is two warp reductions: the
+// largest value, then the lowest index that has it -- the tie rule at no extra cost. Every lane
+// keeps its two largest at hand, so that a pick costs its owner a move and only a lane's second
+// pick a new pass over its values.
+//
+// What bounds it: a row of 256 logits is 1 KiB, 2.7 us for 16384 rows at the copy rate; the
+// instructions of k rounds and of the scores (some 700 a token) take longer than that.
+#include "route.cuh"
 
 namespace epd {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
-constexpr unsigned kFull = 0xffffffffu;
-
-// Order-preserving key of a float that is neither NaN nor -inf; never 0. Adding +0 makes
-// -0 and +0 one value.
-__device__ __forceinline__ uint32_t order_key(float f) {
-    const uint32_t b = __float_as_uint(__fadd_rn(f, 0.0f));
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-
-__device__ __forceinline__ float key_value(uint32_t k) {
-    return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
-}
-
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-    return v;
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    return v;
-}
-
-template <typename T>
-__device__ __forceinline__ float to_f32(T v);
-template <>
-__device__ __forceinline__ float to_f32<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-// A logit as the router reads it: NaN and +inf are reported and count as -inf.
-__device__ __forceinline__ float clean_logit(float l, bool &bad) {
-    if (!(l < CUDART_INF_F)) {
-        bad = true;
-        return -CUDART_INF_F;
-    }
-    return l;
+// The largest value of the warp (no NaN among them).
+__device__ __forceinline__ float redux_max(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 struct RouteArgs {
     const void *logits;
     const float *bias;
-    int T, k, E, groups, keep;
-    int top2, renorm;
+    int T, k, E, groups, keep, size;  // size: experts per group
+    uint32_t by_size;                 // ceil(2^32 / size): e / size = high word of e * by_size
+    int top2, renorm, vec, bias_vec;
     float scale;
     int64_t *idx;
     float *weights;
     int32_t *status;
 };
 
-// The max and the sum of exponentials of a row.
-template <int V>
-__device__ __forceinline__ void softmax_stats(const float (&l)[V], float &m, float &inv) {
-    m = -CUDART_INF_F;
+__device__ __forceinline__ void merge_top2(float &b1, float &b2, float c1, float c2) {
+    b2 = fmaxf(fminf(b1, c1), fmaxf(b2, c2));
+    b1 = fmaxf(b1, c1);
+}
+
+__device__ __forceinline__ float group_score(float b1, float b2, bool top2) {
+    return top2 && b2 > -CUDART_INF_F ? __fadd_rn(b1, b2) : b1;
+}
+
+// Which groups stay, as a bit mask, from the scores of groups g0 + lane of each 32.
+__device__ __forceinline__ uint64_t keep_groups(const float (&mine)[EPD_MAX_GROUPS / 32], int groups, int keep, int lane) {
+    uint64_t kept = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
-    m = warp_max(m);
-    float z = 0.0f;
-    if (m > -CUDART_INF_F) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) z += expf(l[i] - m);
+    for (int h = 0; h < EPD_MAX_GROUPS / 32; ++h) {
+        if (h * 32 >= groups) break;
+        int ahead = 0;
+        for (int o = 0; o < groups; ++o) {
+            const float other = __shfl_sync(kFull, o < 32 ? mine[0] : mine[1], o & 31);
+            ahead += other > mine[h] || (other == mine[h] && o < h * 32 + lane);
+        }
+        kept |= (uint64_t)__ballot_sync(kFull, h * 32 + lane < groups && ahead < keep) << (h * 32);
     }
-    z = warp_sum(z);
-    inv = z > 0.0f ? __fdiv_rn(1.0f, z) : 0.0f;
+    return kept;
 }
 
 template <typename T, int V, int SCORING>
-__global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
+    using L = Layout<T, V>;
     extern __shared__ float s_dyn[];
-    __shared__ float s_group[kWarps][EPD_MAX_GROUPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_trigger();
-    const int t = blockIdx.x * kWarps + warp;
+    const int t = blockIdx.x * kRouteWarps + warp;
     if (t >= a.T) return;
     const T *row = static_cast<const T *>(a.logits) + (int64_t)t * a.E;
-    float l[V];
+    float c[V];  // what decides the choice; -inf for an expert that cannot be chosen
     bool bad = false;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = i * 32 + lane;
-        l[i] = e < a.E ? clean_logit(to_f32(row[e]), bad) : -CUDART_INF_F;
-    }
+    load_row<T, V>(row, a.E, a.vec, lane, c, bad);
     if (bad) report(a.status, EPD_ERR_NONFINITE);
     float m = 0.0f, inv = 0.0f;
-    if (SCORING == EPD_SCORE_SOFTMAX) softmax_stats<V>(l, m, inv);
-    uint32_t key[V];
+    const bool grouped = a.keep < a.groups;
+    // scores are needed where a bias joins them or groups sum them; otherwise the logits order
+    // experts and groups exactly as their scores do
+    const bool scored = a.bias != nullptr || (grouped && a.top2);
+    // renormalised softmax weights are the softmax of the picks alone
+    if (SCORING == EPD_SCORE_SOFTMAX && (scored || !a.renorm)) softmax_stats<false>(c, m, inv);
+    if (scored) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = i * 32 + lane;
-        float c = l[i];
-        if (SCORING == EPD_SCORE_SIGMOID)
-            c = sigmoid_f32(l[i]);
-        else if (a.bias || a.top2)  // compared as scores; otherwise the logits order them
-            c = expf(l[i] - m) * inv;
-        if (a.bias && e < a.E) c = __fadd_rn(c, a.bias[e]);
-        key[i] = l[i] > -CUDART_INF_F ? order_key(c) : 0u;
-    }
-    if (a.keep < a.groups) {
-        // every group is scored by a power-of-two run of lanes from the row in shared memory
-        float *s_row = s_dyn + (size_t)warp * a.E;
+        for (int q = 0; q < L::Q; ++q) {
+            const int e0 = (q * 32 + lane) * L::C;
+            float bias[L::C];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = i * 32 + lane;
-            if (e < a.E) s_row[e] = key[i] ? key_value(key[i]) : -CUDART_INF_F;
-        }
-        __syncwarp();
-        const int size = a.E / a.groups;
-        int per = 1;
-        while (per * 2 * a.groups <= 32) per *= 2;
-        const int at_once = 32 / per;
-        for (int g0 = 0; g0 < a.groups; g0 += at_once) {
-            const int g = g0 + lane / per;
-            float b1 = -CUDART_INF_F, b2 = -CUDART_INF_F;
-            if (g < a.groups) {
-                for (int i = lane % per; i < size; i += per) {
-                    const float c = s_row[g * size + i];
-                    if (c > b1) {
-                        b2 = b1;
-                        b1 = c;
-                    } else {
-                        b2 = fmaxf(b2, c);
+            for (int i = 0; i < L::C; ++i) bias[i] = 0.0f;
+            if (a.bias) {
+                if (a.bias_vec) {
+                    if (e0 < a.E) {
+#pragma unroll
+                        for (int i = 0; i < L::C; i += 4) {
+                            const float4 b = *reinterpret_cast<const float4 *>(a.bias + e0 + i);
+                            bias[i] = b.x;
+                            if (i + 1 < L::C) bias[i + 1] = b.y;
+                            if (i + 2 < L::C) bias[i + 2] = b.z;
+                            if (i + 3 < L::C) bias[i + 3] = b.w;
+                        }
                     }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < L::C; ++i)
+                        if (e0 + i < a.E) bias[i] = a.bias[e0 + i];
                 }
             }
-            for (int o = per / 2; o; o >>= 1) {
-                const float c1 = __shfl_xor_sync(kFull, b1, o), c2 = __shfl_xor_sync(kFull, b2, o);
-                b2 = fmaxf(fminf(b1, c1), fmaxf(b2, c2));
-                b1 = fmaxf(b1, c1);
-            }
-            if (g < a.groups && lane % per == 0) {
-                float s = b1;
-                if (a.top2 && b2 > -CUDART_INF_F) s = __fadd_rn(b1, b2);
-                s_group[warp][g] = s;
-            }
-        }
-        __syncwarp();
-        uint64_t kept = 0;
-        for (int g0 = 0; g0 < a.groups; g0 += 32) {
-            const int g = g0 + lane;
-            int ahead = 0;
-            if (g < a.groups) {
-                const float mine = s_group[warp][g];
-                for (int o = 0; o < a.groups; ++o) {
-                    const float other = s_group[warp][o];
-                    ahead += other > mine || (other == mine && o < g);
-                }
-            }
-            kept |= (uint64_t)__ballot_sync(kFull, g < a.groups && ahead < a.keep) << g0;
-        }
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = i * 32 + lane;
-            if (e < a.E && !((kept >> (e / size)) & 1)) key[i] = 0;
-            else if (a.top2 && SCORING == EPD_SCORE_SOFTMAX && !a.bias && key[i]) key[i] = order_key(l[i]);
+            for (int i = 0; i < L::C; ++i) {
+                float &v = c[q * L::C + i];
+                const float score = SCORING == EPD_SCORE_SIGMOID ? fast_sigmoid(v) : __expf(v - m) * inv;
+                v = v > -CUDART_INF_F ? __fadd_rn(score, bias[i]) : -CUDART_INF_F;
+            }
         }
-    } else if (a.top2 && SCORING == EPD_SCORE_SOFTMAX && !a.bias) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (key[i]) key[i] = order_key(l[i]);
     }
-    // k rounds of argmax; lane j % 32 keeps pick j
-    int pick[2] = {-1, -1};
-    uint32_t best = 0;
-    int best_i = 0;
+    if (grouped) {
+        float mine[EPD_MAX_GROUPS / 32] = {-CUDART_INF_F, -CUDART_INF_F};
+        const int width = a.size / L::C;  // lanes per group, where groups are runs of whole chunks
+        const bool runs = width * L::C == a.size && (width & (width - 1)) == 0 && width <= 32 && a.groups <= 32;
+        if (runs) {
+            const int per = 32 / width;  // groups in each chunk of the warp
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (key[i] > best) best = key[i], best_i = i;
-    for (int j = 0; j < a.k; ++j) {
-        const uint32_t top = __reduce_max_sync(kFull, best);
-        if (top == 0) break;
-        const int e = best_i * 32 + lane;
-        const int chosen = __reduce_min_sync(kFull, best == top ? e : INT32_MAX);
-        if ((j & 31) == lane) pick[j >> 5] = chosen;
-        if ((chosen & 31) == lane) {
-            best = 0;
-            const int gone = chosen >> 5;
+            for (int q = 0; q < L::Q; ++q) {
+                float b1 = c[q * L::C], b2 = -CUDART_INF_F;
+#pragma unroll
+                for (int i = 1; i < L::C; ++i) {
+                    b2 = fmaxf(b2, fminf(b1, c[q * L::C + i]));
+                    b1 = fmaxf(b1, c[q * L::C + i]);
+                }
+                for (int o = width / 2; o; o >>= 1)
+                    merge_top2(b1, b2, __shfl_xor_sync(kFull, b1, o), __shfl_xor_sync(kFull, b2, o));
+                const float s = __shfl_sync(kFull, group_score(b1, b2, a.top2), (lane & (per - 1)) * width);
+                if (lane / per == q) mine[0] = s;
+            }
+            int ahead = 0;
+            for (int o = 0; o < a.groups; ++o) {
+                const float other = __shfl_sync(kFull, mine[0], o);
+                ahead += other > mine[0] || (other == mine[0] && o < lane);
+            }
+            const uint32_t kept = __ballot_sync(kFull, lane < a.groups && ahead < a.keep);
+#pragma unroll
+            for (int q = 0; q < L::Q; ++q) {
+                const bool stays = (kept >> ((q * per + lane / width) & 31)) & 1;
+#pragma unroll
+                for (int i = 0; i < L::C; ++i) c[q * L::C + i] = stays ? c[q * L::C + i] : -CUDART_INF_F;
+            }
+        } else {
+            // any other shape: from the row in shared memory, a power-of-two run of lanes a group
+            float *s_row = s_dyn + (size_t)warp * (a.E + EPD_MAX_GROUPS), *s_group = s_row + a.E;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                if (i == gone) key[i] = 0;
-                if (key[i] > best) best = key[i], best_i = i;
+                const int e = L::index(i, lane);
+                if (e < a.E) s_row[e] = c[i];
+            }
+            __syncwarp();
+            int per = 1;
+            while (per * 2 * a.groups <= 32) per *= 2;
+            for (int g0 = 0; g0 < a.groups; g0 += 32 / per) {
+                const int g = g0 + lane / per;
+                float b1 = -CUDART_INF_F, b2 = -CUDART_INF_F;
+                if (g < a.groups)
+                    for (int i = lane % per; i < a.size; i += per)
+                        merge_top2(b1, b2, s_row[g * a.size + i], -CUDART_INF_F);
+                for (int o = per / 2; o; o >>= 1)
+                    merge_top2(b1, b2, __shfl_xor_sync(kFull, b1, o), __shfl_xor_sync(kFull, b2, o));
+                if (g < a.groups && lane % per == 0) s_group[g] = group_score(b1, b2, a.top2);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < EPD_MAX_GROUPS / 32; ++h)
+                if (h * 32 + lane < a.groups) mine[h] = s_group[h * 32 + lane];
+            const uint64_t kept = keep_groups(mine, a.groups, a.keep, lane);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint32_t e = (uint32_t)L::index(i, lane);
+                const uint32_t g = a.size > 1 ? __umulhi(e, a.by_size) : e;
+                const uint32_t half = g & 32 ? (uint32_t)(kept >> 32) : (uint32_t)kept;
+                if (!((half >> (g & 31)) & 1)) c[i] = -CUDART_INF_F;
+            }
+        }
+        if (a.top2 && !a.bias) {  // groups are summed scores, experts are ordered by their logits
+            float l[V];
+            load_row<T, V>(row, a.E, a.vec, lane, l, bad);
+#pragma unroll
+            for (int i = 0; i < V; ++i) c[i] = c[i] > -CUDART_INF_F ? l[i] : -CUDART_INF_F;
+        }
+    }
+    // k rounds of argmax; lane j % 32 keeps pick j. o1, o2: the two largest's places in the lane's
+    // part of the row, as index(i, 0)
+    int pick[2] = {-1, -1};
+    float b1 = -CUDART_INF_F, b2 = -CUDART_INF_F;
+    int o1 = 0, o2 = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float v = c[i];
+        const bool p1 = v > b1, p2 = v > b2;
+        b2 = fmaxf(b2, fminf(b1, v));
+        o2 = p1 ? o1 : p2 ? L::index(i, 0) : o2;
+        b1 = fmaxf(b1, v);
+        o1 = p1 ? L::index(i, 0) : o1;
+    }
+    bool second = true;  // b2, o2 are this lane's next one
+    for (int j = 0; j < a.k; ++j) {
+        const float top = redux_max(b1);
+        if (top == -CUDART_INF_F) break;
+        const int e = b1 == top ? o1 + lane * L::C : INT32_MAX;
+        const int chosen = __reduce_min_sync(kFull, e);
+        if ((j & 31) == lane) pick[j >> 5] = chosen;
+        if (e == chosen) {
+            if (second) {
+                const int gone = o1;
+                b1 = b2;
+                o1 = o2;
+                o2 = gone;
+                second = false;
+            } else {
+                // o2 is the pick before this one; both leave, and the lane looks again
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (L::index(i, 0) == o1 || L::index(i, 0) == o2) c[i] = -CUDART_INF_F;
+                b1 = -CUDART_INF_F;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    o1 = c[i] > b1 ? L::index(i, 0) : o1;
+                    b1 = fmaxf(b1, c[i]);
+                }
+                o2 = o1;
             }
         }
     }
     float s[2];
     float sum = 0.0f;
 #pragma unroll
+    for (int h = 0; h < 2; ++h) s[h] = pick[h] >= 0 ? to_f32(row[pick[h]]) : -CUDART_INF_F;
+    if (SCORING == EPD_SCORE_SOFTMAX && a.renorm) {
+        m = warp_max(fmaxf(s[0], s[1]));
+        inv = 1.0f;
+    }
+#pragma unroll
     for (int h = 0; h < 2; ++h) {
-        s[h] = 0.0f;
-        if (pick[h] >= 0) {
-            const float v = to_f32(row[pick[h]]);
-            s[h] = SCORING == EPD_SCORE_SIGMOID ? sigmoid_f32(v) : expf(v - m) * inv;
-        }
+        if (SCORING == EPD_SCORE_SIGMOID)
+            s[h] = sigmoid_f32(s[h]);
+        else
+            s[h] = pick[h] >= 0 ? expf(s[h] - m) * inv : 0.0f;
         sum += s[h];
     }
     if (a.renorm) sum = warp_sum(sum);
@@ -224,138 +255,19 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
     }
 }
 
-struct RouteGradArgs {
-    const float *gw;
-    const void *logits;
-    const int64_t *idx;
-    int T, k, E;
-    int renorm;
-    float scale;
-    void *grad;
-    int32_t *status;
-};
-
-__device__ __forceinline__ void store_grad(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store_grad(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
-
 template <typename T, int V, int SCORING>
-__global__ void __launch_bounds__(kThreads) route_backward_kernel(RouteGradArgs a) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    pdl_wait();
-    pdl_trigger();
-    const int t = blockIdx.x * kWarps + warp;
-    if (t >= a.T) return;
-    const T *row = static_cast<const T *>(a.logits) + (int64_t)t * a.E;
-    float s[V];
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = i * 32 + lane;
-        s[i] = e < a.E ? clean_logit(to_f32(row[e]), bad) : -CUDART_INF_F;
-    }
-    if (bad) report(a.status, EPD_ERR_NONFINITE);
-    float m = 0.0f, inv = 0.0f;
-    if (SCORING == EPD_SCORE_SOFTMAX) {
-        softmax_stats<V>(s, m, inv);
-#pragma unroll
-        for (int i = 0; i < V; ++i) s[i] = inv > 0.0f ? expf(s[i] - m) * inv : 0.0f;
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) s[i] = sigmoid_f32(s[i]);
-    }
-    // the picks: lane j % 32 holds pick j, its score and its weight's gradient
-    int pick[2];
-    float g[2], ps[2];
-    float sum = 0.0f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int j = h * 32 + lane;
-        pick[h] = -1;
-        g[h] = ps[h] = 0.0f;
-        if (j < a.k) {
-            const int64_t id = a.idx[(int64_t)t * a.k + j];
-            if (id < -1 || id >= a.E)
-                report(a.status, EPD_ERR_INVALID_EXPERT);
-            else
-                pick[h] = (int)id;
-            if (pick[h] >= 0) {
-                bool b = false;
-                const float v = clean_logit(to_f32(row[pick[h]]), b);
-                ps[h] = SCORING == EPD_SCORE_SIGMOID ? sigmoid_f32(v)
-                                                     : (inv > 0.0f ? expf(v - m) * inv : 0.0f);
-                g[h] = a.gw[(int64_t)t * a.k + j] * a.scale;
-            }
-        }
-        sum += ps[h];
-    }
-    if (a.renorm) {
-        sum = warp_sum(sum);
-        const float rs = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-        float ds[2] = {0.0f, 0.0f};
-        for (int i = 0; i < a.k; ++i) {
-            const float gi = __shfl_sync(kFull, i < 32 ? g[0] : g[1], i & 31);
-            const float pi = __shfl_sync(kFull, i < 32 ? ps[0] : ps[1], i & 31) * rs;
-            ds[0] += (g[0] - gi) * pi;
-            ds[1] += (g[1] - gi) * pi;
-        }
-        g[0] = ds[0] * rs;
-        g[1] = ds[1] * rs;
-    }
-    float d[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) d[i] = 0.0f;
-    for (int j = 0; j < a.k; ++j) {
-        const int e = __shfl_sync(kFull, j < 32 ? pick[0] : pick[1], j & 31);
-        const float v = __shfl_sync(kFull, j < 32 ? g[0] : g[1], j & 31);
-        if (e >= 0 && (e & 31) == lane) {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (i == (e >> 5)) d[i] += v;
-        }
-    }
-    T *out = static_cast<T *>(a.grad) + (int64_t)t * a.E;
-    float dot = 0.0f;
-    if (SCORING == EPD_SCORE_SOFTMAX) {
-        if (!a.renorm) {  // renormalised picks: the sum is zero
-#pragma unroll
-            for (int i = 0; i < V; ++i) dot += d[i] * s[i];
-            dot = warp_sum(dot);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = i * 32 + lane;
-        const float v = SCORING == EPD_SCORE_SIGMOID ? d[i] * s[i] * (1.0f - s[i]) : s[i] * (d[i] - dot);
-        if (e < a.E) store_grad(out + e, v);
-    }
-}
-
-template <typename T, int V, int SCORING>
-epd_status_t launch_route(const RouteArgs &a, cudaStream_t st) {
-    const size_t smem = a.keep < a.groups ? (size_t)kWarps * a.E * sizeof(float) : 0;
-    const int grid = (a.T + kWarps - 1) / kWarps;
+epd_status_t launch_route(RouteArgs a, cudaStream_t st) {
+    a.vec = chunked<T, V>(a.logits, a.E);
+    a.bias_vec = a.vec && Layout<T, V>::C % 4 == 0 && a.bias && aligned16(a.bias);
+    const size_t smem = a.keep < a.groups ? (size_t)kRouteWarps * (a.E + EPD_MAX_GROUPS) * sizeof(float) : 0;
+    const int grid = (a.T + kRouteWarps - 1) / kRouteWarps;
     auto kernel = route_kernel<T, V, SCORING>;
-    if (smem > 48 * 1024 - sizeof(float) * kWarps * EPD_MAX_GROUPS) {
+    if (smem > 48 * 1024) {
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         const epd_status_t rc = record_cuda_error();
         if (rc != EPD_OK) return rc;
     }
-    return launch_pdl(kernel, grid, kThreads, smem, st, a);
-}
-
-template <typename T, int V, int SCORING>
-epd_status_t launch_route_backward(const RouteGradArgs &a, cudaStream_t st) {
-    return launch_pdl(route_backward_kernel<T, V, SCORING>, (a.T + kWarps - 1) / kWarps, kThreads, 0, st, a);
-}
-
-template <typename F>
-epd_status_t by_width(int E, F f) {
-    if (E <= 64) return f(std::integral_constant<int, 2>());
-    if (E <= 128) return f(std::integral_constant<int, 4>());
-    if (E <= 256) return f(std::integral_constant<int, 8>());
-    if (E <= 512) return f(std::integral_constant<int, 16>());
-    if (E <= 1024) return f(std::integral_constant<int, 32>());
-    return f(std::integral_constant<int, EPD_MAX_EXPERTS / 32>());
+    return launch_pdl(kernel, grid, kRouteThreads, smem, st, a);
 }
 
 }  // namespace
@@ -392,6 +304,8 @@ extern "C" epd_status_t ep_route(const void *logits, epd_dtype_t dtype, const fl
     a.E = E;
     a.groups = num_groups;
     a.keep = topk_groups;
+    a.size = E / num_groups;
+    a.by_size = a.size > 1 ? (uint32_t)(((1ull << 32) + a.size - 1) / a.size) : 0;
     a.top2 = group_score == EPD_GROUP_TOP2 && topk_groups < num_groups;
     a.renorm = renormalize != 0;
     a.scale = routed_scale;
@@ -403,51 +317,6 @@ extern "C" epd_status_t ep_route(const void *logits, epd_dtype_t dtype, const fl
         using T_ = decltype(type);
         constexpr int SC = decltype(sc)::value;
         return by_width(E, [&](auto v) { return launch_route<T_, decltype(v)::value, SC>(a, st); });
-    };
-    if (dtype == EPD_F32)
-        return scoring == EPD_SCORE_SOFTMAX ? go(float(), std::integral_constant<int, EPD_SCORE_SOFTMAX>())
-                                            : go(float(), std::integral_constant<int, EPD_SCORE_SIGMOID>());
-    return scoring == EPD_SCORE_SOFTMAX
-               ? go(__nv_bfloat16(), std::integral_constant<int, EPD_SCORE_SOFTMAX>())
-               : go(__nv_bfloat16(), std::integral_constant<int, EPD_SCORE_SIGMOID>());
-}
-
-extern "C" epd_status_t ep_route_backward(const float *grad_weights, const void *logits,
-                                          epd_dtype_t dtype, const int64_t *topk_idx,
-                                          int num_tokens, int num_topk, int num_experts,
-                                          epd_scoring_t scoring, int renormalize,
-                                          float routed_scale, void *grad_logits, int32_t *status,
-                                          epd_stream_t stream) {
-    using namespace epd;
-    const int T = num_tokens, k = num_topk, E = num_experts;
-    if (dtype != EPD_F32 && dtype != EPD_BF16) return EPD_ERR_INVALID_ARG;
-    if (scoring != EPD_SCORE_SOFTMAX && scoring != EPD_SCORE_SIGMOID) return EPD_ERR_INVALID_ARG;
-    if (T < 0 || E < 1 || E > EPD_MAX_EXPERTS || k < 1 || k > EPD_MAX_TOPK)
-        return EPD_ERR_INVALID_ARG;
-    if ((int64_t)T * k > INT32_MAX) return EPD_ERR_INVALID_ARG;
-    if (!status || !aligned4(status)) return EPD_ERR_INVALID_ARG;
-    if (T == 0) return EPD_OK;
-    if (!logits || !topk_idx || !grad_weights || !grad_logits) return EPD_ERR_INVALID_ARG;
-    const uintptr_t item = dtype == EPD_F32 ? 3u : 1u;
-    if (!aligned8(topk_idx) || !aligned4(grad_weights) ||
-        (reinterpret_cast<uintptr_t>(logits) & item) || (reinterpret_cast<uintptr_t>(grad_logits) & item))
-        return EPD_ERR_INVALID_ARG;
-    RouteGradArgs a;
-    a.gw = grad_weights;
-    a.logits = logits;
-    a.idx = topk_idx;
-    a.T = T;
-    a.k = k;
-    a.E = E;
-    a.renorm = renormalize != 0;
-    a.scale = routed_scale;
-    a.grad = grad_logits;
-    a.status = status;
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    auto go = [&](auto type, auto sc) {
-        using T_ = decltype(type);
-        constexpr int SC = decltype(sc)::value;
-        return by_width(E, [&](auto v) { return launch_route_backward<T_, decltype(v)::value, SC>(a, st); });
     };
     if (dtype == EPD_F32)
         return scoring == EPD_SCORE_SOFTMAX ? go(float(), std::integral_constant<int, EPD_SCORE_SOFTMAX>())

@@ -1,0 +1,215 @@
+// route_backward.cu -- gradient of the router's weights (ep_route_backward).
+//
+// Sigmoid scores and renormalised softmax weights (the softmax of the picks alone) depend on the
+// picks' logits only: the gradient is zero but for them, and the row is not read -- a warp fills
+// its row with zeros and its lanes store their picks over them. Softmax weights without
+// renormalising depend on the whole row: one pass over it in registers.
+#include "route.cuh"
+
+namespace epd {
+namespace {
+
+struct RouteGradArgs {
+    const float *gw;
+    const void *logits;
+    const int64_t *idx;
+    int T, k, E;
+    int renorm, vec;
+    float scale;
+    void *grad;
+    int32_t *status;
+};
+
+__device__ __forceinline__ void from_f32(float &p, float v) { p = v; }
+__device__ __forceinline__ void from_f32(__nv_bfloat16 &p, float v) { p = __float2bfloat16_rn(v); }
+
+// What the two kernels know of a token's picks: lane j % 32 holds pick j (its expert, or -1), its
+// logit and its weight's gradient.
+template <typename T>
+__device__ __forceinline__ void load_picks(const RouteGradArgs &a, int t, const T *row, int lane, int (&pick)[2],
+                                           float (&logit)[2], float (&g)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int j = h * 32 + lane;
+        pick[h] = -1;
+        g[h] = 0.0f;
+        logit[h] = -CUDART_INF_F;
+        if (j < a.k) {
+            const int64_t id = a.idx[(int64_t)t * a.k + j];
+            if (id < -1 || id >= a.E) {
+                report(a.status, EPD_ERR_INVALID_EXPERT);
+            } else if (id >= 0) {
+                bool bad = false;
+                pick[h] = (int)id;
+                logit[h] = clean_logit(to_f32(row[id]), bad);
+                if (bad) report(a.status, EPD_ERR_NONFINITE);
+                g[h] = a.gw[(int64_t)t * a.k + j] * a.scale;
+            }
+        }
+    }
+}
+
+template <typename T, int SCORING>
+__global__ void __launch_bounds__(kRouteThreads) route_backward_picks_kernel(RouteGradArgs a) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
+    pdl_trigger();
+    const int t = blockIdx.x * kRouteWarps + warp;
+    if (t >= a.T) return;
+    const T *row = static_cast<const T *>(a.logits) + (int64_t)t * a.E;
+    T *out = static_cast<T *>(a.grad) + (int64_t)t * a.E;
+    int pick[2];
+    float g[2], s[2];
+    load_picks(a, t, row, lane, pick, s, g);
+    if (a.vec) {
+        constexpr int C = 16 / sizeof(T);
+        for (int e = lane * C; e < a.E; e += 32 * C) st16(out + e, make_uint4(0, 0, 0, 0));
+    } else {
+        for (int e = lane; e < a.E; e += 32) from_f32(out[e], 0.0f);
+    }
+    if (SCORING == EPD_SCORE_SOFTMAX) {
+        const float m = warp_max(fmaxf(s[0], s[1]));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s[h] = m > -CUDART_INF_F ? expf(s[h] - m) : 0.0f;
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s[h] = sigmoid_f32(s[h]);
+    }
+    if (a.renorm) {
+        const float sum = warp_sum(s[0] + s[1]);
+        const float rs = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+        float ds[2] = {0.0f, 0.0f};
+        for (int i = 0; i < a.k; ++i) {
+            const float gi = __shfl_sync(kFull, i < 32 ? g[0] : g[1], i & 31);
+            const float pi = __shfl_sync(kFull, i < 32 ? s[0] : s[1], i & 31) * rs;
+            ds[0] += (g[0] - gi) * pi;
+            ds[1] += (g[1] - gi) * pi;
+        }
+        g[0] = ds[0] * rs;
+        g[1] = ds[1] * rs;
+    }
+    // an expert picked more than once: every one of its picks has the sum, in the picks' order
+    float d[2] = {0.0f, 0.0f};
+    for (int i = 0; i < a.k; ++i) {
+        const int e = __shfl_sync(kFull, i < 32 ? pick[0] : pick[1], i & 31);
+        const float v = __shfl_sync(kFull, i < 32 ? g[0] : g[1], i & 31);
+        if (e == pick[0]) d[0] += v;
+        if (e == pick[1]) d[1] += v;
+    }
+    __syncwarp();  // the zeros come first
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (pick[h] >= 0) from_f32(out[pick[h]], SCORING == EPD_SCORE_SIGMOID ? d[h] * s[h] * (1.0f - s[h]) : d[h] * s[h]);
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kRouteThreads) route_backward_row_kernel(RouteGradArgs a) {
+    using L = Layout<T, V>;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
+    pdl_trigger();
+    const int t = blockIdx.x * kRouteWarps + warp;
+    if (t >= a.T) return;
+    const T *row = static_cast<const T *>(a.logits) + (int64_t)t * a.E;
+    int pick[2];
+    float g[2], ps[2], s[V];
+    load_picks(a, t, row, lane, pick, ps, g);
+    bool bad = false;
+    load_row<T, V>(row, a.E, a.vec, lane, s, bad);
+    if (bad) report(a.status, EPD_ERR_NONFINITE);
+    float m, inv;
+    softmax_stats<true>(s, m, inv);
+    float dot = 0.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) dot += pick[h] >= 0 && inv > 0.0f ? g[h] * (expf(ps[h] - m) * inv) : 0.0f;
+    dot = warp_sum(dot);
+    float d[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) d[i] = 0.0f;
+    for (int j = 0; j < a.k; ++j) {
+        const int e = __shfl_sync(kFull, j < 32 ? pick[0] : pick[1], j & 31);
+        const float v = __shfl_sync(kFull, j < 32 ? g[0] : g[1], j & 31);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (e == L::index(i, lane)) d[i] += v;
+    }
+    T *out = static_cast<T *>(a.grad) + (int64_t)t * a.E;
+#pragma unroll
+    for (int q = 0; q < L::Q; ++q) {
+        const int e0 = (q * 32 + lane) * L::C;
+        alignas(16) T v[L::C];
+#pragma unroll
+        for (int c = 0; c < L::C; ++c) {
+            const int i = q * L::C + c;
+            from_f32(v[c], inv > 0.0f ? s[i] * inv * (d[i] - dot) : 0.0f);
+        }
+        if (a.vec) {
+            if (e0 < a.E) {
+                if (sizeof(v) == 16)
+                    *reinterpret_cast<uint4 *>(out + e0) = *reinterpret_cast<const uint4 *>(v);
+                else if (sizeof(v) == 8)
+                    *reinterpret_cast<uint2 *>(out + e0) = *reinterpret_cast<const uint2 *>(v);
+                else
+                    *reinterpret_cast<uint32_t *>(out + e0) = *reinterpret_cast<const uint32_t *>(v);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < L::C; ++c)
+                if (e0 + c < a.E) out[e0 + c] = v[c];
+        }
+    }
+}
+
+template <typename T>
+epd_status_t launch_route_backward(RouteGradArgs a, int scoring, cudaStream_t st) {
+    const int grid = (a.T + kRouteWarps - 1) / kRouteWarps;
+    if (scoring == EPD_SCORE_SOFTMAX && !a.renorm)
+        return by_width(a.E, [&](auto width) {
+            constexpr int V = decltype(width)::value;
+            a.vec = chunked<T, V>(a.logits, a.E) && chunked<T, V>(a.grad, a.E);
+            return launch_pdl(route_backward_row_kernel<T, V>, grid, kRouteThreads, 0, st, a);
+        });
+    a.vec = a.E % (16 / sizeof(T)) == 0 && aligned16(a.grad);
+    return launch_pdl(scoring == EPD_SCORE_SIGMOID ? route_backward_picks_kernel<T, EPD_SCORE_SIGMOID>
+                                                   : route_backward_picks_kernel<T, EPD_SCORE_SOFTMAX>,
+                      grid, kRouteThreads, 0, st, a);
+}
+
+}  // namespace
+}  // namespace epd
+
+extern "C" epd_status_t ep_route_backward(const float *grad_weights, const void *logits,
+                                          epd_dtype_t dtype, const int64_t *topk_idx,
+                                          int num_tokens, int num_topk, int num_experts,
+                                          epd_scoring_t scoring, int renormalize,
+                                          float routed_scale, void *grad_logits, int32_t *status,
+                                          epd_stream_t stream) {
+    using namespace epd;
+    const int T = num_tokens, k = num_topk, E = num_experts;
+    if (dtype != EPD_F32 && dtype != EPD_BF16) return EPD_ERR_INVALID_ARG;
+    if (scoring != EPD_SCORE_SOFTMAX && scoring != EPD_SCORE_SIGMOID) return EPD_ERR_INVALID_ARG;
+    if (T < 0 || E < 1 || E > EPD_MAX_EXPERTS || k < 1 || k > EPD_MAX_TOPK)
+        return EPD_ERR_INVALID_ARG;
+    if ((int64_t)T * k > INT32_MAX) return EPD_ERR_INVALID_ARG;
+    if (!status || !aligned4(status)) return EPD_ERR_INVALID_ARG;
+    if (T == 0) return EPD_OK;
+    if (!logits || !topk_idx || !grad_weights || !grad_logits) return EPD_ERR_INVALID_ARG;
+    const uintptr_t item = dtype == EPD_F32 ? 3u : 1u;
+    if (!aligned8(topk_idx) || !aligned4(grad_weights) ||
+        (reinterpret_cast<uintptr_t>(logits) & item) || (reinterpret_cast<uintptr_t>(grad_logits) & item))
+        return EPD_ERR_INVALID_ARG;
+    RouteGradArgs a;
+    a.gw = grad_weights;
+    a.logits = logits;
+    a.idx = topk_idx;
+    a.T = T;
+    a.k = k;
+    a.E = E;
+    a.renorm = renormalize != 0;
+    a.scale = routed_scale;
+    a.grad = grad_logits;
+    a.status = status;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return dtype == EPD_F32 ? launch_route_backward<float>(a, scoring, st)
+                            : launch_route_backward<__nv_bfloat16>(a, scoring, st);
+}
