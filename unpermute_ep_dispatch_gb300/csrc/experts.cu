@@ -52,7 +52,7 @@ constexpr int kTailBytes = 512;                 // published tiles and barriers
 constexpr int kScaleGroup = 4;                  // reduction steps per group of staged scales
 constexpr int kScaleBytes = 2 * kScaleGroup * 2 * kTileRows * 4;
 constexpr int kRing = 4;                        // tiles published ahead
-constexpr int kCuts = 7;                        // boxes of 64, 32, ... 1 rows (wgrad)
+constexpr int kCuts = 18;                       // wgrad's boxes: 64, 32, 16 and 1 to 15 rows
 constexpr int kGroupTiles = 8;                  // token tiles that share a pass over the features
 
 template <bool FP8>
@@ -93,9 +93,12 @@ __device__ __forceinline__ void expert_region(const epd_expert_rows_t &r, int e,
 }
 
 // The operands' TMA maps. wgrad's reduction runs over a region's rows, whose last step may hold
-// fewer than 64: it is loaded in boxes of 32, 16, ... 1 rows, and what is missing to a multiple
-// of 16 (one mma's reduction) in boxes past the end of the buffer, which read as zero. The
-// other rows of the buffer are never multiplied.
+// fewer than 64: it is loaded in boxes of 32, 16 and 1 to 15 rows, and what is missing to a
+// multiple of 16 (one mma's reduction) in a box past the end of the buffer, which reads as zero.
+// The other rows of the buffer are never multiplied. A box costs some 33 cycles whatever its
+// height (64 experts of 380 rows: 340 us with heights that are powers of two, which take
+// five cuts where these take three).
+constexpr int cut_rows(int i) { return i < 3 ? 64 >> i : i - 2; }
 template <int MODE>
 struct Maps {
     static constexpr int kCount = MODE == kWgrad ? kCuts : 1;
@@ -582,18 +585,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                             } else {
                                 const int used = (left + 15) & ~15;
                                 mbar_arrive_tx_cluster(bar, (2 + boxes) * used * 128);
+                                constexpr int kMaps = Maps<MODE>::kCount;
                                 int r = 0;
 #pragma unroll 1
-                                for (int c = 1; c < kCuts + 4; ++c) {
-                                    // the region's rows in falling powers of two, then the zeros
-                                    const int cut = c < kCuts ? c : c - kCuts + 3;
-                                    if (!(((c < kCuts ? left : used - left) << cut) & 64)) continue;
-                                    const int from = c < kCuts ? at + r : (int)p.rows.capacity_rows;
-                                    tma_2d(a + r * 128, &maps.m[cut % Maps<MODE>::kCount], feat, from, bar);
-                                    tma_2d(a + 8192 + r * 128, &maps.m[cut % Maps<MODE>::kCount], feat + 64, from, bar);
+                                for (int c = 0; c < 4; ++c) {
+                                    // 32 and 16 rows, the last ones, and the zeros after them
+                                    const int rows = c < 2 ? left & (32 >> c) : c == 2 ? left & 15 : used - left;
+                                    if (rows == 0) continue;
+                                    const int map = (rows >= 16 ? (rows == 32 ? 1 : 2) : rows + 2) % kMaps;
+                                    const int from = c < 3 ? at + r : (int)p.rows.capacity_rows;
+                                    tma_2d(a + r * 128, &maps.m[map], feat, from, bar);
+                                    tma_2d(a + 8192 + r * 128, &maps.m[map], feat + 64, from, bar);
                                     for (int i = 0; i < boxes; ++i)
-                                        tma_2d(b + i * 8192 + r * 128, &maps.n[cut % Maps<MODE>::kCount], row + i * 64, from, bar);
-                                    r += 64 >> cut;
+                                        tma_2d(b + i * 8192 + r * 128, &maps.n[map], row + i * 64, from, bar);
+                                    r += rows;
                                 }
                             }
                         } else {
@@ -848,35 +853,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
     if (warp == kMmaWarp) tmem_free_pair(tmem, 512);
 }
 
-// dbias[e, n] = the sum of the expert's rows of dy: a block per 64 columns of an expert, eight
-// rows at a time in a fixed order.
-__global__ void __launch_bounds__(256) bias_grad_kernel(const epd_expert_rows_t rows, const uint8_t *dy, int N,
-                                                        float *dbias, int32_t *status) {
-    __shared__ float s_sum[32][64];
-    pdl_wait();
-    pdl_trigger();
-    const int e = blockIdx.y, oct = threadIdx.x & 7, part = threadIdx.x >> 3;
-    const int n = blockIdx.x * 64 + oct * 8;
-    int start, count;
-    expert_region(rows, e, start, count, status);
-    float sum[8] = {};
-    if (n < N) {
-        for (int r = part; r < count; r += 32) {
-            float f[8];
-            unpack8_bf16(ld_stream16(dy + (((int64_t)start + r) * N + n) * 2), f);
+// dbias[e, n] = the sum of the expert's rows of dy, in a fixed order: a thread sums every 32nd
+// row for eight columns, then the 32 parts are added up. It runs beside the wgrad kernel before
+// it on the stream (a block per SM fits next to that kernel's), which is why it waits for that
+// kernel last: it reads nothing that kernel writes, and cannot start before every block of it has
+// passed its own wait for what came earlier. The wait comes before this kernel ends, so whatever
+// follows on the stream still finds both done.
+constexpr int kBiasThreads = 256, kBiasRows = 8;
+__global__ void __launch_bounds__(kBiasThreads, 1) bias_grad_kernel(const epd_expert_rows_t rows, const uint8_t *dy,
+                                                                    int N, float *dbias, int32_t *status) {
+    __shared__ float s_sum[kBiasThreads / 8][64];
+    const int oct = threadIdx.x & 7, part = threadIdx.x >> 3;
+    const int groups = (N + 63) / 64;
+    for (int item = blockIdx.x; item < groups * rows.num_experts; item += gridDim.x) {
+        const int e = item / groups, n = (item - e * groups) * 64 + oct * 8;
+        int start, count;
+        expert_region(rows, e, start, count, status);
+        float sum[8] = {};
+        if (n < N) {
+            const uint8_t *at = dy + ((int64_t)start * N + n) * 2;
+            const int64_t pitch = (int64_t)N * 2;
+            for (int r = part; r < count; r += kBiasRows * 32) {
+                uint4 v[kBiasRows];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += f[i];
+                for (int i = 0; i < kBiasRows; ++i)
+                    v[i] = r + i * 32 < count ? ld_stream16(at + (r + i * 32) * pitch) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < kBiasRows; ++i) {
+                    float f[8];
+                    unpack8_bf16(v[i], f);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[j] += f[j];
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s_sum[part][oct * 8 + i] = sum[i];
+        __syncthreads();
+        if (threadIdx.x < 64 && n - oct * 8 + (int)threadIdx.x < N) {
+            float v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kBiasThreads / 8; ++i) v += s_sum[i][threadIdx.x];
+            dbias[(int64_t)e * N + n - oct * 8 + threadIdx.x] = v;
         }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s_sum[part][oct * 8 + i] = sum[i];
-    __syncthreads();
-    if (threadIdx.x < 64 && blockIdx.x * 64 + threadIdx.x < N) {
-        float v = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v += s_sum[i][threadIdx.x];
-        dbias[(int64_t)e * N + blockIdx.x * 64 + threadIdx.x] = v;
-    }
+    pdl_wait();
+    pdl_trigger();
 }
 
 // ---------------------------------------------------------------------------- host
@@ -1087,12 +1110,12 @@ extern "C" epd_status_t ep_expert_matmul_wgrad(const epd_expert_rows_t *rows, co
     const bool any = rows->capacity_rows > 0;
     Maps<kWgrad> maps;
     for (int i = 0; i < kCuts; ++i)
-        if (!encode_rows(&maps.m[i], false, any ? x : dw, rows->capacity_rows, K, 64 >> i) ||
-            !encode_rows(&maps.n[i], false, any ? dy : dw, rows->capacity_rows, N, 64 >> i))
+        if (!encode_rows(&maps.m[i], false, any ? x : dw, rows->capacity_rows, K, cut_rows(i)) ||
+            !encode_rows(&maps.n[i], false, any ? dy : dw, rows->capacity_rows, N, cut_rows(i)))
             return EPD_ERR_CUDA;
     const epd_status_t rc = launch<kWgrad, false, false>(maps, p, st);
     if (rc != EPD_OK || !dbias) return rc;
-    bias_grad_kernel<<<dim3((N + 63) / 64, rows->num_experts), 256, 0, st>>>(
-        *rows, static_cast<const uint8_t *>(dy), N, dbias, status);
-    return record_cuda_error();
+    const int64_t items = (int64_t)((N + 63) / 64) * rows->num_experts;
+    return launch_pdl(bias_grad_kernel, (int)(items < sm_count() ? items : sm_count()), kBiasThreads, 0, st, *rows,
+                      static_cast<const uint8_t *>(dy), N, dbias, status);
 }
