@@ -96,15 +96,6 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int
         : "memory");
 }
 
-__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
-                                       uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
-        : "memory");
-}
-
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -125,7 +116,7 @@ __device__ __forceinline__ void tcgen05_fence_before() { asm volatile("tcgen05.f
 __device__ __forceinline__ void tcgen05_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// 32 (16) columns of 16 lanes (the lane offset of `addr` a multiple of 16), as fragments: of
+// 32 columns of 16 lanes (the lane offset of `addr` a multiple of 16), as fragments: of
 // thread t, v[2c + b] is lane 8b + t / 4, column 4c + t % 4. (The 16x256b shape, whose fragments
 // are the mma's own, reads tensor memory at half the rate: 256 against over 440 bytes a clock.)
 __device__ __forceinline__ void tmem_ld_frag(uint32_t (&v)[16], uint32_t addr) {
@@ -137,10 +128,13 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t (&v)[16], uint32_t addr) {
         : "r"(addr));
 }
 
-__device__ __forceinline__ void tmem_ld_frag(uint32_t (&v)[8], uint32_t addr) {
+// 16 columns of this warp's 32 lanes: v[c] = column c of the thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t (&v)[16], uint32_t addr) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x128b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(addr));
 }
 
@@ -174,13 +168,19 @@ __device__ __forceinline__ void sts16(uint32_t addr, const uint4 &v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// (a0, a1) += (d0, d1) * s, one instruction for both.
-__device__ __forceinline__ void fma2(float &a0, float &a1, uint32_t d0, uint32_t d1, float s) {
-    uint64_t a, d, ss;
+// A value in both halves of a pair.
+__device__ __forceinline__ uint64_t twice(float s) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(p) : "f"(s));
+    return p;
+}
+
+// (a0, a1) += (d0, d1) * (s, s), one instruction for both; `s` holds the scale twice.
+__device__ __forceinline__ void fma2(float &a0, float &a1, uint32_t d0, uint32_t d1, uint64_t s) {
+    uint64_t a, d;
     asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
     asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(d0), "r"(d1));
-    asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(d), "l"(ss));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(d), "l"(s));
     asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
 }
 

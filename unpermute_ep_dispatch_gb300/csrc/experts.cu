@@ -13,9 +13,17 @@
 // The features are the instruction's fixed 256 rows and the tokens its free dimension,
 // because experts have few and uneven rows: an expert's c rows are cut into ceil(c / 256)
 // equal tiles and each runs with just the width it needs, where the other way round a tile
-// would be padded to 128 or 256 rows. Each block stages its 128 feature rows and half of the
-// token rows per step of the reduction (128 bytes wide), so a token row that both blocks
-// multiply is staged once.
+// would be padded to 256 rows. Each block stages its 128 feature rows and half of the token
+// rows per step of the reduction (128 bytes wide), so a token row that both blocks multiply is
+// staged once.
+//
+// e4m3 (forward only) is the other way round, D[256 rows x n features]. Rows are scaled per 128
+// columns and weights per 128 x 128, so the product of one 128-wide step cannot stay in the
+// tensor core's accumulator: every step's D goes to registers as acc += D * (x_scale *
+// w_scale). With a row a lane that is one scale a thread and weight block; with a column a row
+// every thread needs all columns' scales from shared memory, whose bandwidth the operands
+// already take whole (each step is written once and read once: 64 KiB in the 512 cycles of its
+// mma), and a step took 867 to 1120 cycles.
 //
 // Warps: the epilogue's 8 (e4m3: 16), the producer, which walks the tiles, publishes them to
 // the others and feeds TMA, one that issues the mma (in the pair's first block), and for e4m3
@@ -23,10 +31,6 @@
 // epilogue runs under the next tile's mma. Blocks walk the tiles of all experts in a fixed
 // order (persistent, one pair per two SMs); the experts' counts are read from device memory,
 // 32 at a time, by the producer itself.
-//
-// e4m3: rows are scaled per 128 columns and weights per 128 x 128, so the product of one
-// 128-wide step cannot stay in the tensor core's accumulator: every step's D goes to
-// registers as acc += D * (x_scale * w_scale), again through the two tensor-memory buffers.
 #include <cuda.h>
 
 #include "epd_math.cuh"
@@ -44,13 +48,14 @@ constexpr int kScaleWarps = 2;
 template <bool FP8>
 constexpr int kThreadsOf = (kEpiWarpsOf<FP8> + 2 + (FP8 ? kScaleWarps : 0)) * 32;
 constexpr int kTileRows = 256;                  // most token rows (wgrad: output rows) of a tile
+constexpr int kAcrossRows = 128;                // e4m3: most rows of a tile with the features as M
 constexpr int kOperandBytes = 128 * 128;        // 128 rows of 128 bytes: one operand of a stage
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kRowBox = 32;                     // token rows per TMA box
 constexpr int kStagingBytes = 32 * 80;          // per epilogue warp: 32 rows of 64 bytes, 80 apart
-constexpr int kTailBytes = 512;                 // published tiles and barriers
+constexpr int kTailBytes = 768;                 // published tiles and barriers
 constexpr int kScaleGroup = 4;                  // reduction steps per group of staged scales
-constexpr int kScaleBytes = 2 * kScaleGroup * 2 * kTileRows * 4;
+constexpr int kScaleBytes = 2 * kScaleGroup * 128 * 8;  // a row's with each of the tile's two weight blocks
 constexpr int kRing = 4;                        // tiles published ahead
 constexpr int kCuts = 18;                       // wgrad's boxes: 64, 32, 16 and 1 to 15 rows
 constexpr int kGroupTiles = 8;                  // token tiles that share a pass over the features
@@ -99,10 +104,12 @@ __device__ __forceinline__ void expert_region(const epd_expert_rows_t &r, int e,
 // height (64 experts of 380 rows: 340 us with heights that are powers of two, which take
 // five cuts where these take three).
 constexpr int cut_rows(int i) { return i < 3 ? 64 >> i : i - 2; }
+// Token rows (forward, dgrad) come in boxes of 32 and, half a tile being a multiple of 16, one of
+// 16: a box more than needed is bandwidth into the SM lost.
 template <int MODE>
 struct Maps {
-    static constexpr int kCount = MODE == kWgrad ? kCuts : 1;
-    CUtensorMap m[kCount], n[kCount];
+    static constexpr int kM = MODE == kWgrad ? kCuts : 1, kN = MODE == kWgrad ? kCuts : 2;
+    CUtensorMap m[kM], n[kN];
 };
 
 // One tile of the work: `rows` valid columns of D from row `row0` (a token row; for wgrad an
@@ -111,6 +118,7 @@ struct alignas(16) Tile {
     int e, start, count;  // e = -1 past the last tile
     int feat0, row0, rows, n;
     int steps;  // of the reduction
+    int across; // e4m3: the features are the M operand
 };
 
 // The producer's tiles, as the other warps of the block get them: a ring in shared memory.
@@ -135,7 +143,7 @@ struct Ring {
 
 // Walks the tiles of one pair, a warp together: lane l holds expert batch + l, and a tile's
 // expert is found by a ballot over the running tile counts.
-template <int MODE, int STEP>
+template <int MODE, int STEP, bool FP8>
 struct Walker {
     const ExpertArgs &p;
     int lane, feat_tiles, feat_step;
@@ -190,10 +198,16 @@ struct Walker {
         const int rt = group * kGroupTiles + rest - ft * width;
         t.feat0 = ft * feat_step;
         const int total = MODE == kWgrad ? p.N : t.count;
-        const int each = ((total + row_tiles - 1) / row_tiles + 31) & ~31;
+        // equal tiles of the least width; e4m3: full tiles of rows, and a last one of at most 128
+        // turned across
+        const int each = FP8 ? kTileRows : ((total + row_tiles - 1) / row_tiles + 31) & ~31;
         t.row0 = rt * each;
         t.rows = min(each, total - t.row0);
-        t.n = t.rows > 0 ? (t.rows + 31) & ~31 : 32;
+        t.across = !FP8 || t.rows <= kAcrossRows;
+        if (t.across)
+            t.n = t.rows > 0 ? (t.rows + 31) & ~31 : 32;
+        else  // feat_step features, gated: and their up
+            t.n = feat_step == 128 ? 256 : (min(256, p.N - t.feat0) + 31) & ~31;
         const int red = MODE == kForward ? p.K : MODE == kDgrad ? p.N : t.count;
         t.steps = (red + STEP - 1) / STEP;
         return true;
@@ -482,11 +496,88 @@ struct Output {
     }
 };
 
+// ---- e4m3: a lane is a row, f[c] its column c of 32.
+__device__ __forceinline__ void put_rows(uint32_t stage, const float (&f)[32], uint8_t *at, int64_t pitch, int rows,
+                                         int parts) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        sts16(stage + lane * kPitch + i * 16,
+              make_uint4(pack2_bf16(f[8 * i], f[8 * i + 1]), pack2_bf16(f[8 * i + 2], f[8 * i + 3]),
+                         pack2_bf16(f[8 * i + 4], f[8 * i + 5]), pack2_bf16(f[8 * i + 6], f[8 * i + 7])));
+    __syncwarp();
+    const int part = lane & 3;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int row = lane_row(it);
+        const uint4 v = lds16(stage + row * kPitch + part * 16);
+        if (part < parts && row < rows) st16(at + row * pitch + part * 16, v);
+    }
+}
+
+// Rows row0 .. row0 + 31 of the tile, columns col0 .. col0 + 31 of its two blocks of features
+// (gated: of its gate features and of their up).
+template <bool GATED>
+__device__ __forceinline__ void finish_rows(const ExpertArgs &p, const Tile &t, int row0, int col0, uint32_t stage,
+                                            float (&acc)[2][32]) {
+    const int rows = t.rows - row0;
+    const int64_t row = (int64_t)t.start + t.row0 + row0, NW = GATED ? 2 * (int64_t)p.N : p.N;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        // features of this block: where they begin in a row of the pre-activations, and how many
+        const int feat = t.feat0 + col0 + (GATED ? 0 : h * 128);
+        const int64_t at = feat + (GATED && h ? (int64_t)p.N : 0);
+        const int parts = max(0, min(4, (p.N - feat) / 8));
+        float(&f)[32] = acc[h];
+        if (p.bias) {
+            const float *b = p.bias + t.e * NW + at;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) f[c] += c < parts * 8 ? b[c] : 0.0f;
+        }
+        if (p.preact) put_rows(stage, f, p.preact + (row * NW + at) * 2, NW * 2, rows, parts);
+        if (GATED) {
+            if (h == 0) continue;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) f[c] = acc[0][c] * fast_sigmoid(acc[0][c]) * f[c];
+        } else if (p.act == EPD_ACT_RELU) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) f[c] = activate<EPD_ACT_RELU>(f[c]);
+        } else if (p.act == EPD_ACT_SILU) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) f[c] = activate<EPD_ACT_SILU>(f[c]);
+        } else if (p.act == EPD_ACT_GELU) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) f[c] = activate<EPD_ACT_GELU>(f[c]);
+        }
+        const int64_t pitch = (int64_t)p.N * 2;
+        if (p.residual) {
+            Ahead r;
+            r.fetch(p.residual + row * pitch + (int64_t)feat * 2, pitch, rows, parts);
+            const int lane = threadIdx.x & 31;
+            __syncwarp();
+#pragma unroll
+            for (int it = 0; it < 4; ++it) sts16(stage + lane_row(it) * kPitch + (lane & 3) * 16, r.v[it]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float e[8];
+                unpack8_bf16(lds16(stage + lane * kPitch + i * 16), e);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) f[8 * i + c] += e[c];
+            }
+        }
+        put_rows(stage, f, p.y + row * pitch + (int64_t)feat * 2, pitch, rows, parts);
+    }
+}
+
 template <int MODE, bool FP8, bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
     expert_kernel(const __grid_constant__ Maps<MODE> maps, const ExpertArgs p) {
     constexpr bool kHalf = GATED && MODE == kForward;  // half of a block's 128 lanes are up features
     constexpr int kStages = kStagesOf<FP8>;
+    // accumulators: two of 256 columns; e4m3, which uses one a step, four of 128 where that is enough
+    constexpr int kAccs = FP8 ? 4 : 2;
     constexpr int kEpiWarps = kEpiWarpsOf<FP8>;
     constexpr int kProducerWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kScaleWarp = kEpiWarps + 2;
     constexpr int kStep = FP8 ? 128 : 64;              // reduction elements per stage
@@ -500,8 +591,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
     Tile *slots = reinterpret_cast<Tile *>(after);
     after += kRing * sizeof(Tile);
     uint64_t *bars = reinterpret_cast<uint64_t *>(after);
-    constexpr int kEmpty = kStages, kAccFull = 2 * kStages, kAccEmpty = kAccFull + 2, kScFull = kAccEmpty + 2,
-                  kScEmpty = kScFull + 2, kTileFull = kScEmpty + 2, kTileEmpty = kTileFull + kRing,
+    constexpr int kEmpty = kStages, kAccFull = 2 * kStages, kAccEmpty = kAccFull + kAccs,
+                  kScFull = kAccEmpty + kAccs, kScEmpty = kScFull + 2, kTileFull = kScEmpty + 2, kTileEmpty = kTileFull + kRing,
                   kSwap = kTileEmpty + kRing, kSlot = kSwap + kEpiWarps / 2;
     static_assert((kSlot + 1) * 8 + kRing * sizeof(Tile) <= kTailBytes, "the barriers fit");
     const uint32_t base = smem_addr(smem), bar0 = smem_addr(bars);
@@ -515,9 +606,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             mbar_init(bars + i, 2);           // both blocks' producers
             mbar_init(bars + kEmpty + i, 1);  // a commit
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kAccs; ++i) {
             mbar_init(bars + kAccFull + i, 1);
             mbar_init(bars + kAccEmpty + i, 2 * kEpiWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(bars + kScFull + i, kScaleWarps);
             mbar_init(bars + kScEmpty + i, kEpiWarps);
         }
@@ -527,10 +620,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         }
         for (int i = 0; i < kEpiWarps / 2; ++i) mbar_init(bars + kSwap + i, 64);
         mbar_init_fence();
-        for (int i = 0; i < Maps<MODE>::kCount; ++i) {
-            tma_prefetch_map(&maps.m[i]);
-            tma_prefetch_map(&maps.n[i]);
-        }
+        for (int i = 0; i < Maps<MODE>::kM; ++i) tma_prefetch_map(&maps.m[i]);
+        for (int i = 0; i < Maps<MODE>::kN; ++i) tma_prefetch_map(&maps.n[i]);
     }
     if (warp == kMmaWarp) tmem_alloc_pair(bar0 + 8 * kSlot, 512);
     tcgen05_fence_before();
@@ -550,7 +641,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         if (warp == kProducerWarp) {
             const uint32_t lead_full = map_to_rank(full, 0);
             const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
-            Walker<MODE, kStep> walk(p, kFeatStep);
+            Walker<MODE, kStep, FP8> walk(p, kFeatStep);
             int stage = 0, issued = 0;
             uint32_t parity = 1;
             for (int tile = pair; ok; tile += pairs) {
@@ -564,16 +655,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 }
                 if (++ring.at == kRing) ring.at = 0, ring.parity ^= 1;
                 if (!more) break;
-                const int half = t.n / 2;
-                const int boxes = MODE == kWgrad ? (half + 63) / 64 : (half + kRowBox - 1) / kRowBox;
-                const uint32_t bytes = kOperandBytes + boxes * (MODE == kWgrad ? 64 : kRowBox) * 128;
+                // this block's token rows: half of the tile's, or (e4m3, rows as M) its 128 as far as
+                // there are any, to a multiple of 16
+                const int half = t.across ? t.n / 2 : max(0, min(128, (t.rows - rank * 128 + 15) & ~15));
+                const int boxes = MODE == kWgrad ? (half + 63) / 64 : half / kRowBox;
+                const uint32_t bytes = kOperandBytes + (MODE == kWgrad ? boxes * 64 : half) * 128;
                 // one thread runs the tile's steps, the warp rejoins for the next tile
                 if (elect_one()) {
-                    const int feat = t.feat0 + rank * (kHalf ? 64 : 128);
-                    const int row = t.row0 + rank * half;
+                    // this block's features, gated: 64 gate and (at feat2) 64 up, or all of one kind
+                    int feat = t.feat0 + rank * (kHalf ? 64 : 128), feat2 = feat + (kHalf ? p.N : 64);
+                    if (!t.across) {
+                        feat = t.feat0 + rank * (kHalf ? p.N : t.n / 2);
+                        feat2 = feat + 64;
+                    }
+                    const int row = t.row0 + rank * (t.across ? half : 128);
+                    // operand M first; a has the features, b the rows
+                    const uint32_t a_at = base + (t.across ? 0 : kOperandBytes);
+                    const uint32_t b_at = base + (t.across ? kOperandBytes : 0);
                     for (int k = 0; k < t.steps; ++k) {
                         if (!(ok = mbar_wait_pipe(empty + 8 * stage, parity))) break;
-                        const uint32_t a = base + stage * kStageBytes, b = a + kOperandBytes;
+                        const uint32_t a = a_at + stage * kStageBytes, b = b_at + stage * kStageBytes;
                         const uint32_t bar = lead_full + 8 * stage;
                         if (MODE == kWgrad) {
                             const int at = t.start + k * kStep, left = t.count - k * kStep;
@@ -585,7 +686,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                             } else {
                                 const int used = (left + 15) & ~15;
                                 mbar_arrive_tx_cluster(bar, (2 + boxes) * used * 128);
-                                constexpr int kMaps = Maps<MODE>::kCount;
+                                constexpr int kMaps = Maps<MODE>::kM;
                                 int r = 0;
 #pragma unroll 1
                                 for (int c = 0; c < 4; ++c) {
@@ -606,13 +707,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                             if (MODE == kDgrad) {
                                 tma_3d(a, &maps.m[0], feat, k * kStep, t.e, bar);
                                 tma_3d(a + 8192, &maps.m[0], feat + 64, k * kStep, t.e, bar);
-                            } else if (kHalf) {
-                                tma_4d(a, &maps.m[0], k * kStep, feat, 0, t.e, bar);
                             } else {
                                 tma_3d(a, &maps.m[0], k * kStep, feat, t.e, bar);
+                                tma_3d(a + 8192, &maps.m[0], k * kStep, feat2, t.e, bar);
                             }
                             for (int i = 0; i < boxes; ++i)
                                 tma_2d(b + i * kRowBox * 128, &maps.n[0], k * kStep, t.start + row + i * kRowBox, bar);
+                            if (half & 16)
+                                tma_2d(b + boxes * kRowBox * 128, &maps.n[Maps<MODE>::kN > 1], k * kStep,
+                                       t.start + row + boxes * kRowBox, bar);
                         }
                         if (++stage == kStages) stage = 0, parity ^= 1;
                     }
@@ -629,19 +732,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             }
         } else if (warp == kMmaWarp) {
             const uint64_t desc_a = smem_desc(base, 8192), desc_b = smem_desc(base + kOperandBytes, 8192);
-            int stage = 0, buf = 0;
-            uint32_t parity = 0, acc_parity = 1;
+            int stage = 0, acc = 0, was = -1;
+            uint32_t parity = 0, parities = (1u << kAccs) - 1;  // of each accumulator's next release
             while (rank == 0 && ring.next(ok)) {
                 const int steps = ring.tile().steps, n = ring.tile().n, left = ring.tile().count & 63;
+                const int across = ring.tile().across;
                 ring.drop();
                 if (steps == 0) continue;
                 const uint32_t desc = mma_desc<FP8, MODE != kForward, MODE == kWgrad>(n);
-                int st = stage, bf = buf;
-                uint32_t ph = parity, aph = acc_parity;
+                const int accs = FP8 && !across ? 2 : kAccs, columns = 512 / accs;
+                if (FP8) acc = 0;
+                int st = stage, c = acc;
+                uint32_t ph = parity, aph = parities;
                 if (elect_one()) {
-                    for (int k = 0; k < steps; ++k) {
+                    if (FP8 && across != was && was >= 0)  // other accumulators lie where these will
+                        for (int i = 0; ok && i < kAccs; ++i) ok = mbar_wait_pipe(acc_empty + 8 * i, (aph >> i) & 1);
+                    for (int k = 0; ok && k < steps; ++k) {
                         const bool fresh = FP8 || k == 0, last = FP8 || k == steps - 1;
-                        if (fresh && !(ok = mbar_wait_pipe(acc_empty + 8 * bf, aph))) break;
+                        if (fresh) {
+                            if (!(ok = mbar_wait_pipe(acc_empty + 8 * c, (aph >> c) & 1))) break;
+                            aph ^= 1u << c;
+                        }
                         if (!(ok = mbar_wait_pipe(full + 8 * st, ph))) break;
                         tcgen05_fence_after();
                         // a quarter of the stage's reduction: 32 bytes along a K-major row, or
@@ -649,16 +760,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                         constexpr uint64_t kA = MODE != kForward ? 128 : 2, kB = MODE == kWgrad ? 128 : 2;
                         const uint64_t da = desc_a + (uint32_t)(st * (kStageBytes >> 4));
                         const uint64_t db = desc_b + (uint32_t)(st * (kStageBytes >> 4));
-                        const uint32_t d = tmem + bf * kTileRows;
+                        const uint32_t d = tmem + c * columns;
                         const int quarters = MODE == kWgrad && left && k == steps - 1 ? (left + 15) / 16 : 4;
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
                             if (q < quarters) mma_pair<FP8>(d, da + q * kA, db + q * kB, desc, !(fresh && q == 0));
                         mma_commit_pair(empty + 8 * st);
                         if (last) {
-                            mma_commit_pair(acc_full + 8 * bf);
-                            bf ^= 1;
-                            if (bf == 0) aph ^= 1;
+                            mma_commit_pair(acc_full + 8 * c);
+                            if (++c == accs) c = 0;
                         }
                         if (++st == kStages) st = 0, ph ^= 1;
                     }
@@ -667,9 +777,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 stage += steps;
                 parity ^= (stage / kStages) & 1;
                 stage %= kStages;
-                buf += FP8 ? steps : 1;
-                acc_parity ^= (buf >> 1) & 1;
-                buf &= 1;
+                was = across;
+                // one flip for each use: whole rounds, then the accumulators up to the next
+                const int used = FP8 ? steps : 1;
+                if (used / accs & 1) parities ^= (1u << accs) - 1;
+                for (int i = 0; i < used % accs; ++i) {
+                    parities ^= 1u << acc;
+                    acc = (acc + 1) % accs;
+                }
             }
         } else if (FP8) {
             const int tid = threadIdx.x - kScaleWarp * 32;
@@ -680,46 +795,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             while (ok && ring.next(ok)) {
                 const Tile t = ring.tile();
                 ring.drop();
-                int b0 = (t.feat0 + rank * (kHalf ? 64 : 128)) / 128;
-                int b1 = kHalf ? b0 + p.N / 128 : b0;
-                if (b0 >= blocks) b0 = 0;  // a block past the features: nothing of it is kept
-                if (b1 >= blocks) b1 = 0;
+                // the tile's two weight blocks; across: this block's (gated: its gate's and its up's)
+                int b0 = (t.feat0 + (t.across ? rank * (kHalf ? 64 : 128) : 0)) / 128;
+                int b1 = kHalf ? b0 + p.N / 128 : b0 + (t.across ? 0 : 1);
+                if (b0 >= blocks) b0 = 0;  // features past the last: nothing of them is kept
+                if (b1 >= blocks) b1 = b0;
                 const float *w0 = p.w_scale + ((int64_t)t.e * blocks + b0) * C;
                 const float *w1 = p.w_scale + ((int64_t)t.e * blocks + b1) * C;
-                const float *xs = p.x_scale + ((int64_t)t.start + t.row0) * p.srow + t.e * p.sexp;
+                const int skip = t.across ? 0 : rank * 128, rows = t.rows - skip;
+                const float *xs = p.x_scale + ((int64_t)t.start + t.row0 + skip) * p.srow + t.e * p.sexp;
                 for (int g = 0; g < t.steps; g += kScaleGroup) {
-                    float sw[2][kScaleGroup], sx[kTileRows / 64][kScaleGroup];
+                    float sw[2][kScaleGroup], sx[2][kScaleGroup];
 #pragma unroll
                     for (int k = 0; k < kScaleGroup; ++k) {
                         sw[0][k] = g + k < C ? w0[g + k] : 0.0f;
-                        sw[1][k] = kHalf && g + k < C ? w1[g + k] : 0.0f;
+                        sw[1][k] = g + k < C ? w1[g + k] : 0.0f;
                     }
 #pragma unroll
-                    for (int i = 0; i < kTileRows / 64; ++i) {
+                    for (int i = 0; i < 2; ++i) {
                         const int c = i * 64 + tid;
-                        if (c < t.rows && p.scale_vec) {
+                        if (c < rows && p.scale_vec) {
                             const float4 v = *reinterpret_cast<const float4 *>(xs + c * p.srow + g);
                             sx[i][0] = v.x, sx[i][1] = v.y, sx[i][2] = v.z, sx[i][3] = v.w;
                         } else {
 #pragma unroll
                             for (int k = 0; k < kScaleGroup; ++k)
-                                sx[i][k] = c < t.rows && g + k < C ? xs[c * p.srow + (g + k) * p.scol] : 0.0f;
+                                sx[i][k] = c < rows && g + k < C ? xs[c * p.srow + (g + k) * p.scol] : 0.0f;
                         }
                     }
                     if (!(ok = mbar_wait_pipe(sc_empty + 8 * buf, parity))) break;
-                    float *dst = scales + buf * kScaleGroup * 2 * kTileRows;
+                    if (!t.across) {  // a row's two, side by side
+                        float2 *dst = reinterpret_cast<float2 *>(scales) + buf * kScaleGroup * 128 + tid;
 #pragma unroll
-                    for (int i = 0; i < kTileRows / 64; ++i) {
-                        const int c = i * 64 + tid;
-                        if (c < t.n) {
-                            // the eight columns of 32 that a lane's fragments hold, side by side
-                            const int to = (c & ~31) + 8 * (c & 3) + ((c >> 2) & 7);
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int k = 0; k < kScaleGroup; ++k)
+                                dst[k * 128 + i * 64] = make_float2(sx[i][k] * sw[0][k], sx[i][k] * sw[1][k]);
+                    } else {  // for each weight block, the eight rows of 32 that a lane's fragments hold
+                        float *dst = scales + buf * kScaleGroup * 256 + (tid & 32) + 8 * (tid & 3) + ((tid >> 2) & 7);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
 #pragma unroll
                             for (int k = 0; k < kScaleGroup; ++k) {
-                                dst[(k * 2) * kTileRows + to] = sx[i][k] * sw[0][k];
-                                if (kHalf) dst[(k * 2 + 1) * kTileRows + to] = sx[i][k] * sw[1][k];
+                                dst[k * 256 + i * 64] = sx[i][k] * sw[0][k];
+                                dst[k * 256 + 128 + i * 64] = sx[i][k] * sw[1][k];
                             }
-                        }
                     }
                     __syncwarp();
                     if (elect_one()) mbar_arrive_own(sc_full + 8 * buf);
@@ -731,77 +851,115 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
         }
     } else {
         if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-        constexpr int kShare = kEpiWarps / 4, kCols = kTileRows / 32 / kShare;  // warps, chunks of columns each
+        constexpr int kShare = kEpiWarps / 4;  // warps that share the columns of 32 lanes
         const int quadrant = warp & 3, share = warp >> 2;
         const uint32_t lead_empty = map_to_rank(acc_empty, 0);
         const uint32_t my_tmem = tmem + ((uint32_t)(quadrant * 32) << 16);
-        int buf = 0;
-        uint32_t parity = 0;
+        uint32_t parities = 0;  // of each accumulator's next result
         if (FP8) {
-            const float *my_scales = scales + 8 * (lane & 3) + (kHalf && quadrant >= 2 ? kTileRows : 0) + share * 32;
+            // A lane is a row; the warp's columns are share * 32 .. + 31 of each of the two weight
+            // blocks, 16 at a time.
+            const float2 *my_scales = reinterpret_cast<const float2 *>(scales) + quadrant * 32 + lane;
             int sbuf = 0;
             uint32_t sparity = 0;
             while (ok && ring.next(ok)) {
                 const int steps = ring.tile().steps;
-                const int own = (ring.tile().n / 32 - share + kShare - 1) / kShare;  // chunks of this warp, of kCols
-                Frag acc[kCols];
-#pragma unroll
-                for (int i = 0; i < kCols; ++i)
+                if (ring.tile().across) {
+                    // a lane is a feature, in fragments; the warp's columns are share * 32 .. + 31
+                    const bool own = share * 32 < ring.tile().n;
+                    const float4 *at = reinterpret_cast<const float4 *>(
+                        scales + (kHalf && quadrant >= 2 ? 128 : 0) + share * 32 + 8 * (lane & 3));
+                    Frag acc;
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) acc[i][h][r] = 0.0f;
+                        for (int r = 0; r < 16; ++r) acc[h][r] = 0.0f;
+                    for (int k = 0; k < steps; ++k) {
+                        const int u = k % kScaleGroup, c = k % kAccs;
+                        if (u == 0 && !(ok = mbar_wait_pipe(sc_full + 8 * sbuf, sparity))) break;
+                        if (!(ok = mbar_wait_pipe(acc_full + 8 * c, (parities >> c) & 1))) break;
+                        parities ^= 1u << c;
+                        tcgen05_fence_after();
+                        if (own) {
+                            const float4 lo = at[(sbuf * kScaleGroup + u) * 64], hi = at[(sbuf * kScaleGroup + u) * 64 + 1];
+                            const float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};  // columns 4c + lane % 4
+                            uint32_t v[2][16];
+                            tmem_ld_frag(v[0], my_tmem + c * 128 + share * 32);
+                            tmem_ld_frag(v[1], my_tmem + c * 128 + share * 32 + (16u << 16));
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int r = 0; r < 16; ++r)
+                                    acc[h][r] = fmaf(__uint_as_float(v[h][r]), f[r >> 1], acc[h][r]);
+                        }
+                        tcgen05_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(lead_empty + 8 * c);
+                        if (u == kScaleGroup - 1 || k == steps - 1) {
+                            if (lane == 0) mbar_arrive_own(sc_empty + 8 * sbuf);
+                            sbuf ^= 1;
+                            if (sbuf == 0) sparity ^= 1;
+                        }
+                    }
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    Output<MODE, GATED> out(p, staging, bar0 + 8 * kSwap, warp);
+                    out.begin(ring.tile(), rank, quadrant);
+                    if (own) {
+                        out.fetch(share * 32);
+                        out.finish(acc, share * 32, kTileRows);
+                    }
+                    ok = out.ok;
+                    ring.drop();
+                    continue;
+                }
+                const int blocks = ring.tile().rows - rank * 128 - quadrant * 32 > 0
+                                       ? (ring.tile().n - share * 32 + 127) / 128 : 0;  // with columns here
+                float acc[2][32];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 32; ++r) acc[h][r] = 0.0f;
                 for (int k = 0; k < steps; ++k) {
-                    const int kg = k % kScaleGroup;
-                    if (kg == 0 && !(ok = mbar_wait_pipe(sc_full + 8 * sbuf, sparity))) break;
-                    const float *sc = my_scales + (sbuf * kScaleGroup + kg) * 2 * kTileRows;
-                    if (!(ok = mbar_wait_pipe(acc_full + 8 * buf, parity))) break;
+                    const int u = k % kScaleGroup, c = k & 1;
+                    if (u == 0 && !(ok = mbar_wait_pipe(sc_full + 8 * sbuf, sparity))) break;
+                    const float2 sc = my_scales[(sbuf * kScaleGroup + u) * 128];
+                    if (!(ok = mbar_wait_pipe(acc_full + 8 * c, (parities >> c) & 1))) break;
+                    parities ^= 1u << c;
                     tcgen05_fence_after();
-                    const uint32_t from = my_tmem + buf * kTileRows + share * 32;
 #pragma unroll
-                    for (int i = 0; i < kCols; ++i) {
-                        if (i < own) {
-                            float4 w[2];  // scales of columns 4c + lane % 4
+                    for (int h = 0; h < 2; ++h) {
+                        if (h < blocks) {
+                            const float f = h ? sc.y : sc.x;
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
+                            for (int q = 0; q < 2; ++q) {
                                 uint32_t v[16];
-                                tmem_ld_frag(v, from + i * kShare * 32 + (h ? 16u << 16 : 0u));
-                                if (h == 0) {
-                                    w[0] = reinterpret_cast<const float4 *>(sc + i * kShare * 32)[0];
-                                    w[1] = reinterpret_cast<const float4 *>(sc + i * kShare * 32)[1];
-                                }
+                                tmem_ld16(v, my_tmem + c * kTileRows + h * 128 + share * 32 + q * 16);
                                 tmem_wait_ld();
-                                const float f[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+                                const uint64_t ff = twice(f);
 #pragma unroll
                                 for (int r = 0; r < 16; r += 2)
-                                    fma2(acc[i][h][r], acc[i][h][r + 1], v[r], v[r + 1], f[r >> 1]);
+                                    fma2(acc[h][q * 16 + r], acc[h][q * 16 + r + 1], v[r], v[r + 1], ff);
                             }
                         }
                     }
                     tcgen05_fence_before();
                     __syncwarp();
-                    if (elect_one()) mbar_arrive_cluster(lead_empty + 8 * buf);
-                    buf ^= 1;
-                    if (buf == 0) parity ^= 1;
-                    if (kg == kScaleGroup - 1 || k == steps - 1) {
-                        __syncwarp();
-                        if (elect_one()) mbar_arrive_own(sc_empty + 8 * sbuf);
+                    if (lane == 0) mbar_arrive_cluster(lead_empty + 8 * c);
+                    if (u == kScaleGroup - 1 || k == steps - 1) {
+                        if (lane == 0) mbar_arrive_own(sc_empty + 8 * sbuf);
                         sbuf ^= 1;
                         if (sbuf == 0) sparity ^= 1;
                     }
                 }
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                Output<MODE, GATED> out(p, staging, bar0 + 8 * kSwap, warp);
-                out.begin(ring.tile(), rank, quadrant);
-                if (own > 0) out.fetch(share * 32);
-#pragma unroll
-                for (int i = 0; i < kCols; ++i)
-                    if (i < own) out.finish(acc[i], (i * kShare + share) * 32, ((i + 1) * kShare + share) * 32);
-                ok = out.ok;
+                if (blocks > 0) finish_rows<GATED>(p, ring.tile(), rank * 128 + quadrant * 32, share * 32,
+                                                   staging + warp * kStagingBytes, acc);
                 ring.drop();
             }
         } else {
             Output<MODE, GATED> out(p, staging, bar0 + 8 * kSwap, warp);
+            int buf = 0;
             while (ok && ring.next(ok)) {
                 const Tile &t = ring.tile();
                 out.begin(t, rank, quadrant);
@@ -810,7 +968,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 ring.drop();
                 if (share < chunks) out.fetch(share * 32);
                 if (any) {
-                    if (!(ok = mbar_wait_pipe(acc_full + 8 * buf, parity))) break;
+                    if (!(ok = mbar_wait_pipe(acc_full + 8 * buf, (parities >> buf) & 1))) break;
+                    parities ^= 1u << buf;
                     tcgen05_fence_after();
                 }
                 for (int ch = share; ch < chunks; ch += kShare) {
@@ -837,7 +996,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     __syncwarp();
                     if (elect_one()) mbar_arrive_cluster(lead_empty + 8 * buf);
                     buf ^= 1;
-                    if (buf == 0) parity ^= 1;
                 }
                 ok = __all_sync(0xffffffffu, out.ok);
             }
@@ -965,11 +1123,9 @@ epd_status_t launch(const Maps<MODE> &maps, const ExpertArgs &p, cudaStream_t st
     }();
     const int features = MODE == kForward ? p.N : p.K;
     const int64_t feat_tiles = (features + (GATED && MODE == kForward ? 127 : 255)) / (GATED && MODE == kForward ? 128 : 256);
-    const int64_t row_tiles = MODE == kWgrad
-                                  ? (int64_t)(p.N + kTileRows - 1) / kTileRows * p.rows.num_experts
-                                  : p.rows.capacity_rows / kTileRows + (p.rows.num_experts < p.rows.capacity_rows
-                                                                            ? p.rows.num_experts
-                                                                            : p.rows.capacity_rows);
+    const int64_t cap = p.rows.capacity_rows, E = p.rows.num_experts;
+    const int64_t row_tiles =
+        MODE == kWgrad ? (int64_t)(p.N + kTileRows - 1) / kTileRows * E : cap / kTileRows + (E < cap ? E : cap);
     const int64_t most = feat_tiles * row_tiles;
     if (most > INT32_MAX / 2) return EPD_ERR_UNSUPPORTED;
     return launch_pdl(kernel, 2 * (int)(most < pairs ? most : pairs), kThreadsOf<FP8>, kSmem, stream, maps, p);
@@ -1032,21 +1188,15 @@ extern "C" epd_status_t ep_expert_matmul(const epd_expert_rows_t *rows, const vo
     p.scale_vec = fp8 && scale_col_stride == 1 && K % 512 == 0 && scale_row_stride % 4 == 0 &&
                   scale_expert_stride % 4 == 0 && aligned16(x_scale);
     Maps<kForward> maps;
-    bool done = encode_rows(&maps.n[0], fp8, x, rows->capacity_rows, K, kRowBox);
+    bool done = encode_rows(&maps.n[0], fp8, x, rows->capacity_rows, K, kRowBox) &&
+                encode_rows(&maps.n[1], fp8, x, rows->capacity_rows, K, kRowBox / 2);
     const cuuint32_t wide = fp8 ? 128 : 64;
     const cuuint64_t E = (cuuint64_t)rows->num_experts;
-    if (gated) {
-        // 64 gate rows, then the same features' 64 up rows
-        const cuuint64_t size[4] = {(cuuint64_t)K, (cuuint64_t)N, 2, E};
-        const int64_t stride[3] = {K, (int64_t)N * K, 2 * (int64_t)N * K};
-        const cuuint32_t box[4] = {wide, 64, 2, 1};
-        done = done && encode(&maps.m[0], fp8, 4, w, size, stride, box);
-    } else {
-        const cuuint64_t size[3] = {(cuuint64_t)K, (cuuint64_t)N, E};
-        const int64_t stride[2] = {K, (int64_t)N * K};
-        const cuuint32_t box[3] = {wide, 128, 1};
-        done = done && encode(&maps.m[0], fp8, 3, w, size, stride, box);
-    }
+    const int64_t NW = gated ? 2 * (int64_t)N : N;
+    const cuuint64_t size[3] = {(cuuint64_t)K, (cuuint64_t)NW, E};
+    const int64_t stride[2] = {K, NW * K};
+    const cuuint32_t box[3] = {wide, 64, 1};
+    done = done && encode(&maps.m[0], fp8, 3, w, size, stride, box);
     if (!done) return EPD_ERR_CUDA;
     if (fp8)
         return gated ? launch<kForward, true, true>(maps, p, st) : launch<kForward, true, false>(maps, p, st);
@@ -1080,6 +1230,7 @@ extern "C" epd_status_t ep_expert_matmul_dgrad(const epd_expert_rows_t *rows, co
     const int64_t stride[2] = {K, (int64_t)N * K};
     const cuuint32_t box[3] = {64, 64, 1};
     if (!encode_rows(&maps.n[0], false, dy, rows->capacity_rows, N, kRowBox) ||
+        !encode_rows(&maps.n[1], false, dy, rows->capacity_rows, N, kRowBox / 2) ||
         !encode(&maps.m[0], false, 3, w, size, stride, box))
         return EPD_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
