@@ -51,7 +51,6 @@ constexpr int kTileRows = 256;                  // most token rows (wgrad: outpu
 constexpr int kAcrossRows = 128;                // e4m3: most rows of a tile with the features as M
 constexpr int kOperandBytes = 128 * 128;        // 128 rows of 128 bytes: one operand of a stage
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kRowBox = 32;                     // token rows per TMA box
 constexpr int kStagingBytes = 32 * 80;          // per epilogue warp: 32 rows of 64 bytes, 80 apart
 constexpr int kTailBytes = 768;                 // published tiles and barriers
 constexpr int kScaleGroup = 4;                  // reduction steps per group of staged scales
@@ -104,11 +103,12 @@ __device__ __forceinline__ void expert_region(const epd_expert_rows_t &r, int e,
 // height (64 experts of 380 rows: 340 us with heights that are powers of two, which take
 // five cuts where these take three).
 constexpr int cut_rows(int i) { return i < 3 ? 64 >> i : i - 2; }
-// Token rows (forward, dgrad) come in boxes of 32 and, half a tile being a multiple of 16, one of
-// 16: a box more than needed is bandwidth into the SM lost.
+// Token rows (forward, dgrad), a multiple of 16 up to 128, come in boxes of 128, 64, 32 and 16:
+// few boxes, and no row that is not needed. The forward weights' maps are one of 128 rows and,
+// gated, one of 64 gate rows and the same features' 64 up rows.
 template <int MODE>
 struct Maps {
-    static constexpr int kM = MODE == kWgrad ? kCuts : 1, kN = MODE == kWgrad ? kCuts : 2;
+    static constexpr int kM = MODE == kWgrad ? kCuts : MODE == kForward ? 2 : 1, kN = MODE == kWgrad ? kCuts : 4;
     CUtensorMap m[kM], n[kN];
 };
 
@@ -658,16 +658,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 // this block's token rows: half of the tile's, or (e4m3, rows as M) its 128 as far as
                 // there are any, to a multiple of 16
                 const int half = t.across ? t.n / 2 : max(0, min(128, (t.rows - rank * 128 + 15) & ~15));
-                const int boxes = MODE == kWgrad ? (half + 63) / 64 : half / kRowBox;
+                const int boxes = (half + 63) / 64;  // wgrad
                 const uint32_t bytes = kOperandBytes + (MODE == kWgrad ? boxes * 64 : half) * 128;
                 // one thread runs the tile's steps, the warp rejoins for the next tile
                 if (elect_one()) {
-                    // this block's features, gated: 64 gate and (at feat2) 64 up, or all of one kind
-                    int feat = t.feat0 + rank * (kHalf ? 64 : 128), feat2 = feat + (kHalf ? p.N : 64);
-                    if (!t.across) {
-                        feat = t.feat0 + rank * (kHalf ? p.N : t.n / 2);
-                        feat2 = feat + 64;
-                    }
+                    // this block's features: gated, 64 and their up, or all 128 of one kind
+                    const int feat = t.feat0 + rank * (!t.across ? (kHalf ? p.N : t.n / 2) : kHalf ? 64 : 128);
                     const int row = t.row0 + rank * (t.across ? half : 128);
                     // operand M first; a has the features, b the rows
                     const uint32_t a_at = base + (t.across ? 0 : kOperandBytes);
@@ -707,15 +703,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                             if (MODE == kDgrad) {
                                 tma_3d(a, &maps.m[0], feat, k * kStep, t.e, bar);
                                 tma_3d(a + 8192, &maps.m[0], feat + 64, k * kStep, t.e, bar);
+                            } else if (kHalf && t.across) {
+                                tma_4d(a, &maps.m[0], k * kStep, feat, 0, t.e, bar);
                             } else {
-                                tma_3d(a, &maps.m[0], k * kStep, feat, t.e, bar);
-                                tma_3d(a + 8192, &maps.m[0], k * kStep, feat2, t.e, bar);
+                                tma_3d(a, &maps.m[Maps<MODE>::kM > 1], k * kStep, feat, t.e, bar);
                             }
-                            for (int i = 0; i < boxes; ++i)
-                                tma_2d(b + i * kRowBox * 128, &maps.n[0], k * kStep, t.start + row + i * kRowBox, bar);
-                            if (half & 16)
-                                tma_2d(b + boxes * kRowBox * 128, &maps.n[Maps<MODE>::kN > 1], k * kStep,
-                                       t.start + row + boxes * kRowBox, bar);
+                            int r = 0;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (!(half & (128 >> i))) continue;
+                                tma_2d(b + r * 128, &maps.n[i], k * kStep, t.start + row + r, bar);
+                                r += 128 >> i;
+                            }
                         }
                         if (++stage == kStages) stage = 0, parity ^= 1;
                     }
@@ -1188,15 +1187,23 @@ extern "C" epd_status_t ep_expert_matmul(const epd_expert_rows_t *rows, const vo
     p.scale_vec = fp8 && scale_col_stride == 1 && K % 512 == 0 && scale_row_stride % 4 == 0 &&
                   scale_expert_stride % 4 == 0 && aligned16(x_scale);
     Maps<kForward> maps;
-    bool done = encode_rows(&maps.n[0], fp8, x, rows->capacity_rows, K, kRowBox) &&
-                encode_rows(&maps.n[1], fp8, x, rows->capacity_rows, K, kRowBox / 2);
+    bool done = true;
+    for (int i = 0; i < 4; ++i) done = done && encode_rows(&maps.n[i], fp8, x, rows->capacity_rows, K, 128 >> i);
     const cuuint32_t wide = fp8 ? 128 : 64;
     const cuuint64_t E = (cuuint64_t)rows->num_experts;
     const int64_t NW = gated ? 2 * (int64_t)N : N;
     const cuuint64_t size[3] = {(cuuint64_t)K, (cuuint64_t)NW, E};
     const int64_t stride[2] = {K, NW * K};
-    const cuuint32_t box[3] = {wide, 64, 1};
-    done = done && encode(&maps.m[0], fp8, 3, w, size, stride, box);
+    const cuuint32_t box[3] = {wide, 128, 1};
+    done = done && encode(&maps.m[1], fp8, 3, w, size, stride, box);
+    if (gated) {
+        const cuuint64_t size2[4] = {(cuuint64_t)K, (cuuint64_t)N, 2, E};
+        const int64_t stride2[3] = {K, (int64_t)N * K, NW * K};
+        const cuuint32_t box2[4] = {wide, 64, 2, 1};
+        done = done && encode(&maps.m[0], fp8, 4, w, size2, stride2, box2);
+    } else {
+        maps.m[0] = maps.m[1];  // not used
+    }
     if (!done) return EPD_ERR_CUDA;
     if (fp8)
         return gated ? launch<kForward, true, true>(maps, p, st) : launch<kForward, true, false>(maps, p, st);
@@ -1229,10 +1236,9 @@ extern "C" epd_status_t ep_expert_matmul_dgrad(const epd_expert_rows_t *rows, co
     const cuuint64_t size[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)rows->num_experts};
     const int64_t stride[2] = {K, (int64_t)N * K};
     const cuuint32_t box[3] = {64, 64, 1};
-    if (!encode_rows(&maps.n[0], false, dy, rows->capacity_rows, N, kRowBox) ||
-        !encode_rows(&maps.n[1], false, dy, rows->capacity_rows, N, kRowBox / 2) ||
-        !encode(&maps.m[0], false, 3, w, size, stride, box))
-        return EPD_ERR_CUDA;
+    bool done = encode(&maps.m[0], false, 3, w, size, stride, box);
+    for (int i = 0; i < 4; ++i) done = done && encode_rows(&maps.n[i], false, dy, rows->capacity_rows, N, 128 >> i);
+    if (!done) return EPD_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     return activation == EPD_ACT_SWIGLU ? launch<kDgrad, false, true>(maps, p, st)
                                         : launch<kDgrad, false, false>(maps, p, st);
