@@ -131,7 +131,7 @@ def version() -> int:
 
 
 def _check(rc: int, where: str):
-    if rc != EPD_OK:
+    if rc:
         raise EpdError(rc, where)
 
 
@@ -148,10 +148,13 @@ def _stream(stream, device) -> int:
 
 
 def _want(t, name, dtype, shape=None, device=None):
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and (shape is None or t.shape == shape)
-            and (t.is_cuda if device is None else t.device == device and t.is_cuda)
-            and t.is_contiguous()):
-        return t
+    # the common case, in few attribute look-ups; what fails it is told apart below
+    try:
+        if (t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous()
+                and (t.is_cuda if device is None else t.get_device() == device.index >= 0)):
+            return t
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -581,12 +584,13 @@ def _choose(table, key, name):
 
 
 def _logits(t):
-    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.float32, torch.bfloat16):
+    dtype = t.dtype if isinstance(t, torch.Tensor) else None
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
         raise ValueError("logits must be a float32 or bfloat16 tensor")
-    _want(t, "logits", t.dtype)
+    _want(t, "logits", dtype)
     if t.dim() != 2:
         raise ValueError("logits must be [num_tokens, num_experts]")
-    return EPD_F32 if t.dtype == torch.float32 else EPD_BF16
+    return EPD_F32 if dtype is torch.float32 else EPD_BF16
 
 
 def ep_route(logits: torch.Tensor, num_topk: int, status: torch.Tensor, scoring: str = "softmax",
