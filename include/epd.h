@@ -434,7 +434,9 @@ EPD_API epd_status_t ep_route(const void *logits, epd_dtype_t dtype, const float
  *   grad_logits = ds * s * (1 - s)                                (sigmoid)
  *               = s * (ds - sum over e of ds_e s_e)               (softmax).
  * Picks of -1 have no gradient; an id outside [-1, E) sets EPD_ERR_INVALID_EXPERT and
- * counts as -1. Every element of grad_logits [T, E] (the logits' type) is written, 0
+ * counts as -1; a pick whose logit is NaN or +inf sets EPD_ERR_NONFINITE and has score 0.
+ * Renormalised softmax weights are the softmax of the picks' logits alone, and are computed
+ * as that, here and in ep_route. Every element of grad_logits [T, E] (the logits' type) is written, 0
  * for an expert that cannot be chosen. An expert that a row picks twice gets both
  * picks' terms.
  */
@@ -454,7 +456,9 @@ EPD_API epd_status_t ep_route_backward(const float *grad_weights, const void *lo
  * (rectangles). The counts and starts are device memory, read by the kernel: nothing goes
  * back to the host. Regions must not overlap. A negative count or start sets
  * EPD_ERR_INVALID_ARG in *status and counts as no rows; a region that does not end within
- * capacity_rows (or within its rectangle) sets EPD_ERR_CAPACITY and is cut there.
+ * capacity_rows (or within its rectangle) sets EPD_ERR_CAPACITY and is cut there. The
+ * products' kernels wait for their own copies and matrix instructions only; each wait is
+ * bounded (two seconds) and running out sets EPD_ERR_TIMEOUT.
  */
 typedef struct {
     int num_experts;
@@ -520,8 +524,9 @@ EPD_API epd_status_t ep_expert_matmul_dgrad(const epd_expert_rows_t *rows, const
  * Gradients of the weights and the bias: for every expert e
  *   dw[e] = sum over its rows s of dy[s, :]^T x[s, :]   (fp32, rounded once to bfloat16)
  *   dbias[e] = sum over its rows s of dy[s, :]          (float32; NULL to leave it out)
- * in an order that depends on the row numbers alone; 0 for an expert without rows. Rows outside the experts' regions
- * are not used, whatever they hold.
+ * in an order that depends on the row numbers alone; 0 for an expert without rows. Rows
+ * outside the experts' regions are not used, whatever they hold. With dbias the call enqueues
+ * two kernels, which run side by side.
  *   dy: [capacity_rows, N], x: [capacity_rows, K], dw: [E, N, K] bfloat16, 16-byte aligned;
  *   dbias: [E, N] float32; N % 8 == 0, K % 8 == 0.
  */

@@ -17,21 +17,34 @@
 // rows per step of the reduction (128 bytes wide), so a token row that both blocks multiply is
 // staged once.
 //
-// e4m3 (forward only) is the other way round, D[256 rows x n features]. Rows are scaled per 128
-// columns and weights per 128 x 128, so the product of one 128-wide step cannot stay in the
-// tensor core's accumulator: every step's D goes to registers as acc += D * (x_scale *
-// w_scale). With a row a lane that is one scale a thread and weight block; with a column a row
-// every thread needs all columns' scales from shared memory, whose bandwidth the operands
-// already take whole (each step is written once and read once: 64 KiB in the 512 cycles of its
-// mma), and a step took 867 to 1120 cycles.
+// e4m3 (forward only) is scaled per row and 128 columns and, the weights, per 128 x 128, so the
+// product of one 128-wide step cannot stay in the tensor core's accumulator: every step's D goes
+// to registers as acc += D * (x_scale * w_scale). Tiles of more than 128 rows have the rows as
+// M, D[256 rows x n features]: a lane is a row and needs one scale for each of the tile's two
+// weight blocks. With a row a column every thread needs all the columns' scales from shared
+// memory, whose bandwidth the operands already take (a step's 32 KiB are written and read once
+// in the 512 cycles of its mma): 256 experts of 256 rows, 4096 x 7168, took 1733 us that way and
+// take 1480 us this way. Tiles of up to 128 rows are turned across all the same, D[256 features
+// x n rows], where a step costs little more than its weights' 16 KiB into the SM: with 4 rows an
+// expert 1329 us the one way and 1100 us the other.
+//
+// What bounds it: bf16 the tensor cores from some 500 rows an expert on (dense 8192^3: 570 us,
+// 1930 TFLOP/s, as cuBLAS here) and with fewer the 64 bytes a clock that come into an SM, since
+// a step of n = 192 columns brings 28 KiB for 384 cycles of mma; wgrad its output, 4.0 TB/s
+// being what this memory takes in writes alone; e4m3 with few rows the weights' way from memory
+// and with many the sums, of which a step has 256 cycles to its mma's 512.
 //
 // Warps: the epilogue's 8 (e4m3: 16), the producer, which walks the tiles, publishes them to
 // the others and feeds TMA, one that issues the mma (in the pair's first block), and for e4m3
-// two that load row scales. Accumulators are double-buffered in tensor memory, so a tile's
-// epilogue runs under the next tile's mma. Blocks walk the tiles of all experts in a fixed
-// order (persistent, one pair per two SMs); the experts' counts are read from device memory,
-// 32 at a time, by the producer itself.
+// two that load row scales. There are two accumulators in tensor memory (e4m3 across: four), so
+// a tile's epilogue, or a step's sums, run under the next one's mma. One thread issues a tile's
+// loads and one its mma without leaving its loop: with a branch to lane 0 in every step the
+// issue alone took 530 cycles a step. Blocks walk the tiles of all experts in a fixed order
+// (persistent, one pair per two SMs); the experts' counts are read from device memory, 32 at a
+// time, by the producer itself.
 #include <cuda.h>
+
+#include <atomic>
 
 #include "epd_math.cuh"
 #include "epd_tcgen05.cuh"
@@ -41,7 +54,9 @@ namespace {
 
 enum { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
-// e4m3 has its sums in registers: 16 epilogue warps of 64 columns each.
+// e4m3 has its sums in registers: 16 epilogue warps of 64 columns each, 16 read at a time. (Eight
+// warps of 128 columns: 1795 us at the shape above. 32 columns at a time, or 16 with the next 16
+// read ahead, spill: 1915 and 3843 us.)
 template <bool FP8>
 constexpr int kEpiWarpsOf = FP8 ? 16 : 8;
 constexpr int kScaleWarps = 2;
@@ -103,6 +118,7 @@ __device__ __forceinline__ void expert_region(const epd_expert_rows_t &r, int e,
 // height (64 experts of 380 rows: 340 us with heights that are powers of two, which take
 // five cuts where these take three).
 constexpr int cut_rows(int i) { return i < 3 ? 64 >> i : i - 2; }
+
 // Token rows (forward, dgrad), a multiple of 16 up to 128, come in boxes of 128, 64, 32 and 16:
 // few boxes, and no row that is not needed. The forward weights' maps are one of 128 rows and,
 // gated, one of 64 gate rows and the same features' 64 up rows.
@@ -727,8 +743,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                 stage = __shfl_sync(0xffffffffu, issued % kStages, 0);
                 parity = 1 ^ ((issued / kStages) & 1);
             }
-            // the last stages' releases arrive before this block may go
-            for (int i = 0; ok && i < min(issued, kStages); ++i) {
+            // every stage's last release arrives before this block may go (a stage that was never
+            // used counts as released)
+            for (int i = 0; ok && i < kStages; ++i) {
                 ok = mbar_wait_pipe(empty + 8 * stage, parity);
                 if (++stage == kStages) stage = 0, parity ^= 1;
             }
@@ -1106,8 +1123,14 @@ template <int MODE, bool FP8, bool GATED>
 epd_status_t launch(const Maps<MODE> &maps, const ExpertArgs &p, cudaStream_t stream) {
     constexpr int kSmem = kSmemOf<FP8>;
     auto kernel = expert_kernel<MODE, FP8, GATED>;
-    static const int pairs = [&] {
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    static std::atomic<int> cached[64];  // resident pairs of blocks, per device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return record_cuda_error();
+    std::atomic<int> &slot = cached[dev >= 0 && dev < 64 ? dev : 0];
+    int pairs = slot.load(std::memory_order_relaxed);
+    if (pairs == 0 || dev >= 64) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+            return record_cuda_error();
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(sm_count() / 2 * 2));
         cfg.blockDim = dim3(kThreadsOf<FP8>);
@@ -1118,11 +1141,12 @@ epd_status_t launch(const Maps<MODE> &maps, const ExpertArgs &p, cudaStream_t st
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        int found = 0;
-        if (cudaOccupancyMaxActiveClusters(&found, kernel, &cfg) != cudaSuccess) found = 0;
-        cudaGetLastError();
-        return found < 1 ? 1 : found;
-    }();
+        if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess || pairs < 1) {
+            cudaGetLastError();
+            pairs = 1;
+        }
+        slot.store(pairs, std::memory_order_relaxed);
+    }
     const int features = MODE == kForward ? p.N : p.K;
     const int64_t feat_tiles = (features + (GATED && MODE == kForward ? 127 : 255)) / (GATED && MODE == kForward ? 128 : 256);
     const int64_t cap = p.rows.capacity_rows, E = p.rows.num_experts;
