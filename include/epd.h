@@ -525,8 +525,7 @@ EPD_API epd_status_t ep_expert_matmul_dgrad(const epd_expert_rows_t *rows, const
  *   dw[e] = sum over its rows s of dy[s, :]^T x[s, :]   (fp32, rounded once to bfloat16)
  *   dbias[e] = sum over its rows s of dy[s, :]          (float32; NULL to leave it out)
  * in an order that depends on the row numbers alone; 0 for an expert without rows. Rows
- * outside the experts' regions are not used, whatever they hold. With dbias the call enqueues
- * two kernels, which run side by side.
+ * outside the experts' regions are not used, whatever they hold.
  *   dy: [capacity_rows, N], x: [capacity_rows, K], dw: [E, N, K] bfloat16, 16-byte aligned;
  *   dbias: [E, N] float32; N % 8 == 0, K % 8 == 0.
  */

@@ -35,8 +35,8 @@
 // and with many the sums, of which a step has 256 cycles to its mma's 512.
 //
 // Warps: the epilogue's 8 (e4m3: 16), the producer, which walks the tiles, publishes them to
-// the others and feeds TMA, one that issues the mma (in the pair's first block), and for e4m3
-// two that load row scales. There are two accumulators in tensor memory (e4m3 across: four), so
+// the others and feeds TMA, one that issues the mma (in the pair's first block), and two helpers
+// that load row scales (e4m3) or sum the bias's gradient (wgrad). There are two accumulators in tensor memory (e4m3 across: four), so
 // a tile's epilogue, or a step's sums, run under the next one's mma. One thread issues a tile's
 // loads and one its mma without leaving its loop: with a branch to lane 0 in every step the
 // issue alone took 530 cycles a step. Blocks walk the tiles of all experts in a fixed order
@@ -59,9 +59,9 @@ enum { kForward = 0, kDgrad = 1, kWgrad = 2 };
 // read ahead, spill: 1915 and 3843 us.)
 template <bool FP8>
 constexpr int kEpiWarpsOf = FP8 ? 16 : 8;
-constexpr int kScaleWarps = 2;
-template <bool FP8>
-constexpr int kThreadsOf = (kEpiWarpsOf<FP8> + 2 + (FP8 ? kScaleWarps : 0)) * 32;
+constexpr int kHelpers = 2;                     // warps that load row scales (e4m3) or sum dbias (wgrad)
+template <int MODE, bool FP8>
+constexpr int kThreadsOf = (kEpiWarpsOf<FP8> + 2 + (FP8 || MODE == kWgrad ? kHelpers : 0)) * 32;
 constexpr int kTileRows = 256;                  // most token rows (wgrad: output rows) of a tile
 constexpr int kAcrossRows = 128;                // e4m3: most rows of a tile with the features as M
 constexpr int kOperandBytes = 128 * 128;        // 128 rows of 128 bytes: one operand of a stage
@@ -90,6 +90,8 @@ struct ExpertArgs {
     const float *bias;
     const uint8_t *residual, *preact_in;
     uint8_t *y, *preact;
+    const uint8_t *dy;  // wgrad: the rows that dbias sums
+    float *dbias;
     int32_t *status;
 };
 
@@ -590,15 +592,57 @@ __device__ __forceinline__ void finish_rows(const ExpertArgs &p, const Tile &t, 
     }
 }
 
+// dbias[e, n] = the sum of the expert's rows of dy: a warp takes 64 columns of an expert, a lane
+// eight of them in every fourth row, and the four parts are added up, all in a fixed order. The
+// helper warps of wgrad do it beside the products, straight from memory: +12 us at 64 experts of
+// 384 rows, 4096 columns, where a kernel of its own after the product took 37.
+__device__ __forceinline__ void sum_bias(const ExpertArgs &p, int worker, int workers) {
+    constexpr int kRows = 16;  // in flight a lane
+    const int lane = threadIdx.x & 31, part = lane >> 3;
+    const int groups = (p.N + 63) / 64;
+    const int64_t pitch = (int64_t)p.N * 2;
+    for (int64_t item = worker; item < (int64_t)groups * p.rows.num_experts; item += workers) {
+        const int e = (int)(item / groups), n = (int)(item - (int64_t)e * groups) * 64 + (lane & 7) * 8;
+        int start, count;
+        expert_region(p.rows, e, start, count, p.status);
+        float sum[8] = {};
+        const uint8_t *at = p.dy + ((int64_t)start * p.N + n) * 2;
+        for (int r = part; n < p.N && r < count; r += 4 * kRows) {
+            uint4 v[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+                v[i] = r + 4 * i < count ? ld_stream16(at + (r + 4 * i) * pitch) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                float f[8];
+                unpack8_bf16(v[i], f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) sum[j] += f[j];
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 8);
+            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 16);
+        }
+        if (part == 0 && n < p.N) {
+            float *out = p.dbias + (int64_t)e * p.N + n;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) out[j] = sum[j];
+        }
+    }
+}
+
 template <int MODE, bool FP8, bool GATED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
     expert_kernel(const __grid_constant__ Maps<MODE> maps, const ExpertArgs p) {
     constexpr bool kHalf = GATED && MODE == kForward;  // half of a block's 128 lanes are up features
     constexpr int kStages = kStagesOf<FP8>;
     // accumulators: two of 256 columns; e4m3, which uses one a step, four of 128 where that is enough
     constexpr int kAccs = FP8 ? 4 : 2;
     constexpr int kEpiWarps = kEpiWarpsOf<FP8>;
-    constexpr int kProducerWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kScaleWarp = kEpiWarps + 2;
+    constexpr int kProducerWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kHelperWarp = kEpiWarps + 2;
     constexpr int kStep = FP8 ? 128 : 64;              // reduction elements per stage
     constexpr int kFeatStep = kHalf ? 128 : 256;       // output features per pair
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -630,12 +674,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
             mbar_init(bars + kAccEmpty + i, 2 * kEpiWarps);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bars + kScFull + i, kScaleWarps);
+            mbar_init(bars + kScFull + i, kHelpers);
             mbar_init(bars + kScEmpty + i, kEpiWarps);
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(bars + kTileFull + i, 1);
-            mbar_init(bars + kTileEmpty + i, kEpiWarps + (rank == 0) + (FP8 ? kScaleWarps : 0));
+            mbar_init(bars + kTileEmpty + i, kEpiWarps + (rank == 0) + (FP8 ? kHelpers : 0));
         }
         for (int i = 0; i < kEpiWarps / 2; ++i) mbar_init(bars + kSwap + i, 64);
         mbar_init_fence();
@@ -805,8 +849,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
                     acc = (acc + 1) % accs;
                 }
             }
+        } else if (MODE == kWgrad) {
+            if (p.dbias) sum_bias(p, blockIdx.x * kHelpers + warp - kHelperWarp, gridDim.x * kHelpers);
         } else if (FP8) {
-            const int tid = threadIdx.x - kScaleWarp * 32;
+            const int tid = threadIdx.x - kHelperWarp * 32;
             const int C = p.K / 128;
             const int64_t blocks = ((GATED ? 2 * p.N : p.N) + 127) / 128;
             int buf = 0;
@@ -1030,55 +1076,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<FP8>, 1)
     if (warp == kMmaWarp) tmem_free_pair(tmem, 512);
 }
 
-// dbias[e, n] = the sum of the expert's rows of dy, in a fixed order: a thread sums every 32nd
-// row for eight columns, then the 32 parts are added up. It runs beside the wgrad kernel before
-// it on the stream (a block per SM fits next to that kernel's), which is why it waits for that
-// kernel last: it reads nothing that kernel writes, and cannot start before every block of it has
-// passed its own wait for what came earlier. The wait comes before this kernel ends, so whatever
-// follows on the stream still finds both done.
-constexpr int kBiasThreads = 256, kBiasRows = 8;
-__global__ void __launch_bounds__(kBiasThreads, 1) bias_grad_kernel(const epd_expert_rows_t rows, const uint8_t *dy,
-                                                                    int N, float *dbias, int32_t *status) {
-    __shared__ float s_sum[kBiasThreads / 8][64];
-    const int oct = threadIdx.x & 7, part = threadIdx.x >> 3;
-    const int groups = (N + 63) / 64;
-    for (int item = blockIdx.x; item < groups * rows.num_experts; item += gridDim.x) {
-        const int e = item / groups, n = (item - e * groups) * 64 + oct * 8;
-        int start, count;
-        expert_region(rows, e, start, count, status);
-        float sum[8] = {};
-        if (n < N) {
-            const uint8_t *at = dy + ((int64_t)start * N + n) * 2;
-            const int64_t pitch = (int64_t)N * 2;
-            for (int r = part; r < count; r += kBiasRows * 32) {
-                uint4 v[kBiasRows];
-#pragma unroll
-                for (int i = 0; i < kBiasRows; ++i)
-                    v[i] = r + i * 32 < count ? ld_stream16(at + (r + i * 32) * pitch) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < kBiasRows; ++i) {
-                    float f[8];
-                    unpack8_bf16(v[i], f);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sum[j] += f[j];
-                }
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s_sum[part][oct * 8 + i] = sum[i];
-        __syncthreads();
-        if (threadIdx.x < 64 && n - oct * 8 + (int)threadIdx.x < N) {
-            float v = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kBiasThreads / 8; ++i) v += s_sum[i][threadIdx.x];
-            dbias[(int64_t)e * N + n - oct * 8 + threadIdx.x] = v;
-        }
-    }
-    pdl_wait();
-    pdl_trigger();
-}
-
 // ---------------------------------------------------------------------------- host
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -1133,7 +1130,7 @@ epd_status_t launch(const Maps<MODE> &maps, const ExpertArgs &p, cudaStream_t st
             return record_cuda_error();
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(sm_count() / 2 * 2));
-        cfg.blockDim = dim3(kThreadsOf<FP8>);
+        cfg.blockDim = dim3(kThreadsOf<MODE, FP8>);
         cfg.dynamicSmemBytes = kSmem;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1154,7 +1151,7 @@ epd_status_t launch(const Maps<MODE> &maps, const ExpertArgs &p, cudaStream_t st
         MODE == kWgrad ? (int64_t)(p.N + kTileRows - 1) / kTileRows * E : cap / kTileRows + (E < cap ? E : cap);
     const int64_t most = feat_tiles * row_tiles;
     if (most > INT32_MAX / 2) return EPD_ERR_UNSUPPORTED;
-    return launch_pdl(kernel, 2 * (int)(most < pairs ? most : pairs), kThreadsOf<FP8>, kSmem, stream, maps, p);
+    return launch_pdl(kernel, 2 * (int)(most < pairs ? most : pairs), kThreadsOf<MODE, FP8>, kSmem, stream, maps, p);
 }
 
 bool rows_ok(const epd_expert_rows_t *r) {
@@ -1288,6 +1285,8 @@ extern "C" epd_status_t ep_expert_matmul_wgrad(const epd_expert_rows_t *rows, co
     p.K = K;
     p.N = N;
     p.y = static_cast<uint8_t *>(dw);
+    p.dy = static_cast<const uint8_t *>(dy);
+    p.dbias = dbias;
     p.status = status;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     // without rows nothing is loaded, but a map has to lie somewhere
@@ -1297,9 +1296,5 @@ extern "C" epd_status_t ep_expert_matmul_wgrad(const epd_expert_rows_t *rows, co
         if (!encode_rows(&maps.m[i], false, any ? x : dw, rows->capacity_rows, K, cut_rows(i)) ||
             !encode_rows(&maps.n[i], false, any ? dy : dw, rows->capacity_rows, N, cut_rows(i)))
             return EPD_ERR_CUDA;
-    const epd_status_t rc = launch<kWgrad, false, false>(maps, p, st);
-    if (rc != EPD_OK || !dbias) return rc;
-    const int64_t items = (int64_t)((N + 63) / 64) * rows->num_experts;
-    return launch_pdl(bias_grad_kernel, (int)(items < sm_count() ? items : sm_count()), kBiasThreads, 0, st, *rows,
-                      static_cast<const uint8_t *>(dy), N, dbias, status);
+    return launch<kWgrad, false, false>(maps, p, st);
 }
