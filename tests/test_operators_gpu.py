@@ -509,6 +509,54 @@ def test_gradients_match_central_differences():
         assert abs(float(prod.sum() - (up - dn) / (2 * h))) <= (2 ** -8 if i < 2 else 2 ** -17) * float(prod.abs().sum()) + 1e-6
 
 
+def test_many_experts():
+    """4096 experts of a few rows each: the walk over the counts goes in batches of 32."""
+    counts = [(i * 2654435761 >> 7) % 4 for i in range(4096)]
+    run_forward(counts, 64, 24, "gelu", seed=11, bias=True, gaps=1)
+    run_forward(counts, 128, 128, "swiglu", seed=12, fp8=True)
+
+
+def sampled(rows, n, seed):
+    return torch.randint(0, rows, (n,), generator=gen(seed), device=DEV)
+
+
+def test_offsets_beyond_32_bits():
+    """Row buffers and weights of more than 2^32 elements: sampled rows of the last regions."""
+    bf = dict(dtype=torch.bfloat16, device=DEV)
+    M, K, N = 1_100_000, 64, 4096                       # y: 4.5e9 elements
+    g = gen(21)
+    x, w = torch.randn(M, K, generator=g, **bf), torch.randn(2, N, K, generator=g, **bf) / 8
+    counts, start = [M - 300, 300], [300, 0]
+    status = epd.new_status()
+    y, z = epd.ep_expert_matmul(x, w, i32(counts), status, expert_start_loc=i32(start), with_preact=True,
+                                activation="relu")
+    check_ok(status)
+    at = torch.cat([sampled(300, 8, 1), M - 1 - sampled(1000, 40, 2), 300 + sampled(M - 300, 40, 3)])
+    want = torch.where((at < 300).unsqueeze(1), x[at].double() @ w[1].double().t(), x[at].double() @ w[0].double().t())
+    tol = 2 ** -8 * want.abs() + 80 * 2.0 ** -23 * (x[at].double().abs() @ w[0].double().abs().t()) * 4
+    assert ((z[at].double() - want).abs() <= tol).all() and ((y[at].double() - want.relu()).abs() <= tol).all()
+    # the same buffer as dy: dx over 4096 columns, and the weights' gradients of 1.1 million rows
+    dx = epd.ep_expert_matmul_dgrad(x, w.transpose(1, 2).contiguous(), i32(counts), status,
+                                    expert_start_loc=i32(start), activation="relu", preact=z)
+    check_ok(status)
+    want = torch.where(z[at] > 0, want, 0.0)
+    assert ((dx[at].double() - want).abs() <= tol).all()
+    del y, z, dx
+    E, K, N = 17, 16392, 16384                           # w: 4.6e9 elements
+    w = torch.randn(E, N, K, generator=g, **bf) / 128
+    x = torch.randn(E * 3, K, generator=g, **bf)
+    y, _ = epd.ep_expert_matmul(x, w, i32([3] * E), status, expert_start_loc=i32([3 * e for e in range(E)]))
+    check_ok(status)
+    want = x[-3:].double() @ w[-1].double().t()
+    mag = x[-3:].double().abs() @ w[-1].double().abs().t()
+    assert ((y[-3:].double() - want).abs() <= 2 ** -8 * want.abs() + K * 2.0 ** -23 * mag).all()
+    dw, _ = epd.ep_expert_matmul_wgrad(y, x, i32([3] * E), status, expert_start_loc=i32([3 * e for e in range(E)]))
+    check_ok(status)
+    rows = sampled(N, 64, 5)
+    want = y[-3:, rows].double().t() @ x[-3:].double()
+    assert ((dw[-1, rows].double() - want).abs() <= 2 ** -8 * want.abs() + 1e-4).all()
+
+
 # ------------------------------------------------------------------------- combine backward
 @pytest.mark.parametrize("T,H,k", [(1, 8, 1), (3, 1032, 5), (130, 2048, 8), (17, 7168, 8), (9, 264, 64), (4, 4104, 11)])
 @pytest.mark.parametrize("drop", [0.0, 0.3, 1.0])
@@ -537,6 +585,25 @@ def test_unpermute_backward(T, H, k, drop):
             a, b = gy[t].double(), eo[s].double()
             assert abs(float(gw[t, j].double() - a @ b)) <= (H + 1) * 2.0 ** -24 * float(a.abs() @ b.abs())
     assert (geo[~filled] == 7).all()
+
+
+def test_unpermute_backward_offsets_beyond_32_bits():
+    T, H, k = 300, 8192, 2
+    M = 530_000                                          # 4.3e9 elements
+    eo = torch.empty(M, H, dtype=torch.bfloat16, device=DEV)
+    index = (M - 1 - torch.randperm(T * k, generator=gen(1), device=DEV)).view(T, k).to(torch.int32)
+    eo[M - T * k:] = torch.randn(T * k, H, generator=gen(2), device=DEV).to(torch.bfloat16)
+    gy = torch.randn(T, H, generator=gen(3), device=DEV).to(torch.bfloat16)
+    w = torch.rand(T, k, generator=gen(4), device=DEV)
+    status = epd.new_status()
+    geo, gw = epd.ep_unpermute_backward(gy, eo, index, w, status)
+    check_ok(status)
+    at = index.long()
+    want = w.double().unsqueeze(2) * gy.double().unsqueeze(1)
+    assert ((geo[at].double() - want).abs() <= 2 ** -8 * want.abs()).all()
+    dot = (eo[at].double() * gy.double().unsqueeze(1)).sum(2)
+    mag = (eo[at].double() * gy.double().unsqueeze(1)).abs().sum(2)
+    assert ((gw.double() - dot).abs() <= (H + 1) * 2.0 ** -24 * mag).all()
 
 
 def test_unpermute_backward_reports_slots_outside():
