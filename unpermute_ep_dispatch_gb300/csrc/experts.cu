@@ -66,7 +66,12 @@ constexpr int kTileRows = 256;                  // most token rows (wgrad: outpu
 constexpr int kAcrossRows = 128;                // e4m3: most rows of a tile with the features as M
 constexpr int kOperandBytes = 128 * 128;        // 128 rows of 128 bytes: one operand of a stage
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kStagingBytes = 32 * 80;          // per epilogue warp: 32 rows of 64 bytes, 80 apart
+// Staging rows per epilogue warp, 64 bytes each and 80 apart. e4m3 has twice the warps and, with
+// half the rows each, room for a sixth stage (few rows an expert: 1130 us with five, 1110 with six).
+template <bool FP8>
+constexpr int kStagedOf = FP8 ? 16 : 32;
+template <bool FP8>
+constexpr int kStagingOf = kStagedOf<FP8> * 80;
 constexpr int kTailBytes = 768;                 // published tiles and barriers
 constexpr int kScaleGroup = 4;                  // reduction steps per group of staged scales
 constexpr int kScaleBytes = 2 * kScaleGroup * 128 * 8;  // a row's with each of the tile's two weight blocks
@@ -75,10 +80,10 @@ constexpr int kCuts = 18;                       // wgrad's boxes: 64, 32, 16 and
 constexpr int kGroupTiles = 8;                  // row tiles that share a pass over the features
 
 template <bool FP8>
-constexpr int kStagesOf = FP8 ? 5 : 6;
+constexpr int kStagesOf = 6;
 
 template <bool FP8>
-constexpr int kSmemOf = kStagesOf<FP8> *kStageBytes + kEpiWarpsOf<FP8> * kStagingBytes + (FP8 ? kScaleBytes : 0) + kTailBytes;
+constexpr int kSmemOf = kStagesOf<FP8> *kStageBytes + kEpiWarpsOf<FP8> * kStagingOf<FP8> + (FP8 ? kScaleBytes : 0) + kTailBytes;
 
 struct ExpertArgs {
     epd_expert_rows_t rows;
@@ -264,50 +269,55 @@ __device__ __forceinline__ void apply(Frag &f) {
         for (int r = 0; r < 16; ++r) f[h][r] = activate<ACT>(f[h][r]);
 }
 
-// Writes the first `rows` of 32 staged rows, `parts` of their four 16-byte parts each, to
-// at + row * pitch.
+// Writes the first `rows` of 32 rows (columns of D), `parts` of their four 16-byte parts each, to
+// at + row * pitch, STAGED rows at a time.
+template <int STAGED>
 __device__ __forceinline__ void put_frag(uint32_t stage, const Frag &f, uint8_t *at, int64_t pitch, int rows,
                                          int parts) {
-    const int lane = threadIdx.x & 31;
-    __syncwarp();
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-        stmatrix_t(stage + (u * 8 + block_column(lane & 7)) * kPitch + (lane >> 3) * 16,
-                   pack2_bf16(f[0][4 * u], f[0][4 * u + 2]), pack2_bf16(f[0][4 * u + 1], f[0][4 * u + 3]),
-                   pack2_bf16(f[1][4 * u], f[1][4 * u + 2]), pack2_bf16(f[1][4 * u + 1], f[1][4 * u + 3]));
-    __syncwarp();
-    const int part = lane & 3;
+    const int lane = threadIdx.x & 31, part = lane & 3;
     at += part * 16;
-    const bool live = part < parts;
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-        const int row = lane_row(it);
-        const uint4 v = lds16(stage + row * kPitch + part * 16);
-        if (live && row < rows) st16(at + row * pitch, v);
+    for (int r0 = 0; r0 < 32; r0 += STAGED) {
+        __syncwarp();
+#pragma unroll
+        for (int u = r0 / 8; u < (r0 + STAGED) / 8; ++u)
+            stmatrix_t(stage + (u * 8 - r0 + block_column(lane & 7)) * kPitch + (lane >> 3) * 16,
+                       pack2_bf16(f[0][4 * u], f[0][4 * u + 2]), pack2_bf16(f[0][4 * u + 1], f[0][4 * u + 3]),
+                       pack2_bf16(f[1][4 * u], f[1][4 * u + 2]), pack2_bf16(f[1][4 * u + 1], f[1][4 * u + 3]));
+        __syncwarp();
+#pragma unroll
+        for (int it = 0; it < STAGED / 8; ++it) {
+            const int row = lane_row(it);
+            const uint4 v = lds16(stage + row * kPitch + part * 16);
+            if (part < parts && r0 + row < rows) st16(at + (r0 + row) * pitch, v);
+        }
     }
 }
 
 // The same for 16 features, a half of the warp's.
+template <int STAGED>
 __device__ __forceinline__ void put_half(uint32_t stage, const float (&f)[16], uint8_t *at, int64_t pitch, int rows, int parts) {
     constexpr int kHalfPitch = 48;
-    const int lane = threadIdx.x & 31;
-    __syncwarp();
+    const int lane = threadIdx.x & 31, part = lane & 1;
 #pragma unroll
-    for (int u = 0; u < 4; u += 2)
-        stmatrix_t(stage + ((u + (lane >> 4)) * 8 + block_column(lane & 7)) * kHalfPitch + ((lane >> 3) & 1) * 16,
-                   pack2_bf16(f[4 * u], f[4 * u + 2]), pack2_bf16(f[4 * u + 1], f[4 * u + 3]),
-                   pack2_bf16(f[4 * u + 4], f[4 * u + 6]), pack2_bf16(f[4 * u + 5], f[4 * u + 7]));
-    __syncwarp();
-    const int part = lane & 1;
+    for (int r0 = 0; r0 < 32; r0 += STAGED) {
+        __syncwarp();
 #pragma unroll
-    for (int it = 0; it < 2; ++it) {
-        const int row = it * 16 + (lane >> 1);
-        const uint4 v = lds16(stage + row * kHalfPitch + part * 16);
-        if (part < parts && row < rows) st16(at + row * pitch + part * 16, v);
+        for (int u = r0 / 8; u < (r0 + STAGED) / 8; u += 2)
+            stmatrix_t(stage + ((u + (lane >> 4)) * 8 - r0 + block_column(lane & 7)) * kHalfPitch + ((lane >> 3) & 1) * 16,
+                       pack2_bf16(f[4 * u], f[4 * u + 2]), pack2_bf16(f[4 * u + 1], f[4 * u + 3]),
+                       pack2_bf16(f[4 * u + 4], f[4 * u + 6]), pack2_bf16(f[4 * u + 5], f[4 * u + 7]));
+        __syncwarp();
+#pragma unroll
+        for (int it = 0; it < STAGED / 16; ++it) {
+            const int row = it * 16 + (lane >> 1);
+            const uint4 v = lds16(stage + row * kHalfPitch + part * 16);
+            if (part < parts && r0 + row < rows) st16(at + (r0 + row) * pitch + part * 16, v);
+        }
     }
 }
 
-// 32 rows of 64 (32) bytes of a bf16 operand, fetched ahead of their use and then turned into
+// 32 rows of 64 bytes of a bf16 operand, fetched ahead of their use and then turned into
 // fragments by way of the staging rows. What lies outside is zero.
 struct Ahead {
     uint4 v[4];
@@ -321,36 +331,54 @@ struct Ahead {
         }
     }
 
+    // Rows r0 .. r0 + STAGED - 1 into the staging rows.
+    template <int STAGED>
+    __device__ __forceinline__ void stage_rows(uint32_t stage, int r0) const {
+        __syncwarp();
+#pragma unroll
+        for (int it = 0; it < STAGED / 8; ++it)
+            sts16(stage + lane_row(it) * kPitch + (threadIdx.x & 3) * 16, v[r0 / 8 + it]);
+        __syncwarp();
+    }
+
+    template <int STAGED>
     __device__ __forceinline__ void turn(uint32_t stage, uint32_t (&w)[2][8]) const {
         const int lane = threadIdx.x & 31;
-        __syncwarp();
 #pragma unroll
-        for (int it = 0; it < 4; ++it) sts16(stage + lane_row(it) * kPitch + (lane & 3) * 16, v[it]);
-        __syncwarp();
+        for (int r0 = 0; r0 < 32; r0 += STAGED) {
+            stage_rows<STAGED>(stage, r0);
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            ldmatrix_t(stage + (u * 8 + block_column(lane & 7)) * kPitch + (lane >> 3) * 16, w[0][2 * u], w[0][2 * u + 1],
-                       w[1][2 * u], w[1][2 * u + 1]);
+            for (int u = r0 / 8; u < (r0 + STAGED) / 8; ++u)
+                ldmatrix_t(stage + (u * 8 - r0 + block_column(lane & 7)) * kPitch + (lane >> 3) * 16, w[0][2 * u],
+                           w[0][2 * u + 1], w[1][2 * u], w[1][2 * u + 1]);
+        }
     }
 };
 
 // Sixteen values a lane to the same lane of the pair's other warp, by way of the staging rows.
+template <int STAGED>
 __device__ __forceinline__ bool swap_half(uint32_t mine, uint32_t other, uint32_t bar, const float (&out)[16], float (&in)[16]) {
+    constexpr int kAtOnce = STAGED / 8;  // of the sixteen's four parts: 512 bytes each
     const uint32_t at = (threadIdx.x & 31) * 16;
-    __syncwarp();
+    bool ok = true;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        sts16(mine + i * 512 + at, make_uint4(__float_as_uint(out[4 * i]), __float_as_uint(out[4 * i + 1]),
-                                              __float_as_uint(out[4 * i + 2]), __float_as_uint(out[4 * i + 3])));
-    mbar_arrive_own(bar);  // of 64: the barrier's two phases, written and read, end as they began
-    bool ok = mbar_wait_pipe(bar, 0);
+    for (int p0 = 0; p0 < 4; p0 += kAtOnce) {
+        __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = lds16f(other + i * 512 + at);
-        in[4 * i] = v.x, in[4 * i + 1] = v.y, in[4 * i + 2] = v.z, in[4 * i + 3] = v.w;
+        for (int i = p0; i < p0 + kAtOnce; ++i)
+            sts16(mine + (i - p0) * 512 + at,
+                  make_uint4(__float_as_uint(out[4 * i]), __float_as_uint(out[4 * i + 1]),
+                             __float_as_uint(out[4 * i + 2]), __float_as_uint(out[4 * i + 3])));
+        mbar_arrive_own(bar);  // of 64: the barrier's two phases, written and read, end as they began
+        ok = ok && mbar_wait_pipe(bar, 0);
+#pragma unroll
+        for (int i = p0; i < p0 + kAtOnce; ++i) {
+            const float4 v = lds16f(other + (i - p0) * 512 + at);
+            in[4 * i] = v.x, in[4 * i + 1] = v.y, in[4 * i + 2] = v.z, in[4 * i + 3] = v.w;
+        }
+        mbar_arrive_own(bar);
+        ok = ok && mbar_wait_pipe(bar, 1);
     }
-    mbar_arrive_own(bar);
-    ok = ok && mbar_wait_pipe(bar, 1);
     return __all_sync(0xffffffffu, ok);
 }
 
@@ -361,7 +389,7 @@ __device__ __forceinline__ float element(const uint32_t (&w)[8], int r) {
 }
 
 // A warp's share of a tile's output.
-template <int MODE, bool GATED>
+template <int MODE, bool GATED, int STAGED>
 struct Output {
     static constexpr bool kHalf = GATED && MODE == kForward;
     const ExpertArgs &p;
@@ -377,8 +405,8 @@ struct Output {
     Ahead a, b;            // the residual, or dgrad's pre-activations (b: their up part)
 
     __device__ Output(const ExpertArgs &args, uint32_t staging, uint32_t bars, int warp) : p(args) {
-        stage = staging + warp * kStagingBytes;
-        other = staging + (warp ^ 2) * kStagingBytes;
+        stage = staging + warp * STAGED * kPitch;
+        other = staging + (warp ^ 2) * STAGED * kPitch;
         up = kHalf ? (warp >> 1) & 1 : 0;
         bar = bars + 8 * ((warp >> 2) * 2 + (warp & 1));
     }
@@ -426,19 +454,19 @@ struct Output {
         uint8_t *at = p.y + (row + col0) * pitch + feat * 2;
         const int left = rows - col0;
         if (MODE == kWgrad) {
-            put_frag(stage, f, at, pitch, left, parts);
+            put_frag<STAGED>(stage, f, at, pitch, left, parts);
             return;
         }
         if (MODE == kDgrad) {
             if (p.act == EPD_ACT_NONE) {
-                put_frag(stage, f, at, pitch, left, parts);
+                put_frag<STAGED>(stage, f, at, pitch, left, parts);
                 return;
             }
             uint32_t z[2][8];
-            a.turn(stage, z);
+            a.turn<STAGED>(stage, z);
             if (GATED) {
                 uint32_t u[2][8];
-                b.turn(stage, u);
+                b.turn<STAGED>(stage, u);
                 if (next < rows) fetch(next);
                 Frag up;
 #pragma unroll
@@ -450,8 +478,8 @@ struct Output {
                         up[h][r] = f[h][r] * g * s;
                         f[h][r] = f[h][r] * w * (s * (1.0f + g * (1.0f - s)));
                     }
-                put_frag(stage, f, at, pitch, left, parts);
-                put_frag(stage, up, at + (int64_t)p.K * 2, pitch, left, parts);
+                put_frag<STAGED>(stage, f, at, pitch, left, parts);
+                put_frag<STAGED>(stage, up, at + (int64_t)p.K * 2, pitch, left, parts);
                 return;
             }
             if (next < rows) fetch(next);
@@ -461,7 +489,7 @@ struct Output {
                 times_slope<EPD_ACT_SILU>(f, z);
             else
                 times_slope<EPD_ACT_GELU>(f, z);
-            put_frag(stage, f, at, pitch, left, parts);
+            put_frag<STAGED>(stage, f, at, pitch, left, parts);
             return;
         }
         if (p.bias) {
@@ -472,29 +500,29 @@ struct Output {
         }
         if (p.preact) {
             const int64_t zp = (int64_t)p.N * 2 * (GATED ? 2 : 1);
-            put_frag(stage, f, p.preact + (row + col0) * zp + ((int64_t)feat + (up ? p.N : 0)) * 2, zp, left, parts);
+            put_frag<STAGED>(stage, f, p.preact + (row + col0) * zp + ((int64_t)feat + (up ? p.N : 0)) * 2, zp, left, parts);
         }
         if (GATED) {
             // the gate warp finishes the first 16 features and the up warp the last: each sends
             // the other what it needs for them
             float in[16];
             if (up) {
-                ok = ok && swap_half(stage, other, bar, f[0], in);
+                ok = ok && swap_half<STAGED>(stage, other, bar, f[0], in);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) f[1][r] = in[r] * fast_sigmoid(in[r]) * f[1][r];
             } else {
-                ok = ok && swap_half(stage, other, bar, f[1], in);
+                ok = ok && swap_half<STAGED>(stage, other, bar, f[1], in);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) f[1][r] = f[0][r] * fast_sigmoid(f[0][r]) * in[r];
             }
             if (p.residual) {
                 uint32_t z[2][8];
-                a.turn(stage, z);
+                a.turn<STAGED>(stage, z);
                 if (next < rows) fetch(next);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) f[1][r] += up ? element(z[1], r) : element(z[0], r);
             }
-            put_half(stage, f[1], at + up * 32, pitch, left, max(0, min(2, parts - 2 * up)));
+            put_half<STAGED>(stage, f[1], at + up * 32, pitch, left, max(0, min(2, parts - 2 * up)));
             return;
         }
         if (p.act == EPD_ACT_RELU) {
@@ -506,34 +534,39 @@ struct Output {
         }
         if (p.residual) {
             uint32_t z[2][8];
-            a.turn(stage, z);
+            a.turn<STAGED>(stage, z);
             if (next < rows) fetch(next);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) f[h][r] += element(z[h], r);
         }
-        put_frag(stage, f, at, pitch, left, parts);
+        put_frag<STAGED>(stage, f, at, pitch, left, parts);
     }
 };
 
 // ---- e4m3: a lane is a row, f[c] its column c of 32.
 __device__ __forceinline__ void put_rows(uint32_t stage, const float (&f)[32], uint8_t *at, int64_t pitch, int rows,
                                          int parts) {
-    const int lane = threadIdx.x & 31;
-    __syncwarp();
+    constexpr int kStaged = kStagedOf<true>;
+    const int lane = threadIdx.x & 31, part = lane & 3;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        sts16(stage + lane * kPitch + i * 16,
-              make_uint4(pack2_bf16(f[8 * i], f[8 * i + 1]), pack2_bf16(f[8 * i + 2], f[8 * i + 3]),
-                         pack2_bf16(f[8 * i + 4], f[8 * i + 5]), pack2_bf16(f[8 * i + 6], f[8 * i + 7])));
-    __syncwarp();
-    const int part = lane & 3;
+    for (int r0 = 0; r0 < 32; r0 += kStaged) {
+        __syncwarp();
+        if (lane / kStaged == r0 / kStaged) {
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-        const int row = lane_row(it);
-        const uint4 v = lds16(stage + row * kPitch + part * 16);
-        if (part < parts && row < rows) st16(at + row * pitch + part * 16, v);
+            for (int i = 0; i < 4; ++i)
+                sts16(stage + lane % kStaged * kPitch + i * 16,
+                      make_uint4(pack2_bf16(f[8 * i], f[8 * i + 1]), pack2_bf16(f[8 * i + 2], f[8 * i + 3]),
+                                 pack2_bf16(f[8 * i + 4], f[8 * i + 5]), pack2_bf16(f[8 * i + 6], f[8 * i + 7])));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int it = 0; it < kStaged / 8; ++it) {
+            const int row = lane_row(it);
+            const uint4 v = lds16(stage + row * kPitch + part * 16);
+            if (part < parts && r0 + row < rows) st16(at + (r0 + row) * pitch + part * 16, v);
+        }
     }
 }
 
@@ -575,17 +608,19 @@ __device__ __forceinline__ void finish_rows(const ExpertArgs &p, const Tile &t, 
         if (p.residual) {
             Ahead r;
             r.fetch(p.residual + row * pitch + (int64_t)feat * 2, pitch, rows, parts);
+            constexpr int kStaged = kStagedOf<true>;
             const int lane = threadIdx.x & 31;
-            __syncwarp();
 #pragma unroll
-            for (int it = 0; it < 4; ++it) sts16(stage + lane_row(it) * kPitch + (lane & 3) * 16, r.v[it]);
-            __syncwarp();
+            for (int r0 = 0; r0 < 32; r0 += kStaged) {
+                r.stage_rows<kStaged>(stage, r0);
+                if (lane / kStaged != r0 / kStaged) continue;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float e[8];
-                unpack8_bf16(lds16(stage + lane * kPitch + i * 16), e);
+                for (int i = 0; i < 4; ++i) {
+                    float e[8];
+                    unpack8_bf16(lds16(stage + lane % kStaged * kPitch + i * 16), e);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) f[8 * i + c] += e[c];
+                    for (int c = 0; c < 8; ++c) f[8 * i + c] += e[c];
+                }
             }
         }
         put_rows(stage, f, p.y + row * pitch + (int64_t)feat * 2, pitch, rows, parts);
@@ -648,7 +683,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<MODE, FP8
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *after = smem + kStages * kStageBytes;
     const uint32_t staging = smem_addr(after);
-    after += kEpiWarps * kStagingBytes;
+    after += kEpiWarps * kStagingOf<FP8>;
     float *scales = reinterpret_cast<float *>(after);
     if (FP8) after += kScaleBytes;
     Tile *slots = reinterpret_cast<Tile *>(after);
@@ -968,7 +1003,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<MODE, FP8
                         }
                     }
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    Output<MODE, GATED> out(p, staging, bar0 + 8 * kSwap, warp);
+                    Output<MODE, GATED, kStagedOf<FP8>> out(p, staging, bar0 + 8 * kSwap, warp);
                     out.begin(ring.tile(), rank, quadrant);
                     if (own) {
                         out.fetch(share * 32);
@@ -1019,11 +1054,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<MODE, FP8
                 }
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 if (blocks > 0) finish_rows<GATED>(p, ring.tile(), rank * 128 + quadrant * 32, share * 32,
-                                                   staging + warp * kStagingBytes, acc);
+                                                   staging + warp * kStagingOf<FP8>, acc);
                 ring.drop();
             }
         } else {
-            Output<MODE, GATED> out(p, staging, bar0 + 8 * kSwap, warp);
+            Output<MODE, GATED, kStagedOf<FP8>> out(p, staging, bar0 + 8 * kSwap, warp);
             int buf = 0;
             while (ok && ring.next(ok)) {
                 const Tile &t = ring.tile();
