@@ -577,10 +577,10 @@ def ep_unpermute(expert_out: torch.Tensor, output_index: torch.Tensor,
 
 # ----------------------------------------------------------------------------- routing
 def _choose(table, key, name):
-    try:
-        return table[key]
-    except KeyError:
-        raise ValueError(f"{name} must be one of {sorted(table)}, got {key!r}") from None
+    v = table.get(key)
+    if v is None:
+        raise ValueError(f"{name} must be one of {sorted(table)}, got {key!r}")
+    return v
 
 
 def _logits(t):
@@ -644,22 +644,23 @@ def ep_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx
 
 
 # ----------------------------------------------------------------------------- experts' products
-def _expert_rows(x, E, tokens_per_expert, expert_start_loc, dev):
-    """epd_expert_rows_t of row buffers shaped like x: [M, *] with expert_start_loc, or the
-    rectangles [E, rows, *] without."""
+def _expert_rows(shape, E, tokens_per_expert, expert_start_loc, dev):
+    """epd_expert_rows_t of row buffers of `shape`: (M, *) with expert_start_loc, or the
+    rectangles (E, rows, *) without."""
     _want(tokens_per_expert, "tokens_per_expert", torch.int32, (E,), dev)
-    if x.dim() == 3:
-        if expert_start_loc is not None:
-            raise ValueError("rectangles [E, rows, *] take no expert_start_loc")
-        if x.shape[0] != E:
-            raise ValueError(f"rectangles must be [{E}, rows, *], got {tuple(x.shape)}")
-        return ExpertRows(E, E * x.shape[1], x.shape[1], None, tokens_per_expert.data_ptr())
-    if x.dim() != 2:
+    if len(shape) == 2:
+        if expert_start_loc is None:
+            raise ValueError("rows [M, *] need expert_start_loc")
+        _want(expert_start_loc, "expert_start_loc", torch.int32, (E,), dev)
+        return ExpertRows(E, shape[0], 0, expert_start_loc.data_ptr(),
+                          tokens_per_expert.data_ptr())
+    if len(shape) != 3:
         raise ValueError("rows must be [M, *], or [E, rows, *] rectangles")
-    if expert_start_loc is None:
-        raise ValueError("rows [M, *] need expert_start_loc")
-    _want(expert_start_loc, "expert_start_loc", torch.int32, (E,), dev)
-    return ExpertRows(E, x.shape[0], 0, expert_start_loc.data_ptr(), tokens_per_expert.data_ptr())
+    if expert_start_loc is not None:
+        raise ValueError("rectangles [E, rows, *] take no expert_start_loc")
+    if shape[0] != E:
+        raise ValueError(f"rectangles must be [{E}, rows, *], got {tuple(shape)}")
+    return ExpertRows(E, E * shape[1], shape[1], None, tokens_per_expert.data_ptr())
 
 
 def ep_expert_matmul(x: torch.Tensor, w: torch.Tensor, tokens_per_expert: torch.Tensor,
@@ -677,43 +678,43 @@ def ep_expert_matmul(x: torch.Tensor, w: torch.Tensor, tokens_per_expert: torch.
     activation: "none", "relu", "silu", "gelu" or "swiglu". Returns (y [M, N] or
     [E, rows, N] bfloat16, preact [.., NW] bfloat16 or None); see epd.h."""
     act = _choose(ACTIVATION, activation, "activation")
-    if x.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-        raise ValueError(f"x must be bfloat16 or float8_e4m3fn, got {x.dtype}")
-    _want(x, "x", x.dtype)
+    dtype = x.dtype
+    fp8 = dtype is torch.float8_e4m3fn
+    if not fp8 and dtype is not torch.bfloat16:
+        raise ValueError(f"x must be bfloat16 or float8_e4m3fn, got {dtype}")
+    _want(x, "x", dtype)
     dev = x.device
-    _want(w, "w", x.dtype, device=dev)
-    if w.dim() != 3 or w.shape[2] != x.shape[-1]:
-        raise ValueError(f"w must be [E, N, {x.shape[-1]}], got {tuple(w.shape)}")
+    _want(w, "w", dtype, device=dev)
+    shape = tuple(x.shape)
+    if w.dim() != 3 or w.shape[2] != shape[-1]:
+        raise ValueError(f"w must be [E, N, {shape[-1]}], got {tuple(w.shape)}")
     E, NW, K = w.shape
     if act == 4 and NW % 2:
         raise ValueError("swiglu weights have an even number of rows")
     N = NW // 2 if act == 4 else NW
-    rows = _expert_rows(x, E, tokens_per_expert, expert_start_loc, dev)
+    rows = _expert_rows(shape, E, tokens_per_expert, expert_start_loc, dev)
     _want(status, "status", torch.int32, (1,), dev)
-    lead = tuple(x.shape[:-1])
+    lead = shape[:-1]
     srow = scol = sexp = 0
-    if x.dtype == torch.float8_e4m3fn:
+    if fp8:
         C = K // 128
         if x_scale is None or w_scale is None:
             raise ValueError("fp8 rows need x_scale and w_scale")
         _want(w_scale, "w_scale", torch.float32, (E, (NW + 127) // 128, C), dev)
-        if x.dim() == 3:
-            R = x.shape[1]
+        if len(shape) == 3:
+            R = shape[1]
             _want(x_scale, "x_scale", torch.float32, (E, C, R), dev)
             srow, scol, sexp = 1, R, (C - 1) * R
         elif scale_col_major:
             _want(x_scale, "x_scale", torch.float32, device=dev)
-            if x_scale.dim() != 2 or x_scale.shape[0] != C or x_scale.shape[1] < x.shape[0]:
-                raise ValueError(f"x_scale must be [{C}, ld >= {x.shape[0]}]")
+            if x_scale.dim() != 2 or x_scale.shape[0] != C or x_scale.shape[1] < shape[0]:
+                raise ValueError(f"x_scale must be [{C}, ld >= {shape[0]}]")
             srow, scol = 1, x_scale.shape[1]
         else:
-            _want(x_scale, "x_scale", torch.float32, (x.shape[0], C), dev)
+            _want(x_scale, "x_scale", torch.float32, (shape[0], C), dev)
             srow, scol = C, 1
-        dt = EPD_FP8_E4M3
-    else:
-        if x_scale is not None or w_scale is not None:
-            raise ValueError("bf16 rows take no scales")
-        dt = EPD_BF16
+    elif x_scale is not None or w_scale is not None:
+        raise ValueError("bf16 rows take no scales")
     if bias is not None:
         _want(bias, "bias", torch.float32, (E, NW), dev)
     if residual is not None:
@@ -722,7 +723,8 @@ def ep_expert_matmul(x: torch.Tensor, w: torch.Tensor, tokens_per_expert: torch.
     if preact is not None or with_preact:
         preact = _out(preact, "preact", torch.bfloat16, (*lead, NW), dev)
     rc = load_library().ep_expert_matmul(
-        ctypes.byref(rows), _ptr(x), dt, _ptr(x_scale), srow, scol, sexp, _ptr(w), _ptr(w_scale),
+        ctypes.byref(rows), _ptr(x), EPD_FP8_E4M3 if fp8 else EPD_BF16, _ptr(x_scale), srow, scol,
+        sexp, _ptr(w), _ptr(w_scale),
         K, N, act, _ptr(bias), _ptr(residual), _ptr(y), _ptr(preact), _ptr(status),
         _stream(stream, dev))
     _check(rc, "ep_expert_matmul")
@@ -740,12 +742,13 @@ def ep_expert_matmul_dgrad(dy: torch.Tensor, w: torch.Tensor, tokens_per_expert:
     _want(dy, "dy", torch.bfloat16)
     dev = dy.device
     _want(w, "w", torch.bfloat16, device=dev)
-    if w.dim() != 3 or w.shape[1] != dy.shape[-1]:
-        raise ValueError(f"w must be [E, {dy.shape[-1]}, K], got {tuple(w.shape)}")
+    rows_shape = tuple(dy.shape)
+    if w.dim() != 3 or w.shape[1] != rows_shape[-1]:
+        raise ValueError(f"w must be [E, {rows_shape[-1]}, K], got {tuple(w.shape)}")
     E, N, K = w.shape
-    rows = _expert_rows(dy, E, tokens_per_expert, expert_start_loc, dev)
+    rows = _expert_rows(rows_shape, E, tokens_per_expert, expert_start_loc, dev)
     _want(status, "status", torch.int32, (1,), dev)
-    shape = (*dy.shape[:-1], 2 * K if act == 4 else K)
+    shape = (*rows_shape[:-1], 2 * K if act == 4 else K)
     if act:
         _want(preact, "preact", torch.bfloat16, shape, dev)
     elif preact is not None:
@@ -767,13 +770,14 @@ def ep_expert_matmul_wgrad(dy: torch.Tensor, x: torch.Tensor, tokens_per_expert:
     _want(dy, "dy", torch.bfloat16)
     dev = dy.device
     _want(x, "x", torch.bfloat16, device=dev)
-    if x.shape[:-1] != dy.shape[:-1]:
+    shape, x_shape = tuple(dy.shape), tuple(x.shape)
+    if x_shape[:-1] != shape[:-1]:
         raise ValueError("dy and x must have the same rows")
     if not isinstance(tokens_per_expert, torch.Tensor) or tokens_per_expert.dim() != 1:
         raise ValueError("tokens_per_expert must be [E]")
     E = tokens_per_expert.shape[0]
-    N, K = dy.shape[-1], x.shape[-1]
-    rows = _expert_rows(dy, E, tokens_per_expert, expert_start_loc, dev)
+    N, K = shape[-1], x_shape[-1]
+    rows = _expert_rows(shape, E, tokens_per_expert, expert_start_loc, dev)
     _want(status, "status", torch.int32, (1,), dev)
     dw = _out(dw, "dw", torch.bfloat16, (E, N, K), dev)
     if dbias is not None or with_dbias:
