@@ -37,9 +37,15 @@ constexpr float kInvSqrt2Pi = 0.39894228040143267794f;
 
 __device__ __forceinline__ float gelu_cdf(float z) { return 0.5f * (1.0f + erff(z * kSqrtHalf)); }
 
-// The sigmoid of the activations, by the hardware's exponential and division: within a few
-// 2^-22 of its value, far below the bf16 it is rounded to.
-__device__ __forceinline__ float fast_sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+// The sigmoid of the activations, by the hardware's exponential and reciprocal: within a few
+// 2^-22 of its value, far below the bf16 it is rounded to (and 0 where it is below 2^-126).
+__device__ __forceinline__ float fast_sigmoid(float x) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -kLog2e));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
 
 // act(z) of the ungated activations.
 template <int ACT>

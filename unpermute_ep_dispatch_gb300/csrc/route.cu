@@ -4,10 +4,13 @@
 // kept in registers as the values that decide the choice. The argmax is two warp reductions: the
 // largest value, then the lowest index that has it -- the tie rule at no extra cost. Every lane
 // keeps its two largest at hand, so that a pick costs its owner a move and only a lane's second
-// pick a new pass over its values.
+// pick a new pass over its values, for those that come after the pick in the order of picks.
 //
-// What bounds it: a row of 256 logits is 1 KiB, 2.7 us for 16384 rows at the copy rate; the
-// instructions of k rounds and of the scores (some 700 a token) take longer than that.
+// What bounds it: a row of 256 logits is 1 KiB, 2.7 us for 16384 rows at the copy rate; its
+// instructions (742 a token with a bias and 4 of 8 groups, 466 for plain softmax; two thirds of
+// them compares, selects and maxima at half rate) take 14.0 and 9.5 us back to back in a graph.
+// Rows of up to 256 logits are held to 32 registers, so that sixteen blocks fit an SM and a call
+// starts under the end of the one before: 4097 rows 5.6 us from 7.2 in a graph, 16384 the same.
 #include "route.cuh"
 
 namespace epd {
@@ -24,6 +27,7 @@ struct RouteArgs {
     const void *logits;
     const float *bias;
     int T, k, E, groups, keep, size;  // size: experts per group
+    int run;                          // log2 of the lanes per group, where groups are runs of whole chunks; or -1
     uint32_t by_size;                 // ceil(2^32 / size): e / size = high word of e * by_size
     int top2, renorm, vec, bias_vec;
     float scale;
@@ -58,7 +62,7 @@ __device__ __forceinline__ uint64_t keep_groups(const float (&mine)[EPD_MAX_GROU
 }
 
 template <typename T, int V, int SCORING>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(kRouteThreads, V <= 8 ? 16 : 1) route_kernel(RouteArgs a) {
     using L = Layout<T, V>;
     extern __shared__ float s_dyn[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -112,11 +116,12 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
         }
     }
     if (grouped) {
-        float mine[EPD_MAX_GROUPS / 32] = {-CUDART_INF_F, -CUDART_INF_F};
-        const int width = a.size / L::C;  // lanes per group, where groups are runs of whole chunks
-        const bool runs = width * L::C == a.size && (width & (width - 1)) == 0 && width <= 32 && a.groups <= 32;
-        if (runs) {
-            const int per = 32 / width;  // groups in each chunk of the warp
+        if (a.run >= 0) {
+            // every lane of a run gets its group's score, and compares it with those of all groups,
+            // one a lane and pass
+            const int width = 1 << a.run, per = 32 >> a.run;  // per: groups in each chunk of the warp
+            float score[L::Q], all = -CUDART_INF_F;           // all: that of group `lane`
+            int ahead[L::Q];
 #pragma unroll
             for (int q = 0; q < L::Q; ++q) {
                 float b1 = c[q * L::C], b2 = -CUDART_INF_F;
@@ -127,21 +132,26 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
                 }
                 for (int o = width / 2; o; o >>= 1)
                     merge_top2(b1, b2, __shfl_xor_sync(kFull, b1, o), __shfl_xor_sync(kFull, b2, o));
-                const float s = __shfl_sync(kFull, group_score(b1, b2, a.top2), (lane & (per - 1)) * width);
-                if (lane / per == q) mine[0] = s;
+                score[q] = group_score(b1, b2, a.top2);
+                const float s = __shfl_sync(kFull, score[q], (lane & (per - 1)) << a.run);
+                if (lane >> (5 - a.run) == q) all = s;
+                ahead[q] = 0;
             }
-            int ahead = 0;
-            for (int o = 0; o < a.groups; ++o) {
-                const float other = __shfl_sync(kFull, mine[0], o);
-                ahead += other > mine[0] || (other == mine[0] && o < lane);
-            }
-            const uint32_t kept = __ballot_sync(kFull, lane < a.groups && ahead < a.keep);
+            const uint32_t mine = (0xffffffffu >> (32 - width)) << (lane & -width);  // this run's lanes
+            for (int o0 = 0; o0 < a.groups; o0 += width) {
+                const int o = o0 + (lane & (width - 1));
+                const float other = __shfl_sync(kFull, all, o);
 #pragma unroll
-            for (int q = 0; q < L::Q; ++q) {
-                const bool stays = (kept >> ((q * per + lane / width) & 31)) & 1;
-#pragma unroll
-                for (int i = 0; i < L::C; ++i) c[q * L::C + i] = stays ? c[q * L::C + i] : -CUDART_INF_F;
+                for (int q = 0; q < L::Q; ++q) {
+                    const int g = q * per + (lane >> a.run);
+                    const bool before = other > score[q] || (other == score[q] && o < g);
+                    ahead[q] += __popc(__ballot_sync(kFull, before) & mine);
+                }
             }
+#pragma unroll
+            for (int q = 0; q < L::Q; ++q)
+#pragma unroll
+                for (int i = 0; i < L::C; ++i) c[q * L::C + i] = ahead[q] < a.keep ? c[q * L::C + i] : -CUDART_INF_F;
         } else {
             // any other shape: from the row in shared memory, a power-of-two run of lanes a group
             float *s_row = s_dyn + (size_t)warp * (a.E + EPD_MAX_GROUPS), *s_group = s_row + a.E;
@@ -164,6 +174,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
                 if (g < a.groups && lane % per == 0) s_group[g] = group_score(b1, b2, a.top2);
             }
             __syncwarp();
+            float mine[EPD_MAX_GROUPS / 32] = {-CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
             for (int h = 0; h < EPD_MAX_GROUPS / 32; ++h)
                 if (h * 32 + lane < a.groups) mine[h] = s_group[h * 32 + lane];
@@ -183,8 +194,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
             for (int i = 0; i < V; ++i) c[i] = c[i] > -CUDART_INF_F ? l[i] : -CUDART_INF_F;
         }
     }
-    // k rounds of argmax; lane j % 32 keeps pick j. o1, o2: the two largest's places in the lane's
-    // part of the row, as index(i, 0)
+    // k rounds of argmax; lane j % 32 keeps pick j. o1, o2: the experts of the lane's two largest
     int pick[2] = {-1, -1};
     float b1 = -CUDART_INF_F, b2 = -CUDART_INF_F;
     int o1 = 0, o2 = 0;
@@ -197,45 +207,43 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
         b1 = fmaxf(b1, v);
         o1 = p1 ? L::index(i, 0) : o1;
     }
-    bool second = true;  // b2, o2 are this lane's next one
+    o1 += lane * L::C, o2 += lane * L::C;
     for (int j = 0; j < a.k; ++j) {
         const float top = redux_max(b1);
         if (top == -CUDART_INF_F) break;
-        const int e = b1 == top ? o1 + lane * L::C : INT32_MAX;
+        const int e = b1 == top ? o1 : INT32_MAX;
         const int chosen = __reduce_min_sync(kFull, e);
-        if ((j & 31) == lane) pick[j >> 5] = chosen;
-        if (e == chosen) {
-            if (second) {
-                const int gone = o1;
-                b1 = b2;
-                o1 = o2;
-                o2 = gone;
-                second = false;
-            } else {
-                // o2 is the pick before this one; both leave, and the lane looks again
+        if (j == lane) pick[0] = chosen;
+        if (j == lane + 32) pick[1] = chosen;
+        if (e == chosen) {  // its next one; NaN once that is not at hand any more
+            b1 = b2;
+            o1 = o2;
+            b2 = CUDART_NAN_F;
+        }
+        if (b1 != b1) {
+            // the lane looks again, among what comes after the pick: picks come in order
+            b1 = -CUDART_INF_F;
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (L::index(i, 0) == o1 || L::index(i, 0) == o2) c[i] = -CUDART_INF_F;
-                b1 = -CUDART_INF_F;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    o1 = c[i] > b1 ? L::index(i, 0) : o1;
-                    b1 = fmaxf(b1, c[i]);
-                }
-                o2 = o1;
+            for (int i = 0; i < V; ++i) {
+                const int at = L::index(i, lane);
+                const bool left = c[i] < top || (c[i] == top && at > chosen);
+                if (left && c[i] > b1) b1 = c[i], o1 = at;
             }
         }
     }
-    float s[2];
+    const int halves = a.k > 32 ? 2 : 1;
+    float s[2] = {-CUDART_INF_F, -CUDART_INF_F};
     float sum = 0.0f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) s[h] = pick[h] >= 0 ? to_f32(row[pick[h]]) : -CUDART_INF_F;
+    for (int h = 0; h < 2; ++h)
+        if (h < halves && pick[h] >= 0) s[h] = to_f32(row[pick[h]]);
     if (SCORING == EPD_SCORE_SOFTMAX && a.renorm) {
         m = warp_max(fmaxf(s[0], s[1]));
         inv = 1.0f;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+        if (h == halves) break;
         if (SCORING == EPD_SCORE_SIGMOID)
             s[h] = sigmoid_f32(s[h]);
         else
@@ -245,6 +253,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(RouteArgs a) {
     if (a.renorm) sum = warp_sum(sum);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+        if (h == halves) break;
         const int j = h * 32 + lane;
         if (j < a.k) {
             float w = s[h];
@@ -259,7 +268,11 @@ template <typename T, int V, int SCORING>
 epd_status_t launch_route(RouteArgs a, cudaStream_t st) {
     a.vec = chunked<T, V>(a.logits, a.E);
     a.bias_vec = a.vec && Layout<T, V>::C % 4 == 0 && a.bias && aligned16(a.bias);
-    const size_t smem = a.keep < a.groups ? (size_t)kRouteWarps * (a.E + EPD_MAX_GROUPS) * sizeof(float) : 0;
+    const int width = a.size / Layout<T, V>::C;
+    a.run = -1;
+    if (width * Layout<T, V>::C == a.size && (width & (width - 1)) == 0 && width <= 32 && a.groups <= 32)
+        for (a.run = 0; width >> a.run > 1;) ++a.run;
+    const size_t smem = a.keep < a.groups && a.run < 0 ? (size_t)kRouteWarps * (a.E + EPD_MAX_GROUPS) * sizeof(float) : 0;
     const int grid = (a.T + kRouteWarps - 1) / kRouteWarps;
     auto kernel = route_kernel<T, V, SCORING>;
     if (smem > 48 * 1024) {

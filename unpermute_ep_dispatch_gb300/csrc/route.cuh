@@ -43,6 +43,13 @@ __device__ __forceinline__ float clean_logit(float l, bool &bad) {
     return l;
 }
 
+// The larger one, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // Lane-interleaved row: chunks of C elements, chunk q of lane l being elements
 // (32 q + l) C .. + C - 1, so that element i of a lane is expert index_of<C>(i) and a chunk is
 // one load of at most 16 bytes.
@@ -71,12 +78,20 @@ __device__ __forceinline__ void load_row(const T *row, int E, bool vec, int lane
                     *reinterpret_cast<uint32_t *>(v) = *reinterpret_cast<const uint32_t *>(row + e0);
             }
 #pragma unroll
-            for (int c = 0; c < L::C; ++c) l[q * L::C + c] = e0 < E ? clean_logit(to_f32(v[c]), bad) : -CUDART_INF_F;
+            for (int c = 0; c < L::C; ++c) l[q * L::C + c] = e0 < E ? to_f32(v[c]) : -CUDART_INF_F;
         } else {
 #pragma unroll
             for (int c = 0; c < L::C; ++c)
-                l[q * L::C + c] = e0 + c < E ? clean_logit(to_f32(row[e0 + c]), bad) : -CUDART_INF_F;
+                l[q * L::C + c] = e0 + c < E ? to_f32(row[e0 + c]) : -CUDART_INF_F;
         }
+    }
+    // one comparison a lane tells whether any of its logits has to be replaced
+    float top = l[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) top = max_nan(top, l[i]);
+    if (!(top < CUDART_INF_F)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) l[i] = clean_logit(l[i], bad);
     }
 }
 
