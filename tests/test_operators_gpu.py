@@ -465,6 +465,78 @@ def test_wgrad(counts, K, N, with_dbias):
             assert ((db[e].double() - a.sum(0)).abs() <= (c + 1) * 2.0 ** -23 * a.abs().sum(0)).all()
 
 
+# Few tiles and a long reduction: several pairs of blocks share it.
+FEW = dict(one=[1], sixteen=[16], two=[40, 7], wide=[130, 3], rows=[200], full=[256], gap=[3, 0, 90], eight=[1] * 8,
+           second=[257])
+
+
+@pytest.mark.parametrize("counts", FEW)
+@pytest.mark.parametrize("K,N,act", [(1544, 200, "none"), (4096, 512, "gelu"), (2000, 136, "swiglu"), (3592, 2304, "none")])
+def test_shared_reduction_bf16(counts, K, N, act):
+    run_forward(FEW[counts], K, N, act, seed=K, bias=act != "none", residual=act == "swiglu", preact=act == "gelu", gaps=1)
+
+
+@pytest.mark.parametrize("counts", FEW)
+@pytest.mark.parametrize("K,N,act", [(1536, 200, "none"), (4096, 512, "gelu"), (2176, 128, "swiglu"), (3200, 2304, "none")])
+def test_shared_reduction_fp8(counts, K, N, act):
+    run_forward(FEW[counts], K, N, act, seed=K, fp8=True, bias=act != "none", residual=act == "swiglu",
+                preact=act == "gelu", gaps=1)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_shared_reduction_of_rectangles(fp8):
+    run_forward([3, 0, 20], 2048, 256, "swiglu", fp8=fp8, rect=24, bias=True)
+
+
+@pytest.mark.parametrize("counts", FEW)
+@pytest.mark.parametrize("K,N,act", [(200, 1544, "none"), (512, 4104, "swiglu"), (136, 2000, "silu"), (2304, 3592, "none")])
+def test_shared_reduction_dgrad(counts, K, N, act):
+    E, start, M, KZ, dy, x, w, z, real, dead = backward_case(FEW[counts], K, N, act, K, 1)
+    status = epd.new_status()
+    dx = torch.full((M, KZ), 7.0, dtype=torch.bfloat16, device=DEV)
+    epd.ep_expert_matmul_dgrad(dy, w, i32(FEW[counts]), status, expert_start_loc=i32(start), activation=act,
+                               preact=None if act == "none" else z, dx=dx)
+    check_ok(status)
+    d = torch.zeros(M, K, dtype=torch.float64, device=DEV)
+    mag = torch.zeros_like(d)
+    for e, (s, c) in enumerate(zip(start, FEW[counts])):
+        d[s:s + c] = dy[s:s + c].double() @ w[e].double()
+        mag[s:s + c] = dy[s:s + c].double().abs() @ w[e].double().abs()
+    zz = z.double().requires_grad_()
+    a = act64(zz, act)
+    slope, = torch.autograd.grad(a, zz, torch.where(dead.unsqueeze(1), 0.0, d)) if act != "none" else (d,)
+    big, = torch.autograd.grad(act64(zz, act), zz, torch.ones_like(a)) if act != "none" else (torch.ones_like(d),)
+    m2 = torch.cat([mag, mag], 1) if act == "swiglu" else mag
+    d2 = torch.cat([d, d], 1) if act == "swiglu" else d
+    tol = (N + 16) * 2.0 ** -23 * m2 * big.abs() + 2 ** -8 * slope.abs() + 16 * 2.0 ** -23 * d2.abs() * (1 + torch.cat([z, z], 1)[:, :KZ].double().abs()) ** 2 + 1e-30
+    assert ((dx[real].double() - slope[real]).abs() <= tol[real]).all()
+    assert (dx[dead] == 7).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("N", [256, 2304])
+def test_shared_reduction_with_more_tiles_than_clusters(fp8, N):
+    """Regions may lie over one another, and then there are more tiles than rows in the buffer
+    account for; both experts have the same weights, so that the order of their writes is no matter."""
+    x, w, cnt, kw, real, y, z, ty, tz = forward_case([300], 4096, N, "none", 11, fp8=fp8)
+    kw |= dict(expert_start_loc=i32([0, 0]))
+    if fp8:
+        kw["w_scale"] = kw["w_scale"].repeat(2, 1, 1)
+    got = []
+    for _ in range(2):
+        status = epd.new_status()
+        got.append(epd.ep_expert_matmul(x, w.repeat(2, 1, 1), i32([300, 300]), status, **kw)[0])
+        check_ok(status)
+        assert ((got[-1].double() - y).abs() <= ty)[real].all()
+    again = []
+    for _ in range(2):
+        status = epd.new_status()
+        again.append(epd.ep_expert_matmul(x, w, cnt, status, **(kw | dict(expert_start_loc=i32([0])) | (
+            dict(w_scale=kw["w_scale"][:1].contiguous()) if fp8 else {})))[0])
+        check_ok(status)
+    assert torch.equal(again[0][real], again[1][real]), "the parts are added in a fixed order"
+
+
 def test_backward_rectangles():
     counts, rect = [3, 0, 70, 128], 130
     E, start, M, KZ, dy, x, w, z, real, dead = backward_case(counts, 64, 96, "silu", 1, 0, rect)

@@ -20,15 +20,26 @@ __device__ __forceinline__ uint64_t global_ns() {
     return t;
 }
 
+// CLUSTER: what the arrivals of other blocks released is visible after it.
+template <bool CLUSTER>
 __device__ __forceinline__ bool mbar_try_pipe(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
+    if (CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
     return ok != 0;
 }
 
@@ -37,12 +48,13 @@ __device__ __forceinline__ bool mbar_try_pipe(uint32_t bar, uint32_t parity) {
 // is wrong, and the kernel returns with an error instead of hanging. The waits are at block
 // scope: what they order is the work of the TMA and tensor-core units, and a wait that
 // acquires at cluster scope costs hundreds of cycles (dense 8192^3: 1558 us with, 661 us
-// without).
+// without); the few that read another block's shared memory do.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_pipe(uint32_t bar, uint32_t parity) {
-    if (mbar_try_pipe(bar, parity)) return true;
+    if (mbar_try_pipe<CLUSTER>(bar, parity)) return true;
     uint64_t t0 = 0;
     for (uint32_t i = 1; i < (1u << 24); ++i) {
-        if (mbar_try_pipe(bar, parity)) return true;
+        if (mbar_try_pipe<CLUSTER>(bar, parity)) return true;
         if ((i & 255u) == 0) {
             const uint64_t t = global_ns();
             if (t0 == 0) t0 = t;
@@ -62,6 +74,21 @@ __device__ __forceinline__ bool elect_one() {
         : "=r"(ok));
     return ok != 0;
 }
+
+__device__ __forceinline__ uint32_t cluster_blocks() {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return n;
+}
+
+// Arrives on a barrier of any block of the cluster (an address from map_to_rank) and releases
+// what this thread has seen and written to the block that waits for it.
+__device__ __forceinline__ void mbar_release_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Orders this thread's accesses to shared memory before later ones of the TMA unit.
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Arrivals on a barrier of either block of the pair (an address from map_to_rank).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
@@ -173,6 +200,13 @@ __device__ __forceinline__ float4 lds16f(uint32_t addr) {
     return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 
+// From the shared memory of any block of the cluster.
+__device__ __forceinline__ float4 ld_cluster16f(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void sts16(uint32_t addr, const uint4 &v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -227,11 +261,12 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
     }
 }
 
-// Arrives on `bar` of both blocks once every earlier mma of this thread has completed.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+// Arrives on `bar` of the blocks in `blocks`, the pair's two, once every earlier mma of this thread
+// has completed.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t blocks) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
+        "h"(blocks)
         : "memory");
 }
 

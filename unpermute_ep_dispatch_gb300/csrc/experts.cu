@@ -32,7 +32,10 @@
 // 1930 TFLOP/s, as cuBLAS here) and with fewer the 64 bytes a clock that come into an SM, since
 // a step of n = 192 columns brings 28 KiB for 384 cycles of mma; wgrad its output, 4.0 TB/s
 // being what this memory takes in writes alone; e4m3 with few rows the weights' way from memory
-// and with many the sums, of which a step has 256 cycles to its mma's 512.
+// and with many the sums, of which a step has 256 cycles to its mma's 512. A lone tile is bound by
+// its two SMs' 64 bytes a clock as well, so a handful of tiles with a long reduction is cut along
+// it: a cluster of up to four pairs shares a tile and its first pair adds up the parts' sums, read
+// from the others' shared memory in a fixed order (kSharedSteps).
 //
 // Warps: the epilogue's 8 (e4m3: 16), the producer, which walks the tiles, publishes them to
 // the others and feeds TMA, one that issues the mma (in the pair's first block), and two helpers
@@ -79,11 +82,20 @@ constexpr int kRing = 4;                        // tiles published ahead
 constexpr int kCuts = 18;                       // wgrad's boxes: 64, 32, 16 and 1 to 15 rows
 constexpr int kGroupTiles = 8;                  // row tiles that share a pass over the features
 
+constexpr int kStages = 6;
+
+// Where few tiles leave most SMs idle, up to four pairs share a tile's reduction, which costs
+// some 1.2 us for the larger cluster and the sums' way between blocks, and takes 0.16 us a step
+// (e4m3 0.24) off as many steps as the others do. It is done from 96 / parts steps on (e4m3 48 /
+// parts). bf16, one expert of 16 rows and 512 features, in four parts and in one: K = 1024 6.4 and
+// 5.7 us, 1536 6.7 and 6.9, 4096 8.5 and 13.4; 64 rows, 7168 features, in two and in one: K = 2048
+// 10.9 and 10.3 us, 3200 13.6 and 14.1. e4m3, the same: 1024 6.4 and 6.0, 1536 6.9 and 7.1, 4096 7.8
+// and 11.7; in two: 2048 9.4 and 9.2, 3200 11.0 and 11.8.
 template <bool FP8>
-constexpr int kStagesOf = 6;
+constexpr int kSharedSteps = FP8 ? 48 : 96;
 
 template <bool FP8>
-constexpr int kSmemOf = kStagesOf<FP8> *kStageBytes + kEpiWarpsOf<FP8> * kStagingOf<FP8> + (FP8 ? kScaleBytes : 0) + kTailBytes;
+constexpr int kSmemOf = kStages * kStageBytes + kEpiWarpsOf<FP8> * kStagingOf<FP8> + (FP8 ? kScaleBytes : 0) + kTailBytes;
 
 struct ExpertArgs {
     epd_expert_rows_t rows;
@@ -142,6 +154,8 @@ struct alignas(16) Tile {
     int feat0, row0, rows, n;
     int steps;  // of the reduction
     int across; // e4m3: the features are the M operand
+    int step0;  // first step of this pair's
+    int part, parts;  // of the reduction: this pair's, and how many pairs share it
 };
 
 // The producer's tiles, as the other warps of the block get them: a ring in shared memory.
@@ -236,7 +250,19 @@ struct Walker {
             t.n = feat_step == 128 ? 256 : (min(256, p.N - t.feat0) + 31) & ~31;
         const int red = MODE == kForward ? p.K : MODE == kDgrad ? p.N : t.count;
         t.steps = (red + STEP - 1) / STEP;
+        t.step0 = t.part = 0;
+        t.parts = 1;
         return true;
+    }
+
+    // Leaves part `part` of `parts` of the tile's reduction, in whole groups of staged scales.
+    __device__ void cut(Tile &t, int part, int parts) const {
+        constexpr int kUnit = FP8 ? kScaleGroup : 1;
+        const int units = (t.steps + kUnit - 1) / kUnit;
+        t.step0 = part * units / parts * kUnit;
+        t.steps = min(t.steps, (part + 1) * units / parts * kUnit) - t.step0;
+        t.part = part;
+        t.parts = parts;
     }
 };
 
@@ -380,6 +406,37 @@ __device__ __forceinline__ bool swap_half(uint32_t mine, uint32_t other, uint32_
         ok = ok && mbar_wait_pipe(bar, 1);
     }
     return __all_sync(0xffffffffu, ok);
+}
+
+// A reduction that several pairs of a cluster share: 32 sums a lane are left in the block's own
+// shared memory (its stages, which nothing fills any more) and fetched by the first pair.
+template <typename F>
+__device__ __forceinline__ void park(uint32_t at, F sum) {
+    at += (threadIdx.x & 31) * 16;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        sts16(at + i * 512, make_uint4(__float_as_uint(sum(4 * i)), __float_as_uint(sum(4 * i + 1)),
+                                       __float_as_uint(sum(4 * i + 2)), __float_as_uint(sum(4 * i + 3))));
+}
+
+// Adds the other parts' sums, in the parts' order.
+template <typename F>
+__device__ __forceinline__ void add_parked(uint32_t at, int rank, int parts, F sum) {
+    at += (threadIdx.x & 31) * 16;
+    for (int s = 1; s < parts; ++s) {
+        const uint32_t from = map_to_rank(at, 2 * s + rank);
+#pragma unroll
+        for (int i0 = 0; i0 < 8; i0 += 4) {
+            float4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = ld_cluster16f(from + (i0 + i) * 512);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 4 * (i0 + i);
+                sum(r) += v[i].x, sum(r + 1) += v[i].y, sum(r + 2) += v[i].z, sum(r + 3) += v[i].w;
+            }
+        }
+    }
 }
 
 // Element r of fragments f[h] in the words that Ahead::turn gives.
@@ -669,11 +726,10 @@ __device__ __forceinline__ void sum_bias(const ExpertArgs &p, int worker, int wo
     }
 }
 
-template <int MODE, bool FP8, bool GATED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
+template <int MODE, bool FP8, bool GATED, bool SPLIT>
+__global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
     expert_kernel(const __grid_constant__ Maps<MODE> maps, const ExpertArgs p) {
     constexpr bool kHalf = GATED && MODE == kForward;  // half of a block's 128 lanes are up features
-    constexpr int kStages = kStagesOf<FP8>;
     // accumulators: two of 256 columns; e4m3, which uses one a step, four of 128 where that is enough
     constexpr int kAccs = FP8 ? 4 : 2;
     constexpr int kEpiWarps = kEpiWarpsOf<FP8>;
@@ -691,14 +747,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<MODE, FP8
     uint64_t *bars = reinterpret_cast<uint64_t *>(after);
     constexpr int kEmpty = kStages, kAccFull = 2 * kStages, kAccEmpty = kAccFull + kAccs,
                   kScFull = kAccEmpty + kAccs, kScEmpty = kScFull + 2, kTileFull = kScEmpty + 2, kTileEmpty = kTileFull + kRing,
-                  kSwap = kTileEmpty + kRing, kSlot = kSwap + kEpiWarps / 2;
+                  kSwap = kTileEmpty + kRing, kParked = kSwap + kEpiWarps / 2, kFetched = kParked + 1, kSlot = kFetched + 1;
     static_assert((kSlot + 1) * 8 + kRing * sizeof(Tile) <= kTailBytes, "the barriers fit");
     const uint32_t base = smem_addr(smem), bar0 = smem_addr(bars);
     const uint32_t full = bar0, empty = bar0 + 8 * kEmpty, acc_full = bar0 + 8 * kAccFull,
                    acc_empty = bar0 + 8 * kAccEmpty, sc_full = bar0 + 8 * kScFull, sc_empty = bar0 + 8 * kScEmpty;
 
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
-    const int rank = (int)cluster_ctarank();
+    // this block's place in its pair, and the pair's in a cluster that shares a reduction
+    const int in_cluster = (int)cluster_ctarank();
+    const int rank = SPLIT ? in_cluster & 1 : in_cluster, lead = SPLIT ? in_cluster - rank : 0;
+    const int part = SPLIT ? lead / 2 : 0, parts = SPLIT ? (int)cluster_blocks() / 2 : 1;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(bars + i, 2);           // both blocks' producers
@@ -717,6 +776,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<MODE, FP8
             mbar_init(bars + kTileEmpty + i, kEpiWarps + (rank == 0) + (FP8 ? kHelpers : 0));
         }
         for (int i = 0; i < kEpiWarps / 2; ++i) mbar_init(bars + kSwap + i, 64);
+        if (SPLIT) {
+            mbar_init(bars + kParked, (parts - 1) * kEpiWarps);
+            mbar_init(bars + kFetched, kEpiWarps);
+        }
         mbar_init_fence();
         for (int i = 0; i < Maps<MODE>::kM; ++i) tma_prefetch_map(&maps.m[i]);
         for (int i = 0; i < Maps<MODE>::kN; ++i) tma_prefetch_map(&maps.n[i]);
@@ -737,14 +800,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<MODE, FP8
         // e4m3: 640 threads launch with 96 registers each, 61440 in all: 512 x 104 + 128 x 64
         if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == kProducerWarp) {
-            const uint32_t lead_full = map_to_rank(full, 0);
+            const uint32_t lead_full = map_to_rank(full, lead);
             const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+            // a cluster's first tile is shared by its pairs; should there be more tiles than
+            // clusters, the others are not
+            const int first = SPLIT ? pair / parts : pair;
             Walker<MODE, kStep, FP8> walk(p, kFeatStep);
             int stage = 0, issued = 0;
             uint32_t parity = 1;
-            for (int tile = pair; ok; tile += pairs) {
+            for (int tile = first; ok; tile = SPLIT && tile == first ? pairs / parts + pair : tile + pairs) {
                 Tile t;
                 const bool more = walk.next(tile, t);
+                if (SPLIT && more) {
+                    if (tile == first) {
+                        walk.cut(t, part, parts);
+                    } else if (part > 0) {  // the stages are free again once the sums are fetched
+                        if (!(ok = mbar_wait_pipe<true>(bar0 + 8 * kFetched, 0))) break;
+                        fence_proxy_async();
+                    }
+                }
                 if (!(ok = mbar_wait_pipe(ring.empty + 8 * ring.at, ring.parity ^ 1))) break;
                 if (elect_one()) {
                     if (!more) t.e = -1;
@@ -766,7 +840,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<MODE, FP8
                     // operand M first; a has the features, b the rows
                     const uint32_t a_at = base + (t.across ? 0 : kOperandBytes);
                     const uint32_t b_at = base + (t.across ? kOperandBytes : 0);
-                    for (int k = 0; k < t.steps; ++k) {
+                    for (int i = 0; i < t.steps; ++i) {
+                        const int k = SPLIT ? t.step0 + i : i;
                         if (!(ok = mbar_wait_pipe(empty + 8 * stage, parity))) break;
                         const uint32_t a = a_at + stage * kStageBytes, b = b_at + stage * kStageBytes;
                         const uint32_t bar = lead_full + 8 * stage;
@@ -829,6 +904,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<MODE, FP8
                 if (++stage == kStages) stage = 0, parity ^= 1;
             }
         } else if (warp == kMmaWarp) {
+            const uint16_t pair_mask = (uint16_t)(3 << lead);
             const uint64_t desc_a = smem_desc(base, 8192), desc_b = smem_desc(base + kOperandBytes, 8192);
             int stage = 0, acc = 0, was = -1;
             uint32_t parity = 0, parities = (1u << kAccs) - 1;  // of each accumulator's next release
@@ -863,9 +939,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<MODE, FP8
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
                             if (q < quarters) mma_pair<FP8>(d, da + q * kA, db + q * kB, desc, !(fresh && q == 0));
-                        mma_commit_pair(empty + 8 * st);
+                        mma_commit_pair(empty + 8 * st, pair_mask);
                         if (last) {
-                            mma_commit_pair(acc_full + 8 * c);
+                            mma_commit_pair(acc_full + 8 * c, pair_mask);
                             if (++c == accs) c = 0;
                         }
                         if (++st == kStages) st = 0, ph ^= 1;
@@ -902,9 +978,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<MODE, FP8
                 if (b1 >= blocks) b1 = b0;
                 const float *w0 = p.w_scale + ((int64_t)t.e * blocks + b0) * C;
                 const float *w1 = p.w_scale + ((int64_t)t.e * blocks + b1) * C;
+                const int end = t.step0 + t.steps;
                 const int skip = t.across ? 0 : rank * 128, rows = t.rows - skip;
                 const float *xs = p.x_scale + ((int64_t)t.start + t.row0 + skip) * p.srow + t.e * p.sexp;
-                for (int g = 0; g < t.steps; g += kScaleGroup) {
+                for (int g = t.step0; g < end; g += kScaleGroup) {
                     float sw[2][kScaleGroup], sx[2][kScaleGroup];
 #pragma unroll
                     for (int k = 0; k < kScaleGroup; ++k) {
@@ -953,7 +1030,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<MODE, FP8
         if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         constexpr int kShare = kEpiWarps / 4;  // warps that share the columns of 32 lanes
         const int quadrant = warp & 3, share = warp >> 2;
-        const uint32_t lead_empty = map_to_rank(acc_empty, 0);
+        const uint32_t lead_empty = map_to_rank(acc_empty, lead);
+        // the end of a part: the first pair waits for the others' sums, they for nothing
+        auto parked = [&]() { return mbar_wait_pipe<true>(bar0 + 8 * kParked, 0); };
+        auto hand_over = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_release_cluster(map_to_rank(bar0 + 8 * kParked, rank));
+        };
+        auto fetched = [&]() {
+            __syncwarp();
+            if (lane > 0 && lane < parts) mbar_release_cluster(map_to_rank(bar0 + 8 * kFetched, 2 * lane + rank));
+        };
         const uint32_t my_tmem = tmem + ((uint32_t)(quadrant * 32) << 16);
         uint32_t parities = 0;  // of each accumulator's next result
         if (FP8) {
@@ -1003,6 +1090,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<MODE, FP8
                         }
                     }
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    if (SPLIT && ring.tile().parts > 1) {
+                        const uint32_t at = base + warp * 4096;
+                        auto sum = [&](int r) -> float & { return acc[r >> 4][r & 15]; };
+                        if (ring.tile().part > 0) {
+                            if (own) park(at, sum);
+                            hand_over();
+                            ring.drop();
+                            continue;
+                        }
+                        if (!(ok = __all_sync(0xffffffffu, parked()))) break;
+                        if (own) add_parked(at, rank, parts, sum);
+                        fetched();
+                    }
                     Output<MODE, GATED, kStagedOf<FP8>> out(p, staging, bar0 + 8 * kSwap, warp);
                     out.begin(ring.tile(), rank, quadrant);
                     if (own) {
@@ -1053,6 +1153,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<MODE, FP8
                     }
                 }
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                if (SPLIT && ring.tile().parts > 1) {
+                    const uint32_t at = base + warp * 8192;
+                    auto gate = [&](int r) -> float & { return acc[0][r]; };
+                    auto rest = [&](int r) -> float & { return acc[1][r]; };
+                    if (ring.tile().part > 0) {
+                        if (blocks > 0) park(at, gate), park(at + 4096, rest);
+                        hand_over();
+                        ring.drop();
+                        continue;
+                    }
+                    if (!(ok = __all_sync(0xffffffffu, parked()))) break;
+                    if (blocks > 0) add_parked(at, rank, parts, gate), add_parked(at + 4096, rank, parts, rest);
+                    fetched();
+                }
                 if (blocks > 0) finish_rows<GATED>(p, ring.tile(), rank * 128 + quadrant * 32, share * 32,
                                                    staging + warp * kStagingOf<FP8>, acc);
                 ring.drop();
@@ -1065,13 +1179,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<MODE, FP8
                 out.begin(t, rank, quadrant);
                 const int chunks = t.n / 32;
                 const bool any = t.steps > 0;  // else wgrad of an expert without rows
+                const bool shared = SPLIT && t.parts > 1, leaves = shared && t.part > 0;
                 ring.drop();
-                if (share < chunks) out.fetch(share * 32);
+                if (share < chunks && !leaves) out.fetch(share * 32);
                 if (any) {
                     if (!(ok = mbar_wait_pipe(acc_full + 8 * buf, (parities >> buf) & 1))) break;
                     parities ^= 1u << buf;
                     tcgen05_fence_after();
                 }
+                if (shared && !leaves && !(ok = __all_sync(0xffffffffu, parked()))) break;
                 for (int ch = share; ch < chunks; ch += kShare) {
                     Frag f;
                     if (any) {
@@ -1089,8 +1205,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsOf<MODE, FP8
 #pragma unroll
                             for (int r = 0; r < 16; ++r) f[h][r] = 0.0f;
                     }
+                    if (shared) {
+                        const uint32_t at = base + (ch * 4 + quadrant) * 4096;
+                        auto sum = [&](int r) -> float & { return f[r >> 4][r & 15]; };
+                        if (leaves) {
+                            park(at, sum);
+                            continue;
+                        }
+                        add_parked(at, rank, parts, sum);
+                    }
                     out.finish(f, ch * 32, (ch + kShare) * 32);
                 }
+                if (leaves) hand_over();
+                if (shared && !leaves) fetched();
                 if (any) {
                     tcgen05_fence_before();
                     __syncwarp();
@@ -1151,42 +1278,64 @@ bool encode_rows(CUtensorMap *map, bool fp8, const void *at, int64_t count, int6
     return encode(map, fp8, 2, at, size, stride, box);
 }
 
-template <int MODE, bool FP8, bool GATED>
-epd_status_t launch(const Maps<MODE> &maps, const ExpertArgs &p, cudaStream_t stream) {
-    constexpr int kSmem = kSmemOf<FP8>;
-    auto kernel = expert_kernel<MODE, FP8, GATED>;
-    static std::atomic<int> cached[64];  // resident pairs of blocks, per device
+// Clusters of `parts` pairs that the device holds at a time (0 where a query fails).
+template <int MODE, bool FP8, bool GATED, bool SPLIT>
+epd_status_t resident(int parts, int &clusters) {
+    static std::atomic<int> cached[3][64];  // one more than the answer, per device
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return record_cuda_error();
-    std::atomic<int> &slot = cached[dev >= 0 && dev < 64 ? dev : 0];
-    int pairs = slot.load(std::memory_order_relaxed);
-    if (pairs == 0 || dev >= 64) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-            return record_cuda_error();
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(sm_count() / 2 * 2));
-        cfg.blockDim = dim3(kThreadsOf<MODE, FP8>);
-        cfg.dynamicSmemBytes = kSmem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg) != cudaSuccess || pairs < 1) {
-            cudaGetLastError();
-            pairs = 1;
-        }
-        slot.store(pairs, std::memory_order_relaxed);
+    std::atomic<int> &slot = cached[parts / 2][dev >= 0 && dev < 64 ? dev : 0];
+    clusters = slot.load(std::memory_order_relaxed) - 1;
+    if (clusters >= 0 && dev < 64) return EPD_OK;
+    auto kernel = expert_kernel<MODE, FP8, GATED, SPLIT>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOf<FP8>) != cudaSuccess)
+        return record_cuda_error();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sm_count() / (2 * parts) * (2 * parts)));
+    cfg.blockDim = dim3(kThreadsOf<MODE, FP8>);
+    cfg.dynamicSmemBytes = kSmemOf<FP8>;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * parts;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess || clusters < 0) {
+        cudaGetLastError();
+        clusters = 0;
     }
+    slot.store(clusters + 1, std::memory_order_relaxed);
+    return EPD_OK;
+}
+
+template <int MODE, bool FP8, bool GATED>
+epd_status_t launch(const Maps<MODE> &maps, const ExpertArgs &p, cudaStream_t stream) {
     const int features = MODE == kForward ? p.N : p.K;
     const int64_t feat_tiles = (features + (GATED && MODE == kForward ? 127 : 255)) / (GATED && MODE == kForward ? 128 : 256);
     const int64_t cap = p.rows.capacity_rows, E = p.rows.num_experts;
-    const int64_t row_tiles =
-        MODE == kWgrad ? (int64_t)(p.N + kTileRows - 1) / kTileRows * E : cap / kTileRows + (E < cap ? E : cap);
-    const int64_t most = feat_tiles * row_tiles;
+    const int64_t row_tiles = MODE == kWgrad ? (int64_t)(p.N + kTileRows - 1) / kTileRows * E
+                              : p.rows.expert_start_loc ? cap / kTileRows + (E < cap ? E : cap)
+                                                        : (p.rows.rows_per_expert + kTileRows - 1) / kTileRows * E;
+    const int64_t most = row_tiles > 0 ? feat_tiles * row_tiles : 1;
     if (most > INT32_MAX / 2) return EPD_ERR_UNSUPPORTED;
-    return launch_pdl(kernel, 2 * (int)(most < pairs ? most : pairs), kThreadsOf<MODE, FP8>, kSmem, stream, maps, p);
+    constexpr int kThreads = kThreadsOf<MODE, FP8>, kSmem = kSmemOf<FP8>;
+    int clusters;
+    if (MODE != kWgrad) {
+        const int steps = ((MODE == kForward ? p.K : p.N) + (FP8 ? 127 : 63)) / (FP8 ? 128 : 64);
+        for (int parts = 4; parts > 1; parts /= 2) {
+            if (steps * parts < kSharedSteps<FP8> || most * parts > sm_count() / 2) continue;
+            const epd_status_t rc = resident<MODE, FP8, GATED, MODE != kWgrad>(parts, clusters);
+            if (rc != EPD_OK) return rc;
+            if (most <= clusters)
+                return launch_pdl_cluster(expert_kernel<MODE, FP8, GATED, MODE != kWgrad>, 2 * parts * (int)most, kThreads,
+                                          kSmem, 2 * parts, stream, maps, p);
+        }
+    }
+    const epd_status_t rc = resident<MODE, FP8, GATED, false>(1, clusters);
+    if (rc != EPD_OK) return rc;
+    if (clusters < 1) clusters = 1;
+    return launch_pdl_cluster(expert_kernel<MODE, FP8, GATED, false>, 2 * (int)(most < clusters ? most : clusters), kThreads,
+                              kSmem, 2, stream, maps, p);
 }
 
 bool rows_ok(const epd_expert_rows_t *r) {
