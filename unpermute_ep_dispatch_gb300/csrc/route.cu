@@ -7,7 +7,7 @@
 // pick a new pass over its values, for those that come after the pick in the order of picks.
 //
 // What bounds it: a row of 256 logits is 1 KiB, 2.7 us for 16384 rows at the copy rate; its
-// instructions (742 a token with a bias and 4 of 8 groups, 466 for plain softmax; two thirds of
+// instructions (745 a token with a bias and 4 of 8 groups, 472 for plain softmax; two thirds of
 // them compares, selects and maxima at half rate) take 14.0 and 9.5 us back to back in a graph.
 // Rows of up to 256 logits are held to 32 registers, so that sixteen blocks fit an SM and a call
 // starts under the end of the one before: 4097 rows 5.6 us from 7.2 in a graph, 16384 the same.
