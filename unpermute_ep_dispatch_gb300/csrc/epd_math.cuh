@@ -32,19 +32,45 @@ __device__ __forceinline__ float sigmoid_f32(float x) {
     return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x)));
 }
 
-constexpr float kSqrtHalf = 0.70710678118654752440f;
 constexpr float kInvSqrt2Pi = 0.39894228040143267794f;
+constexpr float kLog2e = 1.4426950408889634f;
 
-__device__ __forceinline__ float gelu_cdf(float z) { return 0.5f * (1.0f + erff(z * kSqrtHalf)); }
-
-// The sigmoid of the activations, by the hardware's exponential and reciprocal: within a few
-// 2^-22 of its value, far below the bf16 it is rounded to (and 0 where it is below 2^-126).
-__device__ __forceinline__ float fast_sigmoid(float x) {
-    constexpr float kLog2e = 1.4426950408889634f;
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -kLog2e));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+// The hardware's 2^x and 1/x, within 2^-22 and 2^-23 of their values; what is below 2^-126 is 0.
+__device__ __forceinline__ float fast_exp2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The sigmoid of the activations: within a few 2^-22 of its value, far below the bf16 it is
+// rounded to.
+__device__ __forceinline__ float fast_sigmoid(float x) { return fast_rcp(1.0f + fast_exp2(x * -kLog2e)); }
+
+// The normal distribution function, and e = exp(-z^2 / 2), which its derivative is a multiple of.
+// Below zero it is exp(-z^2 / 2) erfcx(|z| / sqrt 2) / 2, and the scaled complementary error
+// function over t = 1 / (1 + 9/32 |z|) is smooth for t in (0, 1]: a polynomial fitted to the least
+// relative error (1.5e-7) takes it, without branches and with one exponential for both (dgrad into
+// GELU, 24 experts of 28 rows, 904 x 520: 7.9 us, with erff and expf 8.9).
+// Absolute error 3e-7, relative 1e-6 for z > -3 and 3e-6 for z > -8.
+__device__ __forceinline__ float normal_cdf(float z, float &e) {
+    const float t = fast_rcp(fmaf(fabsf(z), 0.28125f, 1.0f));
+    e = fast_exp2(z * z * (-0.5f * kLog2e));
+    float q = 0.02489628456532955f;
+    q = fmaf(q, t, -0.09263245016336441f);
+    q = fmaf(q, t, 0.08888789266347885f);
+    q = fmaf(q, t, -0.004765740130096674f);
+    q = fmaf(q, t, 0.07183780521154404f);
+    q = fmaf(q, t, 0.08392227441072464f);
+    q = fmaf(q, t, 0.1034524142742157f);
+    q = fmaf(q, t, 0.11219891905784607f);
+    q = fmaf(q, t, 0.11220253258943558f);
+    const float tail = t * e * q;
+    return z < 0.0f ? tail : 1.0f - tail;
 }
 
 // act(z) of the ungated activations.
@@ -52,7 +78,10 @@ template <int ACT>
 __device__ __forceinline__ float activate(float z) {
     if (ACT == EPD_ACT_RELU) return z < 0.0f ? 0.0f : z;  // keeps NaN
     if (ACT == EPD_ACT_SILU) return z * fast_sigmoid(z);
-    if (ACT == EPD_ACT_GELU) return z * gelu_cdf(z);
+    if (ACT == EPD_ACT_GELU) {
+        float e;
+        return z * normal_cdf(z, e);
+    }
     return z;
 }
 
@@ -64,7 +93,11 @@ __device__ __forceinline__ float activate_grad(float z) {
         const float s = fast_sigmoid(z);
         return s * (1.0f + z * (1.0f - s));
     }
-    if (ACT == EPD_ACT_GELU) return gelu_cdf(z) + z * (kInvSqrt2Pi * expf(-0.5f * z * z));
+    if (ACT == EPD_ACT_GELU) {
+        float e;
+        const float cdf = normal_cdf(z, e);
+        return fmaf(z * e, kInvSqrt2Pi, cdf);
+    }
     return 1.0f;
 }
 
