@@ -67,39 +67,51 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_picks_kernel(Rou
     } else {
         for (int e = lane; e < a.E; e += 32) from_f32(out[e], 0.0f);
     }
+    const bool two = a.k > 32;
     if (SCORING == EPD_SCORE_SOFTMAX) {
         const float m = warp_max(fmaxf(s[0], s[1]));
-#pragma unroll
-        for (int h = 0; h < 2; ++h) s[h] = m > -CUDART_INF_F ? expf(s[h] - m) : 0.0f;
+        s[0] = m > -CUDART_INF_F ? expf(s[0] - m) : 0.0f;
+        if (two) s[1] = m > -CUDART_INF_F ? expf(s[1] - m) : 0.0f;
     } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) s[h] = sigmoid_f32(s[h]);
+        s[0] = sigmoid_f32(s[0]);
+        if (two) s[1] = sigmoid_f32(s[1]);
     }
+    if (!two) s[1] = 0.0f;
     if (a.renorm) {
         const float sum = warp_sum(s[0] + s[1]);
         const float rs = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
         float ds[2] = {0.0f, 0.0f};
-        for (int i = 0; i < a.k; ++i) {
-            const float gi = __shfl_sync(kFull, i < 32 ? g[0] : g[1], i & 31);
-            const float pi = __shfl_sync(kFull, i < 32 ? s[0] : s[1], i & 31) * rs;
+        const float p0 = s[0] * rs, p1 = s[1] * rs;
+        for (int i = 0; i < min(a.k, 32); ++i) {
+            const float gi = __shfl_sync(kFull, g[0], i), pi = __shfl_sync(kFull, p0, i);
+            ds[0] += (g[0] - gi) * pi;
+            if (two) ds[1] += (g[1] - gi) * pi;
+        }
+        for (int i = 32; i < a.k; ++i) {
+            const float gi = __shfl_sync(kFull, g[1], i - 32), pi = __shfl_sync(kFull, p1, i - 32);
             ds[0] += (g[0] - gi) * pi;
             ds[1] += (g[1] - gi) * pi;
         }
         g[0] = ds[0] * rs;
         g[1] = ds[1] * rs;
     }
-    // an expert picked more than once: every one of its picks has the sum, in the picks' order
-    float d[2] = {0.0f, 0.0f};
-    for (int i = 0; i < a.k; ++i) {
-        const int e = __shfl_sync(kFull, i < 32 ? pick[0] : pick[1], i & 31);
-        const float v = __shfl_sync(kFull, i < 32 ? g[0] : g[1], i & 31);
-        if (e == pick[0]) d[0] += v;
-        if (e == pick[1]) d[1] += v;
+    const uint32_t same = __match_any_sync(kFull, pick[0]);
+    if (two || __any_sync(kFull, pick[0] >= 0 && (same & (same - 1)))) {
+        // an expert picked more than once: every one of its picks has the sum, in the picks' order
+        float d[2] = {0.0f, 0.0f};
+        for (int i = 0; i < a.k; ++i) {
+            const int e = __shfl_sync(kFull, i < 32 ? pick[0] : pick[1], i & 31);
+            const float v = __shfl_sync(kFull, i < 32 ? g[0] : g[1], i & 31);
+            if (e == pick[0]) d[0] += v;
+            if (e == pick[1]) d[1] += v;
+        }
+        g[0] = d[0];
+        g[1] = d[1];
     }
     __syncwarp();  // the zeros come first
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-        if (pick[h] >= 0) from_f32(out[pick[h]], SCORING == EPD_SCORE_SIGMOID ? d[h] * s[h] * (1.0f - s[h]) : d[h] * s[h]);
+        if (pick[h] >= 0) from_f32(out[pick[h]], SCORING == EPD_SCORE_SIGMOID ? g[h] * s[h] * (1.0f - s[h]) : g[h] * s[h]);
 }
 
 template <typename T, int V>
