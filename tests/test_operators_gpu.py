@@ -513,6 +513,21 @@ def test_shared_reduction_dgrad(counts, K, N, act):
     assert (dx[dead] == 7).all()
 
 
+@pytest.mark.parametrize("counts", [[1600], [3000, 70], [1537, 0, 1599], [5, 4000], [6145]])
+@pytest.mark.parametrize("K,N", [(64, 72), (264, 256), (1000, 520)])
+def test_shared_reduction_wgrad(counts, K, N):
+    E, start, M, _, dy, x, w, z, real, dead = backward_case(counts, K, N, "none", K, 1)
+    status = epd.new_status()
+    dw, db = epd.ep_expert_matmul_wgrad(dy, x, i32(counts), status, expert_start_loc=i32(start), with_dbias=True)
+    check_ok(status)
+    for e, (s, c) in enumerate(zip(start, counts)):
+        d, v = dy[s:s + c].double(), x[s:s + c].double()
+        want = d.t() @ v
+        tol = (c + 16) * 2.0 ** -23 * (d.abs().t() @ v.abs()) + 2 ** -8 * want.abs() + 1e-30
+        assert ((dw[e].double() - want).abs() <= tol).all()
+        assert ((db[e].double() - d.sum(0)).abs() <= (c + 16) * 2.0 ** -23 * d.abs().sum(0) + 1e-30).all()
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("N", [256, 2304])
 def test_shared_reduction_with_more_tiles_than_clusters(fp8, N):

@@ -34,8 +34,8 @@
 // being what this memory takes in writes alone; e4m3 with few rows the weights' way from memory
 // and with many the sums, of which a step has 256 cycles to its mma's 512. A lone tile is bound by
 // its two SMs' 64 bytes a clock as well, so a handful of tiles with a long reduction is cut along
-// it: a cluster of up to four pairs shares a tile and its first pair adds up the parts' sums, read
-// from the others' shared memory in a fixed order (kSharedSteps).
+// it: a cluster of up to four pairs shares a tile, and its parts' sums are read from the others'
+// shared memory and added up in a fixed order (kSharedSteps).
 //
 // Warps: the epilogue's 8 (e4m3: 16), the producer, which walks the tiles, publishes them to
 // the others and feeds TMA, one that issues the mma (in the pair's first block), and two helpers
@@ -85,14 +85,22 @@ constexpr int kGroupTiles = 8;                  // row tiles that share a pass o
 constexpr int kStages = 6;
 
 // Where few tiles leave most SMs idle, up to four pairs share a tile's reduction, which costs
-// some 1.2 us for the larger cluster and the sums' way between blocks, and takes 0.16 us a step
-// (e4m3 0.24) off as many steps as the others do. It is done from 96 / parts steps on (e4m3 48 /
-// parts). bf16, one expert of 16 rows and 512 features, in four parts and in one: K = 1024 6.4 and
-// 5.7 us, 1536 6.7 and 6.9, 4096 8.5 and 13.4; 64 rows, 7168 features, in two and in one: K = 2048
-// 10.9 and 10.3 us, 3200 13.6 and 14.1. e4m3, the same: 1024 6.4 and 6.0, 1536 6.9 and 7.1, 4096 7.8
-// and 11.7; in two: 2048 9.4 and 9.2, 3200 11.0 and 11.8.
+// 1 to 2 us for the larger cluster and the sums' way between blocks, and takes 0.16 us a step
+// (e4m3 0.24) off as many steps as the others do. It is done from kSharedSteps / parts steps on,
+// and, where a tile has many columns to exchange, from kSharedStepsWide on. One expert, 512 features,
+// in four parts and in one, us, bf16:
+//      16 rows: K = 1024  6.4  5.7   1536  6.5  6.9   4096  8.4  13.4
+//     256 rows: K = 1536 11.9 11.1   2048 12.1 13.1
+// in two and in one (64 rows, 7168 features): K = 2048 10.9 and 10.3, 3200 13.6 and 14.1. e4m3:
+//      16 rows: K = 1024  6.4  6.0   1536  7.2  6.8   2048  7.2   7.8   4096 8.1 11.7
+//     256 rows: K = 1536 14.9 11.2   2048 15.0 12.9
+// in two: K = 2048 9.4 and 9.2, 3200 11.1 and 11.8, and with 256 rows, 4096 features, 4096 17.9 and
+// 20.4. wgrad, 256 x 256, rows = 1536 12.7 and 10.5, 4096 13.6 and 21.0.
 template <bool FP8>
-constexpr int kSharedSteps = FP8 ? 48 : 96;
+constexpr int kSharedSteps = FP8 ? 50 : 96;
+template <bool FP8>
+constexpr int kSharedStepsWide = FP8 ? 24 : 32;
+constexpr int kWideRows = 128;  // more columns of D on average than these are many
 
 template <bool FP8>
 constexpr int kSmemOf = kStages * kStageBytes + kEpiWarpsOf<FP8> * kStagingOf<FP8> + (FP8 ? kScaleBytes : 0) + kTailBytes;
@@ -408,8 +416,12 @@ __device__ __forceinline__ bool swap_half(uint32_t mine, uint32_t other, uint32_
     return __all_sync(0xffffffffu, ok);
 }
 
-// A reduction that several pairs of a cluster share: 32 sums a lane are left in the block's own
-// shared memory (its stages, which nothing fills any more) and fetched by the first pair.
+// A reduction that several pairs of a cluster share: every pair finishes a part of the tile's
+// columns. The others' 32 sums a lane and chunk it leaves in its own shared memory (the stages,
+// which nothing fills any more), and fetches what they have left for it. (All by the first pair:
+// 256 rows, K = 2048: 14.0 us for 12.1.) e4m3 does it all by the first pair: its sums are in
+// registers already, and the code that keeps some and gives others away spills (16 rows, K = 7168,
+// SwiGLU: 14.8 us for 13.1).
 template <typename F>
 __device__ __forceinline__ void park(uint32_t at, F sum) {
     at += (threadIdx.x & 31) * 16;
@@ -421,9 +433,11 @@ __device__ __forceinline__ void park(uint32_t at, F sum) {
 
 // Adds the other parts' sums, in the parts' order.
 template <typename F>
-__device__ __forceinline__ void add_parked(uint32_t at, int rank, int parts, F sum) {
+__device__ __forceinline__ void add_parked(uint32_t at, const Tile &t, F sum) {
     at += (threadIdx.x & 31) * 16;
-    for (int s = 1; s < parts; ++s) {
+    const int rank = cluster_ctarank() & 1;
+    for (int s = 0; s < t.parts; ++s) {
+        if (s == t.part) continue;
         const uint32_t from = map_to_rank(at, 2 * s + rank);
 #pragma unroll
         for (int i0 = 0; i0 < 8; i0 += 4) {
@@ -437,6 +451,26 @@ __device__ __forceinline__ void add_parked(uint32_t at, int rank, int parts, F s
             }
         }
     }
+}
+
+// Arrives on barrier `bar` of the other parts' blocks of this rank, for a warp. (What it needs is read
+// where it is needed: e4m3 has no registers to keep it in.)
+__device__ __forceinline__ void tell_others(uint32_t bar, const Tile &t) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+    if (lane < t.parts && lane != t.part) mbar_release_cluster(map_to_rank(bar, 2 * lane + (cluster_ctarank() & 1)));
+}
+
+// The same for the first pair's alone.
+__device__ __forceinline__ void tell_first(uint32_t bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_release_cluster(map_to_rank(bar, cluster_ctarank() & 1));
+}
+
+// This warp's sums are left for the others, and theirs are there.
+__device__ __forceinline__ bool exchange(uint32_t parked, const Tile &t) {
+    tell_others(parked, t);
+    return __all_sync(0xffffffffu, mbar_wait_pipe<true>(parked, 0)) != 0;
 }
 
 // Element r of fragments f[h] in the words that Ahead::turn gives.
@@ -778,7 +812,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
         for (int i = 0; i < kEpiWarps / 2; ++i) mbar_init(bars + kSwap + i, 64);
         if (SPLIT) {
             mbar_init(bars + kParked, (parts - 1) * kEpiWarps);
-            mbar_init(bars + kFetched, kEpiWarps);
+            mbar_init(bars + kFetched, (FP8 ? 1 : parts - 1) * kEpiWarps);
         }
         mbar_init_fence();
         for (int i = 0; i < Maps<MODE>::kM; ++i) tma_prefetch_map(&maps.m[i]);
@@ -814,7 +848,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
                 if (SPLIT && more) {
                     if (tile == first) {
                         walk.cut(t, part, parts);
-                    } else if (part > 0) {  // the stages are free again once the sums are fetched
+                    } else if (!FP8 || part > 0) {  // the stages are free again once the sums are fetched
                         if (!(ok = mbar_wait_pipe<true>(bar0 + 8 * kFetched, 0))) break;
                         fence_proxy_async();
                     }
@@ -909,7 +943,9 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
             int stage = 0, acc = 0, was = -1;
             uint32_t parity = 0, parities = (1u << kAccs) - 1;  // of each accumulator's next release
             while (rank == 0 && ring.next(ok)) {
-                const int steps = ring.tile().steps, n = ring.tile().n, left = ring.tile().count & 63;
+                const int steps = ring.tile().steps, n = ring.tile().n;
+                // wgrad: rows of the region's last step, if it is this pair's and not a full one
+                const int left = !SPLIT || ring.tile().part == ring.tile().parts - 1 ? ring.tile().count & 63 : 0;
                 const int across = ring.tile().across;
                 ring.drop();
                 if (steps == 0) continue;
@@ -1031,16 +1067,6 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
         constexpr int kShare = kEpiWarps / 4;  // warps that share the columns of 32 lanes
         const int quadrant = warp & 3, share = warp >> 2;
         const uint32_t lead_empty = map_to_rank(acc_empty, lead);
-        // the end of a part: the first pair waits for the others' sums, they for nothing
-        auto parked = [&]() { return mbar_wait_pipe<true>(bar0 + 8 * kParked, 0); };
-        auto hand_over = [&]() {
-            __syncwarp();
-            if (lane == 0) mbar_release_cluster(map_to_rank(bar0 + 8 * kParked, rank));
-        };
-        auto fetched = [&]() {
-            __syncwarp();
-            if (lane > 0 && lane < parts) mbar_release_cluster(map_to_rank(bar0 + 8 * kFetched, 2 * lane + rank));
-        };
         const uint32_t my_tmem = tmem + ((uint32_t)(quadrant * 32) << 16);
         uint32_t parities = 0;  // of each accumulator's next result
         if (FP8) {
@@ -1095,13 +1121,13 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
                         auto sum = [&](int r) -> float & { return acc[r >> 4][r & 15]; };
                         if (ring.tile().part > 0) {
                             if (own) park(at, sum);
-                            hand_over();
+                            tell_first(bar0 + 8 * kParked);
                             ring.drop();
                             continue;
                         }
-                        if (!(ok = __all_sync(0xffffffffu, parked()))) break;
-                        if (own) add_parked(at, rank, parts, sum);
-                        fetched();
+                        if (!(ok = __all_sync(0xffffffffu, mbar_wait_pipe<true>(bar0 + 8 * kParked, 0)))) break;
+                        if (own) add_parked(at, ring.tile(), sum);
+                        tell_others(bar0 + 8 * kFetched, ring.tile());
                     }
                     Output<MODE, GATED, kStagedOf<FP8>> out(p, staging, bar0 + 8 * kSwap, warp);
                     out.begin(ring.tile(), rank, quadrant);
@@ -1159,13 +1185,13 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
                     auto rest = [&](int r) -> float & { return acc[1][r]; };
                     if (ring.tile().part > 0) {
                         if (blocks > 0) park(at, gate), park(at + 4096, rest);
-                        hand_over();
+                        tell_first(bar0 + 8 * kParked);
                         ring.drop();
                         continue;
                     }
-                    if (!(ok = __all_sync(0xffffffffu, parked()))) break;
-                    if (blocks > 0) add_parked(at, rank, parts, gate), add_parked(at + 4096, rank, parts, rest);
-                    fetched();
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait_pipe<true>(bar0 + 8 * kParked, 0)))) break;
+                    if (blocks > 0) add_parked(at, ring.tile(), gate), add_parked(at + 4096, ring.tile(), rest);
+                    tell_others(bar0 + 8 * kFetched, ring.tile());
                 }
                 if (blocks > 0) finish_rows<GATED>(p, ring.tile(), rank * 128 + quadrant * 32, share * 32,
                                                    staging + warp * kStagingOf<FP8>, acc);
@@ -1179,45 +1205,48 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
                 out.begin(t, rank, quadrant);
                 const int chunks = t.n / 32;
                 const bool any = t.steps > 0;  // else wgrad of an expert without rows
-                const bool shared = SPLIT && t.parts > 1, leaves = shared && t.part > 0;
+                Tile part_of;  // parts and this one's number
+                part_of.parts = t.parts, part_of.part = t.part;
+                const bool shared = SPLIT && t.parts > 1;
+                // a shared tile's chunks go round the pairs, as many at a time as its columns are shared by
+                const int from = share + (shared ? kShare * part_of.part : 0), by = shared ? kShare * part_of.parts : kShare;
                 ring.drop();
-                if (share < chunks && !leaves) out.fetch(share * 32);
+                if (from < chunks) out.fetch(from * 32);
                 if (any) {
                     if (!(ok = mbar_wait_pipe(acc_full + 8 * buf, (parities >> buf) & 1))) break;
                     parities ^= 1u << buf;
                     tcgen05_fence_after();
                 }
-                if (shared && !leaves && !(ok = __all_sync(0xffffffffu, parked()))) break;
-                for (int ch = share; ch < chunks; ch += kShare) {
-                    Frag f;
+                auto load = [&](Frag &f, int ch) {
+                    uint32_t v[2][16];
                     if (any) {
-                        uint32_t v[2][16];
                         tmem_ld_frag(v[0], my_tmem + buf * kTileRows + ch * 32);
                         tmem_ld_frag(v[1], my_tmem + buf * kTileRows + ch * 32 + (16u << 16));
                         tmem_wait_ld();
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int r = 0; r < 16; ++r) f[h][r] = __uint_as_float(v[h][r]);
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int r = 0; r < 16; ++r) f[h][r] = 0.0f;
                     }
-                    if (shared) {
-                        const uint32_t at = base + (ch * 4 + quadrant) * 4096;
-                        auto sum = [&](int r) -> float & { return f[r >> 4][r & 15]; };
-                        if (leaves) {
-                            park(at, sum);
-                            continue;
-                        }
-                        add_parked(at, rank, parts, sum);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) f[h][r] = any ? __uint_as_float(v[h][r]) : 0.0f;
+                };
+                if (shared) {
+                    for (int ch = share; ch < chunks; ch += kShare) {
+                        if (ch / kShare % part_of.parts == part_of.part) continue;
+                        Frag f;
+                        load(f, ch);
+                        park(base + (ch * 4 + quadrant) * 4096, [&](int r) -> float & { return f[r >> 4][r & 15]; });
                     }
-                    out.finish(f, ch * 32, (ch + kShare) * 32);
+                    if (!(ok = exchange(bar0 + 8 * kParked, part_of))) break;
                 }
-                if (leaves) hand_over();
-                if (shared && !leaves) fetched();
+                for (int ch = from; ch < chunks; ch += by) {
+                    Frag f;
+                    load(f, ch);
+                    if (shared)
+                        add_parked(base + (ch * 4 + quadrant) * 4096, part_of,
+                                   [&](int r) -> float & { return f[r >> 4][r & 15]; });
+                    out.finish(f, ch * 32, (ch + by) * 32);
+                }
+                if (shared) tell_others(bar0 + 8 * kFetched, part_of);
                 if (any) {
                     tcgen05_fence_before();
                     __syncwarp();
@@ -1320,16 +1349,18 @@ epd_status_t launch(const Maps<MODE> &maps, const ExpertArgs &p, cudaStream_t st
     if (most > INT32_MAX / 2) return EPD_ERR_UNSUPPORTED;
     constexpr int kThreads = kThreadsOf<MODE, FP8>, kSmem = kSmemOf<FP8>;
     int clusters;
-    if (MODE != kWgrad) {
-        const int steps = ((MODE == kForward ? p.K : p.N) + (FP8 ? 127 : 63)) / (FP8 ? 128 : 64);
-        for (int parts = 4; parts > 1; parts /= 2) {
-            if (steps * parts < kSharedSteps<FP8> || most * parts > sm_count() / 2) continue;
-            const epd_status_t rc = resident<MODE, FP8, GATED, MODE != kWgrad>(parts, clusters);
-            if (rc != EPD_OK) return rc;
-            if (most <= clusters)
-                return launch_pdl_cluster(expert_kernel<MODE, FP8, GATED, MODE != kWgrad>, 2 * parts * (int)most, kThreads,
-                                          kSmem, 2 * parts, stream, maps, p);
-        }
+    // the columns of D: an expert's rows, as far as there is room on average (wgrad: these are the
+    // reduction)
+    const int64_t rows = cap / E, columns = MODE == kWgrad ? p.N : rows;
+    const int64_t steps = ((MODE == kForward ? p.K : MODE == kDgrad ? p.N : rows) + (FP8 ? 127 : 63)) / (FP8 ? 128 : 64);
+    for (int parts = 4; parts > 1; parts /= 2) {
+        if (columns > kWideRows ? steps < kSharedStepsWide<FP8> : steps * parts < kSharedSteps<FP8>) continue;
+        if (most * parts > sm_count() / 2) continue;
+        const epd_status_t rc = resident<MODE, FP8, GATED, true>(parts, clusters);
+        if (rc != EPD_OK) return rc;
+        if (most <= clusters)
+            return launch_pdl_cluster(expert_kernel<MODE, FP8, GATED, true>, 2 * parts * (int)most, kThreads, kSmem,
+                                      2 * parts, stream, maps, p);
     }
     const epd_status_t rc = resident<MODE, FP8, GATED, false>(1, clusters);
     if (rc != EPD_OK) return rc;
