@@ -718,26 +718,29 @@ __device__ __forceinline__ void finish_rows(const ExpertArgs &p, const Tile &t, 
     }
 }
 
-// dbias[e, n] = the sum of the expert's rows of dy: a warp takes 64 columns of an expert, a lane
-// eight of them in every fourth row, and the four parts are added up, all in a fixed order. The
-// helper warps of wgrad do it beside the products, straight from memory: +12 us at 64 experts of
-// 384 rows, 4096 columns, where a kernel of its own after the product took 37.
+// dbias[e, n] = the sum of the expert's rows of dy: a warp takes 8 LANES columns of an expert, a
+// lane eight of them in every (32 / LANES)th row, and these parts are added up, all in a fixed
+// order. The helper warps of wgrad do it beside the products, straight from memory: +12 us at 64
+// experts of 384 rows, 4096 x 2048, where a kernel of its own after the product took 37. (Four warps
+// a block: +20 us there; with 256 features, where the product is shorter than the sums, 130 us
+// become 91.)
+template <int LANES>
 __device__ __forceinline__ void sum_bias(const ExpertArgs &p, int worker, int workers) {
-    constexpr int kRows = 16;  // in flight a lane
-    const int lane = threadIdx.x & 31, part = lane >> 3;
-    const int groups = (p.N + 63) / 64;
+    constexpr int kRows = 16, kParts = 32 / LANES;  // in flight a lane; rows at a time
+    const int lane = threadIdx.x & 31, part = lane / LANES;
+    const int groups = (p.N + 8 * LANES - 1) / (8 * LANES);
     const int64_t pitch = (int64_t)p.N * 2;
     for (int64_t item = worker; item < (int64_t)groups * p.rows.num_experts; item += workers) {
-        const int e = (int)(item / groups), n = (int)(item - (int64_t)e * groups) * 64 + (lane & 7) * 8;
+        const int e = (int)(item / groups), n = (int)(item - (int64_t)e * groups) * (8 * LANES) + (lane % LANES) * 8;
         int start, count;
         expert_region(p.rows, e, start, count, p.status);
         float sum[8] = {};
         const uint8_t *at = p.dy + ((int64_t)start * p.N + n) * 2;
-        for (int r = part; n < p.N && r < count; r += 4 * kRows) {
+        for (int r = part; n < p.N && r < count; r += kParts * kRows) {
             uint4 v[kRows];
 #pragma unroll
             for (int i = 0; i < kRows; ++i)
-                v[i] = r + 4 * i < count ? ld_stream16(at + (r + 4 * i) * pitch) : make_uint4(0, 0, 0, 0);
+                v[i] = r + kParts * i < count ? ld_stream16(at + (r + kParts * i) * pitch) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
                 float f[8];
@@ -748,10 +751,9 @@ __device__ __forceinline__ void sum_bias(const ExpertArgs &p, int worker, int wo
         }
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 8);
-            sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 16);
-        }
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int o = LANES; o < 32; o *= 2) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
         if (part == 0 && n < p.N) {
             float *out = p.dbias + (int64_t)e * p.N + n;
 #pragma unroll
@@ -997,7 +999,15 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
                 }
             }
         } else if (MODE == kWgrad) {
-            if (p.dbias) sum_bias(p, blockIdx.x * kHelpers + warp - kHelperWarp, gridDim.x * kHelpers);
+            // 64 columns a warp, or 16 where that leaves warps without any: one expert of 4096 rows,
+            // 1024 x 1024, 32.5 us with 64 and 16.5 with 16
+            const int worker = blockIdx.x * kHelpers + warp - kHelperWarp, workers = gridDim.x * kHelpers;
+            if (p.dbias) {
+                if ((int64_t)((p.N + 63) / 64) * p.rows.num_experts < workers)
+                    sum_bias<2>(p, worker, workers);
+                else
+                    sum_bias<8>(p, worker, workers);
+            }
         } else if (FP8) {
             const int tid = threadIdx.x - kHelperWarp * 32;
             const int C = p.K / 128;
