@@ -92,14 +92,14 @@ constexpr int kStages = 6;
 //      16 rows: K = 1024  6.4  5.7   1536  6.5  6.9   4096  8.4  13.4
 //     256 rows: K = 1536 11.9 11.1   2048 12.1 13.1
 // in two and in one (64 rows, 7168 features): K = 2048 10.9 and 10.3, 3200 13.6 and 14.1. e4m3:
-//      16 rows: K = 1024  6.4  6.0   1536  7.2  6.8   2048  7.2   7.8   4096 8.1 11.7
-//     256 rows: K = 1536 14.9 11.2   2048 15.0 12.9
-// in two: K = 2048 9.4 and 9.2, 3200 11.1 and 11.8, and with 256 rows, 4096 features, 4096 17.9 and
-// 20.4. wgrad, 256 x 256, rows = 1536 12.7 and 10.5, 4096 13.6 and 21.0.
+//      16 rows: K = 1536  7.2  6.6   2048  7.2  7.4   4096  8.1 11.7
+//     256 rows: K = 2048 15.1 12.0   3584 16.7 16.7
+// in two: K = 3200 11.1 and 11.1, 4096 11.8 and 12.8; with 256 rows, 4096 features, K = 3200 16.6 and
+// 16.2, 4096 17.8 and 19.0. wgrad, 256 x 256, rows = 1536 12.7 and 10.5, 4096 13.6 and 21.0.
 template <bool FP8>
-constexpr int kSharedSteps = FP8 ? 50 : 96;
+constexpr int kSharedSteps = FP8 ? 64 : 96;
 template <bool FP8>
-constexpr int kSharedStepsWide = FP8 ? 24 : 32;
+constexpr int kSharedStepsWide = FP8 ? 28 : 32;
 constexpr int kWideRows = 128;  // more columns of D on average than these are many
 
 template <bool FP8>
@@ -830,6 +830,17 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
     pdl_wait();
     pdl_trigger();
 
+    // a cluster's first tile is shared by its pairs; should there be more tiles than clusters, the
+    // others are not
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2, first = SPLIT ? pair / parts : pair;
+    Walker<MODE, kStep, FP8> walk(p, kFeatStep);
+    Tile t;
+    bool more = false;
+    // Where e4m3's first tile is looked up before the warps part, its epilogue keeps what it needs in
+    // registers (without gates, 4096 x 7168, 256 experts of 512 rows: 720 us for 772); for the others
+    // it only comes later that way (a lone tile +0.3 us).
+    constexpr bool kEarly = FP8 && !SPLIT;
+    if (kEarly && warp == kProducerWarp) more = walk.next(first, t);
     Ring ring{slots, bar0 + 8 * kTileFull, bar0 + 8 * kTileEmpty};
     bool ok = true;
     if (warp >= kEpiWarps) {
@@ -837,16 +848,10 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
         if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == kProducerWarp) {
             const uint32_t lead_full = map_to_rank(full, lead);
-            const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
-            // a cluster's first tile is shared by its pairs; should there be more tiles than
-            // clusters, the others are not
-            const int first = SPLIT ? pair / parts : pair;
-            Walker<MODE, kStep, FP8> walk(p, kFeatStep);
             int stage = 0, issued = 0;
             uint32_t parity = 1;
             for (int tile = first; ok; tile = SPLIT && tile == first ? pairs / parts + pair : tile + pairs) {
-                Tile t;
-                const bool more = walk.next(tile, t);
+                if (!kEarly || tile != first) more = walk.next(tile, t);
                 if (SPLIT && more) {
                     if (tile == first) {
                         walk.cut(t, part, parts);
