@@ -1,0 +1,57 @@
+"""The router, the products and their gradients at the ends of their ranges, against plain
+definitions in 64 bits."""
+import pytest
+import torch
+
+import unpermute_ep_dispatch_gb300 as epd
+from test_operators_gpu import DEV, check_ok, gen
+
+pytestmark = pytest.mark.gpu
+
+ULP = 2.0 ** -23     # of a 32-bit value, at most
+TINY = 2.0 ** -149   # spacing of 32-bit values near zero
+TINY_BF16 = 2.0 ** -133
+
+
+def uniform(shape, lo, hi, seed):
+    return lo + (hi - lo) * torch.rand(shape, generator=gen(seed), device=DEV)
+
+
+# Where a sigmoid's rows lie: near one, where 1 - s is far smaller than s, near zero, where s falls
+# below the smallest normal number, and rows with both.
+SATURATED = {"high": (8.0, 20.0), "very high": (20.0, 60.0), "low": (-100.0, -80.0), "lowest": (-103.0, -88.5),
+             "wide": (-100.0, 20.0)}
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows", SATURATED)
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("T,E,k", [(70, 24, 4), (9, 600, 40), (5, 8, 1)])
+def test_route_backward_of_saturated_sigmoids(dtype, rows, renorm, T, E, k):
+    """Within a few units in the last place of dl = ds s (1 - s), and finite. s, 1 - s and a
+    weight p are each within 8 units; a weight of picks that differ by d in their logits within
+    d / 2 units more (the rounding of the difference), and its sum over the picks adds k."""
+    l = uniform((T, E), *SATURATED[rows], T).to(dtype)
+    idx = torch.rand(T, E, generator=gen(E), device=DEV).topk(k, 1).indices
+    g = 1.5 * torch.sign(torch.randn(T, k, generator=gen(k), device=DEV)) + 0.25 * torch.randn(T, k, generator=gen(3), device=DEV)
+    status = epd.new_status()
+    d = epd.ep_route_backward(g, l, idx, status, scoring="sigmoid", renormalize=renorm, routed_scale=2.0)
+    check_ok(status)
+    x = l.double().gather(1, idx)
+    s, c, g = torch.sigmoid(x), torch.sigmoid(-x), 2.0 * g.double()
+    if renorm:
+        p = s / s.sum(1, keepdim=True)
+        apart = g.unsqueeze(2) - g.unsqueeze(1)
+        pick = (apart * p.unsqueeze(1)).sum(2) * p * c
+        far = x.amax(1, keepdim=True) - x
+        bound = (apart.abs() * p.unsqueeze(1)).sum(2) * p * c * (k + 32 + far + far.amax(1, keepdim=True)) * ULP
+        bound = bound + 8 * apart.abs().amax(2) * TINY   # a weight below the smallest normal number
+    else:
+        pick = g * s * c
+        bound = pick.abs() * 24 * ULP + 4 * g.abs() * TINY
+    want = torch.zeros(T, E, dtype=torch.float64, device=DEV).scatter(1, idx, pick)
+    tol = torch.zeros_like(want).scatter(1, idx, bound + 2 * TINY)
+    if dtype == torch.bfloat16:
+        tol = tol + want.abs() * 2 ** -8 + TINY_BF16 * (want != 0)
+    assert torch.isfinite(d).all()
+    assert ((d.double() - want).abs() <= tol).all()

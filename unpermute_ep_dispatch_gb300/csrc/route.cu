@@ -16,13 +16,6 @@
 namespace epd {
 namespace {
 
-// The largest value of the warp (no NaN among them).
-__device__ __forceinline__ float redux_max(float v) {
-    float r;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
-}
-
 struct RouteArgs {
     const void *logits;
     const float *bias;

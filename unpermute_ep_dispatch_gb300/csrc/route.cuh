@@ -34,6 +34,35 @@ __device__ __forceinline__ float to_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 
+// The largest value of the warp (no NaN among them).
+__device__ __forceinline__ float redux_max(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// s = 1 / (1 + exp(-x)) and its complement c = 1 - s, each to the last place or two: the exponential
+// is taken of -|x|, which neither overflows nor loses what is below the smallest normal number, and
+// the complement is not a difference (at x = 15 that would be off by a sixth, from 17 on 0).
+__device__ __forceinline__ void sigmoid_pair(float x, float &s, float &c) {
+    const float e = expf(-fabsf(x)), r = __fdiv_rn(1.0f, 1.0f + e);
+    s = x < 0.0f ? e * r : r;
+    c = x < 0.0f ? r : e * r;
+}
+
+// Scores that are divided by their sum, of picks with sigmoid scores s, complements c and logits x
+// (-inf: no pick). Where all logits are negative, s = exp(x) c is taken times exp(-m), m the largest
+// logit, which the division takes out again: scores near or below the smallest normal number would
+// leave their shares no digits, and the reciprocal of their sum may overflow. 0 where even the
+// largest score is 0.
+__device__ __forceinline__ void lift_low(float (&s)[2], const float (&c)[2], const float (&x)[2]) {
+    const float m = redux_max(fmaxf(x[0], x[1]));
+    if (m >= 0.0f) return;
+    const bool any = expf(m) > 0.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) s[h] = any ? expf(x[h] - m) * c[h] : 0.0f;
+}
+
 // A logit as the router reads it: NaN and +inf are reported and count as -inf.
 __device__ __forceinline__ float clean_logit(float l, bool &bad) {
     if (!(l < CUDART_INF_F)) {

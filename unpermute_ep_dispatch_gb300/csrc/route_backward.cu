@@ -59,8 +59,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_picks_kernel(Rou
     const T *row = static_cast<const T *>(a.logits) + (int64_t)t * a.E;
     T *out = static_cast<T *>(a.grad) + (int64_t)t * a.E;
     int pick[2];
-    float g[2], s[2];
-    load_picks(a, t, row, lane, pick, s, g);
+    float g[2], x[2];
+    load_picks(a, t, row, lane, pick, x, g);
     if (a.vec) {
         constexpr int C = 16 / sizeof(T);
         for (int e = lane * C; e < a.E; e += 32 * C) st16(out + e, make_uint4(0, 0, 0, 0));
@@ -68,32 +68,39 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_picks_kernel(Rou
         for (int e = lane; e < a.E; e += 32) from_f32(out[e], 0.0f);
     }
     const bool two = a.k > 32;
+    // what a pick's own logit does to its weight is ds s c: c = 1 - s for the sigmoid, and for the
+    // softmax of the picks it is in ds already
+    float s[2], c[2] = {1.0f, 1.0f};
     if (SCORING == EPD_SCORE_SOFTMAX) {
-        const float m = warp_max(fmaxf(s[0], s[1]));
-        s[0] = m > -CUDART_INF_F ? expf(s[0] - m) : 0.0f;
-        if (two) s[1] = m > -CUDART_INF_F ? expf(s[1] - m) : 0.0f;
+        const float m = warp_max(fmaxf(x[0], x[1]));
+        s[0] = m > -CUDART_INF_F ? expf(x[0] - m) : 0.0f;
+        s[1] = two && m > -CUDART_INF_F ? expf(x[1] - m) : 0.0f;
     } else {
-        s[0] = sigmoid_f32(s[0]);
-        if (two) s[1] = sigmoid_f32(s[1]);
+        s[1] = 0.0f;
+        sigmoid_pair(x[0], s[0], c[0]);
+        if (two) sigmoid_pair(x[1], s[1], c[1]);
+        if (a.renorm) lift_low(s, c, x);
     }
-    if (!two) s[1] = 0.0f;
     if (a.renorm) {
+        // from here on s are the weights, at most 1: their product with ds neither overflows nor
+        // has to pass through 1 / sum
         const float sum = warp_sum(s[0] + s[1]);
         const float rs = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
         float ds[2] = {0.0f, 0.0f};
-        const float p0 = s[0] * rs, p1 = s[1] * rs;
+        s[0] *= rs;
+        s[1] *= rs;
         for (int i = 0; i < min(a.k, 32); ++i) {
-            const float gi = __shfl_sync(kFull, g[0], i), pi = __shfl_sync(kFull, p0, i);
+            const float gi = __shfl_sync(kFull, g[0], i), pi = __shfl_sync(kFull, s[0], i);
             ds[0] += (g[0] - gi) * pi;
             if (two) ds[1] += (g[1] - gi) * pi;
         }
         for (int i = 32; i < a.k; ++i) {
-            const float gi = __shfl_sync(kFull, g[1], i - 32), pi = __shfl_sync(kFull, p1, i - 32);
+            const float gi = __shfl_sync(kFull, g[1], i - 32), pi = __shfl_sync(kFull, s[1], i - 32);
             ds[0] += (g[0] - gi) * pi;
             ds[1] += (g[1] - gi) * pi;
         }
-        g[0] = ds[0] * rs;
-        g[1] = ds[1] * rs;
+        g[0] = ds[0];
+        g[1] = ds[1];
     }
     const uint32_t same = __match_any_sync(kFull, pick[0]);
     if (two || __any_sync(kFull, pick[0] >= 0 && (same & (same - 1)))) {
@@ -111,7 +118,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_picks_kernel(Rou
     __syncwarp();  // the zeros come first
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-        if (pick[h] >= 0) from_f32(out[pick[h]], SCORING == EPD_SCORE_SIGMOID ? g[h] * s[h] * (1.0f - s[h]) : g[h] * s[h]);
+        if (pick[h] >= 0) from_f32(out[pick[h]], g[h] * s[h] * c[h]);
 }
 
 template <typename T, int V>
