@@ -55,3 +55,42 @@ def test_route_backward_of_saturated_sigmoids(dtype, rows, renorm, T, E, k):
         tol = tol + want.abs() * 2 ** -8 + TINY_BF16 * (want != 0)
     assert torch.isfinite(d).all()
     assert ((d.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("ahead", [0.0, 6.0, 12.0, 18.0, 40.0])
+@pytest.mark.parametrize("T,E,k", [(40, 256, 1), (33, 64, 6), (6, 1030, 40), (9, 5, 5)])
+def test_route_backward_of_confident_softmax(dtype, ahead, T, E, k):
+    """One logit of every row lies `ahead` of the others: 1 - s of it is far smaller than s.
+    dl_e = sum over i of s_e s_i (ds_e - ds_i), each product within the roundings of its two
+    scores (16 units, and half a unit for each unit that the logit lies below the row's largest)
+    and of the sum of E terms in the order of a tree and per lane (E / 32 + k + 8)."""
+    l = torch.randn(T, E, generator=gen(T), device=DEV)
+    top = torch.randint(0, E, (T, 1), generator=gen(E), device=DEV)
+    l = l.scatter_add(1, top, torch.full((T, 1), ahead, device=DEV)).to(dtype)
+    # the confident expert first among the picks of even rows, left out of the others'
+    order = torch.rand(T, E, generator=gen(7), device=DEV)
+    order = order.scatter(1, top, torch.where(torch.arange(T, device=DEV) % 2 == 0, 2.0, -1.0).unsqueeze(1))
+    idx = order.topk(k, 1).indices
+    if k > 2:
+        idx[:, 2] = idx[:, 0]      # picked twice
+        idx[1::3, 1] = -1
+    g = torch.randn(T, k, generator=gen(k), device=DEV)
+    status = epd.new_status()
+    d = epd.ep_route_backward(g, l, idx, status, scoring="softmax", renormalize=False)
+    check_ok(status)
+    x = l.double()
+    s = torch.softmax(x, 1)
+    ds = torch.zeros_like(s).scatter_add(1, idx.clamp(min=0), torch.where(idx >= 0, g.double(), 0.0))
+    want, bound = torch.zeros_like(s), torch.zeros_like(s)
+    for e in range(E):
+        term = s[:, e:e + 1] * s * (ds[:, e:e + 1] - ds)
+        want[:, e], bound[:, e] = term.sum(1), term.abs().sum(1)
+    # duplicate picks are summed first, in 32 bits
+    dup = torch.zeros_like(s).scatter_add(1, idx.clamp(min=0), torch.where(idx >= 0, g.double().abs(), 0.0)).amax(1, keepdim=True)
+    far = (x.amax(1, keepdim=True) - x).amax(1, keepdim=True)
+    others = torch.stack([s[:, torch.arange(E, device=DEV) != e].sum(1) for e in range(E)], 1)
+    tol = bound * (E / 32 + k + 40 + far) * ULP + 2 * ULP * dup * s * others + 4 * TINY
+    if dtype == torch.bfloat16:
+        tol = tol + want.abs() * 2 ** -8 + TINY_BF16
+    assert ((d.double() - want).abs() <= tol).all()
