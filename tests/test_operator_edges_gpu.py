@@ -94,3 +94,28 @@ def test_route_backward_of_confident_softmax(dtype, ahead, T, E, k):
     if dtype == torch.bfloat16:
         tol = tol + want.abs() * 2 ** -8 + TINY_BF16
     assert ((d.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("rows", ["low", "lowest", "wide"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("T,E,k", [(70, 24, 4), (9, 600, 40), (5, 8, 1)])
+def test_route_weights_of_low_sigmoids(rows, renorm, biased, T, E, k):
+    """Scores below the smallest normal number are numbers all the same, and so are their shares."""
+    l = uniform((T, E), *SATURATED[rows], T)
+    bias = 2.0 * torch.randperm(E, generator=gen(E), device=DEV).float() if biased else None
+    status = epd.new_status()
+    idx, w = epd.ep_route(l, k, status, scoring="sigmoid", bias=bias, renormalize=renorm)
+    check_ok(status)
+    x = l.double()
+    order = (torch.sigmoid(x) + bias.double() if biased else x).sort(dim=1, descending=True, stable=True).indices
+    assert torch.equal(idx, order[:, :k])
+    s = torch.sigmoid(x).gather(1, idx)
+    if renorm:
+        s = s / s.sum(1, keepdim=True)
+        # the roundings of a score and of the sum, and half a unit for each unit that a logit lies
+        # below the largest (no more than 120)
+        tol = s * (k + 24 + 64) * ULP + 6 * TINY
+    else:
+        tol = s * 8 * ULP + 3 * TINY
+    assert ((w.double() - s).abs() <= tol).all()

@@ -27,11 +27,6 @@ __device__ __forceinline__ uint4 pack8_bf16(const float (&f)[8]) {
                       pack2_bf16(f[6], f[7]));
 }
 
-// 1 / (1 + exp(-x)): 0 for -inf and for the lowest finite value, 1 for +inf.
-__device__ __forceinline__ float sigmoid_f32(float x) {
-    return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-x)));
-}
-
 constexpr float kInvSqrt2Pi = 0.39894228040143267794f;
 constexpr float kLog2e = 1.4426950408889634f;
 

@@ -225,24 +225,26 @@ __global__ void __launch_bounds__(kRouteThreads, V <= 8 ? 16 : 1) route_kernel(R
         }
     }
     const int halves = a.k > 32 ? 2 : 1;
-    float s[2] = {-CUDART_INF_F, -CUDART_INF_F};
-    float sum = 0.0f;
+    float x[2] = {-CUDART_INF_F, -CUDART_INF_F}, s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-        if (h < halves && pick[h] >= 0) s[h] = to_f32(row[pick[h]]);
-    if (SCORING == EPD_SCORE_SOFTMAX && a.renorm) {
-        m = warp_max(fmaxf(s[0], s[1]));
-        inv = 1.0f;
-    }
+        if (h < halves && pick[h] >= 0) x[h] = to_f32(row[pick[h]]);
+    if (SCORING == EPD_SCORE_SIGMOID) {
+        float c[2] = {1.0f, 1.0f};
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (h == halves) break;
-        if (SCORING == EPD_SCORE_SIGMOID)
-            s[h] = sigmoid_f32(s[h]);
-        else
-            s[h] = pick[h] >= 0 ? expf(s[h] - m) * inv : 0.0f;
-        sum += s[h];
+        for (int h = 0; h < 2; ++h)
+            if (h < halves) sigmoid_pair(x[h], s[h], c[h]);
+        if (a.renorm) lift_low(s, c, x);
+    } else {
+        if (a.renorm) {
+            m = warp_max(fmaxf(x[0], x[1]));
+            inv = 1.0f;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (h < halves && pick[h] >= 0) s[h] = expf(x[h] - m) * inv;
     }
+    float sum = s[0] + s[1];
     if (a.renorm) sum = warp_sum(sum);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
