@@ -408,10 +408,12 @@ typedef enum {
  *       `renormalize` (0 where that sum is 0), times routed_scale.
  * Scores without a bias are compared by their logits, which order them exactly as
  * the scores do but never round two different ones to the same value; with a bias
- * (and in a group's sum of two) they are fp32 values within a few units in the last
- * place. The weights' scores are computed to the last place or two, numbers below the
- * smallest normal one included (a sigmoid is 0 below -103.97), and renormalised weights
- * keep their digits where all the picks' scores are that low.
+ * (and in a group's sum of two) they are fp32 values within 8 units in the last place.
+ * The weights' scores are computed to the last place or two. (Softmax, both: on top of
+ * that the roundings of the sum over the row, and of the logit's difference from the
+ * row's largest, half a unit for each unit of it.) That includes numbers below the
+ * smallest normal one (a sigmoid is 0 below -103.97), and renormalised weights keep
+ * their digits where all the picks' scores are that low.
  * An expert whose logit is -inf cannot be chosen; where fewer than k are left the
  * rest of the row is -1 with weight 0 (the type's lowest finite value is an ordinary
  * logit). A NaN or +inf logit sets EPD_ERR_NONFINITE in *status and counts as -inf.

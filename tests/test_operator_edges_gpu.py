@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import unpermute_ep_dispatch_gb300 as epd
-from test_operators_gpu import DEV, check_ok, gen
+from test_operators_gpu import DEV, INF, check_ok, gen
 
 pytestmark = pytest.mark.gpu
 
@@ -119,3 +119,35 @@ def test_route_weights_of_low_sigmoids(rows, renorm, biased, T, E, k):
     else:
         tol = s * 8 * ULP + 3 * TINY
     assert ((w.double() - s).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("size", [2, 3, 8])
+def test_route_ranks_groups_of_low_scores(scoring, size):
+    """A group's score is within a few units in the last place of the sum of its two best scores,
+    however low: of two groups with one expert each the one whose logit is the next larger
+    number is kept. (That is sixteen units of the score or more from 16 on.)"""
+    low = torch.cat([uniform((400,), -80, -16, 1), -torch.arange(17, 80, device=DEV).float()])
+    T = low.shape[0]
+    up = torch.nextafter(low, torch.zeros_like(low))
+    l = torch.full((T, 4 * size), -INF, device=DEV)
+    l[:, 0] = 0.0                        # the row's largest, kept always
+    l[:, size], l[:, 2 * size + 1] = low, up
+    status = epd.new_status()
+    idx, _ = epd.ep_route(l, 2, status, scoring=scoring, num_groups=4, topk_groups=2, group_score="top2")
+    check_ok(status)
+    assert (idx[:, 0] == 0).all()
+    assert (idx[:, 1] == 2 * size + 1).all()
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+def test_route_chooses_by_exact_scores(scoring):
+    """With a bias of zero the choice goes by the 32-bit scores, which tell logits apart that
+    differ by sixteen units of their score or more."""
+    low = uniform((300,), -80, -16, 2)
+    l = torch.full((300, 12), -INF, device=DEV)
+    l[:, 3], l[:, 4], l[:, 9] = low, torch.nextafter(low, torch.zeros_like(low)), 0.0
+    status = epd.new_status()
+    idx, _ = epd.ep_route(l, 2, status, scoring=scoring, bias=torch.zeros(12, device=DEV))
+    check_ok(status)
+    assert (idx == torch.tensor([9, 4], device=DEV)).all()

@@ -103,7 +103,15 @@ __global__ void __launch_bounds__(kRouteThreads, V <= 8 ? 16 : 1) route_kernel(R
 #pragma unroll
             for (int i = 0; i < L::C; ++i) {
                 float &v = c[q * L::C + i];
-                const float score = SCORING == EPD_SCORE_SIGMOID ? fast_sigmoid(v) : __expf(v - m) * inv;
+                // expf, for the choice is told apart by these: with the hardware's 2^x of a rounded
+                // product neighbouring logits tie from 11 on (16384 tokens grouped: 13.7 us for 14.4)
+                float score;
+                if (SCORING == EPD_SCORE_SIGMOID) {
+                    const float e = expf(-fabsf(v));
+                    score = (v < 0.0f ? e : 1.0f) * fast_rcp(1.0f + e);
+                } else {
+                    score = expf(v - m) * inv;
+                }
                 v = v > -CUDART_INF_F ? __fadd_rn(score, bias[i]) : -CUDART_INF_F;
             }
         }
