@@ -79,7 +79,7 @@ typedef enum {
     EPD_ERR_INVALID_EXPERT = 4, /* (status word) topk_idx held an id outside [-1, E) */
     EPD_ERR_TIMEOUT = 5,        /* (status word) a bounded look-back wait gave up */
     EPD_ERR_CAPACITY = 6,       /* (status word) a slot fell outside [0, capacity_rows) */
-    EPD_ERR_NONFINITE = 7,      /* (status word) a router logit was NaN or +inf */
+    EPD_ERR_NONFINITE = 7,      /* (status word) a router logit was NaN or +inf, or a bias NaN */
 } epd_status_t;
 
 typedef enum {
@@ -416,7 +416,9 @@ typedef enum {
  * their digits where all the picks' scores are that low.
  * An expert whose logit is -inf cannot be chosen; where fewer than k are left the
  * rest of the row is -1 with weight 0 (the type's lowest finite value is an ordinary
- * logit). A NaN or +inf logit sets EPD_ERR_NONFINITE in *status and counts as -inf.
+ * logit). A NaN or +inf logit sets EPD_ERR_NONFINITE in *status and counts as -inf; so
+ * does a NaN bias of an expert that could be chosen. A bias of -inf takes its expert out,
+ * one of +inf puts it first.
  *   logits: [T, E] float32 (EPD_F32) or bfloat16 (EPD_BF16);  bias: [E] float32;
  *   topk_idx: [T, k] int64;  topk_weights: [T, k] float32.
  * E in [1, EPD_MAX_EXPERTS], k in [1, min(E, EPD_MAX_TOPK)], num_groups in

@@ -1,5 +1,7 @@
 """The router, the products and their gradients at the ends of their ranges, against plain
 definitions in 64 bits."""
+import math
+
 import pytest
 import torch
 
@@ -151,3 +153,23 @@ def test_route_chooses_by_exact_scores(scoring):
     idx, _ = epd.ep_route(l, 2, status, scoring=scoring, bias=torch.zeros(12, device=DEV))
     check_ok(status)
     assert (idx == torch.tensor([9, 4], device=DEV)).all()
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("groups,gs", [(1, "max"), (4, "top2"), (3, "top2"), (6, "max")])
+@pytest.mark.parametrize("E", [24, 48, 312])
+def test_route_reports_nan_bias(scoring, groups, gs, E):
+    """A NaN bias is reported, and its expert cannot be chosen nor count for its group."""
+    l = torch.randn(50, E, generator=gen(E), device=DEV)
+    bias = torch.randint(-2, 3, (E,), generator=gen(2), device=DEV).float()
+    gone = torch.arange(E, device=DEV) % 5 == 0
+    keep = max(1, groups // 2)
+    want_status, status = epd.new_status(), epd.new_status()
+    opts = dict(scoring=scoring, num_groups=groups, topk_groups=keep, group_score=gs)
+    want, ww = epd.ep_route(l, 4, want_status, bias=torch.where(gone, -INF, bias), **opts)
+    check_ok(want_status)
+    got, gw = epd.ep_route(l, 4, status, bias=torch.where(gone, math.nan, bias), **opts)
+    torch.cuda.synchronize()
+    assert int(status.item()) == epd.EPD_ERR_NONFINITE
+    assert not (got % 5 == 0).any()
+    assert torch.equal(got, want) and torch.equal(gw, ww)

@@ -1066,7 +1066,7 @@ const char *epd_status_string(int code) {
         case EPD_ERR_INVALID_EXPERT: return "expert id outside [-1, E)";
         case EPD_ERR_TIMEOUT: return "look-back or pipeline wait gave up";
         case EPD_ERR_CAPACITY: return "slot outside the permuted buffer";
-        case EPD_ERR_NONFINITE: return "NaN or +inf router logit";
+        case EPD_ERR_NONFINITE: return "NaN or +inf router logit, or NaN bias";
         default: return "unknown status";
     }
 }

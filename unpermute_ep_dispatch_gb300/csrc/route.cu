@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(kRouteThreads, V <= 8 ? 16 : 1) route_kernel(R
     // renormalised softmax weights are the softmax of the picks alone
     if (SCORING == EPD_SCORE_SOFTMAX && (scored || !a.renorm)) softmax_stats<false>(c, m, inv);
     if (scored) {
+        float worst = -CUDART_INF_F;
 #pragma unroll
         for (int q = 0; q < L::Q; ++q) {
             const int e0 = (q * 32 + lane) * L::C;
@@ -113,7 +114,13 @@ __global__ void __launch_bounds__(kRouteThreads, V <= 8 ? 16 : 1) route_kernel(R
                     score = expf(v - m) * inv;
                 }
                 v = v > -CUDART_INF_F ? __fadd_rn(score, bias[i]) : -CUDART_INF_F;
+                worst = max_nan(worst, v);
             }
+        }
+        if (worst != worst) {  // a NaN bias
+#pragma unroll
+            for (int i = 0; i < V; ++i) c[i] = c[i] == c[i] ? c[i] : -CUDART_INF_F;
+            report(a.status, EPD_ERR_NONFINITE);
         }
     }
     if (grouped) {
