@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import unpermute_ep_dispatch_gb300 as epd
-from test_operators_gpu import DEV, INF, check_ok, gen
+from test_operators_gpu import DEV, INF, backward_case, check_ok, forward_case, gen, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -173,3 +173,39 @@ def test_route_reports_nan_bias(scoring, groups, gs, E):
     assert int(status.item()) == epd.EPD_ERR_NONFINITE
     assert not (got % 5 == 0).any()
     assert torch.equal(got, want) and torch.equal(gw, ww)
+
+
+LOWEST = torch.finfo(torch.bfloat16).min
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "swiglu"])
+def test_dgrad_of_lowest_preactivations(act):
+    """A pre-activation of the type's lowest value has no slope, whatever it is multiplied by."""
+    counts, K, N = [5, 0, 20], 64, 64
+    E, start, M, KZ, dy, x, w, z, real, dead = backward_case(counts, K, N, act, 3, 0)
+    z[:, 0:KZ:3] = LOWEST                       # gates, and for swiglu up features too
+    if act == "swiglu":
+        z[:, K:2 * K:4] = -LOWEST
+        z[:, 1] = LOWEST
+        z[:, K + 1] = LOWEST
+    dy = (dy.float() * 8).to(torch.bfloat16)
+    status = epd.new_status()
+    dx = epd.ep_expert_matmul_dgrad(dy, w, i32(counts), status, expert_start_loc=i32(start), activation=act, preact=z)
+    check_ok(status)
+    gate = z[real][:, :K].float() == LOWEST
+    assert (dx[real][:, :K][gate] == 0).all()
+    if act == "swiglu":
+        assert (dx[real][:, K:][gate] == 0).all()
+    assert not torch.isnan(dx[real].float()).any()
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "swiglu"])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_product_of_lowest_preactivations(act, fp8):
+    counts, K, N = [5, 0, 20], 128, 128
+    x, w, cnt, kw, real, *_ = forward_case(counts, K, N, act, 4, fp8=fp8, bias=True)
+    kw["bias"][:, :N] = torch.finfo(torch.float32).min
+    status = epd.new_status()
+    y, _ = epd.ep_expert_matmul(x, w, cnt, status, **kw)
+    check_ok(status)
+    assert (y[real] == 0).all()

@@ -566,8 +566,10 @@ struct Output {
                     for (int r = 0; r < 16; ++r) {
                         const float g = element(z[h], r), w = element(u[h], r);
                         const float s = fast_sigmoid(g);
-                        up[h][r] = f[h][r] * g * s;
-                        f[h][r] = f[h][r] * w * (s * (1.0f + g * (1.0f - s)));
+                        // what has no slope (s = 0) is 0 whatever else there is: the products of d
+                        // with the pre-activations, which may overflow, come last
+                        up[h][r] = f[h][r] * (g * s);
+                        f[h][r] = f[h][r] * (w * (s * (1.0f + g * (1.0f - s))));
                     }
                 put_frag<STAGED>(stage, f, at, pitch, left, parts);
                 put_frag<STAGED>(stage, up, at + (int64_t)p.K * 2, pitch, left, parts);
