@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import unpermute_ep_dispatch_gb300 as epd
-from test_operators_gpu import DEV, INF, backward_case, check_ok, forward_case, gen, i32
+from test_operators_gpu import (DEV, INF, backward_case, check_ok, forward_case, gen, i32,
+                                route_inputs, route_ref)
 
 pytestmark = pytest.mark.gpu
 
@@ -209,3 +210,72 @@ def test_product_of_lowest_preactivations(act, fp8):
     y, _ = epd.ep_expert_matmul(x, w, cnt, status, **kw)
     check_ok(status)
     assert (y[real] == 0).all()
+
+
+def choice64(l, scoring, bias):
+    """One row in 64 bits: logits, scores, and what the choice goes by (-inf: cannot be chosen)."""
+    row = [v if v < INF else -INF for v in l.double().tolist()]
+    m = max(row)
+    if scoring == "sigmoid":
+        s = [1 / (1 + math.exp(-v)) if v > -700 else 0.0 for v in row]
+    else:
+        ex = [math.exp(v - m) if m > -INF else 0.0 for v in row]
+        s = [v / max(sum(ex), 1e-300) for v in ex]
+    c = [-INF if v == -INF else a + b for v, a, b in zip(row, s, bias or [0.0] * len(row))]
+    return row, s, c
+
+
+@pytest.mark.parametrize("T,E,k,groups,keep,gs", [
+    (64, 256, 8, 8, 4, "top2"), (33, 60, 6, 6, 2, "max"), (17, 600, 40, 40, 7, "top2"), (21, 96, 7, 3, 3, "top2"),
+    (5, 1030, 9, 2, 1, "top2")])
+@pytest.mark.parametrize("scoring,biased", [("softmax", False), ("softmax", True), ("sigmoid", False), ("sigmoid", True)])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("masked,dtype", [(False, torch.float32), (True, torch.float32), (True, torch.bfloat16)])
+def test_route_every_row(T, E, k, groups, keep, gs, scoring, biased, renorm, masked, dtype):
+    """Every row's picks are right to within the roundings of the 32-bit scores, and its weights
+    are those of its picks. A score is within 8 units, so two sums of two differ by 32 at most;
+    a whole bias of up to 2 makes a value of up to 3, and a sum of up to 6, which round by 2^-23
+    and 2^-22: 2^-20 for the two. Values nearer than `near` may come in either order, and where
+    none are the picks are the 64-bit ones exactly."""
+    l = route_inputs(T, E, dtype, T * 5 + E, masked)
+    bias = torch.randint(-2, 3, (E,), generator=gen(E), device=DEV).float() if biased else None
+    status = epd.new_status()
+    idx, w = epd.ep_route(l, k, status, scoring=scoring, bias=bias, num_groups=groups, topk_groups=keep,
+                          group_score=gs, renormalize=renorm, routed_scale=1.5)
+    check_ok(status)
+    ri, _ = route_ref(l, k, scoring, bias, groups, keep, gs, renorm, 1.5)
+    l, idx, w = l.cpu(), idx.cpu(), w.cpu()
+    bias = None if bias is None else bias.double().tolist()
+    size, exact = E // groups, 0
+    for t in range(T):
+        row, s, c = choice64(l[t], scoring, bias)
+        near = (2.0 ** -20 if biased else 0.0) + 32 * ULP * max(s)
+        got = idx[t].tolist()
+        n = sum(e >= 0 for e in got)
+        assert all(e == -1 for e in got[n:]) and len(set(got[:n])) == n
+        assert all(0 <= e < E and c[e] > -INF for e in got[:n])
+        two = []
+        for g in range(groups):
+            own = sorted((v for v in c[g * size:(g + 1) * size] if v > -INF), reverse=True)
+            two.append(sum(own[:2] if gs == "top2" else own[:1]) if own else -INF)
+        cut = sorted(two, reverse=True)[keep - 1]
+        sure = [g for g in range(groups) if two[g] > cut + near] if keep < groups else range(groups)
+        used = {e // size for e in got[:n]}
+        assert len(used) <= keep and all(two[g] >= cut - near for g in used)
+        order = row if scoring == "softmax" and not biased else c
+        assert all(order[a] >= order[b] - near for a, b in zip(got[:n], got[1:n]))
+        kept = [e for g in sure for e in range(g * size, (g + 1) * size) if c[e] > -INF]
+        assert n >= min(k, len(kept))
+        if n == k:
+            assert all(e in got or order[e] <= order[got[-1]] + near for e in kept)
+        close = keep < groups and any(0 < abs(v - cut) <= near for v in two)
+        live = sorted(order)
+        if not close and not any(0 < b - a <= near for a, b in zip(live, live[1:])):
+            assert got == ri[t].tolist()
+            exact += 1
+        total = sum(s[e] for e in got[:n])
+        for j, e in enumerate(got):
+            want = 0.0 if e < 0 or (renorm and total == 0) else s[e] * 1.5 / (total if renorm else 1.0)
+            assert abs(float(w[t, j]) - want) <= (k + 24) * ULP * 1.5
+    if scoring == "softmax" and not biased and (gs == "max" or keep == groups):
+        assert exact == T
