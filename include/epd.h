@@ -487,8 +487,14 @@ typedef enum {
  *   z[s, :] = x[s, :] . w[e]^T + bias[e]           (fp32 accumulation)
  *   y[s, :] = bf16( act(z[s, :]) + residual[s, :] )
  * and, where `preact` is given, preact[s, :] = bf16(z[s, :]) for the backward pass.
- * Rows that belong to no expert are not written. Each value is rounded once, from fp32;
- * the result does not depend on how blocks are scheduled.
+ * Rows that belong to no expert are not written. Each value is rounded once, from fp32.
+ *
+ * Order of the sums, here and in the two gradients below: it does not depend on how blocks
+ * are scheduled, so that the same call on the same device gives the same bits again. It does
+ * depend on the sizes: a few tiles' long reductions are cut into two or four parts, chosen
+ * from capacity_rows, num_experts, K, N and how many blocks the device runs at a time. The
+ * same rows in a larger buffer, beside other experts or on another device may differ by the
+ * roundings of their fp32 sums.
  *   x: [capacity_rows, K] bfloat16 (K % 8 == 0), or e4m3 (K % 128 == 0) with
  *      x_scale, one fp32 scale per row and 128 columns: the scale of row s of expert e and
  *      column block c is x_scale[s * scale_row_stride + c * scale_col_stride + e *
@@ -530,8 +536,8 @@ EPD_API epd_status_t ep_expert_matmul_dgrad(const epd_expert_rows_t *rows, const
  * Gradients of the weights and the bias: for every expert e
  *   dw[e] = sum over its rows s of dy[s, :]^T x[s, :]   (fp32, rounded once to bfloat16)
  *   dbias[e] = sum over its rows s of dy[s, :]          (float32; NULL to leave it out)
- * in an order that depends on the row numbers alone; 0 for an expert without rows. Rows
- * outside the experts' regions are not used, whatever they hold.
+ * in an order that is fixed for given sizes (see ep_expert_matmul); 0 for an expert without
+ * rows. Rows outside the experts' regions are not used, whatever they hold.
  *   dy: [capacity_rows, N], x: [capacity_rows, K], dw: [E, N, K] bfloat16, 16-byte aligned;
  *   dbias: [E, N] float32; N % 8 == 0, K % 8 == 0.
  */

@@ -6,8 +6,8 @@ import pytest
 import torch
 
 import unpermute_ep_dispatch_gb300 as epd
-from test_operators_gpu import (DEV, INF, backward_case, check_ok, forward_case, gen, i32,
-                                route_inputs, route_ref)
+from test_operators_gpu import (DEV, INF, backward_case, check_ok, forward_case, gen, i32, route_inputs,
+                                route_ref)
 
 pytestmark = pytest.mark.gpu
 
@@ -279,3 +279,31 @@ def test_route_every_row(T, E, k, groups, keep, gs, scoring, biased, renorm, mas
             assert abs(float(w[t, j]) - want) <= (k + 24) * ULP * 1.5
     if scoring == "softmax" and not biased and (gs == "max" or keep == groups):
         assert exact == T
+
+
+@pytest.mark.parametrize("few,many", [(1600, 8 * 1600), (300, 40 * 300)])
+def test_the_same_rows_in_a_larger_buffer(few, many):
+    """A call repeats itself to the bit; the same rows in a buffer of another size may be added up
+    in other parts, and are within the roundings of the sums."""
+    K, N = 4096, 512
+    g = gen(few)
+    x = torch.randn(few, K, generator=g, device=DEV).to(torch.bfloat16)
+    dy = torch.randn(few, N, generator=g, device=DEV).to(torch.bfloat16)
+    w = (torch.randn(1, N, K, generator=g, device=DEV) / 64).to(torch.bfloat16)
+    out = []
+    for cap in (few, few, many):
+        xx, yy = torch.full((cap, K), math.nan, dtype=x.dtype, device=DEV), torch.full((cap, N), math.nan, dtype=x.dtype, device=DEV)
+        xx[:few], yy[:few] = x, dy
+        status, rows = epd.new_status(), dict(expert_start_loc=i32([0]))
+        y, _ = epd.ep_expert_matmul(xx, w, i32([few]), status, **rows)
+        dx = epd.ep_expert_matmul_dgrad(yy, w, i32([few]), status, **rows)
+        dw, db = epd.ep_expert_matmul_wgrad(yy, xx, i32([few]), status, with_dbias=True, **rows)
+        check_ok(status)
+        out.append((y[:few], dx[:few], dw, db))
+    assert all(torch.equal(a, b) for a, b in zip(out[0], out[1]))
+    X, D, W = x.double(), dy.double(), w[0].double()
+    for got in (out[0], out[2]):
+        for v, a, b, n in ((got[0], X, W.t(), K), (got[1], D, W, N), (got[2][0], D.t(), X, few)):
+            want = a @ b
+            assert ((v.double() - want).abs() <= 2 ** -8 * want.abs() + (n + 16) * ULP * (a.abs() @ b.abs())).all()
+        assert ((got[3][0].double() - D.sum(0)).abs() <= (few + 16) * ULP * D.abs().sum(0)).all()
