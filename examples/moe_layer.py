@@ -28,7 +28,9 @@ class _Experts(torch.autograd.Function):
     def forward(ctx, x, logits, w1, b1, w2, b2, layer):
         E, k, status = w1.shape[0], layer.topk, layer.status
         idx, weights = epd.ep_route(logits, k, status, **layer.routing, **layer.choice)
-        ws = layer.workspace(x.shape[0], x.device)
+        # a workspace serves one stream at a time: every pass takes its own, from the allocator of
+        # the stream that it runs on, and gives it back there
+        ws = epd.new_workspace(x.shape[0], k, E, 1, 1, x.device)
         d = epd.ep_dispatch(x, None, idx, E, 1, 1, ws, status, with_is_token_in_rank=False)
         rows = dict(tokens_per_expert=d["tokens_per_expert"], status=status,
                     expert_start_loc=d["expert_start_loc"])
@@ -79,13 +81,6 @@ class MoELayer(torch.nn.Module):
         self.choice = dict(bias=choice_bias, num_groups=num_groups, topk_groups=topk_groups,
                            group_score=group_score)
         self.status = epd.new_status(device)
-        self._workspace = {}
-
-    def workspace(self, tokens, device):
-        if tokens not in self._workspace:
-            self._workspace[tokens] = epd.new_workspace(tokens, self.topk, self.w1.shape[0], 1, 1,
-                                                        device)
-        return self._workspace[tokens]
 
     def forward(self, x):
         logits = x.float() @ self.router.t()
