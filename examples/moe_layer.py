@@ -21,6 +21,19 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import unpermute_ep_dispatch_gb300 as epd  # noqa: E402
 
 
+class _NoSecondDerivative(torch.autograd.Function):
+    """Passes gradients on; a derivative of them is an error. (``once_differentiable`` sees only
+    what depends on the incoming gradient, and these depend on the layer's inputs as well.)"""
+
+    @staticmethod
+    def forward(ctx, anchor, *grads):
+        return tuple(g.view_as(g) for g in grads)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the gradients of the expert operators have no derivative")
+
+
 class _Experts(torch.autograd.Function):
     """y = combine(experts(permute(x))), weighted by the router's top-k weights."""
 
@@ -56,7 +69,10 @@ class _Experts(torch.autograd.Function):
         # a token's gradient is the sum of its rows': the combine with weights of one
         dx = epd.ep_unpermute(dxp, index, torch.ones_like(weights), status)
         dlogits = epd.ep_route_backward(dweights, logits, idx, status, **layer.routing)
-        return dx, dlogits, dw1, db1, dw2, db2, None
+        grads = dx, dlogits, dw1, db1, dw2, db2
+        if torch.is_grad_enabled():  # create_graph
+            grads = _NoSecondDerivative.apply(torch.empty(0, requires_grad=True), *grads)
+        return *grads, None
 
 
 class MoELayer(torch.nn.Module):

@@ -51,3 +51,13 @@ def test_batches_of_many_sizes_leave_nothing_behind():
         return torch.cuda.memory_allocated()
     first = run(1)
     assert all(run(t) <= first for t in range(2, 40))
+
+
+def test_second_derivative_is_refused():
+    """The gradients have none of their own: a loss that needs it is an error, not a wrong number."""
+    from examples.moe_layer import MoELayer
+    layer = MoELayer(64, 32, 16, 2)
+    x = torch.randn(20, 64, device="cuda").to(torch.bfloat16).requires_grad_()
+    dx, = torch.autograd.grad(layer(x).float().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="no derivative"):
+        (layer(x).float().sum() + dx.float().pow(2).sum()).backward()
