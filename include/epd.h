@@ -464,7 +464,9 @@ EPD_API epd_status_t ep_route_backward(const float *grad_weights, const void *lo
  * EPD_ERR_INVALID_ARG in *status and counts as no rows; a region that does not end within
  * capacity_rows (or within its rectangle) sets EPD_ERR_CAPACITY and is cut there. The
  * products' kernels wait for their own copies and matrix instructions only; each wait is
- * bounded (two seconds) and running out sets EPD_ERR_TIMEOUT.
+ * bounded (two seconds, and two microseconds for each 64 elements of the longest reduction
+ * that the buffers hold) and running out sets EPD_ERR_TIMEOUT: the kernel then lets what it
+ * has in flight land, and returns.
  */
 typedef struct {
     int num_experts;
@@ -623,6 +625,19 @@ EPD_API epd_status_t epd_test_layout_stalled_tile(const int64_t *topk_idx, int n
                                           uint8_t *is_token_in_rank, void *workspace,
                                           int32_t *status, int stalled_tile,
                                           uint32_t spin_limit, epd_stream_t stream);
+
+/*
+ * Test hook for failure detection, not part of the path: runs ep_expert_matmul (without bias,
+ * residual and preact) with every wait bounded by `wait_ns` nanoseconds (>= 1) and with each
+ * pair of blocks leaving out the matrix instructions from its tile number `stalled_tile` on
+ * (-1: none), so that the waits for them run out. The call still completes; *status then
+ * holds EPD_ERR_TIMEOUT and y is meaningless.
+ */
+EPD_API epd_status_t epd_test_expert_matmul_stalled(
+    const epd_expert_rows_t *rows, const void *x, epd_dtype_t dtype, const float *x_scale,
+    int64_t scale_row_stride, int64_t scale_col_stride, int64_t scale_expert_stride, const void *w,
+    const float *w_scale, int in_features, int out_features, epd_activation_t activation, void *y,
+    int32_t *status, int stalled_tile, int64_t wait_ns, epd_stream_t stream);
 
 #ifdef __cplusplus
 }

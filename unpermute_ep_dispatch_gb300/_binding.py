@@ -85,6 +85,8 @@ SIGNATURES = {
     "ep_expert_matmul_wgrad": (_I, [_ROWS, _P, _P, _I, _I, _P, _P, _P, _P]),
     "ep_unpermute_backward": (_I, [_P, _P, _I64, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
     "ep_dispatch_layout_noalloc": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "epd_test_expert_matmul_stalled": (_I, [_ROWS, _P, _I, _P, _I64, _I64, _I64, _P, _P, _I, _I, _I,
+                                            _P, _P, _I, _I64, _P]),
     "epd_test_layout_stalled_tile": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _I,
                                           _U32, _P]),
 }
@@ -858,3 +860,18 @@ def epd_test_layout_stalled_tile(topk_idx, num_experts, num_ranks, num_rdma_rank
         _ptr(workspace), _ptr(status), int(stalled_tile), int(spin_limit), _stream(stream, dev))
     _check(rc, "epd_test_layout_stalled_tile")
     return per_r, per_n, per_e, itr
+
+
+def epd_test_expert_matmul_stalled(x, w, tokens_per_expert, expert_start_loc, status, y,
+                                   activation="none", x_scale=None, w_scale=None,
+                                   stalled_tile: int = 0, wait_ns: int = 5_000_000, stream=None):
+    """Failure-detection hook: the product with matrix instructions left out (see epd.h)."""
+    act = _choose(ACTIVATION, activation, "activation")
+    E, NW, K = w.shape
+    rows = _expert_rows(tuple(x.shape), E, tokens_per_expert, expert_start_loc, x.device)
+    rc = load_library().epd_test_expert_matmul_stalled(
+        ctypes.byref(rows), _ptr(x), EPD_BF16 if x_scale is None else EPD_FP8_E4M3, _ptr(x_scale),
+        K // 128, 1, 0, _ptr(w), _ptr(w_scale), K, NW // 2 if act == 4 else NW, act, _ptr(y),
+        _ptr(status), int(stalled_tile), int(wait_ns), _stream(stream, x.device))
+    _check(rc, "epd_test_expert_matmul_stalled")
+    return y

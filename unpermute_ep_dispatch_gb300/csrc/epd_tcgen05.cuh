@@ -43,22 +43,22 @@ __device__ __forceinline__ bool mbar_try_pipe(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Waits for phase `parity` of `bar`, for two seconds or 2^24 polls at most: a wait inside
-// these kernels is for one tile's work (microseconds), so running out means that something
-// is wrong, and the kernel returns with an error instead of hanging. The waits are at block
+// Waits for phase `parity` of `bar`, for `limit` nanoseconds at most: a wait inside these kernels is
+// for a tile's work or less, so running out means that something is wrong, and the kernel returns
+// with an error instead of hanging. The waits are at block
 // scope: what they order is the work of the TMA and tensor-core units, and a wait that
 // acquires at cluster scope costs hundreds of cycles (dense 8192^3: 1558 us with, 661 us
 // without); the few that read another block's shared memory do.
 template <bool CLUSTER = false>
-__device__ __forceinline__ bool mbar_wait_pipe(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool mbar_wait_pipe(uint32_t bar, uint32_t parity, uint64_t limit) {
     if (mbar_try_pipe<CLUSTER>(bar, parity)) return true;
     uint64_t t0 = 0;
-    for (uint32_t i = 1; i < (1u << 24); ++i) {
+    for (uint32_t i = 1; i != 0; ++i) {
         if (mbar_try_pipe<CLUSTER>(bar, parity)) return true;
         if ((i & 255u) == 0) {
             const uint64_t t = global_ns();
             if (t0 == 0) t0 = t;
-            if (t - t0 > 2000000000ull) return false;
+            if (t - t0 > limit) return false;
         }
     }
     return false;
@@ -209,6 +209,11 @@ __device__ __forceinline__ float4 ld_cluster16f(uint32_t addr) {
 
 __device__ __forceinline__ void sts16(uint32_t addr, const uint4 &v) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// To the shared memory of any block of the cluster (an address from map_to_rank).
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // A value in both halves of a pair.

@@ -84,6 +84,12 @@ constexpr int kGroupTiles = 8;                  // row tiles that share a pass o
 
 constexpr int kStages = 6;
 
+// A wait's limit, and what each step of the longest reduction adds to it: a wait may be for a whole
+// tile, whose steps take 0.1 to 0.5 us each (wgrad of 2^31 rows of one expert: 2^25 steps).
+constexpr uint64_t kWaitNs = 2000000000, kWaitStepNs = 2000;
+constexpr uint64_t kDrainNs = 1000000000;  // of a wait for what is in flight once another has run out
+constexpr uint32_t kConsumed = 0xffffffff;
+
 // Where few tiles leave most SMs idle, up to four pairs share a tile's reduction, which costs
 // 1 to 2 us for the larger cluster and the sums' way between blocks, and takes 0.16 us a step
 // (e4m3 0.24) off as many steps as the others do. It is done from kSharedSteps / parts steps on,
@@ -118,6 +124,8 @@ struct ExpertArgs {
     const uint8_t *dy;  // wgrad: the rows that dbias sums
     float *dbias;
     int32_t *status;
+    uint64_t wait_ns;  // limit of a wait
+    int stall;         // a test's: the first tile, of each pair, whose mma are left out (-1: none)
 };
 
 // The rows of expert e as they may be read: clipped, with an error where they do not fit.
@@ -174,8 +182,8 @@ struct Ring {
     uint32_t parity = 0;
 
     // Waits for the next tile. The slot stays this warp's until drop().
-    __device__ __forceinline__ bool next(bool &ok) {
-        ok = mbar_wait_pipe(full + 8 * at, parity);
+    __device__ __forceinline__ bool next(bool &ok, const ExpertArgs &p) {
+        ok = mbar_wait_pipe(full + 8 * at, parity, p.wait_ns);
         return ok && slots[at].e >= 0;
     }
     __device__ __forceinline__ const Tile &tile() const { return slots[at]; }
@@ -391,7 +399,8 @@ struct Ahead {
 
 // Sixteen values a lane to the same lane of the pair's other warp, by way of the staging rows.
 template <int STAGED>
-__device__ __forceinline__ bool swap_half(uint32_t mine, uint32_t other, uint32_t bar, const float (&out)[16], float (&in)[16]) {
+__device__ __forceinline__ bool swap_half(uint32_t mine, uint32_t other, uint32_t bar, const float (&out)[16], float (&in)[16],
+                                          const ExpertArgs &p) {
     constexpr int kAtOnce = STAGED / 8;  // of the sixteen's four parts: 512 bytes each
     const uint32_t at = (threadIdx.x & 31) * 16;
     bool ok = true;
@@ -404,14 +413,14 @@ __device__ __forceinline__ bool swap_half(uint32_t mine, uint32_t other, uint32_
                   make_uint4(__float_as_uint(out[4 * i]), __float_as_uint(out[4 * i + 1]),
                              __float_as_uint(out[4 * i + 2]), __float_as_uint(out[4 * i + 3])));
         mbar_arrive_own(bar);  // of 64: the barrier's two phases, written and read, end as they began
-        ok = ok && mbar_wait_pipe(bar, 0);
+        ok = ok && mbar_wait_pipe(bar, 0, p.wait_ns);
 #pragma unroll
         for (int i = p0; i < p0 + kAtOnce; ++i) {
             const float4 v = lds16f(other + (i - p0) * 512 + at);
             in[4 * i] = v.x, in[4 * i + 1] = v.y, in[4 * i + 2] = v.z, in[4 * i + 3] = v.w;
         }
         mbar_arrive_own(bar);
-        ok = ok && mbar_wait_pipe(bar, 1);
+        ok = ok && mbar_wait_pipe(bar, 1, p.wait_ns);
     }
     return __all_sync(0xffffffffu, ok);
 }
@@ -468,9 +477,9 @@ __device__ __forceinline__ void tell_first(uint32_t bar) {
 }
 
 // This warp's sums are left for the others, and theirs are there.
-__device__ __forceinline__ bool exchange(uint32_t parked, const Tile &t) {
+__device__ __forceinline__ bool exchange(uint32_t parked, const Tile &t, const ExpertArgs &p) {
     tell_others(parked, t);
-    return __all_sync(0xffffffffu, mbar_wait_pipe<true>(parked, 0)) != 0;
+    return __all_sync(0xffffffffu, mbar_wait_pipe<true>(parked, 0, p.wait_ns)) != 0;
 }
 
 // Element r of fragments f[h] in the words that Ahead::turn gives.
@@ -600,11 +609,11 @@ struct Output {
             // the other what it needs for them
             float in[16];
             if (up) {
-                ok = ok && swap_half<STAGED>(stage, other, bar, f[0], in);
+                ok = ok && swap_half<STAGED>(stage, other, bar, f[0], in, p);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) f[1][r] = in[r] * fast_sigmoid(in[r]) * f[1][r];
             } else {
-                ok = ok && swap_half<STAGED>(stage, other, bar, f[1], in);
+                ok = ok && swap_half<STAGED>(stage, other, bar, f[1], in, p);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) f[1][r] = f[0][r] * fast_sigmoid(f[0][r]) * in[r];
             }
@@ -785,8 +794,9 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(after);
     constexpr int kEmpty = kStages, kAccFull = 2 * kStages, kAccEmpty = kAccFull + kAccs,
                   kScFull = kAccEmpty + kAccs, kScEmpty = kScFull + 2, kTileFull = kScEmpty + 2, kTileEmpty = kTileFull + kRing,
-                  kSwap = kTileEmpty + kRing, kParked = kSwap + kEpiWarps / 2, kFetched = kParked + 1, kSlot = kFetched + 1;
-    static_assert((kSlot + 1) * 8 + kRing * sizeof(Tile) <= kTailBytes, "the barriers fit");
+                  kSwap = kTileEmpty + kRing, kParked = kSwap + kEpiWarps / 2, kFetched = kParked + 1,
+                  kDrained = kFetched + 1, kSlot = kDrained + 1, kFailed = kSlot + 1;
+    static_assert((kFailed + 2) * 8 + kRing * sizeof(Tile) <= kTailBytes, "the barriers fit");
     const uint32_t base = smem_addr(smem), bar0 = smem_addr(bars);
     const uint32_t full = bar0, empty = bar0 + 8 * kEmpty, acc_full = bar0 + 8 * kAccFull,
                    acc_empty = bar0 + 8 * kAccEmpty, sc_full = bar0 + 8 * kScFull, sc_empty = bar0 + 8 * kScEmpty;
@@ -795,6 +805,10 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
     // this block's place in its pair, and the pair's in a cluster that shares a reduction
     const int in_cluster = (int)cluster_ctarank();
     const int rank = SPLIT ? in_cluster & 1 : in_cluster, lead = SPLIT ? in_cluster - rank : 0;
+    // [0]: a wait of the cluster's ran out; [1], [2], in the leader: the steps that each block's producer
+    // has issued loads of, where it did not see them all consumed. (Not kept: e4m3 has no registers
+    // for it.)
+    const auto failed = [&] { return reinterpret_cast<volatile uint32_t *>(bars + kFailed); };
     const int part = SPLIT ? lead / 2 : 0, parts = SPLIT ? (int)cluster_blocks() / 2 : 1;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -818,6 +832,9 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
             mbar_init(bars + kParked, (parts - 1) * kEpiWarps);
             mbar_init(bars + kFetched, (FP8 ? 1 : parts - 1) * kEpiWarps);
         }
+        mbar_init(bars + kDrained, 1);
+        failed()[0] = 0;
+        failed()[1] = failed()[2] = kConsumed;
         mbar_init_fence();
         for (int i = 0; i < Maps<MODE>::kM; ++i) tma_prefetch_map(&maps.m[i]);
         for (int i = 0; i < Maps<MODE>::kN; ++i) tma_prefetch_map(&maps.n[i]);
@@ -858,11 +875,11 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
                     if (tile == first) {
                         walk.cut(t, part, parts);
                     } else if (!FP8 || part > 0) {  // the stages are free again once the sums are fetched
-                        if (!(ok = mbar_wait_pipe<true>(bar0 + 8 * kFetched, 0))) break;
+                        if (!(ok = mbar_wait_pipe<true>(bar0 + 8 * kFetched, 0, p.wait_ns))) break;
                         fence_proxy_async();
                     }
                 }
-                if (!(ok = mbar_wait_pipe(ring.empty + 8 * ring.at, ring.parity ^ 1))) break;
+                if (!(ok = mbar_wait_pipe(ring.empty + 8 * ring.at, ring.parity ^ 1, p.wait_ns))) break;
                 if (elect_one()) {
                     if (!more) t.e = -1;
                     slots[ring.at] = t;
@@ -876,6 +893,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
                 const int boxes = (half + 63) / 64;  // wgrad
                 const uint32_t bytes = kOperandBytes + (MODE == kWgrad ? boxes * 64 : half) * 128;
                 // one thread runs the tile's steps, the warp rejoins for the next tile
+                int done = 0;
                 if (elect_one()) {
                     // this block's features: gated, 64 and their up, or all 128 of one kind
                     const int feat = t.feat0 + rank * (!t.across ? (kHalf ? p.N : t.n / 2) : kHalf ? 64 : 128);
@@ -885,7 +903,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
                     const uint32_t b_at = base + (t.across ? kOperandBytes : 0);
                     for (int i = 0; i < t.steps; ++i) {
                         const int k = SPLIT ? t.step0 + i : i;
-                        if (!(ok = mbar_wait_pipe(empty + 8 * stage, parity))) break;
+                        if (!(ok = mbar_wait_pipe(empty + 8 * stage, parity, p.wait_ns))) break;
                         const uint32_t a = a_at + stage * kStageBytes, b = b_at + stage * kStageBytes;
                         const uint32_t bar = lead_full + 8 * stage;
                         if (MODE == kWgrad) {
@@ -933,30 +951,33 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
                             }
                         }
                         if (++stage == kStages) stage = 0, parity ^= 1;
+                        ++done;
                     }
                 }
                 ok = __all_sync(0xffffffffu, ok);
-                issued += t.steps;
+                issued += ok ? t.steps : __reduce_max_sync(0xffffffffu, done);
                 stage = __shfl_sync(0xffffffffu, issued % kStages, 0);
                 parity = 1 ^ ((issued / kStages) & 1);
             }
             // every stage's last release arrives before this block may go (a stage that was never
             // used counts as released)
             for (int i = 0; ok && i < kStages; ++i) {
-                ok = mbar_wait_pipe(empty + 8 * stage, parity);
+                ok = mbar_wait_pipe(empty + 8 * stage, parity, p.wait_ns);
                 if (++stage == kStages) stage = 0, parity ^= 1;
             }
+            if (!ok && lane == 0) st_cluster(map_to_rank(smem_addr(bars + kFailed) + 4 + 4 * rank, lead), issued);
         } else if (warp == kMmaWarp) {
             const uint16_t pair_mask = (uint16_t)(3 << lead);
             const uint64_t desc_a = smem_desc(base, 8192), desc_b = smem_desc(base + kOperandBytes, 8192);
-            int stage = 0, acc = 0, was = -1;
+            int stage = 0, acc = 0, was = -1, tiles = 0;
             uint32_t parity = 0, parities = (1u << kAccs) - 1;  // of each accumulator's next release
-            while (rank == 0 && ring.next(ok)) {
+            while (rank == 0 && ring.next(ok, p)) {
                 const int steps = ring.tile().steps, n = ring.tile().n;
                 // wgrad: rows of the region's last step, if it is this pair's and not a full one
                 const int left = !SPLIT || ring.tile().part == ring.tile().parts - 1 ? ring.tile().count & 63 : 0;
                 const int across = ring.tile().across;
                 ring.drop();
+                if (tiles++ == p.stall) break;
                 if (steps == 0) continue;
                 const uint32_t desc = mma_desc<FP8, MODE != kForward, MODE == kWgrad>(n);
                 const int accs = FP8 && !across ? 2 : kAccs, columns = 512 / accs;
@@ -965,14 +986,14 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
                 uint32_t ph = parity, aph = parities;
                 if (elect_one()) {
                     if (FP8 && across != was && was >= 0)  // other accumulators lie where these will
-                        for (int i = 0; ok && i < kAccs; ++i) ok = mbar_wait_pipe(acc_empty + 8 * i, (aph >> i) & 1);
+                        for (int i = 0; ok && i < kAccs; ++i) ok = mbar_wait_pipe(acc_empty + 8 * i, (aph >> i) & 1, p.wait_ns);
                     for (int k = 0; ok && k < steps; ++k) {
                         const bool fresh = FP8 || k == 0, last = FP8 || k == steps - 1;
                         if (fresh) {
-                            if (!(ok = mbar_wait_pipe(acc_empty + 8 * c, (aph >> c) & 1))) break;
+                            if (!(ok = mbar_wait_pipe(acc_empty + 8 * c, (aph >> c) & 1, p.wait_ns))) break;
                             aph ^= 1u << c;
                         }
-                        if (!(ok = mbar_wait_pipe(full + 8 * st, ph))) break;
+                        if (!(ok = mbar_wait_pipe(full + 8 * st, ph, p.wait_ns))) break;
                         tcgen05_fence_after();
                         // a quarter of the stage's reduction: 32 bytes along a K-major row, or
                         // 16 rows of 128 bytes
@@ -1021,7 +1042,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
             const int64_t blocks = ((GATED ? 2 * p.N : p.N) + 127) / 128;
             int buf = 0;
             uint32_t parity = 1;
-            while (ok && ring.next(ok)) {
+            while (ok && ring.next(ok, p)) {
                 const Tile t = ring.tile();
                 ring.drop();
                 // the tile's two weight blocks; across: this block's (gated: its gate's and its up's)
@@ -1053,7 +1074,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
                                 sx[i][k] = c < rows && g + k < C ? xs[c * p.srow + (g + k) * p.scol] : 0.0f;
                         }
                     }
-                    if (!(ok = mbar_wait_pipe(sc_empty + 8 * buf, parity))) break;
+                    if (!(ok = mbar_wait_pipe(sc_empty + 8 * buf, parity, p.wait_ns))) break;
                     if (!t.across) {  // a row's two, side by side
                         float2 *dst = reinterpret_cast<float2 *>(scales) + buf * kScaleGroup * 128 + tid;
 #pragma unroll
@@ -1092,7 +1113,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
             const float2 *my_scales = reinterpret_cast<const float2 *>(scales) + quadrant * 32 + lane;
             int sbuf = 0;
             uint32_t sparity = 0;
-            while (ok && ring.next(ok)) {
+            while (ok && ring.next(ok, p)) {
                 const int steps = ring.tile().steps;
                 if (ring.tile().across) {
                     // a lane is a feature, in fragments; the warp's columns are share * 32 .. + 31
@@ -1106,8 +1127,8 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
                         for (int r = 0; r < 16; ++r) acc[h][r] = 0.0f;
                     for (int k = 0; k < steps; ++k) {
                         const int u = k % kScaleGroup, c = k % kAccs;
-                        if (u == 0 && !(ok = mbar_wait_pipe(sc_full + 8 * sbuf, sparity))) break;
-                        if (!(ok = mbar_wait_pipe(acc_full + 8 * c, (parities >> c) & 1))) break;
+                        if (u == 0 && !(ok = mbar_wait_pipe(sc_full + 8 * sbuf, sparity, p.wait_ns))) break;
+                        if (!(ok = mbar_wait_pipe(acc_full + 8 * c, (parities >> c) & 1, p.wait_ns))) break;
                         parities ^= 1u << c;
                         tcgen05_fence_after();
                         if (own) {
@@ -1142,7 +1163,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
                             ring.drop();
                             continue;
                         }
-                        if (!(ok = __all_sync(0xffffffffu, mbar_wait_pipe<true>(bar0 + 8 * kParked, 0)))) break;
+                        if (!(ok = __all_sync(0xffffffffu, mbar_wait_pipe<true>(bar0 + 8 * kParked, 0, p.wait_ns)))) break;
                         if (own) add_parked(at, ring.tile(), sum);
                         tell_others(bar0 + 8 * kFetched, ring.tile());
                     }
@@ -1165,9 +1186,9 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
                     for (int r = 0; r < 32; ++r) acc[h][r] = 0.0f;
                 for (int k = 0; k < steps; ++k) {
                     const int u = k % kScaleGroup, c = k & 1;
-                    if (u == 0 && !(ok = mbar_wait_pipe(sc_full + 8 * sbuf, sparity))) break;
+                    if (u == 0 && !(ok = mbar_wait_pipe(sc_full + 8 * sbuf, sparity, p.wait_ns))) break;
                     const float2 sc = my_scales[(sbuf * kScaleGroup + u) * 128];
-                    if (!(ok = mbar_wait_pipe(acc_full + 8 * c, (parities >> c) & 1))) break;
+                    if (!(ok = mbar_wait_pipe(acc_full + 8 * c, (parities >> c) & 1, p.wait_ns))) break;
                     parities ^= 1u << c;
                     tcgen05_fence_after();
 #pragma unroll
@@ -1206,7 +1227,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
                         ring.drop();
                         continue;
                     }
-                    if (!(ok = __all_sync(0xffffffffu, mbar_wait_pipe<true>(bar0 + 8 * kParked, 0)))) break;
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait_pipe<true>(bar0 + 8 * kParked, 0, p.wait_ns)))) break;
                     if (blocks > 0) add_parked(at, ring.tile(), gate), add_parked(at + 4096, ring.tile(), rest);
                     tell_others(bar0 + 8 * kFetched, ring.tile());
                 }
@@ -1217,7 +1238,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
         } else {
             Output<MODE, GATED, kStagedOf<FP8>> out(p, staging, bar0 + 8 * kSwap, warp);
             int buf = 0;
-            while (ok && ring.next(ok)) {
+            while (ok && ring.next(ok, p)) {
                 const Tile &t = ring.tile();
                 out.begin(t, rank, quadrant);
                 const int chunks = t.n / 32;
@@ -1230,7 +1251,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
                 ring.drop();
                 if (from < chunks) out.fetch(from * 32);
                 if (any) {
-                    if (!(ok = mbar_wait_pipe(acc_full + 8 * buf, (parities >> buf) & 1))) break;
+                    if (!(ok = mbar_wait_pipe(acc_full + 8 * buf, (parities >> buf) & 1, p.wait_ns))) break;
                     parities ^= 1u << buf;
                     tcgen05_fence_after();
                 }
@@ -1253,7 +1274,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
                         load(f, ch);
                         park(base + (ch * 4 + quadrant) * 4096, [&](int r) -> float & { return f[r >> 4][r & 15]; });
                     }
-                    if (!(ok = exchange(bar0 + 8 * kParked, part_of))) break;
+                    if (!(ok = exchange(bar0 + 8 * kParked, part_of, p))) break;
                 }
                 for (int ch = from; ch < chunks; ch += by) {
                     Frag f;
@@ -1274,13 +1295,41 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
             }
         }
     }
-    if (!ok && lane == 0) report(p.status, EPD_ERR_TIMEOUT);
+    if (!ok && lane == 0) {
+        report(p.status, EPD_ERR_TIMEOUT);
+        for (int i = 0; i < (int)cluster_blocks(); ++i) st_cluster(map_to_rank(smem_addr(bars + kFailed), i), 1);
+    }
     __syncwarp();
     tcgen05_fence_before();
     __syncthreads();
     cluster_arrive_release();
     cluster_wait_acquire();
     tcgen05_fence_after();
+    if (*failed()) {
+        // Nobody issues any more. What is in flight lands before the blocks go: loads write to their
+        // shared memory, matrix instructions to tensor memory.
+        const int first_of = (int)cluster_ctarank() & ~1;  // the pair's leader
+        const bool leads = first_of == (int)cluster_ctarank();
+        if (leads && threadIdx.x == 0) {
+            const uint32_t mine = failed()[1], other = failed()[2];
+            if (mine != kConsumed && other != kConsumed) {
+                const uint32_t both = min(mine, other), any = max(mine, other);
+                for (uint32_t i = any > kStages ? any - kStages : 0; i < any; ++i) {
+                    const uint32_t bar = smem_addr(bars + i % kStages);
+                    if (i >= both) mbar_arrive_own(bar);  // for the producer that did not get there
+                    mbar_wait_pipe(bar, i / kStages & 1, kDrainNs);
+                }
+            }
+        }
+        if (leads && threadIdx.x / 32 == kMmaWarp) {
+            if (elect_one()) mma_commit_pair(smem_addr(bars + kDrained), (uint16_t)(3 << first_of));
+            __syncwarp();
+        }
+        if (threadIdx.x == 0) mbar_wait_pipe(smem_addr(bars + kDrained), 0, kDrainNs);
+        __syncthreads();
+        cluster_arrive_release();
+        cluster_wait_acquire();
+    }
     if (warp == kMmaWarp) tmem_free_pair(tmem, 512);
 }
 
@@ -1355,7 +1404,7 @@ epd_status_t resident(int parts, int &clusters) {
 }
 
 template <int MODE, bool FP8, bool GATED>
-epd_status_t launch(const Maps<MODE> &maps, const ExpertArgs &p, cudaStream_t stream) {
+epd_status_t launch(const Maps<MODE> &maps, ExpertArgs p, cudaStream_t stream) {
     const int features = MODE == kForward ? p.N : p.K;
     const int64_t feat_tiles = (features + (GATED && MODE == kForward ? 127 : 255)) / (GATED && MODE == kForward ? 128 : 256);
     const int64_t cap = p.rows.capacity_rows, E = p.rows.num_experts;
@@ -1370,6 +1419,8 @@ epd_status_t launch(const Maps<MODE> &maps, const ExpertArgs &p, cudaStream_t st
     // reduction)
     const int64_t rows = cap / E, columns = MODE == kWgrad ? p.N : rows;
     const int64_t steps = ((MODE == kForward ? p.K : MODE == kDgrad ? p.N : rows) + (FP8 ? 127 : 63)) / (FP8 ? 128 : 64);
+    // (wgrad: one expert may have all the rows)
+    if (p.wait_ns == 0) p.wait_ns = kWaitNs + (MODE == kWgrad ? (cap + 63) / 64 : steps) * kWaitStepNs;
     for (int parts = 4; parts > 1; parts /= 2) {
         if (columns > kWideRows ? steps < kSharedStepsWide<FP8> : steps * parts < kSharedSteps<FP8>) continue;
         if (most * parts > sm_count() / 2) continue;
@@ -1400,15 +1451,14 @@ bool act_ok(int act) { return act >= EPD_ACT_NONE && act <= EPD_ACT_SWIGLU; }
 }  // namespace
 }  // namespace epd
 
-extern "C" epd_status_t ep_expert_matmul(const epd_expert_rows_t *rows, const void *x,
-                                         epd_dtype_t dtype, const float *x_scale,
-                                         int64_t scale_row_stride, int64_t scale_col_stride,
-                                         int64_t scale_expert_stride, const void *w,
-                                         const float *w_scale, int in_features, int out_features,
-                                         epd_activation_t activation, const float *bias,
-                                         const void *residual, void *y, void *preact,
-                                         int32_t *status, epd_stream_t stream) {
-    using namespace epd;
+namespace epd {
+namespace {
+
+epd_status_t forward(const epd_expert_rows_t *rows, const void *x, epd_dtype_t dtype, const float *x_scale,
+                     int64_t scale_row_stride, int64_t scale_col_stride, int64_t scale_expert_stride, const void *w,
+                     const float *w_scale, int in_features, int out_features, epd_activation_t activation,
+                     const float *bias, const void *residual, void *y, void *preact, int32_t *status,
+                     epd_stream_t stream, int stall, uint64_t wait_ns) {
     const int K = in_features, N = out_features;
     const bool fp8 = dtype == EPD_FP8_E4M3, gated = activation == EPD_ACT_SWIGLU;
     if (!rows_ok(rows) || !act_ok(activation)) return EPD_ERR_INVALID_ARG;
@@ -1425,6 +1475,8 @@ extern "C" epd_status_t ep_expert_matmul(const epd_expert_rows_t *rows, const vo
         (preact && !aligned16(preact)))
         return EPD_ERR_INVALID_ARG;
     ExpertArgs p = {};
+    p.stall = stall;
+    p.wait_ns = wait_ns;
     p.rows = *rows;
     p.act = activation;
     p.x_scale = x_scale;
@@ -1466,6 +1518,32 @@ extern "C" epd_status_t ep_expert_matmul(const epd_expert_rows_t *rows, const vo
     return gated ? launch<kForward, false, true>(maps, p, st) : launch<kForward, false, false>(maps, p, st);
 }
 
+}  // namespace
+}  // namespace epd
+
+extern "C" epd_status_t ep_expert_matmul(const epd_expert_rows_t *rows, const void *x,
+                                         epd_dtype_t dtype, const float *x_scale,
+                                         int64_t scale_row_stride, int64_t scale_col_stride,
+                                         int64_t scale_expert_stride, const void *w,
+                                         const float *w_scale, int in_features, int out_features,
+                                         epd_activation_t activation, const float *bias,
+                                         const void *residual, void *y, void *preact,
+                                         int32_t *status, epd_stream_t stream) {
+    return epd::forward(rows, x, dtype, x_scale, scale_row_stride, scale_col_stride, scale_expert_stride, w, w_scale,
+                        in_features, out_features, activation, bias, residual, y, preact, status, stream, -1, 0);
+}
+
+extern "C" epd_status_t epd_test_expert_matmul_stalled(
+    const epd_expert_rows_t *rows, const void *x, epd_dtype_t dtype, const float *x_scale, int64_t scale_row_stride,
+    int64_t scale_col_stride, int64_t scale_expert_stride, const void *w, const float *w_scale, int in_features,
+    int out_features, epd_activation_t activation, void *y, int32_t *status, int stalled_tile, int64_t wait_ns,
+    epd_stream_t stream) {
+    if (wait_ns < 1) return EPD_ERR_INVALID_ARG;
+    return epd::forward(rows, x, dtype, x_scale, scale_row_stride, scale_col_stride, scale_expert_stride, w, w_scale,
+                        in_features, out_features, activation, nullptr, nullptr, y, nullptr, status, stream,
+                        stalled_tile, (uint64_t)wait_ns);
+}
+
 extern "C" epd_status_t ep_expert_matmul_dgrad(const epd_expert_rows_t *rows, const void *dy,
                                                const void *w, int in_features, int out_features,
                                                epd_activation_t activation, const void *preact,
@@ -1481,6 +1559,7 @@ extern "C" epd_status_t ep_expert_matmul_dgrad(const epd_expert_rows_t *rows, co
     if (!dy || !aligned16(dy) || !dx || !aligned16(dx) || (preact && !aligned16(preact)))
         return EPD_ERR_INVALID_ARG;
     ExpertArgs p = {};
+    p.stall = -1;
     p.rows = *rows;
     p.act = activation;
     p.K = K;
@@ -1513,6 +1592,7 @@ extern "C" epd_status_t ep_expert_matmul_wgrad(const epd_expert_rows_t *rows, co
     if (rows->capacity_rows > 0 && (!dy || !aligned16(dy) || !x || !aligned16(x)))
         return EPD_ERR_INVALID_ARG;
     ExpertArgs p = {};
+    p.stall = -1;
     p.rows = *rows;
     p.K = K;
     p.N = N;
