@@ -195,6 +195,12 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
     return v;
 }
 
+__device__ __forceinline__ uint32_t lds4(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ float4 lds16f(uint32_t addr) {
     const uint4 v = lds16(addr);
     return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));

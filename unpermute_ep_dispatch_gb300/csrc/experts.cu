@@ -773,6 +773,33 @@ __device__ __forceinline__ void sum_bias(const ExpertArgs &p, int worker, int wo
     }
 }
 
+// A wait of this cluster ran out, and nobody in it issues any more. What is in flight lands before
+// its blocks go: loads write to their shared memory, matrix instructions to tensor memory. `issued`
+// (shared memory of a pair's first block): the steps that each of its producers has issued loads of.
+// A function of its own, so that its instructions are not among those that every call fetches (0.1 us).
+__device__ __noinline__ void drain(uint32_t full, uint32_t drained, uint32_t issued, int mma_warp) {
+    const int rank = (int)cluster_ctarank(), lead = rank & ~1;
+    if (rank == lead && threadIdx.x == 0) {
+        const uint32_t mine = lds4(issued), other = lds4(issued + 4);
+        if (mine != kConsumed && other != kConsumed) {
+            const uint32_t both = min(mine, other), any = max(mine, other);
+            for (uint32_t i = any > kStages ? any - kStages : 0; i < any; ++i) {
+                const uint32_t bar = full + 8 * (i % kStages);
+                if (i >= both) mbar_arrive_own(bar);  // for the producer that did not get there
+                mbar_wait_pipe(bar, i / kStages & 1, kDrainNs);
+            }
+        }
+    }
+    if (rank == lead && threadIdx.x / 32 == mma_warp) {
+        if (elect_one()) mma_commit_pair(drained, (uint16_t)(3 << lead));
+        __syncwarp();
+    }
+    if (threadIdx.x == 0) mbar_wait_pipe(drained, 0, kDrainNs);
+    __syncthreads();
+    cluster_arrive_release();
+    cluster_wait_acquire();
+}
+
 template <int MODE, bool FP8, bool GATED, bool SPLIT>
 __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
     expert_kernel(const __grid_constant__ Maps<MODE> maps, const ExpertArgs p) {
@@ -1305,31 +1332,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
     cluster_arrive_release();
     cluster_wait_acquire();
     tcgen05_fence_after();
-    if (*failed()) {
-        // Nobody issues any more. What is in flight lands before the blocks go: loads write to their
-        // shared memory, matrix instructions to tensor memory.
-        const int first_of = (int)cluster_ctarank() & ~1;  // the pair's leader
-        const bool leads = first_of == (int)cluster_ctarank();
-        if (leads && threadIdx.x == 0) {
-            const uint32_t mine = failed()[1], other = failed()[2];
-            if (mine != kConsumed && other != kConsumed) {
-                const uint32_t both = min(mine, other), any = max(mine, other);
-                for (uint32_t i = any > kStages ? any - kStages : 0; i < any; ++i) {
-                    const uint32_t bar = smem_addr(bars + i % kStages);
-                    if (i >= both) mbar_arrive_own(bar);  // for the producer that did not get there
-                    mbar_wait_pipe(bar, i / kStages & 1, kDrainNs);
-                }
-            }
-        }
-        if (leads && threadIdx.x / 32 == kMmaWarp) {
-            if (elect_one()) mma_commit_pair(smem_addr(bars + kDrained), (uint16_t)(3 << first_of));
-            __syncwarp();
-        }
-        if (threadIdx.x == 0) mbar_wait_pipe(smem_addr(bars + kDrained), 0, kDrainNs);
-        __syncthreads();
-        cluster_arrive_release();
-        cluster_wait_acquire();
-    }
+    if (*failed()) drain(smem_addr(bars), smem_addr(bars + kDrained), smem_addr(bars + kFailed) + 4, kMmaWarp);
     if (warp == kMmaWarp) tmem_free_pair(tmem, 512);
 }
 
