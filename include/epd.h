@@ -494,8 +494,8 @@ typedef enum {
  * Order of the sums, here and in the two gradients below: it does not depend on how blocks
  * are scheduled, so that the same call on the same device gives the same bits again. It does
  * depend on the sizes: a few tiles' long reductions are cut into two or four parts, chosen
- * from capacity_rows, num_experts, K, N and how many blocks the device runs at a time. The
- * same rows in a larger buffer, beside other experts or on another device may differ by the
+ * from capacity_rows, num_experts, K, N, how many blocks the device runs at a time and, for
+ * wgrad, the expert's rows. The same rows in a larger buffer, beside other experts or on another device may differ by the
  * roundings of their fp32 sums.
  *   x: [capacity_rows, K] bfloat16 (K % 8 == 0), or e4m3 (K % 128 == 0) with
  *      x_scale, one fp32 scale per row and 128 columns: the scale of row s of expert e and

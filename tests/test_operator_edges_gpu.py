@@ -307,3 +307,25 @@ def test_the_same_rows_in_a_larger_buffer(few, many):
             want = a @ b
             assert ((v.double() - want).abs() <= 2 ** -8 * want.abs() + (n + 16) * ULP * (a.abs() @ b.abs())).all()
         assert ((got[3][0].double() - D.sum(0)).abs() <= (few + 16) * ULP * D.abs().sum(0)).all()
+
+
+@pytest.mark.parametrize("counts", [[16], [0], [3, 0, 5000, 70, 1], [1500, 1600, 24 * 64 - 1, 24 * 64]])
+@pytest.mark.parametrize("K,N", [(64, 64), (256, 256)])
+def test_wgrad_of_few_rows_in_a_large_buffer(counts, K, N):
+    """Whether an expert's reduction is shared goes by the rows it has, not by the buffer's: experts
+    that share theirs beside some that do not, and tiles past the first."""
+    g = gen(sum(counts))
+    cap = max(sum(counts), 4096 * len(counts))
+    start = [sum(counts[:e]) for e in range(len(counts))]
+    x = torch.full((cap, K), math.nan, dtype=torch.bfloat16, device=DEV)
+    dy = torch.full((cap, N), math.nan, dtype=torch.bfloat16, device=DEV)
+    n = sum(counts)
+    x[:n], dy[:n] = torch.randn(n, K, generator=g, device=DEV), torch.randn(n, N, generator=g, device=DEV)
+    status = epd.new_status()
+    dw, db = epd.ep_expert_matmul_wgrad(dy, x, i32(counts), status, expert_start_loc=i32(start), with_dbias=True)
+    check_ok(status)
+    for e, (s, c) in enumerate(zip(start, counts)):
+        a, b = dy[s:s + c].double(), x[s:s + c].double()
+        want = a.t() @ b
+        assert ((dw[e].double() - want).abs() <= (c + 16) * ULP * (a.abs().t() @ b.abs()) + 2 ** -8 * want.abs()).all()
+        assert ((db[e].double() - a.sum(0)).abs() <= (c + 16) * ULP * a.abs().sum(0)).all()

@@ -107,6 +107,10 @@ constexpr int kSharedSteps = FP8 ? 64 : 96;
 template <bool FP8>
 constexpr int kSharedStepsWide = FP8 ? 28 : 32;
 constexpr int kWideRows = 128;  // more columns of D on average than these are many
+template <bool FP8>
+__host__ __device__ constexpr bool worth_sharing(int64_t columns, int64_t steps, int parts) {
+    return columns > kWideRows ? steps >= kSharedStepsWide<FP8> : steps * parts >= kSharedSteps<FP8>;
+}
 
 template <bool FP8>
 constexpr int kSmemOf = kStages * kStageBytes + kEpiWarpsOf<FP8> * kStagingOf<FP8> + (FP8 ? kScaleBytes : 0) + kTailBytes;
@@ -896,12 +900,18 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
             const uint32_t lead_full = map_to_rank(full, lead);
             int stage = 0, issued = 0;
             uint32_t parity = 1;
+            bool cut = false;
             for (int tile = first; ok; tile = SPLIT && tile == first ? pairs / parts + pair : tile + pairs) {
                 if (!kEarly || tile != first) more = walk.next(tile, t);
                 if (SPLIT && more) {
                     if (tile == first) {
-                        walk.cut(t, part, parts);
-                    } else if (!FP8 || part > 0) {  // the stages are free again once the sums are fetched
+                        // wgrad: the host knows the rows that there is room for, not those that there are
+                        cut = MODE != kWgrad || worth_sharing<FP8>(p.N, t.steps, parts);
+                        if (cut)
+                            walk.cut(t, part, parts);
+                        else if (part > 0)
+                            continue;
+                    } else if (cut && (!FP8 || part > 0)) {  // the stages are free again once the sums are fetched
                         if (!(ok = mbar_wait_pipe<true>(bar0 + 8 * kFetched, 0, p.wait_ns))) break;
                         fence_proxy_async();
                     }
@@ -1425,7 +1435,7 @@ epd_status_t launch(const Maps<MODE> &maps, ExpertArgs p, cudaStream_t stream) {
     // (wgrad: one expert may have all the rows)
     if (p.wait_ns == 0) p.wait_ns = kWaitNs + (MODE == kWgrad ? (cap + 63) / 64 : steps) * kWaitStepNs;
     for (int parts = 4; parts > 1; parts /= 2) {
-        if (columns > kWideRows ? steps < kSharedStepsWide<FP8> : steps * parts < kSharedSteps<FP8>) continue;
+        if (!worth_sharing<FP8>(columns, steps, parts)) continue;
         if (most * parts > sm_count() / 2) continue;
         const epd_status_t rc = resident<MODE, FP8, GATED, true>(parts, clusters);
         if (rc != EPD_OK) return rc;
