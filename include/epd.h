@@ -77,7 +77,7 @@ typedef enum {
     EPD_ERR_UNSUPPORTED = 2,    /* valid but beyond a documented limit */
     EPD_ERR_CUDA = 3,           /* a CUDA call failed; epd_last_cuda_error() has the cause */
     EPD_ERR_INVALID_EXPERT = 4, /* (status word) topk_idx held an id outside [-1, E) */
-    EPD_ERR_TIMEOUT = 5,        /* (status word) a bounded look-back wait gave up */
+    EPD_ERR_TIMEOUT = 5,        /* (status word) a bounded wait gave up (look-back, products) */
     EPD_ERR_CAPACITY = 6,       /* (status word) a slot fell outside [0, capacity_rows) */
     EPD_ERR_NONFINITE = 7,      /* (status word) a router logit was NaN or +inf, or a bias NaN */
 } epd_status_t;
@@ -438,7 +438,8 @@ EPD_API epd_status_t ep_route(const void *logits, epd_dtype_t dtype, const float
  *   ds[topk_idx[t, j]] += g_j                                     (no renormalize)
  *                      += sum over i of (g_j - g_i) s_i / S / S   (renormalize),
  *   grad_logits = ds * s * (1 - s)                                (sigmoid)
- *               = s * (ds - sum over e of ds_e s_e)               (softmax).
+ *               = s * (ds - sum over e of ds_e s_e)               (softmax),
+ * computed so that neither 1 - s nor that difference cancels.
  * Picks of -1 have no gradient; an id outside [-1, E) sets EPD_ERR_INVALID_EXPERT and
  * counts as -1; a pick whose logit is NaN or +inf sets EPD_ERR_NONFINITE and has score 0.
  * Renormalised softmax weights are the softmax of the picks' logits alone, and are computed
@@ -508,7 +509,7 @@ typedef enum {
  *   bias: [E, NW] float32 or NULL; residual: [capacity_rows, N] bfloat16 or NULL;
  *   y: [capacity_rows, N], preact: [capacity_rows, NW] bfloat16 (preact may be NULL).
  * N % 8 == 0; for EPD_ACT_SWIGLU with e4m3 N % 128 == 0. All row buffers and w
- * 16-byte aligned. One expert over the whole buffer is an ordinary linear layer.
+ * 16-byte aligned. Outputs must not overlap inputs, here and in the gradients. One expert over the whole buffer is an ordinary linear layer.
  */
 EPD_API epd_status_t ep_expert_matmul(const epd_expert_rows_t *rows, const void *x,
                                       epd_dtype_t dtype, const float *x_scale,

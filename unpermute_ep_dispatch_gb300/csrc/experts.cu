@@ -102,6 +102,10 @@ constexpr uint32_t kConsumed = 0xffffffff;
 //     256 rows: K = 2048 15.1 12.0   3584 16.7 16.7
 // in two: K = 3200 11.1 and 11.1, 4096 11.8 and 12.8; with 256 rows, 4096 features, K = 3200 16.6 and
 // 16.2, 4096 17.8 and 19.0. wgrad, 256 x 256, rows = 1536 12.7 and 10.5, 4096 13.6 and 21.0.
+// How many columns there are the host judges by the buffer's rows. In one that is not full the tiles
+// are fewer or narrower than that, and sharing pays all the same (16 rows of 4096, K = 4096, 512
+// features: 10.6 and 13.8, e4m3 9.1 and 11.3); wgrad's steps, which the rows are, the kernel looks at
+// itself (256 x 256, 16 rows of 4096: 4.7, and 9.2 where that is not done).
 template <bool FP8>
 constexpr int kSharedSteps = FP8 ? 64 : 96;
 template <bool FP8>
@@ -886,8 +890,8 @@ __global__ void __launch_bounds__(kThreadsOf<MODE, FP8>, 1)
     Walker<MODE, kStep, FP8> walk(p, kFeatStep);
     Tile t;
     bool more = false;
-    // Where e4m3's first tile is looked up before the warps part, its epilogue keeps what it needs in
-    // registers (without gates, 4096 x 7168, 256 experts of 512 rows: 720 us for 772); for the others
+    // Where e4m3's first tile is looked up before the warps part, its epilogue keeps all but two words
+    // of what it needs in registers (without gates, 4096 x 7168, 256 experts of 512 rows: 720 us for 772); for the others
     // it only comes later that way (a lone tile +0.3 us).
     constexpr bool kEarly = FP8 && !SPLIT;
     if (kEarly && warp == kProducerWarp) more = walk.next(first, t);

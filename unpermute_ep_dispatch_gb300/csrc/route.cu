@@ -1,16 +1,19 @@
-// route.cu -- routing to experts and its gradient (ep_route, ep_route_backward).
+// route.cu -- routing to experts (ep_route).
 //
 // One warp owns one token: a row is read once, 16 bytes a lane where its alignment allows, and
-// kept in registers as the values that decide the choice. The argmax is two warp reductions: the
+// kept by the lane as the values that decide the choice. The argmax is two warp reductions: the
 // largest value, then the lowest index that has it -- the tie rule at no extra cost. Every lane
 // keeps its two largest at hand, so that a pick costs its owner a move and only a lane's second
 // pick a new pass over its values, for those that come after the pick in the order of picks.
 //
 // What bounds it: a row of 256 logits is 1 KiB, 2.7 us for 16384 rows at the copy rate; its
-// instructions (745 a token with a bias and 4 of 8 groups, 472 for plain softmax; two thirds of
-// them compares, selects and maxima at half rate) take 14.0 and 9.5 us back to back in a graph.
-// Rows of up to 256 logits are held to 32 registers, so that sixteen blocks fit an SM and a call
-// starts under the end of the one before: 4097 rows 5.6 us from 7.2 in a graph, 16384 the same.
+// instructions (817 a token with a bias and 4 of 8 groups, 475 for plain softmax; most of
+// them compares, selects and maxima at half rate) take 14.6 and 9.6 us back to back in a graph.
+// Kernels for rows of up to 256 logits are held to 32 registers a thread, so that sixteen blocks fit
+// an SM and a call starts under the end of the one before: 4097 rows 5.6 us from 7.2 in a graph,
+// 16384 the same. (From 129 logits on, that spills 32 to 52 bytes a thread.) Rows of more than 1024 logits
+// have one form, 128 values a lane in 255 registers with 100 to 170 bytes spilled: 4096 tokens of
+// 4096 logits, softmax, 44 us (9.9 of bytes), of 2048 with a bias 75.
 #include "route.cuh"
 
 namespace epd {
@@ -105,7 +108,7 @@ __global__ void __launch_bounds__(kRouteThreads, V <= 8 ? 16 : 1) route_kernel(R
             for (int i = 0; i < L::C; ++i) {
                 float &v = c[q * L::C + i];
                 // expf, for the choice is told apart by these: with the hardware's 2^x of a rounded
-                // product neighbouring logits tie from 11 on (16384 tokens grouped: 13.7 us for 14.4)
+                // product neighbouring logits tie from 11 on (16384 tokens grouped: 13.7 us for 14.4 so)
                 float score;
                 if (SCORING == EPD_SCORE_SIGMOID) {
                     const float e = expf(-fabsf(v));
