@@ -542,7 +542,7 @@ EPD_API epd_status_t ep_expert_matmul_dgrad(const epd_expert_rows_t *rows, const
  * in an order that is fixed for given sizes (see ep_expert_matmul); 0 for an expert without
  * rows. Rows outside the experts' regions are not used, whatever they hold.
  *   dy: [capacity_rows, N], x: [capacity_rows, K], dw: [E, N, K] bfloat16, 16-byte aligned;
- *   dbias: [E, N] float32; N % 8 == 0, K % 8 == 0.
+ *   dbias: [E, N] float32; N % 8 == 0, K % 8 == 0, both up to 2^30 (EPD_ERR_UNSUPPORTED).
  */
 EPD_API epd_status_t ep_expert_matmul_wgrad(const epd_expert_rows_t *rows, const void *dy,
                                             const void *x, int in_features, int out_features,

@@ -329,3 +329,26 @@ def test_wgrad_of_few_rows_in_a_large_buffer(counts, K, N):
         want = a.t() @ b
         assert ((dw[e].double() - want).abs() <= (c + 16) * ULP * (a.abs().t() @ b.abs()) + 2 ** -8 * want.abs()).all()
         assert ((db[e].double() - a.sum(0)).abs() <= (c + 16) * ULP * a.abs().sum(0)).all()
+
+
+def test_as_many_rows_as_a_buffer_may_have():
+    """2^31 - 1 rows of one expert: row numbers of the last steps and tiles reach 2^31. All but a
+    few rows are zero, and the values are whole, so that every sum is exact."""
+    M, K, N = 2 ** 31 - 1, 8, 8
+    if torch.cuda.mem_get_info()[0] < 110 * 2 ** 30:
+        pytest.skip("needs 103 GB on the device")
+    g = gen(31)
+    at = torch.cat([torch.tensor([0, 1, 63, 12_345_678, 2 ** 30], device=DEV), torch.arange(M - 300, M, device=DEV)])
+    x, dy = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV), torch.zeros(M, N, dtype=torch.bfloat16, device=DEV)
+    x[at] = torch.randint(-4, 5, (len(at), K), generator=g, device=DEV).to(torch.bfloat16)
+    dy[at] = torch.randint(-4, 5, (len(at), N), generator=g, device=DEV).to(torch.bfloat16)
+    w = torch.randint(-4, 5, (1, N, K), generator=g, device=DEV).to(torch.bfloat16)
+    status, rows = epd.new_status(), dict(expert_start_loc=i32([0]))
+    dw, db = epd.ep_expert_matmul_wgrad(dy, x, i32([M]), status, with_dbias=True, **rows)
+    check_ok(status)
+    assert torch.equal(dw[0], (dy[at].double().t() @ x[at].double()).to(torch.bfloat16))
+    assert torch.equal(db[0].double(), dy[at].double().sum(0))
+    y, _ = epd.ep_expert_matmul(x, w, i32([M]), status, **rows)
+    check_ok(status)
+    assert torch.equal(y[at], (x[at].double() @ w[0].double().t()).to(torch.bfloat16))
+    assert (y[2 ** 20:2 ** 20 + 4096] == 0).all() and (y[M - 5000:M - 300] == 0).all()

@@ -94,3 +94,10 @@ def test_unpermute_backward_rejects_bad_args(lib):
 
 def test_new_status_code_has_a_name(lib):
     assert "logit" in _binding.status_string(_binding.EPD_ERR_NONFINITE)
+
+
+def test_wgrad_rejects_features_beyond_half_of_32_bits(lib):
+    call = caller(lib.ep_expert_matmul_wgrad, dict(r=rows(), dy=FAKE, x=FAKE, K=64, N=32, dw=FAKE, db=None, st=FAKE,
+                                                   s=None))
+    assert call(K=1 << 30) == _binding.EPD_ERR_UNSUPPORTED
+    assert call(N=(1 << 31) - 8) == _binding.EPD_ERR_UNSUPPORTED

@@ -82,6 +82,9 @@ constexpr int kRing = 4;                        // tiles published ahead
 constexpr int kCuts = 18;                       // wgrad's boxes: 64, 32, 16 and 1 to 15 rows
 constexpr int kGroupTiles = 8;                  // row tiles that share a pass over the features
 
+// n / d rounded up, for n up to INT32_MAX.
+__host__ __device__ constexpr int ceil_div(int n, int d) { return (int)(((uint32_t)n + (uint32_t)d - 1) / (uint32_t)d); }
+
 constexpr int kStages = 6;
 
 // A wait's limit, and what each step of the longest reduction adds to it: a wait may be for a whole
@@ -214,13 +217,13 @@ struct Walker {
     __device__ Walker(const ExpertArgs &args, int feat_step_) : p(args), feat_step(feat_step_) {
         lane = threadIdx.x & 31;
         const int features = MODE == kForward ? p.N : p.K;
-        feat_tiles = (features + feat_step - 1) / feat_step;
+        feat_tiles = ceil_div(features, feat_step);
     }
 
     __device__ bool next(int tile, Tile &t) {
         int local, row_tiles;
         if (MODE == kWgrad) {
-            row_tiles = (p.N + kTileRows - 1) / kTileRows;
+            row_tiles = ceil_div(p.N, kTileRows);
             const int per = row_tiles * feat_tiles;
             t.e = tile / per;
             if (t.e >= p.rows.num_experts) return false;
@@ -235,7 +238,7 @@ struct Walker {
                 count = start = 0;
                 if (batch + lane < p.rows.num_experts)
                     expert_region(p.rows, batch + lane, start, count, p.status);
-                upto = (count + kTileRows - 1) / kTileRows * feat_tiles;
+                upto = ceil_div(count, kTileRows) * feat_tiles;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int v = __shfl_up_sync(0xffffffffu, upto, o);
@@ -247,7 +250,7 @@ struct Walker {
             t.e = batch + src;
             t.count = __shfl_sync(0xffffffffu, count, src);
             t.start = __shfl_sync(0xffffffffu, start, src);
-            row_tiles = (t.count + kTileRows - 1) / kTileRows;
+            row_tiles = ceil_div(t.count, kTileRows);
             local = tile - before - (__shfl_sync(0xffffffffu, upto, src) - row_tiles * feat_tiles);
         }
         // Groups of row tiles pass over the features together, the row tiles fastest, so that the
@@ -264,7 +267,7 @@ struct Walker {
         const int total = MODE == kWgrad ? p.N : t.count;
         // equal tiles of the least width; e4m3: full tiles of rows, and a last one of at most 128
         // turned across
-        const int each = FP8 ? kTileRows : ((total + row_tiles - 1) / row_tiles + 31) & ~31;
+        const int each = FP8 ? kTileRows : (ceil_div(total, row_tiles) + 31) & ~31;
         t.row0 = rt * each;
         t.rows = min(each, total - t.row0);
         t.across = !FP8 || t.rows <= kAcrossRows;
@@ -273,7 +276,7 @@ struct Walker {
         else  // feat_step features, gated: and their up
             t.n = feat_step == 128 ? 256 : (min(256, p.N - t.feat0) + 31) & ~31;
         const int red = MODE == kForward ? p.K : MODE == kDgrad ? p.N : t.count;
-        t.steps = (red + STEP - 1) / STEP;
+        t.steps = ceil_div(red, STEP);
         t.step0 = t.part = 0;
         t.parts = 1;
         return true;
@@ -747,15 +750,16 @@ template <int LANES>
 __device__ __forceinline__ void sum_bias(const ExpertArgs &p, int worker, int workers) {
     constexpr int kRows = 16, kParts = 32 / LANES;  // in flight a lane; rows at a time
     const int lane = threadIdx.x & 31, part = lane / LANES;
-    const int groups = (p.N + 8 * LANES - 1) / (8 * LANES);
+    const int groups = ceil_div(p.N, 8 * LANES);
     const int64_t pitch = (int64_t)p.N * 2;
     for (int64_t item = worker; item < (int64_t)groups * p.rows.num_experts; item += workers) {
         const int e = (int)(item / groups), n = (int)(item - (int64_t)e * groups) * (8 * LANES) + (lane % LANES) * 8;
-        int start, count;
-        expert_region(p.rows, e, start, count, p.status);
+        int start, rows;
+        expert_region(p.rows, e, start, rows, p.status);
+        const uint32_t count = rows;  // so that a row number past the last, of 2^31 at most, is one
         float sum[8] = {};
         const uint8_t *at = p.dy + ((int64_t)start * p.N + n) * 2;
-        for (int r = part; n < p.N && r < count; r += kParts * kRows) {
+        for (uint32_t r = part; n < p.N && r < count; r += kParts * kRows) {
             uint4 v[kRows];
 #pragma unroll
             for (int i = 0; i < kRows; ++i)
@@ -1423,9 +1427,9 @@ epd_status_t resident(int parts, int &clusters) {
 template <int MODE, bool FP8, bool GATED>
 epd_status_t launch(const Maps<MODE> &maps, ExpertArgs p, cudaStream_t stream) {
     const int features = MODE == kForward ? p.N : p.K;
-    const int64_t feat_tiles = (features + (GATED && MODE == kForward ? 127 : 255)) / (GATED && MODE == kForward ? 128 : 256);
+    const int64_t feat_tiles = ceil_div(features, GATED && MODE == kForward ? 128 : 256);
     const int64_t cap = p.rows.capacity_rows, E = p.rows.num_experts;
-    const int64_t row_tiles = MODE == kWgrad ? (int64_t)(p.N + kTileRows - 1) / kTileRows * E
+    const int64_t row_tiles = MODE == kWgrad ? (int64_t)ceil_div(p.N, kTileRows) * E
                               : p.rows.expert_start_loc ? cap / kTileRows + (E < cap ? E : cap)
                                                         : (p.rows.rows_per_expert + kTileRows - 1) / kTileRows * E;
     const int64_t most = row_tiles > 0 ? feat_tiles * row_tiles : 1;
@@ -1604,6 +1608,7 @@ extern "C" epd_status_t ep_expert_matmul_wgrad(const epd_expert_rows_t *rows, co
     const int K = in_features, N = out_features;
     if (!rows_ok(rows)) return EPD_ERR_INVALID_ARG;
     if (K < 1 || N < 1 || K % 8 != 0 || N % 8 != 0) return EPD_ERR_INVALID_ARG;
+    if (K > INT32_MAX / 2 || N > INT32_MAX / 2) return EPD_ERR_UNSUPPORTED;
     if (!status || !aligned4(status) || !dw || !aligned16(dw) || (dbias && !aligned4(dbias)))
         return EPD_ERR_INVALID_ARG;
     if (rows->capacity_rows > 0 && (!dy || !aligned16(dy) || !x || !aligned16(x)))

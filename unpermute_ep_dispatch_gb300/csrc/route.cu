@@ -286,7 +286,7 @@ epd_status_t launch_route(RouteArgs a, cudaStream_t st) {
     if (width * Layout<T, V>::C == a.size && (width & (width - 1)) == 0 && width <= 32 && a.groups <= 32)
         for (a.run = 0; width >> a.run > 1;) ++a.run;
     const size_t smem = a.keep < a.groups && a.run < 0 ? (size_t)kRouteWarps * (a.E + EPD_MAX_GROUPS) * sizeof(float) : 0;
-    const int grid = (a.T + kRouteWarps - 1) / kRouteWarps;
+    const int grid = (a.T - 1) / kRouteWarps + 1;
     auto kernel = route_kernel<T, V, SCORING>;
     if (smem > 48 * 1024) {
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

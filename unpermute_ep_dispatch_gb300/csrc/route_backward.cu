@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_backward_row_kernel(Route
 
 template <typename T>
 epd_status_t launch_route_backward(RouteGradArgs a, int scoring, cudaStream_t st) {
-    const int grid = (a.T + kRouteWarps - 1) / kRouteWarps;
+    const int grid = (a.T - 1) / kRouteWarps + 1;
     if (scoring == EPD_SCORE_SOFTMAX && !a.renorm)
         return by_width(a.E, [&](auto width) {
             constexpr int V = decltype(width)::value;
