@@ -445,7 +445,7 @@ EPD_API epd_status_t ep_route(const void *logits, epd_dtype_t dtype, const float
  * Renormalised softmax weights are the softmax of the picks' logits alone, and are computed
  * as that, here and in ep_route. Every element of grad_logits [T, E] (the logits' type) is written, 0
  * for an expert that cannot be chosen. An expert that a row picks twice gets both
- * picks' terms.
+ * picks' terms. grad_logits must not overlap logits.
  */
 EPD_API epd_status_t ep_route_backward(const float *grad_weights, const void *logits,
                                        epd_dtype_t dtype, const int64_t *topk_idx, int num_tokens,
@@ -558,7 +558,8 @@ EPD_API epd_status_t ep_expert_matmul_wgrad(const epd_expert_rows_t *rows, const
  * input is ep_unpermute of the rows' gradients with weights of 1.
  *   grad_y: [T, H], expert_out and grad_expert_out: [capacity_rows, H] bfloat16, 16-byte
  *   aligned, H % 8 == 0; topk_weights and grad_weights: [T, k] float32.
- * A slot outside [-1, capacity_rows) sets EPD_ERR_CAPACITY and is skipped.
+ * A slot outside [-1, capacity_rows) sets EPD_ERR_CAPACITY and is skipped. Outputs must not
+ * overlap inputs.
  */
 EPD_API epd_status_t ep_unpermute_backward(const void *grad_y, const void *expert_out,
                                            int64_t capacity_rows, const int32_t *output_index,
