@@ -568,6 +568,61 @@ EPD_API epd_status_t ep_unpermute_backward(const void *grad_y, const void *exper
                                            float *grad_weights, int32_t *status,
                                            epd_stream_t stream);
 
+/* ------------------------------------------------------------------ the norm
+ * Ahead of the router, the dispatch and the projections. */
+typedef enum {
+    EPD_NORM_LAYER = 0, /* centred, divided by the standard deviation */
+    EPD_NORM_RMS = 1,   /* divided by the root mean square */
+} epd_norm_t;
+
+/*
+ * Layer norm. For every row, with s = x + residual (s = x where residual is NULL):
+ *   mean = sum of s / H (EPD_NORM_RMS: 0), rstd = (sum of (s - mean)^2 / H + eps)^-1/2,
+ *   n = (s - mean) * rstd * weight + bias,
+ * in fp32 and rounded once to each of
+ *   sum  [T, H] of x's type: s, the residual stream from here on (only with residual);
+ *   y    [T, H] bfloat16: n, what the router's projection and the products read;
+ *   y_q  [T, H] e4m3 with y_scale [T, H/128] float32: n with one scale per 128 columns,
+ *        amax / 448 (1 where amax is 0), as ep_dispatch and ep_permute take rows
+ *        (H % 128 == 0);
+ *   mean, rstd [T] float32, for ep_layer_norm_backward;
+ * each of which may be NULL, but not y and y_q both. n is computed from s before s is rounded.
+ *   x, residual: [T, H] float32 (EPD_F32) or bfloat16 (EPD_BF16); weight, bias: [H]
+ *   float32, NULL for ones and zeros. H % 8 == 0, H <= 16384 (EPD_ERR_UNSUPPORTED beyond);
+ *   rows, weight and bias 16-byte aligned. sum may be the buffer of x or residual itself, and
+ *   y that of bfloat16 x; otherwise outputs must not overlap inputs. eps >= 0.
+ */
+EPD_API epd_status_t ep_layer_norm(const void *x, epd_dtype_t dtype, const void *residual,
+                                   const float *weight, const float *bias, int num_tokens,
+                                   int hidden, float eps, epd_norm_t kind, void *sum, void *y,
+                                   void *y_q, float *y_scale, float *mean, float *rstd,
+                                   epd_stream_t stream);
+
+/* Workspace size in bytes of ep_layer_norm_backward for rows of `hidden` columns (0 for a size it
+ * does not take). It holds nothing between calls; it serves one stream at a time. */
+EPD_API size_t epd_norm_workspace_bytes(int hidden);
+
+/*
+ * Gradients of ep_layer_norm. With xh = (x - mean) * rstd and g = dy * weight, for every row
+ *   dx = rstd * (g - sum of g / H - xh * (sum of g * xh) / H) + grad_sum
+ * (EPD_NORM_RMS: xh = x * rstd, without the sum of g; mean is not read), and over all rows
+ *   dweight = sum of dy * xh,  dbias = sum of dy   (float32; each NULL to leave it out),
+ * 0 where there are no rows. x is what was normalised: `sum` where a residual was added, whose
+ * gradient is dx as well; grad_sum (NULL for none) is the gradient that `sum` has from
+ * elsewhere. The order of the sums over the rows is fixed for given T, H and a device: the same
+ * call gives the same bits again.
+ *   dy: [T, H] bfloat16; x, grad_sum, dx: [T, H] of `dtype`; mean, rstd: [T] float32;
+ *   dweight, dbias: [H] float32; workspace: epd_norm_workspace_bytes(H) bytes (NULL where neither
+ *   dweight nor dbias is asked for). All but mean and rstd 16-byte aligned. dx may be the buffer
+ *   of x or grad_sum itself, or of dy where x is bfloat16; otherwise outputs must not overlap inputs.
+ */
+EPD_API epd_status_t ep_layer_norm_backward(const void *dy, const void *x, epd_dtype_t dtype,
+                                            const float *weight, const float *mean,
+                                            const float *rstd, const void *grad_sum,
+                                            int num_tokens, int hidden, epd_norm_t kind,
+                                            void *workspace, void *dx, float *dweight,
+                                            float *dbias, epd_stream_t stream);
+
 /*
  * Allocation-free variant of ep_dispatch_layout. The pages have no counterpart:
  * this entry point exists for callers that cannot allocate device memory at

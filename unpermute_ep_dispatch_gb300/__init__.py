@@ -34,4 +34,5 @@ from ._binding import (  # noqa: F401,E402
     ep_permute_ex, ep_permute_lowlatency, ep_scan_offsets, ep_scan_offsets_aligned,
     ep_route, ep_route_backward, ep_unpermute, ep_unpermute_backward, epd_workspace_bytes,
     epd_workspace_init, load_library, new_status, new_workspace, status_string, version,
+    ep_layer_norm, ep_layer_norm_backward, epd_norm_workspace_bytes, new_norm_workspace,
 )

@@ -35,6 +35,7 @@ EPD_MAX_TOPK = 64
 EPD_MAX_GROUPS = 64
 SCORING = {"softmax": 0, "sigmoid": 1}
 GROUP_SCORE = {"max": 0, "top2": 1}
+NORM = {"layer": 0, "rms": 1}
 ACTIVATION = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "swiglu": 4}
 
 class PermuteView(ctypes.Structure):
@@ -84,6 +85,9 @@ SIGNATURES = {
     "ep_expert_matmul_dgrad": (_I, [_ROWS, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
     "ep_expert_matmul_wgrad": (_I, [_ROWS, _P, _P, _I, _I, _P, _P, _P, _P]),
     "ep_unpermute_backward": (_I, [_P, _P, _I64, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
+    "ep_layer_norm": (_I, [_P, _I, _P, _P, _P, _I, _I, _F, _I, _P, _P, _P, _P, _P, _P, _P]),
+    "epd_norm_workspace_bytes": (_SZ, [_I]),
+    "ep_layer_norm_backward": (_I, [_P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P]),
     "ep_dispatch_layout_noalloc": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
     "epd_test_expert_matmul_stalled": (_I, [_ROWS, _P, _I, _P, _I64, _I64, _I64, _P, _P, _I, _I, _I,
                                             _P, _P, _I, _I64, _P]),
@@ -816,6 +820,127 @@ def ep_unpermute_backward(grad_y: torch.Tensor, expert_out: torch.Tensor,
         _ptr(grad_expert_out), _ptr(grad_weights), _ptr(status), _stream(stream, dev))
     _check(rc, "ep_unpermute_backward")
     return grad_expert_out, grad_weights
+
+
+# ----------------------------------------------------------------------------- the norm
+def _launch(fn, dev, *args):
+    """Calls `fn` with `dev`, the tensors' device, as the current one."""
+    if dev.index == torch._C._cuda_getDevice():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
+def _norm_rows(t, name):
+    dtype = t.dtype if isinstance(t, torch.Tensor) else None
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be a float32 or bfloat16 tensor")
+    _want(t, name, dtype)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [num_tokens, hidden]")
+    return EPD_F32 if dtype is torch.float32 else EPD_BF16
+
+
+def ep_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                  bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                  eps: float = 1e-5, kind: str = "layer", with_y: bool = True,
+                  with_fp8: bool = False, with_stats: bool = False, sum=None, y=None, y_q=None,
+                  y_scale=None, mean=None, rstd=None, stream=None):
+    """Layer norm of x [T, H] (float32 or bfloat16), or of x + residual; kind: "layer" or "rms".
+    weight, bias: [H] float32. Returns a dict: y [T, H] bfloat16 (with_y), y_q [T, H]
+    float8_e4m3fn and y_scale [T, H/128] float32 (with_fp8: rows as ep_dispatch takes them), sum
+    (x + residual, of x's type; where residual is given), mean (of "layer") and rstd [T] float32
+    (with_stats). An output that is passed in is written too; the others are None. See epd.h."""
+    dt = _norm_rows(x, "x")
+    kd = _choose(NORM, kind, "kind")
+    dev, dtype = x.device, x.dtype
+    T, H = x.shape
+    if weight is not None:
+        _want(weight, "weight", torch.float32, (H,), dev)
+    if bias is not None:
+        _want(bias, "bias", torch.float32, (H,), dev)
+    if residual is not None:
+        _want(residual, "residual", dtype, (T, H), dev)
+        sum = _out(sum, "sum", dtype, (T, H), dev)
+    elif sum is not None:
+        raise ValueError("sum is an output of a norm with residual")
+    if with_y or y is not None:
+        y = _out(y, "y", torch.bfloat16, (T, H), dev)
+    if with_fp8 or y_q is not None or y_scale is not None:
+        if H % 128:
+            raise ValueError(f"e4m3 rows need a multiple of 128 columns, got {H}")
+        y_q = _out(y_q, "y_q", torch.float8_e4m3fn, (T, H), dev)
+        y_scale = _out(y_scale, "y_scale", torch.float32, (T, H // 128), dev)
+    elif y is None:
+        raise ValueError("a norm without y needs with_fp8")
+    if kd and mean is not None:
+        raise ValueError('kind "rms" has no mean')
+    if (with_stats and not kd) or mean is not None:
+        mean = _out(mean, "mean", torch.float32, (T,), dev)
+    if with_stats or rstd is not None:
+        rstd = _out(rstd, "rstd", torch.float32, (T,), dev)
+    rc = _launch(load_library().ep_layer_norm, dev, _ptr(x), dt, _ptr(residual), _ptr(weight),
+                 _ptr(bias), T, H, float(eps), kd, _ptr(sum), _ptr(y), _ptr(y_q), _ptr(y_scale),
+                 _ptr(mean), _ptr(rstd), _stream(stream, dev))
+    _check(rc, "ep_layer_norm")
+    return dict(y=y, y_q=y_q, y_scale=y_scale, sum=sum, mean=mean, rstd=rstd)
+
+
+def epd_norm_workspace_bytes(hidden: int) -> int:
+    n = int(load_library().epd_norm_workspace_bytes(hidden))
+    if n == 0:
+        raise EpdError(EPD_ERR_INVALID_ARG, "epd_norm_workspace_bytes")
+    return n
+
+
+def new_norm_workspace(hidden: int, device=None) -> torch.Tensor:
+    """A workspace tensor (uint8) for ep_layer_norm_backward on one stream."""
+    return torch.empty(epd_norm_workspace_bytes(hidden), dtype=torch.uint8,
+                       device=device or torch.device("cuda"))
+
+
+def ep_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor],
+                           rstd: torch.Tensor, mean: Optional[torch.Tensor] = None,
+                           kind: str = "layer", grad_sum: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, dx=None, dweight=None,
+                           dbias=None, with_dweight: bool = True, with_dbias: bool = False,
+                           stream=None):
+    """Gradients of ep_layer_norm: dy [T, H] bfloat16, x [T, H] what was normalised (its `sum`
+    where a residual was added), mean (of "layer") and rstd its statistics, grad_sum the gradient
+    that x has from elsewhere. The workspace is allocated where none is given. Returns (dx like x,
+    dweight [H] float32 or None, dbias [H] float32 or None); see epd.h."""
+    dt = _norm_rows(x, "x")
+    kd = _choose(NORM, kind, "kind")
+    dev, dtype = x.device, x.dtype
+    T, H = x.shape
+    _want(dy, "dy", torch.bfloat16, (T, H), dev)
+    _want(rstd, "rstd", torch.float32, (T,), dev)
+    if weight is not None:
+        _want(weight, "weight", torch.float32, (H,), dev)
+    if kd:
+        if mean is not None:
+            raise ValueError('kind "rms" has no mean')
+    else:
+        _want(mean, "mean", torch.float32, (T,), dev)
+    if grad_sum is not None:
+        _want(grad_sum, "grad_sum", dtype, (T, H), dev)
+    dx = _out(dx, "dx", dtype, (T, H), dev)
+    if with_dweight or dweight is not None:
+        dweight = _out(dweight, "dweight", torch.float32, (H,), dev)
+    if with_dbias or dbias is not None:
+        dbias = _out(dbias, "dbias", torch.float32, (H,), dev)
+    if dweight is not None or dbias is not None:
+        if workspace is None:
+            workspace = new_norm_workspace(H, dev)
+        else:
+            _want(workspace, "workspace", torch.uint8, device=dev)
+            if workspace.numel() < epd_norm_workspace_bytes(H):
+                raise ValueError("workspace too small for this norm")
+    rc = _launch(load_library().ep_layer_norm_backward, dev, _ptr(dy), _ptr(x), dt, _ptr(weight),
+                 _ptr(mean), _ptr(rstd), _ptr(grad_sum), T, H, kd, _ptr(workspace), _ptr(dx),
+                 _ptr(dweight), _ptr(dbias), _stream(stream, dev))
+    _check(rc, "ep_layer_norm_backward")
+    return dx, dweight, dbias
 
 
 def ep_dispatch_layout_noalloc(topk_idx: torch.Tensor, num_experts: int, num_ranks: int,

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 #include "epd.h"
@@ -152,6 +153,20 @@ inline epd_status_t launch_pdl_cluster(void (*kernel)(KArgs...), int grid, int b
     cfg.numAttrs = 2;
     cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
     return record_cuda_error();
+}
+
+// Lets `kernel` take up to `bytes` of dynamic shared memory (always the same number), once a device.
+template <auto kernel>
+inline epd_status_t allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return record_cuda_error();
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return EPD_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return record_cuda_error();
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return EPD_OK;
 }
 
 // Resident blocks of `kernel` per SM at `block` threads and `smem` dynamic bytes.

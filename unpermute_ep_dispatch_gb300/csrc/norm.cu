@@ -1,0 +1,497 @@
+// norm.cu -- layer norm and its root-mean-square form (ep_layer_norm), and their gradients
+// (ep_layer_norm_backward).
+//
+//   s = x + residual,  mean = sum s / H,  rstd = (sum (s - mean)^2 / H + eps)^-1/2   (mean 0 for RMS)
+//   y = (s - mean) rstd weight + bias
+//   g = dy weight,  xh = (x - mean) rstd
+//   dx = rstd (g - sum g / H - xh sum(g xh) / H) + grad_sum      (RMS: without sum g)
+//   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+//
+// Bound by HBM: every row is read once and written once. A block owns a row, a thread one
+// 8-column chunk of it (four where the row is wider than 8192), and blocks walk over the rows with
+// the row kept in registers between the sums. Each thread copies its own chunks of the rows to
+// come into its own slots of shared memory (cp.async, up to four rows ahead): no barrier and no
+// wait but the thread's own, and one block a multiprocessor keeps 40 KB or more on the way. The
+// variance is summed from the centred values in a second pass over the registers, which neither
+// cancels nor reads the row again.
+//
+// The weights' gradients: a thread keeps the sums of its columns over all of its block's rows in
+// registers; the blocks' sums go to the workspace and a second kernel adds them in a fixed order.
+#include <cuda_fp8.h>
+
+#include "epd_math.cuh"
+
+namespace epd {
+namespace {
+
+constexpr int kMaxHidden = 16384;
+constexpr int kNormMaxSms = 160;    // blocks that the workspace has room for, per block of a multiprocessor
+constexpr int kReduceThreads = 256;
+constexpr int kRingBytes = 224 * 1024;  // of the 227 KB that a multiprocessor's blocks share
+constexpr unsigned kAll = 0xffffffffu;
+
+struct NormArgs {
+    const uint8_t *x, *residual;
+    const float *weight, *bias;
+    int T, chunks, rms, stages;  // chunks: 8-column pieces of a row
+    float eps, inv_h;
+    uint8_t *sum, *y, *yq;
+    float *yscale, *mean, *rstd;
+};
+
+struct NormGradArgs {
+    const uint8_t *dy, *x, *grad_sum;
+    const float *weight, *mean, *rstd;
+    int T, chunks, rms, stages;
+    float inv_h;
+    uint8_t *dx;
+    float *dweight, *dbias;  // the sums themselves (one block) or the workspace's [block][2][H]
+    int64_t block_stride;    // floats between two blocks' sums
+};
+
+__device__ __forceinline__ void copy16(void *dst_smem, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst_smem)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until the oldest of `stages` groups has landed.
+__device__ __forceinline__ void copy_wait(int stages) {
+    if (stages == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (stages == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+__device__ __forceinline__ float warp_add(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+
+// Sums of a and b over the block, in every thread. `part` alternates between two calls, so that one
+// barrier a call is enough.
+__device__ __forceinline__ void block_add(float &a, float &b, float2 (&part)[32]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    a = warp_add(a);
+    b = warp_add(b);
+    if (warps == 1) return;
+    if (lane == 0) part[warp] = make_float2(a, b);
+    __syncthreads();
+    const float2 v = lane < warps ? part[lane] : make_float2(0.0f, 0.0f);
+    a = warp_add(v.x);
+    b = warp_add(v.y);
+}
+
+// 16-byte pieces of an 8-column chunk of T, and the chunk in 32 bits.
+template <typename T>
+struct Chunk;
+template <>
+struct Chunk<__nv_bfloat16> {
+    static constexpr int P = 1;
+    static __device__ __forceinline__ void unpack(const uint4 *slot, int stride, float (&f)[8]) { unpack8_bf16(slot[0], f); }
+    static __device__ __forceinline__ void store(uint8_t *p, const float (&f)[8]) { st16(p, pack8_bf16(f)); }
+};
+template <>
+struct Chunk<float> {
+    static constexpr int P = 2;
+    static __device__ __forceinline__ void unpack(const uint4 *slot, int stride, float (&f)[8]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 v = slot[h * stride];
+            f[4 * h] = __uint_as_float(v.x), f[4 * h + 1] = __uint_as_float(v.y);
+            f[4 * h + 2] = __uint_as_float(v.z), f[4 * h + 3] = __uint_as_float(v.w);
+        }
+    }
+    static __device__ __forceinline__ void store(uint8_t *p, const float (&f)[8]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            st16(p + 16 * h, make_uint4(__float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]),
+                                        __float_as_uint(f[4 * h + 2]), __float_as_uint(f[4 * h + 3])));
+    }
+};
+
+// Starts the copy of this thread's chunks of one row of `src` into its slots [NV][P] of `at`
+// (slots of one thread lie blockDim.x apart).
+template <typename T, int NV>
+__device__ __forceinline__ void fetch_row(uint4 *at, const uint8_t *src, int64_t row, int chunks) {
+    constexpr int P = Chunk<T>::P;
+    const uint8_t *p = src + row * chunks * (16 * P);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c < chunks) {
+#pragma unroll
+            for (int h = 0; h < P; ++h) copy16(at + (i * P + h) * blockDim.x, p + (int64_t)c * (16 * P) + 16 * h);
+        }
+    }
+}
+
+__device__ __forceinline__ void load8(const float *p, int c, float (&f)[8], float none) {
+    if (!p) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = none;
+        return;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(p + 8 * (int64_t)c) + h);
+        f[4 * h] = v.x, f[4 * h + 1] = v.y, f[4 * h + 2] = v.z, f[4 * h + 3] = v.w;
+    }
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(NormArgs a) {
+    constexpr int P = Chunk<T>::P;
+    extern __shared__ uint4 s_ring[];
+    __shared__ float2 s_part[2][32];
+    const int tid = threadIdx.x, n = blockDim.x;
+    const int arrays = a.residual ? 2 : 1, stage = arrays * NV * P * n;
+    pdl_wait();
+    pdl_trigger();
+    uint4 *const mine = s_ring + tid;
+    auto fetch = [&](int64_t row, int s) {
+        if (row < a.T) {
+            fetch_row<T, NV>(mine + s * stage, a.x, row, a.chunks);
+            if (a.residual) fetch_row<T, NV>(mine + s * stage + NV * P * n, a.residual, row, a.chunks);
+        }
+        copy_commit();
+    };
+    for (int s = 0; s < a.stages; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+    float w[8], b[8];
+    if (NV == 1 && tid < a.chunks) {
+        load8(a.weight, tid, w, 1.0f);
+        load8(a.bias, tid, b, 0.0f);
+    }
+    int s = 0;
+    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+        copy_wait(a.stages);
+        float v[NV][8], sum = 0.0f, none = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = tid + i * n;
+            if (c >= a.chunks) continue;
+            Chunk<T>::unpack(mine + s * stage + i * P * n, n, v[i]);
+            if (a.residual) {
+                float r[8];
+                Chunk<T>::unpack(mine + s * stage + (NV + i) * P * n, n, r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] += r[j];
+                if (a.sum) Chunk<T>::store(a.sum + (row * a.chunks + c) * (16 * P), v[i]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum += v[i][j];
+        }
+        float mean = 0.0f;
+        if (!a.rms) {
+            block_add(sum, none, s_part[0]);
+            mean = __fdiv_rn(sum, (float)(a.chunks * 8));
+        }
+        float sq = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (tid + i * n < a.chunks) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[i][j] -= mean;
+                    sq = fmaf(v[i][j], v[i][j], sq);
+                }
+            }
+        // RMS has one sum a row: its two buffers take turns from row to row
+        block_add(sq, none, a.rms ? s_part[(row / gridDim.x) & 1] : s_part[1]);
+        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(fmaf(sq, a.inv_h, a.eps)));
+        fetch(row + (int64_t)a.stages * gridDim.x, s);
+        if (++s == a.stages) s = 0;
+        if (tid == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = tid + i * n;
+            if (c >= a.chunks) continue;
+            if (NV > 1) {
+                load8(a.weight, c, w, 1.0f);
+                load8(a.bias, c, b, 0.0f);
+            }
+            float o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = fmaf(v[i][j] * rstd, w[j], b[j]);
+            if (a.y) st16(a.y + (row * a.chunks + c) * 16, pack8_bf16(o));
+            if (a.yq) {
+                // 128 columns are 16 neighbouring lanes, all of them with a chunk or none
+                const unsigned half = (tid & 16) ? 0xffff0000u : 0x0000ffffu;
+                float amax = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(o[j]));
+#pragma unroll
+                for (int d = 8; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half, amax, d));
+                const float scale = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+                uint32_t q[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    q[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(o[2 * j], scale), __fdiv_rn(o[2 * j + 1], scale)),
+                                                    __NV_SATFINITE, __NV_E4M3);
+                *reinterpret_cast<uint2 *>(a.yq + (row * a.chunks + c) * 8) =
+                    make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+                if ((c & 15) == 0) a.yscale[row * (a.chunks >> 4) + (c >> 4)] = scale;
+            }
+        }
+    }
+}
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_backward_kernel(NormGradArgs a) {
+    constexpr int P = Chunk<T>::P;
+    extern __shared__ uint4 s_ring[];
+    __shared__ float2 s_part[2][32];
+    const int tid = threadIdx.x, n = blockDim.x;
+    const int stage = NV * (1 + (a.grad_sum ? 2 : 1) * P) * n;
+    pdl_wait();
+    pdl_trigger();
+    uint4 *const mine = s_ring + tid;
+    auto fetch = [&](int64_t row, int s) {
+        if (row < a.T) {
+            fetch_row<__nv_bfloat16, NV>(mine + s * stage, a.dy, row, a.chunks);
+            fetch_row<T, NV>(mine + s * stage + NV * n, a.x, row, a.chunks);
+            if (a.grad_sum) fetch_row<T, NV>(mine + s * stage + NV * (1 + P) * n, a.grad_sum, row, a.chunks);
+        }
+        copy_commit();
+    };
+    for (int s = 0; s < a.stages; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+    float w[8], dw[NV][8] = {}, db[NV][8] = {};
+    if (NV == 1 && tid < a.chunks) load8(a.weight, tid, w, 1.0f);
+    int s = 0;
+    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+        const float rstd = __ldg(a.rstd + row), mean = a.rms ? 0.0f : __ldg(a.mean + row);
+        copy_wait(a.stages);
+        const uint4 *const at = mine + s * stage;
+        auto read = [&](int i, float (&dy)[8], float (&xh)[8]) {
+            unpack8_bf16(at[i * n], dy);
+            Chunk<T>::unpack(at + (NV + i * P) * n, n, xh);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) xh[j] = (xh[j] - mean) * rstd;
+        };
+        // a wide row's chunks are unpacked again for the second pass: four would not stay in registers
+        float g[8], xh[8], sg = 0.0f, sgx = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = tid + i * n;
+            if (c >= a.chunks) continue;
+            if (NV > 1) load8(a.weight, c, w, 1.0f);
+            read(i, g, xh);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                dw[i][j] = fmaf(g[j], xh[j], dw[i][j]);
+                db[i][j] += g[j];
+                g[j] *= w[j];
+                sg += g[j];
+                sgx = fmaf(g[j], xh[j], sgx);
+            }
+        }
+        block_add(sg, sgx, s_part[(row / gridDim.x) & 1]);
+        const float mg = a.rms ? 0.0f : sg * a.inv_h, mgx = sgx * a.inv_h;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = tid + i * n;
+            if (c >= a.chunks) continue;
+            if (NV > 1) {
+                load8(a.weight, c, w, 1.0f);
+                read(i, g, xh);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) g[j] *= w[j];
+            }
+            float r[8], o[8];
+            if (a.grad_sum) Chunk<T>::unpack(at + (NV * (1 + P) + i * P) * n, n, r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                o[j] = rstd * (g[j] - mg - xh[j] * mgx);
+                if (a.grad_sum) o[j] += r[j];
+            }
+            Chunk<T>::store(a.dx + (row * a.chunks + c) * (16 * P), o);
+        }
+        fetch(row + (int64_t)a.stages * gridDim.x, s);
+        if (++s == a.stages) s = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = tid + i * n;
+        if (c >= a.chunks) continue;
+        if (a.dweight) Chunk<float>::store(reinterpret_cast<uint8_t *>(a.dweight + blockIdx.x * a.block_stride + 8 * (int64_t)c), dw[i]);
+        if (a.dbias) Chunk<float>::store(reinterpret_cast<uint8_t *>(a.dbias + blockIdx.x * a.block_stride + 8 * (int64_t)c), db[i]);
+    }
+}
+
+// out[h] = sum over blocks of part[block][h]: a block takes 128 columns, its eight warps every
+// eighth of the rows, joined in the warps' order. blockIdx.y chooses the weight's or the bias's.
+__global__ void __launch_bounds__(kReduceThreads) norm_reduce_kernel(const float *part, int blocks, int64_t stride, int H,
+                                                                     float *dweight, float *dbias) {
+    __shared__ float4 s_sum[kReduceThreads / 32][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool second = blockIdx.y == 1 || !dweight;
+    float *const out = second ? dbias : dweight;
+    const float *const in = part + (second ? H : 0);
+    const int h = (blockIdx.x * 32 + lane) * 4;
+    pdl_wait();
+    pdl_trigger();
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (h < H) {
+#pragma unroll 8
+        for (int b = warp; b < blocks; b += kReduceThreads / 32) {
+            const float4 p = __ldcg(reinterpret_cast<const float4 *>(in + b * stride + h));
+            v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+        }
+    }
+    s_sum[warp][lane] = v;
+    __syncthreads();
+    if (warp == 0 && h < H) {
+#pragma unroll
+        for (int i = 1; i < kReduceThreads / 32; ++i) {
+            const float4 p = s_sum[i][lane];
+            v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+        }
+        *reinterpret_cast<float4 *>(out + h) = v;
+    }
+}
+
+// Threads of a block (a multiple of 32, one or four chunks each) and blocks a multiprocessor.
+struct NormShape {
+    int nv, threads, per_sm;
+};
+inline NormShape norm_shape(int H) {
+    NormShape s;
+    const int chunks = H / 8;
+    s.nv = chunks <= 1024 ? 1 : 4;
+    s.threads = ((chunks + s.nv - 1) / s.nv + 31) / 32 * 32;
+    // the kernels' registers allow 1024 threads (512 of the wide ones), a multiprocessor 32 blocks
+    s.per_sm = (s.nv == 1 ? 1024 : 512) / s.threads;
+    return s;
+}
+
+inline int norm_max_blocks(int H) { return kNormMaxSms * norm_shape(H).per_sm; }
+
+// Rows ahead: four where they fit beside the other blocks of the multiprocessor, else two or one.
+inline int norm_stages(size_t stage_bytes, int per_sm) {
+    const size_t room = (size_t)kRingBytes / per_sm - 2048;
+    return 4 * stage_bytes <= room ? 4 : 2 * stage_bytes <= room ? 2 : 1;
+}
+
+template <auto kernel, typename A>
+epd_status_t launch_rows(A a, const NormShape &s, int grid, size_t stage_bytes, cudaStream_t st) {
+    a.stages = norm_stages(stage_bytes, s.per_sm);
+    if (const epd_status_t rc = allow_smem<kernel>(kRingBytes)) return rc;
+    return launch_pdl(kernel, grid, s.threads, a.stages * stage_bytes, st, a);
+}
+
+bool floats_ok(const float *p) { return aligned16(p); }  // read and written 16 bytes at a time
+
+}  // namespace
+}  // namespace epd
+
+extern "C" epd_status_t ep_layer_norm(const void *x, epd_dtype_t dtype, const void *residual, const float *weight,
+                                      const float *bias, int num_tokens, int hidden, float eps, epd_norm_t kind,
+                                      void *sum, void *y, void *y_q, float *y_scale, float *mean, float *rstd,
+                                      epd_stream_t stream) {
+    using namespace epd;
+    const int T = num_tokens, H = hidden;
+    if (dtype != EPD_F32 && dtype != EPD_BF16) return EPD_ERR_INVALID_ARG;
+    if (kind != EPD_NORM_LAYER && kind != EPD_NORM_RMS) return EPD_ERR_INVALID_ARG;
+    if (T < 0 || H < 8 || H % 8 != 0 || !(eps >= 0.0f)) return EPD_ERR_INVALID_ARG;
+    if ((y_q != nullptr) != (y_scale != nullptr) || (y_q && H % 128 != 0)) return EPD_ERR_INVALID_ARG;
+    if (sum && !residual) return EPD_ERR_INVALID_ARG;
+    if (H > kMaxHidden) return EPD_ERR_UNSUPPORTED;
+    if (T == 0) return EPD_OK;
+    if (!x || (!y && !y_q)) return EPD_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(sum) || !aligned16(y) || !aligned8(y_q) ||
+        !floats_ok(weight) || !floats_ok(bias) || !aligned4(y_scale) || !aligned4(mean) || !aligned4(rstd))
+        return EPD_ERR_INVALID_ARG;
+    NormArgs a;
+    a.x = static_cast<const uint8_t *>(x);
+    a.residual = static_cast<const uint8_t *>(residual);
+    a.weight = weight;
+    a.bias = bias;
+    a.T = T;
+    a.chunks = H / 8;
+    a.rms = kind == EPD_NORM_RMS;
+    a.eps = eps;
+    a.inv_h = 1.0f / (float)H;
+    a.sum = static_cast<uint8_t *>(sum);
+    a.y = static_cast<uint8_t *>(y);
+    a.yq = static_cast<uint8_t *>(y_q);
+    a.yscale = y_scale;
+    a.mean = mean;
+    a.rstd = rstd;
+    const NormShape s = norm_shape(H);
+    const int most = sm_count() * s.per_sm, grid = T < most ? T : most;
+    const size_t item = dtype == EPD_F32 ? 2 : 1;
+    const size_t stage = (size_t)(residual ? 2 : 1) * s.nv * item * s.threads * 16;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (dtype == EPD_F32)
+        return s.nv == 1 ? launch_rows<norm_kernel<float, 1>>(a, s, grid, stage, st)
+                         : launch_rows<norm_kernel<float, 4>>(a, s, grid, stage, st);
+    return s.nv == 1 ? launch_rows<norm_kernel<__nv_bfloat16, 1>>(a, s, grid, stage, st)
+                     : launch_rows<norm_kernel<__nv_bfloat16, 4>>(a, s, grid, stage, st);
+}
+
+extern "C" size_t epd_norm_workspace_bytes(int hidden) {
+    if (hidden < 8 || hidden % 8 != 0 || hidden > epd::kMaxHidden) return 0;
+    return (size_t)epd::norm_max_blocks(hidden) * 2 * hidden * 4;
+}
+
+extern "C" epd_status_t ep_layer_norm_backward(const void *dy, const void *x, epd_dtype_t dtype, const float *weight,
+                                               const float *mean, const float *rstd, const void *grad_sum,
+                                               int num_tokens, int hidden, epd_norm_t kind, void *workspace, void *dx,
+                                               float *dweight, float *dbias, epd_stream_t stream) {
+    using namespace epd;
+    const int T = num_tokens, H = hidden;
+    if (dtype != EPD_F32 && dtype != EPD_BF16) return EPD_ERR_INVALID_ARG;
+    if (kind != EPD_NORM_LAYER && kind != EPD_NORM_RMS) return EPD_ERR_INVALID_ARG;
+    if (T < 0 || H < 8 || H % 8 != 0) return EPD_ERR_INVALID_ARG;
+    if (H > kMaxHidden) return EPD_ERR_UNSUPPORTED;
+    if (T > 0 && (!dy || !x || !rstd || !dx || (kind == EPD_NORM_LAYER && !mean))) return EPD_ERR_INVALID_ARG;
+    if (!aligned16(dy) || !aligned16(x) || !aligned16(grad_sum) || !aligned16(dx) || !floats_ok(weight) ||
+        !floats_ok(dweight) || !floats_ok(dbias) || !aligned4(mean) || !aligned4(rstd) || !aligned16(workspace))
+        return EPD_ERR_INVALID_ARG;
+    const bool sums = dweight || dbias;
+    if (sums && !workspace) return EPD_ERR_INVALID_ARG;
+    if (T == 0 && !sums) return EPD_OK;
+    const NormShape s = norm_shape(H);
+    const int sms = sm_count() < kNormMaxSms ? sm_count() : kNormMaxSms;
+    const int most = sms * s.per_sm, grid = T < 1 ? 1 : T < most ? T : most;
+    NormGradArgs a;
+    a.dy = static_cast<const uint8_t *>(dy);
+    a.x = static_cast<const uint8_t *>(x);
+    a.grad_sum = static_cast<const uint8_t *>(grad_sum);
+    a.weight = weight;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.T = T;
+    a.chunks = H / 8;
+    a.rms = kind == EPD_NORM_RMS;
+    a.inv_h = 1.0f / (float)H;
+    a.dx = static_cast<uint8_t *>(dx);
+    float *const part = static_cast<float *>(workspace);
+    // one block's sums are the gradients themselves
+    a.block_stride = grid == 1 ? 0 : 2 * (int64_t)H;
+    a.dweight = !dweight ? nullptr : grid == 1 ? dweight : part;
+    a.dbias = !dbias ? nullptr : grid == 1 ? dbias : part + H;
+    const size_t item = dtype == EPD_F32 ? 2 : 1;
+    const size_t stage = (1 + (grad_sum ? 2 : 1) * item) * s.nv * s.threads * 16;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    epd_status_t rc;
+    if (dtype == EPD_F32)
+        rc = s.nv == 1 ? launch_rows<norm_backward_kernel<float, 1>>(a, s, grid, stage, st)
+                       : launch_rows<norm_backward_kernel<float, 4>>(a, s, grid, stage, st);
+    else
+        rc = s.nv == 1 ? launch_rows<norm_backward_kernel<__nv_bfloat16, 1>>(a, s, grid, stage, st)
+                       : launch_rows<norm_backward_kernel<__nv_bfloat16, 4>>(a, s, grid, stage, st);
+    if (rc != EPD_OK || !sums || grid == 1) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((H + 127) / 128), dweight && dbias ? 2 : 1);
+    cfg.blockDim = dim3(kReduceThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, norm_reduce_kernel, (const float *)part, grid, a.block_stride, H, dweight, dbias);
+    return record_cuda_error();
+}
