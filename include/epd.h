@@ -78,7 +78,8 @@ typedef enum {
     EPD_ERR_CUDA = 3,           /* a CUDA call failed; epd_last_cuda_error() has the cause */
     EPD_ERR_INVALID_EXPERT = 4, /* (status word) topk_idx held an id outside [-1, E) */
     EPD_ERR_TIMEOUT = 5,        /* (status word) a bounded wait gave up (look-back, products) */
-    EPD_ERR_CAPACITY = 6,       /* (status word) a slot fell outside [0, capacity_rows) */
+    EPD_ERR_CAPACITY = 6,       /* (status word) a slot fell outside [0, capacity_rows), or a
+                                   position or page outside the cache */
     EPD_ERR_NONFINITE = 7,      /* (status word) a router logit was NaN or +inf, or a bias NaN */
 } epd_status_t;
 
@@ -622,6 +623,86 @@ EPD_API epd_status_t ep_layer_norm_backward(const void *dy, const void *x, epd_d
                                             int num_tokens, int hidden, epd_norm_t kind,
                                             void *workspace, void *dx, float *dweight,
                                             float *dbias, epd_stream_t stream);
+
+/* ------------------------------------------------------------------ positions and the cache
+ * For the attention ahead of the layer: rotary positions, the paged key-value cache and what
+ * reads it in a decode step. */
+
+/*
+ * Rotary positions. In every head the first rotary_dim = R elements are R/2 pairs -- elements
+ * (i, i + R/2), or (2i, 2i + 1) with `interleaved` -- and pair i of token t becomes
+ *   (a, b) -> rotary_scale * (a cos p - b sin p, a sin p + b cos p),
+ *   p = 2 pi * positions[t] * steps[i] / 2^64,
+ * in fp32 and rounded once; the other elements are copied. steps[i] is the fraction of a turn
+ * that one position adds to pair i, in units of 2^-64: round(f_i / (2 pi) * 2^64) mod 2^64 for
+ * an angular frequency f_i. The product is taken modulo 2^64, a whole turn, so that the angle is
+ * as good at position 2^31 - 1 as at 1: within 2^-24 of half a turn. With `inverse` the rotation is
+ * by -p: the gradient of the rotation.
+ *   x, out: [T, num_heads, head_dim] bfloat16 with the strides given (in elements, multiples of
+ *   8; the elements of a head lie together), 16-byte aligned; out may be x itself with the same
+ *   strides (the elements past R are then left alone), otherwise they must not overlap.
+ *   positions: [T] int32, any sign; steps: [R/2] uint64.
+ * head_dim % 8 == 0, up to 256 (EPD_ERR_UNSUPPORTED beyond); R even, in [2, head_dim].
+ */
+EPD_API epd_status_t ep_rotary(const void *x, int64_t token_stride, int64_t head_stride,
+                               const int32_t *positions, const uint64_t *steps, int num_tokens,
+                               int num_heads, int head_dim, int rotary_dim, int interleaved,
+                               float rotary_scale, int inverse, void *out,
+                               int64_t out_token_stride, int64_t out_head_stride,
+                               epd_stream_t stream);
+
+/*
+ * A paged key-value cache. Position p of sequence s lies on page n = page_table[s * table_stride
+ * + p / page_size], in its row p % page_size; head h of that row is the head_dim elements from
+ *   k (or v) + n * page_stride + (p % page_size) * token_stride + h * head_stride   (elements),
+ * so that [page, row, head, dim] and [page, head, row, dim] orders are both a matter of strides.
+ * With EPD_FP8_E4M3 every row and head has one float32 scale for its keys and one for its
+ * values, at n * scale_page_stride + (p % page_size) * scale_token_stride + h *
+ * scale_head_stride of k_scale and v_scale: a value is e4m3 * scale.
+ * head_dim % 8 == 0 (e4m3: % 16), up to 256 (EPD_ERR_UNSUPPORTED beyond); strides multiples of 16
+ * bytes; k and v 16-byte aligned; max_pages * page_size <= INT32_MAX. Pages may be shared by
+ * sequences and lie in any order; entries past a sequence's last position are not read. The
+ * struct itself is a host pointer.
+ */
+typedef struct {
+    epd_dtype_t dtype; /* EPD_BF16, or EPD_FP8_E4M3 */
+    int num_kv_heads;
+    int head_dim;
+    int page_size;
+    int64_t num_pages;
+    void *k, *v;
+    float *k_scale, *v_scale; /* EPD_FP8_E4M3 only, else NULL */
+    int64_t page_stride, token_stride, head_stride;
+    int64_t scale_page_stride, scale_token_stride, scale_head_stride;
+    const int32_t *page_table; /* device [num_seqs, max_pages], rows table_stride apart */
+    int num_seqs;
+    int max_pages;
+    int64_t table_stride;
+} epd_cache_t;
+
+/*
+ * Appends keys and values to the cache, the keys (and the queries, where given) rotated as
+ * ep_rotary does. Token t is position positions[t] of sequence token_seq[t] (of sequence t where
+ * token_seq is NULL): its keys and values are written to that position's row, its rotated
+ * queries to q_out. Prompts and single tokens are the same call. An e4m3 cache takes
+ * scale = amax / 448 of the head's fp32 values (1 if amax = 0) and e4m3(value / scale), nearest even.
+ * A token of sequence -1 is padding: nothing of it is read or written. A sequence outside
+ * [-1, num_seqs), a position outside the sequence's pages or a page outside [0, num_pages) sets
+ * EPD_ERR_CAPACITY, and the token is left out like padding. Two tokens at one position: one of
+ * the two is kept for each head.
+ *   q, q_out: [T, num_heads, head_dim], k, v: [T, num_kv_heads, head_dim] bfloat16, the heads of a
+ *   token next to each other, tokens the given strides apart (elements, multiples of 8), 16-byte
+ *   aligned: parts of one projection's rows are taken as they are. q may be NULL; q_out may be q
+ *   itself with the same stride. rotary_dim 0 (steps NULL): no rotation.
+ */
+EPD_API epd_status_t ep_cache_append(const epd_cache_t *cache, const void *q,
+                                     int64_t q_token_stride, int num_heads, const void *k,
+                                     int64_t k_token_stride, const void *v, int64_t v_token_stride,
+                                     const int32_t *positions, const int32_t *token_seq,
+                                     int num_tokens, const uint64_t *steps, int rotary_dim,
+                                     int interleaved, float rotary_scale, void *q_out,
+                                     int64_t q_out_token_stride, int32_t *status,
+                                     epd_stream_t stream);
 
 /*
  * Allocation-free variant of ep_dispatch_layout. The pages have no counterpart:

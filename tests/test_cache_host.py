@@ -1,0 +1,56 @@
+"""Argument checks of the rotary positions' and the cache's C entry points: refused on the host,
+before any launch (no GPU needed)."""
+import ctypes
+
+import pytest
+
+from unpermute_ep_dispatch_gb300 import _binding, build
+
+INVALID, UNSUPPORTED, OK = _binding.EPD_ERR_INVALID_ARG, _binding.EPD_ERR_UNSUPPORTED, _binding.EPD_OK
+FAKE = ctypes.c_void_p(0x10000)        # aligned, never dereferenced
+ODD = ctypes.c_void_p(0x10004)         # 4-aligned, not 16-aligned
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return _binding.load_library()
+
+
+def cache(dt=0, KH=2, D=64, page=16, P=4, k=0x10000, v=0x10000, ks=None, vs=None, sp=2048, st=128, sh=64, cp=0, ct=0,
+          ch=0, table=0x10000, S=4, M=3, ts=3):
+    return ctypes.byref(_binding.KVCache(dt, KH, D, page, P, k, v, ks, vs, sp, st, sh, cp, ct, ch, table, S, M, ts))
+
+
+BAD_CACHES = [dict(dt=2), dict(KH=0), dict(D=0), dict(D=60), dict(page=0), dict(P=-1), dict(P=1 << 31), dict(k=None),
+              dict(v=None), dict(k=0x10004), dict(v=0x10008), dict(ks=0x10000), dict(vs=0x10000), dict(sp=-8),
+              dict(st=4), dict(sh=12), dict(table=None), dict(table=0x10002), dict(S=-1), dict(M=-1), dict(ts=2),
+              dict(page=1 << 30, M=2, ts=2), dict(dt=1), dict(dt=1, ks=0x10000, vs=0x10000, D=72),
+              dict(dt=1, ks=0x10000, vs=0x10000, sh=72), dict(dt=1, ks=0x10002, vs=0x10000)]
+
+
+def test_rotary_rejects_bad_args(lib):
+    ok = dict(x=FAKE, ts=128, hs=64, pos=FAKE, steps=FAKE, T=4, N=2, D=64, R=64, inter=0, scale=1.0, inv=0, out=FAKE,
+              ots=128, ohs=64, s=None)
+    call = lambda **kw: lib.ep_rotary(*dict(ok, **kw).values())  # noqa: E731
+    for kw in (dict(T=-1), dict(N=-1), dict(D=0), dict(D=60), dict(R=0), dict(R=3), dict(R=66), dict(R=-2), dict(x=None),
+               dict(out=None), dict(pos=None), dict(steps=None), dict(x=ODD), dict(out=ODD), dict(ts=4), dict(hs=-8),
+               dict(ots=12), dict(ohs=4), dict(scale=float("nan")), dict(pos=ctypes.c_void_p(0x10002)), dict(steps=ODD)):
+        assert call(**kw) == INVALID, kw
+    assert call(D=264, R=64) == UNSUPPORTED
+    assert call(T=0, x=None, out=None, pos=None) == OK
+    assert call(N=0, x=None, out=None) == OK
+
+
+def test_append_rejects_bad_args(lib):
+    ok = dict(c=cache(), q=None, qs=0, QH=0, k=FAKE, ks=128, v=FAKE, vs=128, pos=FAKE, seq=None, T=4, steps=None, R=0,
+              inter=0, scale=1.0, qo=None, qos=0, st=FAKE, s=None)
+    call = lambda **kw: lib.ep_cache_append(*dict(ok, **kw).values())  # noqa: E731
+    for kw in ([dict(c=cache(**b)) for b in BAD_CACHES] + [
+            dict(c=None), dict(T=-1), dict(T=5), dict(QH=-1), dict(k=None), dict(v=None), dict(k=ODD), dict(v=ODD),
+            dict(ks=4), dict(vs=-8), dict(pos=None), dict(pos=ctypes.c_void_p(0x10002)), dict(st=None), dict(R=64),
+            dict(R=3, steps=FAKE), dict(R=66, steps=FAKE), dict(q=FAKE, QH=4, qs=256), dict(q=ODD, QH=4, qs=256, qo=FAKE),
+            dict(q=FAKE, QH=4, qs=12, qo=FAKE), dict(seq=ctypes.c_void_p(0x10002))]):
+        assert call(**kw) == INVALID, kw
+    assert call(c=cache(D=264)) == UNSUPPORTED
+    assert call(T=0, k=None, v=None, pos=None) == OK

@@ -10,6 +10,7 @@ torch.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 from typing import Optional
@@ -52,11 +53,25 @@ class ExpertRows(ctypes.Structure):
                 ("tokens_per_expert", ctypes.c_void_p)]
 
 
+class KVCache(ctypes.Structure):
+    """epd_cache_t."""
+    _fields_ = [("dtype", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("num_pages", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("scale_page_stride", ctypes.c_int64),
+                ("scale_token_stride", ctypes.c_int64), ("scale_head_stride", ctypes.c_int64),
+                ("page_table", ctypes.c_void_p), ("num_seqs", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("table_stride", ctypes.c_int64)]
+
+
 # name -> (restype, argtypes); mirrors include/epd.h
 _P, _I, _I64, _U32, _SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint32,
                            ctypes.c_size_t)
 _F = ctypes.c_float
 _ROWS = ctypes.POINTER(ExpertRows)
+_CACHE = ctypes.POINTER(KVCache)
 SIGNATURES = {
     "epd_status_string": (ctypes.c_char_p, [_I]),
     "epd_version": (_I, []),
@@ -88,6 +103,9 @@ SIGNATURES = {
     "ep_layer_norm": (_I, [_P, _I, _P, _P, _P, _I, _I, _F, _I, _P, _P, _P, _P, _P, _P, _P]),
     "epd_norm_workspace_bytes": (_SZ, [_I]),
     "ep_layer_norm_backward": (_I, [_P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "ep_rotary": (_I, [_P, _I64, _I64, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P, _I64, _I64, _P]),
+    "ep_cache_append": (_I, [_CACHE, _P, _I64, _I, _P, _I64, _P, _I64, _P, _P, _I, _P, _I, _I, _F,
+                             _P, _I64, _P, _P]),
     "ep_dispatch_layout_noalloc": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
     "epd_test_expert_matmul_stalled": (_I, [_ROWS, _P, _I, _P, _I64, _I64, _I64, _P, _P, _I, _I, _I,
                                             _P, _P, _I, _I64, _P]),
@@ -941,6 +959,208 @@ def ep_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[t
                  _ptr(dweight), _ptr(dbias), _stream(stream, dev))
     _check(rc, "ep_layer_norm_backward")
     return dx, dweight, dbias
+
+
+# ----------------------------------------------------------------------------- positions and the cache
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
+                       factor: float = 1.0, original_length: int = 4096, beta_fast: float = 32.0,
+                       beta_slow: float = 1.0):
+    """Angular frequencies of rotary positions (float64 [rotary_dim/2], on the CPU) and the scale
+    of the rotated values that belongs to them. base ** (-2i / rotary_dim), and for contexts
+    `factor` times longer: "linear" divides them by the factor; "ntk" raises the base so that the
+    slowest pair is slowed by the factor and the fastest not at all; "yarn" divides those that turn
+    less than beta_slow times over original_length, keeps those that turn more than beta_fast
+    times, blends between, and scales by 0.1 ln(factor) + 1."""
+    R = int(rotary_dim)
+    if R < 2 or R % 2:
+        raise ValueError(f"rotary_dim must be even and at least 2, got {rotary_dim}")
+    if not base > 0 or not factor >= 1:
+        raise ValueError("base must be positive and factor at least 1")
+    if scaling not in ("none", "linear", "ntk", "yarn"):
+        raise ValueError(f'scaling must be "none", "linear", "ntk" or "yarn", got {scaling!r}')
+    if scaling == "ntk" and R > 2:
+        base = base * factor ** (R / (R - 2))
+    f = base ** (-torch.arange(0, R, 2, dtype=torch.float64) / R)
+    if scaling == "linear":
+        return f / factor, 1.0
+    if scaling != "yarn" or factor == 1:
+        return f, 1.0
+
+    def pair_of(turns):  # the (fractional) pair that turns so often over the original length
+        return R * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+    low = max(math.floor(pair_of(beta_fast)), 0)
+    high = min(math.ceil(pair_of(beta_slow)), R - 1)
+    slow = ((torch.arange(R // 2, dtype=torch.float64) - low) / max(high - low, 1e-3)).clamp(0, 1)
+    return f * (1 - slow) + f / factor * slow, 0.1 * math.log(factor) + 1.0
+
+
+def rotary_steps(frequencies, device=None) -> torch.Tensor:
+    """`steps` of ep_rotary and ep_cache_append (int64 [rotary_dim/2]: the bits of the unsigned
+    fractions) from angular frequencies: a tensor or sequence of numbers, float64 where far
+    positions matter. Made once (it reads the frequencies on the host)."""
+    if isinstance(frequencies, torch.Tensor):
+        if device is None and frequencies.is_cuda:
+            device = frequencies.device
+        frequencies = frequencies.detach().double().cpu().tolist()
+    steps = []
+    for f in frequencies:
+        turns = float(f) / (2 * math.pi)
+        if not math.isfinite(turns):
+            raise ValueError(f"frequencies must be finite, got {f}")
+        u = round(math.ldexp(math.fmod(turns, 1.0), 64)) % (1 << 64)
+        steps.append(u - (1 << 64) if u >> 63 else u)
+    return torch.tensor(steps, dtype=torch.int64, device=device or torch.device("cuda"))
+
+
+def _heads(t, name, heads=None, dim=None, tokens=None, device=None):
+    """Rows of heads [T, heads, dim], bfloat16, the elements of a head next to each other."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    shape = t.shape
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or \
+            (dim is not None and shape[2] != dim) or (tokens is not None and shape[0] != tokens):
+        want = ", ".join(str(n) if v is None else str(v)
+                         for n, v in (("T", tokens), ("heads", heads), ("dim", dim)))
+        raise ValueError(f"{name} must be [{want}], got {tuple(shape)}")
+    if not t.is_cuda or (device is not None and t.get_device() != device.index):
+        raise ValueError(f"{name} is on {t.device}, expected {device or 'a CUDA device'}")
+    if t.stride(2) != 1 and shape[2] > 1:
+        raise ValueError(f"the elements of {name}'s heads must lie next to each other")
+    return t
+
+
+def _token_rows(t, name, *args, **kw):
+    """_heads whose heads lie next to each other too; returns the tokens' stride."""
+    _heads(t, name, *args, **kw)
+    if t.shape[1] > 1 and t.stride(1) != t.shape[2]:
+        raise ValueError(f"the heads of a token of {name} must lie next to each other")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _steps(steps, dim, device):
+    if steps is None:
+        return 0
+    if not isinstance(steps, torch.Tensor) or steps.dim() != 1:
+        raise ValueError("steps must be an int64 tensor [rotary_dim / 2]")
+    _want(steps, "steps", torch.int64, device=device)
+    if 2 * steps.shape[0] > dim:
+        raise ValueError(f"steps of {steps.shape[0]} pairs, heads of {dim} elements")
+    return 2 * steps.shape[0]
+
+
+def ep_rotary(x: torch.Tensor, positions: torch.Tensor, steps: torch.Tensor,
+              interleaved: bool = False, rotary_scale: float = 1.0, inverse: bool = False,
+              out=None, stream=None):
+    """Rotary positions of x [T, heads, dim] bfloat16 (any strides that are multiples of 8
+    elements, the elements of a head together): the first 2 * len(steps) elements of every head
+    are turned by positions [T] int32 times steps (rotary_steps). inverse: by the negative angle,
+    which is the gradient. out may be x. Returns out [T, heads, dim]; see epd.h."""
+    _heads(x, "x")
+    dev = x.device
+    T, N, D = x.shape
+    _want(positions, "positions", torch.int32, (T,), dev)
+    if steps is None:
+        raise TypeError("steps must be a torch.Tensor")
+    R = _steps(steps, D, dev)
+    if out is None:
+        out = torch.empty((T, N, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _heads(out, "out", N, D, T, dev)
+    rc = _launch(load_library().ep_rotary, dev, _ptr(x), x.stride(0) if T > 1 else 0,
+                 x.stride(1) if N > 1 else 0, _ptr(positions), _ptr(steps), T, N, D, R,
+                 int(bool(interleaved)), float(rotary_scale), int(bool(inverse)), _ptr(out),
+                 out.stride(0) if T > 1 else 0, out.stride(1) if N > 1 else 0,
+                 _stream(stream, dev))
+    _check(rc, "ep_rotary")
+    return out
+
+
+def _cache(k, v, page_table, k_scale, v_scale):
+    """epd_cache_t of k and v [pages, page_size, kv_heads, dim], page_table [seqs, max_pages]."""
+    dtype = k.dtype if isinstance(k, torch.Tensor) else None
+    fp8 = dtype is torch.float8_e4m3fn
+    if not fp8 and dtype is not torch.bfloat16:
+        raise ValueError("the cache must be a bfloat16 or float8_e4m3fn tensor")
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError("the cache must be [pages, page_size, kv_heads, dim]")
+    if not k.is_cuda:
+        raise ValueError("the cache must be a CUDA tensor")
+    dev = k.device
+    P, rows, KH, D = shape
+    sp, st, sh, sd = k.stride()
+    if not isinstance(v, torch.Tensor) or v.dtype is not dtype or v.shape != shape or v.device != dev:
+        raise ValueError("the values' cache must have the keys' type, shape and device")
+    if v.stride() != (sp, st, sh, sd):
+        raise ValueError("the values' cache must have the keys' strides")
+    if sd != 1 and D > 1:
+        raise ValueError("the elements of the cache's heads must lie next to each other")
+    cp = ct = ch = 0
+    if fp8:
+        for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if not isinstance(s, torch.Tensor) or s.dtype is not torch.float32 or \
+                    s.shape != (P, rows, KH) or s.device != dev:
+                raise ValueError(f"{name} must be a float32 tensor {(P, rows, KH)} on {dev}")
+        cp, ct, ch = k_scale.stride()
+        if v_scale.stride() != (cp, ct, ch):
+            raise ValueError("v_scale must have the strides of k_scale")
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("a bf16 cache takes no scales")
+    if not isinstance(page_table, torch.Tensor) or page_table.dtype is not torch.int32 or \
+            page_table.dim() != 2 or page_table.device != dev or \
+            (page_table.stride(1) != 1 and page_table.shape[1] > 1):
+        raise ValueError(f"page_table must be an int32 tensor [seqs, max_pages] on {dev}, "
+                         "its rows' entries next to each other")
+    S, M = page_table.shape
+    return KVCache(EPD_FP8_E4M3 if fp8 else EPD_BF16, KH, D, rows, P, _ptr(k), _ptr(v),
+                   _ptr(k_scale), _ptr(v_scale), sp if P > 1 else 0, st if rows > 1 else 0,
+                   sh if KH > 1 else 0, cp, ct, ch, _ptr(page_table), S, M,
+                   max(M, page_table.stride(0)) if S > 1 else M)
+
+
+def ep_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    page_table: torch.Tensor, positions: torch.Tensor, status: torch.Tensor,
+                    token_seq: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                    steps: Optional[torch.Tensor] = None, interleaved: bool = False,
+                    rotary_scale: float = 1.0, k_scale: Optional[torch.Tensor] = None,
+                    v_scale: Optional[torch.Tensor] = None, q_out=None, stream=None):
+    """Appends k and v [T, kv_heads, dim] bfloat16 to the paged cache k_cache, v_cache [pages,
+    page_size, kv_heads, dim] (bfloat16, or float8_e4m3fn with k_scale, v_scale [pages, page_size,
+    kv_heads] float32; any strides that are multiples of 16 bytes), keys rotated by `steps`. Token
+    t is position positions[t] (int32) of sequence token_seq[t] (int32, -1 for padding; t where
+    None), a row of page_table [seqs, max_pages] int32. q [T, heads, dim] is rotated too. k, v, q
+    may be slices of one projection's rows. Returns q_out [T, heads, dim], or None; see epd.h."""
+    c = _cache(k_cache, v_cache, page_table, k_scale, v_scale)
+    dev = k_cache.device
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be [T, kv_heads, dim]")
+    T, KH, D = k.shape[0], c.num_kv_heads, c.head_dim
+    ks = _token_rows(k, "k", KH, D, T, dev)
+    vs = _token_rows(v, "v", KH, D, T, dev)
+    _want(positions, "positions", torch.int32, (T,), dev)
+    _want(status, "status", torch.int32, (1,), dev)
+    if token_seq is not None:
+        _want(token_seq, "token_seq", torch.int32, (T,), dev)
+    elif T > c.num_seqs:
+        raise ValueError("token_seq is needed for more tokens than sequences")
+    R = _steps(steps, D, dev)
+    QH = qs = os_ = 0
+    if q is not None:
+        qs = _token_rows(q, "q", None, D, T, dev)
+        QH = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, QH, D), dtype=torch.bfloat16, device=dev)
+        os_ = _token_rows(q_out, "q_out", QH, D, T, dev)
+    elif q_out is not None:
+        raise ValueError("q_out is the rotated q")
+    rc = _launch(load_library().ep_cache_append, dev, ctypes.byref(c), _ptr(q), qs, QH, _ptr(k),
+                 ks, _ptr(v), vs, _ptr(positions), _ptr(token_seq), T, _ptr(steps), R,
+                 int(bool(interleaved)), float(rotary_scale), _ptr(q_out), os_, _ptr(status),
+                 _stream(stream, dev))
+    _check(rc, "ep_cache_append")
+    return q_out
 
 
 def ep_dispatch_layout_noalloc(topk_idx: torch.Tensor, num_experts: int, num_ranks: int,

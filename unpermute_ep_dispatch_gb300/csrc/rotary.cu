@@ -1,0 +1,461 @@
+// rotary.cu -- rotary positions (ep_rotary) and appending to the paged cache with the rotation on
+// the way (ep_cache_append).
+//
+// A pair (a, b) of a head becomes A (a cos - b sin), A (a sin + b cos) with the angle position *
+// frequency. The caller gives each pair's frequency as the fraction of a turn that one position adds,
+// in units of 2^-64: position * step, in 64-bit integers, is then the whole angle modulo one turn,
+// without the cancellation that a product in 32 bits (or a range reduction) has at far positions, and
+// without 64-bit floating point, of which this GPU has little.
+//
+// Bound by HBM: every value is read and written once. A head is cut into chunks of V pairs, one a
+// lane, in groups of a power of two of lanes a head; a warp takes its token's heads several at a
+// time, with the loads of up to four such passes in flight, and the lane's sines and cosines serve
+// all of them. What is not rotated travels as pairs of angle zero. In an e4m3 cache every token and
+// head has its own scale, amax / 448, from the head's lanes by shuffles.
+#include <cuda_fp8.h>
+
+#include "cache.cuh"
+
+namespace epd {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kBatch = 4;  // passes whose loads are in flight at once
+constexpr unsigned kAll = 0xffffffffu;
+
+struct Turn {
+    const uint64_t *step;  // [R / 2], null for no rotation
+    int R, inverse;
+    float scale;
+};
+
+// How a warp walks over a token's heads.
+struct Walk {
+    int chunks;     // chunks of a head: the first R / 2V are rotated
+    int lanes_log;  // log2 of the lanes of a head
+    int heads, passes, parts;  // passes: of a warp; parts: warps of a token
+};
+
+struct RotaryArgs {
+    const uint8_t *x;
+    uint8_t *out;
+    int64_t x_token, x_head, out_token, out_head;  // bytes
+    const int32_t *positions;
+    int T, D;
+    Turn turn;
+    Walk walk;
+};
+
+struct AppendArgs {
+    const uint8_t *q, *k, *v;
+    uint8_t *q_out;
+    int64_t q_token, k_token, v_token, q_out_token;  // bytes
+    const int32_t *positions, *token_seq;
+    int T, QH;
+    epd_cache_t cache;
+    Turn turn;
+    Walk walk;
+    int32_t *status;
+};
+
+// Where the pairs of chunk p lie in a head of D elements: V of their first halves from `a`, V of
+// their second halves from `b`; interleaved pairs lie at a + 2 i and a + 2 i + 1.
+template <int V, bool INTER>
+struct Place {
+    int a, b;
+    __device__ __forceinline__ Place(int p, int R, int D) {
+        if (INTER) {
+            a = 2 * V * p;
+            b = a + 1;
+        } else if (p < R / (2 * V)) {
+            a = V * p;
+            b = a + R / 2;
+        } else {
+            a = R + V * (p - R / (2 * V));
+            b = a + (D - R) / 2;
+        }
+    }
+};
+
+// The values are read once, and may be written over by the same thread (not the read-only path).
+__device__ __forceinline__ uint4 ld16(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 ld8(const void *p) {
+    uint2 v;
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+    return v;
+}
+
+// The raw 2 V bf16 values of a chunk: V == 8 halves as two 16-byte words, interleaved V == 4 as one,
+// V == 4 halves as two 8-byte words, V == 1 as one 4-byte word.
+template <int V, bool INTER>
+struct Raw {
+    uint32_t w[V];
+    __device__ __forceinline__ void load(const uint8_t *head, const Place<V, INTER> &at) {
+        if constexpr (V == 8) {
+            const uint4 x = ld16(head + 2 * at.a), y = ld16(head + 2 * at.b);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+        } else if constexpr (V == 4 && INTER) {
+            const uint4 x = ld16(head + 2 * at.a);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+        } else if constexpr (V == 4) {
+            const uint2 x = ld8(head + 2 * at.a), y = ld8(head + 2 * at.b);
+            w[0] = x.x, w[1] = x.y, w[2] = y.x, w[3] = y.y;
+        } else if constexpr (INTER) {
+            w[0] = *reinterpret_cast<const volatile uint32_t *>(head + 2 * at.a);
+        } else {
+            const volatile uint16_t *h = reinterpret_cast<const volatile uint16_t *>(head);
+            w[0] = (uint32_t)h[at.a] | (uint32_t)h[at.b] << 16;
+        }
+    }
+    // In 32 bits, first halves and second halves.
+    __device__ __forceinline__ void values(float (&a)[V], float (&b)[V]) const {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (INTER || V == 1) {
+                a[i] = lo_bf16(w[i]);
+                b[i] = hi_bf16(w[i]);
+            } else {
+                a[i] = i & 1 ? hi_bf16(w[i / 2]) : lo_bf16(w[i / 2]);
+                b[i] = i & 1 ? hi_bf16(w[V / 2 + i / 2]) : lo_bf16(w[V / 2 + i / 2]);
+            }
+        }
+    }
+};
+
+template <int V, bool INTER>
+__device__ __forceinline__ void store_bf16(uint8_t *head, const Place<V, INTER> &at, const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V == 1) {
+        const uint32_t w = pack2_bf16(a[0], b[0]);
+        if (INTER) {
+            *reinterpret_cast<uint32_t *>(head + 2 * at.a) = w;
+        } else {
+            reinterpret_cast<uint16_t *>(head)[at.a] = (uint16_t)w;
+            reinterpret_cast<uint16_t *>(head)[at.b] = (uint16_t)(w >> 16);
+        }
+    } else if constexpr (INTER) {
+        st16(head + 2 * at.a, make_uint4(pack2_bf16(a[0], b[0]), pack2_bf16(a[1], b[1]), pack2_bf16(a[2], b[2]),
+                                         pack2_bf16(a[3], b[3])));
+    } else if constexpr (V == 4) {
+        *reinterpret_cast<uint2 *>(head + 2 * at.a) = make_uint2(pack2_bf16(a[0], a[1]), pack2_bf16(a[2], a[3]));
+        *reinterpret_cast<uint2 *>(head + 2 * at.b) = make_uint2(pack2_bf16(b[0], b[1]), pack2_bf16(b[2], b[3]));
+    } else {
+        st16(head + 2 * at.a, pack8_bf16(a));
+        st16(head + 2 * at.b, pack8_bf16(b));
+    }
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+template <int V, bool INTER>
+__device__ __forceinline__ void store_e4m3(uint8_t *head, const Place<V, INTER> &at, float (&a)[V], float (&b)[V], float scale) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        a[i] = __fdiv_rn(a[i], scale);
+        b[i] = __fdiv_rn(b[i], scale);
+    }
+    if constexpr (V == 1) {
+        const uint32_t w = e4m3x2(a[0], b[0]);
+        head[at.a] = (uint8_t)w;
+        head[at.b] = (uint8_t)(w >> 8);
+    } else if constexpr (INTER) {
+        *reinterpret_cast<uint2 *>(head + at.a) =
+            make_uint2(e4m3x2(a[0], b[0]) | e4m3x2(a[1], b[1]) << 16, e4m3x2(a[2], b[2]) | e4m3x2(a[3], b[3]) << 16);
+    } else {
+        uint32_t u[V / 2];
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            u[i] = e4m3x2(a[4 * i], a[4 * i + 1]) | e4m3x2(a[4 * i + 2], a[4 * i + 3]) << 16;
+            u[V / 4 + i] = e4m3x2(b[4 * i], b[4 * i + 1]) | e4m3x2(b[4 * i + 2], b[4 * i + 3]) << 16;
+        }
+        if constexpr (V == 4) {
+            *reinterpret_cast<uint32_t *>(head + at.a) = u[0];
+            *reinterpret_cast<uint32_t *>(head + at.b) = u[1];
+        } else {
+            *reinterpret_cast<uint2 *>(head + at.a) = make_uint2(u[0], u[1]);
+            *reinterpret_cast<uint2 *>(head + at.b) = make_uint2(u[2], u[3]);
+        }
+    }
+}
+
+// Cosines and sines of chunk p's pairs at a position, times the scale; 1 and 0 past the rotated part.
+template <int V>
+__device__ __forceinline__ void angles(const Turn &t, int p, int position, float (&c)[V], float (&s)[V]) {
+    const bool turned = p < t.R / (2 * V);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        c[i] = 1.0f;
+        s[i] = 0.0f;
+        if (turned) {
+            const uint64_t phase = (uint64_t)(int64_t)position * __ldg(t.step + p * V + i);
+            // half turns in [-1, 1)
+            sincospif((float)(int32_t)(phase >> 32) * 4.656612873077392578125e-10f, &s[i], &c[i]);
+            c[i] *= t.scale;
+            s[i] *= t.inverse ? -t.scale : t.scale;
+        }
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void rotate(float (&a)[V], float (&b)[V], const float (&c)[V], const float (&s)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float x = a[i], y = b[i];
+        a[i] = x * c[i] - y * s[i];
+        b[i] = x * s[i] + y * c[i];
+    }
+}
+
+template <int V, bool INTER>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
+    const int lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_trigger();
+    const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t t = unit / a.walk.parts;
+    if (t >= a.T) return;
+    const int per_pass = 32 >> a.walk.lanes_log, lanes = 1 << a.walk.lanes_log;
+    const int first = (int)(unit - t * a.walk.parts) * a.walk.passes * per_pass + (lane >> a.walk.lanes_log);
+    const int position = __ldg(a.positions + t);
+    const uint8_t *x = a.x + t * a.x_token;
+    uint8_t *out = a.out + t * a.out_token;
+    for (int p = lane & (lanes - 1); p < a.walk.chunks; p += lanes) {
+        const Place<V, INTER> at(p, a.turn.R, a.D);
+        float c[V], s[V];
+        angles<V>(a.turn, p, position, c, s);
+        for (int i0 = 0; i0 < a.walk.passes; i0 += kBatch) {
+            Raw<V, INTER> raw[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int n = first + (i0 + i) * per_pass;
+                if (i0 + i < a.walk.passes && n < a.walk.heads) raw[i].load(x + n * a.x_head, at);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int n = first + (i0 + i) * per_pass;
+                if (i0 + i < a.walk.passes && n < a.walk.heads) {
+                    float u[V], w[V];
+                    raw[i].values(u, w);
+                    rotate<V>(u, w, c, s);
+                    store_bf16<V, INTER>(out + n * a.out_head, at, u, w);
+                }
+            }
+        }
+    }
+}
+
+// NP: chunks of a head that one lane holds (V == 1 only).
+template <int V, bool INTER, bool FP8, int NP>
+__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
+    const int lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_trigger();
+    const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t t = unit / a.walk.parts;
+    if (t >= a.T) return;
+    const epd_cache_t &kv = a.cache;
+    const int D = kv.head_dim, KH = kv.num_kv_heads;
+    const int position = __ldg(a.positions + t);
+    const int seq = a.token_seq ? __ldg(a.token_seq + t) : (int)t;
+    if (seq == -1) return;  // padding
+    int page = -1, inside = 0;
+    if (seq >= 0 && seq < kv.num_seqs && position >= 0 && position < cache_positions(kv)) {
+        page = __ldg(kv.page_table + seq * kv.table_stride + position / kv.page_size);
+        inside = position % kv.page_size;
+    }
+    if (page < 0 || page >= kv.num_pages) {
+        if (lane == 0) report(a.status, EPD_ERR_CAPACITY);
+        return;
+    }
+    const int64_t slot = page * kv.page_stride + inside * kv.token_stride;
+    const int64_t scale_slot = page * kv.scale_page_stride + inside * kv.scale_token_stride;
+    const int per_pass = 32 >> a.walk.lanes_log, lanes = 1 << a.walk.lanes_log;
+    const int first = (int)(unit - t * a.walk.parts) * a.walk.passes * per_pass + (lane >> a.walk.lanes_log);
+    const int p0 = lane & (lanes - 1);
+    constexpr int B = NP == 1 ? kBatch : 1;
+    float c[NP][V], s[NP][V];
+#pragma unroll
+    for (int q = 0; q < NP; ++q) angles<V>(a.turn, p0 + q * lanes, position, c[q], s[q]);
+    for (int i0 = 0; i0 < a.walk.passes; i0 += B) {
+        Raw<V, INTER> raw[B][NP];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int n = first + (i0 + i) * per_pass;
+            if (i0 + i >= a.walk.passes || n >= a.walk.heads) continue;
+            const uint8_t *head = n < a.QH ? a.q + t * a.q_token + (int64_t)n * D * 2
+                : n < a.QH + KH ? a.k + t * a.k_token + (int64_t)(n - a.QH) * D * 2
+                                : a.v + t * a.v_token + (int64_t)(n - a.QH - KH) * D * 2;
+#pragma unroll
+            for (int q = 0; q < NP; ++q)
+                if (p0 + q * lanes < a.walk.chunks)
+                    raw[i][q].load(head, Place<V, INTER>(p0 + q * lanes, a.turn.R, D));
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            if (i0 + i >= a.walk.passes) break;  // the same for the whole warp
+            const int n = first + (i0 + i) * per_pass;
+            const bool has = n < a.walk.heads, is_q = n < a.QH, is_v = n >= a.QH + KH;
+            float u[NP][V], w[NP][V], amax = 0.0f;
+#pragma unroll
+            for (int q = 0; q < NP; ++q)
+                if (has && p0 + q * lanes < a.walk.chunks) {
+                    raw[i][q].values(u[q], w[q]);
+                    if (!is_v) rotate<V>(u[q], w[q], c[q], s[q]);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) amax = fmaxf(amax, fmaxf(fabsf(u[q][j]), fabsf(w[q][j])));
+                }
+            if (FP8)
+                for (int d = lanes >> 1; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, d));
+            if (!has) continue;
+            const int h = is_v ? n - a.QH - KH : n - a.QH;  // of the cache
+            const float scale = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                if (p0 + q * lanes >= a.walk.chunks) continue;
+                const Place<V, INTER> at(p0 + q * lanes, a.turn.R, D);
+                if (is_q) {
+                    store_bf16<V, INTER>(a.q_out + t * a.q_out_token + (int64_t)n * D * 2, at, u[q], w[q]);
+                } else {
+                    uint8_t *base = static_cast<uint8_t *>(is_v ? kv.v : kv.k);
+                    const int64_t off = slot + h * kv.head_stride;
+                    if (FP8) store_e4m3<V, INTER>(base + off, at, u[q], w[q], scale);
+                    else store_bf16<V, INTER>(base + 2 * off, at, u[q], w[q]);
+                }
+            }
+            if (FP8 && !is_q && p0 == 0)
+                (is_v ? kv.v_scale : kv.k_scale)[scale_slot + h * kv.scale_head_stride] = scale;
+        }
+    }
+}
+
+// Chunks of V pairs: 16-byte words where the rotated part and the rest both split into them, 8-byte
+// words where they are multiples of 8, else single pairs.
+inline int pairs_of_chunk(int D, int R, bool inter) {
+    if (inter) return R % 8 == 0 ? 4 : 1;
+    return R % 16 == 0 && (D - R) % 16 == 0 ? 8 : R % 8 == 0 ? 4 : 1;
+}
+
+// `columns` of each of `heads` heads of T tokens in chunks of V pairs. A warp takes several passes
+// over a token's heads, up to eight, where that leaves 16 warps for each multiprocessor: the sines
+// and cosines are then shared by more heads.
+inline Walk walk_of(int T, int heads, int columns, int V) {
+    Walk w;
+    w.chunks = columns / (2 * V);
+    w.lanes_log = 0;
+    while ((1 << w.lanes_log) < w.chunks && w.lanes_log < 5) ++w.lanes_log;
+    w.heads = heads;
+    const int per_pass = 32 >> w.lanes_log, passes = (heads + per_pass - 1) / per_pass;
+    const int64_t share = (int64_t)T * passes / (16 * sm_count());
+    w.passes = share < 1 ? 1 : share < 8 ? (int)share : 8;
+    w.parts = (passes + w.passes - 1) / w.passes;
+    return w;
+}
+
+inline epd_status_t grid_of(int T, const Walk &w, int &grid) {
+    const int64_t warps = (int64_t)T * w.parts, blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
+    if (blocks > INT32_MAX) return EPD_ERR_UNSUPPORTED;
+    grid = (int)blocks;
+    return EPD_OK;
+}
+
+template <int V, bool INTER>
+epd_status_t launch_append(const AppendArgs &a, int grid, cudaStream_t st) {
+    constexpr int NP = V == 1 ? kMaxHeadDim / 2 / 32 : 1;
+    return a.cache.dtype == EPD_BF16 ? launch_pdl(append_kernel<V, INTER, false, NP>, grid, kThreads, 0, st, a)
+                                     : launch_pdl(append_kernel<V, INTER, true, NP>, grid, kThreads, 0, st, a);
+}
+
+inline bool rotation_ok(const uint64_t *steps, int R, int D, float scale) {
+    return R >= 0 && R % 2 == 0 && R <= D && (R == 0 || (steps && aligned8(steps))) && scale == scale;
+}
+
+}  // namespace
+}  // namespace epd
+
+extern "C" epd_status_t ep_rotary(const void *x, int64_t token_stride, int64_t head_stride, const int32_t *positions,
+                                  const uint64_t *steps, int num_tokens, int num_heads, int head_dim, int rotary_dim,
+                                  int interleaved, float rotary_scale, int inverse, void *out,
+                                  int64_t out_token_stride, int64_t out_head_stride, epd_stream_t stream) {
+    using namespace epd;
+    const int T = num_tokens, N = num_heads, D = head_dim, R = rotary_dim;
+    if (T < 0 || N < 0 || D < 8 || D % 8 != 0 || R < 2 || !rotation_ok(steps, R, D, rotary_scale))
+        return EPD_ERR_INVALID_ARG;
+    for (const int64_t s : {token_stride, head_stride, out_token_stride, out_head_stride})
+        if (s < 0 || s % 8 != 0) return EPD_ERR_INVALID_ARG;
+    if (D > kMaxHeadDim) return EPD_ERR_UNSUPPORTED;
+    if (T == 0 || N == 0) return EPD_OK;
+    if (!x || !out || !positions || !aligned16(x) || !aligned16(out) || !aligned4(positions)) return EPD_ERR_INVALID_ARG;
+    RotaryArgs a;
+    a.x = static_cast<const uint8_t *>(x);
+    a.out = static_cast<uint8_t *>(out);
+    a.x_token = 2 * token_stride, a.x_head = 2 * head_stride;
+    a.out_token = 2 * out_token_stride, a.out_head = 2 * out_head_stride;
+    a.positions = positions;
+    a.T = T;
+    a.D = D;
+    a.turn = {steps, R, inverse != 0, rotary_scale};
+    const int V = pairs_of_chunk(D, R, interleaved != 0);
+    // in place the part that is not rotated stays as it is
+    const bool in_place = x == out && token_stride == out_token_stride && head_stride == out_head_stride;
+    a.walk = walk_of(T, N, in_place ? R : D, V);
+    int grid;
+    if (const epd_status_t rc = grid_of(T, a.walk, grid)) return rc;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (interleaved)
+        return V == 4 ? launch_pdl(rotary_kernel<4, true>, grid, kThreads, 0, st, a)
+                      : launch_pdl(rotary_kernel<1, true>, grid, kThreads, 0, st, a);
+    return V == 8   ? launch_pdl(rotary_kernel<8, false>, grid, kThreads, 0, st, a)
+           : V == 4 ? launch_pdl(rotary_kernel<4, false>, grid, kThreads, 0, st, a)
+                    : launch_pdl(rotary_kernel<1, false>, grid, kThreads, 0, st, a);
+}
+
+extern "C" epd_status_t ep_cache_append(const epd_cache_t *cache, const void *q, int64_t q_token_stride,
+                                        int num_heads, const void *k, int64_t k_token_stride, const void *v,
+                                        int64_t v_token_stride, const int32_t *positions, const int32_t *token_seq,
+                                        int num_tokens, const uint64_t *steps, int rotary_dim, int interleaved,
+                                        float rotary_scale, void *q_out, int64_t q_out_token_stride, int32_t *status,
+                                        epd_stream_t stream) {
+    using namespace epd;
+    if (const epd_status_t rc = check_cache(cache)) return rc;
+    const int T = num_tokens, D = cache->head_dim, R = rotary_dim, QH = q ? num_heads : 0;
+    if (T < 0 || num_heads < 0 || !rotation_ok(steps, R, D, rotary_scale)) return EPD_ERR_INVALID_ARG;
+    for (const int64_t s : {q_token_stride, k_token_stride, v_token_stride, q_out_token_stride})
+        if (s < 0 || s % 8 != 0) return EPD_ERR_INVALID_ARG;
+    if (!status || !aligned4(status)) return EPD_ERR_INVALID_ARG;
+    if (!token_seq && T > cache->num_seqs) return EPD_ERR_INVALID_ARG;
+    if ((int64_t)QH + 2 * (int64_t)cache->num_kv_heads > INT32_MAX) return EPD_ERR_INVALID_ARG;
+    if (T == 0) return EPD_OK;
+    if (!k || !v || !positions || !aligned16(k) || !aligned16(v) || !aligned4(positions) || !aligned4(token_seq))
+        return EPD_ERR_INVALID_ARG;
+    if (q && (!q_out || !aligned16(q) || !aligned16(q_out))) return EPD_ERR_INVALID_ARG;
+    AppendArgs a;
+    a.q = static_cast<const uint8_t *>(q);
+    a.k = static_cast<const uint8_t *>(k);
+    a.v = static_cast<const uint8_t *>(v);
+    a.q_out = static_cast<uint8_t *>(q_out);
+    a.q_token = 2 * q_token_stride, a.k_token = 2 * k_token_stride, a.v_token = 2 * v_token_stride;
+    a.q_out_token = 2 * q_out_token_stride;
+    a.positions = positions;
+    a.token_seq = token_seq;
+    a.T = T;
+    a.QH = QH;
+    a.cache = *cache;
+    a.turn = {steps, R, 0, rotary_scale};
+    a.status = status;
+    // without rotation the chunks are runs of 16 bytes
+    const bool inter = interleaved || R == 0;
+    const int V = pairs_of_chunk(D, R, inter);
+    a.walk = walk_of(T, QH + 2 * cache->num_kv_heads, D, V);
+    int grid;
+    if (const epd_status_t rc = grid_of(T, a.walk, grid)) return rc;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (inter) return V == 4 ? launch_append<4, true>(a, grid, st) : launch_append<1, true>(a, grid, st);
+    return V == 8 ? launch_append<8, false>(a, grid, st)
+           : V == 4 ? launch_append<4, false>(a, grid, st)
+                    : launch_append<1, false>(a, grid, st);
+}
