@@ -705,6 +705,42 @@ EPD_API epd_status_t ep_cache_append(const epd_cache_t *cache, const void *q,
                                      epd_stream_t stream);
 
 /*
+ * Workspace size in bytes of ep_decode_attention for up to num_seqs sequences (0 for sizes it
+ * does not take). Host-only arithmetic. The workspace must be zero-filled once before its first use
+ * (epd_workspace_init); every call leaves it ready for calls of any lengths and of any sizes
+ * that fit. It serves one stream at a time: calls that overlap on the GPU and share a
+ * workspace race, two captured graphs included.
+ */
+EPD_API size_t epd_attention_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads,
+                                             int head_dim);
+
+/*
+ * Attention of one new token of every sequence over the paged cache (the token's own keys and
+ * values appended before). With G = num_heads / num_kv_heads, for sequence b and head h,
+ * over its live positions t -- [0, lengths[b]), or the last `window` of them where window > 0:
+ *   s_t = softmax_scale * q[b, h] . k[t, h / G],
+ *   out[b, h] = sum of exp(s_t) v[t, h / G] / sum of exp(s_t),  lse[b, h] = ln sum of exp(s_t)
+ * with fp32 sums and one rounding of out; 0 and -inf for a sequence of length 0. What lies in
+ * the cache outside the live positions is not used, whatever it is. lengths are device memory,
+ * read by the kernel: work is split evenly over the device for any mix of them. The order of the
+ * sums depends on the sizes, the lengths and the device, not on how blocks are scheduled: the same
+ * call gives the same bits again.
+ * A length outside [0, max_pages * page_size] sets EPD_ERR_INVALID_ARG (below) or
+ * EPD_ERR_CAPACITY (above) and counts as the nearer end; a page outside [0, num_pages) sets
+ * EPD_ERR_CAPACITY and its positions are left out.
+ *   q: [num_seqs, num_heads, head_dim] bfloat16, the heads of a sequence next to each other,
+ *   sequences q_token_stride elements apart (a multiple of 8); out: [num_seqs, num_heads,
+ *   head_dim] bfloat16; both 16-byte aligned; lse: [num_seqs, num_heads] float32 or NULL;
+ *   lengths: [num_seqs] int32. num_seqs is the cache's. Any G; heads are taken 16 at a time, so
+ *   that beyond 16 a key is read more than once. out must not overlap q.
+ */
+EPD_API epd_status_t ep_decode_attention(const epd_cache_t *cache, const void *q,
+                                         int64_t q_token_stride, int num_heads,
+                                         const int32_t *lengths, float softmax_scale, int window,
+                                         void *workspace, void *out, float *lse, int32_t *status,
+                                         epd_stream_t stream);
+
+/*
  * Allocation-free variant of ep_dispatch_layout. The pages have no counterpart:
  * this entry point exists for callers that cannot allocate device memory at
  * the moment they need the layout -- for example code running inside an

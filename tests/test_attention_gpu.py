@@ -1,0 +1,260 @@
+"""Decode attention over the paged cache on the GPU against the formula in 64 bits.
+
+Tolerances: half a step of bf16 for the output, and the weights' relative error times the sum of
+weight * |value|. The weights: a score's fp32 sum over D products of size |q| |k| (below 2^5 after
+the scale, 2^-24 for each of D / 16 + 4 additions in a chain: 2^-15), the exponential 2^-22, the
+weights' two bf16 parts 2^-17, together below 2^-14; in an e4m3 cache one fp16 part, 2^-12, on top.
+lse: the same 2^-14, and its own rounding."""
+import pytest
+import torch
+
+import unpermute_ep_dispatch_gb300 as epd
+from cache_formulas import attend, paged, values
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(999 + seed)
+    return g
+
+
+def check(lengths, page, KH, G, D, fp8=False, window=0, scale=None, order="page,row,head", seed=0, workspace=None,
+          q_scale=1.0, garbage=True, v_spread=False):
+    g = gen(seed)
+    B, QH = len(lengths), KH * G
+    most = max(1, -(-max(lengths) // page))
+    pages = B * most
+    k, v, ks, vs = paged(pages, page, KH, D, fp8, DEV, g, order)
+    if v_spread:  # values' scales over ten powers of two
+        vs *= torch.exp2(10 * torch.rand(vs.shape, generator=g, device=DEV) - 5)
+    table = torch.randperm(pages, generator=g, device=DEV).to(torch.int32).view(B, most)
+    lens = torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    # one projection's rows: the queries are slices of them
+    q = (torch.randn(B, QH + 2, D, generator=g, device=DEV) * q_scale).to(torch.bfloat16)[:, 1:QH + 1]
+    want, lse = attend(q, values(k, ks), values(v, vs), table, lens, scale, window)
+    size, _ = attend(q, values(k, ks), values(v, vs).abs(), table, lens, scale, window)
+    if garbage:  # what is not live may hold anything
+        at = torch.arange(most * page, device=DEV)
+        dead = (at >= lens[:, None]) | ((at < lens[:, None] - window) if window else False)
+        where = table[:, at // page].long()[dead], (at % page).expand(B, -1)[dead]
+        for t in (k, v):
+            if fp8:
+                t.view(torch.uint8)[where] = 0x7F
+            else:
+                t[where] = float("nan")
+        if fp8:
+            ks[where], vs[where] = float("nan"), float("inf")
+        table[(at[::page] >= lens[:, None])] = 10**9
+    status = epd.new_status(DEV)
+    if workspace is None:
+        workspace = epd.new_attention_workspace(B, QH, KH, D, DEV)
+    kw = dict(k_scale=ks, v_scale=vs, softmax_scale=scale, window=window, with_lse=True)
+    out, got_lse = epd.ep_decode_attention(q, k, v, table, lens, workspace, status, **kw)
+    assert int(status) == 0
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -14 + (2.0 ** -12 if fp8 else 0)) * size
+    err = (out.double() - want).abs()
+    assert bool((err <= tol).all()), (float((err - tol).max()), float(err.max()))
+    empty = lens <= 0
+    assert bool((out[empty] == 0).all()) and bool((got_lse[empty] == -float("inf")).all())
+    live = ~empty
+    assert bool(((got_lse[live].double() - lse[live]).abs() <= 2.0 ** -14 + 2.0 ** -23 * lse[live].abs()).all())
+    again, lse2 = epd.ep_decode_attention(q, k, v, table, lens, workspace, status, **kw)
+    assert torch.equal(out, again) and torch.equal(got_lse, lse2)
+    return workspace
+
+
+RAGGED = [0, 1, 15, 16, 17, 127, 128, 129, 1000, 2, 0, 333]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [16, 64, 80, 96, 128, 192, 256])
+@pytest.mark.parametrize("KH,G", [(1, 1), (2, 4), (3, 7), (1, 16), (2, 17), (1, 40), (8, 8)])
+def test_heads(KH, G, D, fp8):
+    check(RAGGED, 16, KH, G, D, fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("order", ["page,row,head", "page,head,row"])
+@pytest.mark.parametrize("page", [1, 3, 16, 24, 64, 500])
+def test_pages(page, order, fp8):
+    check(RAGGED, page, 2, 8, 128, fp8, order=order, seed=page)
+
+
+def test_odd_head():
+    check(RAGGED, 5, 2, 3, 8)
+    check(RAGGED, 5, 2, 3, 200)
+    check(RAGGED, 5, 2, 3, 112, True)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("window", [1, 16, 100, 128, 5000])
+def test_window(window, fp8):
+    check(RAGGED + [5000], 16, 2, 4, 128, fp8, window=window)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lengths", [[1], [0], [0, 0, 0], [5], [16 * 128], [100_003], [70_000, 3, 0, 20_001], [4097] * 3])
+def test_lengths(lengths, fp8):
+    check(lengths, 64, 2, 8, 128, fp8)
+    check(lengths, 64, 1, 4, 64 if fp8 else 256, fp8)
+
+
+@pytest.mark.parametrize("B", [151, 152, 153, 256, 257, 700])
+def test_many_sequences(B):
+    check([(i * 37) % 300 for i in range(B)], 16, 2, 4, 64, seed=B)
+
+
+def test_scores_of_all_sizes():
+    """Nearly one-hot and flat softmaxes, given scales, values of very different scales."""
+    for fp8 in (False, True):
+        check([700, 33], 16, 2, 4, 128, fp8, scale=0.0)
+        check([700, 33], 16, 2, 4, 128, fp8, scale=-0.05)
+        check([700, 33], 16, 2, 4, 128, fp8, q_scale=2.0 ** -30)
+    check([700, 33, 4000], 16, 2, 4, 128, True, v_spread=True)
+
+
+def test_large_scores():
+    """Scores in the thousands: the largest takes all, whatever was summed before it."""
+    D, n = 128, 1000
+    k = torch.zeros(1, 1000, 1, D, dtype=torch.bfloat16, device=DEV)
+    k[0, :, 0, 0] = torch.arange(n, device=DEV).bfloat16()  # rounded: 256 steps of 4 at the end
+    v = torch.randn(1, 1000, 1, D, device=DEV).bfloat16()
+    q = torch.zeros(1, 4, D, dtype=torch.bfloat16, device=DEV)
+    q[0, :, 0] = torch.tensor([16.0, -16.0, 1e30, 0.0], device=DEV)
+    table, lens = torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.tensor([n], dtype=torch.int32, device=DEV)
+    status = epd.new_status(DEV)
+    ws = epd.new_attention_workspace(1, 4, 1, D, DEV)
+    out, _ = epd.ep_decode_attention(q, k, v, table, lens, ws, status, softmax_scale=1.0)
+    want, _ = attend(q, k.double(), v.double(), table, lens, 1.0)
+    # scores are exact; weights other than the largest are 0 but for ties and for head 3
+    assert bool(((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -14).all())
+
+
+def test_nonfinite_stays_in_its_sequence():
+    g = gen(1)
+    k, v, _, _ = paged(4, 64, 2, 64, False, DEV, g)
+    table, lens = torch.arange(4, dtype=torch.int32, device=DEV).view(4, 1), torch.tensor([64, 50, 64, 10], dtype=torch.int32, device=DEV)
+    q = torch.randn(4, 8, 64, generator=g, device=DEV).bfloat16()
+    ws, status = epd.new_attention_workspace(4, 8, 2, 64, DEV), epd.new_status(DEV)
+    want, _ = epd.ep_decode_attention(q, k, v, table, lens, ws, status)
+    k[1, 3, 0, 5] = float("nan")
+    v[2, 7, 1, 9] = float("inf")
+    out, _ = epd.ep_decode_attention(q, k, v, table, lens, ws, status)
+    assert bool(out[1, :4].isnan().all()) and torch.equal(out[1, 4:], want[1, 4:])
+    assert bool((out[2, 4:, 9] == float("inf")).all())
+    keep = torch.ones_like(out, dtype=torch.bool)
+    keep[1, :4] = False
+    keep[2, 4:, 9] = False
+    assert torch.equal(out[keep], want[keep])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_bad_pages_and_lengths(fp8):
+    g = gen(2)
+    k, v, ks, vs = paged(6, 16, 2, 64, fp8, DEV, g)
+    table = torch.arange(6, dtype=torch.int32, device=DEV).view(2, 3)
+    q = torch.randn(2, 4, 64, generator=g, device=DEV).bfloat16()
+    ws = epd.new_attention_workspace(2, 4, 2, 64, DEV)
+
+    def run(table, lens):
+        status = epd.new_status(DEV)
+        out, _ = epd.ep_decode_attention(q, k, v, table, torch.tensor(lens, dtype=torch.int32, device=DEV), ws, status,
+                                         k_scale=ks, v_scale=vs)
+        return out, int(status)
+    full, code = run(table, [48, 48])
+    assert code == 0
+    for page in (-1, 6, 2**31 - 1):
+        bad = table.clone()
+        bad[1, 1] = page
+        out, code = run(bad, [48, 48])
+        assert code == epd.EPD_ERR_CAPACITY and torch.equal(out[0], full[0])
+        # as if the page's positions were not there
+        lens = torch.tensor([32], dtype=torch.int32, device=DEV)
+        want, _ = attend(q[1:], values(k, ks), values(v, vs), table[1:, [0, 2]], lens)
+        assert float((out[1:].double() - want).abs().max()) <= 2.0 ** -8 * float(want.abs().max()) + 2.0 ** -11
+    out, code = run(table, [48, 49])
+    assert code == epd.EPD_ERR_CAPACITY and torch.equal(out, full)
+    out, code = run(table, [48, -3])
+    assert code == epd.EPD_ERR_INVALID_ARG and torch.equal(out[0], full[0]) and bool((out[1] == 0).all())
+
+
+def test_one_workspace_for_many_shapes():
+    ws = epd.new_attention_workspace(64, 64, 8, 256, DEV)
+    for i, (lengths, KH, G, D, fp8) in enumerate([([3000] * 3, 8, 8, 128, False), ([17], 1, 1, 64, True), ([900] * 60, 2, 4, 256, False),
+                                                  ([50_000], 1, 16, 128, True), ([5] * 64, 8, 8, 80, False)]):
+        check(lengths, 16, KH, G, D, fp8, workspace=ws, seed=i)
+
+
+def test_offsets_beyond_32_bits():
+    KH, D, page = 8, 128, 64
+    pages = 36_000  # 2.36e9 elements
+    g = gen(5)
+    small_k, small_v, _, _ = paged(4, page, KH, D, False, DEV, g)
+    k = torch.empty(pages, page, KH, D, dtype=torch.bfloat16, device=DEV)
+    v = torch.empty_like(k)
+    at = torch.tensor([pages - 1, 5, pages - 2, 33_000], device=DEV)
+    k[at], v[at] = small_k, small_v
+    q = torch.randn(1, 32, D, generator=g, device=DEV).bfloat16()
+    lens = torch.tensor([250], dtype=torch.int32, device=DEV)
+    ws, status = epd.new_attention_workspace(1, 32, KH, D, DEV), epd.new_status(DEV)
+    out, _ = epd.ep_decode_attention(q, k, v, at.int().view(1, 4), lens, ws, status)
+    want, _ = epd.ep_decode_attention(q, small_k, small_v, torch.arange(4, dtype=torch.int32, device=DEV).view(1, 4), lens, ws, status)
+    assert int(status) == 0 and torch.equal(out, want)
+
+
+def test_graph_and_stream():
+    g = gen(6)
+    k, v, _, _ = paged(40, 16, 2, 128, False, DEV, g)
+    table = torch.randperm(40, generator=g, device=DEV).int().view(4, 10)
+    lens = torch.tensor([160, 3, 77, 0], dtype=torch.int32, device=DEV)
+    q = torch.randn(4, 8, 128, generator=g, device=DEV).bfloat16()
+    ws, status = epd.new_attention_workspace(4, 8, 2, 128, DEV), epd.new_status(DEV)
+
+    def step():
+        return epd.ep_decode_attention(q, k, v, table, lens, ws, status, with_lse=True)
+    want = [t.clone() for t in step()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = [t.clone() for t in step()]
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    lens += 0
+    lens.copy_(torch.tensor([5, 160, 0, 100], dtype=torch.int32, device=DEV))
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in out]
+    assert all(torch.equal(a, b) for a, b in zip(got, step())) and int(status) == 0
+
+
+def test_refusals():
+    g = gen(7)
+    k, v, ks, vs = paged(4, 16, 2, 64, True, DEV, g)
+    kb, vb = k.bfloat16(), v.bfloat16()
+    table, lens = torch.zeros(2, 2, dtype=torch.int32, device=DEV), torch.ones(2, dtype=torch.int32, device=DEV)
+    q = torch.randn(2, 4, 64, device=DEV).bfloat16()
+    ws, st = epd.new_attention_workspace(2, 4, 2, 64, DEV), epd.new_status(DEV)
+    f = epd.ep_decode_attention
+    for bad in (lambda: f(q.float(), kb, vb, table, lens, ws, st), lambda: f(q[:1], kb, vb, table, lens, ws, st),
+                lambda: f(q[:, :3], kb, vb, table, lens, ws, st), lambda: f(q[..., :32], kb, vb, table, lens, ws, st),
+                lambda: f(q, k, v, table, lens, ws, st), lambda: f(q, kb, vb, table, lens, ws, st, k_scale=ks, v_scale=vs),
+                lambda: f(q, kb, v, table, lens, ws, st), lambda: f(q, kb, vb, table, lens.long(), ws, st),
+                lambda: f(q, kb, vb, table, lens[:1], ws, st), lambda: f(q, kb, vb, table, lens, ws[:100], st),
+                lambda: f(q, kb, vb, table.long(), lens, ws, st), lambda: f(q, kb, vb, table, lens, ws, st, out=q.float()),
+                lambda: f(q, kb, vb, table, lens, ws, st, lse=ws), lambda: f(q.cpu(), kb, vb, table, lens, ws, st)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(epd.EpdError):
+        f(q, kb, vb, table, lens, ws, st, window=-1)
+    with pytest.raises(epd.EpdError):
+        f(q, kb, vb, table, lens, ws, st, softmax_scale=float("nan"))
+    with pytest.raises(epd.EpdError):
+        epd.new_attention_workspace(2, 4, 3, 64, DEV)
+    assert int(st) == 0

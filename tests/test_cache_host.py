@@ -54,3 +54,24 @@ def test_append_rejects_bad_args(lib):
         assert call(**kw) == INVALID, kw
     assert call(c=cache(D=264)) == UNSUPPORTED
     assert call(T=0, k=None, v=None, pos=None) == OK
+
+
+def test_attention_rejects_bad_args(lib):
+    ok = dict(c=cache(), q=FAKE, qs=256, QH=4, lens=FAKE, scale=0.1, window=0, ws=FAKE, out=FAKE, lse=None, st=FAKE,
+              s=None)
+    call = lambda **kw: lib.ep_decode_attention(*dict(ok, **kw).values())  # noqa: E731
+    for kw in ([dict(c=cache(**b)) for b in BAD_CACHES] + [
+            dict(c=None), dict(q=None), dict(q=ODD), dict(qs=12), dict(qs=-8), dict(QH=0), dict(QH=3), dict(lens=None),
+            dict(lens=ctypes.c_void_p(0x10002)), dict(scale=float("nan")), dict(window=-1), dict(ws=None), dict(ws=ODD),
+            dict(out=None), dict(out=ODD), dict(lse=ctypes.c_void_p(0x10002)), dict(st=None)]):
+        assert call(**kw) == INVALID, kw
+    assert call(c=cache(D=264)) == UNSUPPORTED
+    assert call(c=cache(S=0), q=None, out=None, lens=None, ws=None) == OK
+
+
+def test_attention_workspace_bytes(lib):
+    f = lib.epd_attention_workspace_bytes
+    assert f(4, 32, 8, 128) >= 152 * 4 + 152 * 2 * 16 * 130 * 4
+    assert f(4, 32, 8, 256) > f(4, 32, 8, 128) > f(4, 32, 8, 64) > 0
+    for bad in ((-1, 32, 8, 128), (4, 0, 8, 128), (4, 32, 0, 128), (4, 32, 5, 128), (4, 32, 8, 0), (4, 32, 8, 100), (4, 32, 8, 264)):
+        assert f(*bad) == 0

@@ -35,5 +35,6 @@ from ._binding import (  # noqa: F401,E402
     ep_route, ep_route_backward, ep_unpermute, ep_unpermute_backward, epd_workspace_bytes,
     epd_workspace_init, load_library, new_status, new_workspace, status_string, version,
     ep_layer_norm, ep_layer_norm_backward, epd_norm_workspace_bytes, new_norm_workspace,
-    ep_cache_append, ep_rotary, rotary_frequencies, rotary_steps,
+    ep_cache_append, ep_decode_attention, ep_rotary, epd_attention_workspace_bytes,
+    new_attention_workspace, rotary_frequencies, rotary_steps,
 )

@@ -106,6 +106,8 @@ SIGNATURES = {
     "ep_rotary": (_I, [_P, _I64, _I64, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P, _I64, _I64, _P]),
     "ep_cache_append": (_I, [_CACHE, _P, _I64, _I, _P, _I64, _P, _I64, _P, _P, _I, _P, _I, _I, _F,
                              _P, _I64, _P, _P]),
+    "epd_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
+    "ep_decode_attention": (_I, [_CACHE, _P, _I64, _I, _P, _F, _I, _P, _P, _P, _P, _P]),
     "ep_dispatch_layout_noalloc": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
     "epd_test_expert_matmul_stalled": (_I, [_ROWS, _P, _I, _P, _I64, _I64, _I64, _P, _P, _I, _I, _I,
                                             _P, _P, _I, _I64, _P]),
@@ -1161,6 +1163,57 @@ def ep_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
                  _stream(stream, dev))
     _check(rc, "ep_cache_append")
     return q_out
+
+
+def epd_attention_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int,
+                                  head_dim: int) -> int:
+    n = int(load_library().epd_attention_workspace_bytes(num_seqs, num_heads, num_kv_heads,
+                                                         head_dim))
+    if n == 0:
+        raise EpdError(EPD_ERR_INVALID_ARG, "epd_attention_workspace_bytes")
+    return n
+
+
+def new_attention_workspace(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                            device=None) -> torch.Tensor:
+    """A zero-filled workspace tensor (uint8) for ep_decode_attention on one stream."""
+    return torch.zeros(epd_attention_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim),
+                       dtype=torch.uint8, device=device or torch.device("cuda"))
+
+
+def ep_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        page_table: torch.Tensor, lengths: torch.Tensor, workspace: torch.Tensor,
+                        status: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+                        v_scale: Optional[torch.Tensor] = None,
+                        softmax_scale: Optional[float] = None, window: int = 0, out=None, lse=None,
+                        with_lse: bool = False, stream=None):
+    """Attention of one new token of every sequence, q [seqs, heads, dim] bfloat16, over the first
+    lengths[s] (int32) positions of its pages (the last `window` of them where window > 0), the
+    cache as in ep_cache_append. softmax_scale: dim ** -0.5 where None. Returns (out [seqs, heads,
+    dim] bfloat16, lse [seqs, heads] float32 or None); see epd.h."""
+    c = _cache(k_cache, v_cache, page_table, k_scale, v_scale)
+    dev = k_cache.device
+    B, KH, D = c.num_seqs, c.num_kv_heads, c.head_dim
+    qs = _token_rows(q, "q", None, D, B, dev)
+    QH = q.shape[1]
+    if QH < 1 or QH % KH:
+        raise ValueError(f"{QH} heads of q, {KH} of the cache")
+    _want(lengths, "lengths", torch.int32, (B,), dev)
+    _want(workspace, "workspace", torch.uint8, device=dev)
+    _want(status, "status", torch.int32, (1,), dev)
+    lib = load_library()
+    need = lib.epd_attention_workspace_bytes(B, QH, KH, D)  # 0: refused below
+    if workspace.numel() < need:
+        raise ValueError("workspace too small for this attention")
+    out = _out(out, "out", torch.bfloat16, (B, QH, D), dev)
+    if with_lse or lse is not None:
+        lse = _out(lse, "lse", torch.float32, (B, QH), dev)
+    scale = D ** -0.5 if softmax_scale is None else float(softmax_scale)
+    rc = _launch(lib.ep_decode_attention, dev, ctypes.byref(c), _ptr(q), qs, QH, _ptr(lengths),
+                 scale, int(window), _ptr(workspace), _ptr(out), _ptr(lse), _ptr(status),
+                 _stream(stream, dev))
+    _check(rc, "ep_decode_attention")
+    return out, lse
 
 
 def ep_dispatch_layout_noalloc(topk_idx: torch.Tensor, num_experts: int, num_ranks: int,

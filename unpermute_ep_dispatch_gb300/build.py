@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build", "libepd")
 LIB = os.path.join(PKG, "libepd.so")
 SOURCES = ["layout.cu", "scan.cu", "permute.cu", "unpermute.cu", "lowlatency.cu", "dispatch.cu", "route.cu", "route_backward.cu",
-           "experts.cu", "unpermute_backward.cu", "norm.cu", "rotary.cu"]
+           "experts.cu", "unpermute_backward.cu", "norm.cu", "rotary.cu", "attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

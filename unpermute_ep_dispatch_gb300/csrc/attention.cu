@@ -1,0 +1,695 @@
+// attention.cu -- attention of one new token over the paged key-value cache (ep_decode_attention).
+//
+//   o[b, h] = sum_t softmax_t(scale q[b, h] . k[t, h / G]) v[t, h / G],   G = heads / kv heads
+//
+// Bound by HBM: every live key and value is read once, for G heads at a time, and G <= 16 heads are
+// 16 operations a byte at most. One pass with running maxima and sums.
+//
+// Split: the (sequence, kv head, block of 16 heads) segments of the batch, each as many tiles of
+// 16 tokens a warp as its length needs, form one line of tiles, and every block takes an equal run of
+// it, whatever the lengths are (they are read on the device). A segment that lies in one block's run
+// is finished there; the parts of one that several blocks share go to the workspace, and the block
+// that comes last joins them in the blocks' order.
+//
+// A warp has its own tokens of each tile, its own ring of stages in shared memory, filled by its own
+// asynchronous copies some tiles ahead (past the ends of segments; page numbers are looked up one
+// tile before), and its own statistics, and does not wait for the other warps before the segment's
+// end. Scores and outputs are matrix products of 16 heads x 16 tokens on the warp-level matrix
+// instructions: with so few rows the 128-row tiles of tcgen05 would be nearly empty, and these take a
+// fraction of the time that the bytes take.
+//
+// Precision: products of bf16 are exact, sums in 32 bits. The weights of a bf16 cache's values are split
+// into two bf16 (15 bits at least), so that the output's own rounding is the only one that matters. An
+// e4m3 cache is widened to fp16, which holds it exactly; the query is scaled by a power of two and
+// the weights, with the values' scales in them, by the largest scale so far, to fp16's range (11
+// bits: an eighth of the output's rounding).
+#include <cuda_fp16.h>
+
+#include "cache.cuh"
+
+namespace epd {
+namespace {
+
+constexpr int kHeads = 16;      // heads of a segment: rows of the matrix instructions
+constexpr int kChunk = 16;      // tokens of a warp's tile
+constexpr int kMaxBlocks = 160; // blocks that the workspace has room for
+constexpr unsigned kAll = 0xffffffffu;
+constexpr float kLn2 = 0.6931471805599453f;
+// A maximum is moved (and everything summed so far scaled down) only when a score passes it by more
+// than 2^8: terms up to 2^8 lose nothing in 32 bits, and the scaling is rare.
+constexpr float kSlack = 8.0f;
+
+struct AttnArgs {
+    const uint8_t *q;
+    int64_t q_stride;  // bytes between tokens
+    int QH, group, blocks_of_group;  // blocks of 16 heads of a group
+    epd_cache_t kv;
+    const int32_t *lengths;
+    int window;
+    float scale_log2;
+    uint8_t *out;  // bf16 [B, QH, D]
+    float *lse;
+    uint32_t *counters;
+    float *parts;
+    int32_t *status;
+};
+
+template <int DP, bool FP8>
+struct Shape {
+    static constexpr int kRow = DP * (FP8 ? 1 : 2);         // bytes of a row in shared memory
+    static constexpr int kUnits = kRow / 16;
+    static constexpr int kTail = FP8 ? 2 * kChunk * 4 + 16 : 16;  // scales and the live tokens' mask
+    static constexpr int kStage = 2 * kChunk * kRow + kTail;
+    static constexpr int kWarps = DP == 256 && !FP8 ? 4 : 8;
+    static constexpr int kJoinCols = 32;
+    static constexpr int kJoin = kWarps * kHeads * (kJoinCols + 8) * 4;
+    static constexpr int kFit = (226 * 1024 - kJoin - 2048) / (kWarps * kStage);
+    static constexpr int kStages = kFit < 6 ? kFit : 6;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kTile = kWarps * kChunk;  // tokens of a tile
+    static constexpr int kSmem = kWarps * kStages * kStage + kJoin;
+    static_assert(kStages >= 2, "a stage is filled while another is read");
+    static_assert(kJoin >= kMaxBlocks * kHeads * 4, "the joining block keeps a weight for every part");
+};
+
+// Floats of a part: 16 rows of DP sums, their maxima and their sums of weights.
+template <int DP>
+constexpr int kPart = kHeads * (DP + 2);
+
+__device__ __forceinline__ void copy16z(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4z(uint32_t dst, const void *src, bool live) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// d += a b, 16 x 8 x 16.
+template <bool FP8>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (FP8)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two e4m3 (the low half of w) as two fp16, exactly.
+__device__ __forceinline__ uint32_t widen2(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Place of 16-byte unit u of a row in shared memory: eight rows of one unit lie in eight bank groups.
+template <int UNITS>
+__device__ __forceinline__ int swizzle(int row, int u) {
+    return UNITS % 8 == 0 ? u ^ (row & 7) : u ^ ((row >> 1) & 3);
+}
+
+// The live positions [lo, n) of a sequence and its tiles (one at least: an empty one is written too).
+struct Span {
+    int lo, n, tiles;
+};
+template <int TILE>
+__device__ __forceinline__ Span span_of(const AttnArgs &a, int len) {
+    const int64_t most = cache_positions(a.kv);
+    Span s;
+    s.n = len < 0 ? 0 : (int64_t)len > most ? (int)most : len;
+    s.lo = a.window > 0 && s.n > a.window ? s.n - a.window : 0;
+    s.tiles = s.n > 0 ? (s.n - s.lo - 1) / TILE + 1 : 1;
+    return s;
+}
+
+// A place on the line of tiles: tile `tile` of segment (b, hh).
+template <int TILE>
+struct Cursor {
+    int b, hh, tile, next_len;
+    Span span;
+    __device__ __forceinline__ void enter(const AttnArgs &a, int len) {
+        span = span_of<TILE>(a, len);
+        next_len = b + 1 < a.kv.num_seqs ? __ldg(a.lengths + b + 1) : 0;
+    }
+    __device__ __forceinline__ void advance(const AttnArgs &a, int heads) {
+        if (++tile < span.tiles) return;
+        tile = 0;
+        if (++hh < heads) return;
+        hh = 0;
+        ++b;
+        enter(a, next_len);
+    }
+};
+
+__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(kAll, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+template <int DP, bool FP8>
+__global__ void __launch_bounds__(Shape<DP, FP8>::kThreads, 1) attention_kernel(AttnArgs a) {
+    using S = Shape<DP, FP8>;
+    constexpr int W = S::kWarps, UNITS = S::kUnits, TILE = S::kTile, NT = DP / 8;
+    extern __shared__ uint4 s_dyn[];
+    __shared__ int64_t s_scan[W];
+    __shared__ int64_t s_prefix;
+    __shared__ int s_seq;
+    __shared__ float s_m[W][kHeads], s_l[W][kHeads], s_mall[kHeads], s_lall[kHeads];
+    __shared__ uint32_t s_last;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, c = lane & 3;
+    const int D = a.kv.head_dim, B = a.kv.num_seqs, heads = a.kv.num_kv_heads * a.blocks_of_group;
+    const uint32_t ring = smem_addr(s_dyn) + warp * S::kStages * S::kStage;
+    float *const s_join = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(s_dyn) + W * S::kStages * S::kStage);
+    // columns past D stay zero
+    if (D < DP) {
+        uint4 *mine = s_dyn + warp * S::kStages * S::kStage / 16;
+        for (int i = lane; i < S::kStages * S::kStage / 16; i += 32) mine[i] = make_uint4(0, 0, 0, 0);
+    }
+    pdl_wait();
+    pdl_trigger();
+
+    // ---- this block's run of the line: the sequences' tiles are summed by the whole block
+    int64_t total = 0;
+    if (B > S::kThreads) {
+        int64_t v = 0;
+        for (int b = tid; b < B; b += S::kThreads) v += span_of<TILE>(a, __ldg(a.lengths + b)).tiles;
+        v = warp_scan(v, lane);
+        if (lane == 31) s_scan[warp] = v;
+        __syncthreads();
+        for (int w = 0; w < W; ++w) total += s_scan[w];
+        __syncthreads();
+    }
+    int64_t r0 = 0, r1 = 0, before = 0, blocks = gridDim.x;  // blocks: that have a tile
+    for (int b0 = 0; b0 < B; b0 += S::kThreads) {
+        const int b = b0 + tid;
+        const int64_t v = b < B ? span_of<TILE>(a, __ldg(a.lengths + b)).tiles : 0;
+        int64_t incl = warp_scan(v, lane);
+        if (lane == 31) s_scan[warp] = incl;
+        __syncthreads();
+        int64_t sum = 0;
+        for (int w = 0; w < W; ++w) {
+            if (w < warp) incl += s_scan[w];
+            sum += s_scan[w];
+        }
+        if (b0 == 0) {
+            if (B <= S::kThreads) total = sum;
+            total *= heads;
+            if (total < blocks) blocks = total;
+            r0 = total * blockIdx.x / blocks;
+            r1 = total * (blockIdx.x + 1) / blocks;
+            if (blockIdx.x >= blocks) return;
+        }
+        incl += before;
+        if ((incl - v) * heads <= r0 && r0 < incl * heads) {
+            s_seq = b;
+            s_prefix = incl - v;
+        }
+        before += sum;
+        __syncthreads();
+        if (before * heads > r0) break;
+    }
+    const int steps = (int)(r1 - r0);
+    Cursor<TILE> ld, cp;
+    ld.b = s_seq;
+    int64_t prefix = s_prefix;  // tiles of the sequences before the compute cursor's
+    ld.enter(a, __ldg(a.lengths + ld.b));
+    {
+        const int64_t rest = r0 - prefix * heads;
+        ld.hh = (int)(rest / ld.span.tiles);
+        ld.tile = (int)(rest - (int64_t)ld.hh * ld.span.tiles);
+    }
+    cp = ld;
+    if (blockIdx.x == 0) {  // lengths that the pages do not hold
+        for (int b = tid; b < B; b += S::kThreads) {
+            const int len = __ldg(a.lengths + b);
+            if (len < 0) report(a.status, EPD_ERR_INVALID_ARG);
+            else if ((int64_t)len > cache_positions(a.kv)) report(a.status, EPD_ERR_CAPACITY);
+        }
+    }
+
+    // ---- loads: lane l looks after token l % 16 of the warp's chunk
+    int token, page, kv_head;
+    auto look_up = [&]() {
+        // (a tile may end past 2^31 - 1, where the sequence ends before)
+        const uint32_t t = (uint32_t)ld.span.lo + (uint32_t)ld.tile * TILE + warp * kChunk + (lane & 15);
+        token = t < (uint32_t)ld.span.n ? (int)t : -1;
+        kv_head = ld.hh / a.blocks_of_group;
+        page = token >= 0 ? __ldg(a.kv.page_table + ld.b * a.kv.table_stride + token / a.kv.page_size) : -1;
+    };
+    auto load = [&](int stage) {
+        const uint32_t at = ring + stage * S::kStage;
+        bool live = token >= 0;
+        if (live && (page < 0 || page >= a.kv.num_pages)) {
+            report(a.status, EPD_ERR_CAPACITY);
+            live = false;
+        }
+        const int inside = token % a.kv.page_size;
+        const int64_t off = live ? page * a.kv.page_stride + inside * a.kv.token_stride + kv_head * a.kv.head_stride : 0;
+        const uint32_t mask = __ballot_sync(kAll, live) & 0xffffu;
+        const int units = D * (FP8 ? 1 : 2) / 16;
+        if (mask) {
+#pragma unroll
+            for (int i = 0; i < kChunk * UNITS / 32; ++i) {
+                const int row = (i * 32 + lane) / UNITS, u = (i * 32 + lane) % UNITS;
+                const int64_t o = __shfl_sync(kAll, off, row) * (FP8 ? 1 : 2) + u * 16;
+                const bool has = (mask >> row) & 1;
+                const uint32_t dst = at + row * S::kRow + swizzle<UNITS>(row, u) * 16;
+                if (u < units) {
+                    copy16z(dst, static_cast<const uint8_t *>(a.kv.k) + (has ? o : 0), has);
+                    copy16z(dst + kChunk * S::kRow, static_cast<const uint8_t *>(a.kv.v) + (has ? o : 0), has);
+                }
+            }
+            if (FP8) {
+                const int64_t so = live ? page * a.kv.scale_page_stride + inside * a.kv.scale_token_stride + kv_head * a.kv.scale_head_stride : 0;
+                copy4z(at + 2 * kChunk * S::kRow + lane * 4, (lane < 16 ? a.kv.k_scale : a.kv.v_scale) + so, live);
+            }
+        }
+        if (lane == 0)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + S::kStage - 16), "r"(mask) : "memory");
+    };
+    __syncwarp();
+    look_up();
+#pragma unroll
+    for (int s = 0; s < S::kStages - 1; ++s) {
+        if (s < steps) {
+            load(s);
+            if (s + 1 < steps) {
+                ld.advance(a, heads);
+                look_up();
+            }
+        }
+        copy_commit();
+    }
+
+    // ---- the line
+    uint32_t q[DP / 16][4];
+    float o[NT][4], m[2], l[2], q_scale = 1.0f, v_ref = 0.0f;
+    const float *const scales = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(s_dyn) + warp * S::kStages * S::kStage + 2 * kChunk * S::kRow);
+    bool fresh = true;
+    int stage = 0;
+    for (int step = 0; step < steps; ++step) {
+        const int h0 = cp.hh / a.blocks_of_group * a.group + cp.hh % a.blocks_of_group * kHeads;  // first head
+        const int rows = min(kHeads, a.group - cp.hh % a.blocks_of_group * kHeads);
+        if (fresh) {
+            fresh = false;
+            const uint8_t *src = a.q + cp.b * a.q_stride + (int64_t)h0 * D * 2;
+            // Fragments of the query: rows g and g + 8, and the columns that the keys' fragments pair
+            // with them -- of a 16-byte unit of an e4m3 row a lane holds four neighbours.
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = g + (i & 1) * 8, col = k * 16 + (FP8 ? 4 * c + (i >> 1) * 2 : 2 * c + (i >> 1) * 8);
+                    q[k][i] = row < rows && col < D ? __ldg(reinterpret_cast<const uint32_t *>(src + ((int64_t)row * D + col) * 2)) : 0;
+                }
+            if (FP8) {
+                float top = 0.0f;
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(lo_bf16(q[k][i])), fabsf(hi_bf16(q[k][i]))));
+#pragma unroll
+                for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+                // to [2^6, 2^7): the power of two from the exponent's bits
+                const int e = top > 0.0f ? min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 100) : 0;
+                const float up = __uint_as_float((uint32_t)(127 + 6 - e) << 23);
+                q_scale = __uint_as_float((uint32_t)(127 - 6 + e) << 23);
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) q[k][i] = pack2_f16(lo_bf16(q[k][i]) * up, hi_bf16(q[k][i]) * up);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+            m[0] = m[1] = -INFINITY;
+            l[0] = l[1] = 0.0f;
+            v_ref = 0.0f;
+        }
+        copy_wait<S::kStages - 2>();
+        __syncwarp();
+        if (step + S::kStages - 1 < steps) {
+            load(stage == 0 ? S::kStages - 1 : stage - 1);
+            if (step + S::kStages < steps) {
+                ld.advance(a, heads);
+                look_up();
+            }
+        }
+        copy_commit();
+
+        const uint32_t at = ring + stage * S::kStage;
+        uint32_t mask;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(mask) : "r"(at + S::kStage - 16) : "memory");
+        if (mask) {
+            // scores of 16 heads and 16 tokens: s[n] has tokens 8 n + 2 c, 8 n + 2 c + 1 of rows g, g + 8
+            float s[2][4] = {};
+            if (FP8) {
+#pragma unroll
+                for (int k = 0; k < UNITS / 2; ++k) {
+                    uint32_t r[4];
+                    const int row = (lane >> 4) * 8 + (lane & 7), u = 2 * k + ((lane >> 3) & 1);
+                    ldsm4(r, at + row * S::kRow + swizzle<UNITS>(row, u) * 16);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mma<true>(s[i >> 1], q[2 * k + (i & 1)], widen2(r[i]), widen2(r[i] >> 16));
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    uint32_t r[4];
+                    const int row = (lane >> 4) * 8 + (lane & 7), u = 2 * k + ((lane >> 3) & 1);
+                    ldsm4(r, at + row * S::kRow + swizzle<UNITS>(row, u) * 16);
+                    mma<false>(s[0], q[k], r[0], r[1]);
+                    mma<false>(s[1], q[k], r[2], r[3]);
+                }
+            }
+            const float *const sc = scales + stage * (S::kStage / 4);
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = 8 * n + 2 * c + (i & 1);
+                    float x = s[n][i] * a.scale_log2;
+                    if (FP8) x = x * q_scale * sc[t];
+                    s[n][i] = (mask >> t) & 1 ? x : -INFINITY;
+                    top[i >> 1] = fmaxf(top[i >> 1], s[n][i]);
+                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 1));
+                top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 2));
+            }
+            if (__any_sync(kAll, top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float now = fmaxf(m[i], top[i]);
+                    const float f = m[i] == -INFINITY ? 0.0f : fast_exp2(m[i] - now);
+                    m[i] = now;
+                    l[i] *= f;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        o[j][2 * i] *= f;
+                        o[j][2 * i + 1] *= f;
+                    }
+                }
+            }
+            float vs[4];
+            if (FP8) {
+                // the values' scales over the largest so far (up to 16 times it without moving it)
+                float most = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    vs[i] = sc[kChunk + 8 * (i >> 1) + 2 * c + (i & 1)];
+                    most = fmaxf(most, vs[i]);
+                }
+                most = fmaxf(most, __shfl_xor_sync(kAll, most, 1));
+                most = fmaxf(most, __shfl_xor_sync(kAll, most, 2));
+                if (most > 16.0f * v_ref) {  // the same in all lanes
+                    const float f = v_ref / most;
+                    v_ref = most;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[j][i] *= f;
+                }
+                const float inv = v_ref > 0.0f ? 1.0f / v_ref : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) vs[i] *= inv;
+            }
+            const float base[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
+            uint32_t p[4], p_lo[4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float x = fast_exp2(s[n][2 * i] - base[i]), y = fast_exp2(s[n][2 * i + 1] - base[i]);
+                    l[i] += x + y;
+                    if (FP8) {
+                        p[2 * n + i] = pack2_f16(x * vs[2 * n], y * vs[2 * n + 1]);
+                    } else {
+                        // the first part is cut off, not rounded, and the second at least 2^-100: neither
+                        // turns an infinite value's product into NaN
+                        const uint32_t hi = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+                        p[2 * n + i] = hi;
+                        p_lo[2 * n + i] = pack2_bf16(fmaxf(x - lo_bf16(hi), 0x1p-100f), fmaxf(y - hi_bf16(hi), 0x1p-100f));
+                    }
+                }
+            const uint32_t av = at + kChunk * S::kRow;
+            const int row = lane & 15;
+            if (FP8) {
+                // a 16-byte unit is 16 columns: its even ones are one tile, its odd ones the next
+#pragma unroll
+                for (int j = 0; j < UNITS / 2; ++j) {
+                    uint32_t r[4];
+                    ldsm4t(r, av + row * S::kRow + swizzle<UNITS>(row, 2 * j + (lane >> 4)) * 16);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t x = __byte_perm(r[2 * h], 0, 0x3120), y = __byte_perm(r[2 * h + 1], 0, 0x3120);
+                        mma<true>(o[4 * j + 2 * h], p, widen2(x), widen2(y));
+                        mma<true>(o[4 * j + 2 * h + 1], p, widen2(x >> 16), widen2(y >> 16));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < NT / 2; ++j) {
+                    uint32_t r[4];
+                    ldsm4t(r, av + row * S::kRow + swizzle<UNITS>(row, 2 * j + (lane >> 4)) * 16);
+                    mma<false>(o[2 * j], p, r[0], r[1]);
+                    mma<false>(o[2 * j + 1], p, r[2], r[3]);
+                    mma<false>(o[2 * j], p_lo, r[0], r[1]);
+                    mma<false>(o[2 * j + 1], p_lo, r[2], r[3]);
+                }
+            }
+        }
+        if (++stage == S::kStages) stage = 0;
+
+        if (cp.tile == cp.span.tiles - 1 || step == steps - 1) {
+            // ---- the segment's end here: join the warps
+            const int64_t seg0 = prefix * heads + (int64_t)cp.hh * cp.span.tiles;  // its first tile on the line
+            const int64_t seg1 = seg0 + cp.span.tiles;
+            const bool whole = r0 <= seg0 && seg1 <= r1;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                l[i] += __shfl_xor_sync(kAll, l[i], 1);
+                l[i] += __shfl_xor_sync(kAll, l[i], 2);
+                if (c == 0) {
+                    s_m[warp][g + 8 * i] = m[i];
+                    s_l[warp][g + 8 * i] = l[i];
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w][g + 8 * i]);
+                float f = m[i] == -INFINITY ? 0.0f : fast_exp2(m[i] - top);
+                if (FP8) f *= v_ref;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    o[j][2 * i] *= f;
+                    o[j][2 * i + 1] *= f;
+                }
+            }
+            if (tid < kHeads) {
+                float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w][tid]);
+#pragma unroll
+                for (int w = 0; w < W; ++w) sum += s_m[w][tid] == -INFINITY ? 0.0f : s_l[w][tid] * fast_exp2(s_m[w][tid] - top);
+                s_mall[tid] = top;
+                s_lall[tid] = sum;
+            }
+            float *const part = a.parts + (2 * blockIdx.x + (r0 < seg0 ? 1 : 0)) * (int64_t)kPart<DP>;
+            uint8_t *const out = a.out + ((int64_t)cp.b * a.QH + h0) * D * 2;
+            constexpr int JC = S::kJoinCols, JS = JC + 8;
+#pragma unroll
+            for (int pass = 0; pass < DP / JC; ++pass) {
+                if (pass * JC < D) {
+                    float *const mine = s_join + warp * kHeads * JS;
+#pragma unroll
+                    for (int j = 0; j < JC / 8; ++j) {
+                        const float(&v)[4] = o[pass * (JC / 8) + j];
+                        if (FP8) {
+                            // tiles of a unit hold its even and odd columns
+                            const int col = (j / 2) * 16 + 4 * c + (j & 1);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) mine[(g + 8 * (i >> 1)) * JS + col + 2 * (i & 1)] = v[i];
+                        } else {
+                            *reinterpret_cast<float2 *>(mine + g * JS + j * 8 + 2 * c) = make_float2(v[0], v[1]);
+                            *reinterpret_cast<float2 *>(mine + (g + 8) * JS + j * 8 + 2 * c) = make_float2(v[2], v[3]);
+                        }
+                    }
+                    __syncthreads();
+                    for (int e = tid; e < rows * (JC / 2); e += S::kThreads) {
+                        const int r = e / (JC / 2), col = e % (JC / 2) * 2;
+                        float2 v = make_float2(0.0f, 0.0f);
+#pragma unroll
+                        for (int w = 0; w < W; ++w) {
+                            const float2 x = *reinterpret_cast<const float2 *>(s_join + (w * kHeads + r) * JS + col);
+                            v.x += x.x;
+                            v.y += x.y;
+                        }
+                        if (pass * JC + col < D) {
+                            if (whole) {
+                                const float inv = s_lall[r] > 0.0f ? __fdiv_rn(1.0f, s_lall[r]) : s_lall[r];
+                                *reinterpret_cast<uint32_t *>(out + ((int64_t)r * D + pass * JC + col) * 2) = pack2_bf16(v.x * inv, v.y * inv);
+                            } else {
+                                *reinterpret_cast<float2 *>(part + r * DP + pass * JC + col) = v;
+                            }
+                        }
+                    }
+                    __syncthreads();
+                }
+            }
+            if (tid < rows) {
+                if (whole) {
+                    if (a.lse) a.lse[(int64_t)cp.b * a.QH + h0 + tid] = s_mall[tid] == -INFINITY ? -INFINITY : (s_mall[tid] + log2f(s_lall[tid])) * kLn2;
+                } else {
+                    part[kHeads * DP + tid] = s_mall[tid];
+                    part[kHeads * DP + kHeads + tid] = s_lall[tid];
+                }
+            }
+            if (!whole) {
+                // ---- the parts of the blocks that share the segment, joined by the last of them
+                const int first = (int)(((seg0 + 1) * blocks - 1) / total), last = (int)((seg1 * blocks - 1) / total);
+                uint32_t *const counter = a.counters + first;  // a block's run has the beginning of one such segment at most
+                __threadfence();
+                __syncthreads();
+                if (tid == 0) {
+                    const uint32_t seen = atomicAdd(counter, 1u);
+                    s_last = seen == (uint32_t)(last - first);
+                    if (s_last) *counter = 0;  // as the next call finds it
+                    __threadfence();
+                }
+                __syncthreads();
+                if (s_last) {
+                    const int n = last - first + 1;
+                    auto part_of = [&](int i) {  // the segment is a block's first, or begins inside its run
+                        const int blk = first + i;
+                        return a.parts + (2 * blk + (total * blk / blocks < seg0 ? 1 : 0)) * (int64_t)kPart<DP>;
+                    };
+                    if (tid < rows) {
+                        float top = -INFINITY, sum = 0.0f;
+                        for (int i = 0; i < n; ++i) top = fmaxf(top, __ldcg(part_of(i) + kHeads * DP + tid));
+                        for (int i = 0; i < n; ++i) {
+                            const float mi = __ldcg(part_of(i) + kHeads * DP + tid);
+                            const float f = mi == -INFINITY ? 0.0f : fast_exp2(mi - top);
+                            s_join[i * kHeads + tid] = f;
+                            sum += f * __ldcg(part_of(i) + kHeads * DP + kHeads + tid);
+                        }
+                        s_lall[tid] = sum > 0.0f ? __fdiv_rn(1.0f, sum) : sum;
+                        if (a.lse) a.lse[(int64_t)cp.b * a.QH + h0 + tid] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
+                    }
+                    __syncthreads();
+                    for (int e = tid; e < rows * (D / 2); e += S::kThreads) {
+                        const int r = e / (D / 2), col = e % (D / 2) * 2;
+                        float2 v = make_float2(0.0f, 0.0f);
+                        for (int i = 0; i < n; ++i) {
+                            const float2 x = __ldcg(reinterpret_cast<const float2 *>(part_of(i) + r * DP + col));
+                            v.x = fmaf(x.x, s_join[i * kHeads + r], v.x);
+                            v.y = fmaf(x.y, s_join[i * kHeads + r], v.y);
+                        }
+                        *reinterpret_cast<uint32_t *>(out + ((int64_t)r * D + col) * 2) = pack2_bf16(v.x * s_lall[r], v.y * s_lall[r]);
+                    }
+                    __syncthreads();
+                }
+            }
+            fresh = true;
+        }
+        if (step + 1 < steps) {
+            const int b = cp.b;
+            const int tiles = cp.span.tiles;
+            cp.advance(a, heads);
+            if (cp.b != b) prefix += tiles;
+        }
+    }
+}
+
+inline int padded_dim(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+
+// The workspace: a counter for every block, zero between calls and in the same place whatever the
+// sizes are, and two parts for every block.
+constexpr size_t kCounterBytes = (kMaxBlocks * 4 + kAlign - 1) / kAlign * kAlign;
+
+template <int DP, bool FP8>
+epd_status_t launch_attention(const AttnArgs &a, cudaStream_t st) {
+    using S = Shape<DP, FP8>;
+    if (const epd_status_t rc = allow_smem<attention_kernel<DP, FP8>>(S::kSmem)) return rc;
+    const int grid = sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks;
+    return launch_pdl(attention_kernel<DP, FP8>, grid, S::kThreads, S::kSmem, st, a);
+}
+
+}  // namespace
+}  // namespace epd
+
+extern "C" size_t epd_attention_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int head_dim) {
+    using namespace epd;
+    if (num_seqs < 0 || num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads || head_dim < 8 ||
+        head_dim % 8 || head_dim > kMaxHeadDim)
+        return 0;
+    return kCounterBytes + (size_t)2 * kMaxBlocks * kHeads * (padded_dim(head_dim) + 2) * 4;
+}
+
+extern "C" epd_status_t ep_decode_attention(const epd_cache_t *cache, const void *q, int64_t q_token_stride,
+                                            int num_heads, const int32_t *lengths, float softmax_scale, int window,
+                                            void *workspace, void *out, float *lse, int32_t *status,
+                                            epd_stream_t stream) {
+    using namespace epd;
+    if (const epd_status_t rc = check_cache(cache)) return rc;
+    const int B = cache->num_seqs, KH = cache->num_kv_heads, D = cache->head_dim;
+    if (num_heads < 1 || num_heads % KH != 0 || window < 0 || q_token_stride < 0 || q_token_stride % 8 != 0 ||
+        softmax_scale != softmax_scale)
+        return EPD_ERR_INVALID_ARG;
+    if (!status || !aligned4(status)) return EPD_ERR_INVALID_ARG;
+    if (B == 0) return EPD_OK;
+    if (!q || !out || !lengths || !workspace || !aligned16(q) || !aligned16(out) || !aligned4(lengths) ||
+        !aligned4(lse) || !aligned16(workspace))
+        return EPD_ERR_INVALID_ARG;
+    AttnArgs a;
+    a.q = static_cast<const uint8_t *>(q);
+    a.q_stride = 2 * q_token_stride;
+    a.QH = num_heads;
+    a.group = num_heads / KH;
+    a.blocks_of_group = (a.group + kHeads - 1) / kHeads;
+    if ((int64_t)KH * a.blocks_of_group * B > INT32_MAX) return EPD_ERR_UNSUPPORTED;
+    a.kv = *cache;
+    a.lengths = lengths;
+    a.window = window;
+    a.scale_log2 = softmax_scale * kLog2e;
+    a.out = static_cast<uint8_t *>(out);
+    a.lse = lse;
+    a.counters = static_cast<uint32_t *>(workspace);
+    a.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kCounterBytes);
+    a.status = status;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int DP = padded_dim(D);
+    if (cache->dtype == EPD_FP8_E4M3)
+        return DP == 64    ? launch_attention<64, true>(a, st)
+               : DP == 128 ? launch_attention<128, true>(a, st)
+                           : launch_attention<256, true>(a, st);
+    return DP == 64    ? launch_attention<64, false>(a, st)
+           : DP == 128 ? launch_attention<128, false>(a, st)
+                       : launch_attention<256, false>(a, st);
+}
