@@ -14,9 +14,10 @@
 // A warp has its own tokens of each tile, its own ring of stages in shared memory, filled by its own
 // asynchronous copies some tiles ahead (past the ends of segments; page numbers are looked up one
 // tile before), and its own statistics, and does not wait for the other warps before the segment's
-// end. Scores and outputs are matrix products of 16 heads x 16 tokens on the warp-level matrix
-// instructions: with so few rows the 128-row tiles of tcgen05 would be nearly empty, and these take a
-// fraction of the time that the bytes take.
+// end. Scores and outputs are products on the warp-level matrix instructions with the tokens (of
+// scores) and the columns (of outputs) as their 16 rows and 8 heads as their columns, so that a group
+// of 8 heads fills them; with so few heads the 128-row tiles of tcgen05 would be nearly empty, and
+// these take a fraction of the time that the bytes take.
 //
 // Precision: products of bf16 are exact, sums in 32 bits. The weights of a bf16 cache's values are split
 // into two bf16 (15 bits at least), so that the output's own rounding is the only one that matters. An
@@ -30,20 +31,31 @@
 namespace epd {
 namespace {
 
-constexpr int kHeads = 16;      // heads of a segment: rows of the matrix instructions
-constexpr int kChunk = 16;      // tokens of a warp's tile
-constexpr int kMaxBlocks = 160; // blocks that the workspace has room for
+constexpr int kMaxBlocks = 160;  // blocks that the workspace has room for
+constexpr int kMaxHeads = 16;    // heads of a segment, at most
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLn2 = 0.6931471805599453f;
 // A maximum is moved (and everything summed so far scaled down) only when a score passes it by more
 // than 2^8: terms up to 2^8 lose nothing in 32 bits, and the scaling is rare.
 constexpr float kSlack = 8.0f;
 
+// t / d for t < 2^31 by a product: mul = ceil(2^(31 + shift) / d), 2^shift >= d.
+struct Divisor {
+    uint32_t mul, shift, d;
+};
+inline Divisor divisor(uint32_t d) {
+    uint32_t s = 0;
+    while ((1ull << s) < d) ++s;
+    return {(uint32_t)(((1ull << (31 + s)) + d - 1) / d), s, d};
+}
+__device__ __forceinline__ uint32_t divide(uint32_t t, const Divisor &v) { return __umulhi(2 * t, v.mul) >> v.shift; }
+
 struct AttnArgs {
     const uint8_t *q;
     int64_t q_stride;  // bytes between tokens
-    int QH, group, blocks_of_group;  // blocks of 16 heads of a group
+    int QH, group, blocks_of_group;  // segments of a group
     epd_cache_t kv;
+    Divisor page;
     const int32_t *lengths;
     int window;
     float scale_log2;
@@ -54,27 +66,26 @@ struct AttnArgs {
     int32_t *status;
 };
 
-template <int DP, bool FP8>
+template <int DP, bool FP8, int NH>
 struct Shape {
+    static constexpr int kHeads = 8 * NH;                   // of a segment
     static constexpr int kRow = DP * (FP8 ? 1 : 2);         // bytes of a row in shared memory
     static constexpr int kUnits = kRow / 16;
-    static constexpr int kTail = FP8 ? 2 * kChunk * 4 + 16 : 16;  // scales and the live tokens' mask
+    static constexpr int kChunk = kRow <= 128 ? 32 : 16;    // tokens of a warp's tile
+    static constexpr int kTail = (FP8 ? 2 * kChunk * 4 : 0) + 16;  // scales and the live tokens' mask
     static constexpr int kStage = 2 * kChunk * kRow + kTail;
-    static constexpr int kWarps = DP == 256 && !FP8 ? 4 : 8;
-    static constexpr int kJoinCols = 32;
-    static constexpr int kJoin = kWarps * kHeads * (kJoinCols + 8) * 4;
+    static constexpr int kWarps = kRow == 512 ? 4 : 8;
+    static constexpr int kJoinCols = NH == 1 ? 64 : 32, kJoinRow = kJoinCols + 4;
+    static constexpr int kJoinSums = kWarps * kHeads * kJoinRow * 4, kJoinWeights = kMaxBlocks * kHeads * 4;
+    static constexpr int kJoin = kJoinSums > kJoinWeights ? kJoinSums : kJoinWeights;
     static constexpr int kFit = (226 * 1024 - kJoin - 2048) / (kWarps * kStage);
     static constexpr int kStages = kFit < 6 ? kFit : 6;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kTile = kWarps * kChunk;  // tokens of a tile
     static constexpr int kSmem = kWarps * kStages * kStage + kJoin;
+    static constexpr int kPart = kHeads * (DP + 2);  // floats: the heads' sums, maxima and sums of weights
     static_assert(kStages >= 2, "a stage is filled while another is read");
-    static_assert(kJoin >= kMaxBlocks * kHeads * 4, "the joining block keeps a weight for every part");
 };
-
-// Floats of a part: 16 rows of DP sums, their maxima and their sums of weights.
-template <int DP>
-constexpr int kPart = kHeads * (DP + 2);
 
 __device__ __forceinline__ void copy16z(uint32_t dst, const void *src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
@@ -139,20 +150,22 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, int len) {
     return s;
 }
 
-// A place on the line of tiles: tile `tile` of segment (b, hh).
+// A place on the line of tiles: tile `tile` of segment (b, h, block).
 template <int TILE>
 struct Cursor {
-    int b, hh, tile, next_len;
+    int b, h, block, tile, next_len;
     Span span;
     __device__ __forceinline__ void enter(const AttnArgs &a, int len) {
         span = span_of<TILE>(a, len);
         next_len = b + 1 < a.kv.num_seqs ? __ldg(a.lengths + b + 1) : 0;
     }
-    __device__ __forceinline__ void advance(const AttnArgs &a, int heads) {
+    __device__ __forceinline__ void advance(const AttnArgs &a) {
         if (++tile < span.tiles) return;
         tile = 0;
-        if (++hh < heads) return;
-        hh = 0;
+        if (++block < a.blocks_of_group) return;
+        block = 0;
+        if (++h < a.kv.num_kv_heads) return;
+        h = 0;
         ++b;
         enter(a, next_len);
     }
@@ -167,15 +180,23 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
     return v;
 }
 
-template <int DP, bool FP8>
-__global__ void __launch_bounds__(Shape<DP, FP8>::kThreads, 1) attention_kernel(AttnArgs a) {
-    using S = Shape<DP, FP8>;
-    constexpr int W = S::kWarps, UNITS = S::kUnits, TILE = S::kTile, NT = DP / 8;
+// The 8 x 8 matrix of 16-bit values with its rows and columns exchanged.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+template <int DP, bool FP8, int NH>
+__global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_kernel(AttnArgs a) {
+    using S = Shape<DP, FP8, NH>;
+    constexpr int W = S::kWarps, UNITS = S::kUnits, TILE = S::kTile, CH = S::kChunk, MT = CH / 16, KT = DP / 16;
+    constexpr int HB = S::kHeads;
     extern __shared__ uint4 s_dyn[];
     __shared__ int64_t s_scan[W];
     __shared__ int64_t s_prefix;
     __shared__ int s_seq;
-    __shared__ float s_m[W][kHeads], s_l[W][kHeads], s_mall[kHeads], s_lall[kHeads];
+    __shared__ float s_m[W][HB], s_l[W][HB], s_mall[HB], s_lall[HB];
     __shared__ uint32_t s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
@@ -237,8 +258,10 @@ __global__ void __launch_bounds__(Shape<DP, FP8>::kThreads, 1) attention_kernel(
     ld.enter(a, __ldg(a.lengths + ld.b));
     {
         const int64_t rest = r0 - prefix * heads;
-        ld.hh = (int)(rest / ld.span.tiles);
-        ld.tile = (int)(rest - (int64_t)ld.hh * ld.span.tiles);
+        const int hh = (int)(rest / ld.span.tiles);
+        ld.tile = (int)(rest - (int64_t)hh * ld.span.tiles);
+        ld.h = hh / a.blocks_of_group;
+        ld.block = hh - ld.h * a.blocks_of_group;
     }
     cp = ld;
     if (blockIdx.x == 0) {  // lengths that the pages do not hold
@@ -249,15 +272,16 @@ __global__ void __launch_bounds__(Shape<DP, FP8>::kThreads, 1) attention_kernel(
         }
     }
 
-    // ---- loads: lane l looks after token l % 16 of the warp's chunk
+    // ---- loads: lane l looks after token l % CH of the warp's chunk
     int token, page, kv_head;
     auto look_up = [&]() {
         // (a tile may end past 2^31 - 1, where the sequence ends before)
-        const uint32_t t = (uint32_t)ld.span.lo + (uint32_t)ld.tile * TILE + warp * kChunk + (lane & 15);
+        const uint32_t t = (uint32_t)ld.span.lo + (uint32_t)ld.tile * TILE + warp * CH + (lane & (CH - 1));
         token = t < (uint32_t)ld.span.n ? (int)t : -1;
-        kv_head = ld.hh / a.blocks_of_group;
-        page = token >= 0 ? __ldg(a.kv.page_table + ld.b * a.kv.table_stride + token / a.kv.page_size) : -1;
+        kv_head = ld.h;
+        page = token >= 0 ? __ldg(a.kv.page_table + ld.b * a.kv.table_stride + divide(t, a.page)) : -1;
     };
+    const int units = D * (FP8 ? 1 : 2) / 16;
     auto load = [&](int stage) {
         const uint32_t at = ring + stage * S::kStage;
         bool live = token >= 0;
@@ -265,25 +289,26 @@ __global__ void __launch_bounds__(Shape<DP, FP8>::kThreads, 1) attention_kernel(
             report(a.status, EPD_ERR_CAPACITY);
             live = false;
         }
-        const int inside = token % a.kv.page_size;
-        const int64_t off = live ? page * a.kv.page_stride + inside * a.kv.token_stride + kv_head * a.kv.head_stride : 0;
-        const uint32_t mask = __ballot_sync(kAll, live) & 0xffffu;
-        const int units = D * (FP8 ? 1 : 2) / 16;
+        const int inside = live ? token - (int)(divide(token, a.page) * a.page.d) : 0;
+        const int64_t off = live ? (page * a.kv.page_stride + inside * a.kv.token_stride + kv_head * a.kv.head_stride) * (FP8 ? 1 : 2) : 0;
+        const uint32_t mask = __ballot_sync(kAll, live) & (CH == 32 ? kAll : 0xffffu);
         if (mask) {
 #pragma unroll
-            for (int i = 0; i < kChunk * UNITS / 32; ++i) {
+            for (int i = 0; i < CH * UNITS / 32; ++i) {
                 const int row = (i * 32 + lane) / UNITS, u = (i * 32 + lane) % UNITS;
-                const int64_t o = __shfl_sync(kAll, off, row) * (FP8 ? 1 : 2) + u * 16;
+                const int64_t o = __shfl_sync(kAll, off, row) + u * 16;
                 const bool has = (mask >> row) & 1;
                 const uint32_t dst = at + row * S::kRow + swizzle<UNITS>(row, u) * 16;
-                if (u < units) {
+                if (u < units) {  // a dead row's copy reads nothing and writes zeros
                     copy16z(dst, static_cast<const uint8_t *>(a.kv.k) + (has ? o : 0), has);
-                    copy16z(dst + kChunk * S::kRow, static_cast<const uint8_t *>(a.kv.v) + (has ? o : 0), has);
+                    copy16z(dst + CH * S::kRow, static_cast<const uint8_t *>(a.kv.v) + (has ? o : 0), has);
                 }
             }
             if (FP8) {
                 const int64_t so = live ? page * a.kv.scale_page_stride + inside * a.kv.scale_token_stride + kv_head * a.kv.scale_head_stride : 0;
-                copy4z(at + 2 * kChunk * S::kRow + lane * 4, (lane < 16 ? a.kv.k_scale : a.kv.v_scale) + so, live);
+                const uint32_t dst = at + 2 * CH * S::kRow + (lane & (CH - 1)) * 4;
+                if (CH == 32 || lane < 16) copy4z(dst, a.kv.k_scale + so, live);
+                if (CH == 32 || lane >= 16) copy4z(dst + CH * 4, a.kv.v_scale + so, live);
             }
         }
         if (lane == 0)
@@ -296,40 +321,42 @@ __global__ void __launch_bounds__(Shape<DP, FP8>::kThreads, 1) attention_kernel(
         if (s < steps) {
             load(s);
             if (s + 1 < steps) {
-                ld.advance(a, heads);
+                ld.advance(a);
                 look_up();
             }
         }
         copy_commit();
     }
 
-    // ---- the line
-    uint32_t q[DP / 16][4];
-    float o[NT][4], m[2], l[2], q_scale = 1.0f, v_ref = 0.0f;
-    const float *const scales = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(s_dyn) + warp * S::kStages * S::kStage + 2 * kChunk * S::kRow);
+    // ---- the line. o[k][n][i]: column 16 k + g + 8 (i / 2) (e4m3: 16 k + 2 g + i / 2) of head
+    // 8 n + 2 c + i % 2; m and l: of heads 8 n + 2 c, 8 n + 2 c + 1, l of the lane's own tokens
+    uint32_t q[KT][NH][2];
+    float o[KT][NH][4], m[NH][2], l[NH][2], q_scale = 1.0f, v_ref = 0.0f, v_inv = 0.0f;
+    const float *const scales = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(s_dyn) + warp * S::kStages * S::kStage + 2 * CH * S::kRow);
     bool fresh = true;
     int stage = 0;
     for (int step = 0; step < steps; ++step) {
-        const int h0 = cp.hh / a.blocks_of_group * a.group + cp.hh % a.blocks_of_group * kHeads;  // first head
-        const int rows = min(kHeads, a.group - cp.hh % a.blocks_of_group * kHeads);
         if (fresh) {
             fresh = false;
-            const uint8_t *src = a.q + cp.b * a.q_stride + (int64_t)h0 * D * 2;
-            // Fragments of the query: rows g and g + 8, and the columns that the keys' fragments pair
-            // with them -- of a 16-byte unit of an e4m3 row a lane holds four neighbours.
+            const int rows = a.group - cp.block * HB;  // heads of the segment, if fewer than HB
+            const uint8_t *src = a.q + cp.b * a.q_stride + (int64_t)(cp.h * a.group + cp.block * HB) * D * 2;
+            // Fragments of the query: head g, and the columns that the keys' fragments pair with
+            // them -- of a 16-byte unit of an e4m3 row a lane holds four neighbours.
 #pragma unroll
-            for (int k = 0; k < DP / 16; ++k)
+            for (int k = 0; k < KT; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = g + (i & 1) * 8, col = k * 16 + (FP8 ? 4 * c + (i >> 1) * 2 : 2 * c + (i >> 1) * 8);
-                    q[k][i] = row < rows && col < D ? __ldg(reinterpret_cast<const uint32_t *>(src + ((int64_t)row * D + col) * 2)) : 0;
-                }
+                for (int n = 0; n < NH; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int row = n * 8 + g, col = k * 16 + (FP8 ? 4 * c + i * 2 : 2 * c + i * 8);
+                        q[k][n][i] = row < rows && col < D ? __ldg(reinterpret_cast<const uint32_t *>(src + ((int64_t)row * D + col) * 2)) : 0;
+                    }
             if (FP8) {
                 float top = 0.0f;
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
+                for (int k = 0; k < KT; ++k)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(lo_bf16(q[k][i])), fabsf(hi_bf16(q[k][i]))));
+                    for (int i = 0; i < 2 * NH; ++i) top = fmaxf(top, fmaxf(fabsf(lo_bf16(q[k][i >> 1][i & 1])), fabsf(hi_bf16(q[k][i >> 1][i & 1]))));
 #pragma unroll
                 for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
                 // to [2^6, 2^7): the power of two from the exponent's bits
@@ -337,22 +364,27 @@ __global__ void __launch_bounds__(Shape<DP, FP8>::kThreads, 1) attention_kernel(
                 const float up = __uint_as_float((uint32_t)(127 + 6 - e) << 23);
                 q_scale = __uint_as_float((uint32_t)(127 - 6 + e) << 23);
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
+                for (int k = 0; k < KT; ++k)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) q[k][i] = pack2_f16(lo_bf16(q[k][i]) * up, hi_bf16(q[k][i]) * up);
+                    for (int n = 0; n < NH; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) q[k][n][i] = pack2_f16(lo_bf16(q[k][n][i]) * up, hi_bf16(q[k][n][i]) * up);
             }
 #pragma unroll
-            for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-            m[0] = m[1] = -INFINITY;
-            l[0] = l[1] = 0.0f;
-            v_ref = 0.0f;
+            for (int n = 0; n < NH; ++n) {
+#pragma unroll
+                for (int k = 0; k < KT; ++k) o[k][n][0] = o[k][n][1] = o[k][n][2] = o[k][n][3] = 0.0f;
+                m[n][0] = m[n][1] = -INFINITY;
+                l[n][0] = l[n][1] = 0.0f;
+            }
+            v_ref = v_inv = 0.0f;
         }
         copy_wait<S::kStages - 2>();
         __syncwarp();
         if (step + S::kStages - 1 < steps) {
             load(stage == 0 ? S::kStages - 1 : stage - 1);
             if (step + S::kStages < steps) {
-                ld.advance(a, heads);
+                ld.advance(a);
                 look_up();
             }
         }
@@ -362,123 +394,162 @@ __global__ void __launch_bounds__(Shape<DP, FP8>::kThreads, 1) attention_kernel(
         uint32_t mask;
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(mask) : "r"(at + S::kStage - 16) : "memory");
         if (mask) {
-            // scores of 16 heads and 16 tokens: s[n] has tokens 8 n + 2 c, 8 n + 2 c + 1 of rows g, g + 8
-            float s[2][4] = {};
-            if (FP8) {
+            // s[t][n][i]: token 16 t + g + 8 (i / 2), head 8 n + 2 c + i % 2
+            float s[MT][NH][4] = {};
+            const int row = lane & 15, right = lane >> 4;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
 #pragma unroll
                 for (int k = 0; k < UNITS / 2; ++k) {
                     uint32_t r[4];
-                    const int row = (lane >> 4) * 8 + (lane & 7), u = 2 * k + ((lane >> 3) & 1);
-                    ldsm4(r, at + row * S::kRow + swizzle<UNITS>(row, u) * 16);
+                    ldsm4(r, at + (t * 16 + row) * S::kRow + swizzle<UNITS>(row, 2 * k + right) * 16);
+                    if (FP8) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) mma<true>(s[i >> 1], q[2 * k + (i & 1)], widen2(r[i]), widen2(r[i] >> 16));
-                }
-            } else {
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t f[4] = {widen2(r[2 * h]), widen2(r[2 * h + 1]), widen2(r[2 * h] >> 16), widen2(r[2 * h + 1] >> 16)};
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k) {
-                    uint32_t r[4];
-                    const int row = (lane >> 4) * 8 + (lane & 7), u = 2 * k + ((lane >> 3) & 1);
-                    ldsm4(r, at + row * S::kRow + swizzle<UNITS>(row, u) * 16);
-                    mma<false>(s[0], q[k], r[0], r[1]);
-                    mma<false>(s[1], q[k], r[2], r[3]);
+                            for (int n = 0; n < NH; ++n) mma<true>(s[t][n], f, q[2 * k + h][n][0], q[2 * k + h][n][1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < NH; ++n) mma<false>(s[t][n], r, q[k][n][0], q[k][n][1]);
+                    }
                 }
             }
             const float *const sc = scales + stage * (S::kStage / 4);
-            float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = 8 * n + 2 * c + (i & 1);
-                    float x = s[n][i] * a.scale_log2;
-                    if (FP8) x = x * q_scale * sc[t];
-                    s[n][i] = (mask >> t) & 1 ? x : -INFINITY;
-                    top[i >> 1] = fmaxf(top[i >> 1], s[n][i]);
+            for (int t = 0; t < MT; ++t) {
+                float f[2] = {a.scale_log2, a.scale_log2};
+                if (FP8) {
+                    f[0] = f[0] * q_scale * sc[16 * t + g];
+                    f[1] = f[1] * q_scale * sc[16 * t + g + 8];
                 }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 1));
-                top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 2));
+                for (int n = 0; n < NH; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s[t][n][i] *= f[i >> 1];
             }
-            if (__any_sync(kAll, top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
+            if (mask != (CH == 32 ? kAll : 0xffffu)) {
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int n = 0; n < NH; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!((mask >> (16 * t + g + 8 * (i >> 1))) & 1)) s[t][n][i] = -INFINITY;
+            }
+            float top[NH][2];
+            bool more = false;
+#pragma unroll
+            for (int n = 0; n < NH; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float now = fmaxf(m[i], top[i]);
-                    const float f = m[i] == -INFINITY ? 0.0f : fast_exp2(m[i] - now);
-                    m[i] = now;
-                    l[i] *= f;
+                    top[n][i] = fmaxf(s[0][n][i], s[0][n][i + 2]);
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        o[j][2 * i] *= f;
-                        o[j][2 * i + 1] *= f;
-                    }
+                    for (int t = 1; t < MT; ++t) top[n][i] = fmaxf(top[n][i], fmaxf(s[t][n][i], s[t][n][i + 2]));
+                    more |= top[n][i] > m[n][i] + kSlack;
                 }
+            if (__any_sync(kAll, more)) {
+#pragma unroll
+                for (int n = 0; n < NH; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float now = top[n][i];
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) now = fmaxf(now, __shfl_xor_sync(kAll, now, d));
+                        now = fmaxf(now, m[n][i]);
+                        const float f = m[n][i] == -INFINITY ? 0.0f : fast_exp2(m[n][i] - now);
+                        m[n][i] = now;
+                        l[n][i] *= f;
+#pragma unroll
+                        for (int k = 0; k < KT; ++k) {
+                            o[k][n][i] *= f;
+                            o[k][n][i + 2] *= f;
+                        }
+                    }
             }
-            float vs[4];
+            float vs[MT][2];
             if (FP8) {
                 // the values' scales over the largest so far (up to 16 times it without moving it)
-                float most = 0.0f;
+                bool larger = false;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    vs[i] = sc[kChunk + 8 * (i >> 1) + 2 * c + (i & 1)];
-                    most = fmaxf(most, vs[i]);
-                }
-                most = fmaxf(most, __shfl_xor_sync(kAll, most, 1));
-                most = fmaxf(most, __shfl_xor_sync(kAll, most, 2));
-                if (most > 16.0f * v_ref) {  // the same in all lanes
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        vs[t][i] = sc[CH + 16 * t + g + 8 * i];
+                        larger |= vs[t][i] > 16.0f * v_ref;
+                    }
+                if (__any_sync(kAll, larger)) {
+                    float most = 0.0f;
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) most = fmaxf(most, fmaxf(vs[t][0], vs[t][1]));
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, d));
                     const float f = v_ref / most;
                     v_ref = most;
+                    v_inv = 1.0f / most;
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
+                    for (int k = 0; k < KT; ++k)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) o[j][i] *= f;
+                        for (int i = 0; i < 4 * NH; ++i) o[k][i >> 2][i & 3] *= f;
                 }
-                const float inv = v_ref > 0.0f ? 1.0f / v_ref : 0.0f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) vs[i] *= inv;
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) vs[t][i] *= v_inv;
             }
-            const float base[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
-            uint32_t p[4], p_lo[4];
+            // the weights, turned from (token, head) to (head, token) fragments
+            uint32_t p[MT][NH][2], p_lo[MT][NH][2];
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < NH; ++n) {
+                const float base[2] = {m[n][0] == -INFINITY ? 0.0f : m[n][0], m[n][1] == -INFINITY ? 0.0f : m[n][1]};
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float x = fast_exp2(s[n][2 * i] - base[i]), y = fast_exp2(s[n][2 * i + 1] - base[i]);
-                    l[i] += x + y;
-                    if (FP8) {
-                        p[2 * n + i] = pack2_f16(x * vs[2 * n], y * vs[2 * n + 1]);
-                    } else {
-                        // the first part is cut off, not rounded, and the second at least 2^-100: neither
-                        // turns an infinite value's product into NaN
-                        const uint32_t hi = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-                        p[2 * n + i] = hi;
-                        p_lo[2 * n + i] = pack2_bf16(fmaxf(x - lo_bf16(hi), 0x1p-100f), fmaxf(y - hi_bf16(hi), 0x1p-100f));
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float x = fast_exp2(s[t][n][2 * i] - base[0]), y = fast_exp2(s[t][n][2 * i + 1] - base[1]);
+                        l[n][0] += x;
+                        l[n][1] += y;
+                        if (FP8) {
+                            p[t][n][i] = transpose8(pack2_f16(x * vs[t][i], y * vs[t][i]));
+                        } else {
+                            // the first part is cut off, not rounded, and the second at least 2^-100:
+                            // neither turns an infinite value's product into NaN
+                            const uint32_t hi = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+                            p[t][n][i] = transpose8(hi);
+                            p_lo[t][n][i] = transpose8(pack2_bf16(fmaxf(x - lo_bf16(hi), 0x1p-100f), fmaxf(y - hi_bf16(hi), 0x1p-100f)));
+                        }
                     }
-                }
-            const uint32_t av = at + kChunk * S::kRow;
-            const int row = lane & 15;
-            if (FP8) {
-                // a 16-byte unit is 16 columns: its even ones are one tile, its odd ones the next
+            }
+            const uint32_t av = at + CH * S::kRow;
 #pragma unroll
-                for (int j = 0; j < UNITS / 2; ++j) {
-                    uint32_t r[4];
-                    ldsm4t(r, av + row * S::kRow + swizzle<UNITS>(row, 2 * j + (lane >> 4)) * 16);
+            for (int t = 0; t < MT; ++t) {
+                if (FP8) {
+                    // a 16-byte unit is 16 columns: its even ones are the first 8 rows, its odd ones the others
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t x = __byte_perm(r[2 * h], 0, 0x3120), y = __byte_perm(r[2 * h + 1], 0, 0x3120);
-                        mma<true>(o[4 * j + 2 * h], p, widen2(x), widen2(y));
-                        mma<true>(o[4 * j + 2 * h + 1], p, widen2(x >> 16), widen2(y >> 16));
+                    for (int k = 0; k < UNITS / 2; ++k) {
+                        uint32_t r[4];
+                        ldsm4t(r, av + (t * 16 + row) * S::kRow + swizzle<UNITS>(row, 2 * k + right) * 16);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t x = __byte_perm(r[2 * h], 0, 0x3120), y = __byte_perm(r[2 * h + 1], 0, 0x3120);
+                            const uint32_t f[4] = {widen2(x), widen2(x >> 16), widen2(y), widen2(y >> 16)};
+#pragma unroll
+                            for (int n = 0; n < NH; ++n) mma<true>(o[2 * k + h][n], f, p[t][n][0], p[t][n][1]);
+                        }
                     }
-                }
-            } else {
+                } else {
+                    const int vrow = (lane & 7) + right * 8;
 #pragma unroll
-                for (int j = 0; j < NT / 2; ++j) {
-                    uint32_t r[4];
-                    ldsm4t(r, av + row * S::kRow + swizzle<UNITS>(row, 2 * j + (lane >> 4)) * 16);
-                    mma<false>(o[2 * j], p, r[0], r[1]);
-                    mma<false>(o[2 * j + 1], p, r[2], r[3]);
-                    mma<false>(o[2 * j], p_lo, r[0], r[1]);
-                    mma<false>(o[2 * j + 1], p_lo, r[2], r[3]);
+                    for (int k = 0; k < KT; ++k) {
+                        uint32_t r[4];
+                        ldsm4t(r, av + (t * 16 + vrow) * S::kRow + swizzle<UNITS>(vrow, 2 * k + ((lane >> 3) & 1)) * 16);
+#pragma unroll
+                        for (int n = 0; n < NH; ++n) {
+                            mma<false>(o[k][n], r, p[t][n][0], p[t][n][1]);
+                            mma<false>(o[k][n], r, p_lo[t][n][0], p_lo[t][n][1]);
+                        }
+                    }
                 }
             }
         }
@@ -486,33 +557,38 @@ __global__ void __launch_bounds__(Shape<DP, FP8>::kThreads, 1) attention_kernel(
 
         if (cp.tile == cp.span.tiles - 1 || step == steps - 1) {
             // ---- the segment's end here: join the warps
-            const int64_t seg0 = prefix * heads + (int64_t)cp.hh * cp.span.tiles;  // its first tile on the line
+            const int h0 = cp.h * a.group + cp.block * HB, rows = min(HB, a.group - cp.block * HB);
+            const int64_t seg0 = prefix * heads + (int64_t)(cp.h * a.blocks_of_group + cp.block) * cp.span.tiles;  // its first tile on the line
             const int64_t seg1 = seg0 + cp.span.tiles;
             const bool whole = r0 <= seg0 && seg1 <= r1;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                l[i] += __shfl_xor_sync(kAll, l[i], 1);
-                l[i] += __shfl_xor_sync(kAll, l[i], 2);
-                if (c == 0) {
-                    s_m[warp][g + 8 * i] = m[i];
-                    s_l[warp][g + 8 * i] = l[i];
+            for (int n = 0; n < NH; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) l[n][i] += __shfl_xor_sync(kAll, l[n][i], d);
+                    if (g == 0) {
+                        s_m[warp][n * 8 + 2 * c + i] = m[n][i];
+                        s_l[warp][n * 8 + 2 * c + i] = l[n][i];
+                    }
                 }
-            }
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float top = -INFINITY;
+            for (int n = 0; n < NH; ++n)
 #pragma unroll
-                for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w][g + 8 * i]);
-                float f = m[i] == -INFINITY ? 0.0f : fast_exp2(m[i] - top);
-                if (FP8) f *= v_ref;
+                for (int i = 0; i < 2; ++i) {
+                    float top = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    o[j][2 * i] *= f;
-                    o[j][2 * i + 1] *= f;
+                    for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w][n * 8 + 2 * c + i]);
+                    float f = m[n][i] == -INFINITY ? 0.0f : fast_exp2(m[n][i] - top);
+                    if (FP8) f *= v_ref;
+#pragma unroll
+                    for (int k = 0; k < KT; ++k) {
+                        o[k][n][i] *= f;
+                        o[k][n][i + 2] *= f;
+                    }
                 }
-            }
-            if (tid < kHeads) {
+            if (tid < HB) {
                 float top = -INFINITY, sum = 0.0f;
 #pragma unroll
                 for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w][tid]);
@@ -521,33 +597,27 @@ __global__ void __launch_bounds__(Shape<DP, FP8>::kThreads, 1) attention_kernel(
                 s_mall[tid] = top;
                 s_lall[tid] = sum;
             }
-            float *const part = a.parts + (2 * blockIdx.x + (r0 < seg0 ? 1 : 0)) * (int64_t)kPart<DP>;
+            float *const part = a.parts + (2 * blockIdx.x + (r0 < seg0 ? 1 : 0)) * (int64_t)S::kPart;
             uint8_t *const out = a.out + ((int64_t)cp.b * a.QH + h0) * D * 2;
-            constexpr int JC = S::kJoinCols, JS = JC + 8;
+            constexpr int JC = S::kJoinCols, JR = S::kJoinRow;
 #pragma unroll
             for (int pass = 0; pass < DP / JC; ++pass) {
                 if (pass * JC < D) {
-                    float *const mine = s_join + warp * kHeads * JS;
+                    float *const mine = s_join + warp * HB * JR;
 #pragma unroll
-                    for (int j = 0; j < JC / 8; ++j) {
-                        const float(&v)[4] = o[pass * (JC / 8) + j];
-                        if (FP8) {
-                            // tiles of a unit hold its even and odd columns
-                            const int col = (j / 2) * 16 + 4 * c + (j & 1);
+                    for (int k = 0; k < JC / 16; ++k)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) mine[(g + 8 * (i >> 1)) * JS + col + 2 * (i & 1)] = v[i];
-                        } else {
-                            *reinterpret_cast<float2 *>(mine + g * JS + j * 8 + 2 * c) = make_float2(v[0], v[1]);
-                            *reinterpret_cast<float2 *>(mine + (g + 8) * JS + j * 8 + 2 * c) = make_float2(v[2], v[3]);
-                        }
-                    }
+                        for (int n = 0; n < NH; ++n)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mine[(n * 8 + 2 * c + (i & 1)) * JR + k * 16 + (FP8 ? 2 * g + (i >> 1) : g + 8 * (i >> 1))] = o[pass * (JC / 16) + k][n][i];
                     __syncthreads();
                     for (int e = tid; e < rows * (JC / 2); e += S::kThreads) {
                         const int r = e / (JC / 2), col = e % (JC / 2) * 2;
                         float2 v = make_float2(0.0f, 0.0f);
 #pragma unroll
                         for (int w = 0; w < W; ++w) {
-                            const float2 x = *reinterpret_cast<const float2 *>(s_join + (w * kHeads + r) * JS + col);
+                            const float2 x = *reinterpret_cast<const float2 *>(s_join + (w * HB + r) * JR + col);
                             v.x += x.x;
                             v.y += x.y;
                         }
@@ -567,17 +637,17 @@ __global__ void __launch_bounds__(Shape<DP, FP8>::kThreads, 1) attention_kernel(
                 if (whole) {
                     if (a.lse) a.lse[(int64_t)cp.b * a.QH + h0 + tid] = s_mall[tid] == -INFINITY ? -INFINITY : (s_mall[tid] + log2f(s_lall[tid])) * kLn2;
                 } else {
-                    part[kHeads * DP + tid] = s_mall[tid];
-                    part[kHeads * DP + kHeads + tid] = s_lall[tid];
+                    part[HB * DP + tid] = s_mall[tid];
+                    part[HB * DP + HB + tid] = s_lall[tid];
                 }
             }
             if (!whole) {
                 // ---- the parts of the blocks that share the segment, joined by the last of them
                 const int first = (int)(((seg0 + 1) * blocks - 1) / total), last = (int)((seg1 * blocks - 1) / total);
                 uint32_t *const counter = a.counters + first;  // a block's run has the beginning of one such segment at most
-                __threadfence();
                 __syncthreads();
                 if (tid == 0) {
+                    __threadfence();  // releases what the whole block wrote before the barrier
                     const uint32_t seen = atomicAdd(counter, 1u);
                     s_last = seen == (uint32_t)(last - first);
                     if (s_last) *counter = 0;  // as the next call finds it
@@ -588,28 +658,36 @@ __global__ void __launch_bounds__(Shape<DP, FP8>::kThreads, 1) attention_kernel(
                     const int n = last - first + 1;
                     auto part_of = [&](int i) {  // the segment is a block's first, or begins inside its run
                         const int blk = first + i;
-                        return a.parts + (2 * blk + (total * blk / blocks < seg0 ? 1 : 0)) * (int64_t)kPart<DP>;
+                        return a.parts + (2 * blk + (total * blk / blocks < seg0 ? 1 : 0)) * (int64_t)S::kPart;
                     };
+                    // only the first block's part can be its second
+                    const float *const part0 = part_of(0), *const part1 = a.parts + 2 * (int64_t)(first + 1) * S::kPart;
+                    auto at_part = [&](int i) { return i == 0 ? part0 : part1 + 2 * (int64_t)(i - 1) * S::kPart; };
+                    for (int e = tid; e < n * HB; e += S::kThreads) s_join[e] = __ldcg(at_part(e / HB) + HB * DP + e % HB);
+                    __syncthreads();
                     if (tid < rows) {
                         float top = -INFINITY, sum = 0.0f;
-                        for (int i = 0; i < n; ++i) top = fmaxf(top, __ldcg(part_of(i) + kHeads * DP + tid));
+                        for (int i = 0; i < n; ++i) top = fmaxf(top, s_join[i * HB + tid]);
+#pragma unroll 4
                         for (int i = 0; i < n; ++i) {
-                            const float mi = __ldcg(part_of(i) + kHeads * DP + tid);
+                            const float mi = s_join[i * HB + tid];
                             const float f = mi == -INFINITY ? 0.0f : fast_exp2(mi - top);
-                            s_join[i * kHeads + tid] = f;
-                            sum += f * __ldcg(part_of(i) + kHeads * DP + kHeads + tid);
+                            s_join[i * HB + tid] = f;
+                            sum = fmaf(f, __ldcg(at_part(i) + HB * DP + HB + tid), sum);
                         }
                         s_lall[tid] = sum > 0.0f ? __fdiv_rn(1.0f, sum) : sum;
                         if (a.lse) a.lse[(int64_t)cp.b * a.QH + h0 + tid] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
                     }
                     __syncthreads();
-                    for (int e = tid; e < rows * (D / 2); e += S::kThreads) {
-                        const int r = e / (D / 2), col = e % (D / 2) * 2;
+                    for (int e = tid; e < rows * (DP / 2); e += S::kThreads) {
+                        const int r = e / (DP / 2), col = e % (DP / 2) * 2;
+                        if (col >= D) continue;
                         float2 v = make_float2(0.0f, 0.0f);
+#pragma unroll 8
                         for (int i = 0; i < n; ++i) {
-                            const float2 x = __ldcg(reinterpret_cast<const float2 *>(part_of(i) + r * DP + col));
-                            v.x = fmaf(x.x, s_join[i * kHeads + r], v.x);
-                            v.y = fmaf(x.y, s_join[i * kHeads + r], v.y);
+                            const float2 x = __ldcg(reinterpret_cast<const float2 *>(at_part(i) + r * DP + col));
+                            v.x = fmaf(x.x, s_join[i * HB + r], v.x);
+                            v.y = fmaf(x.y, s_join[i * HB + r], v.y);
                         }
                         *reinterpret_cast<uint32_t *>(out + ((int64_t)r * D + col) * 2) = pack2_bf16(v.x * s_lall[r], v.y * s_lall[r]);
                     }
@@ -619,9 +697,8 @@ __global__ void __launch_bounds__(Shape<DP, FP8>::kThreads, 1) attention_kernel(
             fresh = true;
         }
         if (step + 1 < steps) {
-            const int b = cp.b;
-            const int tiles = cp.span.tiles;
-            cp.advance(a, heads);
+            const int b = cp.b, tiles = cp.span.tiles;
+            cp.advance(a);
             if (cp.b != b) prefix += tiles;
         }
     }
@@ -633,12 +710,21 @@ inline int padded_dim(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 // sizes are, and two parts for every block.
 constexpr size_t kCounterBytes = (kMaxBlocks * 4 + kAlign - 1) / kAlign * kAlign;
 
-template <int DP, bool FP8>
-epd_status_t launch_attention(const AttnArgs &a, cudaStream_t st) {
-    using S = Shape<DP, FP8>;
-    if (const epd_status_t rc = allow_smem<attention_kernel<DP, FP8>>(S::kSmem)) return rc;
+template <int DP, bool FP8, int NH>
+epd_status_t launch_heads(AttnArgs &a, cudaStream_t st) {
+    using S = Shape<DP, FP8, NH>;
+    a.blocks_of_group = (a.group + S::kHeads - 1) / S::kHeads;
+    if ((int64_t)a.kv.num_kv_heads * a.blocks_of_group > INT32_MAX) return EPD_ERR_UNSUPPORTED;
+    if (const epd_status_t rc = allow_smem<attention_kernel<DP, FP8, NH>>(S::kSmem)) return rc;
     const int grid = sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks;
-    return launch_pdl(attention_kernel<DP, FP8>, grid, S::kThreads, S::kSmem, st, a);
+    return launch_pdl(attention_kernel<DP, FP8, NH>, grid, S::kThreads, S::kSmem, st, a);
+}
+
+// Groups of up to 8 heads take half the registers and matrix instructions; larger ones go 16 heads at a
+// time, so that a group of 16 reads the cache once.
+template <int DP, bool FP8>
+epd_status_t launch_attention(AttnArgs &a, cudaStream_t st) {
+    return a.group <= 8 ? launch_heads<DP, FP8, 1>(a, st) : launch_heads<DP, FP8, 2>(a, st);
 }
 
 }  // namespace
@@ -649,7 +735,7 @@ extern "C" size_t epd_attention_workspace_bytes(int num_seqs, int num_heads, int
     if (num_seqs < 0 || num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads || head_dim < 8 ||
         head_dim % 8 || head_dim > kMaxHeadDim)
         return 0;
-    return kCounterBytes + (size_t)2 * kMaxBlocks * kHeads * (padded_dim(head_dim) + 2) * 4;
+    return kCounterBytes + (size_t)2 * kMaxBlocks * kMaxHeads * (padded_dim(head_dim) + 2) * 4;
 }
 
 extern "C" epd_status_t ep_decode_attention(const epd_cache_t *cache, const void *q, int64_t q_token_stride,
@@ -672,9 +758,8 @@ extern "C" epd_status_t ep_decode_attention(const epd_cache_t *cache, const void
     a.q_stride = 2 * q_token_stride;
     a.QH = num_heads;
     a.group = num_heads / KH;
-    a.blocks_of_group = (a.group + kHeads - 1) / kHeads;
-    if ((int64_t)KH * a.blocks_of_group * B > INT32_MAX) return EPD_ERR_UNSUPPORTED;
     a.kv = *cache;
+    a.page = divisor(cache->page_size);
     a.lengths = lengths;
     a.window = window;
     a.scale_log2 = softmax_scale * kLog2e;
