@@ -79,6 +79,16 @@ def test_rows_of_zeros_and_large_offsets():
     near(d["y"][1], y[1], F32 * 1e4 * 2, torch.bfloat16)
 
 
+def test_tiny_rows():
+    """e4m3 rows whose scale is below the smallest normal number: its reciprocal overflows."""
+    x, w = rand(5, 256), torch.full((256,), 1e-37, device=DEV)
+    d = epd.ep_layer_norm(x, w, with_fp8=True)
+    y = formula(x, None, w, None, 1e-5, "layer")[3]
+    scale = d["y_scale"].double().repeat_interleave(128, 1)
+    # the scale itself has steps of 2^-149, up to 2^-20 of it here
+    assert bool(((d["y_q"].double() * scale - y).abs() <= 2.0 ** -4 * y.abs() + 2.0 ** -10 * scale + 2.0 ** -19 * 448 * scale).all())
+
+
 def test_nonfinite_rows_stay_alone():
     x = rand(64, 1024, dtype=torch.bfloat16)
     want = epd.ep_layer_norm(x)["y"].clone()

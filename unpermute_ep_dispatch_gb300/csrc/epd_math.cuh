@@ -27,6 +27,20 @@ __device__ __forceinline__ uint4 pack8_bf16(const float (&f)[8]) {
                       pack2_bf16(f[6], f[7]));
 }
 
+// v / scale to a unit or two in the last place, by one division for all of them; a scale whose
+// reciprocal may overflow divides each.
+template <int N>
+__device__ __forceinline__ void divide_all(float (&v)[N], float scale) {
+    if (scale >= 0x1p-120f) {
+        const float inv = __fdiv_rn(1.0f, scale);
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] *= inv;
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = __fdiv_rn(v[j], scale);
+    }
+}
+
 constexpr float kInvSqrt2Pi = 0.39894228040143267794f;
 constexpr float kLog2e = 1.4426950408889634f;
 

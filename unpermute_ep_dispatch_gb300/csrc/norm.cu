@@ -25,6 +25,7 @@ namespace epd {
 namespace {
 
 constexpr int kMaxHidden = 16384;
+constexpr int kNormThreads = 512;
 constexpr int kNormMaxSms = 160;    // blocks that the workspace has room for, per block of a multiprocessor
 constexpr int kReduceThreads = 256;
 constexpr int kRingBytes = 224 * 1024;  // of the 227 KB that a multiprocessor's blocks share
@@ -138,7 +139,7 @@ __device__ __forceinline__ void load8(const float *p, int c, float (&f)[8], floa
 }
 
 template <typename T, int NV>
-__global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
     constexpr int P = Chunk<T>::P;
     extern __shared__ uint4 s_ring[];
     __shared__ float2 s_part[2][32];
@@ -155,10 +156,16 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(NormArgs a) 
         copy_commit();
     };
     for (int s = 0; s < a.stages; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
-    float w[8], b[8];
-    if (NV == 1 && tid < a.chunks) {
-        load8(a.weight, tid, w, 1.0f);
-        load8(a.bias, tid, b, 0.0f);
+    constexpr int KEEP = NV <= 2 ? NV : 1;  // chunks whose weights stay in registers
+    float w[KEEP][8], b[KEEP][8];
+    auto load_weights = [&](int i, int k) {
+        if (tid + i * n >= a.chunks) return;
+        load8(a.weight, tid + i * n, w[k], 1.0f);
+        load8(a.bias, tid + i * n, b[k], 0.0f);
+    };
+    if (NV <= 2) {
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i) load_weights(i, i);
     }
     int s = 0;
     for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
@@ -207,13 +214,11 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(NormArgs a) 
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * n;
             if (c >= a.chunks) continue;
-            if (NV > 1) {
-                load8(a.weight, c, w, 1.0f);
-                load8(a.bias, c, b, 0.0f);
-            }
+            const int k = NV <= 2 ? i : 0;
+            if (NV > 2) load_weights(i, 0);
             float o[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = fmaf(v[i][j] * rstd, w[j], b[j]);
+            for (int j = 0; j < 8; ++j) o[j] = fmaf(v[i][j] * rstd, w[k][j], b[k][j]);
             if (a.y) st16(a.y + (row * a.chunks + c) * 16, pack8_bf16(o));
             if (a.yq) {
                 // 128 columns are 16 neighbouring lanes, all of them with a chunk or none
@@ -224,11 +229,11 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(NormArgs a) 
 #pragma unroll
                 for (int d = 8; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half, amax, d));
                 const float scale = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+                divide_all(o, scale);
                 uint32_t q[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    q[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(o[2 * j], scale), __fdiv_rn(o[2 * j + 1], scale)),
-                                                    __NV_SATFINITE, __NV_E4M3);
+                    q[j] = __nv_cvt_float2_to_fp8x2(make_float2(o[2 * j], o[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
                 *reinterpret_cast<uint2 *>(a.yq + (row * a.chunks + c) * 8) =
                     make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
                 if ((c & 15) == 0) a.yscale[row * (a.chunks >> 4) + (c >> 4)] = scale;
@@ -238,7 +243,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_kernel(NormArgs a) 
 }
 
 template <typename T, int NV>
-__global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_backward_kernel(NormGradArgs a) {
+__global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormGradArgs a) {
     constexpr int P = Chunk<T>::P;
     extern __shared__ uint4 s_ring[];
     __shared__ float2 s_part[2][32];
@@ -256,11 +261,25 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_backward_kernel(Nor
         copy_commit();
     };
     for (int s = 0; s < a.stages; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
-    float w[8], dw[NV][8] = {}, db[NV][8] = {};
-    if (NV == 1 && tid < a.chunks) load8(a.weight, tid, w, 1.0f);
+    constexpr int KEEP = NV <= 2 ? NV : 1;
+    float w[KEEP][8], dw[NV][8] = {}, db[NV][8] = {};
+    if (NV <= 2) {
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i)
+            if (tid + i * n < a.chunks) load8(a.weight, tid + i * n, w[i], 1.0f);
+    }
+    // a row's statistics are loaded a row ahead
+    float next_rstd = 0.0f, next_mean = 0.0f;
+    auto statistics = [&](int64_t row) {
+        if (row >= a.T) return;
+        next_rstd = __ldg(a.rstd + row);
+        if (!a.rms) next_mean = __ldg(a.mean + row);
+    };
+    statistics(blockIdx.x);
     int s = 0;
     for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
-        const float rstd = __ldg(a.rstd + row), mean = a.rms ? 0.0f : __ldg(a.mean + row);
+        const float rstd = next_rstd, mean = next_mean;
+        statistics(row + gridDim.x);
         copy_wait(a.stages);
         const uint4 *const at = mine + s * stage;
         auto read = [&](int i, float (&dy)[8], float (&xh)[8]) {
@@ -270,20 +289,21 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_backward_kernel(Nor
             for (int j = 0; j < 8; ++j) xh[j] = (xh[j] - mean) * rstd;
         };
         // a wide row's chunks are unpacked again for the second pass: four would not stay in registers
-        float g[8], xh[8], sg = 0.0f, sgx = 0.0f;
+        float g[KEEP][8], xh[KEEP][8], sg = 0.0f, sgx = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * n;
             if (c >= a.chunks) continue;
-            if (NV > 1) load8(a.weight, c, w, 1.0f);
-            read(i, g, xh);
+            const int k = NV <= 2 ? i : 0;
+            if (NV > 2) load8(a.weight, c, w[k], 1.0f);
+            read(i, g[k], xh[k]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                dw[i][j] = fmaf(g[j], xh[j], dw[i][j]);
-                db[i][j] += g[j];
-                g[j] *= w[j];
-                sg += g[j];
-                sgx = fmaf(g[j], xh[j], sgx);
+                dw[i][j] = fmaf(g[k][j], xh[k][j], dw[i][j]);
+                db[i][j] += g[k][j];
+                g[k][j] *= w[k][j];
+                sg += g[k][j];
+                sgx = fmaf(g[k][j], xh[k][j], sgx);
             }
         }
         block_add(sg, sgx, s_part[(row / gridDim.x) & 1]);
@@ -292,17 +312,18 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) norm_backward_kernel(Nor
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * n;
             if (c >= a.chunks) continue;
-            if (NV > 1) {
-                load8(a.weight, c, w, 1.0f);
-                read(i, g, xh);
+            const int k = NV <= 2 ? i : 0;
+            if (NV > 2) {
+                load8(a.weight, c, w[k], 1.0f);
+                read(i, g[k], xh[k]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) g[j] *= w[j];
+                for (int j = 0; j < 8; ++j) g[k][j] *= w[k][j];
             }
             float r[8], o[8];
             if (a.grad_sum) Chunk<T>::unpack(at + (NV * (1 + P) + i * P) * n, n, r);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                o[j] = rstd * (g[j] - mg - xh[j] * mgx);
+                o[j] = rstd * (g[k][j] - mg - xh[k][j] * mgx);
                 if (a.grad_sum) o[j] += r[j];
             }
             Chunk<T>::store(a.dx + (row * a.chunks + c) * (16 * P), o);
@@ -351,17 +372,18 @@ __global__ void __launch_bounds__(kReduceThreads) norm_reduce_kernel(const float
     }
 }
 
-// Threads of a block (a multiple of 32, one or four chunks each) and blocks a multiprocessor.
+// Chunks of a thread, threads of a block (a multiple of 32) and blocks of a multiprocessor: one chunk
+// where that is a warp or two, two up to 512 threads (the sums over the block and the loop cost
+// every warp the same, whatever it holds), else four.
 struct NormShape {
     int nv, threads, per_sm;
 };
 inline NormShape norm_shape(int H) {
     NormShape s;
     const int chunks = H / 8;
-    s.nv = chunks <= 1024 ? 1 : 4;
+    s.nv = chunks <= 64 ? 1 : chunks <= 2 * kNormThreads ? 2 : 4;
     s.threads = ((chunks + s.nv - 1) / s.nv + 31) / 32 * 32;
-    // the kernels' registers allow 1024 threads (512 of the wide ones), a multiprocessor 32 blocks
-    s.per_sm = (s.nv == 1 ? 1024 : 512) / s.threads;
+    s.per_sm = kNormThreads / s.threads;  // by the kernels' registers
     return s;
 }
 
@@ -424,10 +446,12 @@ extern "C" epd_status_t ep_layer_norm(const void *x, epd_dtype_t dtype, const vo
     const size_t stage = (size_t)(residual ? 2 : 1) * s.nv * item * s.threads * 16;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == EPD_F32)
-        return s.nv == 1 ? launch_rows<norm_kernel<float, 1>>(a, s, grid, stage, st)
-                         : launch_rows<norm_kernel<float, 4>>(a, s, grid, stage, st);
-    return s.nv == 1 ? launch_rows<norm_kernel<__nv_bfloat16, 1>>(a, s, grid, stage, st)
-                     : launch_rows<norm_kernel<__nv_bfloat16, 4>>(a, s, grid, stage, st);
+        return s.nv == 1   ? launch_rows<norm_kernel<float, 1>>(a, s, grid, stage, st)
+               : s.nv == 2 ? launch_rows<norm_kernel<float, 2>>(a, s, grid, stage, st)
+                           : launch_rows<norm_kernel<float, 4>>(a, s, grid, stage, st);
+    return s.nv == 1   ? launch_rows<norm_kernel<__nv_bfloat16, 1>>(a, s, grid, stage, st)
+           : s.nv == 2 ? launch_rows<norm_kernel<__nv_bfloat16, 2>>(a, s, grid, stage, st)
+                       : launch_rows<norm_kernel<__nv_bfloat16, 4>>(a, s, grid, stage, st);
 }
 
 extern "C" size_t epd_norm_workspace_bytes(int hidden) {
@@ -477,11 +501,13 @@ extern "C" epd_status_t ep_layer_norm_backward(const void *dy, const void *x, ep
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     epd_status_t rc;
     if (dtype == EPD_F32)
-        rc = s.nv == 1 ? launch_rows<norm_backward_kernel<float, 1>>(a, s, grid, stage, st)
-                       : launch_rows<norm_backward_kernel<float, 4>>(a, s, grid, stage, st);
+        rc = s.nv == 1   ? launch_rows<norm_backward_kernel<float, 1>>(a, s, grid, stage, st)
+             : s.nv == 2 ? launch_rows<norm_backward_kernel<float, 2>>(a, s, grid, stage, st)
+                         : launch_rows<norm_backward_kernel<float, 4>>(a, s, grid, stage, st);
     else
-        rc = s.nv == 1 ? launch_rows<norm_backward_kernel<__nv_bfloat16, 1>>(a, s, grid, stage, st)
-                       : launch_rows<norm_backward_kernel<__nv_bfloat16, 4>>(a, s, grid, stage, st);
+        rc = s.nv == 1   ? launch_rows<norm_backward_kernel<__nv_bfloat16, 1>>(a, s, grid, stage, st)
+             : s.nv == 2 ? launch_rows<norm_backward_kernel<__nv_bfloat16, 2>>(a, s, grid, stage, st)
+                         : launch_rows<norm_backward_kernel<__nv_bfloat16, 4>>(a, s, grid, stage, st);
     if (rc != EPD_OK || !sums || grid == 1) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((H + 127) / 128), dweight && dbias ? 2 : 1);
