@@ -14,6 +14,8 @@
 // head has its own scale, amax / 448, from the head's lanes by shuffles.
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "cache.cuh"
 
 namespace epd {
@@ -51,10 +53,10 @@ struct AppendArgs {
     uint8_t *q_out;
     int64_t q_token, k_token, v_token, q_out_token;  // bytes
     const int32_t *positions, *token_seq;
-    int T, QH;
+    int T;
     epd_cache_t cache;
     Turn turn;
-    Walk walk;
+    Walk queries, rows;  // rows: keys, then values
     int32_t *status;
 };
 
@@ -154,11 +156,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
 
 template <int V, bool INTER>
 __device__ __forceinline__ void store_e4m3(uint8_t *head, const Place<V, INTER> &at, float (&a)[V], float (&b)[V], float scale) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        a[i] = __fdiv_rn(a[i], scale);
-        b[i] = __fdiv_rn(b[i], scale);
-    }
+    divide_all(a, scale);
+    divide_all(b, scale);
     if constexpr (V == 1) {
         const uint32_t w = e4m3x2(a[0], b[0]);
         head[at.a] = (uint8_t)w;
@@ -255,11 +254,13 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
+    const int parts = a.queries.parts + 2 * a.rows.parts;
     const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t t = unit / a.walk.parts;
+    const int64_t t = unit / parts;
     if (t >= a.T) return;
+    int part = (int)(unit - t * parts);
     const epd_cache_t &kv = a.cache;
-    const int D = kv.head_dim, KH = kv.num_kv_heads;
+    const int D = kv.head_dim;
     const int position = __ldg(a.positions + t);
     const int seq = a.token_seq ? __ldg(a.token_seq + t) : (int)t;
     if (seq == -1) return;  // padding
@@ -272,64 +273,85 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
         if (lane == 0) report(a.status, EPD_ERR_CAPACITY);
         return;
     }
-    const int64_t slot = page * kv.page_stride + inside * kv.token_stride;
-    const int64_t scale_slot = page * kv.scale_page_stride + inside * kv.scale_token_stride;
-    const int per_pass = 32 >> a.walk.lanes_log, lanes = 1 << a.walk.lanes_log;
-    const int first = (int)(unit - t * a.walk.parts) * a.walk.passes * per_pass + (lane >> a.walk.lanes_log);
+    const int lanes_log = a.rows.lanes_log, lanes = 1 << lanes_log, per_pass = 32 >> lanes_log;
     const int p0 = lane & (lanes - 1);
     constexpr int B = NP == 1 ? kBatch : 1;
-    float c[NP][V], s[NP][V];
+    // A warp has queries, keys or values only. `src` and the heads of a token's part; put(n, pass's
+    // chunks) stores head n.
+    auto heads = [&](const uint8_t *src, const Walk &walk, auto is_turned, auto is_held, auto put) {
+        constexpr bool turned = decltype(is_turned)::value, held = decltype(is_held)::value;
+        const int first = part * walk.passes * per_pass + (lane >> lanes_log);
+        float c[NP][V], s[NP][V];
+        if (turned) {
 #pragma unroll
-    for (int q = 0; q < NP; ++q) angles<V>(a.turn, p0 + q * lanes, position, c[q], s[q]);
-    for (int i0 = 0; i0 < a.walk.passes; i0 += B) {
-        Raw<V, INTER> raw[B][NP];
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const int n = first + (i0 + i) * per_pass;
-            if (i0 + i >= a.walk.passes || n >= a.walk.heads) continue;
-            const uint8_t *head = n < a.QH ? a.q + t * a.q_token + (int64_t)n * D * 2
-                : n < a.QH + KH ? a.k + t * a.k_token + (int64_t)(n - a.QH) * D * 2
-                                : a.v + t * a.v_token + (int64_t)(n - a.QH - KH) * D * 2;
-#pragma unroll
-            for (int q = 0; q < NP; ++q)
-                if (p0 + q * lanes < a.walk.chunks)
-                    raw[i][q].load(head, Place<V, INTER>(p0 + q * lanes, a.turn.R, D));
+            for (int q = 0; q < NP; ++q) angles<V>(a.turn, p0 + q * lanes, position, c[q], s[q]);
         }
+        for (int i0 = 0; i0 < walk.passes; i0 += B) {
+            Raw<V, INTER> raw[B][NP];
 #pragma unroll
-        for (int i = 0; i < B; ++i) {
-            if (i0 + i >= a.walk.passes) break;  // the same for the whole warp
-            const int n = first + (i0 + i) * per_pass;
-            const bool has = n < a.walk.heads, is_q = n < a.QH, is_v = n >= a.QH + KH;
-            float u[NP][V], w[NP][V], amax = 0.0f;
+            for (int i = 0; i < B; ++i) {
+                const int n = first + (i0 + i) * per_pass;
+                if (i0 + i >= walk.passes || n >= walk.heads) continue;
 #pragma unroll
-            for (int q = 0; q < NP; ++q)
-                if (has && p0 + q * lanes < a.walk.chunks) {
-                    raw[i][q].values(u[q], w[q]);
-                    if (!is_v) rotate<V>(u[q], w[q], c[q], s[q]);
+                for (int q = 0; q < NP; ++q)
+                    if (p0 + q * lanes < walk.chunks)
+                        raw[i][q].load(src + (int64_t)n * D * 2, Place<V, INTER>(p0 + q * lanes, a.turn.R, D));
+            }
 #pragma unroll
-                    for (int j = 0; j < V; ++j) amax = fmaxf(amax, fmaxf(fabsf(u[q][j]), fabsf(w[q][j])));
+            for (int i = 0; i < B; ++i) {
+                if (i0 + i >= walk.passes) break;  // the same for the whole warp
+                const int n = first + (i0 + i) * per_pass;
+                float u[NP][V], w[NP][V], scale = 1.0f;
+#pragma unroll
+                for (int q = 0; q < NP; ++q)
+                    if (n < walk.heads && p0 + q * lanes < walk.chunks) {
+                        raw[i][q].values(u[q], w[q]);
+                        if (turned) rotate<V>(u[q], w[q], c[q], s[q]);
+                    }
+                if (held && FP8) {
+                    float amax = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < NP; ++q)
+                        if (n < walk.heads && p0 + q * lanes < walk.chunks) {
+#pragma unroll
+                            for (int j = 0; j < V; ++j) amax = fmaxf(amax, fmaxf(fabsf(u[q][j]), fabsf(w[q][j])));
+                        }
+                    for (int d = lanes >> 1; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, d));
+                    if (amax > 0.0f) scale = __fdiv_rn(amax, 448.0f);
                 }
-            if (FP8)
-                for (int d = lanes >> 1; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, d));
-            if (!has) continue;
-            const int h = is_v ? n - a.QH - KH : n - a.QH;  // of the cache
-            const float scale = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+                if (n < walk.heads) {
 #pragma unroll
-            for (int q = 0; q < NP; ++q) {
-                if (p0 + q * lanes >= a.walk.chunks) continue;
-                const Place<V, INTER> at(p0 + q * lanes, a.turn.R, D);
-                if (is_q) {
-                    store_bf16<V, INTER>(a.q_out + t * a.q_out_token + (int64_t)n * D * 2, at, u[q], w[q]);
-                } else {
-                    uint8_t *base = static_cast<uint8_t *>(is_v ? kv.v : kv.k);
-                    const int64_t off = slot + h * kv.head_stride;
-                    if (FP8) store_e4m3<V, INTER>(base + off, at, u[q], w[q], scale);
-                    else store_bf16<V, INTER>(base + 2 * off, at, u[q], w[q]);
+                    for (int q = 0; q < NP; ++q)
+                        if (p0 + q * lanes < walk.chunks) put(n, Place<V, INTER>(p0 + q * lanes, a.turn.R, D), u[q], w[q], scale);
                 }
             }
-            if (FP8 && !is_q && p0 == 0)
-                (is_v ? kv.v_scale : kv.k_scale)[scale_slot + h * kv.scale_head_stride] = scale;
         }
+    };
+    if (part < a.queries.parts) {
+        uint8_t *const out = a.q_out + t * a.q_out_token;
+        heads(a.q + t * a.q_token, a.queries, std::true_type{}, std::false_type{},
+              [&](int n, const Place<V, INTER> &at, float(&u)[V], float(&w)[V], float) { store_bf16<V, INTER>(out + (int64_t)n * D * 2, at, u, w); });
+        return;
+    }
+    const int64_t slot = page * kv.page_stride + inside * kv.token_stride;
+    const int64_t scale_slot = page * kv.scale_page_stride + inside * kv.scale_token_stride;
+    auto hold = [&](void *base, float *scales) {
+        return [=, &kv](int n, const Place<V, INTER> &at, float(&u)[V], float(&w)[V], float scale) {
+            const int64_t off = slot + n * kv.head_stride;
+            if (FP8) {
+                store_e4m3<V, INTER>(static_cast<uint8_t *>(base) + off, at, u, w, scale);
+                if (at.a == 0) scales[scale_slot + n * kv.scale_head_stride] = scale;
+            } else {
+                store_bf16<V, INTER>(static_cast<uint8_t *>(base) + 2 * off, at, u, w);
+            }
+        };
+    };
+    part -= a.queries.parts;
+    if (part < a.rows.parts) {
+        heads(a.k + t * a.k_token, a.rows, std::true_type{}, std::true_type{}, hold(kv.k, kv.k_scale));
+    } else {
+        part -= a.rows.parts;
+        heads(a.v + t * a.v_token, a.rows, std::false_type{}, std::true_type{}, hold(kv.v, kv.v_scale));
     }
 }
 
@@ -341,7 +363,7 @@ inline int pairs_of_chunk(int D, int R, bool inter) {
 }
 
 // `columns` of each of `heads` heads of T tokens in chunks of V pairs. A warp takes several passes
-// over a token's heads, up to eight, where that leaves 16 warps for each multiprocessor: the sines
+// over a token's heads, up to twelve, where that leaves 16 warps for each multiprocessor: the sines
 // and cosines are then shared by more heads.
 inline Walk walk_of(int T, int heads, int columns, int V) {
     Walk w;
@@ -351,13 +373,14 @@ inline Walk walk_of(int T, int heads, int columns, int V) {
     w.heads = heads;
     const int per_pass = 32 >> w.lanes_log, passes = (heads + per_pass - 1) / per_pass;
     const int64_t share = (int64_t)T * passes / (16 * sm_count());
-    w.passes = share < 1 ? 1 : share < 8 ? (int)share : 8;
-    w.parts = (passes + w.passes - 1) / w.passes;
+    const int most = share < 1 ? 1 : share < 12 ? (int)share : 12;
+    w.parts = (passes + most - 1) / most;
+    w.passes = w.parts > 0 ? (passes + w.parts - 1) / w.parts : 0;
     return w;
 }
 
-inline epd_status_t grid_of(int T, const Walk &w, int &grid) {
-    const int64_t warps = (int64_t)T * w.parts, blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
+inline epd_status_t grid_of(int T, int parts, int &grid) {
+    const int64_t warps = (int64_t)T * parts, blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
     if (blocks > INT32_MAX) return EPD_ERR_UNSUPPORTED;
     grid = (int)blocks;
     return EPD_OK;
@@ -404,7 +427,7 @@ extern "C" epd_status_t ep_rotary(const void *x, int64_t token_stride, int64_t h
     const bool in_place = x == out && token_stride == out_token_stride && head_stride == out_head_stride;
     a.walk = walk_of(T, N, in_place ? R : D, V);
     int grid;
-    if (const epd_status_t rc = grid_of(T, a.walk, grid)) return rc;
+    if (const epd_status_t rc = grid_of(T, a.walk.parts, grid)) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (interleaved)
         return V == 4 ? launch_pdl(rotary_kernel<4, true>, grid, kThreads, 0, st, a)
@@ -428,7 +451,7 @@ extern "C" epd_status_t ep_cache_append(const epd_cache_t *cache, const void *q,
         if (s < 0 || s % 8 != 0) return EPD_ERR_INVALID_ARG;
     if (!status || !aligned4(status)) return EPD_ERR_INVALID_ARG;
     if (!token_seq && T > cache->num_seqs) return EPD_ERR_INVALID_ARG;
-    if ((int64_t)QH + 2 * (int64_t)cache->num_kv_heads > INT32_MAX) return EPD_ERR_INVALID_ARG;
+    if ((int64_t)QH + 2 * (int64_t)cache->num_kv_heads > INT32_MAX) return EPD_ERR_UNSUPPORTED;
     if (T == 0) return EPD_OK;
     if (!k || !v || !positions || !aligned16(k) || !aligned16(v) || !aligned4(positions) || !aligned4(token_seq))
         return EPD_ERR_INVALID_ARG;
@@ -443,16 +466,16 @@ extern "C" epd_status_t ep_cache_append(const epd_cache_t *cache, const void *q,
     a.positions = positions;
     a.token_seq = token_seq;
     a.T = T;
-    a.QH = QH;
     a.cache = *cache;
     a.turn = {steps, R, 0, rotary_scale};
     a.status = status;
     // without rotation the chunks are runs of 16 bytes
     const bool inter = interleaved || R == 0;
     const int V = pairs_of_chunk(D, R, inter);
-    a.walk = walk_of(T, QH + 2 * cache->num_kv_heads, D, V);
+    a.queries = walk_of(T, QH, D, V);
+    a.rows = walk_of(T, cache->num_kv_heads, D, V);
     int grid;
-    if (const epd_status_t rc = grid_of(T, a.walk, grid)) return rc;
+    if (const epd_status_t rc = grid_of(T, a.queries.parts + 2 * a.rows.parts, grid)) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (inter) return V == 4 ? launch_append<4, true>(a, grid, st) : launch_append<1, true>(a, grid, st);
     return V == 8 ? launch_append<8, false>(a, grid, st)
