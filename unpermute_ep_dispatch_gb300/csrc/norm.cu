@@ -61,25 +61,45 @@ __device__ __forceinline__ void copy_wait(int stages) {
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-__device__ __forceinline__ float warp_add(float v) {
+// Sums of a and b over the block's warps (16 at most), in every thread. The two take one exchange to
+// lie in a half-warp each and go on together. `part` alternates between two calls, so that one barrier a
+// call is enough.
+__device__ __forceinline__ void block_add(float &a, float &b, float (&part)[2][16]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const bool upper = lane & 16;
+    float v = (upper ? b : a) + __shfl_xor_sync(kAll, upper ? a : b, 16);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-    return v;
+    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    if (warps > 1) {
+        if ((lane & 15) == 0) part[lane >> 4][warp] = v;
+        __syncthreads();
+        v = (lane & 15) < warps ? part[lane >> 4][lane & 15] : 0.0f;
+#pragma unroll
+        for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    }
+    a = __shfl_sync(kAll, v, 0);
+    b = __shfl_sync(kAll, v, 16);
 }
 
-// Sums of a and b over the block, in every thread. `part` alternates between two calls, so that one
-// barrier a call is enough.
-__device__ __forceinline__ void block_add(float &a, float &b, float2 (&part)[32]) {
+// The same of one sum.
+__device__ __forceinline__ void block_add(float &a, float (&part)[16]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    a = warp_add(a);
-    b = warp_add(b);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(kAll, a, o);
     if (warps == 1) return;
-    if (lane == 0) part[warp] = make_float2(a, b);
+    if (lane == 0) part[warp] = a;
     __syncthreads();
-    const float2 v = lane < warps ? part[lane] : make_float2(0.0f, 0.0f);
-    a = warp_add(v.x);
-    b = warp_add(v.y);
+    a = (lane & 15) < warps ? part[lane & 15] : 0.0f;
+#pragma unroll
+    for (int o = 8; o; o >>= 1) a += __shfl_xor_sync(kAll, a, o);
 }
+
+// Eight columns in 32 bits, two to an instruction.
+struct Eight {
+    float2 v[4];
+    __device__ __forceinline__ float get(int j) const { return j & 1 ? v[j >> 1].y : v[j >> 1].x; }
+};
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // 16-byte pieces of an 8-column chunk of T, and the chunk in 32 bits.
 template <typename T>
@@ -87,25 +107,34 @@ struct Chunk;
 template <>
 struct Chunk<__nv_bfloat16> {
     static constexpr int P = 1;
-    static __device__ __forceinline__ void unpack(const uint4 *slot, int stride, float (&f)[8]) { unpack8_bf16(slot[0], f); }
-    static __device__ __forceinline__ void store(uint8_t *p, const float (&f)[8]) { st16(p, pack8_bf16(f)); }
+    static __device__ __forceinline__ void unpack(const uint4 *slot, int, Eight &f) {
+        const uint4 w = slot[0];
+        f.v[0] = make_float2(lo_bf16(w.x), hi_bf16(w.x));
+        f.v[1] = make_float2(lo_bf16(w.y), hi_bf16(w.y));
+        f.v[2] = make_float2(lo_bf16(w.z), hi_bf16(w.z));
+        f.v[3] = make_float2(lo_bf16(w.w), hi_bf16(w.w));
+    }
+    static __device__ __forceinline__ void store(uint8_t *p, const Eight &f) {
+        st16(p, make_uint4(pack2_bf16(f.v[0].x, f.v[0].y), pack2_bf16(f.v[1].x, f.v[1].y),
+                           pack2_bf16(f.v[2].x, f.v[2].y), pack2_bf16(f.v[3].x, f.v[3].y)));
+    }
 };
 template <>
 struct Chunk<float> {
     static constexpr int P = 2;
-    static __device__ __forceinline__ void unpack(const uint4 *slot, int stride, float (&f)[8]) {
+    static __device__ __forceinline__ void unpack(const uint4 *slot, int stride, Eight &f) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint4 v = slot[h * stride];
-            f[4 * h] = __uint_as_float(v.x), f[4 * h + 1] = __uint_as_float(v.y);
-            f[4 * h + 2] = __uint_as_float(v.z), f[4 * h + 3] = __uint_as_float(v.w);
+            const uint4 w = slot[h * stride];
+            f.v[2 * h] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+            f.v[2 * h + 1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
         }
     }
-    static __device__ __forceinline__ void store(uint8_t *p, const float (&f)[8]) {
+    static __device__ __forceinline__ void store(uint8_t *p, const Eight &f) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            st16(p + 16 * h, make_uint4(__float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]),
-                                        __float_as_uint(f[4 * h + 2]), __float_as_uint(f[4 * h + 3])));
+            st16(p + 16 * h, make_uint4(__float_as_uint(f.v[2 * h].x), __float_as_uint(f.v[2 * h].y),
+                                        __float_as_uint(f.v[2 * h + 1].x), __float_as_uint(f.v[2 * h + 1].y)));
     }
 };
 
@@ -114,35 +143,26 @@ struct Chunk<float> {
 template <typename T, int NV>
 __device__ __forceinline__ void fetch_row(uint4 *at, const uint8_t *src, int64_t row, int chunks) {
     constexpr int P = Chunk<T>::P;
-    const uint8_t *p = src + row * chunks * (16 * P);
+    const uint8_t *p = src + (row * chunks + threadIdx.x) * (16 * P);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = threadIdx.x + i * blockDim.x;
-        if (c < chunks) {
+    for (int i = 0; i < NV; ++i)
+        if ((int)(threadIdx.x + i * blockDim.x) < chunks) {
 #pragma unroll
-            for (int h = 0; h < P; ++h) copy16(at + (i * P + h) * blockDim.x, p + (int64_t)c * (16 * P) + 16 * h);
+            for (int h = 0; h < P; ++h) copy16(at + (i * P + h) * blockDim.x, p + i * blockDim.x * (16 * P) + 16 * h);
         }
-    }
 }
 
-__device__ __forceinline__ void load8(const float *p, int c, float (&f)[8], float none) {
-    if (!p) {
+__device__ __forceinline__ void load8(const float *p, int c, Eight &f, float none) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = none;
-        return;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(p + 8 * (int64_t)c) + h);
-        f[4 * h] = v.x, f[4 * h + 1] = v.y, f[4 * h + 2] = v.z, f[4 * h + 3] = v.w;
-    }
+    for (int j = 0; j < 4; ++j) f.v[j] = p ? __ldg(reinterpret_cast<const float2 *>(p + 8 * (int64_t)c) + j) : both(none);
 }
 
 template <typename T, int NV>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
     constexpr int P = Chunk<T>::P;
+    constexpr int KEEP = NV <= 2 ? NV : 1;  // chunks whose weights stay in registers
     extern __shared__ uint4 s_ring[];
-    __shared__ float2 s_part[2][32];
+    __shared__ float s_part[2][16];
     const int tid = threadIdx.x, n = blockDim.x;
     const int arrays = a.residual ? 2 : 1, stage = arrays * NV * P * n;
     pdl_wait();
@@ -156,8 +176,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
         copy_commit();
     };
     for (int s = 0; s < a.stages; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
-    constexpr int KEEP = NV <= 2 ? NV : 1;  // chunks whose weights stay in registers
-    float w[KEEP][8], b[KEEP][8];
+    Eight w[KEEP], b[KEEP];
     auto load_weights = [&](int i, int k) {
         if (tid + i * n >= a.chunks) return;
         load8(a.weight, tid + i * n, w[k], 1.0f);
@@ -167,42 +186,46 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < KEEP; ++i) load_weights(i, i);
     }
-    int s = 0;
+    int s = 0, turn = 0;
     for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
         copy_wait(a.stages);
-        float v[NV][8], sum = 0.0f, none = 0.0f;
+        Eight v[NV];
+        float2 total = both(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * n;
             if (c >= a.chunks) continue;
             Chunk<T>::unpack(mine + s * stage + i * P * n, n, v[i]);
             if (a.residual) {
-                float r[8];
+                Eight r;
                 Chunk<T>::unpack(mine + s * stage + (NV + i) * P * n, n, r);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] += r[j];
+                for (int j = 0; j < 4; ++j) v[i].v[j] = __fadd2_rn(v[i].v[j], r.v[j]);
                 if (a.sum) Chunk<T>::store(a.sum + (row * a.chunks + c) * (16 * P), v[i]);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum += v[i][j];
+            for (int j = 0; j < 4; ++j) total = __fadd2_rn(total, v[i].v[j]);
         }
         float mean = 0.0f;
         if (!a.rms) {
-            block_add(sum, none, s_part[0]);
-            mean = __fdiv_rn(sum, (float)(a.chunks * 8));
+            mean = total.x + total.y;
+            block_add(mean, s_part[0]);
+            mean = __fdiv_rn(mean, (float)(a.chunks * 8));
         }
-        float sq = 0.0f;
+        total = both(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (tid + i * n < a.chunks) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    v[i][j] -= mean;
-                    sq = fmaf(v[i][j], v[i][j], sq);
+                for (int j = 0; j < 4; ++j) {
+                    if (!a.rms) v[i].v[j] = __fadd2_rn(v[i].v[j], both(-mean));
+                    total = __ffma2_rn(v[i].v[j], v[i].v[j], total);
                 }
             }
         // RMS has one sum a row: its two buffers take turns from row to row
-        block_add(sq, none, a.rms ? s_part[(row / gridDim.x) & 1] : s_part[1]);
+        float sq = total.x + total.y;
+        block_add(sq, s_part[a.rms ? turn : 1]);
+        turn ^= 1;
         const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(fmaf(sq, a.inv_h, a.eps)));
         fetch(row + (int64_t)a.stages * gridDim.x, s);
         if (++s == a.stages) s = 0;
@@ -216,24 +239,27 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
             if (c >= a.chunks) continue;
             const int k = NV <= 2 ? i : 0;
             if (NV > 2) load_weights(i, 0);
-            float o[8];
+            Eight o;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = fmaf(v[i][j] * rstd, w[k][j], b[k][j]);
-            if (a.y) st16(a.y + (row * a.chunks + c) * 16, pack8_bf16(o));
+            for (int j = 0; j < 4; ++j) o.v[j] = __ffma2_rn(__fmul2_rn(v[i].v[j], both(rstd)), w[k].v[j], b[k].v[j]);
+            if (a.y) Chunk<__nv_bfloat16>::store(a.y + (row * a.chunks + c) * 16, o);
             if (a.yq) {
                 // 128 columns are 16 neighbouring lanes, all of them with a chunk or none
                 const unsigned half = (tid & 16) ? 0xffff0000u : 0x0000ffffu;
-                float amax = 0.0f;
+                float f[8], amax = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(o[j]));
+                for (int j = 0; j < 8; ++j) {
+                    f[j] = o.get(j);
+                    amax = fmaxf(amax, fabsf(f[j]));
+                }
 #pragma unroll
                 for (int d = 8; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half, amax, d));
                 const float scale = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-                divide_all(o, scale);
+                divide_all(f, scale);
                 uint32_t q[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    q[j] = __nv_cvt_float2_to_fp8x2(make_float2(o[2 * j], o[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
+                    q[j] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * j], f[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
                 *reinterpret_cast<uint2 *>(a.yq + (row * a.chunks + c) * 8) =
                     make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
                 if ((c & 15) == 0) a.yscale[row * (a.chunks >> 4) + (c >> 4)] = scale;
@@ -245,8 +271,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
 template <typename T, int NV>
 __global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormGradArgs a) {
     constexpr int P = Chunk<T>::P;
+    constexpr int KEEP = NV <= 2 ? NV : 1;
     extern __shared__ uint4 s_ring[];
-    __shared__ float2 s_part[2][32];
+    __shared__ float s_part[2][2][16];
     const int tid = threadIdx.x, n = blockDim.x;
     const int stage = NV * (1 + (a.grad_sum ? 2 : 1) * P) * n;
     pdl_wait();
@@ -261,8 +288,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormGradArg
         copy_commit();
     };
     for (int s = 0; s < a.stages; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
-    constexpr int KEEP = NV <= 2 ? NV : 1;
-    float w[KEEP][8], dw[NV][8] = {}, db[NV][8] = {};
+    Eight w[KEEP], dw[NV] = {}, db[NV] = {};
     if (NV <= 2) {
 #pragma unroll
         for (int i = 0; i < KEEP; ++i)
@@ -276,20 +302,21 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormGradArg
         if (!a.rms) next_mean = __ldg(a.mean + row);
     };
     statistics(blockIdx.x);
-    int s = 0;
+    int s = 0, turn = 0;
     for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
         const float rstd = next_rstd, mean = next_mean;
         statistics(row + gridDim.x);
         copy_wait(a.stages);
         const uint4 *const at = mine + s * stage;
-        auto read = [&](int i, float (&dy)[8], float (&xh)[8]) {
-            unpack8_bf16(at[i * n], dy);
+        auto read = [&](int i, Eight &dy, Eight &xh) {
+            Chunk<__nv_bfloat16>::unpack(at + i * n, n, dy);
             Chunk<T>::unpack(at + (NV + i * P) * n, n, xh);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) xh[j] = (xh[j] - mean) * rstd;
+            for (int j = 0; j < 4; ++j) xh.v[j] = __fmul2_rn(__fadd2_rn(xh.v[j], both(-mean)), both(rstd));
         };
         // a wide row's chunks are unpacked again for the second pass: four would not stay in registers
-        float g[KEEP][8], xh[KEEP][8], sg = 0.0f, sgx = 0.0f;
+        Eight g[KEEP], xh[KEEP];
+        float2 sg2 = both(0.0f), sgx2 = both(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * n;
@@ -298,16 +325,19 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormGradArg
             if (NV > 2) load8(a.weight, c, w[k], 1.0f);
             read(i, g[k], xh[k]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                dw[i][j] = fmaf(g[k][j], xh[k][j], dw[i][j]);
-                db[i][j] += g[k][j];
-                g[k][j] *= w[k][j];
-                sg += g[k][j];
-                sgx = fmaf(g[k][j], xh[k][j], sgx);
+            for (int j = 0; j < 4; ++j) {
+                dw[i].v[j] = __ffma2_rn(g[k].v[j], xh[k].v[j], dw[i].v[j]);
+                db[i].v[j] = __fadd2_rn(db[i].v[j], g[k].v[j]);
+                g[k].v[j] = __fmul2_rn(g[k].v[j], w[k].v[j]);
+                sg2 = __fadd2_rn(sg2, g[k].v[j]);
+                sgx2 = __ffma2_rn(g[k].v[j], xh[k].v[j], sgx2);
             }
         }
-        block_add(sg, sgx, s_part[(row / gridDim.x) & 1]);
-        const float mg = a.rms ? 0.0f : sg * a.inv_h, mgx = sgx * a.inv_h;
+        float sg = sg2.x + sg2.y, sgx = sgx2.x + sgx2.y;
+        block_add(sg, sgx, s_part[turn]);
+        turn ^= 1;
+        // dx = g rstd - xh (rstd sgx / H) - rstd sg / H
+        const float by_x = -rstd * (sgx * a.inv_h), by_1 = a.rms ? 0.0f : -rstd * (sg * a.inv_h);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * n;
@@ -317,14 +347,17 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormGradArg
                 load8(a.weight, c, w[k], 1.0f);
                 read(i, g[k], xh[k]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) g[k][j] *= w[k][j];
+                for (int j = 0; j < 4; ++j) g[k].v[j] = __fmul2_rn(g[k].v[j], w[k].v[j]);
             }
-            float r[8], o[8];
-            if (a.grad_sum) Chunk<T>::unpack(at + (NV * (1 + P) + i * P) * n, n, r);
+            Eight o;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                o[j] = rstd * (g[k][j] - mg - xh[k][j] * mgx);
-                if (a.grad_sum) o[j] += r[j];
+            for (int j = 0; j < 4; ++j)
+                o.v[j] = __ffma2_rn(xh[k].v[j], both(by_x), __ffma2_rn(g[k].v[j], both(rstd), both(by_1)));
+            if (a.grad_sum) {
+                Eight r;
+                Chunk<T>::unpack(at + (NV * (1 + P) + i * P) * n, n, r);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o.v[j] = __fadd2_rn(o.v[j], r.v[j]);
             }
             Chunk<T>::store(a.dx + (row * a.chunks + c) * (16 * P), o);
         }
