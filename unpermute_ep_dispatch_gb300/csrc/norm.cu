@@ -373,29 +373,34 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormGradArg
     }
 }
 
-// out[h] = sum over blocks of part[block][h]: a block takes 128 columns, its eight warps every
-// eighth of the rows, joined in the warps' order. blockIdx.y chooses the weight's or the bias's.
+// out[h] = sum over blocks of part[block][h]: a block takes 32 columns, its 32 groups of eight lanes
+// every 32nd of the rows, joined in the groups' order. blockIdx.y chooses the weight's or the bias's.
 __global__ void __launch_bounds__(kReduceThreads) norm_reduce_kernel(const float *part, int blocks, int64_t stride, int H,
                                                                      float *dweight, float *dbias) {
-    __shared__ float4 s_sum[kReduceThreads / 32][32];
+    __shared__ float4 s_sum[kReduceThreads / 32][8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool second = blockIdx.y == 1 || !dweight;
     float *const out = second ? dbias : dweight;
     const float *const in = part + (second ? H : 0);
-    const int h = (blockIdx.x * 32 + lane) * 4;
+    const int h = (blockIdx.x * 8 + (lane & 7)) * 4;
     pdl_wait();
     pdl_trigger();
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (h < H) {
 #pragma unroll 8
-        for (int b = warp; b < blocks; b += kReduceThreads / 32) {
+        for (int b = warp * 4 + (lane >> 3); b < blocks; b += kReduceThreads / 8) {
             const float4 p = __ldcg(reinterpret_cast<const float4 *>(in + b * stride + h));
             v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
         }
     }
-    s_sum[warp][lane] = v;
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+        v.x += __shfl_xor_sync(kAll, v.x, o), v.y += __shfl_xor_sync(kAll, v.y, o);
+        v.z += __shfl_xor_sync(kAll, v.z, o), v.w += __shfl_xor_sync(kAll, v.w, o);
+    }
+    if (lane < 8) s_sum[warp][lane] = v;
     __syncthreads();
-    if (warp == 0 && h < H) {
+    if (warp == 0 && lane < 8 && h < H) {
 #pragma unroll
         for (int i = 1; i < kReduceThreads / 32; ++i) {
             const float4 p = s_sum[i][lane];
@@ -543,7 +548,7 @@ extern "C" epd_status_t ep_layer_norm_backward(const void *dy, const void *x, ep
                          : launch_rows<norm_backward_kernel<__nv_bfloat16, 4>>(a, s, grid, stage, st);
     if (rc != EPD_OK || !sums || grid == 1) return rc;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((H + 127) / 128), dweight && dbias ? 2 : 1);
+    cfg.gridDim = dim3((unsigned)((H + 31) / 32), dweight && dbias ? 2 : 1);
     cfg.blockDim = dim3(kReduceThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
