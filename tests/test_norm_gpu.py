@@ -79,6 +79,17 @@ def test_rows_of_zeros_and_large_offsets():
     near(d["y"][1], y[1], F32 * 1e4 * 2, torch.bfloat16)
 
 
+@pytest.mark.parametrize("shift", [0.0, 0.9, 1.1, 3.0, 100.0])
+def test_means_around_the_deviation(shift):
+    """The variance by the squares' mean and, where the row's mean is above its deviation, by centred values."""
+    x = rand(64, 1000, shift=shift)
+    x[::2] -= 2 * shift
+    d = epd.ep_layer_norm(x, with_stats=True)
+    _, mean, rstd, y, big = formula(x, None, None, None, 1e-5, "layer")
+    near(d["y"], y, F32 * big, torch.bfloat16)
+    near(d["rstd"], rstd.squeeze(1), F32 * rstd.squeeze(1), torch.float32)
+
+
 def test_tiny_rows():
     """e4m3 rows whose scale is below the smallest normal number: its reciprocal overflows."""
     x, w = rand(5, 256), torch.full((256,), 1e-37, device=DEV)

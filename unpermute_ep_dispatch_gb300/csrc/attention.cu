@@ -59,6 +59,7 @@ struct AttnArgs {
     const int32_t *lengths;
     int window;
     float scale_log2;
+    int aligned;  // every run of 16 positions from a multiple of 16 lies on one page, and tiles begin at such
     uint8_t *out;  // bf16 [B, QH, D]
     float *lse;
     uint32_t *counters;
@@ -90,6 +91,9 @@ struct Shape {
 __device__ __forceinline__ void copy16z(uint32_t dst, const void *src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy4z(uint32_t dst, const void *src, bool live) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
 }
@@ -119,11 +123,9 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 (the low half of w) as two fp16, exactly.
-__device__ __forceinline__ uint32_t widen2(uint32_t w) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
-    return r;
+// Four e4m3 as two pairs of fp16, exactly.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
 }
 __device__ __forceinline__ uint32_t pack2_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -292,7 +294,28 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
         const int inside = live ? token - (int)(divide(token, a.page) * a.page.d) : 0;
         const int64_t off = live ? (page * a.kv.page_stride + inside * a.kv.token_stride + kv_head * a.kv.head_stride) * (FP8 ? 1 : 2) : 0;
         const uint32_t mask = __ballot_sync(kAll, live) & (CH == 32 ? kAll : 0xffffu);
-        if (mask) {
+        if (a.aligned && mask == (CH == 32 ? kAll : 0xffffu)) {
+            // every 16 tokens lie on one page: one address for them, and a constant step
+            constexpr int STEP = 32 / UNITS > 0 ? 32 / UNITS : 1;  // rows of one instruction
+            const int64_t step = a.kv.token_stride * (FP8 ? 1 : 2);
+            const int u = lane % UNITS;
+            const uint8_t *const k0 = static_cast<const uint8_t *>(a.kv.k) + (lane / UNITS) * step + u * 16;
+            const int64_t to_v = (int64_t)(reinterpret_cast<uintptr_t>(a.kv.v) - reinterpret_cast<uintptr_t>(a.kv.k));
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const uint8_t *src = k0 + __shfl_sync(kAll, off, 16 * t);
+#pragma unroll
+                for (int i = 0; i < 16 / STEP; ++i) {
+                    const int row = t * 16 + i * STEP + lane / UNITS;
+                    const uint32_t dst = at + row * S::kRow + swizzle<UNITS>(row, u) * 16;
+                    if (u < units) {
+                        copy16(dst, src);
+                        copy16(dst + CH * S::kRow, src + to_v);
+                    }
+                    src += STEP * step;
+                }
+            }
+        } else if (mask) {
 #pragma unroll
             for (int i = 0; i < CH * UNITS / 32; ++i) {
                 const int row = (i * 32 + lane) / UNITS, u = (i * 32 + lane) % UNITS;
@@ -304,12 +327,12 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
                     copy16z(dst + CH * S::kRow, static_cast<const uint8_t *>(a.kv.v) + (has ? o : 0), has);
                 }
             }
-            if (FP8) {
-                const int64_t so = live ? page * a.kv.scale_page_stride + inside * a.kv.scale_token_stride + kv_head * a.kv.scale_head_stride : 0;
-                const uint32_t dst = at + 2 * CH * S::kRow + (lane & (CH - 1)) * 4;
-                if (CH == 32 || lane < 16) copy4z(dst, a.kv.k_scale + so, live);
-                if (CH == 32 || lane >= 16) copy4z(dst + CH * 4, a.kv.v_scale + so, live);
-            }
+        }
+        if (FP8 && mask) {
+            const int64_t so = live ? page * a.kv.scale_page_stride + inside * a.kv.scale_token_stride + kv_head * a.kv.scale_head_stride : 0;
+            const uint32_t dst = at + 2 * CH * S::kRow + (lane & (CH - 1)) * 4;
+            if (CH == 32 || lane < 16) copy4z(dst, a.kv.k_scale + so, live);
+            if (CH == 32 || lane >= 16) copy4z(dst + CH * 4, a.kv.v_scale + so, live);
         }
         if (lane == 0)
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + S::kStage - 16), "r"(mask) : "memory");
@@ -398,15 +421,17 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
             float s[MT][NH][4] = {};
             const int row = lane & 15, right = lane >> 4;
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
+            for (int k = 0; k < UNITS / 2; ++k)
 #pragma unroll
-                for (int k = 0; k < UNITS / 2; ++k) {
+                for (int t = 0; t < MT; ++t) {
                     uint32_t r[4];
                     ldsm4(r, at + (t * 16 + row) * S::kRow + swizzle<UNITS>(row, 2 * k + right) * 16);
                     if (FP8) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const uint32_t f[4] = {widen2(r[2 * h]), widen2(r[2 * h + 1]), widen2(r[2 * h] >> 16), widen2(r[2 * h + 1] >> 16)};
+                            uint32_t f[4];
+                            widen4(r[2 * h], f[0], f[2]);
+                            widen4(r[2 * h + 1], f[1], f[3]);
 #pragma unroll
                             for (int n = 0; n < NH; ++n) mma<true>(s[t][n], f, q[2 * k + h][n][0], q[2 * k + h][n][1]);
                         }
@@ -415,7 +440,6 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
                         for (int n = 0; n < NH; ++n) mma<false>(s[t][n], r, q[k][n][0], q[k][n][1]);
                     }
                 }
-            }
             const float *const sc = scales + stage * (S::kStage / 4);
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
@@ -532,8 +556,9 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
                         ldsm4t(r, av + (t * 16 + row) * S::kRow + swizzle<UNITS>(row, 2 * k + right) * 16);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const uint32_t x = __byte_perm(r[2 * h], 0, 0x3120), y = __byte_perm(r[2 * h + 1], 0, 0x3120);
-                            const uint32_t f[4] = {widen2(x), widen2(x >> 16), widen2(y), widen2(y >> 16)};
+                            uint32_t f[4];
+                            widen4(__byte_perm(r[2 * h], 0, 0x3120), f[0], f[1]);
+                            widen4(__byte_perm(r[2 * h + 1], 0, 0x3120), f[2], f[3]);
 #pragma unroll
                             for (int n = 0; n < NH; ++n) mma<true>(o[2 * k + h][n], f, p[t][n][0], p[t][n][1]);
                         }
@@ -763,6 +788,7 @@ extern "C" epd_status_t ep_decode_attention(const epd_cache_t *cache, const void
     a.lengths = lengths;
     a.window = window;
     a.scale_log2 = softmax_scale * kLog2e;
+    a.aligned = cache->page_size % 16 == 0 && window == 0;
     a.out = static_cast<uint8_t *>(out);
     a.lse = lse;
     a.counters = static_cast<uint32_t *>(workspace);

@@ -9,11 +9,9 @@
 //
 // Bound by HBM: every row is read once and written once. A block owns a row, a thread one
 // 8-column chunk of it (four where the row is wider than 8192), and blocks walk over the rows with
-// the row kept in registers between the sums. Each thread copies its own chunks of the rows to
+// the row kept in registers between the sums and the output. Each thread copies its own chunks of the rows to
 // come into its own slots of shared memory (cp.async, up to four rows ahead): no barrier and no
-// wait but the thread's own, and one block a multiprocessor keeps 40 KB or more on the way. The
-// variance is summed from the centred values in a second pass over the registers, which neither
-// cancels nor reads the row again.
+// wait but the thread's own, and one block a multiprocessor keeps 40 KB or more on the way.
 //
 // The weights' gradients: a thread keeps the sums of its columns over all of its block's rows in
 // registers; the blocks' sums go to the workspace and a second kernel adds them in a fixed order.
@@ -162,7 +160,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
     constexpr int P = Chunk<T>::P;
     constexpr int KEEP = NV <= 2 ? NV : 1;  // chunks whose weights stay in registers
     extern __shared__ uint4 s_ring[];
-    __shared__ float s_part[2][16];
+    __shared__ float s_part[3][2][16];
     const int tid = threadIdx.x, n = blockDim.x;
     const int arrays = a.residual ? 2 : 1, stage = arrays * NV * P * n;
     pdl_wait();
@@ -190,7 +188,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
     for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
         copy_wait(a.stages);
         Eight v[NV];
-        float2 total = both(0.0f);
+        float2 sum2 = both(0.0f), sq2 = both(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * n;
@@ -204,29 +202,40 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
                 if (a.sum) Chunk<T>::store(a.sum + (row * a.chunks + c) * (16 * P), v[i]);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) total = __fadd2_rn(total, v[i].v[j]);
-        }
-        float mean = 0.0f;
-        if (!a.rms) {
-            mean = total.x + total.y;
-            block_add(mean, s_part[0]);
-            mean = __fdiv_rn(mean, (float)(a.chunks * 8));
-        }
-        total = both(0.0f);
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (tid + i * n < a.chunks) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (!a.rms) v[i].v[j] = __fadd2_rn(v[i].v[j], both(-mean));
-                    total = __ffma2_rn(v[i].v[j], v[i].v[j], total);
-                }
+            for (int j = 0; j < 4; ++j) {
+                sum2 = __fadd2_rn(sum2, v[i].v[j]);
+                sq2 = __ffma2_rn(v[i].v[j], v[i].v[j], sq2);
             }
-        // RMS has one sum a row: its two buffers take turns from row to row
-        float sq = total.x + total.y;
-        block_add(sq, s_part[a.rms ? turn : 1]);
+        }
+        float mean = 0.0f, sq = sq2.x + sq2.y, var;
+        if (a.rms) {
+            block_add(sq, s_part[turn][0]);
+            var = sq * a.inv_h;
+        } else {
+            mean = sum2.x + sum2.y;
+            block_add(mean, sq, s_part[turn]);
+            mean = __fdiv_rn(mean, (float)(a.chunks * 8));
+            var = fmaf(-mean, mean, sq * a.inv_h);
+            // The squares' mean less the mean's square loses a bit at most where the mean is below the
+            // deviation; for the rows where it is not, the centred values are summed.
+            if (mean * mean > var) {
+                sq2 = both(0.0f);
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    if (tid + i * n < a.chunks) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 d = __fadd2_rn(v[i].v[j], both(-mean));
+                            sq2 = __ffma2_rn(d, d, sq2);
+                        }
+                    }
+                sq = sq2.x + sq2.y;
+                block_add(sq, s_part[2][0]);
+                var = sq * a.inv_h;
+            }
+        }
         turn ^= 1;
-        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(fmaf(sq, a.inv_h, a.eps)));
+        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
         fetch(row + (int64_t)a.stages * gridDim.x, s);
         if (++s == a.stages) s = 0;
         if (tid == 0) {
@@ -241,7 +250,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
             if (NV > 2) load_weights(i, 0);
             Eight o;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o.v[j] = __ffma2_rn(__fmul2_rn(v[i].v[j], both(rstd)), w[k].v[j], b[k].v[j]);
+            for (int j = 0; j < 4; ++j) o.v[j] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[i].v[j], both(-mean)), both(rstd)), w[k].v[j], b[k].v[j]);
             if (a.y) Chunk<__nv_bfloat16>::store(a.y + (row * a.chunks + c) * 16, o);
             if (a.yq) {
                 // 128 columns are 16 neighbouring lanes, all of them with a chunk or none
