@@ -76,16 +76,18 @@ struct Shape {
     static constexpr int kTail = (FP8 ? 2 * kChunk * 4 : 0) + 16;  // scales and the live tokens' mask
     static constexpr int kStage = 2 * kChunk * kRow + kTail;
     static constexpr int kWarps = kRow == 512 ? 4 : 8;
-    static constexpr int kJoinCols = NH == 1 ? 64 : 32, kJoinRow = kJoinCols + 4;
-    static constexpr int kJoinSums = kWarps * kHeads * kJoinRow * 4, kJoinWeights = kMaxBlocks * kHeads * 4;
+    static constexpr int kJoinCols = DP < 128 ? DP : 128, kJoinRow = kJoinCols + 4;
+    static constexpr int kJoinSums = kWarps * kHeads * kJoinRow * 4, kJoinWeights = 3 * kMaxBlocks * kHeads * 4;
     static constexpr int kJoin = kJoinSums > kJoinWeights ? kJoinSums : kJoinWeights;
-    static constexpr int kFit = (226 * 1024 - kJoin - 2048) / (kWarps * kStage);
-    static constexpr int kStages = kFit < 6 ? kFit : 6;
+    // One stage on the way (64 KB a multiprocessor) while another is read. More in flight fill the same
+    // memory system, but share it less evenly: of 152 blocks with equal runs the fastest then takes
+    // 256 us and the slowest 348 (128 sequences, 2.1 GB; 361 us in all), with two stages 303 and 337 (344).
+    static constexpr int kStages = 2;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kTile = kWarps * kChunk;  // tokens of a tile
     static constexpr int kSmem = kWarps * kStages * kStage + kJoin;
     static constexpr int kPart = kHeads * (DP + 2);  // floats: the heads' sums, maxima and sums of weights
-    static_assert(kStages >= 2, "a stage is filled while another is read");
+    static_assert(kSmem <= 226 * 1024 - 2048, "the ring and the join share what a block may have");
 };
 
 __device__ __forceinline__ void copy16z(uint32_t dst, const void *src, bool live) {
@@ -180,6 +182,12 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
         if (lane >= o) v += u;
     }
     return v;
+}
+
+__device__ __forceinline__ uint32_t add_acq_rel(uint32_t *p, uint32_t v) {
+    uint32_t old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
 }
 
 // The 8 x 8 matrix of 16-bit values with its rows and columns exchanged.
@@ -671,12 +679,10 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
                 const int first = (int)(((seg0 + 1) * blocks - 1) / total), last = (int)((seg1 * blocks - 1) / total);
                 uint32_t *const counter = a.counters + first;  // a block's run has the beginning of one such segment at most
                 __syncthreads();
-                if (tid == 0) {
-                    __threadfence();  // releases what the whole block wrote before the barrier
-                    const uint32_t seen = atomicAdd(counter, 1u);
+                if (tid == 0) {  // releases what the block wrote before the barrier, and acquires what the others did
+                    const uint32_t seen = add_acq_rel(counter, 1u);
                     s_last = seen == (uint32_t)(last - first);
                     if (s_last) *counter = 0;  // as the next call finds it
-                    __threadfence();
                 }
                 __syncthreads();
                 if (s_last) {
@@ -688,33 +694,65 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
                     // only the first block's part can be its second
                     const float *const part0 = part_of(0), *const part1 = a.parts + 2 * (int64_t)(first + 1) * S::kPart;
                     auto at_part = [&](int i) { return i == 0 ? part0 : part1 + 2 * (int64_t)(i - 1) * S::kPart; };
-                    for (int e = tid; e < n * HB; e += S::kThreads) s_join[e] = __ldcg(at_part(e / HB) + HB * DP + e % HB);
+                    // the parts' sums, four columns at a time, sixteen of a thread's on the way
+                    constexpr int ITEMS = (HB * DP / 4 + S::kThreads - 1) / S::kThreads, BATCH = 16 / ITEMS;
+                    float4 x[BATCH][ITEMS], v[ITEMS];
+                    auto fetch = [&](int i0) {
+#pragma unroll
+                        for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+                            for (int j = 0; j < ITEMS; ++j) {
+                                const int e = tid + j * S::kThreads;
+                                x[i][j] = i0 + i < n && e < HB * DP / 4 ? __ldcg(reinterpret_cast<const float4 *>(at_part(i0 + i)) + e) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            }
+                    };
+                    fetch(0);
+                    // meanwhile a weight for every part and head, and the heads' sums
+                    float *const s_max = s_join, *const s_sum = s_join + kMaxBlocks * HB, *const s_by = s_sum + kMaxBlocks * HB;
+                    for (int e = tid; e < n * HB; e += S::kThreads) {
+                        const float *src = at_part(e / HB) + HB * DP + e % HB;
+                        s_max[e] = __ldcg(src);
+                        s_sum[e] = __ldcg(src + HB);
+                    }
+                    __syncthreads();
+                    const int head = tid % HB;
+                    float top = -INFINITY;
+#pragma unroll 8
+                    for (int i = 0; i < n; ++i) top = fmaxf(top, s_max[i * HB + head]);
+                    for (int e = tid; e < n * HB; e += S::kThreads) {  // (kThreads is a multiple of HB: the thread's own head)
+                        const float f = s_max[e] == -INFINITY ? 0.0f : fast_exp2(s_max[e] - top);
+                        s_by[e] = f;
+                        s_sum[e] *= f;
+                    }
                     __syncthreads();
                     if (tid < rows) {
-                        float top = -INFINITY, sum = 0.0f;
-                        for (int i = 0; i < n; ++i) top = fmaxf(top, s_join[i * HB + tid]);
-#pragma unroll 4
-                        for (int i = 0; i < n; ++i) {
-                            const float mi = s_join[i * HB + tid];
-                            const float f = mi == -INFINITY ? 0.0f : fast_exp2(mi - top);
-                            s_join[i * HB + tid] = f;
-                            sum = fmaf(f, __ldcg(at_part(i) + HB * DP + HB + tid), sum);
-                        }
+                        float sum = 0.0f;
+#pragma unroll 8
+                        for (int i = 0; i < n; ++i) sum += s_sum[i * HB + tid];
                         s_lall[tid] = sum > 0.0f ? __fdiv_rn(1.0f, sum) : sum;
                         if (a.lse) a.lse[(int64_t)cp.b * a.QH + h0 + tid] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
                     }
+#pragma unroll
+                    for (int j = 0; j < ITEMS; ++j) v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    for (int i0 = 0; i0 < n; i0 += BATCH) {
+                        if (i0 > 0) fetch(i0);
+#pragma unroll
+                        for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+                            for (int j = 0; j < ITEMS; ++j) {
+                                const int r = (tid + j * S::kThreads) / (DP / 4);
+                                const float f = i0 + i < n && r < HB ? s_by[(i0 + i) * HB + r] : 0.0f;
+                                v[j].x = fmaf(x[i][j].x, f, v[j].x), v[j].y = fmaf(x[i][j].y, f, v[j].y);
+                                v[j].z = fmaf(x[i][j].z, f, v[j].z), v[j].w = fmaf(x[i][j].w, f, v[j].w);
+                            }
+                    }
                     __syncthreads();
-                    for (int e = tid; e < rows * (DP / 2); e += S::kThreads) {
-                        const int r = e / (DP / 2), col = e % (DP / 2) * 2;
-                        if (col >= D) continue;
-                        float2 v = make_float2(0.0f, 0.0f);
-#pragma unroll 8
-                        for (int i = 0; i < n; ++i) {
-                            const float2 x = __ldcg(reinterpret_cast<const float2 *>(at_part(i) + r * DP + col));
-                            v.x = fmaf(x.x, s_join[i * HB + r], v.x);
-                            v.y = fmaf(x.y, s_join[i * HB + r], v.y);
-                        }
-                        *reinterpret_cast<uint32_t *>(out + ((int64_t)r * D + col) * 2) = pack2_bf16(v.x * s_lall[r], v.y * s_lall[r]);
+#pragma unroll
+                    for (int j = 0; j < ITEMS; ++j) {
+                        const int e = tid + j * S::kThreads, r = e / (DP / 4), col = e % (DP / 4) * 4;
+                        if (r < rows && col < D)
+                            *reinterpret_cast<uint2 *>(out + ((int64_t)r * D + col) * 2) =
+                                make_uint2(pack2_bf16(v[j].x * s_lall[r], v[j].y * s_lall[r]), pack2_bf16(v[j].z * s_lall[r], v[j].w * s_lall[r]));
                     }
                     __syncthreads();
                 }
