@@ -39,17 +39,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 // than 2^8: terms up to 2^8 lose nothing in 32 bits, and the scaling is rare.
 constexpr float kSlack = 8.0f;
 
-// t / d for t < 2^31 by a product: mul = ceil(2^(31 + shift) / d), 2^shift >= d.
-struct Divisor {
-    uint32_t mul, shift, d;
-};
-inline Divisor divisor(uint32_t d) {
-    uint32_t s = 0;
-    while ((1ull << s) < d) ++s;
-    return {(uint32_t)(((1ull << (31 + s)) + d - 1) / d), s, d};
-}
-__device__ __forceinline__ uint32_t divide(uint32_t t, const Divisor &v) { return __umulhi(2 * t, v.mul) >> v.shift; }
-
 struct AttnArgs {
     const uint8_t *q;
     int64_t q_stride;  // bytes between tokens

@@ -7,6 +7,17 @@ namespace epd {
 
 constexpr int kMaxHeadDim = 256;
 
+// t / d for t < 2^31 by a product: mul = ceil(2^(31 + shift) / d), 2^shift >= d.
+struct Divisor {
+    uint32_t mul, shift, d;
+};
+inline Divisor divisor(uint32_t d) {
+    uint32_t s = 0;
+    while ((1ull << s) < d) ++s;
+    return {(uint32_t)(((1ull << (31 + s)) + d - 1) / d), s, d};
+}
+__device__ __forceinline__ uint32_t divide(uint32_t t, const Divisor &v) { return __umulhi(2 * t, v.mul) >> v.shift; }
+
 // The largest number of positions that a sequence's pages hold.
 __host__ __device__ inline int64_t cache_positions(const epd_cache_t &c) { return (int64_t)c.max_pages * c.page_size; }
 

@@ -22,7 +22,8 @@ namespace epd {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kBatch = 4;  // passes whose loads are in flight at once
+template <int V>
+constexpr int kBatch = V == 8 ? 4 : 8;  // passes whose loads are in flight at once: 128 bytes a lane
 constexpr unsigned kAll = 0xffffffffu;
 
 struct Turn {
@@ -38,12 +39,23 @@ struct Walk {
     int heads, passes, parts;  // passes: of a warp; parts: warps of a token
 };
 
+// The token and the part of it that a warp has: number `unit` of all parts.
+struct Unit {
+    int t, part;
+    __device__ __forceinline__ Unit(const Divisor &parts) {
+        const uint32_t unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+        t = (int)divide(unit, parts);
+        part = (int)(unit - (uint32_t)t * parts.d);
+    }
+};
+
 struct RotaryArgs {
     const uint8_t *x;
     uint8_t *out;
     int64_t x_token, x_head, out_token, out_head;  // bytes
     const int32_t *positions;
     int T, D;
+    Divisor parts;
     Turn turn;
     Walk walk;
 };
@@ -54,6 +66,7 @@ struct AppendArgs {
     int64_t q_token, k_token, v_token, q_out_token;  // bytes
     const int32_t *positions, *token_seq;
     int T;
+    Divisor parts, page;
     epd_cache_t cache;
     Turn turn;
     Walk queries, rows;  // rows: keys, then values
@@ -183,6 +196,8 @@ __device__ __forceinline__ void store_e4m3(uint8_t *head, const Place<V, INTER> 
 }
 
 // Cosines and sines of chunk p's pairs at a position, times the scale; 1 and 0 past the rotated part.
+// The hardware's sine and cosine of an angle within [-pi, pi] are off by 2^-20.5 at most, a 2000th of a
+// step of the bf16 that they go into.
 template <int V>
 __device__ __forceinline__ void angles(const Turn &t, int p, int position, float (&c)[V], float (&s)[V]) {
     const bool turned = p < t.R / (2 * V);
@@ -192,21 +207,28 @@ __device__ __forceinline__ void angles(const Turn &t, int p, int position, float
         s[i] = 0.0f;
         if (turned) {
             const uint64_t phase = (uint64_t)(int64_t)position * __ldg(t.step + p * V + i);
-            // half turns in [-1, 1)
-            sincospif((float)(int32_t)(phase >> 32) * 4.656612873077392578125e-10f, &s[i], &c[i]);
-            c[i] *= t.scale;
-            s[i] *= t.inverse ? -t.scale : t.scale;
+            const float angle = (float)(int32_t)(phase >> 32) * 1.4629180792671596e-9f;  // pi / 2^31
+            c[i] = __cosf(angle) * t.scale;
+            s[i] = __sinf(angle) * (t.inverse ? -t.scale : t.scale);
         }
     }
 }
 
 template <int V>
 __device__ __forceinline__ void rotate(float (&a)[V], float (&b)[V], const float (&c)[V], const float (&s)[V]) {
+    if constexpr (V == 1) {
+        const float x = a[0], y = b[0];
+        a[0] = x * c[0] - y * s[0];
+        b[0] = x * s[0] + y * c[0];
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const float x = a[i], y = b[i];
-        a[i] = x * c[i] - y * s[i];
-        b[i] = x * s[i] + y * c[i];
+        for (int i = 0; i < V; i += 2) {  // two pairs to an instruction
+            const float2 x = make_float2(a[i], a[i + 1]), y = make_float2(b[i], b[i + 1]);
+            const float2 cc = make_float2(c[i], c[i + 1]), ss = make_float2(s[i], s[i + 1]);
+            const float2 u = __ffma2_rn(x, cc, __fmul2_rn(y, make_float2(-ss.x, -ss.y))), w = __ffma2_rn(x, ss, __fmul2_rn(y, cc));
+            a[i] = u.x, a[i + 1] = u.y;
+            b[i] = w.x, b[i + 1] = w.y;
+        }
     }
 }
 
@@ -215,11 +237,11 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
-    const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t t = unit / a.walk.parts;
+    const Unit unit(a.parts);
+    const int64_t t = unit.t;
     if (t >= a.T) return;
     const int per_pass = 32 >> a.walk.lanes_log, lanes = 1 << a.walk.lanes_log;
-    const int first = (int)(unit - t * a.walk.parts) * a.walk.passes * per_pass + (lane >> a.walk.lanes_log);
+    const int first = unit.part * a.walk.passes * per_pass + (lane >> a.walk.lanes_log);
     const int position = __ldg(a.positions + t);
     const uint8_t *x = a.x + t * a.x_token;
     uint8_t *out = a.out + t * a.out_token;
@@ -227,15 +249,15 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
         const Place<V, INTER> at(p, a.turn.R, a.D);
         float c[V], s[V];
         angles<V>(a.turn, p, position, c, s);
-        for (int i0 = 0; i0 < a.walk.passes; i0 += kBatch) {
-            Raw<V, INTER> raw[kBatch];
+        for (int i0 = 0; i0 < a.walk.passes; i0 += kBatch<V>) {
+            Raw<V, INTER> raw[kBatch<V>];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
+            for (int i = 0; i < kBatch<V>; ++i) {
                 const int n = first + (i0 + i) * per_pass;
                 if (i0 + i < a.walk.passes && n < a.walk.heads) raw[i].load(x + n * a.x_head, at);
             }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
+            for (int i = 0; i < kBatch<V>; ++i) {
                 const int n = first + (i0 + i) * per_pass;
                 if (i0 + i < a.walk.passes && n < a.walk.heads) {
                     float u[V], w[V];
@@ -254,11 +276,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
-    const int parts = a.queries.parts + 2 * a.rows.parts;
-    const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t t = unit / parts;
+    const Unit unit(a.parts);
+    const int64_t t = unit.t;
     if (t >= a.T) return;
-    int part = (int)(unit - t * parts);
+    int part = unit.part;
     const epd_cache_t &kv = a.cache;
     const int D = kv.head_dim;
     const int position = __ldg(a.positions + t);
@@ -266,8 +287,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
     if (seq == -1) return;  // padding
     int page = -1, inside = 0;
     if (seq >= 0 && seq < kv.num_seqs && position >= 0 && position < cache_positions(kv)) {
-        page = __ldg(kv.page_table + seq * kv.table_stride + position / kv.page_size);
-        inside = position % kv.page_size;
+        const int at = (int)divide(position, a.page);
+        page = __ldg(kv.page_table + seq * kv.table_stride + at);
+        inside = position - at * kv.page_size;
     }
     if (page < 0 || page >= kv.num_pages) {
         if (lane == 0) report(a.status, EPD_ERR_CAPACITY);
@@ -275,7 +297,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
     }
     const int lanes_log = a.rows.lanes_log, lanes = 1 << lanes_log, per_pass = 32 >> lanes_log;
     const int p0 = lane & (lanes - 1);
-    constexpr int B = NP == 1 ? kBatch : 1;
+    constexpr int B = NP == 1 ? kBatch<V> : 1;
     // A warp has queries, keys or values only. `src` and the heads of a token's part; put(n, pass's
     // chunks) stores head n.
     auto heads = [&](const uint8_t *src, const Walk &walk, auto is_turned, auto is_held, auto put) {
@@ -363,26 +385,26 @@ inline int pairs_of_chunk(int D, int R, bool inter) {
 }
 
 // `columns` of each of `heads` heads of T tokens in chunks of V pairs. A warp takes several passes
-// over a token's heads, up to twelve, where that leaves 16 warps for each multiprocessor: the sines
-// and cosines are then shared by more heads.
+// over a token's heads, up to three or two batches, where that leaves 16 warps for each
+// multiprocessor: the sines and cosines are then shared by more heads.
 inline Walk walk_of(int T, int heads, int columns, int V) {
     Walk w;
     w.chunks = columns / (2 * V);
     w.lanes_log = 0;
     while ((1 << w.lanes_log) < w.chunks && w.lanes_log < 5) ++w.lanes_log;
     w.heads = heads;
-    const int per_pass = 32 >> w.lanes_log, passes = (heads + per_pass - 1) / per_pass;
+    const int per_pass = 32 >> w.lanes_log, passes = (heads + per_pass - 1) / per_pass, top = V == 8 ? 12 : 16;
     const int64_t share = (int64_t)T * passes / (16 * sm_count());
-    const int most = share < 1 ? 1 : share < 12 ? (int)share : 12;
+    const int most = share < 1 ? 1 : share < top ? (int)share : top;
     w.parts = (passes + most - 1) / most;
     w.passes = w.parts > 0 ? (passes + w.parts - 1) / w.parts : 0;
     return w;
 }
 
 inline epd_status_t grid_of(int T, int parts, int &grid) {
-    const int64_t warps = (int64_t)T * parts, blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    if (blocks > INT32_MAX) return EPD_ERR_UNSUPPORTED;
-    grid = (int)blocks;
+    const int64_t warps = (int64_t)T * parts;
+    if (warps > INT32_MAX - kThreads) return EPD_ERR_UNSUPPORTED;
+    grid = (int)((warps + kThreads / 32 - 1) / (kThreads / 32));
     return EPD_OK;
 }
 
@@ -428,6 +450,7 @@ extern "C" epd_status_t ep_rotary(const void *x, int64_t token_stride, int64_t h
     a.walk = walk_of(T, N, in_place ? R : D, V);
     int grid;
     if (const epd_status_t rc = grid_of(T, a.walk.parts, grid)) return rc;
+    a.parts = divisor(a.walk.parts);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (interleaved)
         return V == 4 ? launch_pdl(rotary_kernel<4, true>, grid, kThreads, 0, st, a)
@@ -475,7 +498,10 @@ extern "C" epd_status_t ep_cache_append(const epd_cache_t *cache, const void *q,
     a.queries = walk_of(T, QH, D, V);
     a.rows = walk_of(T, cache->num_kv_heads, D, V);
     int grid;
-    if (const epd_status_t rc = grid_of(T, a.queries.parts + 2 * a.rows.parts, grid)) return rc;
+    const int parts = a.queries.parts + 2 * a.rows.parts;
+    if (const epd_status_t rc = grid_of(T, parts, grid)) return rc;
+    a.parts = divisor(parts);
+    a.page = divisor(cache->page_size);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (inter) return V == 4 ? launch_append<4, true>(a, grid, st) : launch_append<1, true>(a, grid, st);
     return V == 8 ? launch_append<8, false>(a, grid, st)
