@@ -686,7 +686,7 @@ typedef struct {
  * token_seq is NULL): its keys and values are written to that position's row, its rotated
  * queries to q_out. Prompts and single tokens are the same call. An e4m3 cache takes
  * scale = amax / 448 of the head's fp32 values (1 if amax = 0) and e4m3(value / scale), nearest even.
- * A token of sequence -1 is padding: nothing of it is read or written. A sequence outside
+ * A token of sequence -1 is padding: nothing of it is written. A sequence outside
  * [-1, num_seqs), a position outside the sequence's pages or a page outside [0, num_pages) sets
  * EPD_ERR_CAPACITY, and the token is left out like padding. Two tokens at one position: one of
  * the two is kept for each head.

@@ -1,8 +1,8 @@
 """Rotary positions and the paged cache's append on the GPU against the formulas in 64 bits.
 
 Tolerances: half a step of the output (bf16 2^-8, e4m3 2^-4 of the value or 2^-10 of the scale below
-its smallest normal number) and 2^-20 of |a| + |b| for fp32 arithmetic: the angle is within
-pi 2^-24, the sines within 2^-23, four products and sums of 2^-24 each."""
+its smallest normal number) and 2^-19 of the larger of |a|, |b| for each of the two products in fp32
+arithmetic: the angle is within pi 2^-24, the hardware's sines within 2^-20.5, roundings of 2^-24 each."""
 import pytest
 import torch
 

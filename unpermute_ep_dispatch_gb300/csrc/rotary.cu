@@ -108,7 +108,7 @@ __device__ __forceinline__ uint2 ld8(const void *p) {
 // V == 4 halves as two 8-byte words, V == 1 as one 4-byte word.
 template <int V, bool INTER>
 struct Raw {
-    uint32_t w[V];
+    uint32_t w[V] = {};
     __device__ __forceinline__ void load(const uint8_t *head, const Place<V, INTER> &at) {
         if constexpr (V == 8) {
             const uint4 x = ld16(head + 2 * at.a), y = ld16(head + 2 * at.b);
@@ -284,30 +284,33 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
     const int D = kv.head_dim;
     const int position = __ldg(a.positions + t);
     const int seq = a.token_seq ? __ldg(a.token_seq + t) : (int)t;
-    if (seq == -1) return;  // padding
-    int page = -1, inside = 0;
-    if (seq >= 0 && seq < kv.num_seqs && position >= 0 && position < cache_positions(kv)) {
-        const int at = (int)divide(position, a.page);
-        page = __ldg(kv.page_table + seq * kv.table_stride + at);
-        inside = position - at * kv.page_size;
-    }
-    if (page < 0 || page >= kv.num_pages) {
-        if (lane == 0) report(a.status, EPD_ERR_CAPACITY);
-        return;
-    }
+    // The token's slot in the cache; false where it has none (padding, or out of range).
+    int64_t slot = 0, scale_slot = 0;
+    auto find_slot = [&]() {
+        if (seq == -1) return false;
+        int page = -1, inside = 0;
+        if (seq >= 0 && seq < kv.num_seqs && position >= 0 && position < cache_positions(kv)) {
+            const int at = (int)divide(position, a.page);
+            page = __ldg(kv.page_table + seq * kv.table_stride + at);
+            inside = position - at * kv.page_size;
+        }
+        if (page < 0 || page >= kv.num_pages) {
+            if (lane == 0) report(a.status, EPD_ERR_CAPACITY);
+            return false;
+        }
+        slot = page * kv.page_stride + inside * kv.token_stride;
+        scale_slot = page * kv.scale_page_stride + inside * kv.scale_token_stride;
+        return true;
+    };
     const int lanes_log = a.rows.lanes_log, lanes = 1 << lanes_log, per_pass = 32 >> lanes_log;
     const int p0 = lane & (lanes - 1);
-    constexpr int B = NP == 1 ? kBatch<V> : 1;
     // A warp has queries, keys or values only. `src` and the heads of a token's part; put(n, pass's
     // chunks) stores head n.
     auto heads = [&](const uint8_t *src, const Walk &walk, auto is_turned, auto is_held, auto put) {
-        constexpr bool turned = decltype(is_turned)::value, held = decltype(is_held)::value;
+        constexpr bool turned = decltype(is_turned)::value, scaled = decltype(is_held)::value && FP8;
+        constexpr int B = NP > 1 ? 1 : scaled ? 4 : kBatch<V>;
         const int first = part * walk.passes * per_pass + (lane >> lanes_log);
         float c[NP][V], s[NP][V];
-        if (turned) {
-#pragma unroll
-            for (int q = 0; q < NP; ++q) angles<V>(a.turn, p0 + q * lanes, position, c[q], s[q]);
-        }
         for (int i0 = 0; i0 < walk.passes; i0 += B) {
             Raw<V, INTER> raw[B][NP];
 #pragma unroll
@@ -319,33 +322,53 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
                     if (p0 + q * lanes < walk.chunks)
                         raw[i][q].load(src + (int64_t)n * D * 2, Place<V, INTER>(p0 + q * lanes, a.turn.R, D));
             }
+            if (i0 == 0) {  // with the first values on the way: the slot takes two dependent loads
+                if (turned) {
+#pragma unroll
+                    for (int q = 0; q < NP; ++q) angles<V>(a.turn, p0 + q * lanes, position, c[q], s[q]);
+                }
+                if (!find_slot()) return;
+            }
+            // a batch's scales are found together: each is a chain of exchanges
+            float u[scaled ? B : 1][NP][V], w[scaled ? B : 1][NP][V], scale[B];
+            auto turn = [&](int i, int to) {
+#pragma unroll
+                for (int q = 0; q < NP; ++q) {
+                    raw[i][q].values(u[to][q], w[to][q]);
+                    if (turned) rotate<V>(u[to][q], w[to][q], c[q], s[q]);
+                }
+            };
+            if (scaled) {
+#pragma unroll
+                for (int i = 0; i < B; ++i) {
+                    turn(i, i);
+                    scale[i] = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < NP; ++q) {
+                        float top = 0.0f;
+#pragma unroll
+                        for (int j = 0; j < V; ++j) top = fmaxf(top, fmaxf(fabsf(u[i][q][j]), fabsf(w[i][q][j])));
+                        if (p0 + q * lanes < walk.chunks) scale[i] = fmaxf(scale[i], top);
+                    }
+                }
+#pragma unroll
+                for (int d = 16; d; d >>= 1)
+#pragma unroll
+                    for (int i = 0; i < B; ++i) {
+                        const float other = __shfl_xor_sync(kAll, scale[i], d);
+                        if (d < lanes) scale[i] = fmaxf(scale[i], other);
+                    }
+            }
 #pragma unroll
             for (int i = 0; i < B; ++i) {
-                if (i0 + i >= walk.passes) break;  // the same for the whole warp
                 const int n = first + (i0 + i) * per_pass;
-                float u[NP][V], w[NP][V], scale = 1.0f;
+                if (i0 + i >= walk.passes || n >= walk.heads) continue;
+                if (scaled) scale[i] = scale[i] > 0.0f ? __fdiv_rn(scale[i], 448.0f) : 1.0f;
+                else turn(i, 0);
+                const int k = scaled ? i : 0;
 #pragma unroll
                 for (int q = 0; q < NP; ++q)
-                    if (n < walk.heads && p0 + q * lanes < walk.chunks) {
-                        raw[i][q].values(u[q], w[q]);
-                        if (turned) rotate<V>(u[q], w[q], c[q], s[q]);
-                    }
-                if (held && FP8) {
-                    float amax = 0.0f;
-#pragma unroll
-                    for (int q = 0; q < NP; ++q)
-                        if (n < walk.heads && p0 + q * lanes < walk.chunks) {
-#pragma unroll
-                            for (int j = 0; j < V; ++j) amax = fmaxf(amax, fmaxf(fabsf(u[q][j]), fabsf(w[q][j])));
-                        }
-                    for (int d = lanes >> 1; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, d));
-                    if (amax > 0.0f) scale = __fdiv_rn(amax, 448.0f);
-                }
-                if (n < walk.heads) {
-#pragma unroll
-                    for (int q = 0; q < NP; ++q)
-                        if (p0 + q * lanes < walk.chunks) put(n, Place<V, INTER>(p0 + q * lanes, a.turn.R, D), u[q], w[q], scale);
-                }
+                    if (p0 + q * lanes < walk.chunks) put(n, Place<V, INTER>(p0 + q * lanes, a.turn.R, D), u[k][q], w[k][q], scaled ? scale[i] : 1.0f);
             }
         }
     };
@@ -355,10 +378,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
               [&](int n, const Place<V, INTER> &at, float(&u)[V], float(&w)[V], float) { store_bf16<V, INTER>(out + (int64_t)n * D * 2, at, u, w); });
         return;
     }
-    const int64_t slot = page * kv.page_stride + inside * kv.token_stride;
-    const int64_t scale_slot = page * kv.scale_page_stride + inside * kv.scale_token_stride;
     auto hold = [&](void *base, float *scales) {
-        return [=, &kv](int n, const Place<V, INTER> &at, float(&u)[V], float(&w)[V], float scale) {
+        return [=, &kv, &slot, &scale_slot](int n, const Place<V, INTER> &at, float(&u)[V], float(&w)[V], float scale) {
             const int64_t off = slot + n * kv.head_stride;
             if (FP8) {
                 store_e4m3<V, INTER>(static_cast<uint8_t *>(base) + off, at, u, w, scale);
