@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -71,7 +72,8 @@ _P, _I, _I64, _U32, _SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes
                            ctypes.c_size_t)
 _F = ctypes.c_float
 _ROWS = ctypes.POINTER(ExpertRows)
-_CACHE = ctypes.POINTER(KVCache)
+_CACHE = _P  # a KVCache, or its bytes
+_CACHE_BYTES = struct.Struct("@4iq4P6qP2iq")  # the fields of KVCache
 SIGNATURES = {
     "epd_status_string": (ctypes.c_char_p, [_I]),
     "epd_version": (_I, []),
@@ -1033,9 +1035,17 @@ def _heads(t, name, heads=None, dim=None, tokens=None, device=None):
     return t
 
 
-def _token_rows(t, name, *args, **kw):
+def _token_rows(t, name, heads, dim, tokens, device):
     """_heads whose heads lie next to each other too; returns the tokens' stride."""
-    _heads(t, name, *args, **kw)
+    try:  # the common case, in few attribute look-ups; what fails it is told apart below
+        shape, strides = t.shape, t.stride()
+        if (len(shape) == 3 and shape[0] == tokens and shape[2] == dim == strides[1]
+                and strides[2] == 1 and (heads is None or shape[1] == heads)
+                and t.dtype is torch.bfloat16 and t.get_device() == device.index >= 0):
+            return strides[0] if tokens > 1 else shape[1] * dim
+    except AttributeError:
+        pass
+    _heads(t, name, heads, dim, tokens, device)
     if t.shape[1] > 1 and t.stride(1) != t.shape[2]:
         raise ValueError(f"the heads of a token of {name} must lie next to each other")
     return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
@@ -1080,7 +1090,8 @@ def ep_rotary(x: torch.Tensor, positions: torch.Tensor, steps: torch.Tensor,
 
 
 def _cache(k, v, page_table, k_scale, v_scale):
-    """epd_cache_t of k and v [pages, page_size, kv_heads, dim], page_table [seqs, max_pages]."""
+    """epd_cache_t (its bytes) of k and v [pages, page_size, kv_heads, dim] and page_table [seqs,
+    max_pages], the device, and seqs, kv_heads, dim."""
     dtype = k.dtype if isinstance(k, torch.Tensor) else None
     fp8 = dtype is torch.float8_e4m3fn
     if not fp8 and dtype is not torch.bfloat16:
@@ -1088,38 +1099,49 @@ def _cache(k, v, page_table, k_scale, v_scale):
     shape = k.shape
     if len(shape) != 4:
         raise ValueError("the cache must be [pages, page_size, kv_heads, dim]")
+    dev = k.device
+    index = dev.index
     if not k.is_cuda:
         raise ValueError("the cache must be a CUDA tensor")
-    dev = k.device
     P, rows, KH, D = shape
-    sp, st, sh, sd = k.stride()
-    if not isinstance(v, torch.Tensor) or v.dtype is not dtype or v.shape != shape or v.device != dev:
+    strides = k.stride()
+    if not isinstance(v, torch.Tensor) or v.dtype is not dtype or v.shape != shape or \
+            v.get_device() != index:
         raise ValueError("the values' cache must have the keys' type, shape and device")
-    if v.stride() != (sp, st, sh, sd):
+    if v.stride() != strides:
         raise ValueError("the values' cache must have the keys' strides")
+    sp, st, sh, sd = strides
     if sd != 1 and D > 1:
         raise ValueError("the elements of the cache's heads must lie next to each other")
-    cp = ct = ch = 0
+    kp = vp = cp = ct = ch = 0
     if fp8:
         for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if not isinstance(s, torch.Tensor) or s.dtype is not torch.float32 or \
-                    s.shape != (P, rows, KH) or s.device != dev:
+                    s.shape != shape[:3] or s.get_device() != index:
                 raise ValueError(f"{name} must be a float32 tensor {(P, rows, KH)} on {dev}")
         cp, ct, ch = k_scale.stride()
         if v_scale.stride() != (cp, ct, ch):
             raise ValueError("v_scale must have the strides of k_scale")
+        kp, vp = k_scale.data_ptr(), v_scale.data_ptr()
     elif k_scale is not None or v_scale is not None:
         raise ValueError("a bf16 cache takes no scales")
     if not isinstance(page_table, torch.Tensor) or page_table.dtype is not torch.int32 or \
-            page_table.dim() != 2 or page_table.device != dev or \
-            (page_table.stride(1) != 1 and page_table.shape[1] > 1):
-        raise ValueError(f"page_table must be an int32 tensor [seqs, max_pages] on {dev}, "
-                         "its rows' entries next to each other")
+            page_table.dim() != 2 or page_table.get_device() != index:
+        raise ValueError(f"page_table must be an int32 tensor [seqs, max_pages] on {dev}")
     S, M = page_table.shape
-    return KVCache(EPD_FP8_E4M3 if fp8 else EPD_BF16, KH, D, rows, P, _ptr(k), _ptr(v),
-                   _ptr(k_scale), _ptr(v_scale), sp if P > 1 else 0, st if rows > 1 else 0,
-                   sh if KH > 1 else 0, cp, ct, ch, _ptr(page_table), S, M,
-                   max(M, page_table.stride(0)) if S > 1 else M)
+    ts, tm = page_table.stride()
+    if tm != 1 and M > 1:
+        raise ValueError("the entries of page_table's rows must lie next to each other")
+    if P <= 1:
+        sp = 0
+    if rows <= 1:
+        st = 0
+    if KH <= 1:
+        sh = 0
+    packed = _CACHE_BYTES.pack(EPD_FP8_E4M3 if fp8 else EPD_BF16, KH, D, rows, P, k.data_ptr(),
+                               v.data_ptr(), kp, vp, sp, st, sh, cp, ct, ch,
+                               page_table.data_ptr(), S, M, ts if S > 1 and ts > M else M)
+    return packed, dev, S, KH, D
 
 
 def ep_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -1134,18 +1156,17 @@ def ep_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
     t is position positions[t] (int32) of sequence token_seq[t] (int32, -1 for padding; t where
     None), a row of page_table [seqs, max_pages] int32. q [T, heads, dim] is rotated too. k, v, q
     may be slices of one projection's rows. Returns q_out [T, heads, dim], or None; see epd.h."""
-    c = _cache(k_cache, v_cache, page_table, k_scale, v_scale)
-    dev = k_cache.device
+    cache, dev, S, KH, D = _cache(k_cache, v_cache, page_table, k_scale, v_scale)
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be [T, kv_heads, dim]")
-    T, KH, D = k.shape[0], c.num_kv_heads, c.head_dim
+    T = k.shape[0]
     ks = _token_rows(k, "k", KH, D, T, dev)
     vs = _token_rows(v, "v", KH, D, T, dev)
     _want(positions, "positions", torch.int32, (T,), dev)
     _want(status, "status", torch.int32, (1,), dev)
     if token_seq is not None:
         _want(token_seq, "token_seq", torch.int32, (T,), dev)
-    elif T > c.num_seqs:
+    elif T > S:
         raise ValueError("token_seq is needed for more tokens than sequences")
     R = _steps(steps, D, dev)
     QH = qs = os_ = 0
@@ -1157,7 +1178,7 @@ def ep_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
         os_ = _token_rows(q_out, "q_out", QH, D, T, dev)
     elif q_out is not None:
         raise ValueError("q_out is the rotated q")
-    rc = _launch(load_library().ep_cache_append, dev, ctypes.byref(c), _ptr(q), qs, QH, _ptr(k),
+    rc = _launch(load_library().ep_cache_append, dev, cache, _ptr(q), qs, QH, _ptr(k),
                  ks, _ptr(v), vs, _ptr(positions), _ptr(token_seq), T, _ptr(steps), R,
                  int(bool(interleaved)), float(rotary_scale), _ptr(q_out), os_, _ptr(status),
                  _stream(stream, dev))
@@ -1191,9 +1212,7 @@ def ep_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     lengths[s] (int32) positions of its pages (the last `window` of them where window > 0), the
     cache as in ep_cache_append. softmax_scale: dim ** -0.5 where None. Returns (out [seqs, heads,
     dim] bfloat16, lse [seqs, heads] float32 or None); see epd.h."""
-    c = _cache(k_cache, v_cache, page_table, k_scale, v_scale)
-    dev = k_cache.device
-    B, KH, D = c.num_seqs, c.num_kv_heads, c.head_dim
+    cache, dev, B, KH, D = _cache(k_cache, v_cache, page_table, k_scale, v_scale)
     qs = _token_rows(q, "q", None, D, B, dev)
     QH = q.shape[1]
     if QH < 1 or QH % KH:
@@ -1209,7 +1228,7 @@ def ep_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     if with_lse or lse is not None:
         lse = _out(lse, "lse", torch.float32, (B, QH), dev)
     scale = D ** -0.5 if softmax_scale is None else float(softmax_scale)
-    rc = _launch(lib.ep_decode_attention, dev, ctypes.byref(c), _ptr(q), qs, QH, _ptr(lengths),
+    rc = _launch(lib.ep_decode_attention, dev, cache, _ptr(q), qs, QH, _ptr(lengths),
                  scale, int(window), _ptr(workspace), _ptr(out), _ptr(lse), _ptr(status),
                  _stream(stream, dev))
     _check(rc, "ep_decode_attention")
