@@ -7,11 +7,11 @@
 //   dx = rstd (g - sum g / H - xh sum(g xh) / H) + grad_sum      (RMS: without sum g)
 //   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
 //
-// Bound by HBM: every row is read once and written once. A block owns a row, a thread one
-// 8-column chunk of it (four where the row is wider than 8192), and blocks walk over the rows with
-// the row kept in registers between the sums and the output. Each thread copies its own chunks of the rows to
-// come into its own slots of shared memory (cp.async, up to four rows ahead): no barrier and no
-// wait but the thread's own, and one block a multiprocessor keeps 40 KB or more on the way.
+// Bound by HBM: every row is read once and written once. A block owns a row, a thread 8, 16 or 32 of
+// its columns in chunks of 16 bytes, and blocks walk over the rows with the row kept in registers
+// between the sums and the output. Each thread copies its own chunks of the rows to come into its own
+// slots of shared memory (cp.async, up to four rows ahead): no barrier and no wait but the thread's
+// own, and one block a multiprocessor keeps 40 KB or more on the way.
 //
 // The weights' gradients: a thread keeps the sums of its columns over all of its block's rows in
 // registers; the blocks' sums go to the workspace and a second kernel adds them in a fixed order.
@@ -32,7 +32,7 @@ constexpr unsigned kAll = 0xffffffffu;
 struct NormArgs {
     const uint8_t *x, *residual;
     const float *weight, *bias;
-    int T, chunks, rms, stages;  // chunks: 8-column pieces of a row
+    int T, chunks, rms, stages;  // chunks: 16-byte pieces of a row
     float eps, inv_h;
     uint8_t *sum, *y, *yq;
     float *yscale, *mean, *rstd;
@@ -48,8 +48,22 @@ struct NormGradArgs {
     int64_t block_stride;    // floats between two blocks' sums
 };
 
-__device__ __forceinline__ void copy16(void *dst_smem, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst_smem)), "l"(src) : "memory");
+template <int BYTES>
+__device__ __forceinline__ void copy_piece(uint32_t dst_smem, const void *src) {
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst_smem), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t p) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p) : "memory");
+    return v;
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until the oldest of `stages` groups has landed.
@@ -92,117 +106,123 @@ __device__ __forceinline__ void block_add(float &a, float (&part)[16]) {
     for (int o = 8; o; o >>= 1) a += __shfl_xor_sync(kAll, a, o);
 }
 
-// Eight columns in 32 bits, two to an instruction.
-struct Eight {
-    float2 v[4];
-    __device__ __forceinline__ float get(int j) const { return j & 1 ? v[j >> 1].y : v[j >> 1].x; }
-};
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// 16-byte pieces of an 8-column chunk of T, and the chunk in 32 bits.
+// A chunk in 32 bits, two columns to an instruction: the C columns of 16 bytes of T, so that a warp's
+// loads and stores of x are 512 bytes in a row.
+template <int C>
+struct Columns {
+    float2 v[C / 2];
+};
+
+template <int C>
+__device__ __forceinline__ void unpack_bf16(uint32_t p, Columns<C> &f) {
+    uint32_t u[C / 2];
+    if constexpr (C == 8) {
+        const uint4 x = lds16(p);
+        u[0] = x.x, u[1] = x.y, u[2] = x.z, u[3] = x.w;
+    } else {
+        const uint2 x = lds8(p);
+        u[0] = x.x, u[1] = x.y;
+    }
+#pragma unroll
+    for (int j = 0; j < C / 2; ++j) f.v[j] = make_float2(lo_bf16(u[j]), hi_bf16(u[j]));
+}
+template <int C>
+__device__ __forceinline__ void store_bf16(uint8_t *p, const Columns<C> &f) {
+    if constexpr (C == 8)
+        st16(p, make_uint4(pack2_bf16(f.v[0].x, f.v[0].y), pack2_bf16(f.v[1].x, f.v[1].y), pack2_bf16(f.v[2].x, f.v[2].y), pack2_bf16(f.v[3].x, f.v[3].y)));
+    else
+        *reinterpret_cast<uint2 *>(p) = make_uint2(pack2_bf16(f.v[0].x, f.v[0].y), pack2_bf16(f.v[1].x, f.v[1].y));
+}
+
 template <typename T>
 struct Chunk;
 template <>
 struct Chunk<__nv_bfloat16> {
-    static constexpr int P = 1;
-    static __device__ __forceinline__ void unpack(const uint4 *slot, int, Eight &f) {
-        const uint4 w = slot[0];
-        f.v[0] = make_float2(lo_bf16(w.x), hi_bf16(w.x));
-        f.v[1] = make_float2(lo_bf16(w.y), hi_bf16(w.y));
-        f.v[2] = make_float2(lo_bf16(w.z), hi_bf16(w.z));
-        f.v[3] = make_float2(lo_bf16(w.w), hi_bf16(w.w));
-    }
-    static __device__ __forceinline__ void store(uint8_t *p, const Eight &f) {
-        st16(p, make_uint4(pack2_bf16(f.v[0].x, f.v[0].y), pack2_bf16(f.v[1].x, f.v[1].y),
-                           pack2_bf16(f.v[2].x, f.v[2].y), pack2_bf16(f.v[3].x, f.v[3].y)));
-    }
+    static constexpr int C = 8;
+    static __device__ __forceinline__ void unpack(uint32_t p, Columns<8> &f) { unpack_bf16(p, f); }
+    static __device__ __forceinline__ void store(uint8_t *p, const Columns<8> &f) { store_bf16(p, f); }
 };
 template <>
 struct Chunk<float> {
-    static constexpr int P = 2;
-    static __device__ __forceinline__ void unpack(const uint4 *slot, int stride, Eight &f) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint4 w = slot[h * stride];
-            f.v[2 * h] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
-            f.v[2 * h + 1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
-        }
+    static constexpr int C = 4;
+    static __device__ __forceinline__ void unpack(uint32_t p, Columns<4> &f) {
+        const uint4 w = lds16(p);
+        f.v[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+        f.v[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
     }
-    static __device__ __forceinline__ void store(uint8_t *p, const Eight &f) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            st16(p + 16 * h, make_uint4(__float_as_uint(f.v[2 * h].x), __float_as_uint(f.v[2 * h].y),
-                                        __float_as_uint(f.v[2 * h + 1].x), __float_as_uint(f.v[2 * h + 1].y)));
+    static __device__ __forceinline__ void store(uint8_t *p, const Columns<4> &f) {
+        st16(p, make_uint4(__float_as_uint(f.v[0].x), __float_as_uint(f.v[0].y), __float_as_uint(f.v[1].x), __float_as_uint(f.v[1].y)));
     }
 };
 
-// Starts the copy of this thread's chunks of one row of `src` into its slots [NV][P] of `at`
-// (slots of one thread lie blockDim.x apart).
-template <typename T, int NV>
-__device__ __forceinline__ void fetch_row(uint4 *at, const uint8_t *src, int64_t row, int chunks) {
-    constexpr int P = Chunk<T>::P;
-    const uint8_t *p = src + (row * chunks + threadIdx.x) * (16 * P);
+// Starts the copy of this thread's chunks of a row, BYTES each, into its slots of `at` (chunk i of
+// thread t at (i * blockDim.x + t) * BYTES).
+template <int BYTES, int NV>
+__device__ __forceinline__ void fetch_row(uint32_t at, const uint8_t *src, int64_t row, int chunks) {
+    const int n = blockDim.x, tid = threadIdx.x;
+    const uint8_t *p = src + (row * chunks + tid) * BYTES;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        if ((int)(threadIdx.x + i * blockDim.x) < chunks) {
-#pragma unroll
-            for (int h = 0; h < P; ++h) copy16(at + (i * P + h) * blockDim.x, p + i * blockDim.x * (16 * P) + 16 * h);
-        }
+        if (tid + i * n < chunks) copy_piece<BYTES>(at + (i * n + tid) * BYTES, p + i * n * BYTES);
 }
 
-__device__ __forceinline__ void load8(const float *p, int c, Eight &f, float none) {
+template <int C>
+__device__ __forceinline__ void load_floats(const float *p, int c, Columns<C> &f, float none) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f.v[j] = p ? __ldg(reinterpret_cast<const float2 *>(p + 8 * (int64_t)c) + j) : both(none);
+    for (int j = 0; j < C / 2; ++j) f.v[j] = p ? __ldg(reinterpret_cast<const float2 *>(p + C * (int64_t)c) + j) : both(none);
 }
 
 template <typename T, int NV>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
-    constexpr int P = Chunk<T>::P;
-    constexpr int KEEP = NV <= 2 ? NV : 1;  // chunks whose weights stay in registers
-    extern __shared__ uint4 s_ring[];
+    constexpr int C = Chunk<T>::C;
+    constexpr int KEEP = NV * C <= 16 ? NV : 1;  // chunks whose weights stay in registers
+    extern __shared__ uint4 s_dyn[];
+    const uint32_t s_ring = smem_addr(s_dyn);
     __shared__ float s_part[3][2][16];
     const int tid = threadIdx.x, n = blockDim.x;
-    const int arrays = a.residual ? 2 : 1, stage = arrays * NV * P * n;
+    const int stage = (a.residual ? 2 : 1) * NV * n * 16;
     pdl_wait();
     pdl_trigger();
-    uint4 *const mine = s_ring + tid;
     auto fetch = [&](int64_t row, int s) {
         if (row < a.T) {
-            fetch_row<T, NV>(mine + s * stage, a.x, row, a.chunks);
-            if (a.residual) fetch_row<T, NV>(mine + s * stage + NV * P * n, a.residual, row, a.chunks);
+            fetch_row<16, NV>(s_ring + s * stage, a.x, row, a.chunks);
+            if (a.residual) fetch_row<16, NV>(s_ring + s * stage + NV * n * 16, a.residual, row, a.chunks);
         }
         copy_commit();
     };
     for (int s = 0; s < a.stages; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
-    Eight w[KEEP], b[KEEP];
+    Columns<C> w[KEEP], b[KEEP];
     auto load_weights = [&](int i, int k) {
         if (tid + i * n >= a.chunks) return;
-        load8(a.weight, tid + i * n, w[k], 1.0f);
-        load8(a.bias, tid + i * n, b[k], 0.0f);
+        load_floats(a.weight, tid + i * n, w[k], 1.0f);
+        load_floats(a.bias, tid + i * n, b[k], 0.0f);
     };
-    if (NV <= 2) {
+    if (KEEP == NV) {
 #pragma unroll
         for (int i = 0; i < KEEP; ++i) load_weights(i, i);
     }
     int s = 0, turn = 0;
     for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
         copy_wait(a.stages);
-        Eight v[NV];
+        Columns<C> v[NV];
         float2 sum2 = both(0.0f), sq2 = both(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * n;
             if (c >= a.chunks) continue;
-            Chunk<T>::unpack(mine + s * stage + i * P * n, n, v[i]);
+            const uint32_t slot = s_ring + s * stage + c * 16;
+            Chunk<T>::unpack(slot, v[i]);
             if (a.residual) {
-                Eight r;
-                Chunk<T>::unpack(mine + s * stage + (NV + i) * P * n, n, r);
+                Columns<C> r;
+                Chunk<T>::unpack(slot + NV * n * 16, r);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[i].v[j] = __fadd2_rn(v[i].v[j], r.v[j]);
-                if (a.sum) Chunk<T>::store(a.sum + (row * a.chunks + c) * (16 * P), v[i]);
+                for (int j = 0; j < C / 2; ++j) v[i].v[j] = __fadd2_rn(v[i].v[j], r.v[j]);
+                if (a.sum) Chunk<T>::store(a.sum + (row * a.chunks + c) * 16, v[i]);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < C / 2; ++j) {
                 sum2 = __fadd2_rn(sum2, v[i].v[j]);
                 sq2 = __ffma2_rn(v[i].v[j], v[i].v[j], sq2);
             }
@@ -214,7 +234,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
         } else {
             mean = sum2.x + sum2.y;
             block_add(mean, sq, s_part[turn]);
-            mean = __fdiv_rn(mean, (float)(a.chunks * 8));
+            mean = __fdiv_rn(mean, (float)(a.chunks * C));
             var = fmaf(-mean, mean, sq * a.inv_h);
             // The squares' mean less the mean's square loses a bit at most where the mean is below the
             // deviation; for the rows where it is not, the centred values are summed.
@@ -224,7 +244,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
                 for (int i = 0; i < NV; ++i)
                     if (tid + i * n < a.chunks) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
+                        for (int j = 0; j < C / 2; ++j) {
                             const float2 d = __fadd2_rn(v[i].v[j], both(-mean));
                             sq2 = __ffma2_rn(d, d, sq2);
                         }
@@ -246,32 +266,34 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * n;
             if (c >= a.chunks) continue;
-            const int k = NV <= 2 ? i : 0;
-            if (NV > 2) load_weights(i, 0);
-            Eight o;
+            const int k = KEEP == NV ? i : 0;
+            if (KEEP != NV) load_weights(i, 0);
+            Columns<C> o;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o.v[j] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[i].v[j], both(-mean)), both(rstd)), w[k].v[j], b[k].v[j]);
-            if (a.y) Chunk<__nv_bfloat16>::store(a.y + (row * a.chunks + c) * 16, o);
+            for (int j = 0; j < C / 2; ++j) o.v[j] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[i].v[j], both(-mean)), both(rstd)), w[k].v[j], b[k].v[j]);
+            if (a.y) store_bf16(a.y + (row * a.chunks + c) * (2 * C), o);
             if (a.yq) {
-                // 128 columns are 16 neighbouring lanes, all of them with a chunk or none
-                const unsigned half = (tid & 16) ? 0xffff0000u : 0x0000ffffu;
-                float f[8], amax = 0.0f;
+                // 128 columns are 16 or 32 neighbouring lanes, all of them with a chunk or none
+                const unsigned group = C == 4 ? kAll : (tid & 16) ? 0xffff0000u : 0x0000ffffu;
+                float f[C], amax = 0.0f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    f[j] = o.get(j);
+                for (int j = 0; j < C; ++j) {
+                    f[j] = j & 1 ? o.v[j / 2].y : o.v[j / 2].x;
                     amax = fmaxf(amax, fabsf(f[j]));
                 }
 #pragma unroll
-                for (int d = 8; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half, amax, d));
+                for (int d = 64 / C; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, d));
                 const float scale = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
                 divide_all(f, scale);
-                uint32_t q[4];
+                uint32_t q[C / 4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    q[j] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * j], f[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
-                *reinterpret_cast<uint2 *>(a.yq + (row * a.chunks + c) * 8) =
-                    make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-                if ((c & 15) == 0) a.yscale[row * (a.chunks >> 4) + (c >> 4)] = scale;
+                for (int j = 0; j < C / 4; ++j)
+                    q[j] = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * j], f[4 * j + 1]), __NV_SATFINITE, __NV_E4M3) |
+                           (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f[4 * j + 2], f[4 * j + 3]), __NV_SATFINITE, __NV_E4M3) << 16;
+                uint8_t *const out = a.yq + (row * a.chunks + c) * C;
+                if constexpr (C == 8) *reinterpret_cast<uint2 *>(out) = make_uint2(q[0], q[1]);
+                else *reinterpret_cast<uint32_t *>(out) = q[0];
+                if (c % (128 / C) == 0) a.yscale[row * (a.chunks / (128 / C)) + c / (128 / C)] = scale;
             }
         }
     }
@@ -279,62 +301,63 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
 
 template <typename T, int NV>
 __global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormGradArgs a) {
-    constexpr int P = Chunk<T>::P;
-    constexpr int KEEP = NV <= 2 ? NV : 1;
-    extern __shared__ uint4 s_ring[];
+    constexpr int C = Chunk<T>::C;
+    constexpr int KEEP = NV * C <= 16 ? NV : 1;
+    extern __shared__ uint4 s_dyn[];
+    const uint32_t s_ring = smem_addr(s_dyn);
     __shared__ float s_part[2][2][16];
+    // every warp has a row's rstd and mean copied for itself (as plain loads a row ahead the compiler
+    // put them where their latency showed: 8192 x 7168 took 111 us)
+    __shared__ uint2 s_statistics[4][16];
     const int tid = threadIdx.x, n = blockDim.x;
-    const int stage = NV * (1 + (a.grad_sum ? 2 : 1) * P) * n;
+    const uint32_t statistics = smem_addr(&s_statistics[0][tid >> 5]);
+    // a stage: x, grad_sum (if any), dy
+    const int dy_off = (a.grad_sum ? 2 : 1) * NV * n * 16, stage = dy_off + NV * n * (2 * C);
     pdl_wait();
     pdl_trigger();
-    uint4 *const mine = s_ring + tid;
     auto fetch = [&](int64_t row, int s) {
         if (row < a.T) {
-            fetch_row<__nv_bfloat16, NV>(mine + s * stage, a.dy, row, a.chunks);
-            fetch_row<T, NV>(mine + s * stage + NV * n, a.x, row, a.chunks);
-            if (a.grad_sum) fetch_row<T, NV>(mine + s * stage + NV * (1 + P) * n, a.grad_sum, row, a.chunks);
+            const uint32_t at = s_ring + s * stage;
+            fetch_row<16, NV>(at, a.x, row, a.chunks);
+            if (a.grad_sum) fetch_row<16, NV>(at + NV * n * 16, a.grad_sum, row, a.chunks);
+            fetch_row<2 * C, NV>(at + dy_off, a.dy, row, a.chunks);
+            const int lane = tid & 31;
+            if (lane < (a.rms ? 1 : 2)) copy_piece<4>(statistics + s * (16 * 8) + lane * 4, (lane ? a.mean : a.rstd) + row);
         }
         copy_commit();
     };
     for (int s = 0; s < a.stages; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
-    Eight w[KEEP], dw[NV] = {}, db[NV] = {};
-    if (NV <= 2) {
+    Columns<C> w[KEEP], dw[NV] = {}, db[NV] = {};
+    if (KEEP == NV) {
 #pragma unroll
         for (int i = 0; i < KEEP; ++i)
-            if (tid + i * n < a.chunks) load8(a.weight, tid + i * n, w[i], 1.0f);
+            if (tid + i * n < a.chunks) load_floats(a.weight, tid + i * n, w[i], 1.0f);
     }
-    // a row's statistics are loaded a row ahead
-    float next_rstd = 0.0f, next_mean = 0.0f;
-    auto statistics = [&](int64_t row) {
-        if (row >= a.T) return;
-        next_rstd = __ldg(a.rstd + row);
-        if (!a.rms) next_mean = __ldg(a.mean + row);
-    };
-    statistics(blockIdx.x);
     int s = 0, turn = 0;
     for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x) {
-        const float rstd = next_rstd, mean = next_mean;
-        statistics(row + gridDim.x);
         copy_wait(a.stages);
-        const uint4 *const at = mine + s * stage;
-        auto read = [&](int i, Eight &dy, Eight &xh) {
-            Chunk<__nv_bfloat16>::unpack(at + i * n, n, dy);
-            Chunk<T>::unpack(at + (NV + i * P) * n, n, xh);
+        __syncwarp();  // the statistics are the warp's
+        const uint32_t at = s_ring + s * stage;
+        const uint2 st = lds8(statistics + s * (16 * 8));
+        const float rstd = __uint_as_float(st.x), mean = a.rms ? 0.0f : __uint_as_float(st.y);
+        auto read = [&](int c, Columns<C> &dy, Columns<C> &xh) {
+            unpack_bf16(at + dy_off + c * (2 * C), dy);
+            Chunk<T>::unpack(at + c * 16, xh);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) xh.v[j] = __fmul2_rn(__fadd2_rn(xh.v[j], both(-mean)), both(rstd));
+            for (int j = 0; j < C / 2; ++j) xh.v[j] = __fmul2_rn(__fadd2_rn(xh.v[j], both(-mean)), both(rstd));
         };
-        // a wide row's chunks are unpacked again for the second pass: four would not stay in registers
-        Eight g[KEEP], xh[KEEP];
+        // a wide row's chunks are unpacked again for the second pass: they would not stay in registers
+        Columns<C> g[KEEP], xh[KEEP];
         float2 sg2 = both(0.0f), sgx2 = both(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * n;
             if (c >= a.chunks) continue;
-            const int k = NV <= 2 ? i : 0;
-            if (NV > 2) load8(a.weight, c, w[k], 1.0f);
-            read(i, g[k], xh[k]);
+            const int k = KEEP == NV ? i : 0;
+            if (KEEP != NV) load_floats(a.weight, c, w[k], 1.0f);
+            read(c, g[k], xh[k]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < C / 2; ++j) {
                 dw[i].v[j] = __ffma2_rn(g[k].v[j], xh[k].v[j], dw[i].v[j]);
                 db[i].v[j] = __fadd2_rn(db[i].v[j], g[k].v[j]);
                 g[k].v[j] = __fmul2_rn(g[k].v[j], w[k].v[j]);
@@ -351,34 +374,43 @@ __global__ void __launch_bounds__(kNormThreads) norm_backward_kernel(NormGradArg
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * n;
             if (c >= a.chunks) continue;
-            const int k = NV <= 2 ? i : 0;
-            if (NV > 2) {
-                load8(a.weight, c, w[k], 1.0f);
-                read(i, g[k], xh[k]);
+            const int k = KEEP == NV ? i : 0;
+            if (KEEP != NV) {
+                load_floats(a.weight, c, w[k], 1.0f);
+                read(c, g[k], xh[k]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) g[k].v[j] = __fmul2_rn(g[k].v[j], w[k].v[j]);
+                for (int j = 0; j < C / 2; ++j) g[k].v[j] = __fmul2_rn(g[k].v[j], w[k].v[j]);
             }
-            Eight o;
+            Columns<C> o;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < C / 2; ++j)
                 o.v[j] = __ffma2_rn(xh[k].v[j], both(by_x), __ffma2_rn(g[k].v[j], both(rstd), both(by_1)));
             if (a.grad_sum) {
-                Eight r;
-                Chunk<T>::unpack(at + (NV * (1 + P) + i * P) * n, n, r);
+                Columns<C> r;
+                Chunk<T>::unpack(at + NV * n * 16 + c * 16, r);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o.v[j] = __fadd2_rn(o.v[j], r.v[j]);
+                for (int j = 0; j < C / 2; ++j) o.v[j] = __fadd2_rn(o.v[j], r.v[j]);
             }
-            Chunk<T>::store(a.dx + (row * a.chunks + c) * (16 * P), o);
+            Chunk<T>::store(a.dx + (row * a.chunks + c) * 16, o);
         }
         fetch(row + (int64_t)a.stages * gridDim.x, s);
         if (++s == a.stages) s = 0;
     }
+    float *const outs[2] = {a.dweight, a.dbias};
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = tid + i * n;
-        if (c >= a.chunks) continue;
-        if (a.dweight) Chunk<float>::store(reinterpret_cast<uint8_t *>(a.dweight + blockIdx.x * a.block_stride + 8 * (int64_t)c), dw[i]);
-        if (a.dbias) Chunk<float>::store(reinterpret_cast<uint8_t *>(a.dbias + blockIdx.x * a.block_stride + 8 * (int64_t)c), db[i]);
+    for (int k = 0; k < 2; ++k) {
+        if (!outs[k]) continue;
+        float *const out = outs[k] + blockIdx.x * a.block_stride;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = tid + i * n;
+            if (c >= a.chunks) continue;
+#pragma unroll
+            for (int j = 0; j < C / 4; ++j) {
+                const float2 p = k ? db[i].v[2 * j] : dw[i].v[2 * j], q = k ? db[i].v[2 * j + 1] : dw[i].v[2 * j + 1];
+                *reinterpret_cast<float4 *>(out + C * (int64_t)c + 4 * j) = make_float4(p.x, p.y, q.x, q.y);
+            }
+        }
     }
 }
 
@@ -419,17 +451,16 @@ __global__ void __launch_bounds__(kReduceThreads) norm_reduce_kernel(const float
     }
 }
 
-// Chunks of a thread, threads of a block (a multiple of 32) and blocks of a multiprocessor: one chunk
-// where that is a warp or two, two up to 512 threads (the sums over the block and the loop cost
-// every warp the same, whatever it holds), else four.
+// Columns of a thread, threads of a block (a multiple of 32) and blocks of a multiprocessor: 8 columns
+// where that is a warp or two, 16 up to 512 threads (the sums over the block and the loop cost
+// every warp the same, whatever it holds: 8192 x 2048 bf16 with 8 took 20.8 us, with 16 15.0), else 32.
 struct NormShape {
-    int nv, threads, per_sm;
+    int columns, threads, per_sm;
 };
 inline NormShape norm_shape(int H) {
     NormShape s;
-    const int chunks = H / 8;
-    s.nv = chunks <= 64 ? 1 : chunks <= 2 * kNormThreads ? 2 : 4;
-    s.threads = ((chunks + s.nv - 1) / s.nv + 31) / 32 * 32;
+    s.columns = H <= 512 ? 8 : H <= 16 * kNormThreads ? 16 : 32;
+    s.threads = ((H + s.columns - 1) / s.columns + 31) / 32 * 32;
     s.per_sm = kNormThreads / s.threads;  // by the kernels' registers
     return s;
 }
@@ -477,7 +508,7 @@ extern "C" epd_status_t ep_layer_norm(const void *x, epd_dtype_t dtype, const vo
     a.weight = weight;
     a.bias = bias;
     a.T = T;
-    a.chunks = H / 8;
+    a.chunks = H / (dtype == EPD_F32 ? 4 : 8);
     a.rms = kind == EPD_NORM_RMS;
     a.eps = eps;
     a.inv_h = 1.0f / (float)H;
@@ -489,16 +520,15 @@ extern "C" epd_status_t ep_layer_norm(const void *x, epd_dtype_t dtype, const vo
     a.rstd = rstd;
     const NormShape s = norm_shape(H);
     const int most = sm_count() * s.per_sm, grid = T < most ? T : most;
-    const size_t item = dtype == EPD_F32 ? 2 : 1;
-    const size_t stage = (size_t)(residual ? 2 : 1) * s.nv * item * s.threads * 16;
+    const size_t stage = (size_t)(residual ? 2 : 1) * s.threads * s.columns * (dtype == EPD_F32 ? 4 : 2);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (dtype == EPD_F32)
-        return s.nv == 1   ? launch_rows<norm_kernel<float, 1>>(a, s, grid, stage, st)
-               : s.nv == 2 ? launch_rows<norm_kernel<float, 2>>(a, s, grid, stage, st)
-                           : launch_rows<norm_kernel<float, 4>>(a, s, grid, stage, st);
-    return s.nv == 1   ? launch_rows<norm_kernel<__nv_bfloat16, 1>>(a, s, grid, stage, st)
-           : s.nv == 2 ? launch_rows<norm_kernel<__nv_bfloat16, 2>>(a, s, grid, stage, st)
-                       : launch_rows<norm_kernel<__nv_bfloat16, 4>>(a, s, grid, stage, st);
+        return s.columns == 8    ? launch_rows<norm_kernel<float, 2>>(a, s, grid, stage, st)
+               : s.columns == 16 ? launch_rows<norm_kernel<float, 4>>(a, s, grid, stage, st)
+                                 : launch_rows<norm_kernel<float, 8>>(a, s, grid, stage, st);
+    return s.columns == 8    ? launch_rows<norm_kernel<__nv_bfloat16, 1>>(a, s, grid, stage, st)
+           : s.columns == 16 ? launch_rows<norm_kernel<__nv_bfloat16, 2>>(a, s, grid, stage, st)
+                             : launch_rows<norm_kernel<__nv_bfloat16, 4>>(a, s, grid, stage, st);
 }
 
 extern "C" size_t epd_norm_workspace_bytes(int hidden) {
@@ -525,7 +555,10 @@ extern "C" epd_status_t ep_layer_norm_backward(const void *dy, const void *x, ep
     if (T == 0 && !sums) return EPD_OK;
     const NormShape s = norm_shape(H);
     const int sms = sm_count() < kNormMaxSms ? sm_count() : kNormMaxSms;
-    const int most = sms * s.per_sm, grid = T < 1 ? 1 : T < most ? T : most;
+    // Past two blocks a multiprocessor, four rows a block at least: what the blocks sum up is added
+    // afterwards (4096 x 128: 2432 blocks 12.3 us, 1024 7.2; 333 x 1032: 304 blocks 5.4 us, 84 6.0).
+    const int most = sms * s.per_sm, quarter = (T + 3) / 4, few = T < 2 * sms ? T : 2 * sms;
+    const int want = !sums ? T : quarter > few ? quarter : few, grid = want < 1 ? 1 : want < most ? want : most;
     NormGradArgs a;
     a.dy = static_cast<const uint8_t *>(dy);
     a.x = static_cast<const uint8_t *>(x);
@@ -534,7 +567,7 @@ extern "C" epd_status_t ep_layer_norm_backward(const void *dy, const void *x, ep
     a.mean = mean;
     a.rstd = rstd;
     a.T = T;
-    a.chunks = H / 8;
+    a.chunks = H / (dtype == EPD_F32 ? 4 : 8);
     a.rms = kind == EPD_NORM_RMS;
     a.inv_h = 1.0f / (float)H;
     a.dx = static_cast<uint8_t *>(dx);
@@ -543,18 +576,17 @@ extern "C" epd_status_t ep_layer_norm_backward(const void *dy, const void *x, ep
     a.block_stride = grid == 1 ? 0 : 2 * (int64_t)H;
     a.dweight = !dweight ? nullptr : grid == 1 ? dweight : part;
     a.dbias = !dbias ? nullptr : grid == 1 ? dbias : part + H;
-    const size_t item = dtype == EPD_F32 ? 2 : 1;
-    const size_t stage = (1 + (grad_sum ? 2 : 1) * item) * s.nv * s.threads * 16;
+    const size_t stage = (size_t)s.threads * s.columns * (2 + (grad_sum ? 2 : 1) * (dtype == EPD_F32 ? 4 : 2));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     epd_status_t rc;
     if (dtype == EPD_F32)
-        rc = s.nv == 1   ? launch_rows<norm_backward_kernel<float, 1>>(a, s, grid, stage, st)
-             : s.nv == 2 ? launch_rows<norm_backward_kernel<float, 2>>(a, s, grid, stage, st)
-                         : launch_rows<norm_backward_kernel<float, 4>>(a, s, grid, stage, st);
+        rc = s.columns == 8    ? launch_rows<norm_backward_kernel<float, 2>>(a, s, grid, stage, st)
+             : s.columns == 16 ? launch_rows<norm_backward_kernel<float, 4>>(a, s, grid, stage, st)
+                               : launch_rows<norm_backward_kernel<float, 8>>(a, s, grid, stage, st);
     else
-        rc = s.nv == 1   ? launch_rows<norm_backward_kernel<__nv_bfloat16, 1>>(a, s, grid, stage, st)
-             : s.nv == 2 ? launch_rows<norm_backward_kernel<__nv_bfloat16, 2>>(a, s, grid, stage, st)
-                         : launch_rows<norm_backward_kernel<__nv_bfloat16, 4>>(a, s, grid, stage, st);
+        rc = s.columns == 8    ? launch_rows<norm_backward_kernel<__nv_bfloat16, 1>>(a, s, grid, stage, st)
+             : s.columns == 16 ? launch_rows<norm_backward_kernel<__nv_bfloat16, 2>>(a, s, grid, stage, st)
+                               : launch_rows<norm_backward_kernel<__nv_bfloat16, 4>>(a, s, grid, stage, st);
     if (rc != EPD_OK || !sums || grid == 1) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((H + 31) / 32), dweight && dbias ? 2 : 1);
