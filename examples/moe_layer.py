@@ -6,6 +6,11 @@ between them), the combine, and the backward pass of all of it, in libepd's oper
 for a small batch: the low-latency dispatch casts the tokens to e4m3 rectangles, the first
 product reads them with their scales, the second runs in bf16.
 
+Around them: ``MoEBlock`` puts a norm (with the residual in it) ahead of the training layer,
+and ``attention_step`` is the other half of a block's decode step -- norm, projection, rotary
+positions and the append to the paged cache, attention over it, output projection and residual --
+so that ``block_decode_step`` is a whole block in the library's operators.
+
     python examples/moe_layer.py [--tokens 4096] [--hidden 4096] [--experts 64] [--topk 6]
 """
 from __future__ import annotations
@@ -32,6 +37,26 @@ class _NoSecondDerivative(torch.autograd.Function):
     @staticmethod
     def backward(ctx, *grads):
         raise RuntimeError("the gradients of the expert operators have no derivative")
+
+
+class _Norm(torch.autograd.Function):
+    """(norm(x + residual), x + residual): root-mean-square norm with fp32 weights."""
+
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps):
+        d = epd.ep_layer_norm(x, weight, residual=residual, eps=eps, kind="rms", with_stats=True)
+        ctx.save_for_backward(d["sum"], weight, d["rstd"])
+        return d["y"], d["sum"]
+
+    @staticmethod
+    def backward(ctx, dy, dsum):
+        s, weight, rstd = ctx.saved_tensors
+        dx, dweight, _ = epd.ep_layer_norm_backward(dy.contiguous(), s, weight, rstd, kind="rms",
+                                                    grad_sum=dsum.contiguous())
+        grads = dx, dweight
+        if torch.is_grad_enabled():  # create_graph
+            grads = _NoSecondDerivative.apply(torch.empty(0, requires_grad=True), *grads)
+        return grads[0], grads[0], grads[1], None
 
 
 class _Experts(torch.autograd.Function):
@@ -103,6 +128,21 @@ class MoELayer(torch.nn.Module):
         return _Experts.apply(x, logits, self.w1, self.b1, self.w2, self.b2, self)
 
 
+class MoEBlock(torch.nn.Module):
+    """The MoE half of a block: the residual stream joined and normed, then the layer. Returns the
+    layer's rows and the residual stream, which the next norm adds up."""
+
+    def __init__(self, hidden, *args, eps=1e-5, device="cuda", **kw):
+        super().__init__()
+        self.weight = torch.nn.Parameter(torch.ones(hidden, device=device))
+        self.eps = eps
+        self.layer = MoELayer(hidden, *args, device=device, **kw)
+
+    def forward(self, x, residual):
+        y, stream = _Norm.apply(x, residual, self.weight, self.eps)
+        return self.layer(y), stream
+
+
 def quantize_blocks(w):
     """e4m3 weights [E, N, K] with one fp32 scale per 128 x 128 block (N, K multiples of 128)."""
     E, N, K = w.shape
@@ -126,6 +166,33 @@ def decode_step(x, logits, w1_q, w1_scale, w2, topk, workspace, status, rows_per
                                 activation="swiglu")
     eo, _ = epd.ep_expert_matmul(h, w2, count, status)
     return epd.ep_unpermute(eo.view(E * rows, H), index, weights, status)
+
+
+def attention_step(x, norm_weight, w_qkv, w_o, heads, kv_heads, cache, lengths, positions, steps,
+                   workspace, status, eps=1e-5):
+    """The attention half of a block for one new token of every sequence: x [B, H] bf16, the
+    residual stream. w_qkv [(heads + 2 kv_heads) D, H] and w_o [H, heads D] bf16; cache: a dict of
+    k_cache, v_cache, page_table (and the scales of an e4m3 cache); positions [B] int32 of the new
+    tokens, lengths = positions + 1. Returns x + attention(norm(x)) [B, H]."""
+    B, H = x.shape
+    y = epd.ep_layer_norm(x, norm_weight, eps=eps, kind="rms")["y"]
+    # one expert over all rows is an ordinary linear layer
+    rows = dict(tokens_per_expert=torch.full((1,), B, dtype=torch.int32, device=x.device),
+                expert_start_loc=torch.zeros(1, dtype=torch.int32, device=x.device), status=status)
+    qkv, _ = epd.ep_expert_matmul(y, w_qkv.unsqueeze(0), **rows)
+    qkv = qkv.view(B, heads + 2 * kv_heads, -1)
+    q = epd.ep_cache_append(qkv[:, heads:heads + kv_heads], qkv[:, heads + kv_heads:],
+                            positions=positions, status=status, q=qkv[:, :heads], steps=steps, **cache)
+    o, _ = epd.ep_decode_attention(q, lengths=lengths, workspace=workspace, status=status, **cache)
+    return epd.ep_expert_matmul(o.view(B, -1), w_o.unsqueeze(0), residual=x, **rows)[0]
+
+
+def block_decode_step(x, attention, norm_weight, router, experts, eps=1e-5):
+    """A whole block for one new token of every sequence: `attention` are attention_step's
+    arguments after x, `experts` decode_step's after the logits. Returns the residual stream."""
+    x = attention_step(x, **attention)
+    y = epd.ep_layer_norm(x, norm_weight, eps=eps, kind="rms")["y"]
+    return x + decode_step(y, y.float() @ router.t(), **experts)
 
 
 def _time(f, n=10):
@@ -173,6 +240,27 @@ def main():
                                        layer.status))
     epd.check_status(layer.status, "decode step")
     print(f"decode step: T={t}: {ms * 1e3:.1f} us")
+
+    QH, KH, D, page, length = 32, 8, 128, 64, 4096
+    pages = -(-length // page)
+    kv = [torch.randn(t * pages, page, KH, D, device="cuda").bfloat16() for _ in range(2)]
+    positions = torch.full((t,), length - 1, dtype=torch.int32, device="cuda")
+    attention = dict(
+        norm_weight=torch.ones(H, device="cuda"), heads=QH, kv_heads=KH,
+        w_qkv=(torch.randn((QH + 2 * KH) * D, H, device="cuda") / math.sqrt(H)).bfloat16(),
+        w_o=(torch.randn(H, QH * D, device="cuda") / math.sqrt(QH * D)).bfloat16(),
+        cache=dict(k_cache=kv[0], v_cache=kv[1], page_table=torch.randperm(
+            t * pages, device="cuda").int().view(t, pages)),
+        positions=positions, lengths=positions + 1, status=layer.status,
+        steps=epd.rotary_steps(epd.rotary_frequencies(D)[0], "cuda"),
+        workspace=epd.new_attention_workspace(t, QH, KH, D))
+    experts = dict(w1_q=w1_q, w1_scale=w1_scale, w2=layer.w2.detach(), topk=k, workspace=ws,
+                   status=layer.status)
+    with torch.no_grad():
+        ms = _time(lambda: block_decode_step(xs, attention, torch.ones(H, device="cuda"),
+                                             layer.router, experts))
+    epd.check_status(layer.status, "block decode step")
+    print(f"block decode step: T={t}, {QH} / {KH} heads of {D}, {length} positions: {ms * 1e3:.1f} us")
 
 
 if __name__ == "__main__":
