@@ -5,19 +5,23 @@
 // Bound by HBM: every live key and value is read once, for G heads at a time, and G <= 16 heads are
 // 16 operations a byte at most. One pass with running maxima and sums.
 //
-// Split: the (sequence, kv head, block of 16 heads) segments of the batch, each as many tiles of
-// 16 tokens a warp as its length needs, form one line of tiles, and every block takes an equal run of
-// it, whatever the lengths are (they are read on the device). A segment that lies in one block's run
-// is finished there; the parts of one that several blocks share go to the workspace, and the block
-// that comes last joins them in the blocks' order.
+// Split: a block's warps form teams, one for each of up to eight kv heads, so that a block reads
+// whole rows of a [page, row, head, dim] cache: rows of one head alone, 128 or 256 bytes out of
+// every one or two KB, are served at two thirds of the memory's rate. The (sequence, group of heads)
+// segments of the batch, each as many tiles of a team's tokens as its length needs, form one line of
+// tiles, and every block takes an equal run of it, whatever the lengths are (they are read on the
+// device). A segment that lies in one block's run is finished there, by each team for its head; of one
+// that several blocks share the parts go to the workspace, and the team that comes last joins its
+// head's in the blocks' order. Where the batch has few segments (a long context alone) the teams take
+// fewer heads with more warps each, so that the joins have fewer parts and more blocks for them.
 //
-// A warp has its own tokens of each tile, its own ring of stages in shared memory, filled by its own
-// asynchronous copies some tiles ahead (past the ends of segments; page numbers are looked up one
-// tile before), and its own statistics, and does not wait for the other warps before the segment's
-// end. Scores and outputs are products on the warp-level matrix instructions with the tokens (of
-// scores) and the columns (of outputs) as their 16 rows and 8 heads as their columns, so that a group
-// of 8 heads fills them; with so few heads the 128-row tiles of tcgen05 would be nearly empty, and
-// these take a fraction of the time that the bytes take.
+// A warp has its own tokens of each tile, its own two stages in shared memory, filled by its own
+// asynchronous copies one tile ahead (past the ends of segments; page numbers are looked up one tile
+// before), and its own statistics; warps meet at a segment's end only, and only a team's. Scores
+// and outputs are products on the warp-level matrix instructions with the tokens (of scores) and the
+// columns (of outputs) as their 16 rows and 8 query heads as their columns, so that a group of 8
+// heads fills them; with so few heads the 128-row tiles of tcgen05 would be nearly empty, and these
+// take a fraction of the time that the bytes take.
 //
 // Precision: products of bf16 are exact, sums in 32 bits. The weights of a bf16 cache's values are split
 // into two bf16 (15 bits at least), so that the output's own rounding is the only one that matters. An
@@ -26,13 +30,17 @@
 // bits: an eighth of the output's rounding).
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "cache.cuh"
 
 namespace epd {
 namespace {
 
 constexpr int kMaxBlocks = 160;  // blocks that the workspace has room for
-constexpr int kMaxHeads = 16;    // heads of a segment, at most
+constexpr int kMaxHeads = 16;    // query heads of a segment, at most
+constexpr int kMaxTeams = 8;
+constexpr int kUncut = 4;        // tiles of a segment that one block takes whole
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLn2 = 0.6931471805599453f;
 // A maximum is moved (and everything summed so far scaled down) only when a score passes it by more
@@ -43,6 +51,8 @@ struct AttnArgs {
     const uint8_t *q;
     int64_t q_stride;  // bytes between tokens
     int QH, group, blocks_of_group;  // segments of a group
+    int teams, teams_log, tile_log;  // kv heads at once; log2 of a tile's tokens
+    int head_groups;                 // kv heads / teams
     epd_cache_t kv;
     Divisor page;
     const int32_t *lengths;
@@ -65,16 +75,16 @@ struct Shape {
     static constexpr int kTail = (FP8 ? 2 * kChunk * 4 : 0) + 16;  // scales and the live tokens' mask
     static constexpr int kStage = 2 * kChunk * kRow + kTail;
     static constexpr int kWarps = kRow == 512 ? 4 : 8;
-    static constexpr int kJoinCols = DP < 128 ? DP : 128, kJoinRow = kJoinCols + 4;
-    static constexpr int kJoinSums = kWarps * kHeads * kJoinRow * 4, kJoinWeights = 3 * kMaxBlocks * kHeads * 4;
-    static constexpr int kJoin = kJoinSums > kJoinWeights ? kJoinSums : kJoinWeights;
+    static constexpr bool kQueryInSmem = DP * NH >= 512;    // the query's fragments, where registers have no room
+    static constexpr int kQuery = kQueryInSmem ? DP / 16 * NH * 32 * 8 : 0;  // bytes, of a team
+    static constexpr int kJoinCols = kQueryInSmem ? (FP8 ? 32 : 64) : DP < 128 ? DP : 128, kJoinRow = kJoinCols + 4;
+    static constexpr int kJoin = kWarps * kHeads * kJoinRow * 4;
     // One stage on the way (64 KB a multiprocessor) while another is read. More in flight fill the same
     // memory system, but share it less evenly: of 152 blocks with equal runs the fastest then takes
     // 256 us and the slowest 348 (128 sequences, 2.1 GB; 361 us in all), with two stages 303 and 337 (344).
     static constexpr int kStages = 2;
     static constexpr int kThreads = kWarps * 32;
-    static constexpr int kTile = kWarps * kChunk;  // tokens of a tile
-    static constexpr int kSmem = kWarps * kStages * kStage + kJoin;
+    static constexpr int kSmem = kWarps * (kStages * kStage + kQuery) + kJoin;
     static constexpr int kPart = kHeads * (DP + 2);  // floats: the heads' sums, maxima and sums of weights
     static_assert(kSmem <= 226 * 1024 - 2048, "the ring and the join share what a block may have");
 };
@@ -133,23 +143,21 @@ __device__ __forceinline__ int swizzle(int row, int u) {
 struct Span {
     int lo, n, tiles;
 };
-template <int TILE>
 __device__ __forceinline__ Span span_of(const AttnArgs &a, int len) {
     const int64_t most = cache_positions(a.kv);
     Span s;
     s.n = len < 0 ? 0 : (int64_t)len > most ? (int)most : len;
     s.lo = a.window > 0 && s.n > a.window ? s.n - a.window : 0;
-    s.tiles = s.n > 0 ? (s.n - s.lo - 1) / TILE + 1 : 1;
+    s.tiles = s.n > 0 ? ((s.n - s.lo - 1) >> a.tile_log) + 1 : 1;
     return s;
 }
 
-// A place on the line of tiles: tile `tile` of segment (b, h, block).
-template <int TILE>
+// A place on the line of tiles: tile `tile` of segment (b, heads h * teams and on, block).
 struct Cursor {
     int b, h, block, tile, next_len;
     Span span;
     __device__ __forceinline__ void enter(const AttnArgs &a, int len) {
-        span = span_of<TILE>(a, len);
+        span = span_of(a, len);
         next_len = b + 1 < a.kv.num_seqs ? __ldg(a.lengths + b + 1) : 0;
     }
     __device__ __forceinline__ void advance(const AttnArgs &a) {
@@ -157,7 +165,7 @@ struct Cursor {
         tile = 0;
         if (++block < a.blocks_of_group) return;
         block = 0;
-        if (++h < a.kv.num_kv_heads) return;
+        if (++h < a.head_groups) return;
         h = 0;
         ++b;
         enter(a, next_len);
@@ -186,22 +194,129 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     return r;
 }
 
+// Joins n parts of a segment: part 0 at `part0`, the others `stride` floats apart from `part1`. A warp
+// takes every mates-th row from `sub`, RG of them at a time with the loads of PB parts on the way; lane i
+// has the weights of part i.
+template <int DP, int HB, int RG, int PB>
+__device__ __forceinline__ void combine_parts(const float *part0, const float *part1, int64_t stride, int n, int rows, int sub, int mates,
+                                           int D, uint8_t *out, float *lse) {
+    constexpr int C = DP / 32;
+    const int lane = threadIdx.x & 31, col = lane * C;
+    auto at_part = [&](int i) { return i == 0 ? part0 : part1 + (int64_t)(i - 1) * stride; };
+    for (int rb = sub; rb < rows; rb += RG * mates) {
+        float top[RG], sum[RG], v[RG][C], x[PB][RG][C], m0[RG], l0[RG];
+        auto statistic = [&](int i, int j, int which) {
+            const int r = rb + j * mates;
+            return i < n && r < rows ? __ldcg(at_part(i) + HB * DP + which * HB + r) : which ? 0.0f : -INFINITY;
+        };
+        auto fetch = [&](int i0) {
+#pragma unroll
+            for (int i = 0; i < PB; ++i)
+#pragma unroll
+                for (int j = 0; j < RG; ++j) {
+                    const bool has = i0 + i < n && rb + j * mates < rows;
+                    const float *src = at_part(i0 + i) + (rb + j * mates) * DP + col;
+#pragma unroll
+                    for (int k = 0; k < C; k += C < 4 ? 2 : 4) {
+                        if (C < 4) {
+                            const float2 y = has ? __ldcg(reinterpret_cast<const float2 *>(src)) : make_float2(0.0f, 0.0f);
+                            x[i][j][0] = y.x, x[i][j][1] = y.y;
+                        } else {
+                            const float4 y = has ? __ldcg(reinterpret_cast<const float4 *>(src + k)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            x[i][j][k] = y.x, x[i][j][k + 1] = y.y, x[i][j][(k + 2) % C] = y.z, x[i][j][(k + 3) % C] = y.w;
+                        }
+                    }
+                }
+        };
+        // all that the first parts need is on its way at once
+        fetch(0);
+#pragma unroll
+        for (int j = 0; j < RG; ++j) {
+            m0[j] = statistic(lane, j, 0);
+            l0[j] = statistic(lane, j, 1);
+            top[j] = m0[j];
+            sum[j] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < C; ++i) v[j][i] = 0.0f;
+        }
+        for (int i = lane + 32; i < n; i += 32) {
+#pragma unroll
+            for (int j = 0; j < RG; ++j) top[j] = fmaxf(top[j], statistic(i, j, 0));
+        }
+#pragma unroll
+        for (int j = 0; j < RG; ++j)
+#pragma unroll
+            for (int d = 16; d; d >>= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(kAll, top[j], d));
+        for (int c0 = 0; c0 < n; c0 += 32) {
+            float f[RG];
+#pragma unroll
+            for (int j = 0; j < RG; ++j) {
+                const float mi = c0 == 0 ? m0[j] : statistic(c0 + lane, j, 0), li = c0 == 0 ? l0[j] : statistic(c0 + lane, j, 1);
+                f[j] = mi == -INFINITY ? 0.0f : fast_exp2(mi - top[j]);
+                sum[j] = fmaf(f[j], li, sum[j]);
+            }
+            const int here = min(32, n - c0);
+            for (int i0 = 0; i0 < here; i0 += PB) {
+                if (c0 + i0 > 0) fetch(c0 + i0);
+#pragma unroll
+                for (int i = 0; i < PB; ++i)
+#pragma unroll
+                    for (int j = 0; j < RG; ++j) {
+                        // (what lies past the chunk's 32 parts is never fetched: PB divides 32)
+                        const float by = __shfl_sync(kAll, f[j], i0 + i);
+#pragma unroll
+                        for (int k = 0; k < C; ++k) v[j][k] = fmaf(x[i][j][k], by, v[j][k]);
+                    }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < RG; ++j) {
+            const int r = rb + j * mates;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) sum[j] += __shfl_xor_sync(kAll, sum[j], d);
+            const float inv = sum[j] > 0.0f ? __fdiv_rn(1.0f, sum[j]) : sum[j];
+            if (r >= rows) continue;
+            if (lse && lane == 0) lse[r] = top[j] == -INFINITY ? -INFINITY : (top[j] + log2f(sum[j])) * kLn2;
+            if (col < D) {
+#pragma unroll
+                for (int k = 0; k < C; k += 2)
+                    *reinterpret_cast<uint32_t *>(out + ((int64_t)r * D + col + k) * 2) = pack2_bf16(v[j][k] * inv, v[j][k + 1] * inv);
+            }
+        }
+    }
+}
+
+// v, as a value that the compiler does not know.
+__device__ __forceinline__ int64_t opaque(int64_t v) {
+    asm volatile("" : "+l"(v));
+    return v;
+}
+
 template <int DP, bool FP8, int NH>
 __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_kernel(AttnArgs a) {
     using S = Shape<DP, FP8, NH>;
-    constexpr int W = S::kWarps, UNITS = S::kUnits, TILE = S::kTile, CH = S::kChunk, MT = CH / 16, KT = DP / 16;
+    constexpr int W = S::kWarps, UNITS = S::kUnits, CH = S::kChunk, MT = CH / 16, KT = DP / 16;
     constexpr int HB = S::kHeads;
     extern __shared__ uint4 s_dyn[];
     __shared__ int64_t s_scan[W];
-    __shared__ int64_t s_prefix;
-    __shared__ int s_seq;
-    __shared__ float s_m[W][HB], s_l[W][HB], s_mall[HB], s_lall[HB];
-    __shared__ uint32_t s_last;
+    __shared__ float2 s_ml[W][HB], s_all[W][HB];  // maxima and sums of weights, a warp's and a team's
+    __shared__ uint32_t s_last[W];
+    // what only a segment's end needs, so that it takes no registers of the loop: each warp's place and the
+    // tiles of the sequences before it, and the block's run
+    __shared__ Cursor s_cursor[W], s_load[W];
+    __shared__ int64_t s_before[W], s_run[5];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, c = lane & 3;
-    const int D = a.kv.head_dim, B = a.kv.num_seqs, heads = a.kv.num_kv_heads * a.blocks_of_group;
+    const int D = a.kv.head_dim, B = a.kv.num_seqs, heads = a.head_groups * a.blocks_of_group;  // segments of a sequence
+    // the warp's team, its place there, the team's warps and threads
+    const int team = warp & (a.teams - 1), sub = warp >> a.teams_log, mates = W >> a.teams_log, tt = sub * 32 + lane;
+    auto team_sync = [&]() {
+        if (mates == 1) __syncwarp();
+        else named_barrier_sync(1 + team, mates * 32);
+    };
     const uint32_t ring = smem_addr(s_dyn) + warp * S::kStages * S::kStage;
     float *const s_join = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(s_dyn) + W * S::kStages * S::kStage);
+    uint2 *const s_query = reinterpret_cast<uint2 *>(reinterpret_cast<uint8_t *>(s_join) + S::kJoin + team * S::kQuery);
     // columns past D stay zero
     if (D < DP) {
         uint4 *mine = s_dyn + warp * S::kStages * S::kStage / 16;
@@ -214,17 +329,19 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
     int64_t total = 0;
     if (B > S::kThreads) {
         int64_t v = 0;
-        for (int b = tid; b < B; b += S::kThreads) v += span_of<TILE>(a, __ldg(a.lengths + b)).tiles;
+        for (int b = tid; b < B; b += S::kThreads) v += span_of(a, __ldg(a.lengths + b)).tiles;
         v = warp_scan(v, lane);
         if (lane == 31) s_scan[warp] = v;
         __syncthreads();
         for (int w = 0; w < W; ++w) total += s_scan[w];
         __syncthreads();
     }
+    // The run is [r0, r1) of the line, an equal share of it; a share that begins inside a segment of few tiles
+    // begins after it instead, so that no segment is cut whose join would take longer than its tiles.
     int64_t r0 = 0, r1 = 0, before = 0, blocks = gridDim.x;  // blocks: that have a tile
     for (int b0 = 0; b0 < B; b0 += S::kThreads) {
         const int b = b0 + tid;
-        const int64_t v = b < B ? span_of<TILE>(a, __ldg(a.lengths + b)).tiles : 0;
+        const int64_t v = b < B ? span_of(a, __ldg(a.lengths + b)).tiles : 0;
         int64_t incl = warp_scan(v, lane);
         if (lane == 31) s_scan[warp] = incl;
         __syncthreads();
@@ -237,32 +354,55 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
             if (B <= S::kThreads) total = sum;
             total *= heads;
             if (total < blocks) blocks = total;
+            if (blockIdx.x >= blocks) return;
             r0 = total * blockIdx.x / blocks;
             r1 = total * (blockIdx.x + 1) / blocks;
-            if (blockIdx.x >= blocks) return;
         }
         incl += before;
-        if ((incl - v) * heads <= r0 && r0 < incl * heads) {
-            s_seq = b;
-            s_prefix = incl - v;
+        const int64_t seq0 = (incl - v) * heads, seq1 = incl * heads;
+        if (seq0 <= r0 && r0 < seq1) {
+            const int rest = (int)(r0 - seq0);
+            Cursor at;
+            at.b = b;
+            int hh = rest / (int)v;
+            at.tile = rest - hh * (int)v;
+            int64_t first = r0, prefix = incl - v;
+            if (at.tile > 0 && v <= kUncut) {
+                first += v - at.tile;
+                at.tile = 0;
+                if (++hh == heads) {
+                    hh = 0;
+                    ++at.b;
+                    prefix = incl;
+                }
+            }
+            at.h = hh / a.blocks_of_group;
+            at.block = hh - at.h * a.blocks_of_group;
+            s_cursor[0] = at;
+            s_before[0] = prefix;
+            s_run[0] = first;
+        }
+        if (seq0 < r1 && r1 <= seq1) {
+            const int into = (int)(r1 - seq0) % (int)v;
+            s_run[1] = into > 0 && v <= kUncut ? r1 + v - into : r1;
         }
         before += sum;
         __syncthreads();
-        if (before * heads > r0) break;
+        if (before * heads >= r1) break;
     }
-    const int steps = (int)(r1 - r0);
-    Cursor<TILE> ld, cp;
-    ld.b = s_seq;
-    int64_t prefix = s_prefix;  // tiles of the sequences before the compute cursor's
+    const int steps = (int)(s_run[1] - s_run[0]);
+    if (steps <= 0) return;
+    Cursor ld = s_cursor[0];
+    const int64_t prefix0 = s_before[0];
+    if (tid == 0) s_run[2] = total, s_run[3] = blocks, s_run[4] = r0;
     ld.enter(a, __ldg(a.lengths + ld.b));
-    {
-        const int64_t rest = r0 - prefix * heads;
-        const int hh = (int)(rest / ld.span.tiles);
-        ld.tile = (int)(rest - (int64_t)hh * ld.span.tiles);
-        ld.h = hh / a.blocks_of_group;
-        ld.block = hh - ld.h * a.blocks_of_group;
+    __syncthreads();
+    int left = ld.span.tiles - ld.tile;  // of the segment's tiles
+    if (lane == 0) {
+        s_cursor[warp] = s_load[warp] = ld;
+        s_before[warp] = prefix0;
     }
-    cp = ld;
+    __syncthreads();
     if (blockIdx.x == 0) {  // lengths that the pages do not hold
         for (int b = tid; b < B; b += S::kThreads) {
             const int len = __ldg(a.lengths + b);
@@ -272,32 +412,53 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
     }
 
     // ---- loads: lane l looks after token l % CH of the warp's chunk
-    int token, page, kv_head;
+    uint32_t position, end;         // of the token, and of its sequence (a tile may end past 2^31 - 1)
+    int seq, kv_head, page;         // page: < 0 for a token past the end
+    int load_left;                  // tiles of the segment that are still to be loaded
+    auto enter = [&](const Cursor &at) {
+        position = (uint32_t)at.span.lo + ((uint32_t)at.tile << a.tile_log) + sub * CH + (lane & (CH - 1));
+        end = at.span.n;
+        seq = at.b;
+        kv_head = (at.h << a.teams_log) + team;
+        load_left = at.span.tiles - at.tile;
+    };
     auto look_up = [&]() {
-        // (a tile may end past 2^31 - 1, where the sequence ends before)
-        const uint32_t t = (uint32_t)ld.span.lo + (uint32_t)ld.tile * TILE + warp * CH + (lane & (CH - 1));
-        token = t < (uint32_t)ld.span.n ? (int)t : -1;
-        kv_head = ld.h;
-        page = token >= 0 ? __ldg(a.kv.page_table + ld.b * a.kv.table_stride + divide(t, a.page)) : -1;
+        page = position < end ? __ldg(a.kv.page_table + seq * a.kv.table_stride + divide(position, a.page)) : -2;
+        if (position < end && page < 0) page = INT32_MAX;  // no page either, but reported
+    };
+    auto go_on = [&]() {
+        if (--load_left > 0) {
+            position += 1u << a.tile_log;
+        } else {
+            Cursor at = s_load[warp];
+            at.tile = at.span.tiles - 1;
+            at.advance(a);
+            enter(at);
+            __syncwarp();
+            if (lane == 0) s_load[warp] = at;
+            __syncwarp();
+        }
+        look_up();
     };
     const int units = D * (FP8 ? 1 : 2) / 16;
     auto load = [&](int stage) {
         const uint32_t at = ring + stage * S::kStage;
-        bool live = token >= 0;
-        if (live && (page < 0 || page >= a.kv.num_pages)) {
+        bool live = page >= 0;
+        if (live && page >= a.kv.num_pages) {
             report(a.status, EPD_ERR_CAPACITY);
             live = false;
         }
-        const int inside = live ? token - (int)(divide(token, a.page) * a.page.d) : 0;
+        const int inside = live ? (int)(position - divide(position, a.page) * a.page.d) : 0;
         const int64_t off = live ? (page * a.kv.page_stride + inside * a.kv.token_stride + kv_head * a.kv.head_stride) * (FP8 ? 1 : 2) : 0;
         const uint32_t mask = __ballot_sync(kAll, live) & (CH == 32 ? kAll : 0xffffu);
         if (a.aligned && mask == (CH == 32 ? kAll : 0xffffu)) {
             // every 16 tokens lie on one page: one address for them, and a constant step
             constexpr int STEP = 32 / UNITS > 0 ? 32 / UNITS : 1;  // rows of one instruction
-            const int64_t step = a.kv.token_stride * (FP8 ? 1 : 2);
+            // (not kept in registers from step to step)
+            const int64_t step = opaque(a.kv.token_stride) * (FP8 ? 1 : 2);
             const int u = lane % UNITS;
-            const uint8_t *const k0 = static_cast<const uint8_t *>(a.kv.k) + (lane / UNITS) * step + u * 16;
-            const int64_t to_v = (int64_t)(reinterpret_cast<uintptr_t>(a.kv.v) - reinterpret_cast<uintptr_t>(a.kv.k));
+            const uint8_t *const k0 = reinterpret_cast<const uint8_t *>(opaque(reinterpret_cast<int64_t>(a.kv.k))) + (lane / UNITS) * step + u * 16;
+            const int64_t to_v = opaque((int64_t)(reinterpret_cast<uintptr_t>(a.kv.v) - reinterpret_cast<uintptr_t>(a.kv.k)));
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 const uint8_t *src = k0 + __shfl_sync(kAll, off, 16 * t);
@@ -334,16 +495,13 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
         if (lane == 0)
             asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + S::kStage - 16), "r"(mask) : "memory");
     };
-    __syncwarp();
+    enter(ld);
     look_up();
 #pragma unroll
     for (int s = 0; s < S::kStages - 1; ++s) {
         if (s < steps) {
             load(s);
-            if (s + 1 < steps) {
-                ld.advance(a);
-                look_up();
-            }
+            if (s + 1 < steps) go_on();
         }
         copy_commit();
     }
@@ -352,25 +510,27 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
     // 8 n + 2 c + i % 2; m and l: of heads 8 n + 2 c, 8 n + 2 c + 1, l of the lane's own tokens
     uint32_t q[KT][NH][2];
     float o[KT][NH][4], m[NH][2], l[NH][2], q_scale = 1.0f, v_ref = 0.0f, v_inv = 0.0f;
+    // Fragments of the query: head g, and the columns that the keys' fragments pair with them -- of a
+    // 16-byte unit of an e4m3 row a lane holds four neighbours.
+    auto load_query = [&](const Cursor &at) {
+        const int rows = a.group - at.block * HB;  // heads of the segment, if fewer than HB
+        const uint8_t *src = a.q + at.b * a.q_stride + (int64_t)(((at.h << a.teams_log) + team) * a.group + at.block * HB) * D * 2;
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+            for (int n = 0; n < NH; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = n * 8 + g, col = k * 16 + (FP8 ? 4 * c + i * 2 : 2 * c + i * 8);
+                    q[k][n][i] = row < rows && col < D ? __ldg(reinterpret_cast<const uint32_t *>(src + ((int64_t)row * D + col) * 2)) : 0;
+                }
+    };
+    if (!S::kQueryInSmem) load_query(s_cursor[warp]);
     const float *const scales = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(s_dyn) + warp * S::kStages * S::kStage + 2 * CH * S::kRow);
-    bool fresh = true;
     int stage = 0;
-    for (int step = 0; step < steps; ++step) {
-        if (fresh) {
-            fresh = false;
-            const int rows = a.group - cp.block * HB;  // heads of the segment, if fewer than HB
-            const uint8_t *src = a.q + cp.b * a.q_stride + (int64_t)(cp.h * a.group + cp.block * HB) * D * 2;
-            // Fragments of the query: head g, and the columns that the keys' fragments pair with
-            // them -- of a 16-byte unit of an e4m3 row a lane holds four neighbours.
-#pragma unroll
-            for (int k = 0; k < KT; ++k)
-#pragma unroll
-                for (int n = 0; n < NH; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int row = n * 8 + g, col = k * 16 + (FP8 ? 4 * c + i * 2 : 2 * c + i * 8);
-                        q[k][n][i] = row < rows && col < D ? __ldg(reinterpret_cast<const uint32_t *>(src + ((int64_t)row * D + col) * 2)) : 0;
-                    }
+    for (int step = 0; step < steps;) {
+        {  // a segment begins
+            if (S::kQueryInSmem) load_query(s_cursor[warp]);
             if (FP8) {
                 float top = 0.0f;
 #pragma unroll
@@ -382,13 +542,22 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
                 // to [2^6, 2^7): the power of two from the exponent's bits
                 const int e = top > 0.0f ? min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 100) : 0;
                 const float up = __uint_as_float((uint32_t)(127 + 6 - e) << 23);
-                q_scale = __uint_as_float((uint32_t)(127 - 6 + e) << 23);
+                q_scale = __uint_as_float((uint32_t)(127 - 6 + e) << 23) * a.scale_log2;
 #pragma unroll
                 for (int k = 0; k < KT; ++k)
 #pragma unroll
                     for (int n = 0; n < NH; ++n)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) q[k][n][i] = pack2_f16(lo_bf16(q[k][n][i]) * up, hi_bf16(q[k][n][i]) * up);
+            }
+            if (S::kQueryInSmem) {
+                // every warp of the team has all of it: each writes its share
+#pragma unroll
+                for (int k = 0; k < KT; ++k)
+#pragma unroll
+                    for (int n = 0; n < NH; ++n)
+                        if ((k & (mates - 1)) == sub) s_query[(k * NH + n) * 32 + lane] = make_uint2(q[k][n][0], q[k][n][1]);
+                team_sync();
             }
 #pragma unroll
             for (int n = 0; n < NH; ++n) {
@@ -399,14 +568,12 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
             }
             v_ref = v_inv = 0.0f;
         }
+        for (const int until = step + min(left, steps - step); step < until; ++step) {
         copy_wait<S::kStages - 2>();
         __syncwarp();
         if (step + S::kStages - 1 < steps) {
             load(stage == 0 ? S::kStages - 1 : stage - 1);
-            if (step + S::kStages < steps) {
-                ld.advance(a);
-                look_up();
-            }
+            if (step + S::kStages < steps) go_on();
         }
         copy_commit();
 
@@ -417,6 +584,9 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
             // s[t][n][i]: token 16 t + g + 8 (i / 2), head 8 n + 2 c + i % 2
             float s[MT][NH][4] = {};
             const int row = lane & 15, right = lane >> 4;
+            auto query = [&](int k, int n) {
+                return S::kQueryInSmem ? s_query[(k * NH + n) * 32 + lane] : make_uint2(q[k][n][0], q[k][n][1]);
+            };
 #pragma unroll
             for (int k = 0; k < UNITS / 2; ++k)
 #pragma unroll
@@ -430,11 +600,17 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
                             widen4(r[2 * h], f[0], f[2]);
                             widen4(r[2 * h + 1], f[1], f[3]);
 #pragma unroll
-                            for (int n = 0; n < NH; ++n) mma<true>(s[t][n], f, q[2 * k + h][n][0], q[2 * k + h][n][1]);
+                            for (int n = 0; n < NH; ++n) {
+                                const uint2 b = query(2 * k + h, n);
+                                mma<true>(s[t][n], f, b.x, b.y);
+                            }
                         }
                     } else {
 #pragma unroll
-                        for (int n = 0; n < NH; ++n) mma<false>(s[t][n], r, q[k][n][0], q[k][n][1]);
+                        for (int n = 0; n < NH; ++n) {
+                            const uint2 b = query(k, n);
+                            mma<false>(s[t][n], r, b.x, b.y);
+                        }
                     }
                 }
             const float *const sc = scales + stage * (S::kStage / 4);
@@ -442,8 +618,8 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
             for (int t = 0; t < MT; ++t) {
                 float f[2] = {a.scale_log2, a.scale_log2};
                 if (FP8) {
-                    f[0] = f[0] * q_scale * sc[16 * t + g];
-                    f[1] = f[1] * q_scale * sc[16 * t + g + 8];
+                    f[0] = q_scale * sc[16 * t + g];
+                    f[1] = q_scale * sc[16 * t + g + 8];
                 }
 #pragma unroll
                 for (int n = 0; n < NH; ++n)
@@ -576,10 +752,20 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
             }
         }
         if (++stage == S::kStages) stage = 0;
+        }
 
-        if (cp.tile == cp.span.tiles - 1 || step == steps - 1) {
-            // ---- the segment's end here: join the warps
-            const int h0 = cp.h * a.group + cp.block * HB, rows = min(HB, a.group - cp.block * HB);
+        {
+            // ---- the segment's end here: join the team
+            const Cursor cp = s_cursor[warp];
+            const int64_t prefix = s_before[warp];
+            const int64_t r0 = s_run[0], r1 = s_run[1], total = s_run[2], blocks = s_run[3], share = s_run[4];
+            Cursor next = cp;
+            next.tile = cp.span.tiles - 1;
+            if (step < steps) {
+                next.advance(a);
+                if (!S::kQueryInSmem) load_query(next);  // on its way meanwhile
+            }
+            const int h0 = ((cp.h << a.teams_log) + team) * a.group + cp.block * HB, rows = min(HB, a.group - cp.block * HB);
             const int64_t seg0 = prefix * heads + (int64_t)(cp.h * a.blocks_of_group + cp.block) * cp.span.tiles;  // its first tile on the line
             const int64_t seg1 = seg0 + cp.span.tiles;
             const bool whole = r0 <= seg0 && seg1 <= r1;
@@ -589,19 +775,17 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
                 for (int i = 0; i < 2; ++i) {
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) l[n][i] += __shfl_xor_sync(kAll, l[n][i], d);
-                    if (g == 0) {
-                        s_m[warp][n * 8 + 2 * c + i] = m[n][i];
-                        s_l[warp][n * 8 + 2 * c + i] = l[n][i];
-                    }
+                    if (g == 0) s_ml[warp][n * 8 + 2 * c + i] = make_float2(m[n][i], l[n][i]);
                 }
-            __syncthreads();
+            team_sync();
 #pragma unroll
             for (int n = 0; n < NH; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float top = -INFINITY;
+                    float top = m[n][i];
 #pragma unroll
-                    for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w][n * 8 + 2 * c + i]);
+                    for (int j = 0; j < W; ++j)
+                        if (j < mates) top = fmaxf(top, s_ml[team + (j << a.teams_log)][n * 8 + 2 * c + i].x);
                     float f = m[n][i] == -INFINITY ? 0.0f : fast_exp2(m[n][i] - top);
                     if (FP8) f *= v_ref;
 #pragma unroll
@@ -610,16 +794,20 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
                         o[k][n][i + 2] *= f;
                     }
                 }
-            if (tid < HB) {
+            if (tt < HB) {
+                float2 x[W];
                 float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-                for (int w = 0; w < W; ++w) top = fmaxf(top, s_m[w][tid]);
+                for (int j = 0; j < W; ++j) {
+                    x[j] = j < mates ? s_ml[team + (j << a.teams_log)][tt] : make_float2(-INFINITY, 0.0f);
+                    top = fmaxf(top, x[j].x);
+                }
 #pragma unroll
-                for (int w = 0; w < W; ++w) sum += s_m[w][tid] == -INFINITY ? 0.0f : s_l[w][tid] * fast_exp2(s_m[w][tid] - top);
-                s_mall[tid] = top;
-                s_lall[tid] = sum;
+                for (int j = 0; j < W; ++j) sum += x[j].x == -INFINITY ? 0.0f : x[j].y * fast_exp2(x[j].x - top);
+                s_all[team][tt] = make_float2(top, sum);
             }
-            float *const part = a.parts + (2 * blockIdx.x + (r0 < seg0 ? 1 : 0)) * (int64_t)S::kPart;
+            const int64_t all_parts = (int64_t)S::kPart << a.teams_log;  // of a block's run: one for every team
+            float *const part = a.parts + (2 * blockIdx.x + (share < seg0 ? 1 : 0)) * all_parts + team * S::kPart;
             uint8_t *const out = a.out + ((int64_t)cp.b * a.QH + h0) * D * 2;
             constexpr int JC = S::kJoinCols, JR = S::kJoinRow;
 #pragma unroll
@@ -633,140 +821,98 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 mine[(n * 8 + 2 * c + (i & 1)) * JR + k * 16 + (FP8 ? 2 * g + (i >> 1) : g + 8 * (i >> 1))] = o[pass * (JC / 16) + k][n][i];
-                    __syncthreads();
-                    for (int e = tid; e < rows * (JC / 2); e += S::kThreads) {
+                    team_sync();
+                    for (int e = tt; e < rows * (JC / 2); e += mates * 32) {
                         const int r = e / (JC / 2), col = e % (JC / 2) * 2;
                         float2 v = make_float2(0.0f, 0.0f);
 #pragma unroll
-                        for (int w = 0; w < W; ++w) {
-                            const float2 x = *reinterpret_cast<const float2 *>(s_join + (w * HB + r) * JR + col);
-                            v.x += x.x;
-                            v.y += x.y;
-                        }
+                        for (int j = 0; j < W; ++j)
+                            if (j < mates) {
+                                const float2 x = *reinterpret_cast<const float2 *>(s_join + ((team + (j << a.teams_log)) * HB + r) * JR + col);
+                                v.x += x.x;
+                                v.y += x.y;
+                            }
                         if (pass * JC + col < D) {
                             if (whole) {
-                                const float inv = s_lall[r] > 0.0f ? __fdiv_rn(1.0f, s_lall[r]) : s_lall[r];
+                                const float sum = s_all[team][r].y, inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : sum;
                                 *reinterpret_cast<uint32_t *>(out + ((int64_t)r * D + pass * JC + col) * 2) = pack2_bf16(v.x * inv, v.y * inv);
                             } else {
                                 *reinterpret_cast<float2 *>(part + r * DP + pass * JC + col) = v;
                             }
                         }
                     }
-                    __syncthreads();
+                    team_sync();
                 }
             }
-            if (tid < rows) {
+            if (tt < rows) {
+                const float top = s_all[team][tt].x, sum = s_all[team][tt].y;
                 if (whole) {
-                    if (a.lse) a.lse[(int64_t)cp.b * a.QH + h0 + tid] = s_mall[tid] == -INFINITY ? -INFINITY : (s_mall[tid] + log2f(s_lall[tid])) * kLn2;
+                    if (a.lse) a.lse[(int64_t)cp.b * a.QH + h0 + tt] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
                 } else {
-                    part[HB * DP + tid] = s_mall[tid];
-                    part[HB * DP + HB + tid] = s_lall[tid];
+                    part[HB * DP + tt] = top;
+                    part[HB * DP + HB + tt] = sum;
                 }
             }
             if (!whole) {
-                // ---- the parts of the blocks that share the segment, joined by the last of them
+                // ---- the parts of the blocks that share the segment, joined by the last of their teams
                 const int first = (int)(((seg0 + 1) * blocks - 1) / total), last = (int)((seg1 * blocks - 1) / total);
-                uint32_t *const counter = a.counters + first;  // a block's run has the beginning of one such segment at most
-                __syncthreads();
-                if (tid == 0) {  // releases what the block wrote before the barrier, and acquires what the others did
+                uint32_t *const counter = a.counters + first * kMaxTeams + team;  // a block's run has the beginning of one such segment at most
+                team_sync();
+                if (tt == 0) {  // releases what the team wrote before the barrier, and acquires what the others did
                     const uint32_t seen = add_acq_rel(counter, 1u);
-                    s_last = seen == (uint32_t)(last - first);
-                    if (s_last) *counter = 0;  // as the next call finds it
+                    s_last[team] = seen == (uint32_t)(last - first);
+                    if (s_last[team]) *counter = 0;  // as the next call finds it
                 }
-                __syncthreads();
-                if (s_last) {
+                team_sync();
+                if (s_last[team]) {
                     const int n = last - first + 1;
-                    auto part_of = [&](int i) {  // the segment is a block's first, or begins inside its run
-                        const int blk = first + i;
-                        return a.parts + (2 * blk + (total * blk / blocks < seg0 ? 1 : 0)) * (int64_t)S::kPart;
-                    };
-                    // only the first block's part can be its second
-                    const float *const part0 = part_of(0), *const part1 = a.parts + 2 * (int64_t)(first + 1) * S::kPart;
-                    auto at_part = [&](int i) { return i == 0 ? part0 : part1 + 2 * (int64_t)(i - 1) * S::kPart; };
-                    // the parts' sums, four columns at a time, sixteen of a thread's on the way
-                    constexpr int ITEMS = (HB * DP / 4 + S::kThreads - 1) / S::kThreads, BATCH = 16 / ITEMS;
-                    float4 x[BATCH][ITEMS], v[ITEMS];
-                    auto fetch = [&](int i0) {
-#pragma unroll
-                        for (int i = 0; i < BATCH; ++i)
-#pragma unroll
-                            for (int j = 0; j < ITEMS; ++j) {
-                                const int e = tid + j * S::kThreads;
-                                x[i][j] = i0 + i < n && e < HB * DP / 4 ? __ldcg(reinterpret_cast<const float4 *>(at_part(i0 + i)) + e) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            }
-                    };
-                    fetch(0);
-                    // meanwhile a weight for every part and head, and the heads' sums
-                    float *const s_max = s_join, *const s_sum = s_join + kMaxBlocks * HB, *const s_by = s_sum + kMaxBlocks * HB;
-                    for (int e = tid; e < n * HB; e += S::kThreads) {
-                        const float *src = at_part(e / HB) + HB * DP + e % HB;
-                        s_max[e] = __ldcg(src);
-                        s_sum[e] = __ldcg(src + HB);
-                    }
-                    __syncthreads();
-                    const int head = tid % HB;
-                    float top = -INFINITY;
-#pragma unroll 8
-                    for (int i = 0; i < n; ++i) top = fmaxf(top, s_max[i * HB + head]);
-                    for (int e = tid; e < n * HB; e += S::kThreads) {  // (kThreads is a multiple of HB: the thread's own head)
-                        const float f = s_max[e] == -INFINITY ? 0.0f : fast_exp2(s_max[e] - top);
-                        s_by[e] = f;
-                        s_sum[e] *= f;
-                    }
-                    __syncthreads();
-                    if (tid < rows) {
-                        float sum = 0.0f;
-#pragma unroll 8
-                        for (int i = 0; i < n; ++i) sum += s_sum[i * HB + tid];
-                        s_lall[tid] = sum > 0.0f ? __fdiv_rn(1.0f, sum) : sum;
-                        if (a.lse) a.lse[(int64_t)cp.b * a.QH + h0 + tid] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
-                    }
-#pragma unroll
-                    for (int j = 0; j < ITEMS; ++j) v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    for (int i0 = 0; i0 < n; i0 += BATCH) {
-                        if (i0 > 0) fetch(i0);
-#pragma unroll
-                        for (int i = 0; i < BATCH; ++i)
-#pragma unroll
-                            for (int j = 0; j < ITEMS; ++j) {
-                                const int r = (tid + j * S::kThreads) / (DP / 4);
-                                const float f = i0 + i < n && r < HB ? s_by[(i0 + i) * HB + r] : 0.0f;
-                                v[j].x = fmaf(x[i][j].x, f, v[j].x), v[j].y = fmaf(x[i][j].y, f, v[j].y);
-                                v[j].z = fmaf(x[i][j].z, f, v[j].z), v[j].w = fmaf(x[i][j].w, f, v[j].w);
-                            }
-                    }
-                    __syncthreads();
-#pragma unroll
-                    for (int j = 0; j < ITEMS; ++j) {
-                        const int e = tid + j * S::kThreads, r = e / (DP / 4), col = e % (DP / 4) * 4;
-                        if (r < rows && col < D)
-                            *reinterpret_cast<uint2 *>(out + ((int64_t)r * D + col) * 2) =
-                                make_uint2(pack2_bf16(v[j].x * s_lall[r], v[j].y * s_lall[r]), pack2_bf16(v[j].z * s_lall[r], v[j].w * s_lall[r]));
-                    }
-                    __syncthreads();
+                    // the segment is a block's first, or begins inside its run (of the first block only)
+                    const float *const part0 = a.parts + (2 * first + (total * first / blocks < seg0 ? 1 : 0)) * all_parts + team * S::kPart;
+                    const float *const part1 = a.parts + 2 * (int64_t)(first + 1) * all_parts + team * S::kPart;
+                    float *const lse = a.lse ? a.lse + (int64_t)cp.b * a.QH + h0 : nullptr;
+                    if (HB <= 2 * mates) combine_parts<DP, HB, 1, DP == 256 ? 8 : 16>(part0, part1, 2 * all_parts, n, rows, sub, mates, D, out, lse);
+                    else combine_parts<DP, HB, 4, DP == 256 ? 2 : 4>(part0, part1, 2 * all_parts, n, rows, sub, mates, D, out, lse);
+                    team_sync();
                 }
             }
-            fresh = true;
-        }
-        if (step + 1 < steps) {
-            const int b = cp.b, tiles = cp.span.tiles;
-            cp.advance(a);
-            if (cp.b != b) prefix += tiles;
+            __syncwarp();
+            if (lane == 0) {
+                s_cursor[warp] = next;
+                if (next.b != cp.b) s_before[warp] = prefix + cp.span.tiles;
+            }
+            __syncwarp();
+            left = next.span.tiles;
         }
     }
 }
 
 inline int padded_dim(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
-// The workspace: a counter for every block, zero between calls and in the same place whatever the
-// sizes are, and two parts for every block.
-constexpr size_t kCounterBytes = (kMaxBlocks * 4 + kAlign - 1) / kAlign * kAlign;
+// The workspace: a counter for every block and team, zero between calls and in the same place whatever
+// the sizes are, and two parts for every block and team.
+constexpr size_t kCounterBytes = (kMaxBlocks * kMaxTeams * 4 + kAlign - 1) / kAlign * kAlign;
+
+// The most teams that may be: a power of two of them divides the kv heads.
+inline int most_teams(int KH) {
+    int n = kMaxTeams;
+    while (KH % n) n /= 2;
+    return n;
+}
 
 template <int DP, bool FP8, int NH>
 epd_status_t launch_heads(AttnArgs &a, cudaStream_t st) {
     using S = Shape<DP, FP8, NH>;
     a.blocks_of_group = (a.group + S::kHeads - 1) / S::kHeads;
     if ((int64_t)a.kv.num_kv_heads * a.blocks_of_group > INT32_MAX) return EPD_ERR_UNSUPPORTED;
+    // As many kv heads at once as leave a segment for every fourth multiprocessor.
+    a.teams = most_teams(a.kv.num_kv_heads);
+    if (a.teams > S::kWarps) a.teams = S::kWarps;
+    while (a.teams > 1 && (int64_t)a.kv.num_seqs * (a.kv.num_kv_heads / a.teams) * a.blocks_of_group < sm_count() / 4) a.teams /= 2;
+    a.teams_log = 0;
+    while ((1 << a.teams_log) < a.teams) ++a.teams_log;
+    a.tile_log = 4;
+    while ((1 << a.tile_log) < S::kChunk * (S::kWarps / a.teams)) ++a.tile_log;
+    a.head_groups = a.kv.num_kv_heads / a.teams;
     if (const epd_status_t rc = allow_smem<attention_kernel<DP, FP8, NH>>(S::kSmem)) return rc;
     const int grid = sm_count() < kMaxBlocks ? sm_count() : kMaxBlocks;
     return launch_pdl(attention_kernel<DP, FP8, NH>, grid, S::kThreads, S::kSmem, st, a);
@@ -787,7 +933,8 @@ extern "C" size_t epd_attention_workspace_bytes(int num_seqs, int num_heads, int
     if (num_seqs < 0 || num_heads < 1 || num_kv_heads < 1 || num_heads % num_kv_heads || head_dim < 8 ||
         head_dim % 8 || head_dim > kMaxHeadDim)
         return 0;
-    return kCounterBytes + (size_t)2 * kMaxBlocks * kMaxHeads * (padded_dim(head_dim) + 2) * 4;
+    const int group = num_heads / num_kv_heads;
+    return kCounterBytes + (size_t)2 * kMaxBlocks * most_teams(num_kv_heads) * (group <= 8 ? 8 : kMaxHeads) * (padded_dim(head_dim) + 2) * 4;
 }
 
 extern "C" epd_status_t ep_decode_attention(const epd_cache_t *cache, const void *q, int64_t q_token_stride,
