@@ -688,8 +688,8 @@ typedef struct {
  * scale = amax / 448 of the head's fp32 values (1 if amax = 0) and e4m3(value / scale), nearest even.
  * A token of sequence -1 is padding: nothing of it is written. A sequence outside
  * [-1, num_seqs), a position outside the sequence's pages or a page outside [0, num_pages) sets
- * EPD_ERR_CAPACITY, and the token is left out like padding. Two tokens at one position: one of
- * the two is kept for each head.
+ * EPD_ERR_CAPACITY, and the token is left out like padding. Two tokens at one position must not
+ * be: what that row then holds is unspecified (nothing else is touched).
  *   q, q_out: [T, num_heads, head_dim], k, v: [T, num_kv_heads, head_dim] bfloat16, the heads of a
  *   token next to each other, tokens the given strides apart (elements, multiples of 8), 16-byte
  *   aligned: parts of one projection's rows are taken as they are. q may be NULL; q_out may be q

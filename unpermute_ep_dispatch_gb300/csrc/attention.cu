@@ -361,11 +361,11 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
         incl += before;
         const int64_t seq0 = (incl - v) * heads, seq1 = incl * heads;
         if (seq0 <= r0 && r0 < seq1) {
-            const int rest = (int)(r0 - seq0);
+            const int64_t rest = r0 - seq0;
             Cursor at;
             at.b = b;
-            int hh = rest / (int)v;
-            at.tile = rest - hh * (int)v;
+            int hh = (int)(rest / v);
+            at.tile = (int)(rest - hh * v);
             int64_t first = r0, prefix = incl - v;
             if (at.tile > 0 && v <= kUncut) {
                 first += v - at.tile;
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
             s_run[0] = first;
         }
         if (seq0 < r1 && r1 <= seq1) {
-            const int into = (int)(r1 - seq0) % (int)v;
+            const int64_t into = (r1 - seq0) % v;
             s_run[1] = into > 0 && v <= kUncut ? r1 + v - into : r1;
         }
         before += sum;
