@@ -1,10 +1,14 @@
 """Decode attention over the paged cache on the GPU against the formula in 64 bits.
 
 Tolerances: half a step of bf16 for the output, and the weights' relative error times the sum of
-weight * |value|. The weights: a score's fp32 sum over D products of size |q| |k| (below 2^5 after
-the scale, 2^-24 for each of D / 16 + 4 additions in a chain: 2^-15), the exponential 2^-22, the
-weights' two bf16 parts 2^-17, together below 2^-14; in an e4m3 cache one fp16 part, 2^-12, on top.
+weight * |value|. The weights: a score's fp32 sum over D products of size |q| |k| (below 2^4 after
+the scale, 2^-24 for each of D / 16 + 4 additions in a chain: 2^-15.6 at most), the exponential 2^-22,
+the weights' two bf16 parts 2^-15 (what is left of the first is below 2^-7 of the weight, and half a
+step of the second is 2^-8 of that), 2^-14.3 together. In an e4m3 cache they are one fp16 part instead:
+half a step is finfo(float16).eps / 2 = 2^-11 of the weight, and that comes on top.
 lse: the same 2^-14, and its own rounding."""
+import math
+
 import pytest
 import torch
 
@@ -22,7 +26,7 @@ def gen(seed):
 
 
 def check(lengths, page, KH, G, D, fp8=False, window=0, scale=None, order="page,row,head", seed=0, workspace=None,
-          q_scale=1.0, garbage=True, v_spread=False):
+          q_scale=1.0, garbage=True, v_spread=False, v_power=0):
     g = gen(seed)
     B, QH = len(lengths), KH * G
     most = max(1, -(-max(lengths) // page))
@@ -30,6 +34,8 @@ def check(lengths, page, KH, G, D, fp8=False, window=0, scale=None, order="page,
     k, v, ks, vs = paged(pages, page, KH, D, fp8, DEV, g, order)
     if v_spread:  # values' scales over ten powers of two
         vs *= torch.exp2(10 * torch.rand(vs.shape, generator=g, device=DEV) - 5)
+    if v_power:  # very small or large values
+        (vs if fp8 else v).mul_(2.0 ** v_power)
     table = torch.randperm(pages, generator=g, device=DEV).to(torch.int32).view(B, most)
     lens = torch.tensor(lengths, dtype=torch.int32, device=DEV)
     # one projection's rows: the queries are slices of them
@@ -54,7 +60,8 @@ def check(lengths, page, KH, G, D, fp8=False, window=0, scale=None, order="page,
     kw = dict(k_scale=ks, v_scale=vs, softmax_scale=scale, window=window, with_lse=True)
     out, got_lse = epd.ep_decode_attention(q, k, v, table, lens, workspace, status, **kw)
     assert int(status) == 0
-    tol = 2.0 ** -8 * want.abs() + (2.0 ** -14 + (2.0 ** -12 if fp8 else 0)) * size
+    # (2^-134: half a step of the smallest bf16)
+    tol = 2.0 ** -134 + 2.0 ** -8 * want.abs() + (2.0 ** -14 + (2.0 ** -11 if fp8 else 0)) * size
     err = (out.double() - want).abs()
     assert bool((err <= tol).all()), (float((err - tol).max()), float(err.max()))
     empty = lens <= 0
@@ -105,6 +112,91 @@ def test_lengths(lengths, fp8):
 @pytest.mark.parametrize("B", [151, 152, 153, 256, 257, 700])
 def test_many_sequences(B):
     check([(i * 37) % 300 for i in range(B)], 16, 2, 4, 64, seed=B)
+
+
+MIXED = {  # of few and many tiles, between lengths that no block takes alone
+    "short": [(i * 97) % 200 for i in range(60)],
+    "one long": [5] * 20 + [3001] + [0, 700] * 12,
+    "long first": [3900, 1, 2, 3] + [600] * 36,
+    "equal": [513] * 41,
+    "few": [2000, 100, 511, 512, 513, 0, 1, 33],
+}
+
+
+@pytest.mark.parametrize("order", ["page,row,head", "page,head,row"])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("KH,G,D", [(8, 4, 128), (8, 16, 64), (8, 1, 256), (4, 12, 256), (6, 8, 128), (16, 2, 80), (12, 9, 128)])
+@pytest.mark.parametrize("lengths", list(MIXED))
+def test_heads_together(lengths, KH, G, D, fp8, order):
+    """Several kv heads of a sequence at once, in one block and shared by many."""
+    check(MIXED[lengths], 16, KH, G, D, fp8, order=order, seed=KH)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_heads_together_paged(fp8):
+    for page in (1, 7, 64):
+        check(MIXED["one long"], page, 8, 4, 128, fp8, window=333 if page == 7 else 0, seed=page)
+        check(MIXED["long first"], page, 8, 8, 64, fp8, window=2500 if page == 64 else 0, seed=page)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_bad_pages_of_heads_together(fp8):
+    g = gen(12)
+    B, KH, G, D, page = 48, 8, 4, 128, 16
+    k, v, ks, vs = paged(4 * B, page, KH, D, fp8, DEV, g)
+    table = torch.randperm(4 * B, generator=g, device=DEV).int().view(B, 4)
+    lens = torch.full((B,), 64, dtype=torch.int32, device=DEV)
+    q = torch.randn(B, KH * G, D, generator=g, device=DEV).bfloat16()
+    ws, st = epd.new_attention_workspace(B, KH * G, KH, D, DEV), epd.new_status(DEV)
+    full, _ = epd.ep_decode_attention(q, k, v, table, lens, ws, st, k_scale=ks, v_scale=vs)
+    assert int(st) == 0
+    table[7, 2], table[40, 0] = 4 * B, -5
+    out, _ = epd.ep_decode_attention(q, k, v, table, lens, ws, st, k_scale=ks, v_scale=vs)
+    assert int(st) == epd.EPD_ERR_CAPACITY
+    good = torch.ones(B, dtype=torch.bool, device=DEV)
+    good[[7, 40]] = False
+    assert torch.equal(out[good], full[good])
+    # as if the page's positions were not there
+    for b, rest in ((7, [0, 1, 3]), (40, [1, 2, 3])):
+        want, _ = attend(q[b:b + 1], values(k, ks), values(v, vs), table[b:b + 1, rest], lens[:1] - page)
+        size, _ = attend(q[b:b + 1], values(k, ks), values(v, vs).abs(), table[b:b + 1, rest], lens[:1] - page)
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -14 + (2.0 ** -11 if fp8 else 0)) * size
+        assert bool(((out[b].double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("power", [-125, -60, 60])
+def test_values_of_all_sizes(power):
+    """Values, and the scales of an e4m3 cache's, down to numbers below the smallest normal one."""
+    check([700, 33, 4000], 16, 2, 4, 128, True, v_power=power)
+    check([700, 33, 4000], 16, 2, 4, 128, False, v_power=power)
+
+
+def test_queries_of_all_sizes():
+    for fp8 in (False, True):
+        check([700, 33], 16, 2, 4, 128, fp8, q_scale=2.0 ** 115, scale=2.0 ** -118)
+        check([700, 33], 16, 2, 4, 128, fp8, q_scale=2.0 ** -115, scale=2.0 ** 112)
+
+
+def test_many_small_weights():
+    """One token of weight one among 2^17 of 2^-25.5 whose values count for more: the fp16 weights hold
+    them (to half a step, 2^-34 of the largest weight, times their number and value)."""
+    n, D = 2 ** 17, 64
+    k = torch.zeros(n // 64 + 1, 64, 1, D, device=DEV)
+    k[0, 0, 0, 0] = 448.0
+    v = torch.ones(n // 64 + 1, 64, 1, D, device=DEV)
+    v[0, 0] = 2.0 ** -6
+    k, v = k.to(torch.float8_e4m3fn), v.to(torch.float8_e4m3fn)
+    one = torch.ones(n // 64 + 1, 64, 1, device=DEV)
+    q = torch.zeros(1, 1, D, dtype=torch.bfloat16, device=DEV)
+    q[0, 0, 0] = 1.0
+    table, lens = torch.arange(n // 64 + 1, dtype=torch.int32, device=DEV).view(1, -1), torch.tensor([n + 1], dtype=torch.int32, device=DEV)
+    scale = 25.5 * math.log(2) / 448
+    st = epd.new_status(DEV)
+    out, _ = epd.ep_decode_attention(q, k, v, table, lens, epd.new_attention_workspace(1, 1, 1, D, DEV), st, k_scale=one, v_scale=one,
+                                     softmax_scale=scale)
+    want, _ = attend(q, k.double(), v.double(), table, lens, scale)
+    tol = (2.0 ** -8 + 2.0 ** -14 + 2.0 ** -11) * want.abs() + n * 2.0 ** -34
+    assert int(st) == 0 and bool(((out.double() - want).abs() <= tol).all())
 
 
 def test_scores_of_all_sizes():

@@ -6,14 +6,19 @@
 // 16 operations a byte at most. One pass with running maxima and sums.
 //
 // Split: a block's warps form teams, one for each of up to eight kv heads, so that a block reads
-// whole rows of a [page, row, head, dim] cache: rows of one head alone, 128 or 256 bytes out of
-// every one or two KB, are served at two thirds of the memory's rate. The (sequence, group of heads)
+// whole rows of a [page, row, head, dim] cache: of rows of one head alone, 128 bytes out of every KB
+// are served at two thirds of the memory's rate (128 sequences of 0 to 8191 tokens in e4m3, 64 heads
+// over 8 of 128: 248 us alone, 199 in teams; their 1.1 GB take 166) and 256 out of every two at 0.95
+// (bf16, 32 heads over 8: 345 and 329 us; 2.1 GB take 322). The (sequence, group of heads)
 // segments of the batch, each as many tiles of a team's tokens as its length needs, form one line of
 // tiles, and every block takes an equal run of it, whatever the lengths are (they are read on the
 // device). A segment that lies in one block's run is finished there, by each team for its head; of one
 // that several blocks share the parts go to the workspace, and the team that comes last joins its
 // head's in the blocks' order. Where the batch has few segments (a long context alone) the teams take
-// fewer heads with more warps each, so that the joins have fewer parts and more blocks for them.
+// fewer heads with more warps each, so that the joins have fewer parts and more blocks for them: one
+// sequence of 1000 tokens takes 8.5 us (0.6 for its 4 MB: two trips to memory for lengths and pages, one
+// for the tile, the counter's and the join's), two of 131072 to 200001 in e4m3, 64 heads over 4, 81.5
+// (350 MB take 52; the rest is instructions, the widening of every value before its product most of all).
 //
 // A warp has its own tokens of each tile, its own two stages in shared memory, filled by its own
 // asynchronous copies one tile ahead (past the ends of segments; page numbers are looked up one tile
@@ -40,12 +45,19 @@ namespace {
 constexpr int kMaxBlocks = 160;  // blocks that the workspace has room for
 constexpr int kMaxHeads = 16;    // query heads of a segment, at most
 constexpr int kMaxTeams = 8;
-constexpr int kUncut = 4;        // tiles of a segment that one block takes whole
+// Tiles of a segment that one block takes whole: a join costs as much as about four of them (256
+// sequences of 10 to 300 tokens: 44 us, 76 with all of them cut where the shares end; with 8 tiles one
+// sequence of 1000 tokens is left to 8 blocks, and takes 14.8 us instead of 8.5).
+constexpr int kUncut = 4;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLn2 = 0.6931471805599453f;
 // A maximum is moved (and everything summed so far scaled down) only when a score passes it by more
-// than 2^8: terms up to 2^8 lose nothing in 32 bits, and the scaling is rare.
-constexpr float kSlack = 8.0f;
+// than a factor: terms up to 2^8 lose nothing in 32 bits, and the scaling is rare. Of an e4m3 cache,
+// whose weights are fp16, it is 2^4, the largest value scale moves by factors of 4, and the weights
+// are 2^9 as large as they are: 2^15 at most, and in steps of 2^-33 or 2^-11 of their size, so that
+// what a quarter of a million tokens of small weights lose is far below the output's own rounding.
+constexpr float kSlack = 8.0f, kSlackFp8 = 4.0f;
+constexpr float kValueSlack = 4.0f, kWeightUp = 512.0f;
 
 struct AttnArgs {
     const uint8_t *q;
@@ -80,8 +92,9 @@ struct Shape {
     static constexpr int kJoinCols = kQueryInSmem ? (FP8 ? 32 : 64) : DP < 128 ? DP : 128, kJoinRow = kJoinCols + 4;
     static constexpr int kJoin = kWarps * kHeads * kJoinRow * 4;
     // One stage on the way (64 KB a multiprocessor) while another is read. More in flight fill the same
-    // memory system, but share it less evenly: of 152 blocks with equal runs the fastest then takes
-    // 256 us and the slowest 348 (128 sequences, 2.1 GB; 361 us in all), with two stages 303 and 337 (344).
+    // memory system, but share it less evenly: of 152 blocks with equal runs, each of one kv head's rows,
+    // the fastest then takes 256 us and the slowest 348 (128 sequences, 2.1 GB; 361 us in all), with
+    // two stages 303 and 337 (344).
     static constexpr int kStages = 2;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kSmem = kWarps * (kStages * kStage + kQuery) + kJoin;
@@ -528,6 +541,8 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
     if (!S::kQueryInSmem) load_query(s_cursor[warp]);
     const float *const scales = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(s_dyn) + warp * S::kStages * S::kStage + 2 * CH * S::kRow);
     int stage = 0;
+    // One loop over segments around one over tiles: what only a segment's ends need is out of the inner one's
+    // registers (with one loop for both, e4m3 heads of 256 spilled: 178 us, 64 sequences, where they take 109).
     for (int step = 0; step < steps;) {
         {  // a segment begins
             if (S::kQueryInSmem) load_query(s_cursor[warp]);
@@ -540,7 +555,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
 #pragma unroll
                 for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
                 // to [2^6, 2^7): the power of two from the exponent's bits
-                const int e = top > 0.0f ? min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 100) : 0;
+                const int e = top > 0.0f ? max((int)(__float_as_uint(top) >> 23) - 127, -120) : 0;
                 const float up = __uint_as_float((uint32_t)(127 + 6 - e) << 23);
                 q_scale = __uint_as_float((uint32_t)(127 - 6 + e) << 23) * a.scale_log2;
 #pragma unroll
@@ -569,189 +584,190 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
             v_ref = v_inv = 0.0f;
         }
         for (const int until = step + min(left, steps - step); step < until; ++step) {
-        copy_wait<S::kStages - 2>();
-        __syncwarp();
-        if (step + S::kStages - 1 < steps) {
-            load(stage == 0 ? S::kStages - 1 : stage - 1);
-            if (step + S::kStages < steps) go_on();
-        }
-        copy_commit();
+            copy_wait<S::kStages - 2>();
+            __syncwarp();
+            if (step + S::kStages - 1 < steps) {
+                load(stage == 0 ? S::kStages - 1 : stage - 1);
+                if (step + S::kStages < steps) go_on();
+            }
+            copy_commit();
 
-        const uint32_t at = ring + stage * S::kStage;
-        uint32_t mask;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(mask) : "r"(at + S::kStage - 16) : "memory");
-        if (mask) {
-            // s[t][n][i]: token 16 t + g + 8 (i / 2), head 8 n + 2 c + i % 2
-            float s[MT][NH][4] = {};
-            const int row = lane & 15, right = lane >> 4;
-            auto query = [&](int k, int n) {
-                return S::kQueryInSmem ? s_query[(k * NH + n) * 32 + lane] : make_uint2(q[k][n][0], q[k][n][1]);
-            };
-#pragma unroll
-            for (int k = 0; k < UNITS / 2; ++k)
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    uint32_t r[4];
-                    ldsm4(r, at + (t * 16 + row) * S::kRow + swizzle<UNITS>(row, 2 * k + right) * 16);
-                    if (FP8) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t f[4];
-                            widen4(r[2 * h], f[0], f[2]);
-                            widen4(r[2 * h + 1], f[1], f[3]);
-#pragma unroll
+            const uint32_t at = ring + stage * S::kStage;
+            uint32_t mask;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(mask) : "r"(at + S::kStage - 16) : "memory");
+            if (mask) {
+                // s[t][n][i]: token 16 t + g + 8 (i / 2), head 8 n + 2 c + i % 2
+                float s[MT][NH][4] = {};
+                const int row = lane & 15, right = lane >> 4;
+                auto query = [&](int k, int n) {
+                    return S::kQueryInSmem ? s_query[(k * NH + n) * 32 + lane] : make_uint2(q[k][n][0], q[k][n][1]);
+                };
+    #pragma unroll
+                for (int k = 0; k < UNITS / 2; ++k)
+    #pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        uint32_t r[4];
+                        ldsm4(r, at + (t * 16 + row) * S::kRow + swizzle<UNITS>(row, 2 * k + right) * 16);
+                        if (FP8) {
+    #pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t f[4];
+                                widen4(r[2 * h], f[0], f[2]);
+                                widen4(r[2 * h + 1], f[1], f[3]);
+    #pragma unroll
+                                for (int n = 0; n < NH; ++n) {
+                                    const uint2 b = query(2 * k + h, n);
+                                    mma<true>(s[t][n], f, b.x, b.y);
+                                }
+                            }
+                        } else {
+    #pragma unroll
                             for (int n = 0; n < NH; ++n) {
-                                const uint2 b = query(2 * k + h, n);
-                                mma<true>(s[t][n], f, b.x, b.y);
+                                const uint2 b = query(k, n);
+                                mma<false>(s[t][n], r, b.x, b.y);
+                            }
+                        }
+                    }
+                const float *const sc = scales + stage * (S::kStage / 4);
+    #pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    float f[2] = {a.scale_log2, a.scale_log2};
+                    if (FP8) {
+                        f[0] = q_scale * sc[16 * t + g];
+                        f[1] = q_scale * sc[16 * t + g + 8];
+                    }
+    #pragma unroll
+                    for (int n = 0; n < NH; ++n)
+    #pragma unroll
+                        for (int i = 0; i < 4; ++i) s[t][n][i] *= f[i >> 1];
+                }
+                if (mask != (CH == 32 ? kAll : 0xffffu)) {
+    #pragma unroll
+                    for (int t = 0; t < MT; ++t)
+    #pragma unroll
+                        for (int n = 0; n < NH; ++n)
+    #pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (!((mask >> (16 * t + g + 8 * (i >> 1))) & 1)) s[t][n][i] = -INFINITY;
+                }
+                float top[NH][2];
+                bool more = false;
+    #pragma unroll
+                for (int n = 0; n < NH; ++n)
+    #pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        top[n][i] = fmaxf(s[0][n][i], s[0][n][i + 2]);
+    #pragma unroll
+                        for (int t = 1; t < MT; ++t) top[n][i] = fmaxf(top[n][i], fmaxf(s[t][n][i], s[t][n][i + 2]));
+                        more |= top[n][i] > m[n][i] + (FP8 ? kSlackFp8 : kSlack);
+                    }
+                if (__any_sync(kAll, more)) {
+    #pragma unroll
+                    for (int n = 0; n < NH; ++n)
+    #pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float now = top[n][i];
+    #pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) now = fmaxf(now, __shfl_xor_sync(kAll, now, d));
+                            now = fmaxf(now, m[n][i]);
+                            const float f = m[n][i] == -INFINITY ? 0.0f : fast_exp2(m[n][i] - now);
+                            m[n][i] = now;
+                            l[n][i] *= f;
+    #pragma unroll
+                            for (int k = 0; k < KT; ++k) {
+                                o[k][n][i] *= f;
+                                o[k][n][i + 2] *= f;
+                            }
+                        }
+                }
+                float vs[MT][2];
+                if (FP8) {
+                    // the values' scales over the largest so far, which counts as no less than 2^-110: its inverse is finite
+                    bool larger = false;
+    #pragma unroll
+                    for (int t = 0; t < MT; ++t)
+    #pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            vs[t][i] = sc[CH + 16 * t + g + 8 * i];
+                            larger |= vs[t][i] > kValueSlack * kWeightUp * v_ref;
+                        }
+                    if (__any_sync(kAll, larger)) {
+                        float most = 0.0f;
+    #pragma unroll
+                        for (int t = 0; t < MT; ++t) most = fmaxf(most, fmaxf(vs[t][0], vs[t][1]));
+    #pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, d));
+                        most = fmaxf(most, 0x1p-110f) / kWeightUp;
+                        const float f = v_ref / most;
+                        v_ref = most;
+                        v_inv = 1.0f / most;
+    #pragma unroll
+                        for (int k = 0; k < KT; ++k)
+    #pragma unroll
+                            for (int i = 0; i < 4 * NH; ++i) o[k][i >> 2][i & 3] *= f;
+                    }
+    #pragma unroll
+                    for (int t = 0; t < MT; ++t)
+    #pragma unroll
+                        for (int i = 0; i < 2; ++i) vs[t][i] *= v_inv;
+                }
+                // the weights, turned from (token, head) to (head, token) fragments
+                uint32_t p[MT][NH][2], p_lo[MT][NH][2];
+    #pragma unroll
+                for (int n = 0; n < NH; ++n) {
+                    const float base[2] = {m[n][0] == -INFINITY ? 0.0f : m[n][0], m[n][1] == -INFINITY ? 0.0f : m[n][1]};
+    #pragma unroll
+                    for (int t = 0; t < MT; ++t)
+    #pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float x = fast_exp2(s[t][n][2 * i] - base[0]), y = fast_exp2(s[t][n][2 * i + 1] - base[1]);
+                            l[n][0] += x;
+                            l[n][1] += y;
+                            if (FP8) {
+                                p[t][n][i] = transpose8(pack2_f16(x * vs[t][i], y * vs[t][i]));
+                            } else {
+                                // the first part is cut off, not rounded, and the second at least 2^-100:
+                                // neither turns an infinite value's product into NaN
+                                const uint32_t hi = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+                                p[t][n][i] = transpose8(hi);
+                                p_lo[t][n][i] = transpose8(pack2_bf16(fmaxf(x - lo_bf16(hi), 0x1p-100f), fmaxf(y - hi_bf16(hi), 0x1p-100f)));
+                            }
+                        }
+                }
+                const uint32_t av = at + CH * S::kRow;
+    #pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    if (FP8) {
+                        // a 16-byte unit is 16 columns: its even ones are the first 8 rows, its odd ones the others
+    #pragma unroll
+                        for (int k = 0; k < UNITS / 2; ++k) {
+                            uint32_t r[4];
+                            ldsm4t(r, av + (t * 16 + row) * S::kRow + swizzle<UNITS>(row, 2 * k + right) * 16);
+    #pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t f[4];
+                                widen4(__byte_perm(r[2 * h], 0, 0x3120), f[0], f[1]);
+                                widen4(__byte_perm(r[2 * h + 1], 0, 0x3120), f[2], f[3]);
+    #pragma unroll
+                                for (int n = 0; n < NH; ++n) mma<true>(o[2 * k + h][n], f, p[t][n][0], p[t][n][1]);
                             }
                         }
                     } else {
-#pragma unroll
-                        for (int n = 0; n < NH; ++n) {
-                            const uint2 b = query(k, n);
-                            mma<false>(s[t][n], r, b.x, b.y);
-                        }
-                    }
-                }
-            const float *const sc = scales + stage * (S::kStage / 4);
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                float f[2] = {a.scale_log2, a.scale_log2};
-                if (FP8) {
-                    f[0] = q_scale * sc[16 * t + g];
-                    f[1] = q_scale * sc[16 * t + g + 8];
-                }
-#pragma unroll
-                for (int n = 0; n < NH; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[t][n][i] *= f[i >> 1];
-            }
-            if (mask != (CH == 32 ? kAll : 0xffffu)) {
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int n = 0; n < NH; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (!((mask >> (16 * t + g + 8 * (i >> 1))) & 1)) s[t][n][i] = -INFINITY;
-            }
-            float top[NH][2];
-            bool more = false;
-#pragma unroll
-            for (int n = 0; n < NH; ++n)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    top[n][i] = fmaxf(s[0][n][i], s[0][n][i + 2]);
-#pragma unroll
-                    for (int t = 1; t < MT; ++t) top[n][i] = fmaxf(top[n][i], fmaxf(s[t][n][i], s[t][n][i + 2]));
-                    more |= top[n][i] > m[n][i] + kSlack;
-                }
-            if (__any_sync(kAll, more)) {
-#pragma unroll
-                for (int n = 0; n < NH; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float now = top[n][i];
-#pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) now = fmaxf(now, __shfl_xor_sync(kAll, now, d));
-                        now = fmaxf(now, m[n][i]);
-                        const float f = m[n][i] == -INFINITY ? 0.0f : fast_exp2(m[n][i] - now);
-                        m[n][i] = now;
-                        l[n][i] *= f;
-#pragma unroll
+                        const int vrow = (lane & 7) + right * 8;
+    #pragma unroll
                         for (int k = 0; k < KT; ++k) {
-                            o[k][n][i] *= f;
-                            o[k][n][i + 2] *= f;
-                        }
-                    }
-            }
-            float vs[MT][2];
-            if (FP8) {
-                // the values' scales over the largest so far (up to 16 times it without moving it)
-                bool larger = false;
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        vs[t][i] = sc[CH + 16 * t + g + 8 * i];
-                        larger |= vs[t][i] > 16.0f * v_ref;
-                    }
-                if (__any_sync(kAll, larger)) {
-                    float most = 0.0f;
-#pragma unroll
-                    for (int t = 0; t < MT; ++t) most = fmaxf(most, fmaxf(vs[t][0], vs[t][1]));
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, d));
-                    const float f = v_ref / most;
-                    v_ref = most;
-                    v_inv = 1.0f / most;
-#pragma unroll
-                    for (int k = 0; k < KT; ++k)
-#pragma unroll
-                        for (int i = 0; i < 4 * NH; ++i) o[k][i >> 2][i & 3] *= f;
-                }
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) vs[t][i] *= v_inv;
-            }
-            // the weights, turned from (token, head) to (head, token) fragments
-            uint32_t p[MT][NH][2], p_lo[MT][NH][2];
-#pragma unroll
-            for (int n = 0; n < NH; ++n) {
-                const float base[2] = {m[n][0] == -INFINITY ? 0.0f : m[n][0], m[n][1] == -INFINITY ? 0.0f : m[n][1]};
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float x = fast_exp2(s[t][n][2 * i] - base[0]), y = fast_exp2(s[t][n][2 * i + 1] - base[1]);
-                        l[n][0] += x;
-                        l[n][1] += y;
-                        if (FP8) {
-                            p[t][n][i] = transpose8(pack2_f16(x * vs[t][i], y * vs[t][i]));
-                        } else {
-                            // the first part is cut off, not rounded, and the second at least 2^-100:
-                            // neither turns an infinite value's product into NaN
-                            const uint32_t hi = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-                            p[t][n][i] = transpose8(hi);
-                            p_lo[t][n][i] = transpose8(pack2_bf16(fmaxf(x - lo_bf16(hi), 0x1p-100f), fmaxf(y - hi_bf16(hi), 0x1p-100f)));
-                        }
-                    }
-            }
-            const uint32_t av = at + CH * S::kRow;
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                if (FP8) {
-                    // a 16-byte unit is 16 columns: its even ones are the first 8 rows, its odd ones the others
-#pragma unroll
-                    for (int k = 0; k < UNITS / 2; ++k) {
-                        uint32_t r[4];
-                        ldsm4t(r, av + (t * 16 + row) * S::kRow + swizzle<UNITS>(row, 2 * k + right) * 16);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t f[4];
-                            widen4(__byte_perm(r[2 * h], 0, 0x3120), f[0], f[1]);
-                            widen4(__byte_perm(r[2 * h + 1], 0, 0x3120), f[2], f[3]);
-#pragma unroll
-                            for (int n = 0; n < NH; ++n) mma<true>(o[2 * k + h][n], f, p[t][n][0], p[t][n][1]);
-                        }
-                    }
-                } else {
-                    const int vrow = (lane & 7) + right * 8;
-#pragma unroll
-                    for (int k = 0; k < KT; ++k) {
-                        uint32_t r[4];
-                        ldsm4t(r, av + (t * 16 + vrow) * S::kRow + swizzle<UNITS>(vrow, 2 * k + ((lane >> 3) & 1)) * 16);
-#pragma unroll
-                        for (int n = 0; n < NH; ++n) {
-                            mma<false>(o[k][n], r, p[t][n][0], p[t][n][1]);
-                            mma<false>(o[k][n], r, p_lo[t][n][0], p_lo[t][n][1]);
+                            uint32_t r[4];
+                            ldsm4t(r, av + (t * 16 + vrow) * S::kRow + swizzle<UNITS>(vrow, 2 * k + ((lane >> 3) & 1)) * 16);
+    #pragma unroll
+                            for (int n = 0; n < NH; ++n) {
+                                mma<false>(o[k][n], r, p[t][n][0], p[t][n][1]);
+                                mma<false>(o[k][n], r, p_lo[t][n][0], p_lo[t][n][1]);
+                            }
                         }
                     }
                 }
             }
-        }
-        if (++stage == S::kStages) stage = 0;
+            if (++stage == S::kStages) stage = 0;
         }
 
         {
