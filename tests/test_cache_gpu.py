@@ -60,6 +60,29 @@ def test_rotary(T, N, D, R, interleaved):
 
 
 @pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,R", [(128, 64), (80, 24), (40, 10)])
+def test_rest_of_a_head_is_carried_over(D, R, interleaved):
+    """Infinities, negative zeros and NaN beside one another too, each for itself."""
+    def same(a, b):
+        return bool(((a.contiguous().view(torch.int16) == b.contiguous().view(torch.int16)) | (a.isnan() & b.isnan())).all())
+    x = torch.zeros(3, 2, D, dtype=torch.bfloat16, device=DEV)
+    odd = torch.tensor([float("inf"), 1.0, float("nan"), -0.0, -float("inf"), 3.0, 0.0, 2.0 ** -133], device=DEV).bfloat16()
+    x[..., R:] = odd.repeat(D)[:D - R]
+    x[1, :, R:] = odd.flip(0).repeat(D)[1:D - R + 1]
+    steps = epd.rotary_steps(epd.rotary_frequencies(R)[0], DEV)
+    pos = torch.arange(3, dtype=torch.int32, device=DEV)
+    got = epd.ep_rotary(x, pos, steps, interleaved=interleaved, rotary_scale=1.5)
+    assert same(got[..., R:], x[..., R:])
+    # queries and keys on the way into a cache; the values are carried over whole
+    k, v = (torch.zeros(3, 1, 2, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    table, st = torch.arange(3, dtype=torch.int32, device=DEV).view(3, 1), epd.new_status(DEV)
+    pos = torch.zeros(3, dtype=torch.int32, device=DEV)
+    q = epd.ep_cache_append(x, x, k, v, table, pos, st, q=x, steps=steps, interleaved=interleaved, rotary_scale=1.5)
+    assert int(st) == 0
+    assert same(q[..., R:], x[..., R:]) and same(k[:, 0, :, R:], x[..., R:]) and same(v[:, 0], x)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
 def test_rotary_gradient(interleaved):
     """<dy, rotate(x)> has the gradient rotate_inverse(dy): by the formula's own derivative and by differences."""
     x, dy, d = rand(9, 3, 64), rand(9, 3, 64, seed=1), rand(9, 3, 64, seed=2)

@@ -27,18 +27,18 @@ __device__ __forceinline__ uint4 pack8_bf16(const float (&f)[8]) {
                       pack2_bf16(f[6], f[7]));
 }
 
-// v / scale to a unit or two in the last place, by one division for all of them; a scale whose
-// reciprocal may overflow divides each.
+// v / scale to a unit or two in the last place, by one division for all of them; where its reciprocal
+// may overflow, both are taken 2^100 up first.
 template <int N>
 __device__ __forceinline__ void divide_all(float (&v)[N], float scale) {
-    if (scale >= 0x1p-120f) {
-        const float inv = __fdiv_rn(1.0f, scale);
+    if (scale < 0x1p-120f) {
+        scale *= 0x1p100f;
 #pragma unroll
-        for (int j = 0; j < N; ++j) v[j] *= inv;
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) v[j] = __fdiv_rn(v[j], scale);
+        for (int j = 0; j < N; ++j) v[j] *= 0x1p100f;
     }
+    const float inv = __fdiv_rn(1.0f, scale);
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] *= inv;
 }
 
 constexpr float kInvSqrt2Pi = 0.39894228040143267794f;

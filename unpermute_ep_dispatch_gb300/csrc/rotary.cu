@@ -7,11 +7,11 @@
 // without the cancellation that a product in 32 bits (or a range reduction) has at far positions, and
 // without 64-bit floating point, of which this GPU has little.
 //
-// Bound by HBM: every value is read and written once. A head is cut into chunks of V pairs, one a
-// lane, in groups of a power of two of lanes a head; a warp takes its token's heads several at a
-// time, with the loads of up to four such passes in flight, and the lane's sines and cosines serve
-// all of them. What is not rotated travels as pairs of angle zero. In an e4m3 cache every token and
-// head has its own scale, amax / 448, from the head's lanes by shuffles.
+// Bound by HBM: every value is read and written once (16384 tokens of 64 heads of 128: 79.7 us, 80.4 at
+// a copy's rate). A head is cut into chunks of V pairs, one a lane, in groups of a power of two of lanes
+// a head; a warp takes its token's heads several at a time, with the loads of a few such passes in
+// flight, and the lane's sines and cosines serve all of them. What is not rotated is carried over as it is. In an e4m3 cache every token and head has
+// its own scale, amax / 448, from the head's lanes by shuffles.
 #include <cuda_fp8.h>
 
 #include <type_traits>
@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kThreads = 128;
 template <int V>
-constexpr int kBatch = V == 8 ? 4 : 8;  // passes whose loads are in flight at once: 128 bytes a lane
+constexpr int kBatch = V == 8 ? 4 : 8;  // passes of ep_rotary whose loads are in flight at once: 128 bytes a lane
 constexpr unsigned kAll = 0xffffffffu;
 
 struct Turn {
@@ -139,29 +139,32 @@ struct Raw {
             }
         }
     }
-};
-
-template <int V, bool INTER>
-__device__ __forceinline__ void store_bf16(uint8_t *head, const Place<V, INTER> &at, const float (&a)[V], const float (&b)[V]) {
-    if constexpr (V == 1) {
-        const uint32_t w = pack2_bf16(a[0], b[0]);
-        if (INTER) {
-            *reinterpret_cast<uint32_t *>(head + 2 * at.a) = w;
-        } else {
-            reinterpret_cast<uint16_t *>(head)[at.a] = (uint16_t)w;
-            reinterpret_cast<uint16_t *>(head)[at.b] = (uint16_t)(w >> 16);
+    // Takes the values if `on`, and stays what it was otherwise.
+    __device__ __forceinline__ void take(const float (&a)[V], const float (&b)[V], bool on) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t x = INTER || V == 1 ? pack2_bf16(a[i], b[i]) : i < V / 2 ? pack2_bf16(a[2 * i % V], a[(2 * i + 1) % V])
+                                                                                    : pack2_bf16(b[2 * i % V], b[(2 * i + 1) % V]);
+            w[i] = on ? x : w[i];
         }
-    } else if constexpr (INTER) {
-        st16(head + 2 * at.a, make_uint4(pack2_bf16(a[0], b[0]), pack2_bf16(a[1], b[1]), pack2_bf16(a[2], b[2]),
-                                         pack2_bf16(a[3], b[3])));
-    } else if constexpr (V == 4) {
-        *reinterpret_cast<uint2 *>(head + 2 * at.a) = make_uint2(pack2_bf16(a[0], a[1]), pack2_bf16(a[2], a[3]));
-        *reinterpret_cast<uint2 *>(head + 2 * at.b) = make_uint2(pack2_bf16(b[0], b[1]), pack2_bf16(b[2], b[3]));
-    } else {
-        st16(head + 2 * at.a, pack8_bf16(a));
-        st16(head + 2 * at.b, pack8_bf16(b));
     }
-}
+    __device__ __forceinline__ void store(uint8_t *head, const Place<V, INTER> &at) const {
+        if constexpr (V == 8) {
+            st16(head + 2 * at.a, make_uint4(w[0], w[1], w[2], w[3]));
+            st16(head + 2 * at.b, make_uint4(w[4], w[5], w[6], w[7]));
+        } else if constexpr (V == 4 && INTER) {
+            st16(head + 2 * at.a, make_uint4(w[0], w[1], w[2], w[3]));
+        } else if constexpr (V == 4) {
+            *reinterpret_cast<uint2 *>(head + 2 * at.a) = make_uint2(w[0], w[1]);
+            *reinterpret_cast<uint2 *>(head + 2 * at.b) = make_uint2(w[2], w[3]);
+        } else if constexpr (INTER) {
+            *reinterpret_cast<uint32_t *>(head + 2 * at.a) = w[0];
+        } else {
+            reinterpret_cast<uint16_t *>(head)[at.a] = (uint16_t)w[0];
+            reinterpret_cast<uint16_t *>(head)[at.b] = (uint16_t)(w[0] >> 16);
+        }
+    }
+};
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
@@ -195,23 +198,22 @@ __device__ __forceinline__ void store_e4m3(uint8_t *head, const Place<V, INTER> 
     }
 }
 
-// Cosines and sines of chunk p's pairs at a position, times the scale; 1 and 0 past the rotated part.
+// Cosines and sines of chunk p's pairs at a position, times the scale, where they are rotated.
 // The hardware's sine and cosine of an angle within [-pi, pi] are off by 2^-20.5 at most, a 2000th of a
 // step of the bf16 that they go into.
 template <int V>
-__device__ __forceinline__ void angles(const Turn &t, int p, int position, float (&c)[V], float (&s)[V]) {
-    const bool turned = p < t.R / (2 * V);
+__device__ __forceinline__ bool angles(const Turn &t, int p, int position, float (&c)[V], float (&s)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = s[i] = 0.0f;
+    if (p >= t.R / (2 * V)) return false;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        c[i] = 1.0f;
-        s[i] = 0.0f;
-        if (turned) {
-            const uint64_t phase = (uint64_t)(int64_t)position * __ldg(t.step + p * V + i);
-            const float angle = (float)(int32_t)(phase >> 32) * 1.4629180792671596e-9f;  // pi / 2^31
-            c[i] = __cosf(angle) * t.scale;
-            s[i] = __sinf(angle) * (t.inverse ? -t.scale : t.scale);
-        }
+        const uint64_t phase = (uint64_t)(int64_t)position * __ldg(t.step + p * V + i);
+        const float angle = (float)(int32_t)(phase >> 32) * 1.4629180792671596e-9f;  // pi / 2^31
+        c[i] = __cosf(angle) * t.scale;
+        s[i] = __sinf(angle) * (t.inverse ? -t.scale : t.scale);
     }
+    return true;
 }
 
 template <int V>
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
     for (int p = lane & (lanes - 1); p < a.walk.chunks; p += lanes) {
         const Place<V, INTER> at(p, a.turn.R, a.D);
         float c[V], s[V];
-        angles<V>(a.turn, p, position, c, s);
+        const bool on = angles<V>(a.turn, p, position, c, s);
         for (int i0 = 0; i0 < a.walk.passes; i0 += kBatch<V>) {
             Raw<V, INTER> raw[kBatch<V>];
 #pragma unroll
@@ -263,16 +265,22 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
                     float u[V], w[V];
                     raw[i].values(u, w);
                     rotate<V>(u, w, c, s);
-                    store_bf16<V, INTER>(out + n * a.out_head, at, u, w);
+                    raw[i].take(u, w, on);
+                    raw[i].store(out + n * a.out_head, at);
                 }
             }
         }
     }
 }
 
-// NP: chunks of a head that one lane holds (V == 1 only).
+// NP: chunks of a head that one lane holds (V == 1 only). Bound by HBM, and by how many warps there are to
+// wait for it: 16384 tokens of 64 + 2 x 8 heads of 128 take 98 us into an e4m3 cache, half a head rotated
+// interleaved (0.64 GB: 96), and 100 into a bf16 one (100). With whole batches of 8 passes and 90 to 130
+// registers a thread, five blocks or fewer a multiprocessor, they took 116 and 108, and with halves of a
+// whole head rotated (V == 8) 140, where these limits give 99. An e4m3 cache of 16 + 2 x 16 heads takes
+// 68 (51): the conversion's instructions.
 template <int V, bool INTER, bool FP8, int NP>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, V == 4 ? 9 : V == 8 ? 6 : 1) append_kernel(AppendArgs a) {
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
@@ -304,13 +312,16 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
     };
     const int lanes_log = a.rows.lanes_log, lanes = 1 << lanes_log, per_pass = 32 >> lanes_log;
     const int p0 = lane & (lanes - 1);
-    // A warp has queries, keys or values only. `src` and the heads of a token's part; put(n, pass's
-    // chunks) stores head n.
-    auto heads = [&](const uint8_t *src, const Walk &walk, auto is_turned, auto is_held, auto put) {
-        constexpr bool turned = decltype(is_turned)::value, scaled = decltype(is_held)::value && FP8;
-        constexpr int B = NP > 1 ? 1 : scaled ? 4 : kBatch<V>;
+    // A warp has queries, keys or values only: from `src`, `turned` or not, to heads `step` apart at `to`
+    // (held: in the cache, at the token's slot, with `scales` in an e4m3 one). Keys and values share their
+    // code: a warp runs through it once or twice, and waits for instructions where there is more of it.
+    auto heads = [&](const uint8_t *src, const Walk &walk, bool turned, auto is_held, uint8_t *to, int64_t step, float *scales) {
+        constexpr bool held = decltype(is_held)::value, scaled = held && FP8;
+        constexpr int B = NP > 1 ? 1 : scaled ? 2 : 4;
         const int first = part * walk.passes * per_pass + (lane >> lanes_log);
         float c[NP][V], s[NP][V];
+        bool on[NP];
+#pragma unroll 1
         for (int i0 = 0; i0 < walk.passes; i0 += B) {
             Raw<V, INTER> raw[B][NP];
 #pragma unroll
@@ -323,28 +334,20 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
                         raw[i][q].load(src + (int64_t)n * D * 2, Place<V, INTER>(p0 + q * lanes, a.turn.R, D));
             }
             if (i0 == 0) {  // with the first values on the way: the slot takes two dependent loads
-                if (turned) {
 #pragma unroll
-                    for (int q = 0; q < NP; ++q) angles<V>(a.turn, p0 + q * lanes, position, c[q], s[q]);
-                }
+                for (int q = 0; q < NP; ++q) on[q] = angles<V>(a.turn, turned ? p0 + q * lanes : INT32_MAX, position, c[q], s[q]);
                 if (!find_slot()) return;
             }
-            // a batch's scales are found together: each is a chain of exchanges
-            float u[scaled ? B : 1][NP][V], w[scaled ? B : 1][NP][V], scale[B];
-            auto turn = [&](int i, int to) {
-#pragma unroll
-                for (int q = 0; q < NP; ++q) {
-                    raw[i][q].values(u[to][q], w[to][q]);
-                    if (turned) rotate<V>(u[to][q], w[to][q], c[q], s[q]);
-                }
-            };
-            if (scaled) {
+            if constexpr (scaled) {
+                // a batch's scales are found together: each is a chain of exchanges
+                float u[B][NP][V], w[B][NP][V], scale[B];
 #pragma unroll
                 for (int i = 0; i < B; ++i) {
-                    turn(i, i);
                     scale[i] = 0.0f;
 #pragma unroll
                     for (int q = 0; q < NP; ++q) {
+                        raw[i][q].values(u[i][q], w[i][q]);
+                        if (on[q]) rotate<V>(u[i][q], w[i][q], c[q], s[q]);
                         float top = 0.0f;
 #pragma unroll
                         for (int j = 0; j < V; ++j) top = fmaxf(top, fmaxf(fabsf(u[i][q][j]), fabsf(w[i][q][j])));
@@ -358,44 +361,45 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a) {
                         const float other = __shfl_xor_sync(kAll, scale[i], d);
                         if (d < lanes) scale[i] = fmaxf(scale[i], other);
                     }
-            }
 #pragma unroll
-            for (int i = 0; i < B; ++i) {
-                const int n = first + (i0 + i) * per_pass;
-                if (i0 + i >= walk.passes || n >= walk.heads) continue;
-                if (scaled) scale[i] = scale[i] > 0.0f ? __fdiv_rn(scale[i], 448.0f) : 1.0f;
-                else turn(i, 0);
-                const int k = scaled ? i : 0;
+                for (int i = 0; i < B; ++i) {
+                    const int n = first + (i0 + i) * per_pass;
+                    if (i0 + i >= walk.passes || n >= walk.heads) continue;
+                    const float by = scale[i] > 0.0f ? __fdiv_rn(scale[i], 448.0f) : 1.0f;
+                    uint8_t *const head = to + slot + n * step;
 #pragma unroll
-                for (int q = 0; q < NP; ++q)
-                    if (p0 + q * lanes < walk.chunks) put(n, Place<V, INTER>(p0 + q * lanes, a.turn.R, D), u[k][q], w[k][q], scaled ? scale[i] : 1.0f);
+                    for (int q = 0; q < NP; ++q)
+                        if (p0 + q * lanes < walk.chunks)
+                            store_e4m3<V, INTER>(head, Place<V, INTER>(p0 + q * lanes, a.turn.R, D), u[i][q], w[i][q], by);
+                    if (p0 == 0) scales[scale_slot + n * kv.scale_head_stride] = by;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < B; ++i) {
+                    const int n = first + (i0 + i) * per_pass;
+                    if (i0 + i >= walk.passes || n >= walk.heads) continue;
+                    uint8_t *const head = to + 2 * (held ? slot : 0) + n * step * 2;
+#pragma unroll
+                    for (int q = 0; q < NP; ++q) {
+                        float u[V], w[V];
+                        raw[i][q].values(u, w);
+                        rotate<V>(u, w, c[q], s[q]);
+                        raw[i][q].take(u, w, on[q]);
+                        if (p0 + q * lanes < walk.chunks) raw[i][q].store(head, Place<V, INTER>(p0 + q * lanes, a.turn.R, D));
+                    }
+                }
             }
         }
     };
     if (part < a.queries.parts) {
-        uint8_t *const out = a.q_out + t * a.q_out_token;
-        heads(a.q + t * a.q_token, a.queries, std::true_type{}, std::false_type{},
-              [&](int n, const Place<V, INTER> &at, float(&u)[V], float(&w)[V], float) { store_bf16<V, INTER>(out + (int64_t)n * D * 2, at, u, w); });
+        heads(a.q + t * a.q_token, a.queries, true, std::false_type{}, a.q_out + t * a.q_out_token, D, nullptr);
         return;
     }
-    auto hold = [&](void *base, float *scales) {
-        return [=, &kv, &slot, &scale_slot](int n, const Place<V, INTER> &at, float(&u)[V], float(&w)[V], float scale) {
-            const int64_t off = slot + n * kv.head_stride;
-            if (FP8) {
-                store_e4m3<V, INTER>(static_cast<uint8_t *>(base) + off, at, u, w, scale);
-                if (at.a == 0) scales[scale_slot + n * kv.scale_head_stride] = scale;
-            } else {
-                store_bf16<V, INTER>(static_cast<uint8_t *>(base) + 2 * off, at, u, w);
-            }
-        };
-    };
     part -= a.queries.parts;
-    if (part < a.rows.parts) {
-        heads(a.k + t * a.k_token, a.rows, std::true_type{}, std::true_type{}, hold(kv.k, kv.k_scale));
-    } else {
-        part -= a.rows.parts;
-        heads(a.v + t * a.v_token, a.rows, std::false_type{}, std::true_type{}, hold(kv.v, kv.v_scale));
-    }
+    const bool key = part < a.rows.parts;
+    if (!key) part -= a.rows.parts;
+    heads(key ? a.k + t * a.k_token : a.v + t * a.v_token, a.rows, key, std::true_type{}, static_cast<uint8_t *>(key ? kv.k : kv.v),
+          kv.head_stride, key ? kv.k_scale : kv.v_scale);
 }
 
 // Chunks of V pairs: 16-byte words where the rotated part and the rest both split into them, 8-byte
@@ -406,7 +410,7 @@ inline int pairs_of_chunk(int D, int R, bool inter) {
 }
 
 // `columns` of each of `heads` heads of T tokens in chunks of V pairs. A warp takes several passes
-// over a token's heads, up to three or two batches, where that leaves 16 warps for each
+// over a token's heads, up to 12 or 16, where that leaves 16 warps for each
 // multiprocessor: the sines and cosines are then shared by more heads.
 inline Walk walk_of(int T, int heads, int columns, int V) {
     Walk w;
