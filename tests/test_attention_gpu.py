@@ -177,6 +177,32 @@ def test_queries_of_all_sizes():
         check([700, 33], 16, 2, 4, 128, fp8, q_scale=2.0 ** -115, scale=2.0 ** 112)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("G", [8, 16])
+def test_heads_of_a_group_stand_alone(G, fp8):
+    """Queries of infinities, NaN and of very different sizes beside one another, over the same keys."""
+    g = gen(13)
+    KH, D, n = 2, 128, 300
+    k, v, ks, vs = paged(n, 1, KH, D, fp8, DEV, g)
+    k[..., 0] = 0
+    q = torch.randn(1, KH * G, D, generator=g, device=DEV).bfloat16()
+    q[0, 1] = float("inf")
+    q[0, 2, 7] = float("nan")
+    q[0, 3, 0] = 2.0 ** 100  # of no weight: the keys are 0 there
+    q[0, 5] *= 2.0 ** -60
+    q[0, G + 4, 5] = -float("inf")
+    table, lens = torch.arange(n, dtype=torch.int32, device=DEV).view(1, n), torch.tensor([n], dtype=torch.int32, device=DEV)
+    st = epd.new_status(DEV)
+    out, _ = epd.ep_decode_attention(q, k, v, table, lens, epd.new_attention_workspace(1, KH * G, KH, D, DEV), st, k_scale=ks, v_scale=vs)
+    bad = [1, 2, G + 4]
+    good = [h for h in range(KH * G) if h not in bad + [3]]
+    assert int(st) == 0 and bool(out[0, bad].isnan().all())
+    want, _ = attend(q, values(k, ks), values(v, vs), table, lens)
+    size, _ = attend(q, values(k, ks), values(v, vs).abs(), table, lens)
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -14 + (2.0 ** -11 if fp8 else 0)) * size
+    assert bool(((out.double() - want).abs() <= tol)[0, good].all())
+
+
 def test_many_small_weights():
     """One token of weight one among 2^17 of 2^-25.5 whose values count for more: the fp16 weights hold
     them (to half a step, 2^-34 of the largest weight, times their number and value)."""

@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
     // ---- the line. o[k][n][i]: column 16 k + g + 8 (i / 2) (e4m3: 16 k + 2 g + i / 2) of head
     // 8 n + 2 c + i % 2; m and l: of heads 8 n + 2 c, 8 n + 2 c + 1, l of the lane's own tokens
     uint32_t q[KT][NH][2];
-    float o[KT][NH][4], m[NH][2], l[NH][2], q_scale = 1.0f, v_ref = 0.0f, v_inv = 0.0f;
+    float o[KT][NH][4], m[NH][2], l[NH][2], q_scale[NH][2], v_ref = 0.0f, v_inv = 0.0f;
     // Fragments of the query: head g, and the columns that the keys' fragments pair with them -- of a
     // 16-byte unit of an e4m3 row a lane holds four neighbours.
     auto load_query = [&](const Cursor &at) {
@@ -547,23 +547,26 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
         {  // a segment begins
             if (S::kQueryInSmem) load_query(s_cursor[warp]);
             if (FP8) {
-                float top = 0.0f;
 #pragma unroll
-                for (int k = 0; k < KT; ++k)
+                for (int n = 0; n < NH; ++n) {
+                    float top = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 2 * NH; ++i) top = fmaxf(top, fmaxf(fabsf(lo_bf16(q[k][i >> 1][i & 1])), fabsf(hi_bf16(q[k][i >> 1][i & 1]))));
+                    for (int k = 0; k < KT; ++k)
 #pragma unroll
-                for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
-                // to [2^6, 2^7): the power of two from the exponent's bits
-                const int e = top > 0.0f ? max((int)(__float_as_uint(top) >> 23) - 127, -120) : 0;
-                const float up = __uint_as_float((uint32_t)(127 + 6 - e) << 23);
-                q_scale = __uint_as_float((uint32_t)(127 - 6 + e) << 23) * a.scale_log2;
+                        for (int i = 0; i < 2; ++i) top = fmaxf(top, fmaxf(fabsf(lo_bf16(q[k][n][i])), fabsf(hi_bf16(q[k][n][i]))));
+                    top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+                    // the head's largest to [2^6, 2^(6+1)): the power of two from the exponent's bits
+                    const int e = top > 0.0f ? max((int)(__float_as_uint(top) >> 23) - 127, -120) : 0;
+                    const float up = __uint_as_float((uint32_t)(127 + 6 - e) << 23);
+                    const float down = e < 128 ? __uint_as_float((uint32_t)(127 - 6 + e) << 23) * a.scale_log2 : NAN;
+                    q_scale[n][0] = __shfl_sync(kAll, down, 8 * c);
+                    q_scale[n][1] = __shfl_sync(kAll, down, 8 * c + 4);
 #pragma unroll
-                for (int k = 0; k < KT; ++k)
-#pragma unroll
-                    for (int n = 0; n < NH; ++n)
+                    for (int k = 0; k < KT; ++k)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) q[k][n][i] = pack2_f16(lo_bf16(q[k][n][i]) * up, hi_bf16(q[k][n][i]) * up);
+                }
             }
             if (S::kQueryInSmem) {
                 // every warp of the team has all of it: each writes its share
@@ -602,26 +605,26 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
                 auto query = [&](int k, int n) {
                     return S::kQueryInSmem ? s_query[(k * NH + n) * 32 + lane] : make_uint2(q[k][n][0], q[k][n][1]);
                 };
-    #pragma unroll
+#pragma unroll
                 for (int k = 0; k < UNITS / 2; ++k)
-    #pragma unroll
+#pragma unroll
                     for (int t = 0; t < MT; ++t) {
                         uint32_t r[4];
                         ldsm4(r, at + (t * 16 + row) * S::kRow + swizzle<UNITS>(row, 2 * k + right) * 16);
                         if (FP8) {
-    #pragma unroll
+#pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 uint32_t f[4];
                                 widen4(r[2 * h], f[0], f[2]);
                                 widen4(r[2 * h + 1], f[1], f[3]);
-    #pragma unroll
+#pragma unroll
                                 for (int n = 0; n < NH; ++n) {
                                     const uint2 b = query(2 * k + h, n);
                                     mma<true>(s[t][n], f, b.x, b.y);
                                 }
                             }
                         } else {
-    #pragma unroll
+#pragma unroll
                             for (int n = 0; n < NH; ++n) {
                                 const uint2 b = query(k, n);
                                 mma<false>(s[t][n], r, b.x, b.y);
@@ -629,51 +632,47 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
                         }
                     }
                 const float *const sc = scales + stage * (S::kStage / 4);
-    #pragma unroll
+#pragma unroll
                 for (int t = 0; t < MT; ++t) {
-                    float f[2] = {a.scale_log2, a.scale_log2};
-                    if (FP8) {
-                        f[0] = q_scale * sc[16 * t + g];
-                        f[1] = q_scale * sc[16 * t + g + 8];
-                    }
-    #pragma unroll
+                    const float f[2] = {FP8 ? sc[16 * t + g] : a.scale_log2, FP8 ? sc[16 * t + g + 8] : 0.0f};
+#pragma unroll
                     for (int n = 0; n < NH; ++n)
-    #pragma unroll
-                        for (int i = 0; i < 4; ++i) s[t][n][i] *= f[i >> 1];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[t][n][i] *= FP8 ? q_scale[n][i & 1] * f[i >> 1] : f[0];
                 }
                 if (mask != (CH == 32 ? kAll : 0xffffu)) {
-    #pragma unroll
+#pragma unroll
                     for (int t = 0; t < MT; ++t)
-    #pragma unroll
+#pragma unroll
                         for (int n = 0; n < NH; ++n)
-    #pragma unroll
+#pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 if (!((mask >> (16 * t + g + 8 * (i >> 1))) & 1)) s[t][n][i] = -INFINITY;
                 }
                 float top[NH][2];
                 bool more = false;
-    #pragma unroll
+#pragma unroll
                 for (int n = 0; n < NH; ++n)
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         top[n][i] = fmaxf(s[0][n][i], s[0][n][i + 2]);
-    #pragma unroll
+#pragma unroll
                         for (int t = 1; t < MT; ++t) top[n][i] = fmaxf(top[n][i], fmaxf(s[t][n][i], s[t][n][i + 2]));
                         more |= top[n][i] > m[n][i] + (FP8 ? kSlackFp8 : kSlack);
                     }
                 if (__any_sync(kAll, more)) {
-    #pragma unroll
+#pragma unroll
                     for (int n = 0; n < NH; ++n)
-    #pragma unroll
+#pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             float now = top[n][i];
-    #pragma unroll
+#pragma unroll
                             for (int d = 4; d < 32; d <<= 1) now = fmaxf(now, __shfl_xor_sync(kAll, now, d));
                             now = fmaxf(now, m[n][i]);
                             const float f = m[n][i] == -INFINITY ? 0.0f : fast_exp2(m[n][i] - now);
                             m[n][i] = now;
                             l[n][i] *= f;
-    #pragma unroll
+#pragma unroll
                             for (int k = 0; k < KT; ++k) {
                                 o[k][n][i] *= f;
                                 o[k][n][i + 2] *= f;
@@ -684,41 +683,41 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
                 if (FP8) {
                     // the values' scales over the largest so far, which counts as no less than 2^-110: its inverse is finite
                     bool larger = false;
-    #pragma unroll
+#pragma unroll
                     for (int t = 0; t < MT; ++t)
-    #pragma unroll
+#pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             vs[t][i] = sc[CH + 16 * t + g + 8 * i];
                             larger |= vs[t][i] > kValueSlack * kWeightUp * v_ref;
                         }
                     if (__any_sync(kAll, larger)) {
                         float most = 0.0f;
-    #pragma unroll
+#pragma unroll
                         for (int t = 0; t < MT; ++t) most = fmaxf(most, fmaxf(vs[t][0], vs[t][1]));
-    #pragma unroll
+#pragma unroll
                         for (int d = 4; d < 32; d <<= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, d));
                         most = fmaxf(most, 0x1p-110f) / kWeightUp;
                         const float f = v_ref / most;
                         v_ref = most;
                         v_inv = 1.0f / most;
-    #pragma unroll
+#pragma unroll
                         for (int k = 0; k < KT; ++k)
-    #pragma unroll
+#pragma unroll
                             for (int i = 0; i < 4 * NH; ++i) o[k][i >> 2][i & 3] *= f;
                     }
-    #pragma unroll
+#pragma unroll
                     for (int t = 0; t < MT; ++t)
-    #pragma unroll
+#pragma unroll
                         for (int i = 0; i < 2; ++i) vs[t][i] *= v_inv;
                 }
                 // the weights, turned from (token, head) to (head, token) fragments
                 uint32_t p[MT][NH][2], p_lo[MT][NH][2];
-    #pragma unroll
+#pragma unroll
                 for (int n = 0; n < NH; ++n) {
                     const float base[2] = {m[n][0] == -INFINITY ? 0.0f : m[n][0], m[n][1] == -INFINITY ? 0.0f : m[n][1]};
-    #pragma unroll
+#pragma unroll
                     for (int t = 0; t < MT; ++t)
-    #pragma unroll
+#pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const float x = fast_exp2(s[t][n][2 * i] - base[0]), y = fast_exp2(s[t][n][2 * i + 1] - base[1]);
                             l[n][0] += x;
@@ -735,30 +734,30 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
                         }
                 }
                 const uint32_t av = at + CH * S::kRow;
-    #pragma unroll
+#pragma unroll
                 for (int t = 0; t < MT; ++t) {
                     if (FP8) {
                         // a 16-byte unit is 16 columns: its even ones are the first 8 rows, its odd ones the others
-    #pragma unroll
+#pragma unroll
                         for (int k = 0; k < UNITS / 2; ++k) {
                             uint32_t r[4];
                             ldsm4t(r, av + (t * 16 + row) * S::kRow + swizzle<UNITS>(row, 2 * k + right) * 16);
-    #pragma unroll
+#pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 uint32_t f[4];
                                 widen4(__byte_perm(r[2 * h], 0, 0x3120), f[0], f[1]);
                                 widen4(__byte_perm(r[2 * h + 1], 0, 0x3120), f[2], f[3]);
-    #pragma unroll
+#pragma unroll
                                 for (int n = 0; n < NH; ++n) mma<true>(o[2 * k + h][n], f, p[t][n][0], p[t][n][1]);
                             }
                         }
                     } else {
                         const int vrow = (lane & 7) + right * 8;
-    #pragma unroll
+#pragma unroll
                         for (int k = 0; k < KT; ++k) {
                             uint32_t r[4];
                             ldsm4t(r, av + (t * 16 + vrow) * S::kRow + swizzle<UNITS>(vrow, 2 * k + ((lane >> 3) & 1)) * 16);
-    #pragma unroll
+#pragma unroll
                             for (int n = 0; n < NH; ++n) {
                                 mma<false>(o[k][n], r, p[t][n][0], p[t][n][1]);
                                 mma<false>(o[k][n], r, p_lo[t][n][0], p_lo[t][n][1]);
