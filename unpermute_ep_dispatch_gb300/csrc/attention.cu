@@ -18,7 +18,9 @@
 // fewer heads with more warps each, so that the joins have fewer parts and more blocks for them: one
 // sequence of 1000 tokens takes 8.5 us (0.6 for its 4 MB: two trips to memory for lengths and pages, one
 // for the tile, the counter's and the join's), two of 131072 to 200001 in e4m3, 64 heads over 4, 81.5
-// (350 MB take 52; the rest is instructions, the widening of every value before its product most of all).
+// (350 MB take 52; 8 go into start and joins, and the rest is the chain of a tile's instructions, the
+// widening of every value before its product among them, with two warps on a scheduler: 36 % of the issue
+// slots are used). Teams there make it 93 to 122: their joins have few warps and many parts.
 //
 // A warp has its own tokens of each tile, its own two stages in shared memory, filled by its own
 // asynchronous copies one tile ahead (past the ends of segments; page numbers are looked up one tile
@@ -426,17 +428,21 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
 
     // ---- loads: lane l looks after token l % CH of the warp's chunk
     uint32_t position, end;         // of the token, and of its sequence (a tile may end past 2^31 - 1)
-    int seq, kv_head, page;         // page: < 0 for a token past the end
+    int seq, kv_head, page, inside;  // page: < 0 for a token past the end; inside: its place there
+    int64_t head_off;               // of the kv head in its token
     int load_left;                  // tiles of the segment that are still to be loaded
     auto enter = [&](const Cursor &at) {
         position = (uint32_t)at.span.lo + ((uint32_t)at.tile << a.tile_log) + sub * CH + (lane & (CH - 1));
         end = at.span.n;
         seq = at.b;
         kv_head = (at.h << a.teams_log) + team;
+        head_off = kv_head * a.kv.head_stride;
         load_left = at.span.tiles - at.tile;
     };
     auto look_up = [&]() {
-        page = position < end ? __ldg(a.kv.page_table + seq * a.kv.table_stride + divide(position, a.page)) : -2;
+        const uint32_t nth = divide(position, a.page);
+        inside = (int)(position - nth * a.page.d);
+        page = position < end ? __ldg(a.kv.page_table + seq * a.kv.table_stride + nth) : -2;
         if (position < end && page < 0) page = INT32_MAX;  // no page either, but reported
     };
     auto go_on = [&]() {
@@ -461,8 +467,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
             report(a.status, EPD_ERR_CAPACITY);
             live = false;
         }
-        const int inside = live ? (int)(position - divide(position, a.page) * a.page.d) : 0;
-        const int64_t off = live ? (page * a.kv.page_stride + inside * a.kv.token_stride + kv_head * a.kv.head_stride) * (FP8 ? 1 : 2) : 0;
+        const int64_t off = live ? ((int64_t)page * a.kv.page_stride + (int64_t)inside * a.kv.token_stride + head_off) * (FP8 ? 1 : 2) : 0;
         const uint32_t mask = __ballot_sync(kAll, live) & (CH == 32 ? kAll : 0xffffu);
         if (a.aligned && mask == (CH == 32 ? kAll : 0xffffu)) {
             // every 16 tokens lie on one page: one address for them, and a constant step
@@ -500,7 +505,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
             }
         }
         if (FP8 && mask) {
-            const int64_t so = live ? page * a.kv.scale_page_stride + inside * a.kv.scale_token_stride + kv_head * a.kv.scale_head_stride : 0;
+            const int64_t so = live ? (int64_t)page * a.kv.scale_page_stride + (int64_t)inside * a.kv.scale_token_stride + kv_head * a.kv.scale_head_stride : 0;
             const uint32_t dst = at + 2 * CH * S::kRow + (lane & (CH - 1)) * 4;
             if (CH == 32 || lane < 16) copy4z(dst, a.kv.k_scale + so, live);
             if (CH == 32 || lane >= 16) copy4z(dst + CH * 4, a.kv.v_scale + so, live);
@@ -919,7 +924,10 @@ epd_status_t launch_heads(AttnArgs &a, cudaStream_t st) {
     using S = Shape<DP, FP8, NH>;
     a.blocks_of_group = (a.group + S::kHeads - 1) / S::kHeads;
     if ((int64_t)a.kv.num_kv_heads * a.blocks_of_group > INT32_MAX) return EPD_ERR_UNSUPPORTED;
-    // As many kv heads at once as leave a segment for every fourth multiprocessor.
+    // As many kv heads at once as leave a segment for every fourth multiprocessor. Fewer segments are joined
+    // from more parts by fewer warps: one sequence of 32000 bf16 tokens, 32 heads over 8, takes 29 us with
+    // teams of one head at a time and 31, 44 and 61 with two, four and eight; eight sequences of 30000
+    // in e4m3 99, 95, 93 and 96.
     a.teams = most_teams(a.kv.num_kv_heads);
     if (a.teams > S::kWarps) a.teams = S::kWarps;
     while (a.teams > 1 && (int64_t)a.kv.num_seqs * (a.kv.num_kv_heads / a.teams) * a.blocks_of_group < sm_count() / 4) a.teams /= 2;
