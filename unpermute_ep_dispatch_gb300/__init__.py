@@ -16,7 +16,8 @@ Around them: ``ep_route`` makes the picks and weights from router logits,
 ``ep_expert_matmul`` is the experts' product (bf16 or e4m3 rows; bias, activation and
 residual in its epilogue) between steps 3 and 4, and ``ep_route_backward``,
 ``ep_expert_matmul_dgrad``, ``ep_expert_matmul_wgrad`` and ``ep_unpermute_backward`` are the
-gradients.
+gradients. Beside the experts in a block: ``ep_layer_norm`` and its gradient, ``ep_rotary``,
+``ep_cache_append`` and ``ep_decode_attention`` over the paged cache.
 
 ``ep_dispatch_layout_offsets`` runs steps 1 and 2 in one launch and
 ``ep_dispatch`` steps 1 to 3 in one call (one kernel for a small batch).

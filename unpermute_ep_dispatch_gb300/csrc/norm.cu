@@ -11,7 +11,9 @@
 // its columns in chunks of 16 bytes, and blocks walk over the rows with the row kept in registers
 // between the sums and the output. Each thread copies its own chunks of the rows to come into its own
 // slots of shared memory (cp.async, up to four rows ahead): no barrier and no wait but the thread's
-// own, and one block a multiprocessor keeps 40 KB or more on the way.
+// own, and one block a multiprocessor keeps 40 KB or more on the way. 8192 x 7168 bf16 rows with a
+// residual in and out, into bf16 and e4m3, take 82 us (531 MB: 79 at a copy's rate), 4097 x 4096 fp32 18.8 (15); the
+// gradient of 8192 x 7168 bf16 rows 82 (470 MB: 70), of 4096 x 7168 fp32 65 (53).
 //
 // The weights' gradients: a thread keeps the sums of its columns over all of its block's rows in
 // registers; the blocks' sums go to the workspace and a second kernel adds them in a fixed order.
