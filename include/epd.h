@@ -640,7 +640,8 @@ EPD_API epd_status_t ep_layer_norm_backward(const void *dy, const void *x, epd_d
  * by -p: the gradient of the rotation.
  *   x, out: [T, num_heads, head_dim] bfloat16 with the strides given (in elements, multiples of
  *   8; the elements of a head lie together), 16-byte aligned; out may be x itself with the same
- *   strides (the elements past R are then left alone), otherwise they must not overlap.
+ *   strides (the elements past R are then left alone), otherwise they must not overlap; out's
+ *   strides are not 0 where there is more than one to a stride.
  *   positions: [T] int32, any sign; steps: [R/2] uint64.
  * head_dim % 8 == 0, up to 256 (EPD_ERR_UNSUPPORTED beyond); R even, in [2, head_dim].
  */
@@ -674,7 +675,8 @@ typedef struct {
     float *k_scale, *v_scale; /* EPD_FP8_E4M3 only, else NULL */
     int64_t page_stride, token_stride, head_stride;
     int64_t scale_page_stride, scale_token_stride, scale_head_stride;
-    const int32_t *page_table; /* device [num_seqs, max_pages], rows table_stride apart */
+    const int32_t *page_table; /* device [num_seqs, max_pages], rows table_stride apart (0: one
+                                * row for all sequences) */
     int num_seqs;
     int max_pages;
     int64_t table_stride;
@@ -693,7 +695,8 @@ typedef struct {
  *   q, q_out: [T, num_heads, head_dim], k, v: [T, num_kv_heads, head_dim] bfloat16, the heads of a
  *   token next to each other, tokens the given strides apart (elements, multiples of 8), 16-byte
  *   aligned: parts of one projection's rows are taken as they are. q may be NULL; q_out may be q
- *   itself with the same stride. rotary_dim 0 (steps NULL): no rotation.
+ *   itself with the same stride. rotary_dim 0 (steps NULL): no rotation. Strides of what is written
+ *   (the cache's, q_out's) are not 0 where there is more than one to a stride.
  */
 EPD_API epd_status_t ep_cache_append(const epd_cache_t *cache, const void *q,
                                      int64_t q_token_stride, int num_heads, const void *k,

@@ -299,6 +299,39 @@ def test_bad_pages_and_lengths(fp8):
     assert code == epd.EPD_ERR_INVALID_ARG and torch.equal(out[0], full[0]) and bool((out[1] == 0).all())
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_tables_and_caches_with_other_strides(fp8):
+    """One table row for all sequences, a table that is a part of a wider one, kv heads that share their rows."""
+    g = gen(14)
+    B, KH, D, page, n = 5, 2, 64, 16, 70
+    k, v, ks, vs = paged(8, page, KH, D, fp8, DEV, g)
+    wide = torch.stack([torch.randperm(8, generator=g, device=DEV) for _ in range(B)]).int()
+    q = torch.randn(B, 4, D, generator=g, device=DEV).bfloat16()
+    lens = torch.tensor([n, 3, 0, 80, 17], dtype=torch.int32, device=DEV)
+    ws, st = epd.new_attention_workspace(B, 4, KH, D, DEV), epd.new_status(DEV)
+
+    def f(table, k=k, v=v, ks=ks, vs=vs):
+        return epd.ep_decode_attention(q, k, v, table, lens, ws, st, k_scale=ks, v_scale=vs)[0]
+    one = wide[:1].expand(B, 8)
+    assert torch.equal(f(one), f(one.contiguous()))
+    assert torch.equal(f(wide[:, 1:6]), f(wide[:, 1:6].contiguous()))
+    half = [None if t is None else t[:, :, :1].expand(t.shape) for t in (k, v, ks, vs)]
+    whole = [None if t is None else t.contiguous() for t in half]
+    assert torch.equal(f(wide, *half), f(wide, *whole)) and int(st) == 0
+    # and appending through a shared row; not into rows that heads share
+    new = torch.randn(2, KH, D, generator=g, device=DEV).bfloat16()
+    at = torch.tensor([2, 40], dtype=torch.int32, device=DEV)
+    got, want = [[None if t is None else t.clone() for t in (k, v, ks, vs)] for _ in range(2)]
+    for (a, b, c, d), table in ((got, one), (want, one.contiguous())):
+        epd.ep_cache_append(new, new, a, b, table, at, st, k_scale=c, v_scale=d)
+    assert int(st) == 0 and all(x is None or torch.equal(x.float(), y.float()) for x, y in zip(got, want))
+    assert not torch.equal(got[0].float(), k.float())
+    with pytest.raises(epd.EpdError):
+        epd.ep_cache_append(new, new, half[0], half[1], one, at, st, k_scale=half[2], v_scale=half[3])
+    with pytest.raises(epd.EpdError):
+        f(torch.as_strided(wide, (B, 5), (2, 1)))
+
+
 def test_one_workspace_for_many_shapes():
     ws = epd.new_attention_workspace(64, 64, 8, 256, DEV)
     for i, (lengths, KH, G, D, fp8) in enumerate([([3000] * 3, 8, 8, 128, False), ([17], 1, 1, 64, True), ([900] * 60, 2, 4, 256, False),

@@ -75,3 +75,25 @@ def test_attention_workspace_bytes(lib):
     assert f(4, 32, 8, 256) > f(4, 32, 8, 128) > f(4, 32, 8, 64) > 0
     for bad in ((-1, 32, 8, 128), (4, 0, 8, 128), (4, 32, 0, 128), (4, 32, 5, 128), (4, 32, 8, 0), (4, 32, 8, 100), (4, 32, 8, 264)):
         assert f(*bad) == 0
+
+
+def test_shared_rows(lib):
+    """A table's row may serve all sequences; what is written lies apart."""
+    append = dict(c=cache(), q=None, qs=0, QH=0, k=FAKE, ks=128, v=FAKE, vs=128, pos=FAKE, seq=FAKE, T=0, steps=None, R=0,
+                  inter=0, scale=1.0, qo=None, qos=0, st=FAKE, s=None)
+    call = lambda **kw: lib.ep_cache_append(*dict(append, **kw).values())  # noqa: E731
+    assert call(c=cache(ts=0)) == OK
+    fp8 = dict(dt=1, ks=0x10000, vs=0x10000, cp=32, ct=2, ch=1)
+    assert call(c=cache(**fp8)) == OK
+    for kw in (dict(sp=0), dict(st=0), dict(sh=0), dict(fp8, cp=0), dict(fp8, ct=0), dict(fp8, ch=0), dict(fp8, sh=0)):
+        assert call(c=cache(**kw)) == INVALID, kw
+    assert call(c=cache(sp=0, st=0, sh=0, P=1, page=1, KH=1)) == OK
+    assert call(q=FAKE, QH=4, qs=256, qo=FAKE, qos=0, T=2) == INVALID
+    rotary = dict(x=FAKE, ts=128, hs=64, pos=FAKE, steps=FAKE, T=4, N=2, D=64, R=64, inter=0, scale=1.0, inv=0, out=FAKE,
+                  ots=0, ohs=64, s=None)
+    assert lib.ep_rotary(*rotary.values()) == INVALID
+    assert lib.ep_rotary(*dict(rotary, ots=128, ohs=0).values()) == INVALID
+    # reading is not writing: heads that share their rows
+    attention = dict(c=cache(S=0, sh=0, ts=0), q=None, qs=256, QH=4, lens=None, scale=0.1, window=0, ws=None, out=None, lse=None,
+                     st=FAKE, s=None)
+    assert lib.ep_decode_attention(*attention.values()) == OK

@@ -1140,7 +1140,7 @@ def _cache(k, v, page_table, k_scale, v_scale):
         sh = 0
     packed = _CACHE_BYTES.pack(EPD_FP8_E4M3 if fp8 else EPD_BF16, KH, D, rows, P, k.data_ptr(),
                                v.data_ptr(), kp, vp, sp, st, sh, cp, ct, ch,
-                               page_table.data_ptr(), S, M, ts if S > 1 and ts > M else M)
+                               page_table.data_ptr(), S, M, ts if S > 1 else M)
     return packed, dev, S, KH, D
 
 

@@ -458,6 +458,7 @@ extern "C" epd_status_t ep_rotary(const void *x, int64_t token_stride, int64_t h
     for (const int64_t s : {token_stride, head_stride, out_token_stride, out_head_stride})
         if (s < 0 || s % 8 != 0) return EPD_ERR_INVALID_ARG;
     if (D > kMaxHeadDim) return EPD_ERR_UNSUPPORTED;
+    if ((T > 1 && out_token_stride == 0) || (N > 1 && out_head_stride == 0)) return EPD_ERR_INVALID_ARG;
     if (T == 0 || N == 0) return EPD_OK;
     if (!x || !out || !positions || !aligned16(x) || !aligned16(out) || !aligned4(positions)) return EPD_ERR_INVALID_ARG;
     RotaryArgs a;
@@ -498,6 +499,7 @@ extern "C" epd_status_t ep_cache_append(const epd_cache_t *cache, const void *q,
     for (const int64_t s : {q_token_stride, k_token_stride, v_token_stride, q_out_token_stride})
         if (s < 0 || s % 8 != 0) return EPD_ERR_INVALID_ARG;
     if (!status || !aligned4(status)) return EPD_ERR_INVALID_ARG;
+    if (!rows_apart(*cache) || (T > 1 && QH > 0 && q_out_token_stride == 0)) return EPD_ERR_INVALID_ARG;
     if (!token_seq && T > cache->num_seqs) return EPD_ERR_INVALID_ARG;
     if ((int64_t)QH + 2 * (int64_t)cache->num_kv_heads > INT32_MAX) return EPD_ERR_UNSUPPORTED;
     if (T == 0) return EPD_OK;
