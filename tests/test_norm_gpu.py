@@ -232,6 +232,31 @@ def test_graph_and_stream():
     assert all(torch.equal(a, b) for a, b in zip(out, step()))
 
 
+def test_own_workspace_on_a_given_stream(monkeypatch):
+    """A workspace made by the call stays its own until the given stream has read it."""
+    from unpermute_ep_dispatch_gb300 import _binding
+    H = 8192
+    x, w, dy = rand(300, H, dtype=torch.bfloat16), rand(H, seed=1), rand(300, H, seed=2, dtype=torch.bfloat16)
+    rstd = rand(300, seed=3).abs()
+    want = epd.ep_layer_norm_backward(dy, x, w, rstd, kind="rms")
+    made = []
+
+    def new(*args):
+        t = torch.empty(epd.epd_norm_workspace_bytes(H), dtype=torch.uint8, device=DEV)
+        made.append(t.data_ptr())
+        return t
+    monkeypatch.setattr(_binding, "new_norm_workspace", new)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # some ten milliseconds
+    got = epd.ep_layer_norm_backward(dy, x, w, rstd, kind="rms", stream=side)
+    other = torch.empty(epd.epd_norm_workspace_bytes(H), dtype=torch.uint8, device=DEV)
+    assert other.data_ptr() not in made and len(made) == 1
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got[:2], want[:2]))
+
+
 def test_refusals():
     x, w = rand(4, 256), rand(256)
     st = rand(4)

@@ -954,6 +954,8 @@ def ep_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[t
     if dweight is not None or dbias is not None:
         if workspace is None:
             workspace = new_norm_workspace(H, dev)
+            if stream is not None:  # not to be handed out again before it has been read there
+                workspace.record_stream(stream)
         else:
             _want(workspace, "workspace", torch.uint8, device=dev)
             if workspace.numel() < epd_norm_workspace_bytes(H):
