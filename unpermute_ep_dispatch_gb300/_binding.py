@@ -10,6 +10,7 @@ torch.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import struct
@@ -908,6 +909,7 @@ def ep_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     return dict(y=y, y_q=y_q, y_scale=y_scale, sum=sum, mean=mean, rstd=rstd)
 
 
+@functools.lru_cache(maxsize=256)
 def epd_norm_workspace_bytes(hidden: int) -> int:
     n = int(load_library().epd_norm_workspace_bytes(hidden))
     if n == 0:
@@ -1019,7 +1021,8 @@ def rotary_steps(frequencies, device=None) -> torch.Tensor:
 
 
 def _heads(t, name, heads=None, dim=None, tokens=None, device=None):
-    """Rows of heads [T, heads, dim], bfloat16, the elements of a head next to each other."""
+    """Rows of heads [T, heads, dim], bfloat16, the elements of a head next to each other: their
+    shape and strides."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not torch.bfloat16:
@@ -1032,9 +1035,10 @@ def _heads(t, name, heads=None, dim=None, tokens=None, device=None):
         raise ValueError(f"{name} must be [{want}], got {tuple(shape)}")
     if not t.is_cuda or (device is not None and t.get_device() != device.index):
         raise ValueError(f"{name} is on {t.device}, expected {device or 'a CUDA device'}")
-    if t.stride(2) != 1 and shape[2] > 1:
+    strides = t.stride()
+    if strides[2] != 1 and shape[2] > 1:
         raise ValueError(f"the elements of {name}'s heads must lie next to each other")
-    return t
+    return shape, strides
 
 
 def _token_rows(t, name, heads, dim, tokens, device):
@@ -1059,9 +1063,10 @@ def _steps(steps, dim, device):
     if not isinstance(steps, torch.Tensor) or steps.dim() != 1:
         raise ValueError("steps must be an int64 tensor [rotary_dim / 2]")
     _want(steps, "steps", torch.int64, device=device)
-    if 2 * steps.shape[0] > dim:
-        raise ValueError(f"steps of {steps.shape[0]} pairs, heads of {dim} elements")
-    return 2 * steps.shape[0]
+    R = 2 * steps.numel()
+    if R > dim:
+        raise ValueError(f"steps of {R // 2} pairs, heads of {dim} elements")
+    return R
 
 
 def ep_rotary(x: torch.Tensor, positions: torch.Tensor, steps: torch.Tensor,
@@ -1071,22 +1076,24 @@ def ep_rotary(x: torch.Tensor, positions: torch.Tensor, steps: torch.Tensor,
     elements, the elements of a head together): the first 2 * len(steps) elements of every head
     are turned by positions [T] int32 times steps (rotary_steps). inverse: by the negative angle,
     which is the gradient. out may be x. Returns out [T, heads, dim]; see epd.h."""
-    _heads(x, "x")
+    (T, N, D), (xt, xh, _) = _heads(x, "x")
     dev = x.device
-    T, N, D = x.shape
     _want(positions, "positions", torch.int32, (T,), dev)
     if steps is None:
         raise TypeError("steps must be a torch.Tensor")
     R = _steps(steps, D, dev)
     if out is None:
         out = torch.empty((T, N, D), dtype=torch.bfloat16, device=dev)
+        ot, oh = N * D, D
     else:
-        _heads(out, "out", N, D, T, dev)
-    rc = _launch(load_library().ep_rotary, dev, _ptr(x), x.stride(0) if T > 1 else 0,
-                 x.stride(1) if N > 1 else 0, _ptr(positions), _ptr(steps), T, N, D, R,
-                 int(bool(interleaved)), float(rotary_scale), int(bool(inverse)), _ptr(out),
-                 out.stride(0) if T > 1 else 0, out.stride(1) if N > 1 else 0,
-                 _stream(stream, dev))
+        _, (ot, oh, _) = _heads(out, "out", N, D, T, dev)
+    if T <= 1:
+        xt = ot = 0
+    if N <= 1:
+        xh = oh = 0
+    rc = _launch(load_library().ep_rotary, dev, x.data_ptr(), xt, xh, positions.data_ptr(),
+                 steps.data_ptr(), T, N, D, R, 1 if interleaved else 0, float(rotary_scale),
+                 1 if inverse else 0, out.data_ptr(), ot, oh, _stream(stream, dev))
     _check(rc, "ep_rotary")
     return out
 
@@ -1170,7 +1177,7 @@ def ep_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
         _want(token_seq, "token_seq", torch.int32, (T,), dev)
     elif T > S:
         raise ValueError("token_seq is needed for more tokens than sequences")
-    R = _steps(steps, D, dev)
+    R = 0 if steps is None else _steps(steps, D, dev)
     QH = qs = os_ = 0
     if q is not None:
         qs = _token_rows(q, "q", None, D, T, dev)
@@ -1182,12 +1189,13 @@ def ep_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
         raise ValueError("q_out is the rotated q")
     rc = _launch(load_library().ep_cache_append, dev, cache, _ptr(q), qs, QH, _ptr(k),
                  ks, _ptr(v), vs, _ptr(positions), _ptr(token_seq), T, _ptr(steps), R,
-                 int(bool(interleaved)), float(rotary_scale), _ptr(q_out), os_, _ptr(status),
+                 1 if interleaved else 0, float(rotary_scale), _ptr(q_out), os_, _ptr(status),
                  _stream(stream, dev))
     _check(rc, "ep_cache_append")
     return q_out
 
 
+@functools.lru_cache(maxsize=256)
 def epd_attention_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int,
                                   head_dim: int) -> int:
     n = int(load_library().epd_attention_workspace_bytes(num_seqs, num_heads, num_kv_heads,
@@ -1222,15 +1230,14 @@ def ep_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     _want(lengths, "lengths", torch.int32, (B,), dev)
     _want(workspace, "workspace", torch.uint8, device=dev)
     _want(status, "status", torch.int32, (1,), dev)
-    lib = load_library()
-    need = lib.epd_attention_workspace_bytes(B, QH, KH, D)  # 0: refused below
-    if workspace.numel() < need:
+    # (of any number of sequences: the size does not depend on it)
+    if D % 8 == 0 and 0 < D <= 256 and workspace.numel() < epd_attention_workspace_bytes(1, QH, KH, D):
         raise ValueError("workspace too small for this attention")
     out = _out(out, "out", torch.bfloat16, (B, QH, D), dev)
     if with_lse or lse is not None:
         lse = _out(lse, "lse", torch.float32, (B, QH), dev)
     scale = D ** -0.5 if softmax_scale is None else float(softmax_scale)
-    rc = _launch(lib.ep_decode_attention, dev, cache, _ptr(q), qs, QH, _ptr(lengths),
+    rc = _launch(load_library().ep_decode_attention, dev, cache, _ptr(q), qs, QH, _ptr(lengths),
                  scale, int(window), _ptr(workspace), _ptr(out), _ptr(lse), _ptr(status),
                  _stream(stream, dev))
     _check(rc, "ep_decode_attention")

@@ -458,8 +458,8 @@ extern "C" epd_status_t ep_rotary(const void *x, int64_t token_stride, int64_t h
     for (const int64_t s : {token_stride, head_stride, out_token_stride, out_head_stride})
         if (s < 0 || s % 8 != 0) return EPD_ERR_INVALID_ARG;
     if (D > kMaxHeadDim) return EPD_ERR_UNSUPPORTED;
-    if ((T > 1 && out_token_stride == 0) || (N > 1 && out_head_stride == 0)) return EPD_ERR_INVALID_ARG;
     if (T == 0 || N == 0) return EPD_OK;
+    if ((T > 1 && out_token_stride == 0) || (N > 1 && out_head_stride == 0)) return EPD_ERR_INVALID_ARG;
     if (!x || !out || !positions || !aligned16(x) || !aligned16(out) || !aligned4(positions)) return EPD_ERR_INVALID_ARG;
     RotaryArgs a;
     a.x = static_cast<const uint8_t *>(x);
