@@ -10,10 +10,11 @@
 // Bound by HBM: every row is read once and written once. A block owns a row, a thread 8, 16 or 32 of
 // its columns in chunks of 16 bytes, and blocks walk over the rows with the row kept in registers
 // between the sums and the output. Each thread copies its own chunks of the rows to come into its own
-// slots of shared memory (cp.async, up to four rows ahead): no barrier and no wait but the thread's
+// slots of shared memory (cp.async, two or four rows ahead): no barrier and no wait but the thread's
 // own, and one block a multiprocessor keeps 40 KB or more on the way. 8192 x 7168 bf16 rows with a
-// residual in and out, into bf16 and e4m3, take 82 us (531 MB: 79 at a copy's rate), 4097 x 4096 fp32 18.8 (15); the
-// gradient of 8192 x 7168 bf16 rows 82 (470 MB: 70), of 4096 x 7168 fp32 65 (53).
+// residual in and out take 72.4 us into bf16 (470 MB: 70 at a copy's rate), 69 into e4m3 (62) and 81.5 into
+// both (79), 4097 x 4096 fp32 rows 16.8 (15); the gradient of 8192 x 7168 bf16 rows, joined, 82 (470 MB: 70),
+// of 4096 x 7168 fp32 65 (62).
 //
 // The weights' gradients: a thread keeps the sums of its columns over all of its block's rows in
 // registers; the blocks' sums go to the workspace and a second kernel adds them in a fixed order.
@@ -29,6 +30,7 @@ constexpr int kNormThreads = 512;
 constexpr int kNormMaxSms = 160;    // blocks that the workspace has room for, per block of a multiprocessor
 constexpr int kReduceThreads = 256;
 constexpr int kRingBytes = 224 * 1024;  // of the 227 KB that a multiprocessor's blocks share
+constexpr size_t kAheadBytes = 56 * 1024;
 constexpr unsigned kAll = 0xffffffffu;
 
 struct NormArgs {
@@ -109,6 +111,14 @@ __device__ __forceinline__ void block_add(float &a, float (&part)[16]) {
 }
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// x^-1/2 to a unit in the last place: the hardware's, 2 units off, and a step of Newton's. It is on every
+// row's way from its sums to its output, where a root and a division take three times as long.
+__device__ __forceinline__ float inverse_root(float x) {
+    const float r = rsqrtf(x);
+    const float d = fmaf(-x * r, r, 1.0f);  // (NaN of 0 and of infinity, whose root is exact)
+    return d < 1.0f ? fmaf(0.5f * r, d, r) : r;
+}
 
 // A chunk in 32 bits, two columns to an instruction: the C columns of 16 bytes of T, so that a warp's
 // loads and stores of x are 512 bytes in a row.
@@ -257,36 +267,80 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
             }
         }
         turn ^= 1;
-        const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(var + a.eps));
+        const float rstd = inverse_root(var + a.eps);
         fetch(row + (int64_t)a.stages * gridDim.x, s);
         if (++s == a.stages) s = 0;
         if (tid == 0) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
         }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = tid + i * n;
-            if (c >= a.chunks) continue;
+        auto scaled = [&](int i) {
             const int k = KEEP == NV ? i : 0;
             if (KEEP != NV) load_weights(i, 0);
             Columns<C> o;
 #pragma unroll
             for (int j = 0; j < C / 2; ++j) o.v[j] = __ffma2_rn(__fmul2_rn(__fadd2_rn(v[i].v[j], both(-mean)), both(rstd)), w[k].v[j], b[k].v[j]);
-            if (a.y) store_bf16(a.y + (row * a.chunks + c) * (2 * C), o);
-            if (a.yq) {
-                // 128 columns are 16 or 32 neighbouring lanes, all of them with a chunk or none
-                const unsigned group = C == 4 ? kAll : (tid & 16) ? 0xffff0000u : 0x0000ffffu;
-                float f[C], amax = 0.0f;
+            if (a.y) store_bf16(a.y + (row * a.chunks + tid + i * n) * (2 * C), o);
+            return o;
+        };
+        if (!a.yq) {
 #pragma unroll
-                for (int j = 0; j < C; ++j) {
-                    f[j] = j & 1 ? o.v[j / 2].y : o.v[j / 2].x;
-                    amax = fmaxf(amax, fabsf(f[j]));
+            for (int i = 0; i < NV; ++i)
+                if (tid + i * n < a.chunks) scaled(i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (tid + i * n < a.chunks) v[i] = scaled(i);
+            // 128 columns are G neighbouring lanes, all of them with a chunk or none. The largest of a thread's
+            // chunks take their exchanges together: after each of the first ones a lane has half as many, and
+            // in the end the one of chunk `mine`, whose scale it finds for all of them (8192 x 4096 fp32 into
+            // e4m3 41 us; 55 with an exchange and two divisions for every chunk).
+            constexpr int G = 128 / C;
+            const int lane = tid & 31;
+            float top[NV];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                top[i] = 0.0f;
+                if (tid + i * n >= a.chunks) continue;
+#pragma unroll
+                for (int j = 0; j < C / 2; ++j) top[i] = fmaxf(top[i], fmaxf(fabsf(v[i].v[j].x), fabsf(v[i].v[j].y)));
+            }
+            int mine = 0;
+#pragma unroll
+            for (int step = 1, d = G / 2; d; step *= 2, d /= 2) {
+                if (step < NV) {
+                    const bool upper = lane & d;
+                    mine += upper ? step : 0;
+#pragma unroll
+                    for (int i = 0; i < NV / (2 * step); ++i) {
+                        const float other = __shfl_xor_sync(kAll, upper ? top[2 * i] : top[2 * i + 1], d);
+                        top[i] = fmaxf(upper ? top[2 * i + 1] : top[2 * i], other);
+                    }
+                } else {
+                    top[0] = fmaxf(top[0], __shfl_xor_sync(kAll, top[0], d));
                 }
+            }
+            const float scale = top[0] > 0.0f ? __fdiv_rn(top[0], 448.0f) : 1.0f, inv = __fdiv_rn(1.0f, scale);
+            const int group = (tid + mine * n) / G;
+            if ((lane & (G / NV - 1)) == 0 && group * G < a.chunks) a.yscale[row * (a.chunks / G) + group] = scale;
+            const bool tiny = __any_sync(kAll, scale < 0x1p-120f);  // its inverse may overflow
 #pragma unroll
-                for (int d = 64 / C; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, d));
-                const float scale = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-                divide_all(f, scale);
+            for (int i = 0; i < NV; ++i) {
+                const int c = tid + i * n;
+                int from = lane & ~(G - 1);
+#pragma unroll
+                for (int step = 1, d = G / 2; step < NV; step *= 2, d /= 2) from += i & step ? d : 0;
+                const float by = __shfl_sync(kAll, tiny ? scale : inv, from);
+                if (c >= a.chunks) continue;
+                float f[C];
+#pragma unroll
+                for (int j = 0; j < C; ++j) f[j] = j & 1 ? v[i].v[j / 2].y : v[i].v[j / 2].x;
+                if (tiny) {
+                    divide_all(f, by);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < C; ++j) f[j] *= by;
+                }
                 uint32_t q[C / 4];
 #pragma unroll
                 for (int j = 0; j < C / 4; ++j)
@@ -295,7 +349,6 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
                 uint8_t *const out = a.yq + (row * a.chunks + c) * C;
                 if constexpr (C == 8) *reinterpret_cast<uint2 *>(out) = make_uint2(q[0], q[1]);
                 else *reinterpret_cast<uint32_t *>(out) = q[0];
-                if (c % (128 / C) == 0) a.yscale[row * (a.chunks / (128 / C)) + c / (128 / C)] = scale;
             }
         }
     }
@@ -469,10 +522,13 @@ inline NormShape norm_shape(int H) {
 
 inline int norm_max_blocks(int H) { return kNormMaxSms * norm_shape(H).per_sm; }
 
-// Rows ahead: four where they fit beside the other blocks of the multiprocessor, else two or one.
+// Rows ahead: four while a multiprocessor's blocks have 56 KB of them on the way, else two, or one where two
+// do not fit. More only make the multiprocessors' shares of the memory uneven: 8192 x 7168 bf16 with a
+// residual into bf16 81.5 us with four rows (112 KB) ahead and 72.4 with two, into both 91 and 81.5; 4097 x
+// 4096 fp32 17.2 and 16.8 (but 8192 x 2048, which L2 holds, 19.0 and 20.6).
 inline int norm_stages(size_t stage_bytes, int per_sm) {
     const size_t room = (size_t)kRingBytes / per_sm - 2048;
-    return 4 * stage_bytes <= room ? 4 : 2 * stage_bytes <= room ? 2 : 1;
+    return 4 * stage_bytes <= room && 4 * stage_bytes * per_sm <= kAheadBytes ? 4 : 2 * stage_bytes <= room ? 2 : 1;
 }
 
 template <auto kernel, typename A>
