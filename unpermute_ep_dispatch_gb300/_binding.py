@@ -846,12 +846,15 @@ def ep_unpermute_backward(grad_y: torch.Tensor, expert_out: torch.Tensor,
 
 
 # ----------------------------------------------------------------------------- the norm
-def _launch(fn, dev, *args):
-    """Calls `fn` with `dev`, the tensors' device, as the current one."""
+def _on(fn, dev):
+    """`fn`, to be called with `dev`, the tensors' device, as the current one."""
     if dev.index == torch._C._cuda_getDevice():
-        return fn(*args)
-    with torch.cuda.device(dev):
-        return fn(*args)
+        return fn
+
+    def there(*args):
+        with torch.cuda.device(dev):
+            return fn(*args)
+    return there
 
 
 def _norm_rows(t, name):
@@ -902,9 +905,9 @@ def ep_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
         mean = _out(mean, "mean", torch.float32, (T,), dev)
     if with_stats or rstd is not None:
         rstd = _out(rstd, "rstd", torch.float32, (T,), dev)
-    rc = _launch(load_library().ep_layer_norm, dev, _ptr(x), dt, _ptr(residual), _ptr(weight),
-                 _ptr(bias), T, H, float(eps), kd, _ptr(sum), _ptr(y), _ptr(y_q), _ptr(y_scale),
-                 _ptr(mean), _ptr(rstd), _stream(stream, dev))
+    rc = _on(load_library().ep_layer_norm, dev)(
+        _ptr(x), dt, _ptr(residual), _ptr(weight), _ptr(bias), T, H, float(eps), kd, _ptr(sum),
+        _ptr(y), _ptr(y_q), _ptr(y_scale), _ptr(mean), _ptr(rstd), _stream(stream, dev))
     _check(rc, "ep_layer_norm")
     return dict(y=y, y_q=y_q, y_scale=y_scale, sum=sum, mean=mean, rstd=rstd)
 
@@ -962,9 +965,9 @@ def ep_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[t
             _want(workspace, "workspace", torch.uint8, device=dev)
             if workspace.numel() < epd_norm_workspace_bytes(H):
                 raise ValueError("workspace too small for this norm")
-    rc = _launch(load_library().ep_layer_norm_backward, dev, _ptr(dy), _ptr(x), dt, _ptr(weight),
-                 _ptr(mean), _ptr(rstd), _ptr(grad_sum), T, H, kd, _ptr(workspace), _ptr(dx),
-                 _ptr(dweight), _ptr(dbias), _stream(stream, dev))
+    rc = _on(load_library().ep_layer_norm_backward, dev)(
+        _ptr(dy), _ptr(x), dt, _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(grad_sum), T, H, kd,
+        _ptr(workspace), _ptr(dx), _ptr(dweight), _ptr(dbias), _stream(stream, dev))
     _check(rc, "ep_layer_norm_backward")
     return dx, dweight, dbias
 
@@ -1091,9 +1094,10 @@ def ep_rotary(x: torch.Tensor, positions: torch.Tensor, steps: torch.Tensor,
         xt = ot = 0
     if N <= 1:
         xh = oh = 0
-    rc = _launch(load_library().ep_rotary, dev, x.data_ptr(), xt, xh, positions.data_ptr(),
-                 steps.data_ptr(), T, N, D, R, 1 if interleaved else 0, float(rotary_scale),
-                 1 if inverse else 0, out.data_ptr(), ot, oh, _stream(stream, dev))
+    rc = _on(load_library().ep_rotary, dev)(
+        x.data_ptr(), xt, xh, positions.data_ptr(), steps.data_ptr(), T, N, D, R,
+        1 if interleaved else 0, float(rotary_scale), 1 if inverse else 0, out.data_ptr(), ot, oh,
+        _stream(stream, dev))
     _check(rc, "ep_rotary")
     return out
 
@@ -1187,10 +1191,10 @@ def ep_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
         os_ = _token_rows(q_out, "q_out", QH, D, T, dev)
     elif q_out is not None:
         raise ValueError("q_out is the rotated q")
-    rc = _launch(load_library().ep_cache_append, dev, cache, _ptr(q), qs, QH, _ptr(k),
-                 ks, _ptr(v), vs, _ptr(positions), _ptr(token_seq), T, _ptr(steps), R,
-                 1 if interleaved else 0, float(rotary_scale), _ptr(q_out), os_, _ptr(status),
-                 _stream(stream, dev))
+    rc = _on(load_library().ep_cache_append, dev)(
+        cache, _ptr(q), qs, QH, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(),
+        _ptr(token_seq), T, _ptr(steps), R, 1 if interleaved else 0, float(rotary_scale),
+        _ptr(q_out), os_, status.data_ptr(), _stream(stream, dev))
     _check(rc, "ep_cache_append")
     return q_out
 
@@ -1237,9 +1241,9 @@ def ep_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     if with_lse or lse is not None:
         lse = _out(lse, "lse", torch.float32, (B, QH), dev)
     scale = D ** -0.5 if softmax_scale is None else float(softmax_scale)
-    rc = _launch(load_library().ep_decode_attention, dev, cache, _ptr(q), qs, QH, _ptr(lengths),
-                 scale, int(window), _ptr(workspace), _ptr(out), _ptr(lse), _ptr(status),
-                 _stream(stream, dev))
+    rc = _on(load_library().ep_decode_attention, dev)(
+        cache, q.data_ptr(), qs, QH, lengths.data_ptr(), scale, int(window), workspace.data_ptr(),
+        out.data_ptr(), _ptr(lse), status.data_ptr(), _stream(stream, dev))
     _check(rc, "ep_decode_attention")
     return out, lse
 

@@ -32,7 +32,7 @@
 //
 // Precision: products of bf16 are exact, sums in 32 bits. The weights of a bf16 cache's values are split
 // into two bf16 (15 bits at least), so that the output's own rounding is the only one that matters. An
-// e4m3 cache is widened to fp16, which holds it exactly; the query is scaled by a power of two and
+// e4m3 cache is widened to fp16, which holds it exactly; a head's query is scaled by a power of two and
 // the weights, with the values' scales in them, by the largest scale so far, to fp16's range (11
 // bits: an eighth of the output's rounding).
 #include <cuda_fp16.h>
