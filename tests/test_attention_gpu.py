@@ -409,3 +409,81 @@ def test_refusals():
     with pytest.raises(epd.EpdError):
         epd.new_attention_workspace(2, 4, 3, 64, DEV)
     assert int(st) == 0
+
+
+FAR = {  # values' scales far apart: what a token's row and its scale are replaced by
+    "zero rows": (3, 0, 0.0),       # as the append holds a row of zeros: scale 1
+    "one zero row": (10**6, 0, 0.0),
+    "large rows": (50, 1, 0.0),     # 2^30 times the others' scale, in one column
+    "no weight": (50, 2, -60.0),    # 2^30 times the others' scale, with next to no weight
+    "spread": (1, 3, 0.0),          # from 2^-30 to 2^30 times the others' scale
+}
+
+
+@pytest.mark.parametrize("power", [0, -10, -20, -30, -70])
+@pytest.mark.parametrize("what", list(FAR))
+@pytest.mark.parametrize("KH,G,D", [(2, 4, 128), (1, 16, 128), (8, 8, 64), (2, 12, 256), (1, 1, 80)])
+def test_values_of_far_scales(KH, G, D, what, power):
+    """Rows of an e4m3 cache beside rows of very different scales, each held to the bound of the others:
+    half a step of the output, and 2^-11 and 2^-14 of the sum of |weight value| in its own column."""
+    g = gen(40 + D)
+    lengths, page = [700, 33, 2500, 1, 17, 0, 128], 16
+    B, most = len(lengths), -(-max(lengths) // page)
+    k, v, ks, vs = paged(B * most, page, KH, D, True, DEV, g)
+    table = torch.randperm(B * most, generator=g, device=DEV).int().view(B, most)
+    lens = torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    q = torch.randn(B, KH * G, D, generator=g, device=DEV).bfloat16()
+    vs *= 2.0 ** power
+    every, kind, score = FAR[what]
+    at = torch.arange(0, most * page, every, device=DEV)
+    where = table[:, at // page].long(), (at % page).expand(B, -1)
+    codes = v.view(torch.uint8)
+    if kind == 0:
+        codes[where] = 0
+        vs[where] = 1.0
+    elif kind == 3:
+        vs *= torch.exp2(60 * torch.rand(vs.shape, generator=g, device=DEV) - 30)
+    else:
+        codes[where] &= torch.where(torch.arange(D, device=DEV) == 3, 255, 0).to(torch.uint8)
+        vs[where] *= 2.0 ** 30
+    if score:  # (keys against every query of the sequence's first head; for the others they are as any)
+        away = -q[:, 0].float() / q[:, 0].float().abs().amax(-1, keepdim=True)
+        k.view(torch.uint8)[where[0], where[1], 0] = (448 * away).to(torch.float8_e4m3fn).view(torch.uint8)[:, None]
+        ks[where[0], where[1], 0] = 60.0 * D ** 0.5 / (q[:, 0].float() * 448 * -away).sum(-1)[:, None]
+    want, lse = attend(q, values(k, ks), values(v, vs), table, lens)
+    size, _ = attend(q, values(k, ks), values(v, vs).abs(), table, lens)
+    st = epd.new_status(DEV)
+    f = lambda: epd.ep_decode_attention(q, k, v, table, lens, epd.new_attention_workspace(B, KH * G, KH, D, DEV), st,  # noqa: E731
+                                        k_scale=ks, v_scale=vs, with_lse=True)
+    out, got = f()
+    tol = 2.0 ** -134 + 2.0 ** -8 * want.abs() + (2.0 ** -14 + 2.0 ** -11) * size
+    err = (out.double() - want).abs()
+    assert int(st) == 0 and bool((err <= tol).all()), (float((err / size.clamp(min=1e-300)).max()), float((err - tol).max()))
+    live = lens > 0
+    assert bool(((got[live].double() - lse[live]).abs() <= 2.0 ** -14 + 2.0 ** -23 * lse[live].abs()).all())
+    again = f()
+    assert torch.equal(out, again[0]) and torch.equal(got, again[1])
+
+
+def test_scales_of_either_sign_and_zero():
+    """A value is e4m3 * scale, whatever the scale is."""
+    g = gen(41)
+    k, v, ks, vs = paged(20, 16, 2, 128, True, DEV, g)
+    vs *= torch.where(torch.rand(vs.shape, generator=g, device=DEV) < 0.5, -1.0, 1.0)
+    vs[:, 3] = 0.0
+    vs[4:6] = 0.0
+    vs[7] *= -2.0 ** 12
+    table = torch.arange(20, dtype=torch.int32, device=DEV).view(1, 20)
+    lens = torch.tensor([311], dtype=torch.int32, device=DEV)
+    q = torch.randn(1, 16, 128, generator=g, device=DEV).bfloat16()
+    st = epd.new_status(DEV)
+    out, _ = epd.ep_decode_attention(q, k, v, table, lens, epd.new_attention_workspace(1, 16, 2, 128, DEV), st, k_scale=ks, v_scale=vs)
+    want, _ = attend(q, values(k, ks), values(v, vs), table, lens)
+    size, _ = attend(q, values(k, ks), values(v, vs).abs(), table, lens)
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -14 + 2.0 ** -11) * size
+    assert int(st) == 0 and bool(((out.double() - want).abs() <= tol).all())
+    # an infinite or NaN scale makes its own kv head's output so, and no other's
+    for bad in (float("inf"), float("nan")):
+        vs[9, 2, 1] = bad
+        got, _ = epd.ep_decode_attention(q, k, v, table, lens, epd.new_attention_workspace(1, 16, 2, 128, DEV), st, k_scale=ks, v_scale=vs)
+        assert torch.equal(got[0, :8], out[0, :8]) and not bool(got[0, 8:].isfinite().any())

@@ -33,7 +33,7 @@
 // Precision: products of bf16 are exact, sums in 32 bits. The weights of a bf16 cache's values are split
 // into two bf16 (15 bits at least), so that the output's own rounding is the only one that matters. An
 // e4m3 cache is widened to fp16, which holds it exactly; a head's query is scaled by a power of two and
-// the weights, with the values' scales in them, by the largest scale so far, to fp16's range (11
+// the weights, with the values' scales in them, by a reference that follows the scales, to fp16's range (11
 // bits: an eighth of the output's rounding).
 #include <cuda_fp16.h>
 
@@ -55,11 +55,22 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLn2 = 0.6931471805599453f;
 // A maximum is moved (and everything summed so far scaled down) only when a score passes it by more
 // than a factor: terms up to 2^8 lose nothing in 32 bits, and the scaling is rare. Of an e4m3 cache,
-// whose weights are fp16, it is 2^4, the largest value scale moves by factors of 4, and the weights
-// are 2^9 as large as they are: 2^15 at most, and in steps of 2^-33 or 2^-11 of their size, so that
-// what a quarter of a million tokens of small weights lose is far below the output's own rounding.
+// whose weights are fp16, it is 2^4, the values' scales may pass their reference by 4, and the weights
+// are 2^9 as large as they are: 2^15 at most, and off by 2^-11 of their size, or by 2^-34 where that is more and the
+// scale is the reference, so that what a quarter of a million tokens of small weights lose is far below the
+// output's own rounding.
 constexpr float kSlack = 8.0f, kSlackFp8 = 4.0f;
 constexpr float kValueSlack = 4.0f, kWeightUp = 512.0f;
+// A value's scale goes into its fp16 weight over a reference, a power of two that follows the scales. A tile
+// with one above kValueSlack of it, one below kValueRange or none from kValueNear up moves it to the tile's
+// largest (never below kValueFall of the segment's largest, so that the sums stay in 32 bits), and the
+// scales that are below its range then take another turn over the tile, with a reference of their own: a row of
+// zeros has scale 1, and may lie among values of any size. With one reference that only rose, a single such row
+// among 1000 of scale 2^-27 left 0.6 % of the output wrong, of 2^-37 26 %; now 0.17 % whatever the scales are
+// (the output's own rounding). The check costs 0.5 to 3 % (two of 131072 to 200001 tokens, 64 heads over 4: 81.8 ->
+// 84.6 us); a row of zeros in every 1000 another 1 %, in every 50, where most tiles take two turns, 24 %.
+constexpr float kValueRange = 0x1p-8f, kValueNear = 0x1p-3f, kValueFall = 0x1p-64f;
+constexpr float kLeastRef = 0x1p-119f;  // of a reference over kWeightUp: its inverse is finite
 
 struct AttnArgs {
     const uint8_t *q;
@@ -316,6 +327,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
     __shared__ int64_t s_scan[W];
     __shared__ float2 s_ml[W][HB], s_all[W][HB];  // maxima and sums of weights, a warp's and a team's
     __shared__ uint32_t s_last[W];
+    __shared__ float s_top[W];  // a warp's largest reference of the values' scales in a segment
     // what only a segment's end needs, so that it takes no registers of the loop: each warp's place and the
     // tiles of the sequences before it, and the block's run
     __shared__ Cursor s_cursor[W], s_load[W];
@@ -527,7 +539,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
     // ---- the line. o[k][n][i]: column 16 k + g + 8 (i / 2) (e4m3: 16 k + 2 g + i / 2) of head
     // 8 n + 2 c + i % 2; m and l: of heads 8 n + 2 c, 8 n + 2 c + 1, l of the lane's own tokens
     uint32_t q[KT][NH][2];
-    float o[KT][NH][4], m[NH][2], l[NH][2], q_scale[NH][2], v_ref = 0.0f, v_inv = 0.0f;
+    float o[KT][NH][4], m[NH][2], l[NH][2], q_scale[NH][2], v_ref = kLeastRef;
     // Fragments of the query: head g, and the columns that the keys' fragments pair with them -- of a
     // 16-byte unit of an e4m3 row a lane holds four neighbours.
     auto load_query = [&](const Cursor &at) {
@@ -589,7 +601,8 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
                 m[n][0] = m[n][1] = -INFINITY;
                 l[n][0] = l[n][1] = 0.0f;
             }
-            v_ref = v_inv = 0.0f;
+            v_ref = kLeastRef;
+            if (FP8 && lane == 0) s_top[warp] = 0.0f;
         }
         for (const int until = step + min(left, steps - step); step < until; ++step) {
             copy_wait<S::kStages - 2>();
@@ -603,7 +616,10 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
             const uint32_t at = ring + stage * S::kStage;
             uint32_t mask;
             asm volatile("ld.shared.u32 %0, [%1];" : "=r"(mask) : "r"(at + S::kStage - 16) : "memory");
-            if (mask) {
+            // (an e4m3 tile's values' scales from `done` up have had their turn)
+            float done = NAN;
+            for (bool turn = mask != 0; turn;) {
+                turn = false;
                 // s[t][n][i]: token 16 t + g + 8 (i / 2), head 8 n + 2 c + i % 2
                 float s[MT][NH][4] = {};
                 const int row = lane & 15, right = lane >> 4;
@@ -686,35 +702,61 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
                 }
                 float vs[MT][2];
                 if (FP8) {
-                    // the values' scales over the largest so far, which counts as no less than 2^-110: its inverse is finite
-                    bool larger = false;
+                    float most = 0.0f, least = INFINITY;
 #pragma unroll
                     for (int t = 0; t < MT; ++t)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             vs[t][i] = sc[CH + 16 * t + g + 8 * i];
-                            larger |= vs[t][i] > kValueSlack * kWeightUp * v_ref;
+                            const float size = fabsf(vs[t][i]);
+                            most = fmaxf(most, size);
+                            least = fminf(least, size > 0.0f ? size : INFINITY);
                         }
-                    if (__any_sync(kAll, larger)) {
-                        float most = 0.0f;
+                    const bool out = most > kValueSlack * kWeightUp * v_ref || least < kValueRange * kWeightUp * v_ref;
+                    if (__any_sync(kAll, out) || !__any_sync(kAll, most >= kValueNear * kWeightUp * v_ref)) {
+                        most = 0.0f;
 #pragma unroll
-                        for (int t = 0; t < MT; ++t) most = fmaxf(most, fmaxf(vs[t][0], vs[t][1]));
+                        for (int t = 0; t < MT; ++t)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                if (fabsf(vs[t][i]) >= done) vs[t][i] = 0.0f;
+                                most = fmaxf(most, fabsf(vs[t][i]));
+                            }
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, d));
-                        most = fmaxf(most, 0x1p-110f) / kWeightUp;
-                        const float f = v_ref / most;
-                        v_ref = most;
-                        v_inv = 1.0f / most;
+                        if (most > 0.0f) {
+                            most = __uint_as_float(__float_as_uint(most) & 0x7f800000u) / kWeightUp;
+                            const float now = fmaxf(fmaxf(most, kLeastRef), s_top[warp] * kValueFall), f = v_ref / now;
+                            v_ref = now;
+                            __syncwarp();
+                            if (lane == 0) s_top[warp] = fmaxf(s_top[warp], now);
+                            __syncwarp();
 #pragma unroll
-                        for (int k = 0; k < KT; ++k)
+                            for (int k = 0; k < KT; ++k)
 #pragma unroll
-                            for (int i = 0; i < 4 * NH; ++i) o[k][i >> 2][i & 3] *= f;
+                                for (int i = 0; i < 4 * NH; ++i) o[k][i >> 2][i & 3] *= f;
+                            if (now == most && now < INFINITY) {
+                                const float least = kValueRange * kWeightUp * now;
+                                bool later = false;
+#pragma unroll
+                                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                                    for (int i = 0; i < 2; ++i)
+                                        if (fabsf(vs[t][i]) < least && vs[t][i] != 0.0f) {
+                                            vs[t][i] = 0.0f;
+                                            later = true;
+                                        }
+                                turn = __any_sync(kAll, later);
+                            }
+                        }
                     }
+                    const float v_inv = fast_rcp(v_ref);  // exact: a power of two
 #pragma unroll
                     for (int t = 0; t < MT; ++t)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) vs[t][i] *= v_inv;
                 }
+                const float counts = done == done ? 0.0f : 1.0f;  // a token's weight counts once
                 // the weights, turned from (token, head) to (head, token) fragments
                 uint32_t p[MT][NH][2], p_lo[MT][NH][2];
 #pragma unroll
@@ -725,8 +767,8 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const float x = fast_exp2(s[t][n][2 * i] - base[0]), y = fast_exp2(s[t][n][2 * i + 1] - base[1]);
-                            l[n][0] += x;
-                            l[n][1] += y;
+                            l[n][0] = FP8 ? fmaf(x, counts, l[n][0]) : l[n][0] + x;
+                            l[n][1] = FP8 ? fmaf(y, counts, l[n][1]) : l[n][1] + y;
                             if (FP8) {
                                 p[t][n][i] = transpose8(pack2_f16(x * vs[t][i], y * vs[t][i]));
                             } else {
@@ -770,6 +812,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
                         }
                     }
                 }
+                if (FP8 && turn) done = kValueRange * kWeightUp * v_ref;
             }
             if (++stage == S::kStages) stage = 0;
         }
@@ -806,13 +849,14 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
 #pragma unroll
                     for (int j = 0; j < W; ++j)
                         if (j < mates) top = fmaxf(top, s_ml[team + (j << a.teams_log)][n * 8 + 2 * c + i].x);
-                    float f = m[n][i] == -INFINITY ? 0.0f : fast_exp2(m[n][i] - top);
-                    if (FP8) f *= v_ref;
+                    const float f = m[n][i] == -INFINITY ? 0.0f : fast_exp2(m[n][i] - top);
 #pragma unroll
-                    for (int k = 0; k < KT; ++k) {
-                        o[k][n][i] *= f;
-                        o[k][n][i + 2] *= f;
-                    }
+                    for (int k = 0; k < KT; ++k)
+#pragma unroll
+                        for (int j = i; j < 4; j += 2) {
+                            o[k][n][j] *= f;
+                            if (FP8) o[k][n][j] *= v_ref;  // (apart: their product may be too small a number)
+                        }
                 }
             if (tt < HB) {
                 float2 x[W];
