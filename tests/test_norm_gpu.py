@@ -281,3 +281,29 @@ def test_refusals():
         epd.ep_layer_norm(rand(1, 16392))
     with pytest.raises(epd.EpdError):
         epd.ep_layer_norm(x, eps=-1.0)
+
+
+def test_own_workspace_belongs_to_the_given_stream(monkeypatch):
+    """What a call on the current stream still has to write is not handed to a call on another one."""
+    from unpermute_ep_dispatch_gb300 import _binding
+    H = 8192
+    args = [(rand(300, H, seed=i, dtype=torch.bfloat16), rand(300, H, seed=i + 5, dtype=torch.bfloat16), rand(H, seed=i + 10),
+             rand(300, seed=i + 15).abs()) for i in range(2)]
+    want = [epd.ep_layer_norm_backward(*a, kind="rms") for a in args]
+    made, plain = [], _binding.new_norm_workspace
+
+    def new(*a):
+        made.append(plain(*a))
+        return made[-1]
+    monkeypatch.setattr(_binding, "new_norm_workspace", new)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # some ten milliseconds of the current stream
+    first = epd.ep_layer_norm_backward(*args[0], kind="rms")
+    places = [made.pop().data_ptr()]
+    second = epd.ep_layer_norm_backward(*args[1], kind="rms", stream=side)
+    places.append(made.pop().data_ptr())
+    torch.cuda.synchronize()
+    assert places[0] != places[1]
+    for got, ref in zip((first, second), want):
+        assert all(torch.equal(a, b) for a, b in zip(got[:2], ref[:2]))

@@ -9,6 +9,7 @@ torch.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import math
@@ -197,6 +198,14 @@ def _want(t, name, dtype, shape=None, device=None):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
+
+
+def _allocating(stream, device):
+    """Where a call's own memory is allocated: on the stream that it runs on, so that it is none that
+    another stream still has work on."""
+    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(device.index):
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream)
 
 
 def _out(t, name, dtype, shape, device):
@@ -958,9 +967,8 @@ def ep_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[t
         dbias = _out(dbias, "dbias", torch.float32, (H,), dev)
     if dweight is not None or dbias is not None:
         if workspace is None:
-            workspace = new_norm_workspace(H, dev)
-            if stream is not None:  # not to be handed out again before it has been read there
-                workspace.record_stream(stream)
+            with _allocating(stream, dev):
+                workspace = new_norm_workspace(H, dev)
         else:
             _want(workspace, "workspace", torch.uint8, device=dev)
             if workspace.numel() < epd_norm_workspace_bytes(H):
