@@ -5,7 +5,8 @@ pointers and the current CUDA stream to the C call of the same name and raises
 ``EpdError`` when the call returns a non-zero status. Every step of the path
 runs in libepd's kernels; there is no fallback. Output tensors may be passed in
 (for CUDA-graph capture and allocation-free steps) or are allocated here with
-torch.
+torch, on the stream that the call runs on: a call with ``stream=s`` is one under
+``torch.cuda.stream(s)``.
 """
 from __future__ import annotations
 
@@ -208,9 +209,16 @@ def _allocating(stream, device):
     return torch.cuda.stream(stream)
 
 
-def _out(t, name, dtype, shape, device):
-    if t is None:
+def _empty(shape, dtype, device, stream):
+    if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    with _allocating(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _out(t, name, dtype, shape, device, stream):
+    if t is None:
+        return _empty(shape, dtype, device, stream)
     return _want(t, name, dtype, shape, device)
 
 
@@ -270,11 +278,11 @@ def ep_dispatch_layout(topk_idx: torch.Tensor, num_experts: int, num_ranks: int,
         raise ValueError("workspace too small for this layout")
     if with_rdma is None:
         with_rdma = N > 1 or tokens_per_rdma_rank is not None
-    per_e = _out(tokens_per_expert, "tokens_per_expert", torch.int32, (E,), dev)
-    per_r = _out(tokens_per_rank, "tokens_per_rank", torch.int32, (R,), dev)
-    per_n = _out(tokens_per_rdma_rank, "tokens_per_rdma_rank", torch.int32, (N,), dev) \
+    per_e = _out(tokens_per_expert, "tokens_per_expert", torch.int32, (E,), dev, stream)
+    per_r = _out(tokens_per_rank, "tokens_per_rank", torch.int32, (R,), dev, stream)
+    per_n = _out(tokens_per_rdma_rank, "tokens_per_rdma_rank", torch.int32, (N,), dev, stream) \
         if with_rdma else None
-    itr = _out(is_token_in_rank, "is_token_in_rank", torch.bool, (T, R), dev) \
+    itr = _out(is_token_in_rank, "is_token_in_rank", torch.bool, (T, R), dev, stream) \
         if with_is_token_in_rank else None
     rc = load_library().ep_dispatch_layout(_ptr(topk_idx), T, k, E, R, N, _ptr(per_e),
                                            _ptr(per_r), _ptr(per_n), _ptr(itr), _ptr(workspace),
@@ -304,14 +312,14 @@ def ep_dispatch_layout_offsets(topk_idx: torch.Tensor, num_experts: int, num_ran
         raise ValueError("workspace too small for this layout")
     if with_rdma is None:
         with_rdma = N > 1 or tokens_per_rdma_rank is not None
-    per_e = _out(tokens_per_expert, "tokens_per_expert", torch.int32, (E,), dev)
-    per_r = _out(tokens_per_rank, "tokens_per_rank", torch.int32, (R,), dev)
-    per_n = _out(tokens_per_rdma_rank, "tokens_per_rdma_rank", torch.int32, (N,), dev) \
+    per_e = _out(tokens_per_expert, "tokens_per_expert", torch.int32, (E,), dev, stream)
+    per_r = _out(tokens_per_rank, "tokens_per_rank", torch.int32, (R,), dev, stream)
+    per_n = _out(tokens_per_rdma_rank, "tokens_per_rdma_rank", torch.int32, (N,), dev, stream) \
         if with_rdma else None
-    itr = _out(is_token_in_rank, "is_token_in_rank", torch.bool, (T, R), dev) \
+    itr = _out(is_token_in_rank, "is_token_in_rank", torch.bool, (T, R), dev, stream) \
         if with_is_token_in_rank else None
-    start = _out(expert_start_loc, "expert_start_loc", torch.int32, (E,), dev)
-    total = _out(total_rows, "total_rows", torch.int32, (1,), dev)
+    start = _out(expert_start_loc, "expert_start_loc", torch.int32, (E,), dev, stream)
+    total = _out(total_rows, "total_rows", torch.int32, (1,), dev, stream)
     rc = load_library().ep_dispatch_layout_offsets(
         _ptr(topk_idx), T, k, E, R, N, _ptr(per_e), _ptr(per_r), _ptr(per_n), _ptr(itr),
         int(alignment), _ptr(start), _ptr(total), _ptr(workspace), _ptr(status),
@@ -327,8 +335,8 @@ def ep_scan_offsets(tokens_per_expert: torch.Tensor, status: torch.Tensor,
     dev = tokens_per_expert.device
     E = tokens_per_expert.numel()
     _want(status, "status", torch.int32, (1,), dev)
-    start = _out(expert_start_loc, "expert_start_loc", torch.int32, (E,), dev)
-    total = _out(total_rows, "total_rows", torch.int32, (1,), dev)
+    start = _out(expert_start_loc, "expert_start_loc", torch.int32, (E,), dev, stream)
+    total = _out(total_rows, "total_rows", torch.int32, (1,), dev, stream)
     rc = load_library().ep_scan_offsets(_ptr(tokens_per_expert), E, _ptr(start), _ptr(total),
                                         _ptr(status), _stream(stream, dev))
     _check(rc, "ep_scan_offsets")
@@ -344,8 +352,8 @@ def ep_scan_offsets_aligned(tokens_per_expert: torch.Tensor, alignment: int,
     dev = tokens_per_expert.device
     E = tokens_per_expert.numel()
     _want(status, "status", torch.int32, (1,), dev)
-    start = _out(expert_start_loc, "expert_start_loc", torch.int32, (E,), dev)
-    total = _out(total_rows, "total_rows", torch.int32, (1,), dev)
+    start = _out(expert_start_loc, "expert_start_loc", torch.int32, (E,), dev, stream)
+    total = _out(total_rows, "total_rows", torch.int32, (1,), dev, stream)
     rc = load_library().ep_scan_offsets_aligned(_ptr(tokens_per_expert), E, int(alignment),
                                                 _ptr(start), _ptr(total), _ptr(status),
                                                 _stream(stream, dev))
@@ -387,14 +395,14 @@ def ep_permute(x: torch.Tensor, x_scale: Optional[torch.Tensor], topk_idx: torch
     _want(expert_start_loc, "expert_start_loc", torch.int32, (num_experts,), dev)
     _want(workspace, "workspace", torch.uint8, device=dev)
     _want(status, "status", torch.int32, (1,), dev)
-    out = _out(out, "out", x.dtype, (M, H), dev)
+    out = _out(out, "out", x.dtype, (M, H), dev, stream)
     if dt == EPD_FP8_E4M3:
         _want(x_scale, "x_scale", torch.float32, (T, H // 128), dev)
-        out_scale = _out(out_scale, "out_scale", torch.float32, (M, H // 128), dev)
+        out_scale = _out(out_scale, "out_scale", torch.float32, (M, H // 128), dev, stream)
     else:
         out_scale = None
-    m_indices = _out(m_indices, "m_indices", torch.int32, (M,), dev)
-    output_index = _out(output_index, "output_index", torch.int32, (T, k), dev)
+    m_indices = _out(m_indices, "m_indices", torch.int32, (M,), dev, stream)
+    output_index = _out(output_index, "output_index", torch.int32, (T, k), dev, stream)
     rc = load_library().ep_permute(_ptr(x), dt, _ptr(x_scale), _ptr(topk_idx), T, k, H,
                                    int(num_experts), _ptr(expert_start_loc), _ptr(workspace), M,
                                    _ptr(out), _ptr(out_scale), _ptr(m_indices),
@@ -441,22 +449,22 @@ def ep_dispatch(x: torch.Tensor, x_scale: Optional[torch.Tensor], topk_idx: torc
         raise ValueError("workspace too small for this layout")
     if with_rdma is None:
         with_rdma = N > 1 or tokens_per_rdma_rank is not None
-    per_e = _out(tokens_per_expert, "tokens_per_expert", torch.int32, (E,), dev)
-    per_r = _out(tokens_per_rank, "tokens_per_rank", torch.int32, (R,), dev)
-    per_n = _out(tokens_per_rdma_rank, "tokens_per_rdma_rank", torch.int32, (N,), dev) \
+    per_e = _out(tokens_per_expert, "tokens_per_expert", torch.int32, (E,), dev, stream)
+    per_r = _out(tokens_per_rank, "tokens_per_rank", torch.int32, (R,), dev, stream)
+    per_n = _out(tokens_per_rdma_rank, "tokens_per_rdma_rank", torch.int32, (N,), dev, stream) \
         if with_rdma else None
-    itr = _out(is_token_in_rank, "is_token_in_rank", torch.bool, (T, R), dev) \
+    itr = _out(is_token_in_rank, "is_token_in_rank", torch.bool, (T, R), dev, stream) \
         if with_is_token_in_rank else None
-    start = _out(expert_start_loc, "expert_start_loc", torch.int32, (E,), dev)
-    total = _out(total_rows, "total_rows", torch.int32, (1,), dev)
-    out = _out(out, "out", x.dtype, (M, H), dev)
+    start = _out(expert_start_loc, "expert_start_loc", torch.int32, (E,), dev, stream)
+    total = _out(total_rows, "total_rows", torch.int32, (1,), dev, stream)
+    out = _out(out, "out", x.dtype, (M, H), dev, stream)
     if dt == EPD_FP8_E4M3:
         _want(x_scale, "x_scale", torch.float32, (T, H // 128), dev)
-        out_scale = _out(out_scale, "out_scale", torch.float32, (M, H // 128), dev)
+        out_scale = _out(out_scale, "out_scale", torch.float32, (M, H // 128), dev, stream)
     else:
         out_scale = None
-    m_indices = _out(m_indices, "m_indices", torch.int32, (M,), dev)
-    output_index = _out(output_index, "output_index", torch.int32, (T, k), dev)
+    m_indices = _out(m_indices, "m_indices", torch.int32, (M,), dev, stream)
+    output_index = _out(output_index, "output_index", torch.int32, (T, k), dev, stream)
     rc = load_library().ep_dispatch(
         _ptr(x), dt, _ptr(x_scale), _ptr(topk_idx), T, k, H, E, R, N, int(alignment),
         _ptr(per_e), _ptr(per_r), _ptr(per_n), _ptr(itr), _ptr(start), _ptr(total),
@@ -493,7 +501,7 @@ def ep_permute_ex(x: torch.Tensor, x_scale: Optional[torch.Tensor], topk_idx: to
     _want(expert_start_loc, "expert_start_loc", torch.int32, (E,), dev)
     _want(workspace, "workspace", torch.uint8, device=dev)
     _want(status, "status", torch.int32, (1,), dev)
-    out = _out(out, "out", x.dtype, (M, *x.shape[1:]), dev)
+    out = _out(out, "out", x.dtype, (M, *x.shape[1:]), dev, stream)
     C = 0
     if x_scale is not None:
         if x_scale.dtype not in (torch.float32, torch.int32) or x_scale.dim() != 2:
@@ -502,12 +510,12 @@ def ep_permute_ex(x: torch.Tensor, x_scale: Optional[torch.Tensor], topk_idx: to
         C = x_scale.shape[1]
         ld = M if scale_ld is None else int(scale_ld)
         shape = (C, ld) if scale_col_major else (M, C)
-        out_scale = _out(out_scale, "out_scale", x_scale.dtype, shape, dev)
+        out_scale = _out(out_scale, "out_scale", x_scale.dtype, shape, dev, stream)
     else:
         ld = 0
         out_scale = None
-    m_indices = _out(m_indices, "m_indices", torch.int32, (M,), dev)
-    output_index = _out(output_index, "output_index", torch.int32, (T, k), dev)
+    m_indices = _out(m_indices, "m_indices", torch.int32, (M,), dev, stream)
+    output_index = _out(output_index, "output_index", torch.int32, (T, k), dev, stream)
     view = PermuteView(int(expert_begin), e_end, C, int(bool(scale_col_major)), ld)
     rc = load_library().ep_permute_ex(_ptr(x), row_bytes, _ptr(x_scale), _ptr(topk_idx), T, k, E,
                                       _ptr(expert_start_loc), _ptr(workspace), M,
@@ -540,12 +548,12 @@ def ep_permute_lowlatency(x: torch.Tensor, topk_idx: torch.Tensor, num_experts: 
     rows = int(rows_per_expert)
     _want(workspace, "workspace", torch.uint8, device=dev)
     _want(status, "status", torch.int32, (1,), dev)
-    out_q = _out(out_q, "out_q", torch.float8_e4m3fn, (EV, rows, H), dev)
-    out_scale = _out(out_scale, "out_scale", torch.float32, (EV, H // 128, rows), dev)
-    recv_count = _out(recv_count, "recv_count", torch.int32, (EV,), dev)
-    output_index = _out(output_index, "output_index", torch.int32, (T, k), dev)
+    out_q = _out(out_q, "out_q", torch.float8_e4m3fn, (EV, rows, H), dev, stream)
+    out_scale = _out(out_scale, "out_scale", torch.float32, (EV, H // 128, rows), dev, stream)
+    recv_count = _out(recv_count, "recv_count", torch.int32, (EV,), dev, stream)
+    output_index = _out(output_index, "output_index", torch.int32, (T, k), dev, stream)
     if with_src_token:
-        src_token = _out(src_token, "src_token", torch.int32, (EV, rows), dev)
+        src_token = _out(src_token, "src_token", torch.int32, (EV, rows), dev, stream)
     rc = load_library().ep_permute_lowlatency(
         _ptr(x), _ptr(topk_idx), T, k, H, E, int(expert_begin), e_end, rows, _ptr(workspace),
         _ptr(out_q), _ptr(out_scale), _ptr(recv_count), _ptr(output_index), _ptr(src_token),
@@ -579,12 +587,12 @@ def ep_dispatch_lowlatency(x: torch.Tensor, topk_idx: torch.Tensor, num_experts:
     _want(status, "status", torch.int32, (1,), dev)
     if workspace.numel() < epd_workspace_bytes(T, k, E, R, N):
         raise ValueError("workspace too small for this layout")
-    out_q = _out(out_q, "out_q", torch.float8_e4m3fn, (EV, rows, H), dev)
-    out_scale = _out(out_scale, "out_scale", torch.float32, (EV, H // 128, rows), dev)
-    recv_count = _out(recv_count, "recv_count", torch.int32, (EV,), dev)
-    output_index = _out(output_index, "output_index", torch.int32, (T, k), dev)
+    out_q = _out(out_q, "out_q", torch.float8_e4m3fn, (EV, rows, H), dev, stream)
+    out_scale = _out(out_scale, "out_scale", torch.float32, (EV, H // 128, rows), dev, stream)
+    recv_count = _out(recv_count, "recv_count", torch.int32, (EV,), dev, stream)
+    output_index = _out(output_index, "output_index", torch.int32, (T, k), dev, stream)
     if with_src_token:
-        src_token = _out(src_token, "src_token", torch.int32, (EV, rows), dev)
+        src_token = _out(src_token, "src_token", torch.int32, (EV, rows), dev, stream)
     rc = load_library().ep_dispatch_lowlatency(
         _ptr(x), _ptr(topk_idx), T, k, H, E, R, N, int(expert_begin), e_end, rows,
         _ptr(workspace), _ptr(out_q), _ptr(out_scale), _ptr(recv_count), _ptr(output_index),
@@ -606,7 +614,7 @@ def ep_unpermute(expert_out: torch.Tensor, output_index: torch.Tensor,
     T, k = output_index.shape
     _want(topk_weights, "topk_weights", torch.float32, (T, k), dev)
     _want(status, "status", torch.int32, (1,), dev)
-    y = _out(y, "y", torch.bfloat16, (T, H), dev)
+    y = _out(y, "y", torch.bfloat16, (T, H), dev, stream)
     rc = load_library().ep_unpermute(_ptr(expert_out), M, _ptr(output_index), _ptr(topk_weights),
                                      T, k, H, _ptr(y), _ptr(status), _stream(stream, dev))
     _check(rc, "ep_unpermute")
@@ -648,8 +656,8 @@ def ep_route(logits: torch.Tensor, num_topk: int, status: torch.Tensor, scoring:
     _want(status, "status", torch.int32, (1,), dev)
     if bias is not None:
         _want(bias, "bias", torch.float32, (E,), dev)
-    topk_idx = _out(topk_idx, "topk_idx", torch.int64, (T, k), dev)
-    topk_weights = _out(topk_weights, "topk_weights", torch.float32, (T, k), dev)
+    topk_idx = _out(topk_idx, "topk_idx", torch.int64, (T, k), dev, stream)
+    topk_weights = _out(topk_weights, "topk_weights", torch.float32, (T, k), dev, stream)
     rc = load_library().ep_route(_ptr(logits), dt, _ptr(bias), T, k, E, int(num_groups),
                                  int(topk_groups), gs, sc, int(bool(renormalize)),
                                  float(routed_scale), _ptr(topk_idx), _ptr(topk_weights),
@@ -673,7 +681,7 @@ def ep_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx
     k = topk_idx.shape[1]
     _want(grad_weights, "grad_weights", torch.float32, (T, k), dev)
     _want(status, "status", torch.int32, (1,), dev)
-    grad_logits = _out(grad_logits, "grad_logits", logits.dtype, (T, E), dev)
+    grad_logits = _out(grad_logits, "grad_logits", logits.dtype, (T, E), dev, stream)
     rc = load_library().ep_route_backward(_ptr(grad_weights), _ptr(logits), dt, _ptr(topk_idx), T,
                                           k, E, sc, int(bool(renormalize)), float(routed_scale),
                                           _ptr(grad_logits), _ptr(status), _stream(stream, dev))
@@ -757,9 +765,9 @@ def ep_expert_matmul(x: torch.Tensor, w: torch.Tensor, tokens_per_expert: torch.
         _want(bias, "bias", torch.float32, (E, NW), dev)
     if residual is not None:
         _want(residual, "residual", torch.bfloat16, (*lead, N), dev)
-    y = _out(y, "y", torch.bfloat16, (*lead, N), dev)
+    y = _out(y, "y", torch.bfloat16, (*lead, N), dev, stream)
     if preact is not None or with_preact:
-        preact = _out(preact, "preact", torch.bfloat16, (*lead, NW), dev)
+        preact = _out(preact, "preact", torch.bfloat16, (*lead, NW), dev, stream)
     rc = load_library().ep_expert_matmul(
         ctypes.byref(rows), _ptr(x), EPD_FP8_E4M3 if fp8 else EPD_BF16, _ptr(x_scale), srow, scol,
         sexp, _ptr(w), _ptr(w_scale),
@@ -791,7 +799,7 @@ def ep_expert_matmul_dgrad(dy: torch.Tensor, w: torch.Tensor, tokens_per_expert:
         _want(preact, "preact", torch.bfloat16, shape, dev)
     elif preact is not None:
         raise ValueError('activation "none" takes no preact')
-    dx = _out(dx, "dx", torch.bfloat16, shape, dev)
+    dx = _out(dx, "dx", torch.bfloat16, shape, dev, stream)
     rc = load_library().ep_expert_matmul_dgrad(ctypes.byref(rows), _ptr(dy), _ptr(w), K, N, act,
                                                _ptr(preact), _ptr(dx), _ptr(status),
                                                _stream(stream, dev))
@@ -817,9 +825,9 @@ def ep_expert_matmul_wgrad(dy: torch.Tensor, x: torch.Tensor, tokens_per_expert:
     N, K = shape[-1], x_shape[-1]
     rows = _expert_rows(shape, E, tokens_per_expert, expert_start_loc, dev)
     _want(status, "status", torch.int32, (1,), dev)
-    dw = _out(dw, "dw", torch.bfloat16, (E, N, K), dev)
+    dw = _out(dw, "dw", torch.bfloat16, (E, N, K), dev, stream)
     if dbias is not None or with_dbias:
-        dbias = _out(dbias, "dbias", torch.float32, (E, N), dev)
+        dbias = _out(dbias, "dbias", torch.float32, (E, N), dev, stream)
     rc = load_library().ep_expert_matmul_wgrad(ctypes.byref(rows), _ptr(dy), _ptr(x), K, N,
                                                _ptr(dw), _ptr(dbias), _ptr(status),
                                                _stream(stream, dev))
@@ -845,8 +853,8 @@ def ep_unpermute_backward(grad_y: torch.Tensor, expert_out: torch.Tensor,
     _want(grad_y, "grad_y", torch.bfloat16, (T, H), dev)
     _want(topk_weights, "topk_weights", torch.float32, (T, k), dev)
     _want(status, "status", torch.int32, (1,), dev)
-    grad_expert_out = _out(grad_expert_out, "grad_expert_out", torch.bfloat16, (M, H), dev)
-    grad_weights = _out(grad_weights, "grad_weights", torch.float32, (T, k), dev)
+    grad_expert_out = _out(grad_expert_out, "grad_expert_out", torch.bfloat16, (M, H), dev, stream)
+    grad_weights = _out(grad_weights, "grad_weights", torch.float32, (T, k), dev, stream)
     rc = load_library().ep_unpermute_backward(
         _ptr(grad_y), _ptr(expert_out), M, _ptr(output_index), _ptr(topk_weights), T, k, H,
         _ptr(grad_expert_out), _ptr(grad_weights), _ptr(status), _stream(stream, dev))
@@ -896,24 +904,24 @@ def ep_layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
         _want(bias, "bias", torch.float32, (H,), dev)
     if residual is not None:
         _want(residual, "residual", dtype, (T, H), dev)
-        sum = _out(sum, "sum", dtype, (T, H), dev)
+        sum = _out(sum, "sum", dtype, (T, H), dev, stream)
     elif sum is not None:
         raise ValueError("sum is an output of a norm with residual")
     if with_y or y is not None:
-        y = _out(y, "y", torch.bfloat16, (T, H), dev)
+        y = _out(y, "y", torch.bfloat16, (T, H), dev, stream)
     if with_fp8 or y_q is not None or y_scale is not None:
         if H % 128:
             raise ValueError(f"e4m3 rows need a multiple of 128 columns, got {H}")
-        y_q = _out(y_q, "y_q", torch.float8_e4m3fn, (T, H), dev)
-        y_scale = _out(y_scale, "y_scale", torch.float32, (T, H // 128), dev)
+        y_q = _out(y_q, "y_q", torch.float8_e4m3fn, (T, H), dev, stream)
+        y_scale = _out(y_scale, "y_scale", torch.float32, (T, H // 128), dev, stream)
     elif y is None:
         raise ValueError("a norm without y needs with_fp8")
     if kd and mean is not None:
         raise ValueError('kind "rms" has no mean')
     if (with_stats and not kd) or mean is not None:
-        mean = _out(mean, "mean", torch.float32, (T,), dev)
+        mean = _out(mean, "mean", torch.float32, (T,), dev, stream)
     if with_stats or rstd is not None:
-        rstd = _out(rstd, "rstd", torch.float32, (T,), dev)
+        rstd = _out(rstd, "rstd", torch.float32, (T,), dev, stream)
     rc = _on(load_library().ep_layer_norm, dev)(
         _ptr(x), dt, _ptr(residual), _ptr(weight), _ptr(bias), T, H, float(eps), kd, _ptr(sum),
         _ptr(y), _ptr(y_q), _ptr(y_scale), _ptr(mean), _ptr(rstd), _stream(stream, dev))
@@ -960,11 +968,11 @@ def ep_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[t
         _want(mean, "mean", torch.float32, (T,), dev)
     if grad_sum is not None:
         _want(grad_sum, "grad_sum", dtype, (T, H), dev)
-    dx = _out(dx, "dx", dtype, (T, H), dev)
+    dx = _out(dx, "dx", dtype, (T, H), dev, stream)
     if with_dweight or dweight is not None:
-        dweight = _out(dweight, "dweight", torch.float32, (H,), dev)
+        dweight = _out(dweight, "dweight", torch.float32, (H,), dev, stream)
     if with_dbias or dbias is not None:
-        dbias = _out(dbias, "dbias", torch.float32, (H,), dev)
+        dbias = _out(dbias, "dbias", torch.float32, (H,), dev, stream)
     if dweight is not None or dbias is not None:
         if workspace is None:
             with _allocating(stream, dev):
@@ -1094,7 +1102,7 @@ def ep_rotary(x: torch.Tensor, positions: torch.Tensor, steps: torch.Tensor,
         raise TypeError("steps must be a torch.Tensor")
     R = _steps(steps, D, dev)
     if out is None:
-        out = torch.empty((T, N, D), dtype=torch.bfloat16, device=dev)
+        out = _empty((T, N, D), torch.bfloat16, dev, stream)
         ot, oh = N * D, D
     else:
         _, (ot, oh, _) = _heads(out, "out", N, D, T, dev)
@@ -1195,7 +1203,7 @@ def ep_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
         qs = _token_rows(q, "q", None, D, T, dev)
         QH = q.shape[1]
         if q_out is None:
-            q_out = torch.empty((T, QH, D), dtype=torch.bfloat16, device=dev)
+            q_out = _empty((T, QH, D), torch.bfloat16, dev, stream)
         os_ = _token_rows(q_out, "q_out", QH, D, T, dev)
     elif q_out is not None:
         raise ValueError("q_out is the rotated q")
@@ -1245,9 +1253,9 @@ def ep_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     # (of any number of sequences: the size does not depend on it)
     if D % 8 == 0 and 0 < D <= 256 and workspace.numel() < epd_attention_workspace_bytes(1, QH, KH, D):
         raise ValueError("workspace too small for this attention")
-    out = _out(out, "out", torch.bfloat16, (B, QH, D), dev)
+    out = _out(out, "out", torch.bfloat16, (B, QH, D), dev, stream)
     if with_lse or lse is not None:
-        lse = _out(lse, "lse", torch.float32, (B, QH), dev)
+        lse = _out(lse, "lse", torch.float32, (B, QH), dev, stream)
     scale = D ** -0.5 if softmax_scale is None else float(softmax_scale)
     rc = _on(load_library().ep_decode_attention, dev)(
         cache, q.data_ptr(), qs, QH, lengths.data_ptr(), scale, int(window), workspace.data_ptr(),
@@ -1289,10 +1297,10 @@ def epd_test_layout_stalled_tile(topk_idx, num_experts, num_ranks, num_rdma_rank
     dev = topk_idx.device
     T, k = topk_idx.shape
     E, R, N = int(num_experts), int(num_ranks), int(num_rdma_ranks)
-    per_e = torch.empty(E, dtype=torch.int32, device=dev)
-    per_r = torch.empty(R, dtype=torch.int32, device=dev)
-    per_n = torch.empty(N, dtype=torch.int32, device=dev)
-    itr = torch.empty(T, R, dtype=torch.bool, device=dev)
+    per_e = _empty(E, torch.int32, dev, stream)
+    per_r = _empty(R, torch.int32, dev, stream)
+    per_n = _empty(N, torch.int32, dev, stream)
+    itr = _empty((T, R), torch.bool, dev, stream)
     rc = load_library().epd_test_layout_stalled_tile(
         _ptr(topk_idx), T, k, E, R, N, _ptr(per_e), _ptr(per_r), _ptr(per_n), _ptr(itr),
         _ptr(workspace), _ptr(status), int(stalled_tile), int(spin_limit), _stream(stream, dev))
