@@ -307,3 +307,24 @@ def test_own_workspace_belongs_to_the_given_stream(monkeypatch):
     assert places[0] != places[1]
     for got, ref in zip((first, second), want):
         assert all(torch.equal(a, b) for a, b in zip(got[:2], ref[:2]))
+
+
+@pytest.mark.parametrize("dtype,size,deviation", [(torch.float32, 2.0 ** 57, 1e14), (torch.float32, 1e18, 1e15), (torch.bfloat16, 1e18, 1e17),
+                                                  (torch.float32, 1e20, 1e17), (torch.float32, 1e25, 0.0), (torch.bfloat16, 1e25, 0.0)])
+def test_means_whose_squares_overflow(size, deviation, dtype):
+    """The squares' sum is infinite; the centred values' is not."""
+    T, H = 5, 7168
+    x = (size + deviation * rand(T, H)).to(dtype)
+    w, b = rand(H, seed=2, scale=0.3, shift=1.0), rand(H, seed=3)
+    if deviation == 0.0:  # every centred value is the mean's error, at most the root of the mean of their squares
+        d = epd.ep_layer_norm(x, with_stats=True)
+        near(d["mean"], x.double().mean(1), F32 * x.double().abs().amax(1), torch.float32)
+        assert bool((d["y"].float().abs() <= 1).all())
+        return
+    d = epd.ep_layer_norm(x, w, bias=b, with_stats=True)
+    s, mean, rstd, y, big = formula(x, None, w, b, 1e-5, "layer")
+    near(d["mean"], mean.squeeze(1), F32 * s.abs().amax(1), torch.float32)
+    # the mean's error adds its square to the variance: half of (F32 mean rstd)^2 of the root
+    off = F32 + (F32 * s.abs().amax(1, keepdim=True) * rstd).square() / 2
+    near(d["rstd"], rstd.squeeze(1), (off * rstd).squeeze(1), torch.float32)
+    near(d["y"], y, F32 * big + off * (y - b.double()).abs(), torch.bfloat16)

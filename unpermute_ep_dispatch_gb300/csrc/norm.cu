@@ -249,8 +249,9 @@ __global__ void __launch_bounds__(kNormThreads, NV * Chunk<T>::C <= 8 ? 2 : 1) n
             mean = __fdiv_rn(mean, (float)(a.chunks * C));
             var = fmaf(-mean, mean, sq * a.inv_h);
             // The squares' mean less the mean's square loses a bit at most where the mean is below the
-            // deviation; for the rows where it is not, the centred values are summed.
-            if (mean * mean > var) {
+            // deviation; for the rows where it is not, and those whose squares do not fit, the centred values are
+            // summed.
+            if (mean * mean > var || var == INFINITY) {
                 sq2 = both(0.0f);
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
