@@ -337,3 +337,34 @@ def test_graph_and_stream():
     torch.cuda.synchronize()
     got = [t.clone() for t in out]
     assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
+@pytest.mark.parametrize("D,R,interleaved", [(128, 128, False), (128, 64, True), (64, 0, False), (80, 24, False), (48, 6, True), (256, 256, False)])
+def test_append_carries_values_over(D, R, interleaved):
+    """Values (and keys that are not rotated) are written as they are, or as e4m3 numbers of the quotients by
+    their scale: both to the last bit."""
+    T, KH, page = 1500, 4, 16
+    qkv = rand(T, 2 * KH, D, seed=D)
+    pages = -(-T // page) + 3
+    table = torch.randperm(pages, generator=gen(D), device=DEV).int().view(1, pages)
+    pos = torch.randperm(pages * page, generator=gen(D + 1), device=DEV)[:T].int()
+    seq = torch.zeros(T, dtype=torch.int32, device=DEV)
+    seq[::5] = -1
+    live = seq == 0
+    at = table[0, pos.long() // page].long()[live], pos.long()[live] % page
+    steps = epd.rotary_steps(epd.rotary_frequencies(R)[0], DEV) if R else None
+    for fp8 in (False, True):
+        k, v, ks, vs = paged(pages, page, KH, D, fp8, DEV, gen(1))
+        st = epd.new_status(DEV)
+        epd.ep_cache_append(qkv[:, :KH], qkv[:, KH:], k, v, table, pos, st, token_seq=seq, steps=steps, interleaved=interleaved,
+                            k_scale=ks, v_scale=vs)
+        assert int(st) == 0
+        for cache, scale, rows in ((v, vs, qkv[live, KH:]),) + (() if R else ((k, ks, qkv[live, :KH]),)):
+            if not fp8:
+                assert torch.equal(cache[at], rows)
+                continue
+            rows = rows.float()
+            want = rows.abs().amax(-1) / torch.full(rows.shape[:2], 448.0, device=DEV)
+            assert torch.equal(scale[at], want)
+            codes = (rows / want.unsqueeze(-1).expand_as(rows)).clamp(-448, 448).to(FP8)
+            assert torch.equal(cache.view(torch.uint8)[at], codes.view(torch.uint8))

@@ -328,3 +328,23 @@ def test_means_whose_squares_overflow(size, deviation, dtype):
     off = F32 + (F32 * s.abs().amax(1, keepdim=True) * rstd).square() / 2
     near(d["rstd"], rstd.squeeze(1), (off * rstd).squeeze(1), torch.float32)
     near(d["y"], y, F32 * big + off * (y - b.double()).abs(), torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H", [128, 512, 1152, 7168, 8320])
+def test_e4m3_rows_are_the_rounded_quotients(H, dtype):
+    """x = 1 or -1 is its own root-mean-square norm: the rows are the weights, whose e4m3 numbers are those
+    of the quotients by the scale, to the last one."""
+    T = 700
+    x = torch.where(rand(T, H) < 0, -1.0, 1.0).to(dtype)
+    for seed in range(20):
+        w = rand(H, seed=seed, scale=2.0 ** (seed - 10))
+        if seed % 2:
+            w = w.bfloat16().float()
+        d = epd.ep_layer_norm(x, w, eps=0.0, kind="rms", with_fp8=True)
+        b = w.view(-1, 128)
+        scale = b.abs().amax(1) / torch.full((H // 128,), 448.0, device=DEV)
+        assert torch.equal(d["y_scale"], scale.expand(T, -1))
+        want = (x.float() * w).view(T, -1, 128) / scale[:, None].expand(T, -1, 128)
+        want = want.clamp(-448, 448).to(torch.float8_e4m3fn).view(T, H)
+        assert torch.equal(d["y_q"].float(), want.float())

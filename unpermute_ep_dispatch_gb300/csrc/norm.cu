@@ -324,23 +324,27 @@ __global__ void __launch_bounds__(kNormThreads, NV * Chunk<T>::C <= 8 ? 2 : 1) n
             const float scale = top[0] > 0.0f ? __fdiv_rn(top[0], 448.0f) : 1.0f, inv = __fdiv_rn(1.0f, scale);
             const int group = (tid + mine * n) / G;
             if ((lane & (G / NV - 1)) == 0 && group * G < a.chunks) a.yscale[row * (a.chunks / G) + group] = scale;
-            const bool tiny = __any_sync(kAll, scale < 0x1p-120f);  // its inverse may overflow
+            const bool tiny = __any_sync(kAll, scale < kTinyScale);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = tid + i * n;
                 int from = lane & ~(G - 1);
 #pragma unroll
                 for (int step = 1, d = G / 2; step < NV; step *= 2, d /= 2) from += i & step ? d : 0;
-                const float by = __shfl_sync(kAll, tiny ? scale : inv, from);
+                const float by = __shfl_sync(kAll, scale, from), inverse = __shfl_sync(kAll, inv, from);
                 if (c >= a.chunks) continue;
                 float f[C];
-#pragma unroll
-                for (int j = 0; j < C; ++j) f[j] = j & 1 ? v[i].v[j / 2].y : v[i].v[j / 2].x;
                 if (tiny) {
+#pragma unroll
+                    for (int j = 0; j < C; ++j) f[j] = j & 1 ? v[i].v[j / 2].y : v[i].v[j / 2].x;
                     divide_all(f, by);
                 } else {
+                    const Quotient quotient(by, inverse);
 #pragma unroll
-                    for (int j = 0; j < C; ++j) f[j] *= by;
+                    for (int j = 0; j < C; j += 2) {
+                        const float2 u = quotient(v[i].v[j / 2]);
+                        f[j] = u.x, f[j + 1] = u.y;
+                    }
                 }
                 uint32_t q[C / 4];
 #pragma unroll
