@@ -368,3 +368,24 @@ def test_append_carries_values_over(D, R, interleaved):
             assert torch.equal(scale[at], want)
             codes = (rows / want.unsqueeze(-1).expand_as(rows)).clamp(-448, 448).to(FP8)
             assert torch.equal(cache.view(torch.uint8)[at], codes.view(torch.uint8))
+
+
+def test_append_of_rows_below_448_of_the_smallest_number():
+    """A rotary scale may take keys below 2^-141, where amax / 448 rounds to 0: their scale is the smallest
+    number there is then, never 0."""
+    k, v, ks, vs = paged(4, 8, 2, 64, True, DEV, gen(0))
+    x = rand(4, 2, 64)
+    x[..., ::3] = 0
+    table = torch.arange(4, dtype=torch.int32, device=DEV).view(4, 1)
+    pos = torch.zeros(4, dtype=torch.int32, device=DEV)
+    st = epd.new_status(DEV)
+    steps = epd.rotary_steps(epd.rotary_frequencies(64)[0], DEV)
+    for power in (-120, -140, -146):
+        epd.ep_cache_append(x, x, k, v, table, pos, st, steps=steps, rotary_scale=2.0 ** power, k_scale=ks, v_scale=vs)
+        rows, scale = x.double() * 2.0 ** power, ks[:, 0].double()
+        assert bool((scale > 0).all())
+        # half a step of e4m3, a step of the products (2^-149 each), half a step of the scale times 448
+        got = k[:, 0].double() * scale.unsqueeze(-1)
+        tol = 2.0 ** -4 * rows.abs() + 2.0 ** -10 * scale.unsqueeze(-1) + 226 * 2.0 ** -149
+        assert bool(((got - rows).abs() <= tol).all())
+    assert int(st) == 0

@@ -348,3 +348,18 @@ def test_e4m3_rows_are_the_rounded_quotients(H, dtype):
         want = (x.float() * w).view(T, -1, 128) / scale[:, None].expand(T, -1, 128)
         want = want.clamp(-448, 448).to(torch.float8_e4m3fn).view(T, H)
         assert torch.equal(d["y_q"].float(), want.float())
+
+
+@pytest.mark.parametrize("power", [-126, -139, -143, -147])
+def test_rows_below_448_of_the_smallest_number(power):
+    """amax / 448 rounds to 0 below 2^-141: the scale is the smallest number there is then, never 0."""
+    x = torch.where(rand(9, 512) < 0, -1.0, 1.0)
+    w = rand(512).abs() * 2.0 ** power
+    w[::7] = 0.0
+    d = epd.ep_layer_norm(x, w, eps=0.0, kind="rms", with_fp8=True)
+    y = x.double() * w.double()
+    scale = d["y_scale"].double().repeat_interleave(128, 1)
+    assert bool((scale > 0).all())
+    # half a step of e4m3, and 448 half steps of the scale's own 2^-149
+    tol = 2.0 ** -4 * y.abs() + 2.0 ** -10 * scale + 224 * 2.0 ** -149
+    assert bool(((d["y_q"].double() * scale - y).abs() <= tol).all())

@@ -45,6 +45,12 @@ struct Quotient {
     }
 };
 
+// The scale of e4m3 numbers whose largest is amax: amax / 448, 1 of 0; where it would round to 0, the
+// smallest number there is.
+__device__ __forceinline__ float e4m3_scale(float amax) {
+    return amax > 0.0f ? fmaxf(__fdiv_rn(amax, 448.0f), 0x1p-149f) : 1.0f;
+}
+
 // Scales below this: the remainder, or the scale's inverse, may not fit.
 constexpr float kTinyScale = 0x1p-80f;
 

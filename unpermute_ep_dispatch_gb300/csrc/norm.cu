@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kNormThreads, NV * Chunk<T>::C <= 8 ? 2 : 1) n
                     top[0] = fmaxf(top[0], __shfl_xor_sync(kAll, top[0], d));
                 }
             }
-            const float scale = top[0] > 0.0f ? __fdiv_rn(top[0], 448.0f) : 1.0f, inv = __fdiv_rn(1.0f, scale);
+            const float scale = e4m3_scale(top[0]), inv = __fdiv_rn(1.0f, scale);
             const int group = (tid + mine * n) / G;
             if ((lane & (G / NV - 1)) == 0 && group * G < a.chunks) a.yscale[row * (a.chunks / G) + group] = scale;
             const bool tiny = __any_sync(kAll, scale < kTinyScale);

@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, V == 4 ? 9 : V == 8 ? 6 : 1) append_
                 for (int i = 0; i < B; ++i) {
                     const int n = first + (i0 + i) * per_pass;
                     if (i0 + i >= walk.passes || n >= walk.heads) continue;
-                    const float by = scale[i] > 0.0f ? __fdiv_rn(scale[i], 448.0f) : 1.0f;
+                    const float by = e4m3_scale(scale[i]);
                     uint8_t *const head = to + slot + n * step;
 #pragma unroll
                     for (int q = 0; q < NP; ++q)
