@@ -487,3 +487,23 @@ def test_scales_of_either_sign_and_zero():
         vs[9, 2, 1] = bad
         got, _ = epd.ep_decode_attention(q, k, v, table, lens, epd.new_attention_workspace(1, 16, 2, 128, DEV), st, k_scale=ks, v_scale=vs)
         assert torch.equal(got[0, :8], out[0, :8]) and not bool(got[0, 8:].isfinite().any())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [1, 17, 33, 129, 300, 513, 5000])
+def test_lse_of_nan_scores(n, fp8):
+    """A NaN key makes its kv head's output and lse NaN, wherever its tile is joined."""
+    g = gen(n)
+    for at in (0, n - 1):
+        k, v, ks, vs = paged(-(-n // 16), 16, 2, 64, fp8, DEV, g)
+        if fp8:
+            ks[at // 16, at % 16, 1] = float("nan")
+        else:
+            k[at // 16, at % 16, 1, 5] = float("nan")
+        table = torch.arange(-(-n // 16), dtype=torch.int32, device=DEV).view(1, -1)
+        q = torch.randn(1, 8, 64, generator=g, device=DEV).bfloat16()
+        st = epd.new_status(DEV)
+        out, lse = epd.ep_decode_attention(q, k, v, table, torch.tensor([n], dtype=torch.int32, device=DEV),
+                                           epd.new_attention_workspace(1, 8, 2, 64, DEV), st, k_scale=ks, v_scale=vs, with_lse=True)
+        assert bool(out[0, 4:].isnan().all()) and bool(lse[0, 4:].isnan().all())
+        assert bool(out[0, :4].isfinite().all()) and bool(lse[0, :4].isfinite().all())

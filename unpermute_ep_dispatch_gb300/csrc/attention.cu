@@ -302,7 +302,7 @@ __device__ __forceinline__ void combine_parts(const float *part0, const float *p
             for (int d = 16; d; d >>= 1) sum[j] += __shfl_xor_sync(kAll, sum[j], d);
             const float inv = sum[j] > 0.0f ? __fdiv_rn(1.0f, sum[j]) : sum[j];
             if (r >= rows) continue;
-            if (lse && lane == 0) lse[r] = top[j] == -INFINITY ? -INFINITY : (top[j] + log2f(sum[j])) * kLn2;
+            if (lse && lane == 0) lse[r] = (top[j] + log2f(sum[j])) * kLn2;  // -inf of none
             if (col < D) {
 #pragma unroll
                 for (int k = 0; k < C; k += 2)
@@ -867,7 +867,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
                     top = fmaxf(top, x[j].x);
                 }
 #pragma unroll
-                for (int j = 0; j < W; ++j) sum += x[j].x == -INFINITY ? 0.0f : x[j].y * fast_exp2(x[j].x - top);
+                for (int j = 0; j < W; ++j) sum += x[j].x == -INFINITY ? x[j].y : x[j].y * fast_exp2(x[j].x - top);  // (0, or NaN of NaN scores alone)
                 s_all[team][tt] = make_float2(top, sum);
             }
             const int64_t all_parts = (int64_t)S::kPart << a.teams_log;  // of a block's run: one for every team
@@ -911,7 +911,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
             if (tt < rows) {
                 const float top = s_all[team][tt].x, sum = s_all[team][tt].y;
                 if (whole) {
-                    if (a.lse) a.lse[(int64_t)cp.b * a.QH + h0 + tt] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
+                    if (a.lse) a.lse[(int64_t)cp.b * a.QH + h0 + tt] = (top + log2f(sum)) * kLn2;
                 } else {
                     part[HB * DP + tt] = top;
                     part[HB * DP + HB + tt] = sum;
