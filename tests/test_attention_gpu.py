@@ -507,3 +507,21 @@ def test_lse_of_nan_scores(n, fp8):
                                            epd.new_attention_workspace(1, 8, 2, 64, DEV), st, k_scale=ks, v_scale=vs, with_lse=True)
         assert bool(out[0, 4:].isnan().all()) and bool(lse[0, 4:].isnan().all())
         assert bool(out[0, :4].isfinite().all()) and bool(lse[0, :4].isfinite().all())
+
+
+def test_windows_of_any_size():
+    """A window past 2^31 - 1 is the whole context, and no remainder of it."""
+    g = gen(42)
+    k, v, _, _ = paged(20, 16, 2, 64, False, DEV, g)
+    table, lens = torch.arange(20, dtype=torch.int32, device=DEV).view(1, 20), torch.tensor([300], dtype=torch.int32, device=DEV)
+    q = torch.randn(1, 4, 64, generator=g, device=DEV).bfloat16()
+    ws, st = epd.new_attention_workspace(1, 4, 2, 64, DEV), epd.new_status(DEV)
+
+    def f(window):
+        return epd.ep_decode_attention(q, k, v, table, lens, ws, st, window=window)[0]
+    whole = f(0)
+    for window in (300, 2**31 - 1, 2**31, 2**32, 2**32 + 5, 2**63 + 7):
+        assert torch.equal(f(window), whole), window
+    for window in (-1, -2**31, -2**32, -2**32 + 5):
+        with pytest.raises(epd.EpdError):
+            f(window)

@@ -38,6 +38,7 @@ EPD_F32 = 2
 EPD_MAX_EXPERTS = 4096
 EPD_MAX_TOPK = 64
 EPD_MAX_GROUPS = 64
+_INT_MAX = 2**31 - 1
 SCORING = {"softmax": 0, "sigmoid": 1}
 GROUP_SCORE = {"max": 0, "top2": 1}
 NORM = {"layer": 0, "rms": 1}
@@ -1257,8 +1258,9 @@ def ep_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     if with_lse or lse is not None:
         lse = _out(lse, "lse", torch.float32, (B, QH), dev, stream)
     scale = D ** -0.5 if softmax_scale is None else float(softmax_scale)
+    window = max(-1, min(int(window), _INT_MAX))  # no sequence is longer
     rc = _on(load_library().ep_decode_attention, dev)(
-        cache, q.data_ptr(), qs, QH, lengths.data_ptr(), scale, int(window), workspace.data_ptr(),
+        cache, q.data_ptr(), qs, QH, lengths.data_ptr(), scale, window, workspace.data_ptr(),
         out.data_ptr(), _ptr(lse), status.data_ptr(), _stream(stream, dev))
     _check(rc, "ep_decode_attention")
     return out, lse
