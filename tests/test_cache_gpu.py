@@ -389,3 +389,20 @@ def test_append_of_rows_below_448_of_the_smallest_number():
         tol = 2.0 ** -4 * rows.abs() + 2.0 ** -10 * scale.unsqueeze(-1) + 226 * 2.0 ** -149
         assert bool(((got - rows).abs() <= tol).all())
     assert int(st) == 0
+
+
+def test_sizes_past_32_bits_are_refused():
+    """The C entry points take 32-bit sizes: a larger one is an error, not its remainder."""
+    few = torch.zeros(8, dtype=torch.int32, device=DEV)
+    many = 2 ** 32 + 8
+    rows = torch.zeros(1, 8, dtype=torch.bfloat16, device=DEV).expand(many, 8)
+    heads = torch.zeros(1, 1, 8, dtype=torch.bfloat16, device=DEV).expand(many, 1, 8)
+    steps, st = epd.rotary_steps([1.0, 0.5, 0.2, 0.1], DEV), epd.new_status(DEV)
+    cache = torch.zeros(2, 4, 1, 8, dtype=torch.bfloat16, device=DEV)
+    table = torch.zeros(1, 2, dtype=torch.int32, device=DEV)
+    for bad in (lambda: epd.ep_layer_norm(rows), lambda: epd.ep_layer_norm_backward(rows, rows, None, few, kind="rms"),
+                lambda: epd.ep_rotary(heads, few, steps), lambda: epd.ep_rotary(heads.transpose(0, 1), few, steps),
+                lambda: epd.ep_cache_append(heads, heads, cache, cache, table, few, st, token_seq=few),
+                lambda: epd.ep_decode_attention(heads, cache, cache, table.expand(many, 2), few, few.view(torch.uint8), st)):
+        with pytest.raises(ValueError, match="2147483647"):
+            bad()

@@ -875,10 +875,17 @@ def _on(fn, dev):
     return there
 
 
+def _sizes(shape, name):
+    """Refuses what the C entry points' 32-bit sizes do not hold."""
+    if max(shape, default=0) > _INT_MAX:
+        raise ValueError(f"{name} has a size past {_INT_MAX}: {tuple(shape)}")
+
+
 def _norm_rows(t, name):
     dtype = t.dtype if isinstance(t, torch.Tensor) else None
     if dtype is not torch.float32 and dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be a float32 or bfloat16 tensor")
+    _sizes(t.shape, name)
     _want(t, name, dtype)
     if t.dim() != 2:
         raise ValueError(f"{name} must be [num_tokens, hidden]")
@@ -1048,6 +1055,7 @@ def _heads(t, name, heads=None, dim=None, tokens=None, device=None):
     if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
     shape = t.shape
+    _sizes(shape, name)
     if len(shape) != 3 or (heads is not None and shape[1] != heads) or \
             (dim is not None and shape[2] != dim) or (tokens is not None and shape[0] != tokens):
         want = ", ".join(str(n) if v is None else str(v)
@@ -1066,7 +1074,7 @@ def _token_rows(t, name, heads, dim, tokens, device):
     try:  # the common case, in few attribute look-ups; what fails it is told apart below
         shape, strides = t.shape, t.stride()
         if (len(shape) == 3 and shape[0] == tokens and shape[2] == dim == strides[1]
-                and strides[2] == 1 and (heads is None or shape[1] == heads)
+                and strides[2] == 1 and (shape[1] <= _INT_MAX if heads is None else shape[1] == heads)
                 and t.dtype is torch.bfloat16 and t.get_device() == device.index >= 0):
             return strides[0] if tokens > 1 else shape[1] * dim
     except AttributeError:
@@ -1168,9 +1176,14 @@ def _cache(k, v, page_table, k_scale, v_scale):
         st = 0
     if KH <= 1:
         sh = 0
-    packed = _CACHE_BYTES.pack(EPD_FP8_E4M3 if fp8 else EPD_BF16, KH, D, rows, P, k.data_ptr(),
-                               v.data_ptr(), kp, vp, sp, st, sh, cp, ct, ch,
-                               page_table.data_ptr(), S, M, ts if S > 1 else M)
+    try:
+        packed = _CACHE_BYTES.pack(EPD_FP8_E4M3 if fp8 else EPD_BF16, KH, D, rows, P, k.data_ptr(),
+                                   v.data_ptr(), kp, vp, sp, st, sh, cp, ct, ch,
+                                   page_table.data_ptr(), S, M, ts if S > 1 else M)
+    except struct.error:
+        _sizes(shape[1:], "the cache")
+        _sizes((S, M), "page_table")
+        raise
     return packed, dev, S, KH, D
 
 
@@ -1190,6 +1203,8 @@ def ep_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_c
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be [T, kv_heads, dim]")
     T = k.shape[0]
+    if T > _INT_MAX:
+        _sizes(k.shape, "k")
     ks = _token_rows(k, "k", KH, D, T, dev)
     vs = _token_rows(v, "v", KH, D, T, dev)
     _want(positions, "positions", torch.int32, (T,), dev)
