@@ -97,3 +97,16 @@ def test_shared_rows(lib):
     attention = dict(c=cache(S=0, sh=0, ts=0), q=None, qs=256, QH=4, lens=None, scale=0.1, window=0, ws=None, out=None, lse=None,
                      st=FAKE, s=None)
     assert lib.ep_decode_attention(*attention.values()) == OK
+
+
+def test_frequencies_refuse_what_has_no_blend():
+    """The blend's ends are logarithms to the base of turns over the original length."""
+    f = _binding.rotary_frequencies
+    for bad in (dict(base=1.0), dict(base=0.5), dict(beta_fast=0.0), dict(beta_slow=0.0), dict(beta_slow=-1.0), dict(original_length=0),
+                dict(base=float("nan")), dict(base=float("inf")), dict(factor=float("inf")), dict(beta_fast=0.5)):
+        with pytest.raises(ValueError):
+            f(64, **{**dict(scaling="yarn", factor=4.0), **bad})
+    for bad in (dict(base=float("inf")), dict(factor=float("inf"), scaling="linear"), dict(factor=float("inf"), scaling="ntk")):
+        with pytest.raises(ValueError):
+            f(64, **bad)
+    assert float(f(64, base=0.5)[0][0]) == 1.0  # (without a blend any positive base does)

@@ -1009,8 +1009,8 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "n
     R = int(rotary_dim)
     if R < 2 or R % 2:
         raise ValueError(f"rotary_dim must be even and at least 2, got {rotary_dim}")
-    if not base > 0 or not factor >= 1:
-        raise ValueError("base must be positive and factor at least 1")
+    if not 0 < base < math.inf or not 1 <= factor < math.inf:
+        raise ValueError("base must be positive and factor at least 1, both finite")
     if scaling not in ("none", "linear", "ntk", "yarn"):
         raise ValueError(f'scaling must be "none", "linear", "ntk" or "yarn", got {scaling!r}')
     if scaling == "ntk" and R > 2:
@@ -1020,6 +1020,9 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "n
         return f / factor, 1.0
     if scaling != "yarn" or factor == 1:
         return f, 1.0
+
+    if not base > 1 or not 0 < beta_slow <= beta_fast or not original_length > 0:
+        raise ValueError("yarn needs base > 1, 0 < beta_slow <= beta_fast and a positive original_length")
 
     def pair_of(turns):  # the (fractional) pair that turns so often over the original length
         return R * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
