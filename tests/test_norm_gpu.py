@@ -363,3 +363,22 @@ def test_rows_below_448_of_the_smallest_number(power):
     # half a step of e4m3, and 448 half steps of the scale's own 2^-149
     tol = 2.0 ** -4 * y.abs() + 2.0 ** -10 * scale + 224 * 2.0 ** -149
     assert bool(((d["y_q"].double() * scale - y).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H", [(700, 128), (5000, 256), (9000, 512), (33, 640), (1300, 1152), (5, 8320), (400, 8320), (170, 16256)])
+def test_e4m3_rows_of_ragged_widths(T, H, dtype, residual):
+    """Blocks that walk over many rows, and widths whose last groups of 128 some of a block's lanes have and others have not."""
+    x, r = rand(T, H, dtype=dtype, scale=2.0, shift=0.7), rand(T, H, seed=1, dtype=dtype) if residual else None
+    w, b = rand(H, seed=2, scale=0.3, shift=1.0), rand(H, seed=3)
+    d = epd.ep_layer_norm(x, w, bias=b, residual=r, with_fp8=True)
+    s, _, _, y, big = formula(x, r, w, b, 1e-5, "layer")
+    near(d["y"], y, F32 * big, torch.bfloat16)
+    blocks, bigs = y.view(T, -1, 128).abs().amax(2), big.reshape(T, -1, 128).amax(2)
+    near(d["y_scale"], blocks / 448, F32 * bigs / 448 + 2.0 ** -24 * blocks / 448, torch.float32)
+    scale = d["y_scale"].double().repeat_interleave(128, 1)
+    tol = HALF[torch.float8_e4m3fn] * y.abs() + 2.0 ** -10 * scale + 2 * F32 * big
+    assert bool(((d["y_q"].double() * scale - y).abs() <= tol).all())
+    only = epd.ep_layer_norm(x, w, bias=b, residual=r, with_y=False, with_fp8=True)
+    assert torch.equal(only["y_q"].view(torch.uint8), d["y_q"].view(torch.uint8)) and torch.equal(only["y_scale"], d["y_scale"])
