@@ -583,9 +583,9 @@ typedef enum {
  * in fp32 and rounded once to each of
  *   sum  [T, H] of x's type: s, the residual stream from here on (only with residual);
  *   y    [T, H] bfloat16: n, what the router's projection and the products read;
- *   y_q  [T, H] e4m3 with y_scale [T, H/128] float32: n with one scale per 128 columns,
- *        amax / 448 (1 where amax is 0), as ep_dispatch and ep_permute take rows
- *        (H % 128 == 0);
+ *   y_q  [T, H] e4m3 with y_scale [T, H/128] float32: n / scale with one scale per 128
+ *        columns, amax / 448 (1 where amax is 0, never below 2^-149), as ep_dispatch and
+ *        ep_permute take rows (H % 128 == 0);
  *   mean, rstd [T] float32, for ep_layer_norm_backward;
  * each of which may be NULL, but not y and y_q both. n is computed from s before s is rounded.
  *   x, residual: [T, H] float32 (EPD_F32) or bfloat16 (EPD_BF16); weight, bias: [H]
@@ -633,7 +633,7 @@ EPD_API epd_status_t ep_layer_norm_backward(const void *dy, const void *x, epd_d
  * (i, i + R/2), or (2i, 2i + 1) with `interleaved` -- and pair i of token t becomes
  *   (a, b) -> rotary_scale * (a cos p - b sin p, a sin p + b cos p),
  *   p = 2 pi * positions[t] * steps[i] / 2^64,
- * in fp32 and rounded once; the other elements are copied. steps[i] is the fraction of a turn
+ * in fp32 (sine and cosine within 2^-20) and rounded once; the other elements are copied. steps[i] is the fraction of a turn
  * that one position adds to pair i, in units of 2^-64: round(f_i / (2 pi) * 2^64) mod 2^64 for
  * an angular frequency f_i. The product is taken modulo 2^64, a whole turn, so that the angle is
  * as good at position 2^31 - 1 as at 1: within 2^-24 of half a turn. With `inverse` the rotation is
@@ -687,7 +687,8 @@ typedef struct {
  * ep_rotary does. Token t is position positions[t] of sequence token_seq[t] (of sequence t where
  * token_seq is NULL): its keys and values are written to that position's row, its rotated
  * queries to q_out. Prompts and single tokens are the same call. An e4m3 cache takes
- * scale = amax / 448 of the head's fp32 values (1 if amax = 0) and e4m3(value / scale), nearest even.
+ * scale = amax / 448 of the head's fp32 values (1 if amax = 0, never below 2^-149) and
+ * e4m3(value / scale), nearest even of the fp32 quotient.
  * A token of sequence -1 is padding: nothing of it is written. A sequence outside
  * [-1, num_seqs), a position outside the sequence's pages or a page outside [0, num_pages) sets
  * EPD_ERR_CAPACITY, and the token is left out like padding. Two tokens at one position must not
@@ -723,11 +724,14 @@ EPD_API size_t epd_attention_workspace_bytes(int num_seqs, int num_heads, int nu
  * over its live positions t -- [0, lengths[b]), or the last `window` of them where window > 0:
  *   s_t = softmax_scale * q[b, h] . k[t, h / G],
  *   out[b, h] = sum of exp(s_t) v[t, h / G] / sum of exp(s_t),  lse[b, h] = ln sum of exp(s_t)
- * with fp32 sums and one rounding of out; 0 and -inf for a sequence of length 0. What lies in
- * the cache outside the live positions is not used, whatever it is. lengths are device memory,
- * read by the kernel: work is split evenly over the device for any mix of them. The order of the
- * sums depends on the sizes, the lengths and the device, not on how blocks are scheduled: the same
- * call gives the same bits again.
+ * with fp32 sums and one rounding of out; 0 and -inf for a sequence of length 0, NaN where a score is
+ * NaN. What lies in the cache outside the live positions is not used, whatever it is.
+ * On the way a bf16 cache's weights exp(s_t) are held to 2^-15 of their size and 2^-100 of the
+ * largest; an e4m3 cache's to 2^-11 of their size (an eighth of out's rounding) and 2^-26 of the
+ * largest, with values' scales up to 2^64 apart, and its queries to 2^-31 of a head's largest element.
+ * lengths are device memory, read by the kernel: work is split evenly over the device for any mix
+ * of them. The order of the sums depends on the sizes, the lengths and the device, not on how blocks
+ * are scheduled: the same call gives the same bits again.
  * A length outside [0, max_pages * page_size] sets EPD_ERR_INVALID_ARG (below) or
  * EPD_ERR_CAPACITY (above) and counts as the nearer end; a page outside [0, num_pages) sets
  * EPD_ERR_CAPACITY and its positions are left out.

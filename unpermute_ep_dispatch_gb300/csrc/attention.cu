@@ -8,7 +8,7 @@
 // Split: a block's warps form teams, one for each of up to eight kv heads, so that a block reads
 // whole rows of a [page, row, head, dim] cache: of rows of one head alone, 128 bytes out of every KB
 // are served at two thirds of the memory's rate (128 sequences of 0 to 8191 tokens in e4m3, 64 heads
-// over 8 of 128: 248 us alone, 199 in teams; their 1.1 GB take 166) and 256 out of every two at 0.95
+// over 8 of 128: 248 us alone, 199 in teams, 205 with the check of the values' scales; their 1.1 GB take 166) and 256 out of every two at 0.95
 // (bf16, 32 heads over 8: 345 and 329 us; 2.1 GB take 322). The (sequence, group of heads)
 // segments of the batch, each as many tiles of a team's tokens as its length needs, form one line of
 // tiles, and every block takes an equal run of it, whatever the lengths are (they are read on the
@@ -17,18 +17,19 @@
 // head's in the blocks' order. Where the batch has few segments (a long context alone) the teams take
 // fewer heads with more warps each, so that the joins have fewer parts and more blocks for them: one
 // sequence of 1000 tokens takes 8.5 us (0.6 for its 4 MB: two trips to memory for lengths and pages, one
-// for the tile, the counter's and the join's), two of 131072 to 200001 in e4m3, 64 heads over 4, 81.5
+// for the tile, the counter's and the join's), two of 131072 to 200001 in e4m3, 64 heads over 4, 84.4
 // (350 MB take 52; 8 go into start and joins, and the rest is the chain of a tile's instructions, the
-// widening of every value before its product among them, with two warps on a scheduler: 36 % of the issue
-// slots are used). Teams there make it 93 to 122: their joins have few warps and many parts.
+// widening of every value before its product among them, with two warps on a scheduler: 37 % of the issue
+// slots are used). Teams there made 81.5 into 93 to 122: their joins have few warps and many parts.
 //
 // A warp has its own tokens of each tile, its own two stages in shared memory, filled by its own
 // asynchronous copies one tile ahead (past the ends of segments; page numbers are looked up one tile
 // before), and its own statistics; warps meet at a segment's end only, and only a team's. Scores
 // and outputs are products on the warp-level matrix instructions with the tokens (of scores) and the
 // columns (of outputs) as their 16 rows and 8 query heads as their columns, so that a group of 8
-// heads fills them; with so few heads the 128-row tiles of tcgen05 would be nearly empty, and these
-// take a fraction of the time that the bytes take.
+// heads fills them. A bf16 cache's take a fraction of the time that its bytes take (12 % of the tensor pipe),
+// and tcgen05's could not make it shorter; of an e4m3 cache with 16 heads, where they and the widening do
+// take longer than the bytes, tcgen05 with 128 tokens as its rows and e4m3 operands has not been tried.
 //
 // Precision: products of bf16 are exact, sums in 32 bits. The weights of a bf16 cache's values are split
 // into two bf16 (15 bits at least), so that the output's own rounding is the only one that matters. An

@@ -12,7 +12,7 @@
 // between the sums and the output. Each thread copies its own chunks of the rows to come into its own
 // slots of shared memory (cp.async, two or four rows ahead): no barrier and no wait but the thread's
 // own, and one block a multiprocessor keeps 40 KB or more on the way. 8192 x 7168 bf16 rows with a
-// residual in and out take 72.4 us into bf16 (470 MB: 70 at a copy's rate), 69 into e4m3 (62) and 81.5 into
+// residual in and out take 72.4 us into bf16 (470 MB: 70 at a copy's rate), 73 into e4m3 (62) and 81.5 into
 // both (79), 4097 x 4096 fp32 rows 16.8 (15); the gradient of 8192 x 7168 bf16 rows, joined, 82 (470 MB: 70),
 // of 4096 x 7168 fp32 65 (62).
 //
@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(kNormThreads, NV * Chunk<T>::C <= 8 ? 2 : 1) n
             // 128 columns are G neighbouring lanes, all of them with a chunk or none. The largest of a thread's
             // chunks take their exchanges together: after each of the first ones a lane has half as many, and
             // in the end the one of chunk `mine`, whose scale it finds for all of them (8192 x 4096 fp32 into
-            // e4m3 41 us; 55 with an exchange and two divisions for every chunk).
+            // e4m3 41 us; 55 with an exchange and two divisions for every chunk). The quotients' remainders, which
+            // make them the rounded ones, take 2 to 4 us of that size's and the next's (42.3; 8192 x 8192 bf16 68.5).
             constexpr int G = 128 / C;
             const int lane = tid & 31;
             float top[NV];
@@ -582,7 +583,7 @@ extern "C" epd_status_t ep_layer_norm(const void *x, epd_dtype_t dtype, const vo
     a.mean = mean;
     a.rstd = rstd;
     NormShape s = norm_shape(H);
-    // Eight columns leave room in the registers for twice the blocks (16384 x 512 bf16 into e4m3 11.1 us, 13.6
+    // Eight columns leave room in the registers for twice the blocks (16384 x 512 bf16 into e4m3 11.7 us, 2.4 more
     // with as many as of 16 columns, which spill in half the registers: 8192 x 7168 72 -> 92).
     if (s.columns == 8) s.per_sm *= 2;
     const int most = sm_count() * s.per_sm, grid = T < most ? T : most;

@@ -274,11 +274,12 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(RotaryArgs a) {
 }
 
 // NP: chunks of a head that one lane holds (V == 1 only). Bound by HBM, and by how many warps there are to
-// wait for it: 16384 tokens of 64 + 2 x 8 heads of 128 take 98 us into an e4m3 cache, half a head rotated
-// interleaved (0.64 GB: 96), and 100 into a bf16 one (100). With whole batches of 8 passes and 90 to 130
-// registers a thread, five blocks or fewer a multiprocessor, they took 116 and 108, and with halves of a
-// whole head rotated (V == 8) 140, where these limits give 99. An e4m3 cache of 16 + 2 x 16 heads takes
-// 68 (51): the conversion's instructions.
+// wait for it: 16384 tokens of 64 + 2 x 8 heads of 128 take 99.3 us into an e4m3 cache, half a head rotated
+// interleaved (0.64 GB: 96), 99.9 with halves of the whole head, and 100 into a bf16 one (100). With whole
+// batches of 8 passes and 90 to 130 registers a thread, five blocks or fewer a multiprocessor, they took 116, 140
+// and 108. At these limits the halves' e4m3 instances spill 64 bytes a thread. An e4m3 cache of 16 + 2 x 16 heads
+// takes 70.5 (halves), 77 (interleaved; 51) and 79 of 96 elements, 24 of them rotated (38): the conversion's
+// instructions, 3 to 5 % of the time the remainders that make its quotients the rounded ones.
 template <int V, bool INTER, bool FP8, int NP>
 __global__ void __launch_bounds__(kThreads, V == 4 ? 9 : V == 8 ? 6 : 1) append_kernel(AppendArgs a) {
     const int lane = threadIdx.x & 31;
