@@ -525,3 +525,68 @@ def test_windows_of_any_size():
     for window in (-1, -2**31, -2**32, -2**32 + 5):
         with pytest.raises(epd.EpdError):
             f(window)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("KH,G,D", [(8, 4, 128), (8, 12, 64), (4, 8, 256), (4, 16, 256)])
+def test_long_runs_of_one_warp(KH, G, D, fp8):
+    """A sequence for every block, of so many tokens that the matrix instructions' sums, which are cut off and
+    not rounded, would lose more than the output's own rounding: its pages are a few, over and over."""
+    g = gen(50 + D)
+    page, few, times, B = 64, 48, 500, 152
+    k, v, ks, vs = paged(few, page, KH, D, fp8, DEV, g)
+    if fp8:
+        x = (values(v, vs) * 0.25 + 1).float()
+        vs = x.abs().amax(-1) / 448
+        v = (x / vs.unsqueeze(-1)).clamp(-448, 448).to(torch.float8_e4m3fn)
+    else:
+        v = (v.float() * 0.25 + 1).bfloat16()
+    q = torch.randn(1, KH * G, D, generator=g, device=DEV).bfloat16()
+    once = torch.randperm(few, generator=g, device=DEV).int().view(1, few)
+    want, lse = attend(q, values(k, ks), values(v, vs), once, torch.tensor([few * page]))
+    size, _ = attend(q, values(k, ks), values(v, vs).abs(), once, torch.tensor([few * page]))
+    table, n = once.repeat(1, times).expand(B, few * times), few * page * times
+    lens = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    st = epd.new_status(DEV)
+    f = lambda: epd.ep_decode_attention(q.expand(B, KH * G, D), k, v, table, lens, epd.new_attention_workspace(B, KH * G, KH, D, DEV),  # noqa: E731
+                                        st, k_scale=ks, v_scale=vs, with_lse=True)
+    out, got = f()
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -14 + (2.0 ** -11 if fp8 else 0)) * size
+    assert int(st) == 0 and bool(((out.double() - want).abs() <= tol).all()), float(((out.double() - want) / size).mean())
+    assert bool(((got.double() - lse - math.log(times)).abs() <= 2.0 ** -14 + 2.0 ** -23 * lse.abs()).all())
+    again = f()
+    assert torch.equal(out, again[0]) and torch.equal(got, again[1])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_long_runs_whose_maxima_and_scales_move(fp8):
+    """What a run has put aside is brought to the maxima and scales that came after it: scores that rise and
+    fall by hundreds, and values' scales by 2^20, along the sequence."""
+    g = gen(60)
+    KH, G, D, page, pages, B = 8, 2, 64, 64, 1200, 152
+    k, v, ks, vs = paged(pages, page, KH, D, fp8, DEV, g)
+    q = torch.randn(1, KH * G, D, generator=g, device=DEV).bfloat16()
+    n = pages * page - 17
+    at = torch.arange(pages * page, device=DEV).view(pages, page) / (pages * page)
+    rise = (300 * torch.sin(9 * at) * at).unsqueeze(-1)  # of the scores of every kv head's first query
+    unit = q[0].float().view(KH, G, D)[:, 0]
+    along = unit / unit.square().sum(-1, keepdim=True)
+    if fp8:
+        vs *= torch.exp2(torch.round(20 * torch.cos(23 * at))).unsqueeze(-1)
+        x = along * rise.unsqueeze(-1) + values(k, ks).float() * 0.1
+        ks = x.abs().amax(-1) / 448
+        k = (x / ks.unsqueeze(-1)).clamp(-448, 448).to(torch.float8_e4m3fn)
+    else:
+        k = (along * rise.unsqueeze(-1) + k.float() * 0.1).bfloat16()
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).view(1, pages)
+    want, lse = attend(q, values(k, ks), values(v, vs), table, torch.tensor([n]), 1.0)
+    size, _ = attend(q, values(k, ks), values(v, vs).abs(), table, torch.tensor([n]), 1.0)
+    lens = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    st = epd.new_status(DEV)
+    out, got = epd.ep_decode_attention(q.expand(B, KH * G, D), k, v, table.expand(B, pages), lens,
+                                       epd.new_attention_workspace(B, KH * G, KH, D, DEV), st, k_scale=ks, v_scale=vs,
+                                       softmax_scale=1.0, with_lse=True)
+    # scores up to 2^8.3 and products up to some 2^10: 2^-24 of that for each of D / 16 + 4 additions, 2^-11
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -11 + (2.0 ** -11 if fp8 else 0)) * size
+    assert int(st) == 0 and bool(((out.double() - want).abs() <= tol).all()), float(((out.double() - want).abs() / size).max())
+    assert bool(((got.double() - lse).abs() <= 2.0 ** -11 + 2.0 ** -23 * lse.abs()).all())

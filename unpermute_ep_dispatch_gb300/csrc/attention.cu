@@ -52,6 +52,11 @@ constexpr int kMaxTeams = 8;
 // sequences of 10 to 300 tokens: 44 us, 76 with all of them cut where the shares end; with 8 tiles one
 // sequence of 1000 tokens is left to 8 blocks, and takes 14.8 us instead of 8.5).
 constexpr int kUncut = 4;
+// Tokens of a segment after which a warp puts its sums aside and starts new ones. The matrix instructions cut
+// their sums off where an addition would round, which loses in one direction: 1e-4 of the output over 9000 tokens
+// of a bf16 cache in one warp, 3.5e-4 over 30000 and 3.3e-3 (the output's own rounding) over 300000, half of
+// that of an e4m3 cache. With runs of 2048 it is 2e-5 whatever the length is.
+constexpr int kRunTokens = 2048;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLn2 = 0.6931471805599453f;
 // A maximum is moved (and everything summed so far scaled down) only when a score passes it by more
@@ -88,9 +93,12 @@ struct AttnArgs {
     uint8_t *out;  // bf16 [B, QH, D]
     float *lse;
     uint32_t *counters;
-    float *parts;
+    float *parts, *aside;
     int32_t *status;
 };
+
+// Floats of a warp's sums put aside: of outputs, of weights with their maxima, and the values' reference.
+constexpr int aside_floats(int DP, int NH) { return (DP / 16 * NH * 4 + NH * 4 + 4) * 32; }
 
 template <int DP, bool FP8, int NH>
 struct Shape {
@@ -113,6 +121,7 @@ struct Shape {
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kSmem = kWarps * (kStages * kStage + kQuery) + kJoin;
     static constexpr int kPart = kHeads * (DP + 2);  // floats: the heads' sums, maxima and sums of weights
+    static constexpr int kAside = aside_floats(DP, NH);
     static_assert(kSmem <= 226 * 1024 - 2048, "the ring and the join share what a block may have");
 };
 
@@ -605,217 +614,259 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
             v_ref = kLeastRef;
             if (FP8 && lane == 0) s_top[warp] = 0.0f;
         }
-        for (const int until = step + min(left, steps - step); step < until; ++step) {
-            copy_wait<S::kStages - 2>();
-            __syncwarp();
-            if (step + S::kStages - 1 < steps) {
-                load(stage == 0 ? S::kStages - 1 : stage - 1);
-                if (step + S::kStages < steps) go_on();
-            }
-            copy_commit();
+        // the segment's tiles, in runs after which the sums are put aside
+        const int until = step + min(left, steps - step);
+        for (bool aside = false;; aside = true) {
+            for (const int stop = min(until, step + kRunTokens / CH); step < stop; ++step) {
+                copy_wait<S::kStages - 2>();
+                __syncwarp();
+                if (step + S::kStages - 1 < steps) {
+                    load(stage == 0 ? S::kStages - 1 : stage - 1);
+                    if (step + S::kStages < steps) go_on();
+                }
+                copy_commit();
 
-            const uint32_t at = ring + stage * S::kStage;
-            uint32_t mask;
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(mask) : "r"(at + S::kStage - 16) : "memory");
-            // (an e4m3 tile's values' scales from `done` up have had their turn)
-            float done = NAN;
-            for (bool turn = mask != 0; turn;) {
-                turn = false;
-                // s[t][n][i]: token 16 t + g + 8 (i / 2), head 8 n + 2 c + i % 2
-                float s[MT][NH][4] = {};
-                const int row = lane & 15, right = lane >> 4;
-                auto query = [&](int k, int n) {
-                    return S::kQueryInSmem ? s_query[(k * NH + n) * 32 + lane] : make_uint2(q[k][n][0], q[k][n][1]);
-                };
+                const uint32_t at = ring + stage * S::kStage;
+                uint32_t mask;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(mask) : "r"(at + S::kStage - 16) : "memory");
+                // (an e4m3 tile's values' scales from `done` up have had their turn)
+                float done = NAN;
+                for (bool turn = mask != 0; turn;) {
+                    turn = false;
+                    // s[t][n][i]: token 16 t + g + 8 (i / 2), head 8 n + 2 c + i % 2
+                    float s[MT][NH][4] = {};
+                    const int row = lane & 15, right = lane >> 4;
+                    auto query = [&](int k, int n) {
+                        return S::kQueryInSmem ? s_query[(k * NH + n) * 32 + lane] : make_uint2(q[k][n][0], q[k][n][1]);
+                    };
 #pragma unroll
-                for (int k = 0; k < UNITS / 2; ++k)
+                    for (int k = 0; k < UNITS / 2; ++k)
 #pragma unroll
-                    for (int t = 0; t < MT; ++t) {
-                        uint32_t r[4];
-                        ldsm4(r, at + (t * 16 + row) * S::kRow + swizzle<UNITS>(row, 2 * k + right) * 16);
-                        if (FP8) {
+                        for (int t = 0; t < MT; ++t) {
+                            uint32_t r[4];
+                            ldsm4(r, at + (t * 16 + row) * S::kRow + swizzle<UNITS>(row, 2 * k + right) * 16);
+                            if (FP8) {
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                uint32_t f[4];
-                                widen4(r[2 * h], f[0], f[2]);
-                                widen4(r[2 * h + 1], f[1], f[3]);
+                                for (int h = 0; h < 2; ++h) {
+                                    uint32_t f[4];
+                                    widen4(r[2 * h], f[0], f[2]);
+                                    widen4(r[2 * h + 1], f[1], f[3]);
+#pragma unroll
+                                    for (int n = 0; n < NH; ++n) {
+                                        const uint2 b = query(2 * k + h, n);
+                                        mma<true>(s[t][n], f, b.x, b.y);
+                                    }
+                                }
+                            } else {
 #pragma unroll
                                 for (int n = 0; n < NH; ++n) {
-                                    const uint2 b = query(2 * k + h, n);
-                                    mma<true>(s[t][n], f, b.x, b.y);
+                                    const uint2 b = query(k, n);
+                                    mma<false>(s[t][n], r, b.x, b.y);
                                 }
                             }
-                        } else {
-#pragma unroll
-                            for (int n = 0; n < NH; ++n) {
-                                const uint2 b = query(k, n);
-                                mma<false>(s[t][n], r, b.x, b.y);
-                            }
                         }
-                    }
-                const float *const sc = scales + stage * (S::kStage / 4);
+                    const float *const sc = scales + stage * (S::kStage / 4);
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    const float f[2] = {FP8 ? sc[16 * t + g] : a.scale_log2, FP8 ? sc[16 * t + g + 8] : 0.0f};
-#pragma unroll
-                    for (int n = 0; n < NH; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) s[t][n][i] *= FP8 ? q_scale[n][i & 1] * f[i >> 1] : f[0];
-                }
-                if (mask != (CH == 32 ? kAll : 0xffffu)) {
-#pragma unroll
-                    for (int t = 0; t < MT; ++t)
+                    for (int t = 0; t < MT; ++t) {
+                        const float f[2] = {FP8 ? sc[16 * t + g] : a.scale_log2, FP8 ? sc[16 * t + g + 8] : 0.0f};
 #pragma unroll
                         for (int n = 0; n < NH; ++n)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (!((mask >> (16 * t + g + 8 * (i >> 1))) & 1)) s[t][n][i] = -INFINITY;
-                }
-                float top[NH][2];
-                bool more = false;
-#pragma unroll
-                for (int n = 0; n < NH; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        top[n][i] = fmaxf(s[0][n][i], s[0][n][i + 2]);
-#pragma unroll
-                        for (int t = 1; t < MT; ++t) top[n][i] = fmaxf(top[n][i], fmaxf(s[t][n][i], s[t][n][i + 2]));
-                        more |= top[n][i] > m[n][i] + (FP8 ? kSlackFp8 : kSlack);
+                            for (int i = 0; i < 4; ++i) s[t][n][i] *= FP8 ? q_scale[n][i & 1] * f[i >> 1] : f[0];
                     }
-                if (__any_sync(kAll, more)) {
+                    if (mask != (CH == 32 ? kAll : 0xffffu)) {
+#pragma unroll
+                        for (int t = 0; t < MT; ++t)
+#pragma unroll
+                            for (int n = 0; n < NH; ++n)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (!((mask >> (16 * t + g + 8 * (i >> 1))) & 1)) s[t][n][i] = -INFINITY;
+                    }
+                    float top[NH][2];
+                    bool more = false;
 #pragma unroll
                     for (int n = 0; n < NH; ++n)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            float now = top[n][i];
+                            top[n][i] = fmaxf(s[0][n][i], s[0][n][i + 2]);
 #pragma unroll
-                            for (int d = 4; d < 32; d <<= 1) now = fmaxf(now, __shfl_xor_sync(kAll, now, d));
-                            now = fmaxf(now, m[n][i]);
-                            const float f = m[n][i] == -INFINITY ? 0.0f : fast_exp2(m[n][i] - now);
-                            m[n][i] = now;
-                            l[n][i] *= f;
+                            for (int t = 1; t < MT; ++t) top[n][i] = fmaxf(top[n][i], fmaxf(s[t][n][i], s[t][n][i + 2]));
+                            more |= top[n][i] > m[n][i] + (FP8 ? kSlackFp8 : kSlack);
+                        }
+                    if (__any_sync(kAll, more)) {
 #pragma unroll
-                            for (int k = 0; k < KT; ++k) {
-                                o[k][n][i] *= f;
-                                o[k][n][i + 2] *= f;
+                        for (int n = 0; n < NH; ++n)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                float now = top[n][i];
+#pragma unroll
+                                for (int d = 4; d < 32; d <<= 1) now = fmaxf(now, __shfl_xor_sync(kAll, now, d));
+                                now = fmaxf(now, m[n][i]);
+                                const float f = m[n][i] == -INFINITY ? 0.0f : fast_exp2(m[n][i] - now);
+                                m[n][i] = now;
+                                l[n][i] *= f;
+#pragma unroll
+                                for (int k = 0; k < KT; ++k) {
+                                    o[k][n][i] *= f;
+                                    o[k][n][i + 2] *= f;
+                                }
                             }
-                        }
-                }
-                float vs[MT][2];
-                if (FP8) {
-                    float most = 0.0f, least = INFINITY;
-#pragma unroll
-                    for (int t = 0; t < MT; ++t)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            vs[t][i] = sc[CH + 16 * t + g + 8 * i];
-                            const float size = fabsf(vs[t][i]);
-                            most = fmaxf(most, size);
-                            least = fminf(least, size > 0.0f ? size : INFINITY);
-                        }
-                    const bool out = most > kValueSlack * kWeightUp * v_ref || least < kValueRange * kWeightUp * v_ref;
-                    if (__any_sync(kAll, out) || !__any_sync(kAll, most >= kValueNear * kWeightUp * v_ref)) {
-                        most = 0.0f;
+                    }
+                    float vs[MT][2];
+                    if (FP8) {
+                        float most = 0.0f, least = INFINITY;
 #pragma unroll
                         for (int t = 0; t < MT; ++t)
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
-                                if (fabsf(vs[t][i]) >= done) vs[t][i] = 0.0f;
-                                most = fmaxf(most, fabsf(vs[t][i]));
+                                vs[t][i] = sc[CH + 16 * t + g + 8 * i];
+                                const float size = fabsf(vs[t][i]);
+                                most = fmaxf(most, size);
+                                least = fminf(least, size > 0.0f ? size : INFINITY);
                             }
+                        const bool out = most > kValueSlack * kWeightUp * v_ref || least < kValueRange * kWeightUp * v_ref;
+                        if (__any_sync(kAll, out) || !__any_sync(kAll, most >= kValueNear * kWeightUp * v_ref)) {
+                            most = 0.0f;
 #pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, d));
-                        if (most > 0.0f) {
-                            most = __uint_as_float(__float_as_uint(most) & 0x7f800000u) / kWeightUp;
-                            const float now = fmaxf(fmaxf(most, kLeastRef), s_top[warp] * kValueFall), f = v_ref / now;
-                            v_ref = now;
-                            __syncwarp();
-                            if (lane == 0) s_top[warp] = fmaxf(s_top[warp], now);
-                            __syncwarp();
+                            for (int t = 0; t < MT; ++t)
 #pragma unroll
-                            for (int k = 0; k < KT; ++k)
+                                for (int i = 0; i < 2; ++i) {
+                                    if (fabsf(vs[t][i]) >= done) vs[t][i] = 0.0f;
+                                    most = fmaxf(most, fabsf(vs[t][i]));
+                                }
 #pragma unroll
-                                for (int i = 0; i < 4 * NH; ++i) o[k][i >> 2][i & 3] *= f;
-                            if (now == most && now < INFINITY) {
-                                const float least = kValueRange * kWeightUp * now;
-                                bool later = false;
+                            for (int d = 4; d < 32; d <<= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, d));
+                            if (most > 0.0f) {
+                                most = __uint_as_float(__float_as_uint(most) & 0x7f800000u) / kWeightUp;
+                                const float now = fmaxf(fmaxf(most, kLeastRef), s_top[warp] * kValueFall), f = v_ref / now;
+                                v_ref = now;
+                                __syncwarp();
+                                if (lane == 0) s_top[warp] = fmaxf(s_top[warp], now);
+                                __syncwarp();
 #pragma unroll
-                                for (int t = 0; t < MT; ++t)
+                                for (int k = 0; k < KT; ++k)
 #pragma unroll
-                                    for (int i = 0; i < 2; ++i)
-                                        if (fabsf(vs[t][i]) < least && vs[t][i] != 0.0f) {
-                                            vs[t][i] = 0.0f;
-                                            later = true;
-                                        }
-                                turn = __any_sync(kAll, later);
+                                    for (int i = 0; i < 4 * NH; ++i) o[k][i >> 2][i & 3] *= f;
+                                if (now == most && now < INFINITY) {
+                                    const float least = kValueRange * kWeightUp * now;
+                                    bool later = false;
+#pragma unroll
+                                    for (int t = 0; t < MT; ++t)
+#pragma unroll
+                                        for (int i = 0; i < 2; ++i)
+                                            if (fabsf(vs[t][i]) < least && vs[t][i] != 0.0f) {
+                                                vs[t][i] = 0.0f;
+                                                later = true;
+                                            }
+                                    turn = __any_sync(kAll, later);
+                                }
+                            }
+                        }
+                        const float v_inv = fast_rcp(v_ref);  // exact: a power of two
+#pragma unroll
+                        for (int t = 0; t < MT; ++t)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) vs[t][i] *= v_inv;
+                    }
+                    const float counts = done == done ? 0.0f : 1.0f;  // a token's weight counts once
+                    // the weights, turned from (token, head) to (head, token) fragments
+                    uint32_t p[MT][NH][2], p_lo[MT][NH][2];
+#pragma unroll
+                    for (int n = 0; n < NH; ++n) {
+                        const float base[2] = {m[n][0] == -INFINITY ? 0.0f : m[n][0], m[n][1] == -INFINITY ? 0.0f : m[n][1]};
+#pragma unroll
+                        for (int t = 0; t < MT; ++t)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const float x = fast_exp2(s[t][n][2 * i] - base[0]), y = fast_exp2(s[t][n][2 * i + 1] - base[1]);
+                                l[n][0] = FP8 ? fmaf(x, counts, l[n][0]) : l[n][0] + x;
+                                l[n][1] = FP8 ? fmaf(y, counts, l[n][1]) : l[n][1] + y;
+                                if (FP8) {
+                                    p[t][n][i] = transpose8(pack2_f16(x * vs[t][i], y * vs[t][i]));
+                                } else {
+                                    // the first part is cut off, not rounded, and the second at least 2^-100:
+                                    // neither turns an infinite value's product into NaN
+                                    const uint32_t hi = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+                                    p[t][n][i] = transpose8(hi);
+                                    p_lo[t][n][i] = transpose8(pack2_bf16(fmaxf(x - lo_bf16(hi), 0x1p-100f), fmaxf(y - hi_bf16(hi), 0x1p-100f)));
+                                }
+                            }
+                    }
+                    const uint32_t av = at + CH * S::kRow;
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        if (FP8) {
+                            // a 16-byte unit is 16 columns: its even ones are the first 8 rows, its odd ones the others
+#pragma unroll
+                            for (int k = 0; k < UNITS / 2; ++k) {
+                                uint32_t r[4];
+                                ldsm4t(r, av + (t * 16 + row) * S::kRow + swizzle<UNITS>(row, 2 * k + right) * 16);
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    uint32_t f[4];
+                                    widen4(__byte_perm(r[2 * h], 0, 0x3120), f[0], f[1]);
+                                    widen4(__byte_perm(r[2 * h + 1], 0, 0x3120), f[2], f[3]);
+#pragma unroll
+                                    for (int n = 0; n < NH; ++n) mma<true>(o[2 * k + h][n], f, p[t][n][0], p[t][n][1]);
+                                }
+                            }
+                        } else {
+                            const int vrow = (lane & 7) + right * 8;
+#pragma unroll
+                            for (int k = 0; k < KT; ++k) {
+                                uint32_t r[4];
+                                ldsm4t(r, av + (t * 16 + vrow) * S::kRow + swizzle<UNITS>(vrow, 2 * k + ((lane >> 3) & 1)) * 16);
+#pragma unroll
+                                for (int n = 0; n < NH; ++n) {
+                                    mma<false>(o[k][n], r, p[t][n][0], p[t][n][1]);
+                                    mma<false>(o[k][n], r, p_lo[t][n][0], p_lo[t][n][1]);
+                                }
                             }
                         }
                     }
-                    const float v_inv = fast_rcp(v_ref);  // exact: a power of two
-#pragma unroll
-                    for (int t = 0; t < MT; ++t)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) vs[t][i] *= v_inv;
+                    if (FP8 && turn) done = kValueRange * kWeightUp * v_ref;
                 }
-                const float counts = done == done ? 0.0f : 1.0f;  // a token's weight counts once
-                // the weights, turned from (token, head) to (head, token) fragments
-                uint32_t p[MT][NH][2], p_lo[MT][NH][2];
+                if (++stage == S::kStages) stage = 0;
+            }
+            if (!aside && step == until) break;
+            // ---- the sums so far and those put aside before, brought to the present maxima and reference
+            float4 *const kept = reinterpret_cast<float4 *>(a.aside + (int64_t)(blockIdx.x * W + warp) * S::kAside) + lane;
+            if (aside) {
+                const float fall = FP8 ? kept[(KT + 1) * NH * 32].x / v_ref : 1.0f;
+                float by[NH][2];
 #pragma unroll
                 for (int n = 0; n < NH; ++n) {
-                    const float base[2] = {m[n][0] == -INFINITY ? 0.0f : m[n][0], m[n][1] == -INFINITY ? 0.0f : m[n][1]};
-#pragma unroll
-                    for (int t = 0; t < MT; ++t)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float x = fast_exp2(s[t][n][2 * i] - base[0]), y = fast_exp2(s[t][n][2 * i + 1] - base[1]);
-                            l[n][0] = FP8 ? fmaf(x, counts, l[n][0]) : l[n][0] + x;
-                            l[n][1] = FP8 ? fmaf(y, counts, l[n][1]) : l[n][1] + y;
-                            if (FP8) {
-                                p[t][n][i] = transpose8(pack2_f16(x * vs[t][i], y * vs[t][i]));
-                            } else {
-                                // the first part is cut off, not rounded, and the second at least 2^-100:
-                                // neither turns an infinite value's product into NaN
-                                const uint32_t hi = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-                                p[t][n][i] = transpose8(hi);
-                                p_lo[t][n][i] = transpose8(pack2_bf16(fmaxf(x - lo_bf16(hi), 0x1p-100f), fmaxf(y - hi_bf16(hi), 0x1p-100f)));
-                            }
-                        }
+                    const float4 x = kept[(KT * NH + n) * 32];
+                    by[n][0] = x.x == -INFINITY ? 0.0f : fast_exp2(x.x - m[n][0]);
+                    by[n][1] = x.y == -INFINITY ? 0.0f : fast_exp2(x.y - m[n][1]);
+                    l[n][0] = fmaf(x.z, by[n][0], l[n][0]);
+                    l[n][1] = fmaf(x.w, by[n][1], l[n][1]);
+                    if (FP8) by[n][0] *= fall, by[n][1] *= fall;
                 }
-                const uint32_t av = at + CH * S::kRow;
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    if (FP8) {
-                        // a 16-byte unit is 16 columns: its even ones are the first 8 rows, its odd ones the others
+                for (int k = 0; k < KT; ++k)
 #pragma unroll
-                        for (int k = 0; k < UNITS / 2; ++k) {
-                            uint32_t r[4];
-                            ldsm4t(r, av + (t * 16 + row) * S::kRow + swizzle<UNITS>(row, 2 * k + right) * 16);
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                uint32_t f[4];
-                                widen4(__byte_perm(r[2 * h], 0, 0x3120), f[0], f[1]);
-                                widen4(__byte_perm(r[2 * h + 1], 0, 0x3120), f[2], f[3]);
-#pragma unroll
-                                for (int n = 0; n < NH; ++n) mma<true>(o[2 * k + h][n], f, p[t][n][0], p[t][n][1]);
-                            }
-                        }
-                    } else {
-                        const int vrow = (lane & 7) + right * 8;
-#pragma unroll
-                        for (int k = 0; k < KT; ++k) {
-                            uint32_t r[4];
-                            ldsm4t(r, av + (t * 16 + vrow) * S::kRow + swizzle<UNITS>(vrow, 2 * k + ((lane >> 3) & 1)) * 16);
-#pragma unroll
-                            for (int n = 0; n < NH; ++n) {
-                                mma<false>(o[k][n], r, p[t][n][0], p[t][n][1]);
-                                mma<false>(o[k][n], r, p_lo[t][n][0], p_lo[t][n][1]);
-                            }
-                        }
+                    for (int n = 0; n < NH; ++n) {
+                        const float4 x = kept[(k * NH + n) * 32];
+                        o[k][n][0] = fmaf(x.x, by[n][0], o[k][n][0]);
+                        o[k][n][1] = fmaf(x.y, by[n][1], o[k][n][1]);
+                        o[k][n][2] = fmaf(x.z, by[n][0], o[k][n][2]);
+                        o[k][n][3] = fmaf(x.w, by[n][1], o[k][n][3]);
                     }
-                }
-                if (FP8 && turn) done = kValueRange * kWeightUp * v_ref;
             }
-            if (++stage == S::kStages) stage = 0;
+            if (step == until) break;
+            if (FP8) kept[(KT + 1) * NH * 32].x = v_ref;
+#pragma unroll
+            for (int n = 0; n < NH; ++n) {
+                kept[(KT * NH + n) * 32] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
+                l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < KT; ++k) {
+                    kept[(k * NH + n) * 32] = make_float4(o[k][n][0], o[k][n][1], o[k][n][2], o[k][n][3]);
+                    o[k][n][0] = o[k][n][1] = o[k][n][2] = o[k][n][3] = 0.0f;
+                }
+            }
         }
 
         {
@@ -954,7 +1005,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, NH>::kThreads, 1) attention_ker
 inline int padded_dim(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
 // The workspace: a counter for every block and team, zero between calls and in the same place whatever
-// the sizes are, and two parts for every block and team.
+// the sizes are, two parts for every block and team, and what every warp puts aside.
 constexpr size_t kCounterBytes = (kMaxBlocks * kMaxTeams * 4 + kAlign - 1) / kAlign * kAlign;
 
 // The most teams that may be: a power of two of them divides the kv heads.
@@ -963,6 +1014,9 @@ inline int most_teams(int KH) {
     while (KH % n) n /= 2;
     return n;
 }
+
+// The parts' bytes, a multiple of 16.
+inline size_t parts_bytes(int group, int KH, int DP) { return (size_t)2 * kMaxBlocks * most_teams(KH) * (group <= 8 ? 8 : kMaxHeads) * (DP + 2) * 4; }
 
 template <int DP, bool FP8, int NH>
 epd_status_t launch_heads(AttnArgs &a, cudaStream_t st) {
@@ -1002,7 +1056,8 @@ extern "C" size_t epd_attention_workspace_bytes(int num_seqs, int num_heads, int
         head_dim % 8 || head_dim > kMaxHeadDim)
         return 0;
     const int group = num_heads / num_kv_heads;
-    return kCounterBytes + (size_t)2 * kMaxBlocks * most_teams(num_kv_heads) * (group <= 8 ? 8 : kMaxHeads) * (padded_dim(head_dim) + 2) * 4;
+    return kCounterBytes + parts_bytes(group, num_kv_heads, padded_dim(head_dim)) +
+           (size_t)kMaxBlocks * 8 * aside_floats(padded_dim(head_dim), group <= 8 ? 1 : 2) * 4;
 }
 
 extern "C" epd_status_t ep_decode_attention(const epd_cache_t *cache, const void *q, int64_t q_token_stride,
@@ -1034,10 +1089,11 @@ extern "C" epd_status_t ep_decode_attention(const epd_cache_t *cache, const void
     a.out = static_cast<uint8_t *>(out);
     a.lse = lse;
     a.counters = static_cast<uint32_t *>(workspace);
+    const int DP = padded_dim(D);
     a.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kCounterBytes);
+    a.aside = a.parts + parts_bytes(a.group, KH, DP) / 4;
     a.status = status;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const int DP = padded_dim(D);
     if (cache->dtype == EPD_FP8_E4M3)
         return DP == 64    ? launch_attention<64, true>(a, st)
                : DP == 128 ? launch_attention<128, true>(a, st)
