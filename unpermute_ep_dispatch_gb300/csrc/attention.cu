@@ -17,7 +17,7 @@
 // head's in the blocks' order. Where the batch has few segments (a long context alone) the teams take
 // fewer heads with more warps each, so that the joins have fewer parts and more blocks for them: one
 // sequence of 1000 tokens takes 8.5 us (0.6 for its 4 MB: two trips to memory for lengths and pages, one
-// for the tile, the counter's and the join's), two of 131072 to 200001 in e4m3, 64 heads over 4, 84.4
+// for the tile, the counter's and the join's), two of 131072 to 200001 in e4m3, 64 heads over 4, 82.4
 // (350 MB take 52; 8 go into start and joins, and the rest is the chain of a tile's instructions, the
 // widening of every value before its product among them, with two warps on a scheduler: 37 % of the issue
 // slots are used). Teams there made 81.5 into 93 to 122: their joins have few warps and many parts.
@@ -73,8 +73,8 @@ constexpr float kValueSlack = 4.0f, kWeightUp = 512.0f;
 // scales that are below its range then take another turn over the tile, with a reference of their own: a row of
 // zeros has scale 1, and may lie among values of any size. With one reference that only rose, a single such row
 // among 1000 of scale 2^-27 left 0.6 % of the output wrong, of 2^-37 26 %; now 0.17 % whatever the scales are
-// (the output's own rounding). The check costs 0.5 to 3 % (two of 131072 to 200001 tokens, 64 heads over 4: 81.8 ->
-// 84.6 us); a row of zeros in every 1000 another 1 %, in every 50, where most tiles take two turns, 24 %.
+// (the output's own rounding). The check cost 0.5 to 3 % (two of 131072 to 200001 tokens, 64 heads over 4: 81.8 and
+// 84.6 us with it); a row of zeros in every 1000 another 1 %, in every 50, where most tiles take two turns, 24 %.
 constexpr float kValueRange = 0x1p-8f, kValueNear = 0x1p-3f, kValueFall = 0x1p-64f;
 constexpr float kLeastRef = 0x1p-119f;  // of a reference over kWeightUp: its inverse is finite
 
