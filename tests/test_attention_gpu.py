@@ -590,3 +590,23 @@ def test_long_runs_whose_maxima_and_scales_move(fp8):
     tol = 2.0 ** -8 * want.abs() + (2.0 ** -11 + (2.0 ** -11 if fp8 else 0)) * size
     assert int(st) == 0 and bool(((out.double() - want).abs() <= tol).all()), float(((out.double() - want).abs() / size).max())
     assert bool(((got.double() - lse).abs() <= 2.0 ** -11 + 2.0 ** -23 * lse.abs()).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,KH,G,D", [(3, 1, 4, 128), (2, 2, 16, 64), (5, 1, 9, 256)])
+def test_long_runs_shared_by_blocks(B, KH, G, D, fp8):
+    """Millions of tokens of a sequence, in the runs of many warps of many blocks, all joined."""
+    g = gen(70 + D)
+    page, few, times = 64, 48, 2000
+    k, v, ks, vs = paged(few, page, KH, D, fp8, DEV, g)
+    q = torch.randn(B, KH * G, D, generator=g, device=DEV).bfloat16()
+    once = torch.stack([torch.randperm(few, generator=g, device=DEV) for _ in range(B)]).int()
+    lens = torch.full((B,), few * page, dtype=torch.int32, device=DEV)
+    want, lse = attend(q, values(k, ks), values(v, vs), once, lens)
+    size, _ = attend(q, values(k, ks), values(v, vs).abs(), once, lens)
+    st = epd.new_status(DEV)
+    out, got = epd.ep_decode_attention(q, k, v, once.repeat(1, times), lens * times, epd.new_attention_workspace(B, KH * G, KH, D, DEV),
+                                       st, k_scale=ks, v_scale=vs, with_lse=True)
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -14 + (2.0 ** -11 if fp8 else 0)) * size
+    assert int(st) == 0 and bool(((out.double() - want).abs() <= tol).all())
+    assert bool(((got.double() - lse - math.log(times)).abs() <= 2.0 ** -14 + 2.0 ** -23 * lse.abs()).all())

@@ -75,3 +75,26 @@ def test_outputs_belong_to_the_given_stream(name):
     for a, b in zip(got, want):
         if name not in ("dispatch", "matmul", "unpermute_backward", "dgrad"):  # (rows past the last are no one's)
             assert torch.equal(a.reshape(-1).view(torch.uint8), b.reshape(-1).view(torch.uint8))
+
+
+@pytest.mark.parametrize("name", ["dispatch", "norm", "norm_backward", "append", "attention"])
+def test_given_streams_in_a_graph(name):
+    """A captured call on a stream that the capture forks to, its outputs used on the first one."""
+    op = operators()[name]
+    side = torch.cuda.Stream()
+    op(stream=side)
+    torch.cuda.synchronize()
+    want = [t.clone() for t in tensors(op())]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        out = tensors(op(stream=side))
+        torch.cuda.current_stream().wait_stream(side)
+        got = [t.clone() for t in out]
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        if name != "dispatch":  # (rows past the last are no one's)
+            assert torch.equal(a.reshape(-1).view(torch.uint8), b.reshape(-1).view(torch.uint8))
