@@ -19,7 +19,7 @@
 // sequence of 1000 tokens takes 8.5 us (0.6 for its 4 MB: two trips to memory for lengths and pages, one
 // for the tile, the counter's and the join's), two of 131072 to 200001 in e4m3, 64 heads over 4, 82.4
 // (350 MB take 52; 8 go into start and joins, and the rest is the chain of a tile's instructions, the
-// widening of every value before its product among them, with two warps on a scheduler: 37 % of the issue
+// widening of every value before its product among them, with two warps on a scheduler: 36 % of the issue
 // slots are used). Teams there made 81.5 into 93 to 122: their joins have few warps and many parts.
 //
 // A warp has its own tokens of each tile, its own two stages in shared memory, filled by its own
